@@ -89,7 +89,7 @@ Dims dims_of(const q3tts_config& c) {
   // default prefill chunk: up to 1024 positions (long prompts read the
   // weights fewer times and give the attention more query tiles per launch)
   d.chunk = c.prefill_chunk > 0 ? c.prefill_chunk : std::min(std::max(c.kv_cap_steps, 16), 1024);
-  d.m_max = std::max(d.chunk, 2 * d.S);
+  d.m_max = std::max(std::max(d.chunk, 2 * d.S), Q3TTS_MAX_TREE_NODES);
   d.esz = c.weight_dtype == Q3TTS_F32 ? 4 : (c.weight_dtype == Q3TTS_FP8 ? 1 : 2);  // matrix elements
   d.kvesz = c.kv_dtype == Q3TTS_F32 ? 4 : 2;
   return d;
@@ -136,7 +136,20 @@ size_t carve(const q3tts_config& c, void* base, q3tts_handle* h) {
   float* g_uni = cv.take<float>((size_t)d.S * Q3TTS_N_CODEBOOKS);
   int32_t* g_forced = cv.take<int32_t>((size_t)d.S * Q3TTS_N_CODEBOOKS);
   int32_t* g_codes = cv.take<int32_t>((size_t)d.S * Q3TTS_N_CODEBOOKS);
+  int32_t* tree_codes = cv.take<int32_t>((size_t)Q3TTS_MAX_TREE_NODES * Q3TTS_N_CODEBOOKS);
+  float* tree_h = cv.take<float>((size_t)Q3TTS_MAX_TREE_NODES * d.Dt);
+  float* tree_logits = cv.take<float>((size_t)Q3TTS_MAX_TREE_NODES * d.Vt);
+  unsigned long long* tree_masks = cv.take<unsigned long long>(Q3TTS_MAX_TREE_NODES);
+  q3::TreeMeta* tree_meta = cv.take<q3::TreeMeta>(1);
+  int* beam_ids = cv.take<int>(d.S);
+  int32_t* beam_tokens = cv.take<int32_t>(d.S);
+  int32_t* beam_parents = cv.take<int32_t>(d.S);
+  float* beam_scores = cv.take<float>(d.S);
   if (h) {
+    h->tree_codes = tree_codes; h->tree_h = tree_h; h->tree_logits = tree_logits;
+    h->tree_masks = tree_masks; h->tree_meta = tree_meta;
+    h->beam_ids = beam_ids; h->beam_tokens = beam_tokens; h->beam_parents = beam_parents;
+    h->beam_scores = beam_scores;
     h->rope_cos = rope_cos; h->rope_sin = rope_sin; h->kv_pool = kv_pool;
     h->page_table = page_table; h->cp_kv = cpkv; h->cp_page_table = cp_pt;
     h->pending_h = pend_h; h->pending_logits = pend_l; h->history = hist; h->finished = fin;
@@ -153,8 +166,22 @@ size_t carve(const q3tts_config& c, void* base, q3tts_handle* h) {
 }
 
 void free_stream_pages(q3tts_handle* h, int sid) {
-  for (int p : h->pages[sid]) h->free_pages.push_back(p);
+  for (int p : h->pages[sid]) q3::drop_page(h, p);
   h->pages[sid].clear();
+  if (h->tree_sid == sid) h->tree_sid = -1;
+}
+
+}  // namespace
+
+namespace q3 {
+
+void take_page(q3tts_handle* h, int sid, int page) {
+  h->page_ref[page] = 1;
+  h->pages[sid].push_back(page);
+}
+
+void drop_page(q3tts_handle* h, int page) {
+  if (--h->page_ref[page] == 0) h->free_pages.push_back(page);
 }
 
 bool check_sampling(const q3tts_sampling& p, int Vt) {
@@ -180,9 +207,12 @@ q3tts_sampling device_sampling(const q3tts_sampling& p, int Vt) {
   return d;
 }
 
-}  // namespace
+}  // namespace q3
 
 extern "C" {
+
+using q3::check_sampling;
+using q3::device_sampling;
 
 size_t q3tts_workspace_size(const q3tts_config* cfg) {
   if (check_config(cfg) != Q3TTS_OK) return 0;
@@ -289,8 +319,10 @@ int q3tts_create(const q3tts_config* cfg, const q3tts_weights* w, void* workspac
   }
   h->len.assign(d.S, -1);
   h->pages.assign(d.S, std::vector<int>());
+  for (auto& v : h->pages) v.reserve(d.pps);
   h->free_pages.clear();
   for (int p = d.n_pages - 1; p >= 0; --p) h->free_pages.push_back(p);
+  h->page_ref.assign(d.n_pages, 0);
   rc = q3::frame_kernel_create(h);
   if (rc != Q3TTS_OK) {
     for (cudaEvent_t& e : h->chunk_ev) cudaEventDestroy(e);
@@ -322,7 +354,7 @@ int q3tts_prefill(q3tts_handle* h, int sid, const float* embeds_dev, int len) {
   for (int i = 0; i < need; ++i) {
     row[i] = h->free_pages.back();
     h->free_pages.pop_back();
-    h->pages[sid].push_back(row[i]);
+    q3::take_page(h, sid, row[i]);
   }
   cudaStream_t s = h->s;
   // pageable source: staged before the call returns, so `row` may go away
@@ -374,8 +406,9 @@ int q3tts_step_frame(q3tts_handle* h, const q3tts_sampling* params, const int32_
     rc = q3::step_layered(h, d, uniforms_dev, codes_dev, forced_dev, logits_dev);
   if (rc != Q3TTS_OK) return rc;
   for (int b = 0; b < n_active; ++b) {
-    if (d.newpage[b] >= 0) h->pages[stream_ids[b]].push_back(d.newpage[b]);
+    if (d.newpage[b] >= 0) q3::take_page(h, stream_ids[b], d.newpage[b]);
     h->len[stream_ids[b]] += 1;
+    if (h->tree_sid == stream_ids[b]) h->tree_sid = -1;
   }
   h->free_pages.resize(h->free_pages.size() - taken);
   return Q3TTS_OK;
@@ -420,8 +453,8 @@ int q3tts_frames_ready(q3tts_handle* h) {
 // Batch-1 frame with the persistent kernel's per-frame scratch in a static
 // device array.  Validation and stream bookkeeping follow q3tts_step_frame,
 // but nothing here allocates: no std::vector, no thread-local descriptor, and
-// the page lists were reserved to their maximum length by the handle's first
-// call, so pushing a page never grows them.
+// the page lists were reserved to their maximum length at create, so pushing a
+// page never grows them.
 int q3tts_step_frame_static(q3tts_handle* h, const q3tts_sampling* params, int stream_id,
                             const float* uniforms_dev, int32_t* codes_dev,
                             const int32_t* forced_dev, float* logits_dev) {
@@ -433,10 +466,6 @@ int q3tts_step_frame_static(q3tts_handle* h, const q3tts_sampling* params, int s
   if (rc != Q3TTS_OK) return rc;
   if (h->len[s] < 1) return Q3TTS_ERR_STATE;
   if (h->len[s] >= h->c.kv_cap_steps) return Q3TTS_ERR_CAPACITY;
-  if (!h->static_ready) {
-    for (auto& v : h->pages) v.reserve(h->pps);
-    h->static_ready = true;
-  }
   const bool grow = h->len[s] / h->c.page_size >= (int)h->pages[s].size();
   if (grow && h->free_pages.empty()) return Q3TTS_ERR_CAPACITY;
   const int newpage = grow ? h->free_pages.back() : -1;
@@ -445,9 +474,10 @@ int q3tts_step_frame_static(q3tts_handle* h, const q3tts_sampling* params, int s
   if (rc != Q3TTS_OK) return rc;
   if (grow) {
     h->free_pages.pop_back();
-    h->pages[s].push_back(newpage);
+    q3::take_page(h, s, newpage);
   }
   h->len[s] += 1;
+  if (h->tree_sid == s) h->tree_sid = -1;
   return Q3TTS_OK;
 }
 

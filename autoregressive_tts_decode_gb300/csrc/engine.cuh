@@ -7,7 +7,7 @@
 #include <vector>
 
 #include "common.cuh"
-#include "q3tts.h"
+#include "q3tts_branch.h"
 
 namespace q3 {
 
@@ -18,6 +18,20 @@ struct StepDesc {
   int pos[Q3TTS_MAX_STREAMS];       // Talker position the frame writes
   int newpage[Q3TTS_MAX_STREAMS];   // page id to enter at pos / page_size, or -1
   q3tts_sampling sp[Q3TTS_MAX_STREAMS];
+};
+
+// Where a layered step's fed codes come from: the draws, the caller's forced
+// codes, or a beam selection's semantic codes (h->beam_tokens) with the
+// acoustic codes drawn.
+enum class FeedMode { kDrawn, kForced, kBeam };
+
+// Per-call arrays of a drafted tree, uploaded in one copy.
+struct TreeMeta {
+  int length;         // committed positions
+  int node_start[2];  // 0, nodes
+  int path_len;
+  int path[Q3TTS_MAX_TREE_NODES];
+  int rope_pos[Q3TTS_MAX_TREE_NODES];
 };
 
 struct FrameKernelState;  // persistent frame kernel (frame_kernel.cu)
@@ -70,11 +84,30 @@ struct q3tts_handle {
   float* g_uni;      // [max_streams][16]
   int32_t* g_forced;  // [max_streams][16]
   int32_t* g_codes;   // [max_streams][16]
+  // drafted trees (q3tts_tree_step): the latest tree's node states and the
+  // small arrays its kernels read
+  int32_t* tree_codes;  // [Q3TTS_MAX_TREE_NODES][16]
+  float* tree_h;        // [Q3TTS_MAX_TREE_NODES][D_t] final-normed hiddens
+  float* tree_logits;   // [Q3TTS_MAX_TREE_NODES][V_t]
+  unsigned long long* tree_masks;  // [Q3TTS_MAX_TREE_NODES]
+  q3::TreeMeta* tree_meta;
+  // beams (q3tts_beam_frame): [max_streams] each
+  int* beam_ids;
+  int32_t* beam_tokens;
+  int32_t* beam_parents;
+  float* beam_scores;
 
-  // host-side stream bookkeeping
+  // host-side stream bookkeeping.  A page holds positions of one stream, or of
+  // several (forks, beams) that share a prefix; page_ref counts its holders.
+  // Only whole pages are shared, and positions are only ever appended, so a
+  // shared page is never written.
   std::vector<int> len;  // Talker positions held; -1 = no prompt yet
-  std::vector<std::vector<int>> pages;
+  std::vector<std::vector<int>> pages;  // reserved to their longest at create: they never grow later
   std::vector<int> free_pages;
+  std::vector<int> page_ref;
+  // the latest drafted tree (tree_sid -1: none): its stream, nodes and parents
+  int tree_sid = -1, tree_n = 0;
+  int tree_parent[Q3TTS_MAX_TREE_NODES];
 
   q3::FrameKernelState* fk;
   char* fk_base;           // workspace region of the persistent frame kernel
@@ -83,7 +116,6 @@ struct q3tts_handle {
   // failure-path test (q3tts_debug_fail_barrier), armed for one persistent launch
   int dbg_fail_bar = -1;
   long long dbg_wait_cycles = 0;
-  bool static_ready = false;  // per-stream page lists reserved for it
   uint64_t launches = 0;
   // streaming chunks (q3tts_step_frames): one event per frame, recorded after
   // the frame's codes are copied out
@@ -93,7 +125,7 @@ struct q3tts_handle {
   // forced codes); g_launches kernels per replay
   cudaGraphExec_t gexec = nullptr;
   int g_n = 0;
-  bool g_forced_on = false;
+  q3::FeedMode g_feed = q3::FeedMode::kDrawn;
   uint64_t g_launches = 0;
   cudaStream_t cap_stream = nullptr;  // stream the step is captured on
   bool graph_off = false;             // Q3TTS_GRAPH=0: launch the layered step kernel by kernel
@@ -103,9 +135,21 @@ namespace q3 {
 
 // Layered frame step (one kernel per operation), any number of streams.
 int step_layered(q3tts_handle* h, const StepDesc& d, const float* uniforms, int32_t* codes,
-                 const int32_t* forced, float* logits);
+                 const int32_t* forced, float* logits, bool beam = false);
+// Talker pass over the n nodes of the tree described by h->tree_meta,
+// tree_masks and tree_codes; leaves tree_h and tree_logits.
+int tree_layered(q3tts_handle* h, int sid, int n);
+// Rows h->tree_meta->path of stream sid moved behind its context, the codes'
+// history marked and the last node's state made pending.
+int tree_commit(q3tts_handle* h, int sid, int n, int last, bool move);
 int prefill_layered(q3tts_handle* h, int sid, const float* embeds, int len);
 void step_graph_destroy(q3tts_handle* h);
+
+// Page bookkeeping (api.cu).
+void take_page(q3tts_handle* h, int sid, int page);  // a page off the free list joins sid's
+void drop_page(q3tts_handle* h, int page);           // one holder less; free at none
+bool check_sampling(const q3tts_sampling& p, int Vt);
+q3tts_sampling device_sampling(const q3tts_sampling& p, int Vt);
 
 KVDesc talker_kv(const q3tts_handle* h);
 KVDesc cp_kv(const q3tts_handle* h);

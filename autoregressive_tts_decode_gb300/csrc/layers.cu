@@ -209,6 +209,7 @@ __global__ void qk_rope_append_kernel(float* __restrict__ qkv, int ld, TokDesc t
   const int nw = blockDim.x >> 5;
   const int stream = td.tok_stream[m];
   const int pos = td.tok_pos ? td.tok_pos[m] : td.pos_const;
+  const int rpos = td.rope_pos ? td.rope_pos[m] : pos;
   const int Hkv = kv.Hkv;
   float* row = qkv + (size_t)m * ld;
   for (int hh = warp; hh < Hq + 2 * Hkv; hh += nw) {
@@ -231,7 +232,7 @@ __global__ void qk_rope_append_kernel(float* __restrict__ qkv, int ld, TokDesc t
 #pragma unroll
       for (int j = 0; j < P; ++j) {
         const int i = lane + 32 * j;
-        const float c = rc[(size_t)pos * HALF + i], sn = rs[(size_t)pos * HALF + i];
+        const float c = rc[(size_t)rpos * HALF + i], sn = rs[(size_t)rpos * HALF + i];
         const float x0 = v[j], x1 = v[j + P];
         v[j] = x0 * c - x1 * sn;
         v[j + P] = x1 * c + x0 * sn;

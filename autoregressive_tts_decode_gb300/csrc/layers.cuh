@@ -20,6 +20,7 @@ struct TokDesc {
   const int* tok_stream;
   const int* tok_pos;  // NULL: every token at pos_const
   int pos_const;
+  const int* rope_pos = nullptr;  // positions to rotate at, where they differ from the cache slots (drafted trees)
 };
 
 // Y[m, n] (+)= sum_k X[m, k] W[n, k] for m < M, n < N (FP8 W: times the row

@@ -10,6 +10,7 @@
 // pending logits.
 #include "engine.cuh"
 #include "layers.cuh"
+#include "ops.cuh"
 #include "sampler.cuh"
 
 namespace q3 {
@@ -121,6 +122,60 @@ __global__ void __launch_bounds__(256) sample_kernel(
   }
 }
 
+// The semantic code of a beam frame: the selected one of slot b instead of a
+// draw, with the sampler's history and stop bookkeeping.  A slot that no
+// candidate was left for (token -1) feeds code 0.
+__global__ void beam_feed_kernel(const int32_t* __restrict__ tokens, int n, int V, const int* __restrict__ sid,
+                                 const q3tts_sampling* __restrict__ sp, uint8_t* history, uint8_t* finished,
+                                 int32_t* __restrict__ codes, int* __restrict__ fed) {
+  pdl_wait();  // inputs come from the previous kernel
+  pdl_trigger();
+  for (int b = threadIdx.x; b < n; b += blockDim.x) {
+    const int s = sid[b], f = min(max(tokens[b], 0), V - 1);
+    const bool before = finished[s] != 0;
+    if (!before && sp[b].eos_token >= 0 && f == sp[b].eos_token) finished[s] = 1;
+    fed[b * 16] = f;
+    codes[b * 16] = before ? -1 : f;
+    history[(size_t)s * V + f] = 1;
+  }
+}
+
+// Talker inputs of drafted frames: the sum of a node's 16 code embeddings.  A
+// code outside its vocabulary is reported and code 0 read in its place.
+template <class WT>
+__global__ void tree_embed_kernel(const int32_t* __restrict__ codes, const WT* __restrict__ e_codec,
+                                  const WT* __restrict__ cp_embeds, int Dt, int Vt, int Vc, float* __restrict__ x,
+                                  int* err) {
+  pdl_wait();  // inputs come from the previous kernel
+  pdl_trigger();
+  const int b = blockIdx.y;
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  float acc = 0.f;
+  for (int j = 0; j < Q3TTS_N_CODEBOOKS; ++j) {
+    int c = codes[b * 16 + j];
+    if (c < 0 || c >= (j == 0 ? Vt : Vc)) {
+      if (i == 0) atomicCAS(err, 0, Q3TTS_ERR_ARG);
+      c = 0;
+    }
+    if (i < Dt) acc += to_f(j == 0 ? e_codec[(size_t)c * Dt + i] : cp_embeds[((size_t)(j - 1) * Vc + c) * Dt + i]);
+  }
+  if (i < Dt) x[(size_t)b * Dt + i] = acc;
+}
+
+// The accepted path's semantic codes enter the stream's history; the last
+// node's hidden and logits become its pending state.
+__global__ void tree_commit_kernel(const TreeMeta* __restrict__ t, const int32_t* __restrict__ codes, int n, int last,
+                                   int sid, const float* __restrict__ th, const float* __restrict__ tl, int Dt, int Vt,
+                                   float* __restrict__ pending_h, float* __restrict__ pending_logits,
+                                   uint8_t* history) {
+  pdl_wait();  // inputs come from the previous kernel
+  pdl_trigger();
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < Dt) pending_h[(size_t)sid * Dt + i] = th[(size_t)last * Dt + i];
+  if (i < Vt) pending_logits[(size_t)sid * Vt + i] = tl[(size_t)last * Vt + i];
+  if (i < n) history[(size_t)sid * Vt + min(max(codes[t->path[i] * 16], 0), Vt - 1)] = 1;
+}
+
 template <class WT>
 __global__ void cp_input_kernel(int j, int n, const int* __restrict__ sid,
                                 const int* __restrict__ fed, const float* __restrict__ pending_h,
@@ -203,10 +258,10 @@ static void norm_in(q3tts_handle* h, const float* X, int ldx, int in_mul, int in
 
 // M tokens through all layers of one decoder stack (residual stream x [M, D]).
 // pf_sid >= 0: the tokens are a prefill chunk of stream pf_sid at positions
-// pf_pos0 .. pf_pos0 + M - 1.
+// pf_pos0 .. pf_pos0 + M - 1.  tree: the tokens are the nodes of a drafted tree.
 static void stack_pass(q3tts_handle* h, const q3tts_layer_weights* lw, int layers, int D, int F,
                        float* x, int M, TokDesc td, KVDesc kv, int kdt, int max_ctx, int pf_sid = -1,
-                       int pf_pos0 = 0) {
+                       int pf_pos0 = 0, TreeArgs* tree = nullptr) {
   cudaStream_t s = h->s;
   const int gdt = gain_dt(h), HqD = h->Hq * h->hd;
   for (int l = 0; l < layers; ++l) {
@@ -215,11 +270,15 @@ static void stack_pass(q3tts_handle* h, const q3tts_layer_weights* lw, int layer
     proj(h, h->hb, D, L.w_qkv, h->qkv_rows, D, h->qkv, h->qkv_rows, M, false, L.s_qkv);
     launch_qk_rope_append(gdt, kdt, h->qkv, h->qkv_rows, M, td, L.g_q_norm, L.g_k_norm,
                           h->c.qk_norm, h->c.rms_eps, h->rope_cos, h->rope_sin, kv, l, h->Hq, s);
+    if (tree) {
+      tree->layer = l;
+      if (launch_tree_attention(*tree, kdt, s) != Q3TTS_OK) h->tc_failed = true;
+    }
     // a prefill chunk: query tiles on the tensor cores; contexts longer than
     // one span: spread over the GPU by span
-    const bool fa = pf_sid >= 0 && launch_fa_prefill(h->qkv, h->qkv_rows, M, pf_sid, pf_pos0, kv, kdt, l, h->Hq,
+    const bool fa = !tree && pf_sid >= 0 && launch_fa_prefill(h->qkv, h->qkv_rows, M, pf_sid, pf_pos0, kv, kdt, l, h->Hq,
                                                       h->att, HqD, h->d_err, s);
-    if (!fa && (max_ctx <= 64 || !launch_attention_split(kdt, h->qkv, h->qkv_rows, M, td, kv, l, h->Hq, h->att,
+    if (!tree && !fa && (max_ctx <= 64 || !launch_attention_split(kdt, h->qkv, h->qkv_rows, M, td, kv, l, h->Hq, h->att,
                                                          HqD, h->spl_part, h->spl_cnt, h->spl_nsmax, s)))
       launch_attention(kdt, h->qkv, h->qkv_rows, M, td, kv, l, h->Hq, h->att, HqD, max_ctx, s);
     if (h->tc) launch_split_hilo(h->att, HqD, hilo(h), M, HqD, s);
@@ -267,14 +326,18 @@ int prefill_layered(q3tts_handle* h, int sid, const float* embeds, int len) {
 // The layered step's kernels for n active streams, whose descriptor is in
 // h->d_desc; the attention kernels are sized for contexts up to max_ctx.
 static void step_kernels(q3tts_handle* h, int n, int max_ctx, const float* uniforms, int32_t* codes,
-                         const int32_t* forced, float* logits) {
+                         const int32_t* forced, float* logits, bool beam) {
   cudaStream_t s = h->s;
   const int Dt = h->Dt, Dc = h->Dc, Vt = h->Vt, Vc = h->Vc, gdt = gain_dt(h);
   const int dump_ld = Vt + (Q3TTS_N_CODEBOOKS - 1) * Vc;
   const size_t smem = sizeof(SamplerSmem);
   launch_pdl(setup_kernel, dim3(1), dim3(256), 0, s, h->d_desc, h->d_sid, h->d_pos, h->d_sp, h->page_table, h->pps,
                                  h->c.page_size, h->d_tok_stream, h->d_tok_pos);
-  launch_pdl(sample_kernel, dim3(n), dim3(256), smem, s, h->pending_logits, Vt, 1, h->d_sid, h->d_sp, h->history, h->finished,
+  if (beam)
+    launch_pdl(beam_feed_kernel, dim3(1), dim3(256), 0, s, h->beam_tokens, n, Vt, h->d_sid, h->d_sp, h->history,
+               h->finished, codes, h->d_fed);
+  else
+    launch_pdl(sample_kernel, dim3(n), dim3(256), smem, s, h->pending_logits, Vt, 1, h->d_sid, h->d_sp, h->history, h->finished,
                                      uniforms, 0, forced, codes, h->d_fed, logits, dump_ld, 0,
                                      h->d_err);
   const size_t es = wbytes(h);
@@ -338,7 +401,7 @@ void step_graph_destroy(q3tts_handle* h) {
 
 // Captures the step's kernels for n streams into h->gexec (inputs and
 // outputs in the handle's fixed buffers); false if capture is not possible.
-static bool step_graph_build(q3tts_handle* h, int n, bool with_forced) {
+static bool step_graph_build(q3tts_handle* h, int n, FeedMode feed) {
   if (h->gexec) cudaGraphExecDestroy(h->gexec);
   h->gexec = nullptr;
   if (!h->cap_stream && cudaStreamCreateWithFlags(&h->cap_stream, cudaStreamNonBlocking) != cudaSuccess) {
@@ -351,7 +414,8 @@ static bool step_graph_build(q3tts_handle* h, int n, bool with_forced) {
   cudaGraph_t g = nullptr;
   bool ok = cudaStreamBeginCapture(h->s, cudaStreamCaptureModeThreadLocal) == cudaSuccess;
   if (ok) {
-    step_kernels(h, n, h->c.kv_cap_steps, h->g_uni, h->g_codes, with_forced ? h->g_forced : nullptr, nullptr);
+    step_kernels(h, n, h->c.kv_cap_steps, h->g_uni, h->g_codes,
+                 feed == FeedMode::kForced ? h->g_forced : nullptr, nullptr, feed == FeedMode::kBeam);
     ok = cudaStreamEndCapture(h->s, &g) == cudaSuccess && g != nullptr;
   }
   h->s = user;
@@ -366,25 +430,25 @@ static bool step_graph_build(q3tts_handle* h, int n, bool with_forced) {
     return false;
   }
   h->g_n = n;
-  h->g_forced_on = with_forced;
+  h->g_feed = feed;
   return true;
 }
 
 // The layered frame step.  Without a logits dump it is replayed from a CUDA
-// graph captured once per (active streams, forced or not): the descriptor
+// graph captured once per (active streams, feed mode): the descriptor
 // goes to the device ahead of it, the caller's uniforms and forced codes are
 // copied into the handle's buffers and the codes copied out after it.
 int step_layered(q3tts_handle* h, const StepDesc& d, const float* uniforms, int32_t* codes,
-                 const int32_t* forced, float* logits) {
+                 const int32_t* forced, float* logits, bool beam) {
   cudaStream_t s = h->s;
   const int n = d.n;
+  const FeedMode feed = beam ? FeedMode::kBeam : (forced ? FeedMode::kForced : FeedMode::kDrawn);
   // pageable source: the copy is staged before the call returns, so d may change
   if (cudaMemcpyAsync(h->d_desc, &d, sizeof(StepDesc), cudaMemcpyHostToDevice, s) != cudaSuccess)
     return Q3TTS_ERR_CUDA;
   const size_t att_smem = sizeof(float) * (size_t)(h->hd + h->c.kv_cap_steps);  // non-grouped attention
   const bool graph = !h->graph_off && !logits && (((h->hd == 128 || h->hd == 64) && h->Hq / h->Hkv <= 4) || att_smem <= 48 * 1024);
-  if (graph && ((h->gexec && h->g_n == n && h->g_forced_on == (forced != nullptr)) ||
-                step_graph_build(h, n, forced != nullptr))) {
+  if (graph && ((h->gexec && h->g_n == n && h->g_feed == feed) || step_graph_build(h, n, feed))) {
     const size_t nb = sizeof(int32_t) * (size_t)n * Q3TTS_N_CODEBOOKS;
     cudaMemcpyAsync(h->g_uni, uniforms, nb, cudaMemcpyDeviceToDevice, s);
     if (forced) cudaMemcpyAsync(h->g_forced, forced, nb, cudaMemcpyDeviceToDevice, s);
@@ -394,12 +458,71 @@ int step_layered(q3tts_handle* h, const StepDesc& d, const float* uniforms, int3
   } else {
     int max_ctx = 0;
     for (int b = 0; b < n; ++b) max_ctx = d.pos[b] + 1 > max_ctx ? d.pos[b] + 1 : max_ctx;
-    step_kernels(h, n, max_ctx, uniforms, codes, forced, logits);
+    step_kernels(h, n, max_ctx, uniforms, codes, forced, logits, beam);
   }
   if (h->tc_failed) {
     h->tc_failed = false;
     return Q3TTS_ERR_CUDA;
   }
+  return cudaGetLastError() == cudaSuccess ? Q3TTS_OK : Q3TTS_ERR_CUDA;
+}
+
+int tree_layered(q3tts_handle* h, int sid, int n) {
+  cudaStream_t s = h->s;
+  const int Dt = h->Dt, Vt = h->Vt, Vc = h->Vc;
+  launch_pdl(fill_tokens_kernel, dim3(1), dim3(256), 0, s, h->d_tok_stream, h->d_tok_pos, n, sid, h->len[sid]);
+  const dim3 eg((Dt + 255) / 256, n);
+  if (gain_dt(h) == Q3TTS_BF16)
+    launch_pdl(tree_embed_kernel<bf16>, eg, dim3(256), 0, s, h->tree_codes, (const bf16*)h->w.talker_e_codec,
+               (const bf16*)h->w.cp_embeds, Dt, Vt, Vc, h->x, h->d_err);
+  else
+    launch_pdl(tree_embed_kernel<float>, eg, dim3(256), 0, s, h->tree_codes, (const float*)h->w.talker_e_codec,
+               (const float*)h->w.cp_embeds, Dt, Vt, Vc, h->x, h->d_err);
+  TokDesc td{h->d_tok_stream, h->d_tok_pos, 0, h->tree_meta->rope_pos};
+  TreeArgs t;
+  t.kv = talker_kv(h);
+  t.kv.page_table += (size_t)sid * h->pps;
+  t.n_seqs = 1;
+  t.lengths = &h->tree_meta->length;
+  t.node_start = h->tree_meta->node_start;
+  t.masks = h->tree_masks;
+  t.n_rows = t.max_nodes = n;
+  t.Hq = h->Hq;
+  t.q = h->qkv;
+  t.ldq = h->qkv_rows;
+  t.out = h->att;
+  t.ldo = h->Hq * h->hd;
+  t.status = h->d_err;
+  stack_pass(h, h->tl.data(), h->c.talker_layers, Dt, h->Ft, h->x, n, td, talker_kv(h), h->c.kv_dtype,
+             h->len[sid] + n, -1, 0, &t);
+  launch_rmsnorm(gain_dt(h), h->x, Dt, 1, 0, h->w.talker_g_final, h->tree_h, Dt, n, Dt, h->c.rms_eps, s);
+  if (h->tc) {
+    launch_split_hilo(h->tree_h, Dt, hilo(h), n, Dt, s);
+    h->launches += 1;
+  }
+  proj(h, h->tree_h, Dt, h->w.talker_w_head, Vt, Dt, h->tree_logits, Vt, n, false, h->w.s_head);
+  h->launches += 4;  // tokens, embeddings, final norm, head
+  if (h->tc_failed) {
+    h->tc_failed = false;
+    return Q3TTS_ERR_CUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? Q3TTS_OK : Q3TTS_ERR_CUDA;
+}
+
+int tree_commit(q3tts_handle* h, int sid, int n, int last, bool move) {
+  if (move) {
+    KVDesc kv = talker_kv(h);
+    kv.page_table += (size_t)sid * h->pps;
+    const int rc = launch_compact_rows(kv, h->c.talker_layers, h->c.kv_dtype == Q3TTS_F32 ? 4 : 2, 1,
+                                       &h->tree_meta->length, h->tree_meta->path, n, &h->tree_meta->path_len, h->d_err,
+                                       h->s);
+    if (rc != Q3TTS_OK) return rc;
+    h->launches += 1;
+  }
+  const int most = h->Dt > h->Vt ? h->Dt : h->Vt;
+  launch_pdl(tree_commit_kernel, dim3((most + 255) / 256), dim3(256), 0, h->s, h->tree_meta, h->tree_codes, n, last, sid,
+             h->tree_h, h->tree_logits, h->Dt, h->Vt, h->pending_h, h->pending_logits, h->history);
+  h->launches += 1;
   return cudaGetLastError() == cudaSuccess ? Q3TTS_OK : Q3TTS_ERR_CUDA;
 }
 

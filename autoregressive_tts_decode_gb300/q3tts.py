@@ -1,4 +1,5 @@
-"""ctypes binding of libq3tts (include/q3tts.h): argument marshalling only.
+"""ctypes binding of libq3tts (include/q3tts.h, include/q3tts_branch.h): argument
+marshalling only.
 
 Every step of the decode runs in the CUDA library; this module turns torch
 tensors into device pointers and status codes into exceptions.  It refuses to
@@ -44,6 +45,16 @@ class LayerWeights(C.Structure):
     _fields_ = [(k, C.c_void_p) for k in LAYER_KEYS + LAYER_SCALES]
 
 
+class KVCache(C.Structure):
+    _fields_ = [("pool", C.c_void_p)] + [(n, C.c_int) for n in (
+        "layers", "n_pages", "n_kv_heads", "page_size", "head_dim", "kv_dtype")]
+
+
+class Rows(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("row_bytes", C.c_size_t),
+                ("src_stride", C.c_size_t), ("dst_stride", C.c_size_t)]
+
+
 class Weights(C.Structure):
     _fields_ = [("talker_layers", C.POINTER(LayerWeights)), ("talker_g_final", C.c_void_p),
                 ("talker_w_head", C.c_void_p), ("talker_e_codec", C.c_void_p),
@@ -64,7 +75,13 @@ EXPORTS = ("q3tts_workspace_size", "q3tts_create", "q3tts_prefill", "q3tts_step_
            "q3tts_kernel_launches", "q3tts_destroy", "q3tts_strerror",
            "q3tts_step_frame_static", "q3tts_debug_fail_barrier", "q3tts_stream_finished",
            "q3tts_step_frames", "q3tts_frames_ready")
+# include/q3tts_branch.h
+BRANCH_EXPORTS = ("q3tts_fork", "q3tts_tree_step", "q3tts_tree_accept", "q3tts_beam_frame",
+                  "q3tts_tree_attention", "q3tts_copy_pages", "q3tts_compact_rows",
+                  "q3tts_beam_select", "q3tts_reorder_rows")
 MAX_CHUNK = 64
+MAX_TREE_NODES = 64
+MAX_BEAMS = 32
 
 _lib = None
 
@@ -98,6 +115,19 @@ def load(path: str = LIB_PATH):
     L.q3tts_step_frames.argtypes = [vp, C.POINTER(Sampling), C.POINTER(C.c_int32), C.c_int, C.c_int, vp, vp,
                                     vp, vp]
     L.q3tts_frames_ready.argtypes = [vp]
+    i32p = C.POINTER(C.c_int32)
+    L.q3tts_fork.argtypes = [vp, C.c_int, i32p, C.c_int]
+    L.q3tts_tree_step.argtypes = [vp, C.c_int, vp, i32p, C.c_int, vp, vp]
+    L.q3tts_tree_accept.argtypes = [vp, C.c_int, i32p, C.c_int]
+    L.q3tts_beam_frame.argtypes = [vp, C.POINTER(Sampling), i32p, C.c_int, C.c_int, vp, vp, vp, i32p]
+    kvp = C.POINTER(KVCache)
+    L.q3tts_tree_attention.argtypes = [kvp, C.c_int, vp, C.c_int, C.c_int, vp, vp, vp, C.c_int, C.c_int, C.c_int,
+                                       vp, C.c_int, vp, C.c_int, vp, vp]
+    L.q3tts_copy_pages.argtypes = [kvp, vp, vp, C.c_int, vp]
+    L.q3tts_compact_rows.argtypes = [kvp, vp, C.c_int, C.c_int, vp, vp, C.c_int, vp, vp, vp]
+    L.q3tts_beam_select.argtypes = [vp, C.c_size_t, vp, C.c_int, C.c_int, C.c_int, vp, vp, vp, C.c_int, C.c_int,
+                                    C.c_float, C.c_int, vp, vp, vp, vp]
+    L.q3tts_reorder_rows.argtypes = [C.POINTER(Rows), C.c_int, vp, vp, C.c_int, C.c_int, C.c_int, vp, vp]
     L.q3tts_strerror.restype = C.c_char_p
     L.q3tts_strerror.argtypes = [C.c_int]
     _lib = L
@@ -146,6 +176,210 @@ def _need(t, name: str, dtype, numel: int, what: str):
     if not ok:
         raise Q3TTSError(ERR_ARG, f"{what}: {name} must be a contiguous CUDA {dtype} tensor "
                                   f"of at least {numel} elements")
+
+
+# ---- branching-decode operators over caller-owned buffers (include/q3tts_branch.h).
+# They run on the current torch stream of their tensors' device; results do not
+# depend on which device is current.
+
+def _bad(what: str, name: str, want: str):
+    raise Q3TTSError(ERR_ARG, f"{what}: {name} must be {want}")
+
+
+def _cuda(t, name: str, dtype, shape, what: str, device=None):
+    """Raises unless t is a contiguous CUDA tensor of dtype and shape (and on
+    `device`)."""
+    if not (t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_cuda and t.is_contiguous()
+            and (device is None or t.device == device)):
+        _bad(what, name, f"a contiguous CUDA {dtype} tensor of shape {tuple(shape)}"
+                         + ("" if device is None else f" on {device}"))
+
+
+def _on(device, call):
+    """Runs call(stream handle) with `device` current."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream(device).cuda_stream)
+    with torch.cuda.device(device):
+        return call(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _cache(pool, what: str) -> KVCache:
+    import torch
+    kinds = {torch.float32: F32, torch.bfloat16: BF16}
+    if not (pool.is_cuda and pool.is_contiguous() and pool.dim() == 6 and pool.shape[2] == 2
+            and pool.dtype in kinds):
+        _bad(what, "pool", "a contiguous CUDA fp32 or bf16 tensor "
+                           "[layers, pages, 2, kv heads, page size, head dim]")
+    layers, pages, _, heads, page, hd = pool.shape
+    return KVCache(pool.data_ptr(), layers, pages, heads, page, hd, kinds[pool.dtype])
+
+
+def _heads(t, name: str, what: str) -> int:
+    """Row pitch of a [rows, heads, head dim] view whose rows are contiguous."""
+    n, h, d = t.shape
+    if (h > 1 and t.stride(1) != d) or (d > 1 and t.stride(2) != 1) or (n > 1 and t.stride(0) < h * d):
+        _bad(what, name, "[rows, heads, head dim] with contiguous rows")
+    return t.stride(0) if n > 1 else h * d
+
+
+def tree_attention(pool, layer: int, page_table, lengths, node_start, masks, q, max_nodes: Optional[int] = None,
+                   out=None, status=None):
+    """q3tts_tree_attention.  pool: CUDA fp32/bf16 [layers, pages, 2, kv heads, page
+    size, head dim]; page_table int32 [seqs, pages per seq]; lengths int32 [seqs];
+    node_start int32 [seqs + 1]; masks int64 (or uint64) [rows], bit j of a row's
+    word: the row's node sees node j of its sequence; q fp32 [rows, q heads, head
+    dim] (rows contiguous, any row pitch); max_nodes: the most nodes of a sequence
+    (default: as many as there are rows, up to MAX_TREE_NODES).  Returns out
+    (fp32, as q; made if None, with zeroes in rows outside every sequence)."""
+    import torch
+    what = "q3tts_tree_attention"
+    kv = _cache(pool, what)
+    dev = pool.device
+    if q.dim() != 3 or q.dtype != torch.float32 or q.device != dev or q.shape[2] != kv.head_dim:
+        _bad(what, "q", f"a CUDA fp32 tensor [rows, q heads, {kv.head_dim}] on {dev}")
+    rows, heads, _ = q.shape
+    if page_table.dim() != 2:
+        _bad(what, "page_table", "[seqs, pages per seq]")
+    seqs, pps = page_table.shape
+    _cuda(page_table, "page_table", torch.int32, (seqs, pps), what, dev)
+    _cuda(lengths, "lengths", torch.int32, (seqs,), what, dev)
+    _cuda(node_start, "node_start", torch.int32, (seqs + 1,), what, dev)
+    _cuda(masks, "masks", torch.uint64 if masks.dtype == torch.uint64 else torch.int64, (rows,), what, dev)
+    if status is not None:
+        _cuda(status, "status", torch.int32, (1,), what, dev)
+    if out is None:
+        out = torch.zeros((rows, heads, kv.head_dim), dtype=torch.float32, device=dev)
+    elif out.shape != q.shape or out.dtype != torch.float32 or out.device != dev:
+        _bad(what, "out", f"a CUDA fp32 tensor of q's shape on {dev}")
+    if max_nodes is None:
+        max_nodes = max(1, min(rows, MAX_TREE_NODES))
+    ldq, ldo = _heads(q, "q", what), _heads(out, "out", what)
+    _check(_on(dev, lambda s: load().q3tts_tree_attention(
+        C.byref(kv), layer, page_table.data_ptr(), pps, seqs, lengths.data_ptr(), node_start.data_ptr(),
+        masks.data_ptr(), rows, max_nodes, heads, q.data_ptr(), ldq, out.data_ptr(), ldo, _ptr(status), s)), what)
+    return out
+
+
+def _host_ids(v, name: str, what: str):
+    """A CPU int32 tensor of ids (v: one, or a sequence of ints)."""
+    import torch
+    t = v if isinstance(v, torch.Tensor) else torch.tensor(list(v), dtype=torch.int32)
+    if t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        _bad(what, name, "page ids on the host (a sequence, or a contiguous CPU int32 tensor)")
+    return t
+
+
+def copy_pages(pool, src, dst):
+    """q3tts_copy_pages: page src[i] to page dst[i] in every layer of pool (as for
+    tree_attention).  src, dst: sequences of ints or CPU int32 tensors.  Returns pool."""
+    what = "q3tts_copy_pages"
+    kv = _cache(pool, what)
+    src, dst = _host_ids(src, "src", what), _host_ids(dst, "dst", what)
+    if src.numel() != dst.numel():
+        _bad(what, "dst", "as long as src")
+    _check(_on(pool.device, lambda s: load().q3tts_copy_pages(C.byref(kv), src.data_ptr(), dst.data_ptr(),
+                                                              src.numel(), s)), what)
+    return pool
+
+
+def compact_rows(pool, page_table, lengths, path, path_len, status=None):
+    """q3tts_compact_rows: positions lengths[s] + path[s, i] to lengths[s] + i, i <
+    path_len[s], in place.  page_table int32 [seqs, pages per seq], lengths and
+    path_len int32 [seqs], path int32 [seqs, most].  Returns pool."""
+    import torch
+    what = "q3tts_compact_rows"
+    kv = _cache(pool, what)
+    dev = pool.device
+    if page_table.dim() != 2 or path.dim() != 2:
+        _bad(what, "page_table and path", "[seqs, ..]")
+    seqs, pps = page_table.shape
+    _cuda(page_table, "page_table", torch.int32, (seqs, pps), what, dev)
+    _cuda(lengths, "lengths", torch.int32, (seqs,), what, dev)
+    _cuda(path, "path", torch.int32, (seqs, path.shape[1]), what, dev)
+    _cuda(path_len, "path_len", torch.int32, (seqs,), what, dev)
+    if status is not None:
+        _cuda(status, "status", torch.int32, (1,), what, dev)
+    _check(_on(dev, lambda s: load().q3tts_compact_rows(
+        C.byref(kv), page_table.data_ptr(), pps, seqs, lengths.data_ptr(), path.data_ptr(), path.shape[1],
+        path_len.data_ptr(), _ptr(status), s)), what)
+    return pool
+
+
+def beam_select(logits, scores, k: Optional[int] = None, row_ids=None, finished=None, history=None,
+                eos_token: int = -1, special_from: int = 0, repetition_penalty: float = 1.0, out=None):
+    """q3tts_beam_select.  scores fp32 [groups, beams]; logits fp32 [groups, beams,
+    vocab] with contiguous rows, or [rows, vocab] with row_ids int32 [groups,
+    beams]; finished uint8 and history uint8 of logits' rows; k: candidates kept
+    (default: beams).  Returns (tokens int32, parents int32, scores fp32), [groups,
+    k] each; out: three tensors to write them to."""
+    import torch
+    what = "q3tts_beam_select"
+    dev = logits.device
+    if scores.dim() != 2:
+        _bad(what, "scores", "[groups, beams]")
+    groups, beams = scores.shape
+    _cuda(scores, "scores", torch.float32, (groups, beams), what, dev)
+    vocab = logits.shape[-1]
+    lead = tuple(logits.shape[:-1])
+    if (not logits.is_cuda or logits.dtype != torch.float32 or logits.stride(-1) != 1
+            or len(lead) != (2 if row_ids is None else 1) or (row_ids is None and lead != (groups, beams))):
+        _bad(what, "logits", "a CUDA fp32 tensor [groups, beams, vocab], or [rows, vocab] with row_ids")
+    if row_ids is None:
+        ld = logits.stride(1) if beams > 1 else (logits.stride(0) if groups > 1 else vocab)
+        if groups > 1 and logits.stride(0) != beams * ld:
+            _bad(what, "logits", "equally spaced rows")
+    else:
+        _cuda(row_ids, "row_ids", torch.int32, (groups, beams), what, dev)
+        ld = logits.stride(0) if lead[0] > 1 else vocab
+    if finished is not None:
+        _cuda(finished, "finished", torch.uint8, lead, what, dev)
+    if history is not None:
+        _cuda(history, "history", torch.uint8, lead + (vocab,), what, dev)
+    k = beams if k is None else int(k)
+    if out is None:
+        # one block for the three results
+        block = torch.empty((3, groups, max(k, 0)), dtype=torch.int32, device=dev)
+        tokens, parents, best = block[0], block[1], block[2].view(torch.float32)
+    else:
+        tokens, parents, best = out
+        _cuda(tokens, "out[0]", torch.int32, (groups, k), what, dev)
+        _cuda(parents, "out[1]", torch.int32, (groups, k), what, dev)
+        _cuda(best, "out[2]", torch.float32, (groups, k), what, dev)
+    _check(_on(dev, lambda s: load().q3tts_beam_select(
+        logits.data_ptr(), ld, _ptr(row_ids), groups, beams, vocab, scores.data_ptr(), _ptr(finished), _ptr(history),
+        eos_token, special_from, repetition_penalty, k, tokens.data_ptr(), parents.data_ptr(), best.data_ptr(), s)),
+        what)
+    return tokens, parents, best
+
+
+def reorder_rows(src, dst, parents, status=None):
+    """q3tts_reorder_rows: dst[i][g, j] = src[i][g, parents[g, j]] for lists of
+    contiguous CUDA tensors [groups, beams, ..] of any type; dst[i] may be src[i].
+    parents int32 [groups, beams out].  Returns dst."""
+    import torch
+    what = "q3tts_reorder_rows"
+    if parents.dim() != 2 or len(src) != len(dst):
+        _bad(what, "parents", "[groups, beams], with as many dst as src")
+    groups, k = parents.shape
+    dev = parents.device
+    _cuda(parents, "parents", torch.int32, (groups, k), what, dev)
+    if status is not None:
+        _cuda(status, "status", torch.int32, (1,), what, dev)
+    if not src:
+        return dst
+    beams = src[0].shape[1] if src[0].dim() > 1 else 0
+    sets = (Rows * len(src))()
+    for i, (a, b) in enumerate(zip(src, dst)):
+        if a.dim() < 2 or a.shape[0] != groups or a.shape[1] != beams or not a.is_cuda:
+            _bad(what, f"src[{i}]", f"a CUDA tensor [{groups}, {beams}, ..]")
+        _cuda(a, f"src[{i}]", a.dtype, a.shape, what, dev)
+        _cuda(b, f"dst[{i}]", a.dtype, (groups, k) + tuple(a.shape[2:]), what, dev)
+        n = a.element_size() * (a.numel() // max(1, groups * beams))
+        sets[i] = Rows(a.data_ptr(), b.data_ptr(), n, n, n)
+    _check(_on(dev, lambda s: load().q3tts_reorder_rows(sets, len(src), None, parents.data_ptr(), groups, beams, k,
+                                                        _ptr(status), s)), what)
+    return dst
 
 
 class Engine:
@@ -340,6 +574,50 @@ class Engine:
         f = C.c_int(0)
         _check(load().q3tts_stream_finished(self.h, stream_id, C.byref(f)), "q3tts_stream_finished")
         return bool(f.value)
+
+    def fork(self, src: int, dst: Sequence[int]) -> None:
+        """q3tts_fork: the streams dst become what stream src is now."""
+        ids = (C.c_int32 * max(1, len(dst)))(*[int(i) for i in dst])
+        _check(load().q3tts_fork(self.h, int(src), ids, len(dst)), "q3tts_fork")
+
+    def tree_step(self, stream_id: int, codes, parents: Sequence[int], hidden=None, logits=None) -> None:
+        """q3tts_tree_step: codes CUDA int32 [n, 16], parents n ints (-1: the context);
+        hidden: None or CUDA fp32 [n, D_t], logits: None or CUDA fp32 [n, V_t] (written)."""
+        import torch
+        n, what = len(parents), "q3tts_tree_step"
+        _need(codes, "codes", torch.int32, n * N_CODEBOOKS, what)
+        if hidden is not None:
+            _need(hidden, "hidden", torch.float32, n * self.shape.talker_hidden, what)
+        if logits is not None:
+            _need(logits, "logits", torch.float32, n * self.shape.codec_vocab, what)
+        p = (C.c_int32 * max(1, n))(*[int(i) for i in parents])
+        _check(load().q3tts_tree_step(self.h, int(stream_id), codes.data_ptr(), p, n, _ptr(hidden), _ptr(logits)),
+               what)
+
+    def tree_accept(self, stream_id: int, path: Sequence[int]) -> None:
+        """q3tts_tree_accept: the path's frames become part of the stream."""
+        p = (C.c_int32 * max(1, len(path)))(*[int(i) for i in path])
+        _check(load().q3tts_tree_accept(self.h, int(stream_id), p, len(path)), "q3tts_tree_accept")
+
+    def beam_frame(self, stream_ids: Sequence[Sequence[int]], sampling, scores, uniforms, codes):
+        """q3tts_beam_frame: stream_ids [groups][beams]; scores CUDA fp32 [groups, beams]
+        (read and written); uniforms CUDA fp32 and codes CUDA int32 [groups * beams,
+        16].  Returns the parents, an int32 array [groups, beams]."""
+        import numpy as np
+        import torch
+        what = "q3tts_beam_frame"
+        groups, beams = len(stream_ids), len(stream_ids[0]) if stream_ids else 0
+        if any(len(g) != beams for g in stream_ids):
+            _bad(what, "stream_ids", "groups of equally many streams")
+        n = groups * beams
+        _need(scores, "scores", torch.float32, n, what)
+        self._check_frame_buffers(n, uniforms, codes, None, None, what)
+        ids = (C.c_int32 * max(1, n))(*[int(i) for g in stream_ids for i in g])
+        par = (C.c_int32 * max(1, n))()
+        sp = sampling_struct(sampling)
+        _check(load().q3tts_beam_frame(self.h, C.byref(sp), ids, groups, beams, scores.data_ptr(), uniforms.data_ptr(),
+                                       codes.data_ptr(), par), what)
+        return np.frombuffer(par, dtype=np.int32)[:n].reshape(groups, beams).copy()
 
     def kernel_launches(self) -> int:
         return int(load().q3tts_kernel_launches(self.h))

@@ -1,0 +1,488 @@
+"""The branching-decode operators on the GPU against their definitions in 64
+bits: tree attention, page copies, compaction, beam selection, reordering, and
+the five of them together as a search uses them."""
+import math
+
+import numpy as np
+import pytest
+
+from tests import branch_util as bu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q3():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from autoregressive_tts_decode_gb300 import build, q3tts
+    build.build()
+    return q3tts
+
+
+def tree_case(rng, lens, nodes, heads, kv_heads, hd, page, dtype, layers=2, parents=None):
+    import torch
+    pool, table = bu.paged_cache(rng, [a + b for a, b in zip(lens, nodes)], page, layers, kv_heads, hd, dtype)
+    masks = []
+    for i, n in enumerate(nodes):
+        masks += bu.tree_masks(parents[i] if parents else bu.tree_parents(rng, n))
+    start = np.concatenate([[0], np.cumsum(nodes)]).astype(np.int32)
+    gen = torch.Generator(device="cuda").manual_seed(int(rng.integers(1 << 31)))
+    q = torch.randn((len(masks), heads, hd), generator=gen, device="cuda")
+    return dict(pool=pool, table=table, lens=lens, nodes=nodes, masks=masks, q=q,
+                lengths=torch.tensor(lens, dtype=torch.int32, device="cuda"), start=torch.from_numpy(start).cuda())
+
+
+def run_tree(q3, c, layer=1, **kw):
+    return q3.tree_attention(c["pool"], layer, c["table"], c["lengths"], c["start"], bu.masks_tensor(c["masks"]),
+                             c["q"], max_nodes=max(1, max(c["nodes"])), **kw)
+
+
+def check_tree(c, out, layer=1):
+    want, tol = bu.tree_reference(c["pool"], layer, c["table"], c["lens"], c["nodes"], c["masks"], c["q"])
+    off = (out.double() - want).abs() / tol
+    assert bool((off <= 1).all()), f"{float(off.max()):.3g} of the bound"
+
+
+TREES = [
+    # lens, nodes, heads, kv heads, head dim, page
+    ([0], [1], 2, 1, 64, 16), ([1], [1], 4, 2, 128, 16), ([0], [64], 2, 1, 128, 16),
+    ([131], [8], 16, 8, 128, 16), ([127, 128, 129], [1, 1, 1], 4, 2, 128, 16),
+    ([15, 16, 17, 0], [1, 16, 17, 3], 4, 2, 64, 16), ([100, 0, 50], [0, 5, 0], 4, 2, 128, 16),
+    ([777, 3, 260], [64, 1, 33], 8, 2, 128, 16), ([500], [9], 3, 3, 64, 12), ([200, 31], [7, 2], 8, 1, 128, 8),
+    ([300], [20], 12, 3, 128, 32), ([129], [5], 4, 2, 64, 64), ([511], [40], 4, 4, 64, 128),
+    ([600], [13], 4, 2, 128, 256), ([70], [64], 16, 1, 64, 16), ([45], [6], 2, 1, 128, 1),
+    ([2048], [16], 16, 8, 128, 16), ([5000, 1], [3, 3], 2, 1, 64, 16), ([333], [17], 10, 2, 128, 24),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("case", TREES, ids=lambda c: "-".join(str(x) for x in c).replace(" ", ""))
+def test_tree_attention(q3, case, dtype):
+    import torch
+    c = tree_case(np.random.default_rng(7), *case, dtype=getattr(torch, dtype))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = run_tree(q3, c, status=status)
+    check_tree(c, out)
+    assert int(status) == 0
+
+
+def test_tree_attention_many_sequences(q3):
+    import torch
+    rng = np.random.default_rng(8)
+    lens, nodes = rng.integers(0, 700, 97).tolist(), rng.integers(0, 13, 97).tolist()
+    c = tree_case(rng, lens, nodes, 16, 8, 128, 16, torch.bfloat16)
+    check_tree(c, run_tree(q3, c))
+
+
+def test_chain_and_masks_that_see_nothing(q3):
+    """A chain is causal attention; a mask of zeroes sees the context only, and
+    without a context nothing: zeroes, whatever the cache holds."""
+    import torch
+    c = tree_case(np.random.default_rng(9), [40, 0, 0], [12, 4, 5], 4, 2, 128, 16, torch.bfloat16,
+                  parents=[list(range(-1, 11)), [-1, 0, 1, 2], [-1] * 5])
+    c["masks"][12 + 2] = 0
+    c["masks"][3] = 0
+    out = run_tree(q3, c)
+    check_tree(c, out)
+    assert bool((out[12 + 2] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_large_scores_and_masked_infinities(q3, dtype):
+    """Scores hundreds apart, rising along the context; infinities and NaN at
+    nodes that no mask shows."""
+    import torch
+    c = tree_case(np.random.default_rng(10), [400], [6], 4, 2, 128, 16, getattr(torch, dtype),
+                  parents=[[-1, 0, -1, 2, -1, 4]])
+    pos = torch.arange(406, device="cuda")
+    pg, slot = c["table"][0].long()[pos // 16], pos % 16
+    ramp = torch.linspace(0.02, 6.0, 406, device="cuda")[:, None, None, None]
+    k = c["pool"][:, pg, 0, :, slot]
+    c["pool"][:, pg, 0, :, slot] = (k.float() * ramp).to(k.dtype)
+    for j, bad in ((404, math.inf), (405, math.nan)):  # nodes 4 and 5
+        c["pool"][:, pg[j], :, :, slot[j]] = bad
+    c["nodes"], c["masks"] = [6], c["masks"][:4] + [1, 2]
+    out = run_tree(q3, c)
+    c["pool"][:, pg[404], :, :, slot[404]] = 0
+    c["pool"][:, pg[405], :, :, slot[405]] = 0
+    # an unseen value still meets a weight of zero: only the keys may be infinite
+    finite = torch.isfinite(out)
+    want, tol = bu.tree_reference(c["pool"], 1, c["table"], c["lens"], c["nodes"], c["masks"], c["q"])
+    assert bool(finite.all())
+    assert bool(((out.double() - want).abs() <= tol).all())
+
+
+def test_row_pitches_and_rows_left_alone(q3):
+    """q inside a wider buffer at an odd pitch, out likewise; rows behind the last
+    sequence and other columns keep their values."""
+    import torch
+    c = tree_case(np.random.default_rng(11), [33, 90], [5, 7], 4, 2, 64, 16, torch.bfloat16)
+    wide = torch.full((15, 4 * 64 + 37), 3.25, device="cuda")
+    wide[:12, 1:257] = c["q"].reshape(12, -1)
+    qv = wide[:, 1:257].unflatten(1, (4, 64))
+    outw = torch.full((15, 4 * 64 + 3), -7.5, device="cuda")
+    ov = outw[:, 3:].unflatten(1, (4, 64))
+    masks = torch.cat([bu.masks_tensor(c["masks"]), torch.zeros(3, dtype=torch.int64, device="cuda")])
+    q3.tree_attention(c["pool"], 1, c["table"], c["lengths"], c["start"], masks, qv, max_nodes=7, out=ov)
+    check_tree(c, ov[:12])
+    assert bool((outw[12:] == -7.5).all()) and bool((outw[:, :3] == -7.5).all())
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_bad_device_entries_are_reported(q3, dtype):
+    """Lengths, row offsets and page ids that do not fit: reported, the others'
+    rows are right, and the left-out rows keep their values."""
+    import torch
+    c = tree_case(np.random.default_rng(12), [20, 30, 40], [3, 3, 3], 4, 2, 64, 16, getattr(torch, dtype))
+    for change in ("length", "negative", "start", "page"):
+        lengths, start, table = c["lengths"].clone(), c["start"].clone(), c["table"].clone()
+        if change == "length":
+            lengths[1] = table.shape[1] * 16 - 2
+        elif change == "negative":
+            lengths[1] = -1
+        elif change == "start":
+            start[3] = 100
+        else:
+            table[1, 1] = c["pool"].shape[1]
+        out = torch.full_like(c["q"], -7.5)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        q3.tree_attention(c["pool"], 1, table, lengths, start, bu.masks_tensor(c["masks"]), c["q"], max_nodes=3,
+                          out=out, status=status)
+        assert int(status) == q3.ERR_ARG
+        want, tol = bu.tree_reference(c["pool"], 1, c["table"], c["lens"], c["nodes"], c["masks"], c["q"])
+        bad = slice(6, 9) if change == "start" else slice(3, 6)
+        ok = (out.double() - want).abs() <= tol
+        ok[bad] = True
+        assert bool(ok.all())
+        if change != "page":
+            assert bool((out[bad] == -7.5).all())
+
+
+def test_tree_attention_repeats_captures_and_follows_new_lengths(q3):
+    """The same bits on every run; a captured call replays with other lengths and
+    masks; two graphs of it replay side by side on two streams."""
+    import torch
+    c = tree_case(np.random.default_rng(13), [250, 61], [9, 4], 16, 8, 128, 16, torch.bfloat16)
+    masks = bu.masks_tensor(c["masks"])
+    first = run_tree(q3, c)
+    assert torch.equal(first, run_tree(q3, c))
+    outs = [torch.zeros_like(first) for _ in range(2)]
+    graphs, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for o, s in zip(outs, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+            q3.tree_attention(c["pool"], 1, c["table"], c["lengths"], c["start"], masks, c["q"], max_nodes=9, out=o)
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for g, s in zip(graphs, streams):
+        with torch.cuda.stream(s):
+            for _ in range(5):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(first, o) for o in outs)
+    c["lens"] = [100, 60]
+    c["lengths"].copy_(torch.tensor(c["lens"], dtype=torch.int32))
+    c["masks"] = bu.tree_masks([-1] * 9) + bu.tree_masks([-1, 0, 1, 2])
+    masks.copy_(bu.masks_tensor(c["masks"]))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    check_tree(c, outs[0])
+
+
+def test_cache_offsets_past_32_bits(q3):
+    """A cache of more than 2^32 elements: pages near its end are read and copied."""
+    import torch
+    pages = 70000
+    pool = torch.zeros((1, pages, 2, 4, 64, 128), dtype=torch.bfloat16, device="cuda")  # 4.6e9 elements, 9.2 GB
+    rng = np.random.default_rng(14)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    used = [pages - 1, pages - 5, 2]
+    for p in used:
+        pool[0, p] = torch.randn((2, 4, 64, 128), generator=gen, device="cuda").to(torch.bfloat16)
+    lens, nodes = [150], [20]
+    masks = bu.tree_masks(bu.tree_parents(rng, 20))
+    table = torch.tensor([used], dtype=torch.int32, device="cuda")
+    q = torch.randn((20, 4, 128), generator=gen, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = q3.tree_attention(pool, 0, table, torch.tensor(lens, **i32), torch.tensor([0, 20], **i32),
+                            bu.masks_tensor(masks), q, max_nodes=20)
+    want, tol = bu.tree_reference(pool, 0, table, lens, nodes, masks, q)
+    assert bool(((out.double() - want).abs() <= tol).all())
+    q3.copy_pages(pool, [pages - 1], [pages - 2])
+    assert torch.equal(pool[0, pages - 1], pool[0, pages - 2])
+
+
+# ------------------------------------------------------------------ pages
+@pytest.mark.parametrize("n", [1, 3, 449])
+@pytest.mark.parametrize("shape", [(2, 1, 16, 64), (3, 2, 12, 128), (1, 8, 16, 128), (5, 1, 1, 64)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_copy_pages(q3, n, shape, dtype):
+    import torch
+    layers, heads, page, hd = shape
+    pages = 2 * n + 3
+    pool = torch.randn((layers, pages, 2, heads, page, hd), device="cuda").to(getattr(torch, dtype))
+    want = pool.clone()
+    perm = np.random.default_rng(n).permutation(pages)[:2 * n]
+    src = perm[:n].tolist()
+    src[0] = src[-1]  # one page may be copied to several
+    want[:, perm[n:].tolist()] = want[:, src]
+    q3.copy_pages(pool, src, perm[n:].tolist())
+    assert torch.equal(pool, want)
+
+
+@pytest.mark.parametrize("page,hd,dtype", [(16, 128, "bfloat16"), (12, 64, "float32"), (1, 64, "bfloat16"),
+                                           (64, 128, "float32")])
+def test_compact_rows(q3, page, hd, dtype):
+    import torch
+    rng = np.random.default_rng(page)
+    lens, most = [0, 5, 31, 64, 100, 7], 64
+    pool, table = bu.paged_cache(rng, [n + most for n in lens], page, 3, 2, hd, getattr(torch, dtype))
+    paths = [list(range(64)), [], [0, 1, 5, 6, 63], sorted(rng.permutation(64)[:40].tolist()), [63],
+             list(range(1, 64))]
+    path = np.full((len(lens), most), -9, np.int32)
+    for s, p in enumerate(paths):
+        path[s, :len(p)] = p
+    want = pool.clone()
+    for s, p in enumerate(paths):
+        for to, of in enumerate(p):
+            a, b = lens[s] + of, lens[s] + to
+            want[:, table[s, b // page], :, :, b % page] = pool[:, table[s, a // page], :, :, a % page]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, **i32)
+    q3.compact_rows(pool, table, torch.tensor(lens, **i32), torch.from_numpy(path).cuda(),
+                    torch.tensor([len(p) for p in paths], **i32), status=status)
+    assert torch.equal(torch.nan_to_num(pool.float()), torch.nan_to_num(want.float())) and int(status) == 0
+
+
+@pytest.mark.parametrize("bad", ["descending", "twice", "negative", "long", "count", "length"])
+def test_compact_rows_leaves_bad_sequences(q3, bad):
+    import torch
+    rng = np.random.default_rng(5)
+    pool, table = bu.paged_cache(rng, [40, 40], 16, 2, 2, 64, torch.bfloat16)
+    before = pool.clone()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    path = {"descending": [3, 2, 5], "twice": [2, 2, 5], "negative": [-1, 2, 5], "long": [1, 2, 40]}.get(bad, [1, 2, 5])
+    lengths, count = [30, 30], [3, 3]
+    if bad == "count":
+        count[0] = 4
+    if bad == "length":
+        lengths[0] = -1
+    status = torch.zeros(1, **i32)
+    q3.compact_rows(pool, table, torch.tensor(lengths, **i32), torch.tensor([path, [1, 2, 5]], **i32),
+                    torch.tensor(count, **i32), status=status)
+    assert int(status) == q3.ERR_ARG
+    seq0 = table[0].long()
+    seq0 = seq0[seq0 < pool.shape[1]]
+    assert torch.equal(torch.nan_to_num(pool[:, seq0].float()), torch.nan_to_num(before[:, seq0].float()))
+    a, b = 31, 30
+    assert torch.equal(pool[:, table[1, b // 16], :, :, b % 16], before[:, table[1, a // 16], :, :, a % 16])
+
+
+# ------------------------------------------------------------------ beams
+def run_beam(q3, logits, scores, k, **kw):
+    import torch
+    for n in ("history", "finished"):
+        if kw.get(n) is not None:
+            kw[n] = torch.from_numpy(kw[n]).cuda()
+    return [t.cpu().numpy() for t in q3.beam_select(torch.from_numpy(logits).cuda(), torch.from_numpy(scores).cuda(),
+                                                    k=k, **kw)]
+
+
+def check_beam(got, logits, scores, k, history=None, finished=None, eos_token=-1, special_from=0,
+               repetition_penalty=1.0):
+    """The scores' order decides; candidates closer than the fp32 sums can tell
+    (each exponential and sum within a few 2^-24 of the row's sum: 2^-20 covers
+    vocabularies up to 2^17 summed in fp32 by 512 threads) may swap."""
+    kw = dict(history=history, finished=finished, eos=eos_token, special=special_from, penalty=repetition_penalty)
+    tok, par, best = bu.beam_reference(logits, scores, k, **kw)
+    sc, _ = bu.beam_scores(logits, scores, **kw)
+    gt, gp, gs = got
+    live = best > -np.inf
+    assert np.array_equal(gt == -1, ~live) and np.all(gp[~live] == 0) and np.all(np.isneginf(gs[~live]))
+    eps = 2.0 ** -20
+    assert np.all(np.abs(gs[live] - best[live]) <= eps + 2.0 ** -24 * np.abs(best[live]))
+    for g, j in zip(*np.nonzero(live)):
+        assert abs(sc[g, gp[g, j], gt[g, j]] - best[g, j]) <= eps
+    for g in range(gt.shape[0]):
+        pairs = [(int(a), int(b)) for a, b, ok in zip(gp[g], gt[g], live[g]) if ok]
+        assert len(set(pairs)) == len(pairs)
+    return np.array_equal(gt, tok) and np.array_equal(gp, par)
+
+
+@pytest.mark.parametrize("groups,beams,k,vocab", [(1, 1, 1, 1), (1, 1, 4, 7), (3, 4, 4, 2048), (2, 5, 3, 4095),
+                                                  (1, 32, 32, 4096), (2, 3, 32, 33), (1, 1, 8, 100003),
+                                                  (2, 2, 5, 32768), (5, 16, 16, 8193), (1, 2, 32, 9)])
+def test_beam_select(q3, groups, beams, k, vocab):
+    rng = np.random.default_rng(vocab + k)
+    logits = (3 * rng.standard_normal((groups, beams, vocab))).astype(np.float32)
+    scores = (-5 * rng.random((groups, beams))).astype(np.float32)
+    assert check_beam(run_beam(q3, logits, scores, k), logits, scores, k)
+
+
+@pytest.mark.parametrize("vocab", [50, 2048, 20001])
+def test_beam_select_rules(q3, vocab):
+    """Penalty, special codes, finished beams, dead beams."""
+    rng = np.random.default_rng(vocab)
+    g, b, k = 4, 6, 6
+    logits = (2 * rng.standard_normal((g, b, vocab))).astype(np.float32)
+    scores = (-5 * rng.random((g, b))).astype(np.float32)
+    scores[1, 2:] = -np.inf
+    scores[2, 0] = np.nan
+    kw = dict(history=(rng.random((g, b, vocab)) < 0.3).astype(np.uint8),
+              finished=(rng.random((g, b)) < 0.4).astype(np.uint8), eos_token=vocab - 3, special_from=vocab - 20,
+              repetition_penalty=1.3)
+    kw["finished"][3] = 1
+    assert check_beam(run_beam(q3, logits, scores, k, **dict(kw)), logits, scores, k, **kw)
+
+
+@pytest.mark.parametrize("vocab", [6, 2048, 8192, 40000])
+@pytest.mark.parametrize("kind", ["equal", "ascending", "descending", "masked", "infinite", "nan", "huge"])
+def test_beam_select_hard_rows(q3, kind, vocab):
+    """Equal logits (the lower code, the lower beam first), sorted ones, rows with
+    little or nothing to pick, infinities and NaN."""
+    g, b, k = 2, 3, 8
+    rng = np.random.default_rng(vocab)
+    logits = np.zeros((g, b, vocab), np.float32)
+    scores = np.zeros((g, b), np.float32)
+    if kind == "ascending":
+        logits += np.arange(vocab, dtype=np.float32) / 64
+    elif kind == "descending":
+        logits -= np.arange(vocab, dtype=np.float32) / 64
+    elif kind == "masked":
+        logits[:] = -np.inf
+        logits[0, 1, vocab // 2] = 1.5
+        logits[0, 2, [0, vocab - 1]] = -3e38
+    elif kind == "infinite":
+        logits = rng.standard_normal((g, b, vocab)).astype(np.float32)
+        logits[0, 0, [1, 4]] = np.inf
+        logits[1, :, 3] = np.inf
+        logits[1, 1, 0] = -np.inf
+    elif kind == "nan":
+        logits = rng.standard_normal((g, b, vocab)).astype(np.float32)
+        logits[0, 0, ::2] = np.nan
+        logits[1, 1] = np.nan
+    elif kind == "huge":
+        logits = (1e38 * rng.standard_normal((g, b, vocab)).clip(-3, 3)).astype(np.float32)
+    assert check_beam(run_beam(q3, logits, scores, k), logits, scores, k)
+
+
+def test_beam_select_row_ids_pitch_and_in_place_scores(q3):
+    import torch
+    rng = np.random.default_rng(21)
+    rows, vocab = 11, 1001
+    full = (2 * rng.standard_normal((rows, vocab + 6))).astype(np.float32)
+    hist = (rng.random((rows, vocab)) < 0.2).astype(np.uint8)
+    fin = (rng.random(rows) < 0.3).astype(np.uint8)
+    ids = rng.permutation(rows)[:6].reshape(2, 3).astype(np.int32)
+    scores = (-rng.random((2, 3))).astype(np.float32)
+    lg = torch.from_numpy(full).cuda()[:, 3:3 + vocab]
+    sc = torch.from_numpy(scores).cuda()
+    out = (torch.zeros((2, 3), dtype=torch.int32, device="cuda"), torch.zeros((2, 3), dtype=torch.int32, device="cuda"),
+           sc)
+    kw = dict(eos_token=5, repetition_penalty=1.2)
+    q3.beam_select(lg, sc, row_ids=torch.from_numpy(ids).cuda(), history=torch.from_numpy(hist).cuda(),
+                   finished=torch.from_numpy(fin).cuda(), out=out, **kw)
+    assert check_beam([t.cpu().numpy() for t in out], full[ids][..., 3:3 + vocab], scores, 3, history=hist[ids],
+                      finished=fin[ids], **kw)
+
+
+@pytest.mark.parametrize("tail,dtype", [((64,), "float32"), ((7,), "uint8"), ((3, 5), "float32"), ((), "uint8"),
+                                        ((2000,), "bfloat16"), ((4099,), "int64")])
+@pytest.mark.parametrize("groups,beams,k", [(1, 1, 1), (3, 4, 4), (2, 3, 7), (1, 32, 32), (2, 9, 2)])
+def test_reorder_rows(q3, tail, dtype, groups, beams, k):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    src = torch.randint(0, 200, (groups, beams) + tail, generator=gen, device="cuda").to(getattr(torch, dtype))
+    par = torch.randint(0, beams, (groups, k), generator=gen, device="cuda").int()
+    want = torch.stack([src[g, par[g].long()] for g in range(groups)])
+    dst = torch.empty_like(want)
+    q3.reorder_rows([src], [dst], par)
+    assert torch.equal(dst, want)
+    if beams == k:
+        sets = [src.clone() for _ in range(9)]  # more sets than one launch takes
+        q3.reorder_rows(sets, sets, par)
+        assert all(torch.equal(t, want) for t in sets)
+
+
+def test_reorder_rows_reports_bad_parents(q3):
+    import torch
+    for inplace in (False, True):
+        src = torch.arange(12, device="cuda", dtype=torch.float32).reshape(1, 3, 4).clone()
+        dst = src if inplace else torch.full_like(src, -1)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        par = torch.tensor([[2, 3, 0]], dtype=torch.int32, device="cuda")
+        want = [8.0, 4.0 if inplace else -1.0, 0.0]
+        q3.reorder_rows([src], [dst], par, status=status)
+        assert int(status) == q3.ERR_ARG and dst[0, :, 0].tolist() == want
+
+
+# --------------------------------------------------------------- together
+def test_a_search_step_with_the_operators(q3):
+    """Trees are scored for two sequences, paths accepted, a page forked, beams
+    selected and their states moved: each step reads what the one before wrote,
+    on a stream other than the default, and captured into a graph."""
+    import torch
+    rng = np.random.default_rng(30)
+    c = tree_case(rng, [37, 90], [6, 6], 8, 4, 128, 16, torch.bfloat16,
+                  parents=[[-1, 0, 0, 1, 3, 2], [-1, -1, 1, 2, 2, 4]])
+    paths = [[0, 2, 5], [1, 2, 4]]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    path, count = torch.tensor(paths, **i32), torch.tensor([3, 3], **i32)
+    after = c["lengths"] + count
+    one = torch.tensor([0, 1, 2], **i32)
+    bit = torch.zeros(2, dtype=torch.int64, device="cuda")
+    spare = [p for p in range(c["pool"].shape[1]) if p not in c["table"].flatten().tolist()]
+    last = int(c["table"][0, 39 // 16])
+    q2 = torch.randn((2, 8, 128), device="cuda")
+    logits, scores = torch.randn((1, 2, 500), device="cuda"), torch.zeros((1, 2), device="cuda")
+    state, moved = torch.randn((1, 2, 65), device="cuda"), torch.empty((1, 2, 65), device="cuda")
+    before = c["pool"].clone()
+    res = {}
+
+    def step():
+        res["tree"] = run_tree(q3, c)
+        q3.compact_rows(c["pool"], c["table"], c["lengths"], path, count)
+        res["next"] = q3.tree_attention(c["pool"], 1, c["table"], after, one, bit, q2, max_nodes=1)
+        q3.copy_pages(c["pool"], [last], [spare[0]])
+        res["beam"] = q3.beam_select(logits, scores)
+        q3.reorder_rows([state], [moved], res["beam"][1])
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for captured in (False, True):
+        c["pool"].copy_(before)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            if captured:
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g, stream=s):
+                    res["tree"] = q3.tree_attention(c["pool"], 1, c["table"], c["lengths"], c["start"], res["m"],
+                                                    c["q"], max_nodes=6)
+                    q3.compact_rows(c["pool"], c["table"], c["lengths"], path, count)
+                    res["next"] = q3.tree_attention(c["pool"], 1, c["table"], after, one, bit, q2, max_nodes=1)
+                    q3.copy_pages(c["pool"], [last], [spare[0]])
+                    res["beam"] = q3.beam_select(logits, scores)
+                    q3.reorder_rows([state], [moved], res["beam"][1])
+                g.replay()
+            else:
+                res["m"] = bu.masks_tensor(c["masks"])
+                step()
+        torch.cuda.synchronize()
+        kept, c["pool"] = c["pool"], before
+        check_tree(c, res["tree"])
+        c["pool"] = kept
+        # the accepted nodes' rows now follow the context, and the node that
+        # attends to the context alone sees them
+        for i, p in enumerate(paths):
+            for to, of in enumerate(p):
+                a, b = c["lens"][i] + of, c["lens"][i] + to
+                assert torch.equal(c["pool"][:, c["table"][i, b // 16], :, :, b % 16],
+                                   before[:, c["table"][i, a // 16], :, :, a % 16])
+        full = torch.nan_to_num(c["pool"])
+        want, tol = bu.tree_reference(full, 1, c["table"], after.tolist(), [1, 1], [0, 0], q2)
+        assert bool(((res["next"].double() - want).abs() <= tol).all())
+        assert torch.equal(torch.nan_to_num(c["pool"][:, spare[0]].float()), torch.nan_to_num(c["pool"][:, last].float()))
+        tok, par, best = (t.cpu().numpy() for t in res["beam"])
+        assert check_beam([tok, par, best], logits.cpu().numpy(), scores.cpu().numpy(), 2)
+        assert torch.equal(moved, state[:, par[0].tolist()])
