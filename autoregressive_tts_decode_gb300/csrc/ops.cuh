@@ -40,7 +40,7 @@ struct TreeArgs {
   int ldo;
   int* status;
 };
-int launch_tree_attention(const TreeArgs& a, int kdt, cudaStream_t s);
+int launch_tree_attention(const TreeArgs& a, int layers, int kdt, cudaStream_t s);
 
 // Page copies and compaction (kv_pages.cu).
 int launch_copy_pages(const KVDesc& kv, int layers, int esz, const int32_t* src, const int32_t* dst, int n,

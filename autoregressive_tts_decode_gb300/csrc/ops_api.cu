@@ -95,7 +95,7 @@ int q3tts_tree_attention(const q3tts_kv_cache* kv, int layer, const int32_t* pag
   a.out = out_dev;
   a.ldo = ldo;
   a.status = status_dev;
-  return q3::launch_tree_attention(a, kv->kv_dtype, (cudaStream_t)cuda_stream);
+  return q3::launch_tree_attention(a, kv->layers, kv->kv_dtype, (cudaStream_t)cuda_stream);
 }
 
 int q3tts_copy_pages(const q3tts_kv_cache* kv, const int32_t* src, const int32_t* dst, int n, void* cuda_stream) {

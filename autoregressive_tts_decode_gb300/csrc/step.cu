@@ -272,7 +272,7 @@ static void stack_pass(q3tts_handle* h, const q3tts_layer_weights* lw, int layer
                           h->c.qk_norm, h->c.rms_eps, h->rope_cos, h->rope_sin, kv, l, h->Hq, s);
     if (tree) {
       tree->layer = l;
-      if (launch_tree_attention(*tree, kdt, s) != Q3TTS_OK) h->tc_failed = true;
+      if (launch_tree_attention(*tree, layers, kdt, s) != Q3TTS_OK) h->tc_failed = true;
     }
     // a prefill chunk: query tiles on the tensor cores; contexts longer than
     // one span: spread over the GPU by span

@@ -19,33 +19,13 @@
 #include <cooperative_groups.h>
 
 #include "ops.cuh"
+#include "tree.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace q3 {
 
 namespace {
-
-// What a CTA works on; false when it has no rows.  Lengths and row offsets
-// come from device memory, so they are checked here: a sequence whose entries
-// do not fit the cache or the buffers is left out and reported.
-struct TreeSeq {
-  int L, T, row0, P;  // committed positions, nodes, first row of q/out, L + T
-};
-__device__ __forceinline__ bool tree_seq(const TreeArgs& a, int seq, TreeSeq& t) {
-  t.L = a.lengths[seq];
-  t.row0 = a.node_start[seq];
-  const int end = a.node_start[seq + 1];
-  const long long cap = (long long)a.kv.pages_per_stream * a.kv.page_size;
-  if (t.row0 < 0 || end < t.row0 || end > a.n_rows || end - t.row0 > a.max_nodes || t.L < 0 ||
-      (long long)t.L + (end - t.row0) > cap) {
-    op_status(a.status, Q3TTS_ERR_ARG);
-    return false;
-  }
-  t.T = end - t.row0;
-  t.P = t.L + t.T;
-  return t.T > 0;
-}
 
 // Element offset of (position, k|v, kv head) of a sequence; a page id outside
 // the pool is reported and page 0 read in its place.
@@ -279,14 +259,6 @@ __global__ void __launch_bounds__(TF_THREADS) tree_fma_kernel(TreeArgs a, int ro
   cl.sync();  // the others may still read this CTA's shared memory
 }
 
-// CTAs of a cluster: enough to give every SM work, no more than there are
-// tiles at the sequences' capacity, at most 8 (the portable cluster size).
-int cluster_size(long items, int tiles, int n_sm) {
-  int c = 1;
-  while (c < 8 && items * c * 2 <= n_sm && c * 2 <= tiles) c *= 2;
-  return c;
-}
-
 template <class KT, int HD, int RT>
 int launch_fma(const TreeArgs& a, int dev, int n_sm, cudaStream_t s) {
   using C = TfCfg<KT, HD, RT>;
@@ -300,7 +272,7 @@ int launch_fma(const TreeArgs& a, int dev, int n_sm, cudaStream_t s) {
   const int rep = a.Hq / a.kv.Hkv, row_tiles = (a.max_nodes * rep + RT - 1) / RT;
   const long items = (long)a.n_seqs * a.kv.Hkv * row_tiles;
   const int tiles = (int)(((long)a.kv.pages_per_stream * a.kv.page_size + TF_PT - 1) / TF_PT);
-  const int c = cluster_size(items, tiles, 4 * n_sm);
+  const int c = tree_cluster(items, tiles, 4 * n_sm);
   if (items * c > 0x7fffffffL) return Q3TTS_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * c));
@@ -328,10 +300,17 @@ int launch_fma_any(const TreeArgs& a, int dev, int n_sm, cudaStream_t s) {
 
 }  // namespace
 
-int launch_tree_attention(const TreeArgs& a, int kdt, cudaStream_t s) {
+int tree_cluster(long items, int tiles, long slots) {
+  int c = 1;
+  while (c < 8 && items * c * 2 <= slots && c * 2 <= tiles) c *= 2;
+  return c;
+}
+
+int launch_tree_attention(const TreeArgs& a, int layers, int kdt, cudaStream_t s) {
   if (a.n_seqs <= 0 || a.n_rows <= 0) return Q3TTS_OK;
   int dev = 0, n_sm = 0;
   if (!current_device(&dev, &n_sm)) return Q3TTS_ERR_CUDA;
+  if (tree_mma_ok(a, layers, kdt)) return launch_tree_mma(a, layers, dev, n_sm, s);
   return kdt == Q3TTS_BF16 ? launch_fma_any<bf16>(a, dev, n_sm, s) : launch_fma_any<float>(a, dev, n_sm, s);
 }
 

@@ -1,0 +1,901 @@
+// tree_mma.cu -- attention of drafted tree nodes on the 5th-generation tensor
+// cores, for bf16 caches (tree_attention.cu has the definition and the fp32
+// form for the other shapes).
+//
+// The few query rows that share a kv head (nodes x q heads of the group) are
+// the MMA's N side, 128 cached positions its M side, so that one row costs no
+// more lanes than sixteen:
+//   S^T = K Q^T   M 128 positions, K the head dimension; K arrives by TMA, page
+//                 by page, as it lies in the cache;
+//   P^T = 2^(c S^T - base)  c = log2(e) / sqrt(hd), in registers, a running
+//                 base per row;
+//   O^T = V^T P^T M the head dimension, K 128 positions; V is read as it lies in
+//                 the cache (an M-major operand).
+// The base of a row follows its largest score only when a score passes it by
+// more than 2^8: until then weights up to 256 are exact multiples that the
+// final division removes, and a tile needs one vote of the softmax threads
+// instead of a maximum over them.
+//
+// Precision.  Keys and values are bf16 as cached; Q and P enter as three bf16
+// terms each, which hold all 24 bits of an fp32 value (two terms of P alone
+// leave 2e-6 of the output).  The terms are stacked along N, so that a tile of
+// K or V is read from shared memory once for all of them; each has its own
+// accumulator columns (of 64 rows, the two small ones share) and they are added
+// in fp32 registers, like the outputs of successive tiles: the tensor cores
+// truncate as they accumulate, and summed in tensor memory over 32768 positions
+// the error was 3.7e-5 of the output.
+//
+// Roles of a CTA (one per SM): one warp issues the TMA loads into a ring of K
+// and V tiles, one thread the MMAs (scores of tile t + 1 before the outputs of
+// tile t), four warps are the softmax and two bring in the queries.  A CTA works
+// through several items (sequence, kv head, tile of rows) and the roles run
+// ahead into the next one, so only the first pays the latency of its start.
+// Items are dealt longest first, in rounds of alternating direction: on 128
+// sequences of 256..2048 positions the SMs then end together.
+// The bound is the cache's bytes, read once for up to 64 rows.
+// Every wait is bounded; on expiry the CTA records Q3TTS_ERR_TIMEOUT, waits
+// (bounded) for its copies and MMAs in flight, frees its tensor memory and
+// writes nothing more.
+#include <cooperative_groups.h>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "ops.cuh"
+#include "tree.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace q3 {
+
+namespace {
+
+constexpr int TM_PT = 128;       // positions of a tile
+constexpr int TM_THREADS = 256;  // softmax warps 0..3, TMA warp 4, MMA warp 5, query warps 6 and 7
+constexpr int TM_QTHREADS = 64;
+constexpr int TM_SORT = 256;     // sequences that are dealt by length
+constexpr int TM_MASKS = 4;      // items whose masks are held: the softmax's, and the scores may be three ahead
+constexpr long long TM_WAIT_CYCLES = 4000000000ll;  // ~2 s
+constexpr float TM_FLOOR = -1e30f;  // base of a row that has seen nothing: below every score
+constexpr float TM_SLACK = 8.f;     // how far (log2) a score may pass its row's base
+
+template <int HD, int N>
+struct TmCfg {
+  static constexpr int BLK = HD / 64;               // 128-byte swizzle blocks of a row
+  static constexpr uint32_t SLOT = TM_PT * HD * 2;  // a K or V tile
+  static constexpr uint32_t TERM = N * 128;         // one term of one 64-element block (of Q or P)
+  static constexpr uint32_t QBYTES = BLK * 3 * TERM, PBYTES = 2 * 3 * TERM;
+  static constexpr int G = N <= 32 ? 3 : 2;         // accumulator groups: the terms, or the large one and the others
+  static constexpr int NP = N <= 32 ? 2 : 1;        // P buffers
+  static constexpr uint32_t Q = 0, P = QBYTES, RING = P + NP * PBYTES;
+  static constexpr uint32_t CTL_BYTES = 6144;
+  static constexpr int FIT = (int)((227u * 1024 - 1024 - CTL_BYTES - RING) / SLOT);
+  static constexpr int S = FIT < 8 ? FIT : 8;       // tiles in the ring
+  static constexpr uint32_t CTL = RING + S * SLOT;
+  static constexpr size_t SMEM = 1024 + CTL + CTL_BYTES;
+  static constexpr uint32_t TM_S = G * N, TM_O = 2 * TM_S;  // columns: S twice, O twice
+  static constexpr uint32_t TMEM_COLS = 4 * G * N <= 256 ? 256 : 512;
+  // three: the softmax of tile t waits for V_t, which takes the place of K_t at the latest
+  static_assert(S >= 3 && 4 * G * N <= 512 && N * HD * 4 <= (int)(S * SLOT), "ring, tensor memory, joined output");
+};
+
+// Control block (shared memory).
+template <int N, int S>
+struct TmCtl {
+  unsigned long long full[S], empty[S], s_full[2], s_free[2], p_full[2], p_free[2], q_full[TM_MASKS], q_free, done;
+  uint32_t tmem;
+  int abort_w;
+  float base[N], corr[N], sum[N];  // a row's base, the factor of its last rise, its sum of weights
+  float part[4][N];
+  unsigned long long mask[TM_MASKS][N];
+  uint16_t order[TM_SORT];  // sequences, longest first
+};
+
+__device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(uint32_t b, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(b), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 128-byte swizzled operand tiles: rows of 128 bytes, 8-row atoms 1024 bytes
+// apart (stride byte offset), descriptor version 1, swizzle mode 2.  K-major:
+// the leading offset is not used.  M-major (V^T: 64 head-dim elements are a
+// row's 128 bytes, positions the rows): the leading offset is the distance of
+// the second 64 elements' block.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lead = 16) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lead & 0x3FFFFu) >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16: D fp32, A and B bf16, B K-major; A K-major or M-major (bit 15).
+__host__ __device__ constexpr uint32_t f16_idesc(int M, int N, bool a_m_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_m_major ? 1u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(
+          tmem_d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// 16 fp32 columns of the warp's 32 lanes, one lane per thread (complete after wait::ld).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// N fp32 columns of 16 lanes, eight columns at a time in the fragment order of
+// an 8 x 8 matrix store: registers 4 b and 4 b + 1 hold columns 8 b + 2 (lane % 4)
+// and the next of lane / 4, registers 4 b + 2 and 4 b + 3 the same of
+// lane / 4 + 8.
+template <int N>
+__device__ __forceinline__ void tmem_frag(uint32_t taddr, uint32_t (&r)[N / 2]);
+template <>
+__device__ __forceinline__ void tmem_frag<16>(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+template <>
+__device__ __forceinline__ void tmem_frag<32>(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr));
+}
+// Four 8 x 8 matrices of 16-bit elements, transposed on the way: matrix m goes
+// to the rows at lanes 8 m .. 8 m + 7's addresses.
+__device__ __forceinline__ void store_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+// Pairs of floats (one 64-bit register pair, one instruction each).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
+      " mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// Two floats to bf16 (x in the low half).
+__device__ __forceinline__ uint32_t pack_bf16(float2 v) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Barrier and vote of the 128 softmax threads.
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool soft_any(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)p)
+      : "memory");
+  return r != 0;
+}
+
+// Bounded wait on an mbarrier phase; false on expiry or when another role of
+// the CTA has given up.
+__device__ __forceinline__ bool tm_wait(uint32_t bar, uint32_t parity, volatile int* abort_w, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  unsigned it = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    if ((++it & 63u) == 0) {
+      if (*abort_w) return false;
+      if (clock64() - t0 > TM_WAIT_CYCLES) {
+        *abort_w = 1;
+        op_status(status, Q3TTS_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
+// Max or sum over the lanes that hold the same columns (lane % 4).
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Ring position of tile t's K and V among n tiles: K0 K1 V0 K2 V1 .. V(n-1).
+__device__ __forceinline__ int k_item(int t) { return t == 0 ? 0 : 2 * t - 1; }
+__device__ __forceinline__ int v_item(int t, int n) { return t == n - 1 ? 2 * n - 1 : 2 * t + 2; }
+
+// One item of work.
+struct TmItem {
+  TreeSeq t;
+  int seq, g, n0, rows;  // kv head, first row of the tile, rows
+  int t0, nt;            // first position tile, tiles
+};
+
+template <int HD, int N>
+__global__ void __launch_bounds__(TM_THREADS, 1)
+    tree_mma_kernel(const __grid_constant__ CUtensorMap map, TreeArgs a, int row_tiles, int box, int items, int vec) {
+  using C = TmCfg<HD, N>;
+  using Ctl = TmCtl<N, C::S>;
+  static_assert(sizeof(Ctl) <= C::CTL_BYTES, "control block");
+  extern __shared__ uint8_t tm_raw[];
+  const uint32_t raw = su32(tm_raw), sbase = (raw + 1023u) & ~1023u;
+  uint8_t* sp = tm_raw + (sbase - raw);
+  Ctl& ctl = *reinterpret_cast<Ctl*>(sp + C::CTL);
+  volatile int* abort_w = &ctl.abort_w;
+
+  cg::cluster_group cl = cg::this_cluster();
+  const int CL = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rep = a.Hq / a.kv.Hkv;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::S; ++i) {
+      mbar_init(su32(&ctl.full[i]), 1);
+      mbar_init(su32(&ctl.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(su32(&ctl.s_full[i]), 1);
+      mbar_init(su32(&ctl.s_free[i]), 128);
+      mbar_init(su32(&ctl.p_full[i]), 128);
+      mbar_init(su32(&ctl.p_free[i]), 1);
+    }
+    for (int i = 0; i < TM_MASKS; ++i) mbar_init(su32(&ctl.q_full[i]), TM_QTHREADS);
+    mbar_init(su32(&ctl.q_free), 1);
+    mbar_init(su32(&ctl.done), 1);
+    ctl.abort_w = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&ctl.tmem)),
+                 "r"(C::TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();  // q and the appended keys and values come from the previous kernels
+  const bool sorted = items > (int)gridDim.x / CL && a.n_seqs <= TM_SORT;
+  if (sorted && tid < a.n_seqs) {
+    const int mine = a.lengths[tid];
+    int r = 0;
+    for (int j = 0; j < a.n_seqs; ++j) {
+      const int o = a.lengths[j];
+      r += o > mine || (o == mine && j < tid);
+    }
+    ctl.order[r] = (uint16_t)tid;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  const uint32_t ring = sbase + C::RING;
+
+  // The k-th item of this CTA: 1 if there is one, 0 if it has no rows (or does
+  // not fit, which is reported), -1 past the last.
+  const int stride = (int)gridDim.x / CL, first = (int)blockIdx.x / CL;
+  auto get_item = [&](int k, TmItem& m) -> int {
+    if ((long long)k * stride >= items) return -1;
+    const int idx = k * stride + ((k & 1) ? stride - 1 - first : first);
+    if (idx >= items) return 0;
+    const int rt = idx % row_tiles;
+    m.g = idx / row_tiles % a.kv.Hkv;
+    m.seq = idx / row_tiles / a.kv.Hkv;
+    if (sorted) m.seq = ctl.order[m.seq];
+    m.n0 = rt * N;
+    if (!tree_seq(a, m.seq, m.t) || m.n0 >= m.t.T * rep) return 0;
+    m.rows = min(N, m.t.T * rep - m.n0);
+    const int all = (m.t.P + TM_PT - 1) / TM_PT, per = (all + CL - 1) / CL;
+    m.t0 = min(all, rank * per);
+    m.nt = min(all, m.t0 + per) - m.t0;
+    return 1;
+  };
+  TmItem m;
+  int have = 0;
+  bool ok = true;
+
+  if (warp == 4) {
+    // ---- TMA: lane (b, blk) copies block blk of page b's rows of a tile
+    const int b = lane / C::BLK, blk = lane % C::BLK;
+    const int boxes = TM_PT / box;
+    const int ps = a.kv.page_size;
+    const long long plane = (long long)a.kv.Hkv * ps;  // rows of a page's keys (or values)
+    int ic = 0;                                        // tiles put into the ring
+    for (int k = 0; ok && (have = get_item(k, m)) >= 0; ++k) {
+      if (have == 0 || m.nt == 0) continue;
+      const int* table = a.kv.page_table + (size_t)m.seq * a.kv.pages_per_stream;
+      // first row of this lane's box in tile i (keys), or -1 past the sequence
+      auto box_row = [&](int i) -> int {
+        const int pos = (m.t0 + i) * TM_PT + b * box;
+        if (b >= boxes || i >= m.nt || pos >= m.t.P) return -1;
+        int page = table[pos / ps];
+        if (page < 0 || page >= a.kv.n_pages) {
+          op_status(a.status, Q3TTS_ERR_ARG);
+          page = 0;
+        }
+        return (int)((((long long)a.layer * a.kv.n_pages + page) * 2) * plane + (long long)m.g * ps + pos % ps);
+      };
+      int row_even = box_row(0), row_odd = box_row(1);
+      for (int i = 0; i < 2 * m.nt; ++i, ++ic) {
+        const bool is_v = i == 2 * m.nt - 1 || (i >= 2 && (i & 1) == 0);
+        const int tile = is_v ? (i == 2 * m.nt - 1 ? m.nt - 1 : i / 2 - 1) : (i + 1) / 2;
+        const int row = (tile & 1) ? row_odd : row_even;
+        const int slot = ic % C::S;
+        const uint32_t fb = su32(&ctl.full[slot]);
+        ok = __all_sync(0xffffffffu,
+                        tm_wait(su32(&ctl.empty[slot]), ((uint32_t)(ic / C::S) & 1u) ^ 1u, abort_w, a.status));
+        if (!ok) break;
+        const int held = min(TM_PT, m.t.P - (m.t0 + tile) * TM_PT);
+        if (lane == 0) mbar_expect_tx(fb, (uint32_t)((held + box - 1) / box * box * HD * 2));
+        __syncwarp();
+        if (row >= 0)
+          tma_load(ring + slot * C::SLOT + blk * (TM_PT * 128) + b * box * 128, &map, blk * 64,
+                   row + (is_v ? (int)plane : 0), fb);
+        if (is_v) {  // the tile's row is done with: the one two tiles on takes its place
+          if (tile & 1) row_odd = box_row(tile + 2); else row_even = box_row(tile + 2);
+        }
+      }
+    }
+    // copies in flight land before the CTA may leave
+    for (int j = ic > C::S ? ic - C::S : 0; j < ic; ++j) {
+      const long long c0 = clock64();
+      while (!mbar_try_wait(su32(&ctl.full[j % C::S]), (uint32_t)(j / C::S) & 1u) && clock64() - c0 < TM_WAIT_CYCLES) {
+      }
+    }
+  } else if (warp == 5) {
+    // ---- MMA issue
+    if (lane == 0) {
+      constexpr uint32_t idS = f16_idesc(TM_PT, (C::G == 3 ? 3 : 2) * N, false), idS1 = f16_idesc(TM_PT, N, false);
+      constexpr uint32_t idO = f16_idesc(TM_PT, (C::G == 3 ? 3 : 2) * N, true), idO1 = f16_idesc(TM_PT, N, true);
+      // a head dimension of 64 fills half of M: the other half's rows are read
+      // from the next atom and their results are not used
+      constexpr uint32_t v_lead = HD == 128 ? TM_PT * 128 : 1024;
+      int ic = 0, tc = 0, qi = 0;  // ring tiles, position tiles and items so far
+      for (int k = 0; ok && (have = get_item(k, m)) >= 0; ++k) {
+        if (have == 0 || m.nt == 0) continue;
+        ok = tm_wait(su32(&ctl.q_full[qi % TM_MASKS]), (uint32_t)(qi / TM_MASKS) & 1u, abort_w, a.status);
+        tc_fence_after();
+        for (int i = 0; i <= m.nt && ok; ++i) {
+          if (i < m.nt) {  // scores of tile i
+            const int it = ic + k_item(i), slot = it % C::S, t = tc + i;
+            ok = tm_wait(su32(&ctl.full[slot]), (uint32_t)(it / C::S) & 1u, abort_w, a.status) &&
+                 tm_wait(su32(&ctl.s_free[t & 1]), ((uint32_t)(t >> 1) & 1u) ^ 1u, abort_w, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t kb = ring + slot * C::SLOT, d = tmem + (t & 1) * C::TM_S;
+#pragma unroll
+            for (int blk = 0; blk < C::BLK; ++blk) {
+              const uint64_t dk = sw128_desc(kb + blk * (TM_PT * 128));
+              const uint64_t dq = sw128_desc(sbase + C::Q + blk * 3 * C::TERM);
+#pragma unroll
+              for (int s = 0; s < 4; ++s) {
+                mma_bf16(d, dk + s * 2, dq + s * 2, idS, (blk | s) != 0 ? 1u : 0u);
+                if constexpr (C::G == 2) mma_bf16(d + N, dk + s * 2, dq + ((2 * C::TERM) >> 4) + s * 2, idS1, 1u);
+              }
+            }
+            mma_commit(su32(&ctl.empty[slot]));
+            mma_commit(su32(&ctl.s_full[t & 1]));
+            if (i == m.nt - 1) mma_commit(su32(&ctl.q_free));
+          }
+          if (i > 0) {  // outputs of tile i - 1
+            const int it = ic + v_item(i - 1, m.nt), slot = it % C::S, t = tc + i - 1, pb = t % C::NP;
+            ok = tm_wait(su32(&ctl.full[slot]), (uint32_t)(it / C::S) & 1u, abort_w, a.status) &&
+                 tm_wait(su32(&ctl.p_full[pb]), (uint32_t)(t / C::NP) & 1u, abort_w, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t vb = ring + slot * C::SLOT, pbuf = sbase + C::P + pb * C::PBYTES;
+            const uint32_t d = tmem + C::TM_O + (t & 1) * C::TM_S;
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+              const uint64_t dv = sw128_desc(vb + s * 2048, v_lead);
+              const uint64_t dp = sw128_desc(pbuf + (s >> 2) * 3 * C::TERM) + (s & 3) * 2;
+              mma_bf16(d, dv, dp, idO, s != 0 ? 1u : 0u);
+              if constexpr (C::G == 2) mma_bf16(d + N, dv, dp + ((2 * C::TERM) >> 4), idO1, 1u);
+            }
+            mma_commit(su32(&ctl.empty[slot]));
+            mma_commit(su32(&ctl.p_free[pb]));
+          }
+        }
+        ic += 2 * m.nt;
+        tc += m.nt;
+        ++qi;
+      }
+      if (!ok) {  // what was issued completes before the tensor memory is given back
+        mma_commit(su32(&ctl.done));
+        const long long c0 = clock64();
+        while (!mbar_try_wait(su32(&ctl.done), 0u) && clock64() - c0 < TM_WAIT_CYCLES) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 6) {
+    // ---- queries and masks of the next item, as soon as the scores of the one before are done
+    const int qt = tid - 192;
+    int qi = 0;
+    for (int k = 0; ok && (have = get_item(k, m)) >= 0; ++k) {
+      if (have == 0 || m.nt == 0) continue;
+      ok = tm_wait(su32(&ctl.q_free), ((uint32_t)qi & 1u) ^ 1u, abort_w, a.status);
+      if (!ok) break;
+      constexpr int CH = HD / 8, UNITS = N * CH / TM_QTHREADS, UB = UNITS < 4 ? UNITS : 4;
+#pragma unroll 1
+      for (int u0 = 0; u0 < UNITS; u0 += UB) {
+        float x[UB][8];
+#pragma unroll
+        for (int u = 0; u < UB; ++u) {
+          const int e = (u0 + u) * TM_QTHREADS + qt, n = e / CH, c = e % CH, row = m.n0 + n;
+          const float* q = a.q + (size_t)(m.t.row0 + row / rep) * a.ldq + (size_t)(m.g * rep + row % rep) * HD + c * 8;
+          if (n >= m.rows) {
+#pragma unroll
+            for (int h = 0; h < 8; ++h) x[u][h] = 0.f;
+          } else if (vec) {
+            const float4 v = *reinterpret_cast<const float4*>(q), w = *reinterpret_cast<const float4*>(q + 4);
+            x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
+            x[u][4] = w.x; x[u][5] = w.y; x[u][6] = w.z; x[u][7] = w.w;
+          } else {
+#pragma unroll
+            for (int h = 0; h < 8; ++h) x[u][h] = q[h];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < UB; ++u) {
+          const int e = (u0 + u) * TM_QTHREADS + qt, n = e / CH, c = e % CH;
+          uint8_t* dst = sp + C::Q + (c >> 3) * 3 * C::TERM + n * 128 + (((c & 7) ^ (n & 7)) << 4);
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {  // x = the sum of its three terms
+            uint32_t w[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              w[h] = pack_bf16(make_float2(x[u][2 * h], x[u][2 * h + 1]));
+              x[u][2 * h] -= __uint_as_float(w[h] << 16);
+              x[u][2 * h + 1] -= __uint_as_float(w[h] & 0xffff0000u);
+            }
+            *reinterpret_cast<uint4*>(dst + term * C::TERM) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      for (int n = qt; n < N; n += TM_QTHREADS)
+        ctl.mask[qi % TM_MASKS][n] = n < m.rows ? a.masks[m.t.row0 + (m.n0 + n) / rep] : 0ull;
+      proxy_fence();
+      mbar_arrive(su32(&ctl.q_full[qi % TM_MASKS]));
+      ++qi;
+    }
+  } else {
+    // ---- softmax
+    const float c = 1.4426950408889634f / sqrtf((float)HD);
+    const float2 c2 = make_float2(c, c);
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    constexpr int NB = N / 8;  // blocks of eight rows; this thread holds rows n2, n2 + 1 of each
+    const int n2 = (lane & 3) * 2;
+    // where this lane's row of the four matrices of a block starts in P: row
+    // lane % 8, positions 32 warp + 8 (lane / 8) ..
+    const uint32_t p_lane = (uint32_t)(warp >> 1) * (3 * C::TERM) + (lane & 7) * 128 +
+                            (((((warp & 1) * 4) + (lane >> 3)) ^ (lane & 7)) << 4);
+    int ic = 0, tc = 0, qi = 0;
+    for (int k = 0; ok && (have = get_item(k, m)) >= 0; ++k) {
+      if (have == 0) continue;
+      float2 base[NB], l[NB];  // negated base, sum of the weights
+      float o[N];              // element tid of the running output's rows
+      bool added = true;       // the output of the tile before is in o
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        base[b] = make_float2(-TM_FLOOR, -TM_FLOOR);
+        l[b] = make_float2(0.f, 0.f);
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n) o[n] = 0.f;
+      if (tid < N) {
+        ctl.base[tid] = TM_FLOOR;
+        ctl.sum[tid] = 0.f;
+      }
+      // adds the output of the CTA's t-th tile to the running one, once it is complete
+      auto add_output = [&](int t, bool wait) -> bool {
+        if (wait && !tm_wait(su32(&ctl.p_free[t % C::NP]), (uint32_t)(t / C::NP) & 1u, abort_w, a.status)) return false;
+        tc_fence_after();
+        const uint32_t src = tmem + C::TM_O + (t & 1) * C::TM_S + lanes;
+#pragma unroll
+        for (int n = 0; n < N; n += 16) {
+          uint32_t v[C::G][16];
+#pragma unroll
+          for (int gr = 0; gr < C::G; ++gr) tmem_ld16(src + gr * N + n, v[gr]);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            float2 r = make_float2(__uint_as_float(v[C::G - 1][e]), __uint_as_float(v[C::G - 1][e + 1]));
+#pragma unroll
+            for (int gr = C::G - 2; gr >= 0; --gr)
+              r = add2(r, make_float2(__uint_as_float(v[gr][e]), __uint_as_float(v[gr][e + 1])));
+            r = add2(r, make_float2(o[n + e], o[n + e + 1]));
+            o[n + e] = r.x;
+            o[n + e + 1] = r.y;
+          }
+        }
+        return true;
+      };
+      if (m.nt > 0) {  // the item's masks are there
+        ok = tm_wait(su32(&ctl.q_full[qi % TM_MASKS]), (uint32_t)(qi / TM_MASKS) & 1u, abort_w, a.status);
+        if (soft_any(!ok)) {
+          ok = false;
+          break;
+        }
+      }
+      for (int i = 0; i < m.nt; ++i) {
+        const int t = tc + i, pb = t % C::NP;
+        ok = tm_wait(su32(&ctl.s_full[t & 1]), (uint32_t)(t >> 1) & 1u, abort_w, a.status) && ok;
+        if (soft_any(!ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // scores of positions 32 warp + 16 h + 8 r + lane / 4, 32 rows at a time
+        uint32_t f[2][N / 2];
+        constexpr int W = N < 32 ? N : 32;
+#pragma unroll
+        for (int n = 0; n < N; n += W) {
+          uint32_t v[C::G][2][W / 2];
+#pragma unroll
+          for (int gr = 0; gr < C::G; ++gr)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              tmem_frag<W>(tmem + (t & 1) * C::TM_S + gr * N + n + lanes + ((uint32_t)(16 * h) << 16), v[gr][h]);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < W / 2; e += 2) {
+              float2 r = make_float2(__uint_as_float(v[C::G - 1][h][e]), __uint_as_float(v[C::G - 1][h][e + 1]));
+#pragma unroll
+              for (int gr = C::G - 2; gr >= 0; --gr)
+                r = add2(r, make_float2(__uint_as_float(v[gr][h][e]), __uint_as_float(v[gr][h][e + 1])));
+              f[h][n / 2 + e] = __float_as_uint(r.x);
+              f[h][n / 2 + e + 1] = __float_as_uint(r.y);
+            }
+        }
+        tc_fence_before();
+        mbar_arrive(su32(&ctl.s_free[t & 1]));
+        const int p0 = (m.t0 + i) * TM_PT + warp * 32;  // the warp's first position
+        if ((m.t0 + i + 1) * TM_PT > m.t.L) {  // the tile reaches past the committed positions
+          // the value row of a position no row may meet is zeroed: one past the
+          // sequence (whatever lies there), or a node's with an infinity or NaN
+          const int it = ic + v_item(i, m.nt), slot = it % C::S, pos = p0 + lane;
+          ok = tm_wait(su32(&ctl.full[slot]), (uint32_t)(it / C::S) & 1u, abort_w, a.status);
+          if (soft_any(!ok)) {
+            ok = false;
+            break;
+          }
+          uint4* vr = reinterpret_cast<uint4*>(sp + C::RING + slot * C::SLOT + tid * 128);
+          bool mine = false;
+          if (pos >= m.t.L && pos < m.t.P) {
+#pragma unroll
+            for (int e = 0; e < C::BLK * 8; ++e) {
+              const uint4 u = vr[(e >> 3) * (TM_PT * 8) + (e & 7)];
+              const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int h = 0; h < 4; ++h)
+                mine = mine || (x[h] & 0x7f80u) == 0x7f80u || (x[h] & 0x7f800000u) == 0x7f800000u;
+            }
+          }
+          if (pos >= m.t.P || mine) {
+#pragma unroll
+            for (int e = 0; e < C::BLK * 8; ++e) vr[(e >> 3) * (TM_PT * 8) + (e & 7)] = make_uint4(0, 0, 0, 0);
+          }
+          // positions of the warp whose values are infinite or NaN: a row that sees one is NaN
+          const unsigned bad = __ballot_sync(0xffffffffu, mine);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int off = 8 * q + (lane >> 2), ps = p0 + off;
+            if (ps >= m.t.L) {
+              const int j = min(ps - m.t.L, 63);
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  uint32_t& x = f[q >> 1][4 * b + 2 * (q & 1) + e];
+                  if (ps >= m.t.P || ((ctl.mask[qi % TM_MASKS][8 * b + n2 + e] >> j) & 1ull) == 0)
+                    x = 0xff800000u;  // -inf
+                  else if ((bad >> off) & 1u)
+                    x = 0x7fc00000u;
+                }
+            }
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t* x = &f[q >> 1][4 * b + 2 * (q & 1)];
+            const float2 v = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, base[b]);
+            top = fmaxf(top, fmaxf(v.x, v.y));
+          }
+        if (soft_any(top > TM_SLACK)) {
+          // new bases: the rows' largest scores so far
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              mx = fmaxf(mx, __uint_as_float(f[q >> 1][4 * b + 2 * (q & 1)]));
+              my = fmaxf(my, __uint_as_float(f[q >> 1][4 * b + 2 * (q & 1) + 1]));
+            }
+            mx = lanes_max(mx);
+            my = lanes_max(my);
+            if (lane < 4) {
+              ctl.part[warp][8 * b + n2] = mx * c;
+              ctl.part[warp][8 * b + n2 + 1] = my * c;
+            }
+          }
+          soft_sync();
+          if (tid < N) {
+            const float old = ctl.base[tid];
+            const float nb = fmaxf(fmaxf(fmaxf(ctl.part[0][tid], ctl.part[1][tid]),
+                                         fmaxf(ctl.part[2][tid], ctl.part[3][tid])), old);
+            ctl.corr[tid] = nb == old ? 1.f : exp2_fast(old - nb);
+            ctl.base[tid] = nb;
+          }
+          if (!added) ok = add_output(t - 1, true);
+          added = true;
+          if (soft_any(!ok)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const int n = 8 * b + n2;
+            base[b] = make_float2(-ctl.base[n], -ctl.base[n + 1]);
+            l[b].x *= ctl.corr[n];
+            l[b].y *= ctl.corr[n + 1];
+          }
+#pragma unroll
+          for (int n = 0; n < N; ++n) o[n] *= ctl.corr[n];
+        }
+        ok = tm_wait(su32(&ctl.p_free[pb]), ((uint32_t)(t / C::NP) & 1u) ^ 1u, abort_w, a.status) && ok;
+        const uint32_t ph = sbase + C::P + pb * C::PBYTES + p_lane;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float2 p[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t* x = &f[q >> 1][4 * b + 2 * (q & 1)];
+            const float2 e = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, base[b]);
+            p[q] = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+            l[b] = add2(l[b], p[q]);
+          }
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              w[q] = pack_bf16(p[q]);
+              p[q] = add2(p[q], make_float2(-__uint_as_float(w[q] << 16), -__uint_as_float(w[q] & 0xffff0000u)));
+            }
+            store_t(ph + term * C::TERM + b * 1024, w[0], w[1], w[2], w[3]);
+          }
+        }
+        proxy_fence();
+        tc_fence_before();
+        mbar_arrive(su32(&ctl.p_full[pb]));
+        // the tensor cores have had this tile's softmax to finish the one before
+        // (one P buffer: it was complete before this tile's P was written, and
+        // its barrier may be a phase further by now)
+        if (!added) ok = add_output(t - 1, C::NP > 1) && ok;
+        added = false;
+      }
+      if (m.nt > 0) {
+        if (ok) ok = add_output(tc + m.nt - 1, true);
+        if (soft_any(!ok)) {  // every softmax thread comes here, whichever of them gave up
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float sx = lanes_sum(l[b].x), sy = lanes_sum(l[b].y);
+          if (lane < 4) {
+            ctl.part[warp][8 * b + n2] = sx;
+            ctl.part[warp][8 * b + n2 + 1] = sy;
+          }
+        }
+        soft_sync();
+        if (tid < N) ctl.sum[tid] = (ctl.part[0][tid] + ctl.part[1][tid]) + (ctl.part[2][tid] + ctl.part[3][tid]);
+        soft_sync();
+        if (CL > 1) {
+          float* os = reinterpret_cast<float*>(sp + C::RING);  // [N][HD]: the ring is idle now
+          if (tid < HD) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) os[n * HD + tid] = o[n];
+          }
+        } else if (tid < HD) {
+          int node = m.n0 / rep, r = m.n0 % rep;
+          float* dst = a.out + (size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + r) * HD + tid;
+          const int wrap = a.ldo - (rep - 1) * HD;
+#pragma unroll
+          for (int n = 0; n < N; ++n)
+            if (n < m.rows) {
+              const float sum = ctl.sum[n];
+              *dst = sum == 0.f ? 0.f : o[n] / sum;
+              if (++r == rep) {
+                r = 0;
+                dst += wrap;
+              } else {
+                dst += HD;
+              }
+            }
+        }
+        soft_sync();  // the sums may be written again
+        ic += 2 * m.nt;
+        tc += m.nt;
+        ++qi;
+      }
+      if (CL > 1) break;  // one item for a cluster
+    }
+    if (!ok) *abort_w = 1;
+  }
+  if (CL > 1 && (have = get_item(0, m)) == 1) {
+    // join: each CTA takes every CL-th row
+    cl.sync();
+    if (warp < 4 && !*abort_w && tid < HD) {
+      for (int n = rank; n < m.rows; n += CL) {
+        float mx = TM_FLOOR;
+        for (int r = 0; r < CL; ++r) mx = fmaxf(mx, *cl.map_shared_rank(&ctl.base[n], r));
+        float sum = 0.f, acc = 0.f;
+        for (int r = 0; r < CL; ++r) {
+          const float lr = *cl.map_shared_rank(&ctl.sum[n], r);
+          if (lr == 0.f) continue;  // this share saw nothing
+          const float f = exp2_fast(*cl.map_shared_rank(&ctl.base[n], r) - mx);
+          sum = fmaf(lr, f, sum);
+          acc = fmaf(cl.map_shared_rank(reinterpret_cast<float*>(sp + C::RING), r)[n * HD + tid], f, acc);
+        }
+        const int row = m.n0 + n;
+        a.out[(size_t)(m.t.row0 + row / rep) * a.ldo + (size_t)(m.g * rep + row % rep) * HD + tid] =
+            sum == 0.f ? 0.f : acc / sum;
+      }
+    }
+    cl.sync();  // the others may still read this CTA's shared memory
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
+}
+
+// ------------------------------------------------------------- host side
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    else
+      cudaGetLastError();
+  });
+  return fn;
+}
+
+template <int HD, int N>
+int launch_mma(const TreeArgs& a, int layers, int dev, int n_sm, cudaStream_t s) {
+  using C = TmCfg<HD, N>;
+  static bool ready[kMaxDevices] = {};  // the attribute is the device's
+  if (!ready[dev]) {
+    if (cudaFuncSetAttribute(tree_mma_kernel<HD, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) !=
+        cudaSuccess)
+      return Q3TTS_ERR_CUDA;
+    ready[dev] = true;
+  }
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (!enc) return Q3TTS_ERR_CUDA;
+  // the pool as a matrix of head-dim rows, read one page's rows (at most a
+  // tile's) by 64 elements at a time
+  const int box = a.kv.page_size < TM_PT ? a.kv.page_size : TM_PT;
+  CUtensorMap map;
+  const cuuint64_t dims[2] = {(cuuint64_t)HD, (cuuint64_t)tree_pool_rows(a.kv, layers)};
+  const cuuint64_t strides[1] = {(cuuint64_t)HD * 2};
+  const cuuint32_t boxd[2] = {64, (cuuint32_t)box};
+  const cuuint32_t estr[2] = {1, 1};
+  if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.kv.pool, dims, strides, boxd, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return Q3TTS_ERR_CUDA;
+  const int row_tiles = (a.max_nodes * (a.Hq / a.kv.Hkv) + N - 1) / N;
+  const long items = (long)a.n_seqs * a.kv.Hkv * row_tiles;
+  const int tiles = (int)(((long)a.kv.pages_per_stream * a.kv.page_size + TM_PT - 1) / TM_PT);
+  const int c = tree_cluster(items, tiles, n_sm);
+  if (items > 0x7fffffffL / 2) return Q3TTS_ERR_UNSUPPORTED;
+  // split items: one for each cluster; whole ones: a CTA on every SM works through them
+  const long grid = c > 1 ? items * c : (items < n_sm ? items : n_sm);
+  const int vec = ((uintptr_t)a.q & 15) == 0 && a.ldq % 4 == 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(TM_THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = c;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, tree_mma_kernel<HD, N>, map, a, row_tiles, box, (int)items, vec) == cudaSuccess
+             ? Q3TTS_OK
+             : Q3TTS_ERR_CUDA;
+}
+
+}  // namespace
+
+long long tree_pool_rows(const KVDesc& kv, int layers) {
+  return (long long)layers * kv.n_pages * 2 * kv.Hkv * kv.page_size;
+}
+
+// bf16 cache; pages that fill a tile a whole number of times or hold whole
+// tiles, in multiples of 8 rows (a swizzle atom); rows within 32-bit
+// coordinates.
+bool tree_mma_ok(const TreeArgs& a, int layers, int kdt) {
+  const int ps = a.kv.page_size;
+  return kdt == Q3TTS_BF16 && ((ps >= 8 && ps <= TM_PT && TM_PT % ps == 0) || ps % TM_PT == 0) &&
+         tree_pool_rows(a.kv, layers) <= 0x7fffffffll;
+}
+
+int launch_tree_mma(const TreeArgs& a, int layers, int dev, int n_sm, cudaStream_t s) {
+  const int rows = a.max_nodes * (a.Hq / a.kv.Hkv);
+  if (a.kv.hd == 128) {
+    if (rows <= 16) return launch_mma<128, 16>(a, layers, dev, n_sm, s);
+    if (rows <= 32) return launch_mma<128, 32>(a, layers, dev, n_sm, s);
+    return launch_mma<128, 64>(a, layers, dev, n_sm, s);
+  }
+  if (rows <= 16) return launch_mma<64, 16>(a, layers, dev, n_sm, s);
+  if (rows <= 32) return launch_mma<64, 32>(a, layers, dev, n_sm, s);
+  return launch_mma<64, 64>(a, layers, dev, n_sm, s);
+}
+
+}  // namespace q3
