@@ -11,6 +11,7 @@
 
 #include "engine.cuh"
 #include "layers.cuh"
+#include "ops.cuh"
 
 namespace q3 {
 int sampler_setup();
@@ -145,11 +146,12 @@ size_t carve(const q3tts_config& c, void* base, q3tts_handle* h) {
   int32_t* beam_tokens = cv.take<int32_t>(d.S);
   int32_t* beam_parents = cv.take<int32_t>(d.S);
   float* beam_scores = cv.take<float>(d.S);
+  char* beam_ws = cv.take<char>(q3::beam_workspace(1, 1, 1, 1) * d.S);
   if (h) {
     h->tree_codes = tree_codes; h->tree_h = tree_h; h->tree_logits = tree_logits;
     h->tree_masks = tree_masks; h->tree_meta = tree_meta;
     h->beam_ids = beam_ids; h->beam_tokens = beam_tokens; h->beam_parents = beam_parents;
-    h->beam_scores = beam_scores;
+    h->beam_scores = beam_scores; h->beam_ws = beam_ws;
     h->rope_cos = rope_cos; h->rope_sin = rope_sin; h->kv_pool = kv_pool;
     h->page_table = page_table; h->cp_kv = cpkv; h->cp_page_table = cp_pt;
     h->pending_h = pend_h; h->pending_logits = pend_l; h->history = hist; h->finished = fin;

@@ -12,14 +12,18 @@
 //
 // Within a row scores order as logits do, so a row's own k best logits are all
 // it can contribute.  One pass over a row keeps the running maximum and sum of
-// its softmax and its k best logits; the CTAs of one cluster share a group's
-// rows (and pieces of long rows) and the first of them joins the lists through
-// distributed shared memory: one launch, no workspace.
-#include <cooperative_groups.h>
-
+// its softmax and a buffer of candidates above a bound of its k best logits
+// (first the k-th largest maximum of 32 groups of threads, then, whenever the
+// buffer fills, the k-th best itself), so most tiles of a long row need one
+// barrier and no selection at all.  A CTA scans a row, or a piece of a long one
+// where there are few, and leaves its maximum, sum and list in the workspace; a
+// second kernel joins a group's.  (Joining in a cluster of 16 CTAs, through
+// distributed shared memory, took one launch but 47 us for 8 groups of 16 beams
+// over 131072 codes: no more than 7 such clusters run at once, or their CTAs
+// share SMs.)
+// The GPU's fp64 rate is low: the few values that need 64 bits (a row's log sum,
+// a candidate's score) are computed in them, and compared as ordered integers.
 #include "ops.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace q3 {
 
@@ -30,45 +34,71 @@ constexpr int BM_PER = 16;                       // logits of a thread per tile
 constexpr int BM_TILE = BM_THREADS * BM_PER;     // logits of a tile
 constexpr int BM_MAXK = 32;                      // candidates kept
 constexpr int BM_MAXB = 32;                      // beams of a group
-constexpr int BM_MAXC = 8;                       // CTAs of a cluster
-constexpr int BM_UNITS = BM_MAXB;                // units a CTA can hold (a cluster of one)
-constexpr int BM_CAND = BM_TILE + BM_MAXK;       // candidates of one tile at most
+constexpr int BM_LISTS = 128;                    // lists (rows or pieces of rows) of a group at most
+constexpr int BM_FULL = 256;                     // buffered candidates that call for a selection
+constexpr int BM_CAND = BM_FULL + BM_TILE;       // a tile adds all of its logits at most
+static_assert(BM_LISTS >= BM_MAXB, "a list for every beam");
 
 typedef unsigned long long u64;
 
+// Ordered integers: larger value, larger integer.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ u64 ordered(double x) {
+  const u64 b = (u64)__double_as_longlong(x);
+  return (b >> 63) ? ~b : (b | (1ull << 63));
+}
 // Larger key: larger logit, then lower code.  Keys of a row are distinct; 0 is
 // below every key.
-__device__ __forceinline__ u64 make_key(float x, int v) {
-  const uint32_t b = __float_as_uint(x);
-  const uint32_t o = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return ((u64)o << 32) | (uint32_t)~v;
-}
+__device__ __forceinline__ u64 make_key(float x, int v) { return ((u64)ordered(x) << 32) | (uint32_t)~v; }
 __device__ __forceinline__ float key_value(u64 k) {
   const uint32_t o = (uint32_t)(k >> 32);
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 __device__ __forceinline__ int key_code(u64 k) { return (int)~(uint32_t)k; }
 
+// What a scan leaves of its piece (in the workspace): the maximum, the sum of
+// e^(x - maximum), and the best keys in order (0: none).
+struct Piece {
+  float mx, sum;
+  u64 list[BM_MAXK];
+};
+
 struct BeamSmem {
-  u64 list[BM_UNITS][BM_MAXK];  // a unit's best keys in order (0: none)
-  float mx[BM_UNITS], sum[BM_UNITS];
-  int done[BM_UNITS];
   float red[2][32];
-  float group[32];
+  float group[64];
   u64 best[BM_MAXK], top[BM_MAXK];
   int n_cand;
   u64 cand[BM_CAND];
 };
 
-// What the first CTA joins: candidates of all rows, at most max(beams, CTAs) k.
 struct JoinSmem {
-  double lse[BM_MAXB];  // log of the row's sum, relative to its maximum
+  double lse[BM_MAXB];  // the beam's score less the log of its row's sum (relative to its maximum)
   float mx[BM_MAXB];
-  double score[BM_MAXB * BM_MAXK];
-  u64 key[BM_MAXB * BM_MAXK];
-  int row[BM_MAXB * BM_MAXK];
+  u64 group[64];
+  int n_cand;
+  u64 score[BM_LISTS * BM_MAXK], key[BM_LISTS * BM_MAXK];  // the candidates that may be kept
+  int row[BM_LISTS * BM_MAXK];
 };
-static_assert(sizeof(JoinSmem) <= sizeof(u64) * BM_CAND, "the join reuses the candidate buffer");
+
+// The k-th largest of 64 values in shared memory (k <= 64), for every lane of a
+// warp; v0 and v1 are the lane's two of them.
+template <class T>
+__device__ __forceinline__ T kth_of_64(const T* g, int k) {
+  const int lane = threadIdx.x & 31;
+  const T v0 = g[lane], v1 = g[lane + 32];
+  int r0 = 0, r1 = 0;  // how many come before each: larger, or equal and earlier
+#pragma unroll 8
+  for (int j = 0; j < 32; ++j) {
+    const T a = g[j], b = g[j + 32];
+    r0 += (a > v0 || (a == v0 && j < lane)) + (b > v0);
+    r1 += (a >= v1) + (b > v1 || (b == v1 && j < lane));
+  }
+  const unsigned at0 = __ballot_sync(0xffffffffu, r0 == k - 1), at1 = __ballot_sync(0xffffffffu, r1 == k - 1);
+  return at0 ? __shfl_sync(0xffffffffu, v0, __ffs(at0) - 1) : __shfl_sync(0xffffffffu, v1, __ffs(at1) - 1);
+}
 
 // The k best of sm.cand[0 .. n) into sm.best, in order, the rest 0.  All
 // threads.  More candidates than threads (equal or ascending logits): the k-th
@@ -98,101 +128,190 @@ __device__ void keep_best(BeamSmem& sm, int n, int k) {
   if (tid < n) {
     const u64 key = from[tid];
     int r = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) r += from[j] > key;
     if (r < k) sm.best[r] = key;
   }
   __syncthreads();
 }
 
-// A finite or +inf logit after penalty and mask; -inf where it cannot be
-// picked (NaN counts as -inf).
-__device__ __forceinline__ float rule(float x, int v, bool seen, const BeamArgs& a) {
-  if (seen) x = x > 0.f ? x / a.penalty : x * a.penalty;
-  if (a.special_from > 0 && v >= a.special_from && v != a.eos) x = -INFINITY;
-  return x > -INFINITY ? x : -INFINITY;
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Pairs of floats, one instruction each.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
+      " mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n"
+      " mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+// e^(x - m), with e^0 = 1 where both are infinite (and 0 where nothing can be picked)
+__device__ __forceinline__ float exp_off(float x, float m) {
+  return x == m ? (x == -INFINITY ? 0.f : 1.f) : exp2_fast((x - m) * kLog2e);
 }
 
-// e^(x - m), with e^0 = 1 where both are infinite
-__device__ __forceinline__ float exp_off(float x, float m) { return x == m ? (x == -INFINITY ? 0.f : 1.f) : expf(x - m); }
-
-// One row's codes [v0, v1): running maximum and sum, and the k best keys.
-__device__ void scan_piece(BeamSmem& sm, const BeamArgs& a, const float* x, const uint8_t* hist, int v0, int v1,
-                           int unit) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
-  const bool vec = ((uintptr_t)(x + v0) & 15) == 0 && (!hist || ((uintptr_t)(hist + v0) & 3) == 0);
-  float m = -INFINITY, s = 0.f;
-  int have = 0;  // candidates kept so far
-  float thr = -INFINITY;
-  if (tid < BM_MAXK) sm.best[tid] = 0;
-  for (int t0 = v0; t0 < v1; t0 += BM_TILE) {
-    float f[BM_PER];
-    int code0[BM_PER / 4];
+// A tile's logits (and history bytes) of one thread, four codes in a row at a
+// time; codes from v1 on are -inf.
+template <bool HIST>
+__device__ __forceinline__ void load_tile(const float* x, const uint8_t* hist, bool vec, int t0, int v1,
+                                          float (&f)[BM_PER], uint32_t (&hb)[BM_PER / 4]) {
+  const int tid = threadIdx.x;
+  if (vec && t0 + BM_TILE <= v1) {  // a whole tile: every load under way before the first is waited for
+    const float4* p = reinterpret_cast<const float4*>(x + t0) + tid;
+    float4 w[BM_PER / 4];
+#pragma unroll
+    for (int j = 0; j < BM_PER / 4; ++j) w[j] = __ldcs(p + j * BM_THREADS);
+#pragma unroll
+    for (int j = 0; j < BM_PER / 4; ++j)
+      if (HIST) hb[j] = __ldcs(reinterpret_cast<const unsigned int*>(hist + t0) + j * BM_THREADS + tid);
 #pragma unroll
     for (int j = 0; j < BM_PER / 4; ++j) {
-      const int c = t0 + (j * BM_THREADS + tid) * 4;
-      code0[j] = c;
-      float4 w = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      uint32_t hb = 0;
-      if (vec && c + 4 <= v1) {
-        w = __ldcs(reinterpret_cast<const float4*>(x + c));
-        if (hist) hb = __ldcs(reinterpret_cast<const unsigned int*>(hist + c));
-      } else {
-        if (c < v1) w.x = x[c];
-        if (c + 1 < v1) w.y = x[c + 1];
-        if (c + 2 < v1) w.z = x[c + 2];
-        if (c + 3 < v1) w.w = x[c + 3];
-        if (hist)
-          for (int e = 0; e < 4; ++e)
-            if (c + e < v1) hb |= (uint32_t)hist[c + e] << (8 * e);
+      f[4 * j] = w[j].x;
+      f[4 * j + 1] = w[j].y;
+      f[4 * j + 2] = w[j].z;
+      f[4 * j + 3] = w[j].w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < BM_PER / 4; ++j) {
+    const int c = t0 + (j * BM_THREADS + tid) * 4;
+    float4 w = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    uint32_t h = 0;
+    if (vec && c + 4 <= v1) {
+      w = __ldcs(reinterpret_cast<const float4*>(x + c));
+      if (HIST) h = __ldcs(reinterpret_cast<const unsigned int*>(hist + c));
+    } else if (c < v1) {
+      w.x = x[c];
+      if (c + 1 < v1) w.y = x[c + 1];
+      if (c + 2 < v1) w.z = x[c + 2];
+      if (c + 3 < v1) w.w = x[c + 3];
+      if (HIST)
+        for (int e = 0; e < 4; ++e)
+          if (c + e < v1) h |= (uint32_t)hist[c + e] << (8 * e);
+    }
+    f[4 * j] = w.x;
+    f[4 * j + 1] = w.y;
+    f[4 * j + 2] = w.z;
+    f[4 * j + 3] = w.w;
+    if (HIST) hb[j] = h;
+  }
+}
+
+// sum of e^(f[i] - m), m the largest of them or more, finite
+__device__ __forceinline__ float tile_sum(const float (&f)[BM_PER], float m) {
+  const float2 mm = make_float2(-m, -m), ll = make_float2(kLog2e, kLog2e);
+  float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < BM_PER; i += 2) {
+    const float2 d = mul2(add2(make_float2(f[i], f[i + 1]), mm), ll);
+    acc = add2(acc, make_float2(exp2_fast(d.x), exp2_fast(d.y)));
+  }
+  return acc.x + acc.y;
+}
+
+// One row's codes [v0, v1): running maximum and sum, and the k best keys.
+template <bool HIST>
+__device__ __forceinline__ void scan_piece(BeamSmem& sm, Piece& out, const BeamArgs& a, const float* x,
+                                           const uint8_t* hist, int v0, int v1) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
+  const bool vec = ((uintptr_t)(x + v0) & 15) == 0 && (!HIST || ((uintptr_t)(hist + v0) & 3) == 0);
+  float m = -INFINITY, s = 0.f;
+  float thr = -INFINITY;  // only logits above it can still be among the k best
+  if (tid == 0) sm.n_cand = 0;
+  float nf[BM_PER];  // the next tile, on its way while this one is worked on
+  uint32_t nh[BM_PER / 4];
+  load_tile<HIST>(x, hist, vec, v0, v1, nf, nh);
+  for (int t0 = v0; t0 < v1; t0 += BM_TILE) {
+    float f[BM_PER];
+    uint32_t hb[BM_PER / 4];
+#pragma unroll
+    for (int i = 0; i < BM_PER; ++i) f[i] = nf[i];
+#pragma unroll
+    for (int i = 0; i < BM_PER / 4; ++i)
+      if (HIST) hb[i] = nh[i];
+    if (t0 + BM_TILE < v1) load_tile<HIST>(x, hist, vec, t0 + BM_TILE, v1, nf, nh);
+    // the sampler's rule: penalty on the codes of the history, special codes masked
+    if (HIST) {
+#pragma unroll
+      for (int i = 0; i < BM_PER; ++i)
+        if ((hb[i >> 2] >> (8 * (i & 3))) & 0xffu) f[i] = f[i] > 0.f ? f[i] / a.penalty : f[i] * a.penalty;
+    }
+    if (a.special_from > 0 && t0 + BM_TILE > a.special_from) {
+#pragma unroll
+      for (int i = 0; i < BM_PER; ++i) {
+        const int v = t0 + ((i >> 2) * BM_THREADS + tid) * 4 + (i & 3);
+        if (v >= a.special_from && v != a.eos) f[i] = -INFINITY;
       }
-      f[4 * j] = rule(w.x, c, hb & 0xffu, a);
-      f[4 * j + 1] = rule(w.y, c + 1, hb & 0xff00u, a);
-      f[4 * j + 2] = rule(w.z, c + 2, hb & 0xff0000u, a);
-      f[4 * j + 3] = rule(w.w, c + 3, hb & 0xff000000u, a);
     }
-    float tm = f[0];
+    float tm = -INFINITY;  // of the numbers among them: a NaN is passed over
 #pragma unroll
-    for (int i = 1; i < BM_PER; ++i) tm = fmaxf(tm, f[i]);
-    const float mn = fmaxf(m, tm);
-    s *= exp_off(m, mn);
-#pragma unroll
-    for (int i = 0; i < BM_PER; ++i) s += exp_off(f[i], mn);
-    m = mn;
-    // candidates: logits above the k-th kept one (a later equal logit has a
-    // higher code and loses)
-    if (!__syncthreads_or(tm > thr)) continue;
-    // a bound from this tile: the k-th largest of the maxima of 32 groups of
-    // 16 threads has at least k logits at or above it
-    float gm = tm;
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
-    if ((lane & 15) == 0) sm.group[warp * 2 + (lane >> 4)] = gm;
-    if (tid < have) sm.cand[tid] = sm.best[tid];
-    if (tid == 0) sm.n_cand = have;
-    __syncthreads();
-    const float gv = sm.group[lane];
-    int r = 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float o = __shfl_sync(0xffffffffu, gv, j);
-      r += o > gv || (o == gv && j < lane);
+    for (int i = 0; i < BM_PER; ++i) tm = fmaxf(tm, f[i]);
+    if (tm > m) {
+      s *= exp_off(m, tm);
+      m = tm;
     }
-    const unsigned at = __ballot_sync(0xffffffffu, r == k - 1);
-    const float bound = __shfl_sync(0xffffffffu, gv, __ffs(at) - 1);
+    if (m > -INFINITY && m < INFINITY) {
+      float ts = tile_sum(f, m);
+      if (ts != ts) {  // a NaN logit counts as -inf
+#pragma unroll
+        for (int i = 0; i < BM_PER; ++i) f[i] = fmaxf(f[i], -INFINITY);
+        ts = tile_sum(f, m);
+      }
+      s += ts;
+    } else if (m == INFINITY) {
+#pragma unroll
+      for (int i = 0; i < BM_PER; ++i) s += exp_off(fmaxf(f[i], -INFINITY), m);
+    }
+    const int some = __syncthreads_count(tm > thr);
+    if (some == 0) continue;
+    float bound = -INFINITY;
+    if (some > BM_FULL / 4) {
+      // many: the k-th largest of the maxima of 64 groups of 8 threads has at
+      // least k of this tile's logits at or above it
+      float gm = tm;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+      if ((lane & 7) == 0) sm.group[warp * 4 + (lane >> 3)] = gm;
+      __syncthreads();
+      bound = kth_of_64(sm.group, k);
+    }
+    int at = -1;
     if (tm > thr && tm >= bound) {
 #pragma unroll
       for (int i = 0; i < BM_PER; ++i)
         if (f[i] > thr && f[i] >= bound) {
-          const int c = code0[i >> 2] + (i & 3);
-          sm.cand[atomicAdd(&sm.n_cand, 1)] = make_key(f[i], c);
+          at = atomicAdd(&sm.n_cand, 1);
+          sm.cand[at] = make_key(f[i], t0 + ((i >> 2) * BM_THREADS + tid) * 4 + (i & 3));
         }
     }
-    __syncthreads();
-    const int n = sm.n_cand;
-    keep_best(sm, n, k);
-    have = min(n, k);
-    if (have == k) thr = key_value(sm.best[k - 1]);
+    // k logits with lower codes are at or above the bound: a later one must pass it
+    thr = fmaxf(thr, bound);
+    // the buffer is full, or this was the first of several tiles: from now on a
+    // logit must pass the k-th best so far
+    if (__syncthreads_or(at >= BM_FULL || (at >= k && t0 == v0 && t0 + BM_TILE < v1))) {
+      keep_best(sm, sm.n_cand, k);
+      if (tid < k) sm.cand[tid] = sm.best[tid];
+      if (tid == 0) sm.n_cand = k;
+      thr = key_value(sm.best[k - 1]);
+      __syncthreads();
+    }
   }
+  __syncthreads();
+  keep_best(sm, sm.n_cand, k);
   // the threads' maxima and sums
   const float wm = warp_max(m);
   const float ws = warp_sum(s * exp_off(m, wm));
@@ -207,100 +326,140 @@ __device__ void scan_piece(BeamSmem& sm, const BeamArgs& a, const float* x, cons
     const float mm = warp_max(m1);
     const float ss = warp_sum(s1 * exp_off(m1, mm));
     if (lane == 0) {
-      sm.mx[unit] = mm;
-      sm.sum[unit] = ss;
+      out.mx = mm;
+      out.sum = ss;
     }
+    if (lane < k) out.list[lane] = sm.best[lane];
   }
-  if (tid < BM_MAXK) sm.list[unit][tid] = tid < have ? sm.best[tid] : 0;
-  __syncthreads();
 }
 
-__global__ void __launch_bounds__(BM_THREADS) beam_select_kernel(BeamArgs a, int pieces, int piece_len) {
-  pdl_wait();
-  pdl_trigger();
+template <bool HIST>
+__global__ void __launch_bounds__(BM_THREADS, 2) beam_scan_kernel(BeamArgs a, int pieces, int piece_len, Piece* ws) {
   extern __shared__ __align__(16) uint8_t bm_raw[];
   BeamSmem& sm = *reinterpret_cast<BeamSmem*>(bm_raw);
-  cg::cluster_group cl = cg::this_cluster();
-  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-  const int g = blockIdx.x / C, tid = threadIdx.x, k = a.k;
-  const int units = a.beams * pieces;
-  for (int u = rank, slot = 0; u < units; u += C, ++slot) {
-    const int b = u / pieces, piece = u % pieces;
-    const int row = a.row_ids ? a.row_ids[g * a.beams + b] : g * a.beams + b;
-    const bool done = a.finished && a.finished[row];
-    if (tid == 0) sm.done[slot] = done;
-    if (done) {  // one candidate, from the first piece
-      if (tid < BM_MAXK) sm.list[slot][tid] = piece == 0 && tid == 0 ? make_key(0.f, a.eos) : 0;
-      if (tid == 0) {
-        sm.mx[slot] = 0.f;
-        sm.sum[slot] = piece == 0 ? 1.f : 0.f;
-      }
-      __syncthreads();
-    } else {
-      const int v0 = piece * piece_len, v1 = min(a.vocab, v0 + piece_len);
-      scan_piece(sm, a, a.logits + (size_t)row * a.ld, a.history ? a.history + (size_t)row * a.vocab : nullptr, v0, v1,
-                 slot);
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, gb = blockIdx.x / pieces, piece = blockIdx.x % pieces;
+  const int row = a.row_ids ? a.row_ids[gb] : gb;
+  Piece& out = ws[blockIdx.x];
+  if (a.finished && a.finished[row]) {  // one candidate, from the first piece
+    if (tid < a.k) out.list[tid] = piece == 0 && tid == 0 ? make_key(0.f, a.eos) : 0;
+    if (tid == 0) {
+      out.mx = 0.f;
+      out.sum = piece == 0 ? 1.f : 0.f;
+    }
+    return;
+  }
+  const int v0 = piece * piece_len, v1 = min(a.vocab, v0 + piece_len);
+  scan_piece<HIST>(sm, out, a, a.logits + (size_t)row * a.ld, HIST ? a.history + (size_t)row * a.vocab : nullptr, v0, v1);
+}
+
+// Natural logarithm of a positive normal number to about 1e-10: x = 2^e m with m
+// in [sqrt(1/2), sqrt(2)), log m = 2 atanh(t) = 2 (t + t^3/3 + t^5/5 + ..), t =
+// (m - 1) / (m + 1), |t| <= 0.172 (the first term left out is below 2e-11).  A
+// short chain: the fp64 units are slow, and the sums it is taken of are fp32's.
+__device__ __forceinline__ double log_of(double x) {
+  const long long b = __double_as_longlong(x);
+  int e = (int)(b >> 52) - 1023;
+  double m = __longlong_as_double((b & 0xfffffffffffffll) | 0x3ff0000000000000ll);
+  if (m > 1.4142135623730951) {
+    m *= 0.5;
+    e += 1;
+  }
+  const double d = m + 1.0;
+  double r = (double)(1.0f / (float)d);
+  r = fma(r, fma(-d, r, 1.0), r);  // one Newton step
+  const double t = (m - 1.0) * r, t2 = t * t;
+  const double p = fma(t2, fma(t2, fma(t2, fma(t2, 1.0 / 11.0, 1.0 / 9.0), 1.0 / 7.0), 1.0 / 5.0), 1.0 / 3.0);
+  return fma((double)e, 0.6931471805599453, 2.0 * fma(t * t2, p, t));
+}
+
+// Joins a group's lists: every entry's score in 64 bits, a bound that the k
+// best are at or above (as in the scan), and the order of what passes it.  Lane
+// i of a warp holds entry i of its lists.
+__global__ void __launch_bounds__(BM_THREADS) beam_join_kernel(BeamArgs a, int pieces, const Piece* ws) {
+  extern __shared__ __align__(16) uint8_t bm_raw[];
+  JoinSmem& jn = *reinterpret_cast<JoinSmem*>(bm_raw);
+  constexpr int PER = BM_LISTS / BM_WARPS;  // lists of a warp
+  pdl_wait();
+  pdl_trigger();
+  const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
+  const Piece* pc = ws + (size_t)g * a.beams * pieces;
+  const int lists = a.beams * pieces;
+  u64 key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int u = warp + i * BM_WARPS;
+    key[i] = u < lists && lane < k ? pc[u].list[lane] : 0;
+  }
+  if (tid < a.beams) {
+    const Piece* p0 = pc + tid * pieces;
+    float mm = -INFINITY;
+#pragma unroll 4
+    for (int p = 0; p < pieces; ++p) mm = fmaxf(mm, p0[p].mx);
+    double ss = 0.0;
+#pragma unroll 4
+    for (int p = 0; p < pieces; ++p) ss += (double)(p0[p].sum * exp_off(p0[p].mx, mm));
+    // what a candidate's logit is scored against
+    jn.lse[tid] = ss > 0.0 ? (double)a.scores[g * a.beams + tid] - log_of(ss) : 0.0;  // 0: a row without candidates
+    jn.mx[tid] = mm;
+  }
+  if (tid == 0) jn.n_cand = 0;
+  __syncthreads();
+  u64 sc[PER], best = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    sc[i] = 0;
+    if (key[i] != 0) {
+      const int b = (warp + i * BM_WARPS) / pieces;
+      const float x = key_value(key[i]), mm = jn.mx[b];
+      // score + (x - max) - log sum; infinite logits share the weight
+      const double v = jn.lse[b] + (x == mm ? 0.0 : (double)x - (double)mm);
+      if (v > -INFINITY) sc[i] = ordered(v);
+    }
+    best = sc[i] > best ? sc[i] : best;
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    const u64 v = __shfl_xor_sync(0xffffffffu, best, o);
+    best = v > best ? v : best;
+  }
+  if ((lane & 7) == 0) jn.group[warp * 4 + (lane >> 3)] = best;
+  __syncthreads();
+  const u64 bound = kth_of_64(jn.group, k);
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (sc[i] != 0 && sc[i] >= bound) {
+      const int at = atomicAdd(&jn.n_cand, 1);
+      jn.score[at] = sc[i];
+      jn.key[at] = key[i];
+      jn.row[at] = (warp + i * BM_WARPS) / pieces;
+    }
+  __syncthreads();
+  const int n = jn.n_cand;
+  for (int i = tid; i < n; i += BM_THREADS) {
+    const u64 sc = jn.score[i];
+    const u64 key = jn.key[i];
+    const int b = jn.row[i];
+    int r = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const u64 so = jn.score[j];
+      r += so > sc;
+      if (so == sc && j != i) r += jn.row[j] < b || (jn.row[j] == b && jn.key[j] > key);
+    }
+    if (r < k) {
+      a.tokens[g * k + r] = key_code(key);
+      a.parents[g * k + r] = b;
+      const u64 raw = (sc >> 63) ? (sc & ~(1ull << 63)) : ~sc;
+      a.scores_out[g * k + r] = (float)__longlong_as_double((long long)raw);
     }
   }
-  cl.sync();
-  if (rank == 0) {
-    JoinSmem& jn = *reinterpret_cast<JoinSmem*>(sm.cand);
-    // log of each row's sum, relative to its maximum, in 64 bits
-    if (tid < a.beams) {
-      float mm = -INFINITY;
-      for (int p = 0; p < pieces; ++p) {
-        const int u = tid * pieces + p;
-        mm = fmaxf(mm, *cl.map_shared_rank(&sm.mx[u / C], u % C));
-      }
-      double ss = 0.0;
-      for (int p = 0; p < pieces; ++p) {
-        const int u = tid * pieces + p;
-        const float pm = *cl.map_shared_rank(&sm.mx[u / C], u % C);
-        ss += (double)*cl.map_shared_rank(&sm.sum[u / C], u % C) * (double)exp_off(pm, mm);
-      }
-      jn.lse[tid] = log(ss);
-      jn.mx[tid] = mm;
-    }
-    if (tid == 0) sm.n_cand = 0;
-    __syncthreads();
-    for (int e = tid; e < units * k; e += BM_THREADS) {
-      const int u = e / k, b = u / pieces;
-      const u64 key = *cl.map_shared_rank(&sm.list[u / C][e % k], u % C);
-      if (key == 0) continue;
-      const float x = key_value(key), mm = jn.mx[b];
-      // (x - max) - log sum; infinite logits share the weight
-      const double d = x == mm ? 0.0 : (double)x - (double)mm;
-      const double sc = (double)a.scores[g * a.beams + b] + (d - jn.lse[b]);
-      if (!(sc > -INFINITY)) continue;
-      const int i = atomicAdd(&sm.n_cand, 1);
-      jn.score[i] = sc;
-      jn.key[i] = key;
-      jn.row[i] = b;
-    }
-    __syncthreads();
-    const int n = sm.n_cand;
-    for (int i = tid; i < n; i += BM_THREADS) {
-      const double sc = jn.score[i];
-      const u64 key = jn.key[i];
-      const int b = jn.row[i];
-      int r = 0;
-      for (int j = 0; j < n && r < k; ++j) {
-        const double so = jn.score[j];
-        r += so > sc || (so == sc && (jn.row[j] < b || (jn.row[j] == b && jn.key[j] > key)));
-      }
-      if (r < k) {
-        a.tokens[g * k + r] = key_code(key);
-        a.parents[g * k + r] = b;
-        a.scores_out[g * k + r] = (float)sc;
-      }
-    }
-    if (tid >= n && tid < k) {  // no candidate left for the slot
-      a.tokens[g * k + tid] = -1;
-      a.parents[g * k + tid] = 0;
-      a.scores_out[g * k + tid] = -INFINITY;
-    }
+  if (tid >= n && tid < k) {  // no candidate left for the slot
+    a.tokens[g * k + tid] = -1;
+    a.parents[g * k + tid] = 0;
+    a.scores_out[g * k + tid] = -INFINITY;
   }
-  cl.sync();  // rank 0 still reads the others' lists until here
 }
 
 // --------------------------------------------------------------- reordering
@@ -391,41 +550,50 @@ __global__ void __launch_bounds__(RO_THREADS) permute_rows_kernel(const __grid_c
 
 }  // namespace
 
-int launch_beam_select(const BeamArgs& a, cudaStream_t s) {
+// Pieces of a row: enough CTAs for two on every SM, each of whole tiles, and no
+// more lists in a group than the join holds.
+static int beam_pieces(int groups, int beams, int vocab, int n_sm, int* len) {
+  const int tiles = (vocab + BM_TILE - 1) / BM_TILE;
+  const long rows = (long)groups * beams;
+  long p = 2l * n_sm / rows;
+  p = p < BM_LISTS / beams ? p : BM_LISTS / beams;
+  p = p < 1 ? 1 : (p < tiles ? p : tiles);
+  const int per = (tiles + (int)p - 1) / (int)p;
+  *len = per * BM_TILE;
+  return (tiles + per - 1) / per;
+}
+
+size_t beam_workspace(int groups, int beams, int vocab, int n_sm) {
+  int len = 0;
+  return sizeof(Piece) * (size_t)groups * beams * beam_pieces(groups, beams, vocab, n_sm, &len);
+}
+
+int launch_beam_select(const BeamArgs& a, void* workspace, cudaStream_t s) {
   if (a.groups <= 0) return Q3TTS_OK;
   int dev = 0, n_sm = 0;
   if (!current_device(&dev, &n_sm)) return Q3TTS_ERR_CUDA;
-  static bool ready[kMaxDevices] = {};
+  static bool ready[kMaxDevices] = {};  // the attributes are the device's
   if (!ready[dev]) {
-    if (cudaFuncSetAttribute(beam_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(BeamSmem)) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(beam_scan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(BeamSmem)) != cudaSuccess ||
+        cudaFuncSetAttribute(beam_scan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(BeamSmem)) != cudaSuccess ||
+        cudaFuncSetAttribute(beam_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(JoinSmem)) !=
+            cudaSuccess)
       return Q3TTS_ERR_CUDA;
     ready[dev] = true;
   }
-  // CTAs of a group: one per tile of its rows, at most the portable cluster
-  // size; rows are cut into pieces where a group has fewer rows than CTAs
-  const int tiles = (a.vocab + BM_TILE - 1) / BM_TILE;
-  int c = 1;
-  while (c < BM_MAXC && c < a.beams * tiles) c *= 2;
-  const int want = a.beams < c ? c / a.beams : 1;
-  const int per = (tiles + want - 1) / want;  // tiles of a piece
-  const int pieces = (tiles + per - 1) / per;
-  if ((long)a.groups * c > 0x7fffffffL) return Q3TTS_ERR_UNSUPPORTED;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.groups * c));
-  cfg.blockDim = dim3(BM_THREADS);
-  cfg.dynamicSmemBytes = sizeof(BeamSmem);
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = c;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, beam_select_kernel, a, pieces, per * BM_TILE) == cudaSuccess ? Q3TTS_OK
-                                                                                              : Q3TTS_ERR_CUDA;
+  int len = 0;
+  const int pieces = beam_pieces(a.groups, a.beams, a.vocab, n_sm, &len);
+  Piece* ws = static_cast<Piece*>(workspace);
+  const dim3 grid((unsigned)((long)a.groups * a.beams * pieces));
+  const cudaError_t e = launch_pdl(a.history ? beam_scan_kernel<true> : beam_scan_kernel<false>, grid, dim3(BM_THREADS),
+                                   sizeof(BeamSmem), s, a, pieces, len, ws);
+  if (e != cudaSuccess ||
+      launch_pdl(beam_join_kernel, dim3(a.groups), dim3(BM_THREADS), sizeof(JoinSmem), s, a, pieces, (const Piece*)ws) !=
+          cudaSuccess)
+    return Q3TTS_ERR_CUDA;
+  return Q3TTS_OK;
 }
 
 int launch_reorder_rows(const q3tts_rows* sets, int n_sets, const int* row_ids, const int* parents, int groups,

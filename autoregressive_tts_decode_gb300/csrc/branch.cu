@@ -241,9 +241,9 @@ int beam_frame(q3tts_handle* h, const q3tts_sampling& sp, const int32_t* ids, in
   a.tokens = h->beam_tokens;
   a.parents = h->beam_parents;
   a.scores_out = h->beam_scores;
-  rc = launch_beam_select(a, h->s);
+  rc = launch_beam_select(a, h->beam_ws, h->s);
   if (rc != Q3TTS_OK) return rc;
-  h->launches += 1;
+  h->launches += 2;
   // the page lists are host data: the parents are read back before the streams move
   std::vector<int> par(n);
   if (cudaMemcpyAsync(par.data(), h->beam_parents, sizeof(int) * n, cudaMemcpyDeviceToHost, h->s) != cudaSuccess ||

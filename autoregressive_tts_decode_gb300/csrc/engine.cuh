@@ -96,6 +96,7 @@ struct q3tts_handle {
   int32_t* beam_tokens;
   int32_t* beam_parents;
   float* beam_scores;
+  char* beam_ws;  // the selection's workspace (rows of up to 4096 codes are scanned whole)
 
   // host-side stream bookkeeping.  A page holds positions of one stream, or of
   // several (forks, beams) that share a prefix; page_ref counts its holders.

@@ -64,7 +64,9 @@ struct BeamArgs {
   int32_t* parents;
   float* scores_out;
 };
-int launch_beam_select(const BeamArgs& a, cudaStream_t s);
+// 8-byte aligned bytes of workspace a selection needs on a GPU of n_sm SMs.
+size_t beam_workspace(int groups, int beams, int vocab, int n_sm);
+int launch_beam_select(const BeamArgs& a, void* workspace, cudaStream_t s);
 int launch_reorder_rows(const q3tts_rows* sets, int n_sets, const int* row_ids, const int* parents, int groups,
                         int beams_in, int beams_out, int* status, cudaStream_t s);
 

@@ -52,6 +52,11 @@ q3::KVDesc desc(const q3tts_kv_cache& c, const int32_t* table, int pps) {
 // positions of a sequence are 32-bit with room to spare
 bool table_ok(const q3tts_kv_cache& c, int pps) { return pps >= 1 && (long long)pps * c.page_size <= 1 << 30; }
 
+bool beam_shape(int groups, int beams, int vocab, int k) {
+  return groups >= 0 && beams >= 1 && beams <= Q3TTS_MAX_BEAMS && vocab >= 1 && vocab <= 1 << 24 && k >= 1 &&
+         k <= Q3TTS_MAX_BEAMS && (long long)groups * Q3TTS_MAX_BEAMS <= 1 << 24;
+}
+
 // [p, p + n) and [q, q + m) share a byte
 bool overlap(const void* p, size_t n, const void* q, size_t m) {
   const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
@@ -134,19 +139,24 @@ int q3tts_compact_rows(const q3tts_kv_cache* kv, const int32_t* page_table_dev, 
                                  (cudaStream_t)cuda_stream);
 }
 
+size_t q3tts_beam_workspace_size(int groups, int beams, int vocab, int k) {
+  int dev = 0, n_sm = 0;
+  if (!beam_shape(groups, beams, vocab, k) || !q3::current_device(&dev, &n_sm)) return 0;
+  return groups ? q3::beam_workspace(groups, beams, vocab, n_sm) : 0;
+}
+
 int q3tts_beam_select(const float* logits_dev, size_t ld, const int32_t* row_ids_dev, int groups, int beams, int vocab,
                       const float* scores_dev, const uint8_t* finished_dev, const uint8_t* history_dev, int eos_token,
                       int special_from, float repetition_penalty, int k, int32_t* tokens_dev, int32_t* parents_dev,
-                      float* scores_out_dev, void* cuda_stream) {
+                      float* scores_out_dev, void* workspace_dev, size_t workspace_bytes, void* cuda_stream) {
   if (groups < 0 || beams < 1 || vocab < 1 || k < 1 || ld < (size_t)vocab) return Q3TTS_ERR_ARG;
-  if (beams > Q3TTS_MAX_BEAMS || k > Q3TTS_MAX_BEAMS || vocab > 1 << 24 || (long long)groups * Q3TTS_MAX_BEAMS > 1 << 24)
-    return Q3TTS_ERR_UNSUPPORTED;
+  if (!beam_shape(groups, beams, vocab, k)) return Q3TTS_ERR_UNSUPPORTED;
   if (!(repetition_penalty > 0.f) || eos_token >= vocab || special_from > vocab) return Q3TTS_ERR_ARG;
   if (finished_dev && eos_token < 0) return Q3TTS_ERR_ARG;  // a finished beam's candidate is its end code
   if (groups == 0) return Q3TTS_OK;
   if (!logits_dev || !scores_dev || !tokens_dev || !parents_dev || !scores_out_dev || !aligned(logits_dev, 4) ||
       !aligned(row_ids_dev, 4) || !aligned(scores_dev, 4) || !aligned(tokens_dev, 4) || !aligned(parents_dev, 4) ||
-      !aligned(scores_out_dev, 4))
+      !aligned(scores_out_dev, 4) || !workspace_dev || !aligned(workspace_dev, 8))
     return Q3TTS_ERR_ARG;
   // a group's scores are read after another group's may have been written
   if (overlap(scores_dev, sizeof(float) * (size_t)groups * beams, scores_out_dev, sizeof(float) * (size_t)groups * k) &&
@@ -169,7 +179,10 @@ int q3tts_beam_select(const float* logits_dev, size_t ld, const int32_t* row_ids
   a.tokens = tokens_dev;
   a.parents = parents_dev;
   a.scores_out = scores_out_dev;
-  return q3::launch_beam_select(a, (cudaStream_t)cuda_stream);
+  int dev = 0, n_sm = 0;
+  if (!q3::current_device(&dev, &n_sm)) return Q3TTS_ERR_CUDA;
+  if (workspace_bytes < q3::beam_workspace(groups, beams, vocab, n_sm)) return Q3TTS_ERR_ARG;
+  return q3::launch_beam_select(a, workspace_dev, (cudaStream_t)cuda_stream);
 }
 
 int q3tts_reorder_rows(const q3tts_rows* sets, int n_sets, const int32_t* row_ids_dev, const int32_t* parents_dev,

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import Dict, Optional, Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -78,7 +79,7 @@ EXPORTS = ("q3tts_workspace_size", "q3tts_create", "q3tts_prefill", "q3tts_step_
 # include/q3tts_branch.h
 BRANCH_EXPORTS = ("q3tts_fork", "q3tts_tree_step", "q3tts_tree_accept", "q3tts_beam_frame",
                   "q3tts_tree_attention", "q3tts_copy_pages", "q3tts_compact_rows",
-                  "q3tts_beam_select", "q3tts_reorder_rows")
+                  "q3tts_beam_workspace_size", "q3tts_beam_select", "q3tts_reorder_rows")
 MAX_CHUNK = 64
 MAX_TREE_NODES = 64
 MAX_BEAMS = 32
@@ -120,14 +121,16 @@ def load(path: str = LIB_PATH):
     L.q3tts_tree_step.argtypes = [vp, C.c_int, vp, i32p, C.c_int, vp, vp]
     L.q3tts_tree_accept.argtypes = [vp, C.c_int, i32p, C.c_int]
     L.q3tts_beam_frame.argtypes = [vp, C.POINTER(Sampling), i32p, C.c_int, C.c_int, vp, vp, vp, i32p]
-    kvp = C.POINTER(KVCache)
-    L.q3tts_tree_attention.argtypes = [kvp, C.c_int, vp, C.c_int, C.c_int, vp, vp, vp, C.c_int, C.c_int, C.c_int,
+    # structs by address: a ctypes instance (byref) or packed bytes
+    L.q3tts_tree_attention.argtypes = [vp, C.c_int, vp, C.c_int, C.c_int, vp, vp, vp, C.c_int, C.c_int, C.c_int,
                                        vp, C.c_int, vp, C.c_int, vp, vp]
-    L.q3tts_copy_pages.argtypes = [kvp, vp, vp, C.c_int, vp]
-    L.q3tts_compact_rows.argtypes = [kvp, vp, C.c_int, C.c_int, vp, vp, C.c_int, vp, vp, vp]
+    L.q3tts_copy_pages.argtypes = [vp, vp, vp, C.c_int, vp]
+    L.q3tts_compact_rows.argtypes = [vp, vp, C.c_int, C.c_int, vp, vp, C.c_int, vp, vp, vp]
     L.q3tts_beam_select.argtypes = [vp, C.c_size_t, vp, C.c_int, C.c_int, C.c_int, vp, vp, vp, C.c_int, C.c_int,
-                                    C.c_float, C.c_int, vp, vp, vp, vp]
-    L.q3tts_reorder_rows.argtypes = [C.POINTER(Rows), C.c_int, vp, vp, C.c_int, C.c_int, C.c_int, vp, vp]
+                                    C.c_float, C.c_int, vp, vp, vp, vp, C.c_size_t, vp]
+    L.q3tts_beam_workspace_size.argtypes = [C.c_int] * 4
+    L.q3tts_beam_workspace_size.restype = C.c_size_t
+    L.q3tts_reorder_rows.argtypes = [vp, C.c_int, vp, vp, C.c_int, C.c_int, C.c_int, vp, vp]
     L.q3tts_strerror.restype = C.c_char_p
     L.q3tts_strerror.argtypes = [C.c_int]
     _lib = L
@@ -179,48 +182,62 @@ def _need(t, name: str, dtype, numel: int, what: str):
 
 
 # ---- branching-decode operators over caller-owned buffers (include/q3tts_branch.h).
-# They run on the current torch stream of their tensors' device; results do not
-# depend on which device is current.
+# They run on the current torch stream of their tensors' device, whichever device
+# is current.  A single call of the smallest sizes costs the GPU 3 to 10 us, so
+# the checks here read few tensor attributes and structs travel as packed bytes.
+
+_CACHE = struct.Struct("P6i")  # q3tts_kv_cache
+_ROWS = struct.Struct("PPNNN")  # q3tts_rows
+
 
 def _bad(what: str, name: str, want: str):
     raise Q3TTSError(ERR_ARG, f"{what}: {name} must be {want}")
 
 
-def _cuda(t, name: str, dtype, shape, what: str, device=None):
-    """Raises unless t is a contiguous CUDA tensor of dtype and shape (and on
-    `device`)."""
-    if not (t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_cuda and t.is_contiguous()
-            and (device is None or t.device == device)):
-        _bad(what, name, f"a contiguous CUDA {dtype} tensor of shape {tuple(shape)}"
-                         + ("" if device is None else f" on {device}"))
+def _cuda(t, name: str, dtype, dev: int, numel: int, what: str) -> int:
+    """data_ptr of t; raises unless it is a contiguous tensor of dtype on CUDA
+    device dev with numel elements."""
+    if t.dtype != dtype or t.get_device() != dev or t.numel() != numel or not t.is_contiguous():
+        _bad(what, name, f"a contiguous {dtype} tensor of {numel} elements on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _on(device, call):
-    """Runs call(stream handle) with `device` current."""
+def _call(dev: int, fn, what: str, *args):
+    """fn(*args, the current stream of device dev) with that device current."""
+    from torch import _C
+    if dev < 0:
+        _bad(what, "every tensor", "on a CUDA device")
+    if dev == _C._cuda_getDevice():
+        rc = fn(*args, _C._cuda_getCurrentRawStream(dev))
+    else:
+        import torch
+        with torch.cuda.device(dev):
+            rc = fn(*args, _C._cuda_getCurrentRawStream(dev))
+    if rc != OK:
+        raise Q3TTSError(rc, what)
+
+
+def _cache(pool, what: str):
+    """(device, packed q3tts_kv_cache, head dim)."""
     import torch
-    if device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream(device).cuda_stream)
-    with torch.cuda.device(device):
-        return call(torch.cuda.current_stream(device).cuda_stream)
+    dev, dt = pool.get_device(), pool.dtype
+    kind = BF16 if dt == torch.bfloat16 else F32
+    if dev < 0 or not pool.is_contiguous() or pool.dim() != 6 or (kind == F32 and dt != torch.float32):
+        _bad(what, "pool", "a contiguous CUDA fp32 or bf16 tensor [layers, pages, 2, kv heads, page size, head dim]")
+    layers, pages, two, heads, page, hd = pool.shape
+    if two != 2:
+        _bad(what, "pool", "[layers, pages, 2, kv heads, page size, head dim]")
+    return dev, _CACHE.pack(pool.data_ptr(), layers, pages, heads, page, hd, kind), hd
 
 
-def _cache(pool, what: str) -> KVCache:
-    import torch
-    kinds = {torch.float32: F32, torch.bfloat16: BF16}
-    if not (pool.is_cuda and pool.is_contiguous() and pool.dim() == 6 and pool.shape[2] == 2
-            and pool.dtype in kinds):
-        _bad(what, "pool", "a contiguous CUDA fp32 or bf16 tensor "
-                           "[layers, pages, 2, kv heads, page size, head dim]")
-    layers, pages, _, heads, page, hd = pool.shape
-    return KVCache(pool.data_ptr(), layers, pages, heads, page, hd, kinds[pool.dtype])
-
-
-def _heads(t, name: str, what: str) -> int:
+def _pitch(t, rows: int, heads: int, hd: int, name: str, what: str) -> int:
     """Row pitch of a [rows, heads, head dim] view whose rows are contiguous."""
-    n, h, d = t.shape
-    if (h > 1 and t.stride(1) != d) or (d > 1 and t.stride(2) != 1) or (n > 1 and t.stride(0) < h * d):
+    if t.is_contiguous():
+        return heads * hd
+    n, h, d = t.stride()
+    if (heads > 1 and h != hd) or d != 1 or (rows > 1 and n < heads * hd):
         _bad(what, name, "[rows, heads, head dim] with contiguous rows")
-    return t.stride(0) if n > 1 else h * d
+    return n if rows > 1 else heads * hd
 
 
 def tree_attention(pool, layer: int, page_table, lengths, node_start, masks, q, max_nodes: Optional[int] = None,
@@ -234,30 +251,27 @@ def tree_attention(pool, layer: int, page_table, lengths, node_start, masks, q, 
     (fp32, as q; made if None, with zeroes in rows outside every sequence)."""
     import torch
     what = "q3tts_tree_attention"
-    kv = _cache(pool, what)
-    dev = pool.device
-    if q.dim() != 3 or q.dtype != torch.float32 or q.device != dev or q.shape[2] != kv.head_dim:
-        _bad(what, "q", f"a CUDA fp32 tensor [rows, q heads, {kv.head_dim}] on {dev}")
-    rows, heads, _ = q.shape
-    if page_table.dim() != 2:
-        _bad(what, "page_table", "[seqs, pages per seq]")
+    dev, kv, hd = _cache(pool, what)
+    if q.dim() != 3 or q.dtype != torch.float32 or q.get_device() != dev or page_table.dim() != 2:
+        _bad(what, "q and page_table", f"fp32 [rows, q heads, {hd}] and [seqs, pages per seq] on cuda:{dev}")
+    rows, heads, width = q.shape
     seqs, pps = page_table.shape
-    _cuda(page_table, "page_table", torch.int32, (seqs, pps), what, dev)
-    _cuda(lengths, "lengths", torch.int32, (seqs,), what, dev)
-    _cuda(node_start, "node_start", torch.int32, (seqs + 1,), what, dev)
-    _cuda(masks, "masks", torch.uint64 if masks.dtype == torch.uint64 else torch.int64, (rows,), what, dev)
-    if status is not None:
-        _cuda(status, "status", torch.int32, (1,), what, dev)
+    if width != hd:
+        _bad(what, "q", f"[rows, q heads, {hd}]")
+    i32 = torch.int32
     if out is None:
-        out = torch.zeros((rows, heads, kv.head_dim), dtype=torch.float32, device=dev)
-    elif out.shape != q.shape or out.dtype != torch.float32 or out.device != dev:
-        _bad(what, "out", f"a CUDA fp32 tensor of q's shape on {dev}")
+        out = torch.zeros(q.shape, dtype=torch.float32, device=q.device)
+    elif out.shape != q.shape or out.dtype != torch.float32 or out.get_device() != dev:
+        _bad(what, "out", f"an fp32 tensor of q's shape on cuda:{dev}")
     if max_nodes is None:
         max_nodes = max(1, min(rows, MAX_TREE_NODES))
-    ldq, ldo = _heads(q, "q", what), _heads(out, "out", what)
-    _check(_on(dev, lambda s: load().q3tts_tree_attention(
-        C.byref(kv), layer, page_table.data_ptr(), pps, seqs, lengths.data_ptr(), node_start.data_ptr(),
-        masks.data_ptr(), rows, max_nodes, heads, q.data_ptr(), ldq, out.data_ptr(), ldo, _ptr(status), s)), what)
+    _call(dev, load().q3tts_tree_attention, what, kv, layer,
+          _cuda(page_table, "page_table", i32, dev, seqs * pps, what), pps, seqs,
+          _cuda(lengths, "lengths", i32, dev, seqs, what), _cuda(node_start, "node_start", i32, dev, seqs + 1, what),
+          _cuda(masks, "masks", torch.uint64 if masks.dtype == torch.uint64 else torch.int64, dev, rows, what),
+          rows, max_nodes, heads, q.data_ptr(), _pitch(q, rows, heads, hd, "q", what),
+          out.data_ptr(), _pitch(out, rows, heads, hd, "out", what),
+          None if status is None else _cuda(status, "status", i32, dev, 1, what))
     return out
 
 
@@ -265,7 +279,7 @@ def _host_ids(v, name: str, what: str):
     """A CPU int32 tensor of ids (v: one, or a sequence of ints)."""
     import torch
     t = v if isinstance(v, torch.Tensor) else torch.tensor(list(v), dtype=torch.int32)
-    if t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+    if t.get_device() >= 0 or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
         _bad(what, name, "page ids on the host (a sequence, or a contiguous CPU int32 tensor)")
     return t
 
@@ -274,12 +288,12 @@ def copy_pages(pool, src, dst):
     """q3tts_copy_pages: page src[i] to page dst[i] in every layer of pool (as for
     tree_attention).  src, dst: sequences of ints or CPU int32 tensors.  Returns pool."""
     what = "q3tts_copy_pages"
-    kv = _cache(pool, what)
+    dev, kv, _ = _cache(pool, what)
     src, dst = _host_ids(src, "src", what), _host_ids(dst, "dst", what)
-    if src.numel() != dst.numel():
+    n = src.numel()
+    if n != dst.numel():
         _bad(what, "dst", "as long as src")
-    _check(_on(pool.device, lambda s: load().q3tts_copy_pages(C.byref(kv), src.data_ptr(), dst.data_ptr(),
-                                                              src.numel(), s)), what)
+    _call(dev, load().q3tts_copy_pages, what, kv, src.data_ptr(), dst.data_ptr(), n)
     return pool
 
 
@@ -289,67 +303,73 @@ def compact_rows(pool, page_table, lengths, path, path_len, status=None):
     path_len int32 [seqs], path int32 [seqs, most].  Returns pool."""
     import torch
     what = "q3tts_compact_rows"
-    kv = _cache(pool, what)
-    dev = pool.device
+    dev, kv, _ = _cache(pool, what)
     if page_table.dim() != 2 or path.dim() != 2:
         _bad(what, "page_table and path", "[seqs, ..]")
     seqs, pps = page_table.shape
-    _cuda(page_table, "page_table", torch.int32, (seqs, pps), what, dev)
-    _cuda(lengths, "lengths", torch.int32, (seqs,), what, dev)
-    _cuda(path, "path", torch.int32, (seqs, path.shape[1]), what, dev)
-    _cuda(path_len, "path_len", torch.int32, (seqs,), what, dev)
-    if status is not None:
-        _cuda(status, "status", torch.int32, (1,), what, dev)
-    _check(_on(dev, lambda s: load().q3tts_compact_rows(
-        C.byref(kv), page_table.data_ptr(), pps, seqs, lengths.data_ptr(), path.data_ptr(), path.shape[1],
-        path_len.data_ptr(), _ptr(status), s)), what)
+    most = path.shape[1]
+    i32 = torch.int32
+    _call(dev, load().q3tts_compact_rows, what, kv, _cuda(page_table, "page_table", i32, dev, seqs * pps, what), pps,
+          seqs, _cuda(lengths, "lengths", i32, dev, seqs, what), _cuda(path, "path", i32, dev, seqs * most, what), most,
+          _cuda(path_len, "path_len", i32, dev, seqs, what),
+          None if status is None else _cuda(status, "status", i32, dev, 1, what))
     return pool
 
 
+def beam_workspace_size(groups: int, beams: int, vocab: int, k: int) -> int:
+    """Bytes of workspace beam_select uses for this shape on the current device."""
+    return int(load().q3tts_beam_workspace_size(groups, beams, vocab, k))
+
+
 def beam_select(logits, scores, k: Optional[int] = None, row_ids=None, finished=None, history=None,
-                eos_token: int = -1, special_from: int = 0, repetition_penalty: float = 1.0, out=None):
+                eos_token: int = -1, special_from: int = 0, repetition_penalty: float = 1.0, out=None,
+                workspace=None):
     """q3tts_beam_select.  scores fp32 [groups, beams]; logits fp32 [groups, beams,
     vocab] with contiguous rows, or [rows, vocab] with row_ids int32 [groups,
     beams]; finished uint8 and history uint8 of logits' rows; k: candidates kept
     (default: beams).  Returns (tokens int32, parents int32, scores fp32), [groups,
-    k] each; out: three tensors to write them to."""
+    k] each; out: three tensors to write them to; workspace: a contiguous CUDA uint8
+    tensor of beam_workspace_size bytes (made if None)."""
     import torch
     what = "q3tts_beam_select"
-    dev = logits.device
+    dev = logits.get_device()
     if scores.dim() != 2:
         _bad(what, "scores", "[groups, beams]")
     groups, beams = scores.shape
-    _cuda(scores, "scores", torch.float32, (groups, beams), what, dev)
-    vocab = logits.shape[-1]
-    lead = tuple(logits.shape[:-1])
-    if (not logits.is_cuda or logits.dtype != torch.float32 or logits.stride(-1) != 1
-            or len(lead) != (2 if row_ids is None else 1) or (row_ids is None and lead != (groups, beams))):
+    n = groups * beams
+    if dev < 0 or logits.dtype != torch.float32 or logits.dim() != (3 if row_ids is None else 2):
         _bad(what, "logits", "a CUDA fp32 tensor [groups, beams, vocab], or [rows, vocab] with row_ids")
-    if row_ids is None:
-        ld = logits.stride(1) if beams > 1 else (logits.stride(0) if groups > 1 else vocab)
-        if groups > 1 and logits.stride(0) != beams * ld:
-            _bad(what, "logits", "equally spaced rows")
-    else:
-        _cuda(row_ids, "row_ids", torch.int32, (groups, beams), what, dev)
-        ld = logits.stride(0) if lead[0] > 1 else vocab
-    if finished is not None:
-        _cuda(finished, "finished", torch.uint8, lead, what, dev)
-    if history is not None:
-        _cuda(history, "history", torch.uint8, lead + (vocab,), what, dev)
+    vocab = logits.shape[-1]
+    rows = n if row_ids is None else logits.shape[0]
+    ld = vocab
+    if row_ids is None and (logits.shape[0] != groups or logits.shape[1] != beams):
+        _bad(what, "logits", f"[{groups}, {beams}, vocab]")
+    if not logits.is_contiguous():
+        st = logits.stride()
+        ld = st[-2] if logits.shape[-2] > 1 else (st[0] if logits.shape[0] > 1 else vocab)
+        if st[-1] != 1 or (row_ids is None and groups > 1 and st[0] != beams * ld):
+            _bad(what, "logits", "equally spaced rows of contiguous logits")
+    i32 = torch.int32
     k = beams if k is None else int(k)
     if out is None:
-        # one block for the three results
-        block = torch.empty((3, groups, max(k, 0)), dtype=torch.int32, device=dev)
-        tokens, parents, best = block[0], block[1], block[2].view(torch.float32)
+        best = torch.empty_like(scores) if k == beams else scores.new_empty((groups, max(k, 0)))
+        tokens = torch.empty_like(best, dtype=i32)
+        parents = torch.empty_like(best, dtype=i32)
+        p_out = tokens.data_ptr(), parents.data_ptr(), best.data_ptr()
     else:
         tokens, parents, best = out
-        _cuda(tokens, "out[0]", torch.int32, (groups, k), what, dev)
-        _cuda(parents, "out[1]", torch.int32, (groups, k), what, dev)
-        _cuda(best, "out[2]", torch.float32, (groups, k), what, dev)
-    _check(_on(dev, lambda s: load().q3tts_beam_select(
-        logits.data_ptr(), ld, _ptr(row_ids), groups, beams, vocab, scores.data_ptr(), _ptr(finished), _ptr(history),
-        eos_token, special_from, repetition_penalty, k, tokens.data_ptr(), parents.data_ptr(), best.data_ptr(), s)),
-        what)
+        p_out = (_cuda(tokens, "out[0]", i32, dev, groups * k, what), _cuda(parents, "out[1]", i32, dev, groups * k, what),
+                 _cuda(best, "out[2]", torch.float32, dev, groups * k, what))
+    if workspace is None:
+        workspace = torch.empty(beam_workspace_size(groups, beams, vocab, k), dtype=torch.uint8, device=logits.device)
+    n_ws = workspace.numel()
+    _call(dev, load().q3tts_beam_select, what, logits.data_ptr(), ld,
+          None if row_ids is None else _cuda(row_ids, "row_ids", i32, dev, n, what), groups, beams, vocab,
+          _cuda(scores, "scores", torch.float32, dev, n, what),
+          None if finished is None else _cuda(finished, "finished", torch.uint8, dev, rows, what),
+          None if history is None else _cuda(history, "history", torch.uint8, dev, rows * vocab, what),
+          eos_token, special_from, repetition_penalty, k, *p_out,
+          _cuda(workspace, "workspace", torch.uint8, dev, n_ws, what), n_ws)
     return tokens, parents, best
 
 
@@ -362,23 +382,19 @@ def reorder_rows(src, dst, parents, status=None):
     if parents.dim() != 2 or len(src) != len(dst):
         _bad(what, "parents", "[groups, beams], with as many dst as src")
     groups, k = parents.shape
-    dev = parents.device
-    _cuda(parents, "parents", torch.int32, (groups, k), what, dev)
-    if status is not None:
-        _cuda(status, "status", torch.int32, (1,), what, dev)
-    if not src:
-        return dst
-    beams = src[0].shape[1] if src[0].dim() > 1 else 0
-    sets = (Rows * len(src))()
-    for i, (a, b) in enumerate(zip(src, dst)):
-        if a.dim() < 2 or a.shape[0] != groups or a.shape[1] != beams or not a.is_cuda:
-            _bad(what, f"src[{i}]", f"a CUDA tensor [{groups}, {beams}, ..]")
-        _cuda(a, f"src[{i}]", a.dtype, a.shape, what, dev)
-        _cuda(b, f"dst[{i}]", a.dtype, (groups, k) + tuple(a.shape[2:]), what, dev)
-        n = a.element_size() * (a.numel() // max(1, groups * beams))
-        sets[i] = Rows(a.data_ptr(), b.data_ptr(), n, n, n)
-    _check(_on(dev, lambda s: load().q3tts_reorder_rows(sets, len(src), None, parents.data_ptr(), groups, beams, k,
-                                                        _ptr(status), s)), what)
+    dev = parents.get_device()
+    p = _cuda(parents, "parents", torch.int32, dev, groups * k, what)
+    sets = b""
+    beams = src[0].shape[1] if src and src[0].dim() > 1 else 0
+    for a, b in zip(src, dst):
+        sa, sb, dt, na = a.shape, b.shape, a.dtype, a.numel()
+        if len(sa) < 2 or sa[0] != groups or sa[1] != beams or sb[0] != groups or sb[1:2] != (k,) or sa[2:] != sb[2:]:
+            _bad(what, "src and dst", f"[{groups}, {beams}, ..] and [{groups}, {k}, ..]")
+        n = na // max(1, groups * beams) * a.element_size()
+        sets += _ROWS.pack(_cuda(a, "src", dt, dev, na, what), _cuda(b, "dst", dt, dev, b.numel(), what), n, n, n)
+    if sets:
+        _call(dev, load().q3tts_reorder_rows, what, sets, len(src), None, p, groups, beams, k,
+              None if status is None else _cuda(status, "status", torch.int32, dev, 1, what))
     return dst
 
 

@@ -87,9 +87,9 @@ int q3tts_beam_frame(q3tts_handle* h, const q3tts_sampling* params, const int32_
  * What the calls above are made of, for programs that keep their own caches
  * and beams.  Device buffers are caller-owned and must stay valid until the
  * work has run; everything is enqueued on cuda_stream (a stream of the current
- * device) and is asynchronous; nothing is allocated on the device, no
- * workspace is needed, and the calls can be captured into a CUDA graph (host
- * arrays are read during the call).  Sizes of zero are no work.
+ * device) and is asynchronous; nothing is allocated on the device, and the
+ * calls can be captured into a CUDA graph (host arrays are read during the
+ * call).  Sizes of zero are no work.
  * status_dev, where a call has it, is NULL or a device int32: what can only be
  * checked on the device (lengths, paths, page ids, parents) and is wrong is
  * left out, and Q3TTS_ERR_ARG put there unless it already holds a code; the
@@ -160,11 +160,15 @@ int q3tts_compact_rows(const q3tts_kv_cache* kv, const int32_t* page_table_dev, 
  * lower beam comes first, then the larger logit, then the lower code.  A slot
  * without a candidate above -INFINITY gets token -1, parent 0 and score
  * -INFINITY.  beams and k up to Q3TTS_MAX_BEAMS, vocab up to 2^24.  Row ids
- * are not checked. */
+ * are not checked.  workspace_dev: device memory, 8-byte aligned, of at least
+ * q3tts_beam_workspace_size bytes (on the current device; 0 for a shape that is
+ * not taken), whose contents do not matter before and after; calls that may
+ * run at the same time need one each. */
+size_t q3tts_beam_workspace_size(int groups, int beams, int vocab, int k);
 int q3tts_beam_select(const float* logits_dev, size_t ld, const int32_t* row_ids_dev, int groups, int beams, int vocab,
                       const float* scores_dev, const uint8_t* finished_dev, const uint8_t* history_dev, int eos_token,
                       int special_from, float repetition_penalty, int k, int32_t* tokens_dev, int32_t* parents_dev,
-                      float* scores_out_dev, void* cuda_stream);
+                      float* scores_out_dev, void* workspace_dev, size_t workspace_bytes, void* cuda_stream);
 
 /* Per-beam state to be reordered: rows of row_bytes, src_stride and dst_stride
  * bytes apart, in device memory. */

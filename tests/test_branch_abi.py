@@ -35,7 +35,7 @@ def header():
 
 
 def test_exports_every_declared_function(lib):
-    names = set(re.findall(r"^int (q3tts_[a-z_]+)\(", header(), re.M))
+    names = set(re.findall(r"^(?:int|size_t) (q3tts_[a-z_]+)\(", header(), re.M))
     assert names == set(q3tts.BRANCH_EXPORTS) and not names & set(q3tts.EXPORTS)
     for n in names:
         assert hasattr(lib, n), n
@@ -47,6 +47,8 @@ def test_struct_layouts_match_header():
         body = re.search(r"typedef struct " + name + r" \{(.*?)\} " + name, src, re.S).group(1)
         names = [n.strip().split()[-1].lstrip("*") for d in body.split(";") if d.strip() for n in d.split(",")]
         assert names == [f[0] for f in struct._fields_]
+    # the binding packs the same layouts as bytes
+    assert q3tts._CACHE.size == C.sizeof(q3tts.KVCache) and q3tts._ROWS.size == C.sizeof(q3tts.Rows)
     consts = dict(re.findall(r"#define (Q3TTS_[A-Z_0-9]+) \(?(-?\d+)\)?", src))
     assert int(consts["Q3TTS_MAX_TREE_NODES"]) == q3tts.MAX_TREE_NODES
     assert int(consts["Q3TTS_MAX_BEAMS"]) == q3tts.MAX_BEAMS
@@ -107,12 +109,12 @@ def test_compact_rows_refuses(lib, args):
 
 
 BEAM = ["logits", "ld", "ids", "groups", "beams", "vocab", "scores", "finished", "history", "eos", "special",
-        "penalty", "k", "tokens", "parents", "out"]
+        "penalty", "k", "tokens", "parents", "out", "ws", "ws_bytes"]
 
 
 def beam(lib, **kw):
     a = dict(logits=A, ld=100, ids=None, groups=2, beams=4, vocab=100, scores=A + 4096, finished=None, history=None,
-             eos=-1, special=0, penalty=1.0, k=4, tokens=A + 8192, parents=A + 12288, out=A + 16384)
+             eos=-1, special=0, penalty=1.0, k=4, tokens=A + 8192, parents=A + 12288, out=A + 16384, ws=A + 20480, ws_bytes=1 << 30)
     a.update(kw)
     return lib.q3tts_beam_select(*[a[n] for n in BEAM], None)
 
@@ -123,6 +125,7 @@ def beam(lib, **kw):
     (dict(k=0), q3tts.ERR_ARG), (dict(scores=None), q3tts.ERR_ARG), (dict(tokens=None), q3tts.ERR_ARG),
     (dict(parents=None), q3tts.ERR_ARG), (dict(out=None), q3tts.ERR_ARG), (dict(eos=100), q3tts.ERR_ARG),
     (dict(special=101), q3tts.ERR_ARG), (dict(penalty=0.0), q3tts.ERR_ARG), (dict(finished=A), q3tts.ERR_ARG),
+    (dict(ws=None), q3tts.ERR_ARG), (dict(ws=A + 4), q3tts.ERR_ARG),
     (dict(out=A + 4096 + 4), q3tts.ERR_ARG), (dict(out=A + 4096, k=3), q3tts.ERR_ARG),
     (dict(beams=33), q3tts.ERR_UNSUPPORTED), (dict(k=33), q3tts.ERR_UNSUPPORTED),
     (dict(vocab=(1 << 24) + 1, ld=1 << 25), q3tts.ERR_UNSUPPORTED)])
