@@ -52,8 +52,8 @@ namespace q3 {
 namespace {
 
 constexpr int TM_PT = 128;       // positions of a tile
-constexpr int TM_THREADS = 256;  // softmax warps 0..3, TMA warp 4, MMA warp 5, query warps 6 and 7
-constexpr int TM_QTHREADS = 64;
+constexpr int TM_THREADS = 256;  // softmax warps 0..3, TMA warps 4 (keys) and 7 (values), MMA warp 5, query warp 6
+constexpr int TM_QTHREADS = 32;
 constexpr int TM_SORT = 256;     // sequences that are dealt by length
 constexpr int TM_MASKS = 4;      // items whose masks are held: the softmax's, and the scores may be three ahead
 constexpr long long TM_WAIT_CYCLES = 4000000000ll;  // ~2 s
@@ -263,7 +263,8 @@ struct TmItem {
 
 template <int HD, int N>
 __global__ void __launch_bounds__(TM_THREADS, 1)
-    tree_mma_kernel(const __grid_constant__ CUtensorMap map, TreeArgs a, int row_tiles, int box, int items, int vec) {
+    tree_mma_kernel(const __grid_constant__ CUtensorMap map, TreeArgs a, int row_tiles, int box, int items, int vec,
+                    unsigned rep_inv) {
   using C = TmCfg<HD, N>;
   using Ctl = TmCtl<N, C::S>;
   static_assert(sizeof(Ctl) <= C::CTL_BYTES, "control block");
@@ -337,12 +338,18 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
     m.nt = min(all, m.t0 + per) - m.t0;
     return 1;
   };
+  // row / rep for rows of an item (rep_inv = ceil(2^32 / rep); exact for rows and rep up to 2^16)
+  auto div_rep = [&](int row) -> int { return rep == 1 ? row : (int)__umulhi((unsigned)row, rep_inv); };
   TmItem m;
   int have = 0;
   bool ok = true;
 
-  if (warp == 4) {
-    // ---- TMA: lane (b, blk) copies block blk of page b's rows of a tile
+  if (warp == 4 || warp == 7) {
+    // ---- TMA: lane (b, blk) copies block blk of page b's rows of a tile; the
+    // keys and the values each have a warp (a warp's lanes issue one by one, 55
+    // cycles each: 32 copies of 2 KB for a tile of 16-position pages took longer
+    // from one warp than the tile's bytes)
+    const bool values = warp == 7;
     const int b = lane / C::BLK, blk = lane % C::BLK;
     const int boxes = TM_PT / box;
     const int ps = a.kv.page_size;
@@ -351,22 +358,19 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
     for (int k = 0; ok && (have = get_item(k, m)) >= 0; ++k) {
       if (have == 0 || m.nt == 0) continue;
       const int* table = a.kv.page_table + (size_t)m.seq * a.kv.pages_per_stream;
-      // first row of this lane's box in tile i (keys), or -1 past the sequence
-      auto box_row = [&](int i) -> int {
+      // the page of this lane's box in tile i; looked up two tiles ahead and not
+      // touched until then, so the lookup's latency is never waited for
+      auto page_of = [&](int i) -> int {
         const int pos = (m.t0 + i) * TM_PT + b * box;
-        if (b >= boxes || i >= m.nt || pos >= m.t.P) return -1;
-        int page = table[pos / ps];
-        if (page < 0 || page >= a.kv.n_pages) {
-          op_status(a.status, Q3TTS_ERR_ARG);
-          page = 0;
-        }
-        return (int)((((long long)a.layer * a.kv.n_pages + page) * 2) * plane + (long long)m.g * ps + pos % ps);
+        return b < boxes && i < m.nt && pos < m.t.P ? __ldg(table + pos / ps) : 0;
       };
-      int row_even = box_row(0), row_odd = box_row(1);
+      int page_even = page_of(0), page_odd = page_of(1);
       for (int i = 0; i < 2 * m.nt; ++i, ++ic) {
         const bool is_v = i == 2 * m.nt - 1 || (i >= 2 && (i & 1) == 0);
+        if (is_v != values) continue;
         const int tile = is_v ? (i == 2 * m.nt - 1 ? m.nt - 1 : i / 2 - 1) : (i + 1) / 2;
-        const int row = (tile & 1) ? row_odd : row_even;
+        const int pos = (m.t0 + tile) * TM_PT + b * box;
+        int page = (tile & 1) ? page_odd : page_even;
         const int slot = ic % C::S;
         const uint32_t fb = su32(&ctl.full[slot]);
         ok = __all_sync(0xffffffffu,
@@ -375,12 +379,18 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
         const int held = min(TM_PT, m.t.P - (m.t0 + tile) * TM_PT);
         if (lane == 0) mbar_expect_tx(fb, (uint32_t)((held + box - 1) / box * box * HD * 2));
         __syncwarp();
-        if (row >= 0)
-          tma_load(ring + slot * C::SLOT + blk * (TM_PT * 128) + b * box * 128, &map, blk * 64,
-                   row + (is_v ? (int)plane : 0), fb);
-        if (is_v) {  // the tile's row is done with: the one two tiles on takes its place
-          if (tile & 1) row_odd = box_row(tile + 2); else row_even = box_row(tile + 2);
+        if (b < boxes && pos < m.t.P) {
+          if (page < 0 || page >= a.kv.n_pages) {
+            op_status(a.status, Q3TTS_ERR_ARG);
+            page = 0;
+          }
+          // rows of the pool: [layer][page][k|v][kv head][position]
+          const int row = (int)((((long long)a.layer * a.kv.n_pages + page) * 2 + (is_v ? 1 : 0)) * plane +
+                                (long long)m.g * ps + pos % ps);
+          tma_load(ring + slot * C::SLOT + blk * (TM_PT * 128) + b * box * 128, &map, blk * 64, row, fb);
         }
+        // the page two tiles on takes this one's place
+        if (tile & 1) page_odd = page_of(tile + 2); else page_even = page_of(tile + 2);
       }
     }
     // copies in flight land before the CTA may leave
@@ -455,53 +465,67 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= 6) {
+  } else if (warp == 6) {
     // ---- queries and masks of the next item, as soon as the scores of the one before are done
-    const int qt = tid - 192;
+    const int qt = lane;
     int qi = 0;
     for (int k = 0; ok && (have = get_item(k, m)) >= 0; ++k) {
       if (have == 0 || m.nt == 0) continue;
-      ok = tm_wait(su32(&ctl.q_free), ((uint32_t)qi & 1u) ^ 1u, abort_w, a.status);
-      if (!ok) break;
-      constexpr int CH = HD / 8, UNITS = N * CH / TM_QTHREADS, UB = UNITS < 4 ? UNITS : 4;
+      // all of the item's queries on their way before any is waited for, and
+      // before the scores of the item before are done with their places
+      constexpr int CH = HD / 8, ALL = N * CH / TM_QTHREADS, UNITS = ALL < 16 ? ALL : 16;
+      unsigned long long mask[(N + 31) / 32];
+      float x[UNITS][8];
 #pragma unroll 1
-      for (int u0 = 0; u0 < UNITS; u0 += UB) {
-        float x[UB][8];
+      for (int u0 = 0; u0 < ALL; u0 += UNITS) {
 #pragma unroll
-        for (int u = 0; u < UB; ++u) {
-          const int e = (u0 + u) * TM_QTHREADS + qt, n = e / CH, c = e % CH, row = m.n0 + n;
-          const float* q = a.q + (size_t)(m.t.row0 + row / rep) * a.ldq + (size_t)(m.g * rep + row % rep) * HD + c * 8;
-          if (n >= m.rows) {
+      for (int u = 0; u < UNITS; ++u) {
+        const int e = (u0 + u) * TM_QTHREADS + qt, n = e / CH, c = e % CH, row = m.n0 + n, node = div_rep(row);
+        const float* q = a.q + (size_t)(m.t.row0 + node) * a.ldq + (size_t)(m.g * rep + row - node * rep) * HD + c * 8;
+        if (n >= m.rows) {
 #pragma unroll
-            for (int h = 0; h < 8; ++h) x[u][h] = 0.f;
-          } else if (vec) {
-            const float4 v = *reinterpret_cast<const float4*>(q), w = *reinterpret_cast<const float4*>(q + 4);
-            x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
-            x[u][4] = w.x; x[u][5] = w.y; x[u][6] = w.z; x[u][7] = w.w;
-          } else {
+          for (int h = 0; h < 8; ++h) x[u][h] = 0.f;
+        } else if (vec) {
+          const float4 v = *reinterpret_cast<const float4*>(q), w = *reinterpret_cast<const float4*>(q + 4);
+          x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
+          x[u][4] = w.x; x[u][5] = w.y; x[u][6] = w.z; x[u][7] = w.w;
+        } else {
 #pragma unroll
-            for (int h = 0; h < 8; ++h) x[u][h] = q[h];
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < UB; ++u) {
-          const int e = (u0 + u) * TM_QTHREADS + qt, n = e / CH, c = e % CH;
-          uint8_t* dst = sp + C::Q + (c >> 3) * 3 * C::TERM + n * 128 + (((c & 7) ^ (n & 7)) << 4);
-#pragma unroll
-          for (int term = 0; term < 3; ++term) {  // x = the sum of its three terms
-            uint32_t w[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              w[h] = pack_bf16(make_float2(x[u][2 * h], x[u][2 * h + 1]));
-              x[u][2 * h] -= __uint_as_float(w[h] << 16);
-              x[u][2 * h + 1] -= __uint_as_float(w[h] & 0xffff0000u);
-            }
-            *reinterpret_cast<uint4*>(dst + term * C::TERM) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int h = 0; h < 8; ++h) x[u][h] = q[h];
         }
       }
-      for (int n = qt; n < N; n += TM_QTHREADS)
-        ctl.mask[qi % TM_MASKS][n] = n < m.rows ? a.masks[m.t.row0 + (m.n0 + n) / rep] : 0ull;
+      if (u0 == 0) {
+#pragma unroll
+        for (int j = 0; j < (N + 31) / 32; ++j) {
+          const int n = qt + 32 * j;
+          mask[j] = n < m.rows ? a.masks[m.t.row0 + div_rep(m.n0 + n)] : 0ull;
+        }
+        ok = tm_wait(su32(&ctl.q_free), ((uint32_t)qi & 1u) ^ 1u, abort_w, a.status);
+        if (!ok) break;
+      }
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int e = (u0 + u) * TM_QTHREADS + qt, n = e / CH, c = e % CH;
+        uint8_t* dst = sp + C::Q + (c >> 3) * 3 * C::TERM + n * 128 + (((c & 7) ^ (n & 7)) << 4);
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {  // x = the sum of its three terms
+          uint32_t w[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            w[h] = pack_bf16(make_float2(x[u][2 * h], x[u][2 * h + 1]));
+            const float2 r = add2(make_float2(x[u][2 * h], x[u][2 * h + 1]),
+                                  make_float2(-__uint_as_float(w[h] << 16), -__uint_as_float(w[h] & 0xffff0000u)));
+            x[u][2 * h] = r.x;
+            x[u][2 * h + 1] = r.y;
+          }
+          *reinterpret_cast<uint4*>(dst + term * C::TERM) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int j = 0; j < (N + 31) / 32; ++j)
+        if (qt + 32 * j < N) ctl.mask[qi % TM_MASKS][qt + 32 * j] = mask[j];
       proxy_fence();
       mbar_arrive(su32(&ctl.q_full[qi % TM_MASKS]));
       ++qi;
@@ -627,23 +651,25 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
           }
           // positions of the warp whose values are infinite or NaN: a row that sees one is NaN
           const unsigned bad = __ballot_sync(0xffffffffu, mine);
+          const int first = p0 + (lane >> 2) - m.t.L;  // this lane's positions, counted from the first node: first + 8 q
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int off = 8 * q + (lane >> 2), ps = p0 + off;
-            if (ps >= m.t.L) {
-              const int j = min(ps - m.t.L, 63);
+          for (int b = 0; b < NB; ++b)
 #pragma unroll
-              for (int b = 0; b < NB; ++b)
+            for (int e = 0; e < 2; ++e) {
+              const unsigned long long mk = ctl.mask[qi % TM_MASKS][8 * b + n2 + e];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  uint32_t& x = f[q >> 1][4 * b + 2 * (q & 1) + e];
-                  if (ps >= m.t.P || ((ctl.mask[qi % TM_MASKS][8 * b + n2 + e] >> j) & 1ull) == 0)
+              for (int q = 0; q < 4; ++q) {
+                uint32_t& x = f[q >> 1][4 * b + 2 * (q & 1) + e];
+                const int j = first + 8 * q;
+                const uint32_t word = (j & 32) ? (uint32_t)(mk >> 32) : (uint32_t)mk;
+                if (j >= 0) {
+                  if (j >= m.t.T || ((word >> (j & 31)) & 1u) == 0)
                     x = 0xff800000u;  // -inf
-                  else if ((bad >> off) & 1u)
+                  else if ((bad >> (8 * q + (lane >> 2))) & 1u)
                     x = 0x7fc00000u;
                 }
+              }
             }
-          }
         }
         float top = -INFINITY;
 #pragma unroll
@@ -742,7 +768,10 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
           }
         }
         soft_sync();
-        if (tid < N) ctl.sum[tid] = (ctl.part[0][tid] + ctl.part[1][tid]) + (ctl.part[2][tid] + ctl.part[3][tid]);
+        if (tid < N) {
+          const float sum = (ctl.part[0][tid] + ctl.part[1][tid]) + (ctl.part[2][tid] + ctl.part[3][tid]);
+          ctl.sum[tid] = CL > 1 ? sum : (sum == 0.f ? 0.f : 1.f / sum);  // a row that saw nothing: zeroes
+        }
         soft_sync();
         if (CL > 1) {
           float* os = reinterpret_cast<float*>(sp + C::RING);  // [N][HD]: the ring is idle now
@@ -757,8 +786,7 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
 #pragma unroll
           for (int n = 0; n < N; ++n)
             if (n < m.rows) {
-              const float sum = ctl.sum[n];
-              *dst = sum == 0.f ? 0.f : o[n] / sum;
+              *dst = o[n] * ctl.sum[n];
               if (++r == rep) {
                 r = 0;
                 dst += wrap;
@@ -853,6 +881,7 @@ int launch_mma(const TreeArgs& a, int layers, int dev, int n_sm, cudaStream_t s)
   // split items: one for each cluster; whole ones: a CTA on every SM works through them
   const long grid = c > 1 ? items * c : (items < n_sm ? items : n_sm);
   const int vec = ((uintptr_t)a.q & 15) == 0 && a.ldq % 4 == 0;
+  const unsigned rep = (unsigned)(a.Hq / a.kv.Hkv), rep_inv = (unsigned)(((1ull << 32) + rep - 1) / rep);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(TM_THREADS);
@@ -866,7 +895,7 @@ int launch_mma(const TreeArgs& a, int layers, int dev, int n_sm, cudaStream_t s)
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, tree_mma_kernel<HD, N>, map, a, row_tiles, box, (int)items, vec) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, tree_mma_kernel<HD, N>, map, a, row_tiles, box, (int)items, vec, rep_inv) == cudaSuccess
              ? Q3TTS_OK
              : Q3TTS_ERR_CUDA;
 }

@@ -120,7 +120,8 @@ typedef struct q3tts_kv_cache {
  *   masks_dev       uint64 [n_rows], 8-byte aligned.
  *   q_dev, out_dev  fp32 [n_rows] rows of n_q_heads x head_dim, ldq and ldo
  *                   elements apart; q head h reads kv head
- *                   h / (n_q_heads / n_kv_heads); scale 1 / sqrt(head_dim).
+ *                   h / (n_q_heads / n_kv_heads), at most 1024 of them one;
+ *                   scale 1 / sqrt(head_dim).
  * Rows outside every sequence's range are left as they were, like the rows of
  * a sequence whose entries do not fit (reported in status_dev).  out may not
  * overlap q.  Accumulation in fp32; a row's result does not depend on the run,
