@@ -54,7 +54,7 @@ namespace {
 constexpr int TM_PT = 128;       // positions of a tile
 constexpr int TM_THREADS = 256;  // softmax warps 0..3, TMA warps 4 (keys) and 7 (values), MMA warp 5, query warp 6
 constexpr int TM_QTHREADS = 32;
-constexpr int TM_SORT = 256;     // sequences that are dealt by length
+constexpr int TM_SORT = TM_THREADS;  // sequences that are dealt by length, at most
 constexpr int TM_MASKS = 4;      // items whose masks are held: the softmax's, and the scores may be three ahead
 constexpr long long TM_WAIT_CYCLES = 4000000000ll;  // ~2 s
 constexpr float TM_FLOOR = -1e30f;  // base of a row that has seen nothing: below every score
@@ -77,7 +77,7 @@ struct TmCfg {
   static constexpr uint32_t TM_S = G * N, TM_O = 2 * TM_S;  // columns: S twice, O twice
   static constexpr uint32_t TMEM_COLS = 4 * G * N <= 256 ? 256 : 512;
   // three: the softmax of tile t waits for V_t, which takes the place of K_t at the latest
-  static_assert(S >= 3 && 4 * G * N <= 512 && N * HD * 4 <= (int)(S * SLOT), "ring, tensor memory, joined output");
+  static_assert(S >= 3 && 4 * G * N <= 512 && N * HD * 4 <= (int)(NP * PBYTES), "ring, tensor memory, output rows");
 };
 
 // Control block (shared memory).
@@ -89,6 +89,7 @@ struct TmCtl {
   float base[N], corr[N], sum[N];  // a row's base, the factor of its last rise, its sum of weights
   float part[4][N];
   unsigned long long mask[TM_MASKS][N];
+  int len[TM_SORT];
   uint16_t order[TM_SORT];  // sequences, longest first
 };
 
@@ -221,8 +222,7 @@ __device__ __forceinline__ bool soft_any(bool p) {
 
 // Bounded wait on an mbarrier phase; false on expiry or when another role of
 // the CTA has given up.
-__device__ __forceinline__ bool tm_wait(uint32_t bar, uint32_t parity, volatile int* abort_w, int* status) {
-  if (mbar_try_wait(bar, parity)) return true;
+__device__ __noinline__ bool tm_wait_long(uint32_t bar, uint32_t parity, volatile int* abort_w, int* status) {
   const long long t0 = clock64();
   unsigned it = 0;
   while (!mbar_try_wait(bar, parity)) {
@@ -236,6 +236,9 @@ __device__ __forceinline__ bool tm_wait(uint32_t bar, uint32_t parity, volatile 
     }
   }
   return true;
+}
+__device__ __forceinline__ bool tm_wait(uint32_t bar, uint32_t parity, volatile int* abort_w, int* status) {
+  return mbar_try_wait(bar, parity) || tm_wait_long(bar, parity, abort_w, status);
 }
 
 // Max or sum over the lanes that hold the same columns (lane % 4).
@@ -261,9 +264,36 @@ struct TmItem {
   int t0, nt;            // first position tile, tiles
 };
 
+// How the items are dealt.
+struct TmDeal {
+  int items, row_tiles, rows;  // rows of a tile
+  int stride, first;           // clusters, this one
+  int rank, cl;                // CTA of the cluster, CTAs
+  const uint16_t* order;       // sequences, longest first, or NULL
+};
+
+// The k-th item of a CTA: 1 if there is one, 0 if it has no rows (or does not
+// fit, which is reported), -1 past the last.
+__device__ __forceinline__ int tm_item(const TreeArgs& a, const TmDeal& d, int k, TmItem& m) {
+  if ((long long)k * d.stride >= d.items) return -1;
+  const int idx = k * d.stride + ((k & 1) ? d.stride - 1 - d.first : d.first);
+  if (idx >= d.items) return 0;
+  const int rep = a.Hq / a.kv.Hkv;
+  m.g = idx / d.row_tiles % a.kv.Hkv;
+  m.seq = idx / d.row_tiles / a.kv.Hkv;
+  if (d.order) m.seq = d.order[m.seq];
+  m.n0 = idx % d.row_tiles * d.rows;
+  if (!tree_seq(a, m.seq, m.t) || m.n0 >= m.t.T * rep) return 0;
+  m.rows = min(d.rows, m.t.T * rep - m.n0);
+  const int all = (m.t.P + TM_PT - 1) / TM_PT, per = (all + d.cl - 1) / d.cl;
+  m.t0 = min(all, d.rank * per);
+  m.nt = min(all, m.t0 + per) - m.t0;
+  return 1;
+}
+
 template <int HD, int N>
 __global__ void __launch_bounds__(TM_THREADS, 1)
-    tree_mma_kernel(const __grid_constant__ CUtensorMap map, TreeArgs a, int row_tiles, int box, int items, int vec,
+    tree_mma_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ TreeArgs a, int row_tiles, int box, int items, int vec,
                     unsigned rep_inv) {
   using C = TmCfg<HD, N>;
   using Ctl = TmCtl<N, C::S>;
@@ -304,14 +334,17 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
   }
   pdl_wait();  // q and the appended keys and values come from the previous kernels
   const bool sorted = items > (int)gridDim.x / CL && a.n_seqs <= TM_SORT;
-  if (sorted && tid < a.n_seqs) {
-    const int mine = a.lengths[tid];
+  if (sorted) {
+    const int mine = tid < a.n_seqs ? a.lengths[tid] : 0;
+    ctl.len[tid] = mine;
+    __syncthreads();
     int r = 0;
+#pragma unroll 8
     for (int j = 0; j < a.n_seqs; ++j) {
-      const int o = a.lengths[j];
+      const int o = ctl.len[j];
       r += o > mine || (o == mine && j < tid);
     }
-    ctl.order[r] = (uint16_t)tid;
+    if (tid < a.n_seqs) ctl.order[r] = (uint16_t)tid;
   }
   tc_fence_before();
   __syncthreads();
@@ -319,25 +352,8 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
   const uint32_t tmem = ctl.tmem;
   const uint32_t ring = sbase + C::RING;
 
-  // The k-th item of this CTA: 1 if there is one, 0 if it has no rows (or does
-  // not fit, which is reported), -1 past the last.
-  const int stride = (int)gridDim.x / CL, first = (int)blockIdx.x / CL;
-  auto get_item = [&](int k, TmItem& m) -> int {
-    if ((long long)k * stride >= items) return -1;
-    const int idx = k * stride + ((k & 1) ? stride - 1 - first : first);
-    if (idx >= items) return 0;
-    const int rt = idx % row_tiles;
-    m.g = idx / row_tiles % a.kv.Hkv;
-    m.seq = idx / row_tiles / a.kv.Hkv;
-    if (sorted) m.seq = ctl.order[m.seq];
-    m.n0 = rt * N;
-    if (!tree_seq(a, m.seq, m.t) || m.n0 >= m.t.T * rep) return 0;
-    m.rows = min(N, m.t.T * rep - m.n0);
-    const int all = (m.t.P + TM_PT - 1) / TM_PT, per = (all + CL - 1) / CL;
-    m.t0 = min(all, rank * per);
-    m.nt = min(all, m.t0 + per) - m.t0;
-    return 1;
-  };
+  const TmDeal deal{items, row_tiles, N, (int)gridDim.x / CL, (int)blockIdx.x / CL, rank, CL,
+                    sorted ? ctl.order : nullptr};
   // row / rep for rows of an item (rep_inv = ceil(2^32 / rep); exact for rows and rep up to 2^16)
   auto div_rep = [&](int row) -> int { return rep == 1 ? row : (int)__umulhi((unsigned)row, rep_inv); };
   TmItem m;
@@ -355,7 +371,7 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
     const int ps = a.kv.page_size;
     const long long plane = (long long)a.kv.Hkv * ps;  // rows of a page's keys (or values)
     int ic = 0;                                        // tiles put into the ring
-    for (int k = 0; ok && (have = get_item(k, m)) >= 0; ++k) {
+    for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
       if (have == 0 || m.nt == 0) continue;
       const int* table = a.kv.page_table + (size_t)m.seq * a.kv.pages_per_stream;
       // the page of this lane's box in tile i; looked up two tiles ahead and not
@@ -408,7 +424,7 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
       // from the next atom and their results are not used
       constexpr uint32_t v_lead = HD == 128 ? TM_PT * 128 : 1024;
       int ic = 0, tc = 0, qi = 0;  // ring tiles, position tiles and items so far
-      for (int k = 0; ok && (have = get_item(k, m)) >= 0; ++k) {
+      for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
         if (have == 0 || m.nt == 0) continue;
         ok = tm_wait(su32(&ctl.q_full[qi % TM_MASKS]), (uint32_t)(qi / TM_MASKS) & 1u, abort_w, a.status);
         tc_fence_after();
@@ -467,65 +483,51 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
     __syncwarp();
   } else if (warp == 6) {
     // ---- queries and masks of the next item, as soon as the scores of the one before are done
-    const int qt = lane;
     int qi = 0;
-    for (int k = 0; ok && (have = get_item(k, m)) >= 0; ++k) {
+    for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
       if (have == 0 || m.nt == 0) continue;
-      // all of the item's queries on their way before any is waited for, and
-      // before the scores of the item before are done with their places
-      constexpr int CH = HD / 8, ALL = N * CH / TM_QTHREADS, UNITS = ALL < 16 ? ALL : 16;
-      unsigned long long mask[(N + 31) / 32];
-      float x[UNITS][8];
+      // four elements of a row per lane, eight loads on their way at a time;
+      // the first before the scores of the item before are done with Q's place
+      constexpr int CH = HD / 4, ALL = N * CH / TM_QTHREADS, UNITS = 8, MK = (N + 31) / 32;
+      unsigned long long mask[MK];
+#pragma unroll
+      for (int j = 0; j < MK; ++j) {
+        const int n = lane + 32 * j;
+        mask[j] = n < m.rows ? a.masks[m.t.row0 + div_rep(m.n0 + n)] : 0ull;
+      }
 #pragma unroll 1
-      for (int u0 = 0; u0 < ALL; u0 += UNITS) {
+      for (int u0 = 0; u0 < ALL && ok; u0 += UNITS) {
+        float4 x[UNITS];
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        const int e = (u0 + u) * TM_QTHREADS + qt, n = e / CH, c = e % CH, row = m.n0 + n, node = div_rep(row);
-        const float* q = a.q + (size_t)(m.t.row0 + node) * a.ldq + (size_t)(m.g * rep + row - node * rep) * HD + c * 8;
-        if (n >= m.rows) {
-#pragma unroll
-          for (int h = 0; h < 8; ++h) x[u][h] = 0.f;
-        } else if (vec) {
-          const float4 v = *reinterpret_cast<const float4*>(q), w = *reinterpret_cast<const float4*>(q + 4);
-          x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
-          x[u][4] = w.x; x[u][5] = w.y; x[u][6] = w.z; x[u][7] = w.w;
-        } else {
-#pragma unroll
-          for (int h = 0; h < 8; ++h) x[u][h] = q[h];
+        for (int u = 0; u < UNITS; ++u) {
+          const int e = (u0 + u) * TM_QTHREADS + lane, n = e / CH, row = m.n0 + n, node = div_rep(row);
+          const float* q =
+              a.q + (size_t)(m.t.row0 + node) * a.ldq + (size_t)(m.g * rep + row - node * rep) * HD + e % CH * 4;
+          x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (n < m.rows) x[u] = (vec & 1) ? *reinterpret_cast<const float4*>(q) : make_float4(q[0], q[1], q[2], q[3]);
         }
-      }
-      if (u0 == 0) {
-#pragma unroll
-        for (int j = 0; j < (N + 31) / 32; ++j) {
-          const int n = qt + 32 * j;
-          mask[j] = n < m.rows ? a.masks[m.t.row0 + div_rep(m.n0 + n)] : 0ull;
-        }
-        ok = tm_wait(su32(&ctl.q_free), ((uint32_t)qi & 1u) ^ 1u, abort_w, a.status);
+        if (u0 == 0) ok = tm_wait(su32(&ctl.q_free), ((uint32_t)qi & 1u) ^ 1u, abort_w, a.status);
         if (!ok) break;
-      }
+        if (u0 == 0) {
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        const int e = (u0 + u) * TM_QTHREADS + qt, n = e / CH, c = e % CH;
-        uint8_t* dst = sp + C::Q + (c >> 3) * 3 * C::TERM + n * 128 + (((c & 7) ^ (n & 7)) << 4);
-#pragma unroll
-        for (int term = 0; term < 3; ++term) {  // x = the sum of its three terms
-          uint32_t w[4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            w[h] = pack_bf16(make_float2(x[u][2 * h], x[u][2 * h + 1]));
-            const float2 r = add2(make_float2(x[u][2 * h], x[u][2 * h + 1]),
-                                  make_float2(-__uint_as_float(w[h] << 16), -__uint_as_float(w[h] & 0xffff0000u)));
-            x[u][2 * h] = r.x;
-            x[u][2 * h + 1] = r.y;
-          }
-          *reinterpret_cast<uint4*>(dst + term * C::TERM) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int j = 0; j < MK; ++j)
+            if (lane + 32 * j < N) ctl.mask[qi % TM_MASKS][lane + 32 * j] = mask[j];
         }
-      }
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          const int e = (u0 + u) * TM_QTHREADS + lane, n = e / CH, c = e % CH;
+          uint8_t* dst = sp + C::Q + (c >> 4) * 3 * C::TERM + n * 128 + ((((c >> 1) & 7) ^ (n & 7)) << 4) + (c & 1) * 8;
+          float2 v = make_float2(x[u].x, x[u].y), w = make_float2(x[u].z, x[u].w);
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {  // x = the sum of its three terms
+            const uint32_t p = pack_bf16(v), r = pack_bf16(w);
+            *reinterpret_cast<uint2*>(dst + term * C::TERM) = make_uint2(p, r);
+            v = add2(v, make_float2(-__uint_as_float(p << 16), -__uint_as_float(p & 0xffff0000u)));
+            w = add2(w, make_float2(-__uint_as_float(r << 16), -__uint_as_float(r & 0xffff0000u)));
+          }
+        }
       }
       if (!ok) break;
-#pragma unroll
-      for (int j = 0; j < (N + 31) / 32; ++j)
-        if (qt + 32 * j < N) ctl.mask[qi % TM_MASKS][qt + 32 * j] = mask[j];
       proxy_fence();
       mbar_arrive(su32(&ctl.q_full[qi % TM_MASKS]));
       ++qi;
@@ -542,11 +544,11 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
     const uint32_t p_lane = (uint32_t)(warp >> 1) * (3 * C::TERM) + (lane & 7) * 128 +
                             (((((warp & 1) * 4) + (lane >> 3)) ^ (lane & 7)) << 4);
     int ic = 0, tc = 0, qi = 0;
-    for (int k = 0; ok && (have = get_item(k, m)) >= 0; ++k) {
+    for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
       if (have == 0) continue;
       float2 base[NB], l[NB];  // negated base, sum of the weights
       float o[N];              // element tid of the running output's rows
-      bool added = true;       // the output of the tile before is in o
+      bool scaled = false;     // the bases rose with this tile: the outputs before it are still to be scaled
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         base[b] = make_float2(-TM_FLOOR, -TM_FLOOR);
@@ -558,30 +560,6 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
         ctl.base[tid] = TM_FLOOR;
         ctl.sum[tid] = 0.f;
       }
-      // adds the output of the CTA's t-th tile to the running one, once it is complete
-      auto add_output = [&](int t, bool wait) -> bool {
-        if (wait && !tm_wait(su32(&ctl.p_free[t % C::NP]), (uint32_t)(t / C::NP) & 1u, abort_w, a.status)) return false;
-        tc_fence_after();
-        const uint32_t src = tmem + C::TM_O + (t & 1) * C::TM_S + lanes;
-#pragma unroll
-        for (int n = 0; n < N; n += 16) {
-          uint32_t v[C::G][16];
-#pragma unroll
-          for (int gr = 0; gr < C::G; ++gr) tmem_ld16(src + gr * N + n, v[gr]);
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float2 r = make_float2(__uint_as_float(v[C::G - 1][e]), __uint_as_float(v[C::G - 1][e + 1]));
-#pragma unroll
-            for (int gr = C::G - 2; gr >= 0; --gr)
-              r = add2(r, make_float2(__uint_as_float(v[gr][e]), __uint_as_float(v[gr][e + 1])));
-            r = add2(r, make_float2(o[n + e], o[n + e + 1]));
-            o[n + e] = r.x;
-            o[n + e + 1] = r.y;
-          }
-        }
-        return true;
-      };
       if (m.nt > 0) {  // the item's masks are there
         ok = tm_wait(su32(&ctl.q_full[qi % TM_MASKS]), (uint32_t)(qi / TM_MASKS) & 1u, abort_w, a.status);
         if (soft_any(!ok)) {
@@ -589,8 +567,9 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
           break;
         }
       }
-      for (int i = 0; i < m.nt; ++i) {
+      for (int i = 0; i <= m.nt; ++i) {
         const int t = tc + i, pb = t % C::NP;
+        if (i < m.nt) {
         ok = tm_wait(su32(&ctl.s_full[t & 1]), (uint32_t)(t >> 1) & 1u, abort_w, a.status) && ok;
         if (soft_any(!ok)) {
           ok = false;
@@ -646,30 +625,29 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
             }
           }
           if (pos >= m.t.P || mine) {
-#pragma unroll
+#pragma unroll 4
             for (int e = 0; e < C::BLK * 8; ++e) vr[(e >> 3) * (TM_PT * 8) + (e & 7)] = make_uint4(0, 0, 0, 0);
           }
           // positions of the warp whose values are infinite or NaN: a row that sees one is NaN
           const unsigned bad = __ballot_sync(0xffffffffu, mine);
-          const int first = p0 + (lane >> 2) - m.t.L;  // this lane's positions, counted from the first node: first + 8 q
+          // this lane's positions, counted from the first node (negative: committed)
+          const uint32_t* words = reinterpret_cast<const uint32_t*>(ctl.mask[qi % TM_MASKS]) + 2 * n2;
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
+          for (int q = 0; q < 4; ++q) {
+            const int off = 8 * q + (lane >> 2), j = p0 + off - m.t.L;
+            if (j >= 0) {
+              const uint32_t past = j >= m.t.T ? 0u : ~0u, seen = (bad >> off) & 1u ? 0x7fc00000u : 0u;
+              const uint32_t* w = words + (min(j, 63) >> 5);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const unsigned long long mk = ctl.mask[qi % TM_MASKS][8 * b + n2 + e];
+              for (int b = 0; b < NB; ++b)
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                uint32_t& x = f[q >> 1][4 * b + 2 * (q & 1) + e];
-                const int j = first + 8 * q;
-                const uint32_t word = (j & 32) ? (uint32_t)(mk >> 32) : (uint32_t)mk;
-                if (j >= 0) {
-                  if (j >= m.t.T || ((word >> (j & 31)) & 1u) == 0)
-                    x = 0xff800000u;  // -inf
-                  else if ((bad >> (8 * q + (lane >> 2))) & 1u)
-                    x = 0x7fc00000u;
+                for (int e = 0; e < 2; ++e) {
+                  uint32_t& x = f[q >> 1][4 * b + 2 * (q & 1) + e];
+                  const bool sees = ((w[16 * b + 2 * e] & past) >> (j & 31)) & 1u;
+                  x = sees ? (seen ? seen : x) : 0xff800000u;  // -inf
                 }
-              }
             }
+          }
         }
         float top = -INFINITY;
 #pragma unroll
@@ -705,12 +683,7 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
             ctl.corr[tid] = nb == old ? 1.f : exp2_fast(old - nb);
             ctl.base[tid] = nb;
           }
-          if (!added) ok = add_output(t - 1, true);
-          added = true;
-          if (soft_any(!ok)) {
-            ok = false;
-            break;
-          }
+          soft_sync();
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             const int n = 8 * b + n2;
@@ -718,8 +691,7 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
             l[b].x *= ctl.corr[n];
             l[b].y *= ctl.corr[n + 1];
           }
-#pragma unroll
-          for (int n = 0; n < N; ++n) o[n] *= ctl.corr[n];
+          scaled = true;
         }
         ok = tm_wait(su32(&ctl.p_free[pb]), ((uint32_t)(t / C::NP) & 1u) ^ 1u, abort_w, a.status) && ok;
         const uint32_t ph = sbase + C::P + pb * C::PBYTES + p_lane;
@@ -747,14 +719,40 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
         proxy_fence();
         tc_fence_before();
         mbar_arrive(su32(&ctl.p_full[pb]));
-        // the tensor cores have had this tile's softmax to finish the one before
-        // (one P buffer: it was complete before this tile's P was written, and
-        // its barrier may be a phase further by now)
-        if (!added) ok = add_output(t - 1, C::NP > 1) && ok;
-        added = false;
+        }
+        // the output of the tile before joins the running one: the tensor cores
+        // have had this tile's softmax to finish it (one P buffer: it was complete
+        // before this tile's P was written, and its barrier may be a phase on)
+        if (i > 0) {
+          if (C::NP > 1 || i == m.nt)
+            ok = tm_wait(su32(&ctl.p_free[(t - 1) % C::NP]), (uint32_t)((t - 1) / C::NP) & 1u, abort_w, a.status) && ok;
+          tc_fence_after();
+          const uint32_t src = tmem + C::TM_O + ((t - 1) & 1) * C::TM_S + lanes;
+#pragma unroll
+          for (int n = 0; n < N; n += 16) {
+            uint32_t v[C::G][16];
+#pragma unroll
+            for (int gr = 0; gr < C::G; ++gr) tmem_ld16(src + gr * N + n, v[gr]);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              float2 r = make_float2(__uint_as_float(v[C::G - 1][e]), __uint_as_float(v[C::G - 1][e + 1]));
+#pragma unroll
+              for (int gr = C::G - 2; gr >= 0; --gr)
+                r = add2(r, make_float2(__uint_as_float(v[gr][e]), __uint_as_float(v[gr][e + 1])));
+              r = add2(r, make_float2(o[n + e], o[n + e + 1]));
+              o[n + e] = r.x;
+              o[n + e + 1] = r.y;
+            }
+          }
+          if (scaled) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) o[n] *= ctl.corr[n];
+          }
+        }
+        scaled = false;
       }
       if (m.nt > 0) {
-        if (ok) ok = add_output(tc + m.nt - 1, true);
         if (soft_any(!ok)) {  // every softmax thread comes here, whichever of them gave up
           ok = false;
           break;
@@ -773,29 +771,32 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
           ctl.sum[tid] = CL > 1 ? sum : (sum == 0.f ? 0.f : 1.f / sum);  // a row that saw nothing: zeroes
         }
         soft_sync();
-        if (CL > 1) {
-          float* os = reinterpret_cast<float*>(sp + C::RING);  // [N][HD]: the ring is idle now
-          if (tid < HD) {
+        // the rows, through P's place (its readers are done) to whole lines
+        float* os = reinterpret_cast<float*>(sp + C::P);  // [N][HD]
+        if (tid < HD) {
 #pragma unroll
-            for (int n = 0; n < N; ++n) os[n * HD + tid] = o[n];
-          }
-        } else if (tid < HD) {
-          int node = m.n0 / rep, r = m.n0 % rep;
-          float* dst = a.out + (size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + r) * HD + tid;
-          const int wrap = a.ldo - (rep - 1) * HD;
-#pragma unroll
-          for (int n = 0; n < N; ++n)
-            if (n < m.rows) {
-              *dst = o[n] * ctl.sum[n];
-              if (++r == rep) {
-                r = 0;
-                dst += wrap;
-              } else {
-                dst += HD;
-              }
-            }
+          for (int n = 0; n < N; ++n) os[n * HD + tid] = o[n];
         }
-        soft_sync();  // the sums may be written again
+        soft_sync();
+        if (CL == 1) {
+          constexpr int LPR = HD / 4;  // lanes of a row
+#pragma unroll 1
+          for (int n = tid / LPR; n < m.rows; n += 128 / LPR) {
+            const int row = m.n0 + n, node = div_rep(row), d = tid % LPR * 4;
+            const float4 v = *reinterpret_cast<const float4*>(os + n * HD + d);
+            const float f = ctl.sum[n];
+            float* dst = a.out + (size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + row - node * rep) * HD + d;
+            if (vec & 2) {
+              *reinterpret_cast<float4*>(dst) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+            } else {
+              dst[0] = v.x * f;
+              dst[1] = v.y * f;
+              dst[2] = v.z * f;
+              dst[3] = v.w * f;
+            }
+          }
+          soft_sync();  // P and the sums may be written again
+        }
         ic += 2 * m.nt;
         tc += m.nt;
         ++qi;
@@ -804,24 +805,61 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
     }
     if (!ok) *abort_w = 1;
   }
-  if (CL > 1 && (have = get_item(0, m)) == 1) {
-    // join: each CTA takes every CL-th row
+  if (CL > 1 && (have = tm_item(a, deal, 0, m)) == 1) {
+    // join: what each share's output of a row counts for, then every CL-th row
     cl.sync();
-    if (warp < 4 && !*abort_w && tid < HD) {
-      for (int n = rank; n < m.rows; n += CL) {
-        float mx = TM_FLOOR;
-        for (int r = 0; r < CL; ++r) mx = fmaxf(mx, *cl.map_shared_rank(&ctl.base[n], r));
-        float sum = 0.f, acc = 0.f;
-        for (int r = 0; r < CL; ++r) {
-          const float lr = *cl.map_shared_rank(&ctl.sum[n], r);
-          if (lr == 0.f) continue;  // this share saw nothing
-          const float f = exp2_fast(*cl.map_shared_rank(&ctl.base[n], r) - mx);
-          sum = fmaf(lr, f, sum);
-          acc = fmaf(cl.map_shared_rank(reinterpret_cast<float*>(sp + C::RING), r)[n * HD + tid], f, acc);
+    float* fac = reinterpret_cast<float*>(ctl.mask);  // [CL][N], where the masks were
+    static_assert(sizeof(ctl.mask) >= 8 * N * sizeof(float), "a factor per share and row");
+    if (tid < N) {
+      float bs[8], sm[8], mx = TM_FLOOR, sum = 0.f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        bs[r] = r < CL ? *cl.map_shared_rank(&ctl.base[tid], r) : TM_FLOOR;
+        sm[r] = r < CL ? *cl.map_shared_rank(&ctl.sum[tid], r) : 0.f;
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r) mx = fmaxf(mx, bs[r]);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        bs[r] = sm[r] == 0.f ? 0.f : exp2_fast(bs[r] - mx);  // 0: the share saw nothing
+        sum = fmaf(sm[r], bs[r], sum);
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < CL) fac[r * N + tid] = sum == 0.f ? 0.f : bs[r] / sum;
+    }
+    __syncthreads();
+    constexpr int LPR = HD / 4;  // lanes of a row
+    if (!*abort_w) {
+      for (int n = rank + CL * (tid / LPR); n < m.rows; n += CL * (TM_THREADS / LPR)) {
+        const int d = tid % LPR * 4;
+        float4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)  // a share without tiles wrote no output: its factor is 0
+          v[r] = r < CL && fac[r * N + n] != 0.f
+                     ? *reinterpret_cast<const float4*>(
+                           cl.map_shared_rank(reinterpret_cast<float*>(sp + C::P), r) + n * HD + d)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < CL) {
+            const float f = fac[r * N + n];
+            o.x = fmaf(v[r].x, f, o.x);
+            o.y = fmaf(v[r].y, f, o.y);
+            o.z = fmaf(v[r].z, f, o.z);
+            o.w = fmaf(v[r].w, f, o.w);
+          }
+        const int row = m.n0 + n, node = div_rep(row);
+        float* dst = a.out + (size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + row - node * rep) * HD + d;
+        if (vec & 2) {
+          *reinterpret_cast<float4*>(dst) = o;
+        } else {
+          dst[0] = o.x;
+          dst[1] = o.y;
+          dst[2] = o.z;
+          dst[3] = o.w;
         }
-        const int row = m.n0 + n;
-        a.out[(size_t)(m.t.row0 + row / rep) * a.ldo + (size_t)(m.g * rep + row % rep) * HD + tid] =
-            sum == 0.f ? 0.f : acc / sum;
       }
     }
     cl.sync();  // the others may still read this CTA's shared memory
@@ -880,7 +918,8 @@ int launch_mma(const TreeArgs& a, int layers, int dev, int n_sm, cudaStream_t s)
   if (items > 0x7fffffffL / 2) return Q3TTS_ERR_UNSUPPORTED;
   // split items: one for each cluster; whole ones: a CTA on every SM works through them
   const long grid = c > 1 ? items * c : (items < n_sm ? items : n_sm);
-  const int vec = ((uintptr_t)a.q & 15) == 0 && a.ldq % 4 == 0;
+  const int vec = (((uintptr_t)a.q & 15) == 0 && a.ldq % 4 == 0 ? 1 : 0) |  // float4 loads of q, stores of out
+                  (((uintptr_t)a.out & 15) == 0 && a.ldo % 4 == 0 ? 2 : 0);
   const unsigned rep = (unsigned)(a.Hq / a.kv.Hkv), rep_inv = (unsigned)(((1ull << 32) + rep - 1) / rep);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
