@@ -52,9 +52,11 @@ namespace q3 {
 namespace {
 
 constexpr int TM_PT = 128;       // positions of a tile
-constexpr int TM_THREADS = 256;  // softmax warps 0..3, TMA warps 4 (keys) and 7 (values), MMA warp 5, query warp 6
+#ifndef TM_ONE
+#define TM_ONE 32
+#endif
 constexpr int TM_QTHREADS = 32;
-constexpr int TM_SORT = TM_THREADS;  // sequences that are dealt by length, at most
+constexpr int TM_SORT = 256;     // sequences that are dealt by length, at most (no more than threads)
 constexpr int TM_MASKS = 4;      // items whose masks are held: the softmax's, and the scores may be three ahead
 constexpr long long TM_WAIT_CYCLES = 4000000000ll;  // ~2 s
 constexpr float TM_FLOOR = -1e30f;  // base of a row that has seen nothing: below every score
@@ -62,6 +64,11 @@ constexpr float TM_SLACK = 8.f;     // how far (log2) a score may pass its row's
 
 template <int HD, int N>
 struct TmCfg {
+  // softmax groups of four warps, each with its share of the rows; then one warp
+  // each for the keys' copies, the MMAs, the queries and the values' copies
+  static constexpr int SW = N <= TM_ONE ? 1 : 2, NC = N / SW;
+  static constexpr int KEY_WARP = 4 * SW, MMA_WARP = KEY_WARP + 1, QUERY_WARP = KEY_WARP + 2, VALUE_WARP = KEY_WARP + 3;
+  static constexpr int THREADS = 128 * SW + 128;
   static constexpr int BLK = HD / 64;               // 128-byte swizzle blocks of a row
   static constexpr uint32_t SLOT = TM_PT * HD * 2;  // a K or V tile
   static constexpr uint32_t TERM = N * 128;         // one term of one 64-element block (of Q or P)
@@ -88,6 +95,7 @@ struct TmCtl {
   int abort_w;
   float base[N], corr[N], sum[N];  // a row's base, the factor of its last rise, its sum of weights
   float part[4][N];
+  unsigned bad[4];
   unsigned long long mask[TM_MASKS][N];
   int len[TM_SORT];
   uint16_t order[TM_SORT];  // sequences, longest first
@@ -208,14 +216,28 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Barrier and vote of the 128 softmax threads.
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool soft_any(bool p) {
+// Barrier and vote of the 128 threads of softmax group wg.
+__device__ __forceinline__ void soft_sync(int wg) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + 2 * wg) : "memory");
+}
+__device__ __forceinline__ bool soft_any(bool p, int wg) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"((uint32_t)p)
+      : "r"((uint32_t)p), "r"(2 + 2 * wg)
+      : "memory");
+  return r != 0;
+}
+// Barrier and vote of all softmax threads; giving up is decided here alone, so
+// that both groups leave together.
+template <int COUNT>
+__device__ __forceinline__ bool all_any(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 5, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "n"(COUNT)
       : "memory");
   return r != 0;
 }
@@ -292,7 +314,7 @@ __device__ __forceinline__ int tm_item(const TreeArgs& a, const TmDeal& d, int k
 }
 
 template <int HD, int N>
-__global__ void __launch_bounds__(TM_THREADS, 1)
+__global__ void __launch_bounds__(TmCfg<HD, N>::THREADS, 1)
     tree_mma_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ TreeArgs a, int row_tiles, int box, int items, int vec,
                     unsigned rep_inv) {
   using C = TmCfg<HD, N>;
@@ -316,8 +338,8 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(su32(&ctl.s_full[i]), 1);
-      mbar_init(su32(&ctl.s_free[i]), 128);
-      mbar_init(su32(&ctl.p_full[i]), 128);
+      mbar_init(su32(&ctl.s_free[i]), 128 * C::SW);
+      mbar_init(su32(&ctl.p_full[i]), 128 * C::SW);
       mbar_init(su32(&ctl.p_free[i]), 1);
     }
     for (int i = 0; i < TM_MASKS; ++i) mbar_init(su32(&ctl.q_full[i]), TM_QTHREADS);
@@ -326,7 +348,7 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
     ctl.abort_w = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 5) {
+  if (warp == C::MMA_WARP) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&ctl.tmem)),
                  "r"(C::TMEM_COLS)
                  : "memory");
@@ -336,7 +358,7 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
   const bool sorted = items > (int)gridDim.x / CL && a.n_seqs <= TM_SORT;
   if (sorted) {
     const int mine = tid < a.n_seqs ? a.lengths[tid] : 0;
-    ctl.len[tid] = mine;
+    if (tid < TM_SORT) ctl.len[tid] = mine;
     __syncthreads();
     int r = 0;
 #pragma unroll 8
@@ -360,12 +382,12 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
   int have = 0;
   bool ok = true;
 
-  if (warp == 4 || warp == 7) {
+  if (warp == C::KEY_WARP || warp == C::VALUE_WARP) {
     // ---- TMA: lane (b, blk) copies block blk of page b's rows of a tile; the
     // keys and the values each have a warp (a warp's lanes issue one by one, 55
     // cycles each: 32 copies of 2 KB for a tile of 16-position pages took longer
     // from one warp than the tile's bytes)
-    const bool values = warp == 7;
+    const bool values = warp == C::VALUE_WARP;
     const int b = lane / C::BLK, blk = lane % C::BLK;
     const int boxes = TM_PT / box;
     const int ps = a.kv.page_size;
@@ -415,7 +437,7 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
       while (!mbar_try_wait(su32(&ctl.full[j % C::S]), (uint32_t)(j / C::S) & 1u) && clock64() - c0 < TM_WAIT_CYCLES) {
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == C::MMA_WARP) {
     // ---- MMA issue
     if (lane == 0) {
       constexpr uint32_t idS = f16_idesc(TM_PT, (C::G == 3 ? 3 : 2) * N, false), idS1 = f16_idesc(TM_PT, N, false);
@@ -481,7 +503,7 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 6) {
+  } else if (warp == C::QUERY_WARP) {
     // ---- queries and masks of the next item, as soon as the scores of the one before are done
     int qi = 0;
     for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
@@ -533,21 +555,23 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
       ++qi;
     }
   } else {
-    // ---- softmax
+    // ---- softmax: group wg has rows c0 .. c0 + NC - 1 of the tile, one thread a position
+    constexpr int NC = C::NC;
+    const int wg = warp >> 2, wt = tid & 127, w4 = warp & 3, c0 = wg * NC;
     const float c = 1.4426950408889634f / sqrtf((float)HD);
     const float2 c2 = make_float2(c, c);
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    constexpr int NB = N / 8;  // blocks of eight rows; this thread holds rows n2, n2 + 1 of each
-    const int n2 = (lane & 3) * 2;
+    const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
+    constexpr int NB = NC / 8;  // blocks of eight rows; this thread holds rows n2, n2 + 1 of each
+    const int n2 = c0 + (lane & 3) * 2;
     // where this lane's row of the four matrices of a block starts in P: row
-    // lane % 8, positions 32 warp + 8 (lane / 8) ..
-    const uint32_t p_lane = (uint32_t)(warp >> 1) * (3 * C::TERM) + (lane & 7) * 128 +
-                            (((((warp & 1) * 4) + (lane >> 3)) ^ (lane & 7)) << 4);
+    // lane % 8, positions 32 w4 + 8 (lane / 8) ..
+    const uint32_t p_lane = (uint32_t)(w4 >> 1) * (3 * C::TERM) + (c0 + (lane & 7)) * 128 +
+                            (((((w4 & 1) * 4) + (lane >> 3)) ^ (lane & 7)) << 4);
     int ic = 0, tc = 0, qi = 0;
     for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
       if (have == 0) continue;
       float2 base[NB], l[NB];  // negated base, sum of the weights
-      float o[N];              // element tid of the running output's rows
+      float o[NC];             // element wt of the running output's rows
       bool scaled = false;     // the bases rose with this tile: the outputs before it are still to be scaled
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -555,14 +579,14 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
         l[b] = make_float2(0.f, 0.f);
       }
 #pragma unroll
-      for (int n = 0; n < N; ++n) o[n] = 0.f;
-      if (tid < N) {
-        ctl.base[tid] = TM_FLOOR;
-        ctl.sum[tid] = 0.f;
+      for (int n = 0; n < NC; ++n) o[n] = 0.f;
+      if (wt < NC) {
+        ctl.base[c0 + wt] = TM_FLOOR;
+        ctl.sum[c0 + wt] = 0.f;
       }
       if (m.nt > 0) {  // the item's masks are there
         ok = tm_wait(su32(&ctl.q_full[qi % TM_MASKS]), (uint32_t)(qi / TM_MASKS) & 1u, abort_w, a.status);
-        if (soft_any(!ok)) {
+        if (all_any<128 * C::SW>(!ok)) {
           ok = false;
           break;
         }
@@ -571,22 +595,22 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
         const int t = tc + i, pb = t % C::NP;
         if (i < m.nt) {
         ok = tm_wait(su32(&ctl.s_full[t & 1]), (uint32_t)(t >> 1) & 1u, abort_w, a.status) && ok;
-        if (soft_any(!ok)) {
+        if (all_any<128 * C::SW>(!ok)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        // scores of positions 32 warp + 16 h + 8 r + lane / 4, 32 rows at a time
-        uint32_t f[2][N / 2];
-        constexpr int W = N < 32 ? N : 32;
+        // scores of positions 32 w4 + 16 h + 8 r + lane / 4, 32 rows at a time
+        uint32_t f[2][NC / 2];
+        constexpr int W = NC < 32 ? NC : 32;
 #pragma unroll
-        for (int n = 0; n < N; n += W) {
+        for (int n = 0; n < NC; n += W) {
           uint32_t v[C::G][2][W / 2];
 #pragma unroll
           for (int gr = 0; gr < C::G; ++gr)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              tmem_frag<W>(tmem + (t & 1) * C::TM_S + gr * N + n + lanes + ((uint32_t)(16 * h) << 16), v[gr][h]);
+              tmem_frag<W>(tmem + (t & 1) * C::TM_S + gr * N + c0 + n + lanes + ((uint32_t)(16 * h) << 16), v[gr][h]);
           asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -602,34 +626,38 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
         }
         tc_fence_before();
         mbar_arrive(su32(&ctl.s_free[t & 1]));
-        const int p0 = (m.t0 + i) * TM_PT + warp * 32;  // the warp's first position
+        const int p0 = (m.t0 + i) * TM_PT + w4 * 32;  // the warp's first position
         if ((m.t0 + i + 1) * TM_PT > m.t.L) {  // the tile reaches past the committed positions
           // the value row of a position no row may meet is zeroed: one past the
           // sequence (whatever lies there), or a node's with an infinity or NaN
           const int it = ic + v_item(i, m.nt), slot = it % C::S, pos = p0 + lane;
           ok = tm_wait(su32(&ctl.full[slot]), (uint32_t)(it / C::S) & 1u, abort_w, a.status);
-          if (soft_any(!ok)) {
+          if (wg == 0 && ok) {
+            uint4* vr = reinterpret_cast<uint4*>(sp + C::RING + slot * C::SLOT + wt * 128);
+            bool mine = false;
+            if (pos >= m.t.L && pos < m.t.P) {
+#pragma unroll
+              for (int e = 0; e < C::BLK * 8; ++e) {
+                const uint4 u = vr[(e >> 3) * (TM_PT * 8) + (e & 7)];
+                const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                  mine = mine || (x[h] & 0x7f80u) == 0x7f80u || (x[h] & 0x7f800000u) == 0x7f800000u;
+              }
+            }
+            if (pos >= m.t.P || mine) {
+#pragma unroll 4
+              for (int e = 0; e < C::BLK * 8; ++e) vr[(e >> 3) * (TM_PT * 8) + (e & 7)] = make_uint4(0, 0, 0, 0);
+            }
+            // positions of the warp whose values are infinite or NaN: a row that sees one is NaN
+            const unsigned found = __ballot_sync(0xffffffffu, mine);
+            if (lane == 0) ctl.bad[w4] = found;
+          }
+          if (all_any<128 * C::SW>(!ok)) {
             ok = false;
             break;
           }
-          uint4* vr = reinterpret_cast<uint4*>(sp + C::RING + slot * C::SLOT + tid * 128);
-          bool mine = false;
-          if (pos >= m.t.L && pos < m.t.P) {
-#pragma unroll
-            for (int e = 0; e < C::BLK * 8; ++e) {
-              const uint4 u = vr[(e >> 3) * (TM_PT * 8) + (e & 7)];
-              const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-              for (int h = 0; h < 4; ++h)
-                mine = mine || (x[h] & 0x7f80u) == 0x7f80u || (x[h] & 0x7f800000u) == 0x7f800000u;
-            }
-          }
-          if (pos >= m.t.P || mine) {
-#pragma unroll 4
-            for (int e = 0; e < C::BLK * 8; ++e) vr[(e >> 3) * (TM_PT * 8) + (e & 7)] = make_uint4(0, 0, 0, 0);
-          }
-          // positions of the warp whose values are infinite or NaN: a row that sees one is NaN
-          const unsigned bad = __ballot_sync(0xffffffffu, mine);
+          const unsigned bad = ctl.bad[w4];
           // this lane's positions, counted from the first node (negative: committed)
           const uint32_t* words = reinterpret_cast<const uint32_t*>(ctl.mask[qi % TM_MASKS]) + 2 * n2;
 #pragma unroll
@@ -658,7 +686,7 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
             const float2 v = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, base[b]);
             top = fmaxf(top, fmaxf(v.x, v.y));
           }
-        if (soft_any(top > TM_SLACK)) {
+        if (soft_any(top > TM_SLACK, wg)) {
           // new bases: the rows' largest scores so far
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
@@ -671,19 +699,20 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
             mx = lanes_max(mx);
             my = lanes_max(my);
             if (lane < 4) {
-              ctl.part[warp][8 * b + n2] = mx * c;
-              ctl.part[warp][8 * b + n2 + 1] = my * c;
+              ctl.part[w4][8 * b + n2] = mx * c;
+              ctl.part[w4][8 * b + n2 + 1] = my * c;
             }
           }
-          soft_sync();
-          if (tid < N) {
-            const float old = ctl.base[tid];
-            const float nb = fmaxf(fmaxf(fmaxf(ctl.part[0][tid], ctl.part[1][tid]),
-                                         fmaxf(ctl.part[2][tid], ctl.part[3][tid])), old);
-            ctl.corr[tid] = nb == old ? 1.f : exp2_fast(old - nb);
-            ctl.base[tid] = nb;
+          soft_sync(wg);
+          if (wt < NC) {
+            const int n = c0 + wt;
+            const float old = ctl.base[n];
+            const float nb =
+                fmaxf(fmaxf(fmaxf(ctl.part[0][n], ctl.part[1][n]), fmaxf(ctl.part[2][n], ctl.part[3][n])), old);
+            ctl.corr[n] = nb == old ? 1.f : exp2_fast(old - nb);
+            ctl.base[n] = nb;
           }
-          soft_sync();
+          soft_sync(wg);
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             const int n = 8 * b + n2;
@@ -729,10 +758,10 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
           tc_fence_after();
           const uint32_t src = tmem + C::TM_O + ((t - 1) & 1) * C::TM_S + lanes;
 #pragma unroll
-          for (int n = 0; n < N; n += 16) {
+          for (int n = 0; n < NC; n += 16) {
             uint32_t v[C::G][16];
 #pragma unroll
-            for (int gr = 0; gr < C::G; ++gr) tmem_ld16(src + gr * N + n, v[gr]);
+            for (int gr = 0; gr < C::G; ++gr) tmem_ld16(src + gr * N + c0 + n, v[gr]);
             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
@@ -747,13 +776,13 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
           }
           if (scaled) {
 #pragma unroll
-            for (int n = 0; n < N; ++n) o[n] *= ctl.corr[n];
+            for (int n = 0; n < NC; ++n) o[n] *= ctl.corr[c0 + n];
           }
         }
         scaled = false;
       }
       if (m.nt > 0) {
-        if (soft_any(!ok)) {  // every softmax thread comes here, whichever of them gave up
+        if (all_any<128 * C::SW>(!ok)) {  // every softmax thread comes here, whichever of them gave up
           ok = false;
           break;
         }
@@ -761,28 +790,28 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
         for (int b = 0; b < NB; ++b) {
           const float sx = lanes_sum(l[b].x), sy = lanes_sum(l[b].y);
           if (lane < 4) {
-            ctl.part[warp][8 * b + n2] = sx;
-            ctl.part[warp][8 * b + n2 + 1] = sy;
+            ctl.part[w4][8 * b + n2] = sx;
+            ctl.part[w4][8 * b + n2 + 1] = sy;
           }
         }
-        soft_sync();
-        if (tid < N) {
-          const float sum = (ctl.part[0][tid] + ctl.part[1][tid]) + (ctl.part[2][tid] + ctl.part[3][tid]);
-          ctl.sum[tid] = CL > 1 ? sum : (sum == 0.f ? 0.f : 1.f / sum);  // a row that saw nothing: zeroes
+        soft_sync(wg);
+        if (wt < NC) {
+          const int n = c0 + wt;
+          const float sum = (ctl.part[0][n] + ctl.part[1][n]) + (ctl.part[2][n] + ctl.part[3][n]);
+          ctl.sum[n] = CL > 1 ? sum : (sum == 0.f ? 0.f : 1.f / sum);  // a row that saw nothing: zeroes
         }
-        soft_sync();
         // the rows, through P's place (its readers are done) to whole lines
         float* os = reinterpret_cast<float*>(sp + C::P);  // [N][HD]
-        if (tid < HD) {
+        if (wt < HD) {
 #pragma unroll
-          for (int n = 0; n < N; ++n) os[n * HD + tid] = o[n];
+          for (int n = 0; n < NC; ++n) os[(c0 + n) * HD + wt] = o[n];
         }
-        soft_sync();
+        soft_sync(wg);
         if (CL == 1) {
           constexpr int LPR = HD / 4;  // lanes of a row
 #pragma unroll 1
-          for (int n = tid / LPR; n < m.rows; n += 128 / LPR) {
-            const int row = m.n0 + n, node = div_rep(row), d = tid % LPR * 4;
+          for (int n = c0 + wt / LPR; n < min(m.rows, c0 + NC); n += 128 / LPR) {
+            const int row = m.n0 + n, node = div_rep(row), d = wt % LPR * 4;
             const float4 v = *reinterpret_cast<const float4*>(os + n * HD + d);
             const float f = ctl.sum[n];
             float* dst = a.out + (size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + row - node * rep) * HD + d;
@@ -795,7 +824,7 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
               dst[3] = v.w * f;
             }
           }
-          soft_sync();  // P and the sums may be written again
+          all_any<128 * C::SW>(false);  // P and the sums may be written again
         }
         ic += 2 * m.nt;
         tc += m.nt;
@@ -831,7 +860,7 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
     __syncthreads();
     constexpr int LPR = HD / 4;  // lanes of a row
     if (!*abort_w) {
-      for (int n = rank + CL * (tid / LPR); n < m.rows; n += CL * (TM_THREADS / LPR)) {
+      for (int n = rank + CL * (tid / LPR); n < m.rows; n += CL * (C::THREADS / LPR)) {
         const int d = tid % LPR * 4;
         float4 v[8];
 #pragma unroll
@@ -866,7 +895,7 @@ __global__ void __launch_bounds__(TM_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5)
+  if (warp == C::MMA_WARP)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
 }
 
@@ -923,7 +952,7 @@ int launch_mma(const TreeArgs& a, int layers, int dev, int n_sm, cudaStream_t s)
   const unsigned rep = (unsigned)(a.Hq / a.kv.Hkv), rep_inv = (unsigned)(((1ull << 32) + rep - 1) / rep);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(TM_THREADS);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
