@@ -329,6 +329,7 @@ int q3tts_tree_step(q3tts_handle* h, int stream_id, const int32_t* codes_dev, co
     return Q3TTS_ERR_ARG;
   for (int i = 0; i < n_nodes; ++i)
     if (parents[i] < -1 || parents[i] >= i) return Q3TTS_ERR_ARG;
+  if (!q3::tree_attention_ok(q3::talker_kv(h), h->c.talker_layers, h->Hq)) return Q3TTS_ERR_UNSUPPORTED;
   if (h->len[stream_id] < 1) return Q3TTS_ERR_STATE;
   if (h->len[stream_id] + n_nodes > h->c.kv_cap_steps) return Q3TTS_ERR_CAPACITY;
   return q3::guarded(

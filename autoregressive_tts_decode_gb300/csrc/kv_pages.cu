@@ -43,67 +43,71 @@ __global__ void __launch_bounds__(CP_THREADS) copy_pages_kernel(uint4* pool, lon
 // ------------------------------------------------------------- compaction
 //
 // Row L + path[i] moves to row L + i, for every layer, kv head, k and v.  The
-// path ascends, so path[i] >= i: rows are taken in order, a chunk is loaded
-// whole before any of it is stored, and a row is never written before it has
-// been read.  One warp moves the rows of one (sequence, layer, k|v, head).
-constexpr int CR_WARPS = 4;
-constexpr int CR_UNROLL = 8;  // 16-byte loads in flight per lane
+// path ascends, so path[i] >= i: rows are taken in order, a chunk of them is
+// loaded whole before any of it is stored, and a row is never written before it
+// has been read.  A CTA moves one sequence's rows in one layer: path and pages
+// are looked up once for all heads.
+constexpr int CR_THREADS = 256;
+constexpr int CR_UNROLL = 8;  // 16-byte loads in flight per thread
+constexpr int CR_ROWS = 256;  // rows looked up at a time
 
-__global__ void __launch_bounds__(CR_WARPS * 32) compact_rows_kernel(KVDesc kv, int row_words, const int* lengths,
-                                                                     const int* path, int max_path,
-                                                                     const int* path_len, int units, int* status) {
+__global__ void __launch_bounds__(CR_THREADS) compact_rows_kernel(KVDesc kv, int row_shift, const int* lengths,
+                                                                  const int* path, int max_path, const int* path_len,
+                                                                  int* status) {
   pdl_wait();
   pdl_trigger();
-  const int seq = blockIdx.y, lane = threadIdx.x & 31;
-  const int unit = blockIdx.x * CR_WARPS + (threadIdx.x >> 5);  // (layer, k|v, head)
-  if (unit >= units) return;
+  __shared__ long long from[CR_ROWS], to[CR_ROWS];  // 16-byte words from the layer's start: a row's first key head
+  const int seq = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x;
   const int n = path_len[seq], L = lengths[seq];
   const int* pa = path + (size_t)seq * max_path;
+  const int* table = kv.page_table + (size_t)seq * kv.pages_per_stream;
   const long long cap = (long long)kv.pages_per_stream * kv.page_size;
   bool ok = n >= 0 && n <= max_path && L >= 0;
+  // the row's place, -1 if its page is outside the pool
+  auto place = [&](int pos) -> long long {
+    const int page = table[pos / kv.page_size];
+    if (page < 0 || page >= kv.n_pages) return -1;
+    return ((long long)page * 2 * kv.Hkv * kv.page_size + pos % kv.page_size) << row_shift;
+  };
   if (ok)
-    for (int i = lane; i < n; i += 32) {
+    for (int i = tid; i < n; i += CR_THREADS) {
       const int p = pa[i];
-      ok = ok && p >= 0 && (long long)L + p < cap && (i == 0 || p > pa[i - 1]);
+      ok = ok && p >= 0 && (long long)L + p < cap && (i == 0 || p > pa[i - 1]) && place(L + p) >= 0 && place(L + i) >= 0;
     }
-  if (!__all_sync(0xffffffffu, ok)) {
-    if (lane == 0) op_status(status, Q3TTS_ERR_ARG);
+  if (!__syncthreads_and(ok)) {
+    if (tid == 0 && layer == 0) op_status(status, Q3TTS_ERR_ARG);
     return;
   }
-  const int head = unit % kv.Hkv, sel = unit / kv.Hkv % 2, layer = unit / kv.Hkv / 2;
-  const int* table = kv.page_table + (size_t)seq * kv.pages_per_stream;
-  uint4* pool = reinterpret_cast<uint4*>(kv.pool);
-  auto at = [&](int pos) -> uint4* {
-    const int page = table[pos / kv.page_size];
-    if (page < 0 || page >= kv.n_pages) {
-      op_status(status, Q3TTS_ERR_ARG);
-      return nullptr;
+  uint4* pool = reinterpret_cast<uint4*>(kv.pool) +
+                (((long long)layer * kv.n_pages * 2 * kv.Hkv * kv.page_size) << row_shift);
+  const int units = 2 * kv.Hkv;                                        // (k|v, head)
+  const long long unit_words = (long long)kv.page_size << row_shift;  // from one to the next
+  const int c = tid & ((1 << row_shift) - 1), step = CR_THREADS >> row_shift;
+  for (int i0 = 0; i0 < n; i0 += CR_ROWS) {
+    const int m = min(CR_ROWS, n - i0);
+    __syncthreads();
+    if (tid < m) {
+      const int i = i0 + tid, p = pa[i];
+      from[tid] = place(L + p);
+      to[tid] = p == i ? -1 : place(L + i);  // -1: already there
     }
-    return pool + (((((size_t)layer * kv.n_pages + page) * 2 + sel) * kv.Hkv + head) * kv.page_size +
-                   pos % kv.page_size) * row_words;
-  };
-  const int words = n * row_words;
-  for (int w0 = 0; w0 < words; w0 += 32 * CR_UNROLL) {
-    uint4 v[CR_UNROLL];
-    uint4* dst[CR_UNROLL];
+    __syncthreads();
+    for (int e0 = tid >> row_shift; e0 - (tid >> row_shift) < m * units; e0 += step * CR_UNROLL) {
+      uint4 v[CR_UNROLL];
+      long long dst[CR_UNROLL];
 #pragma unroll
-    for (int i = 0; i < CR_UNROLL; ++i) {
-      const int w = w0 + i * 32 + lane, r = w / row_words, c = w % row_words;
-      dst[i] = nullptr;
-      if (w < words && pa[r] != r) {
-        const uint4* s = at(L + pa[r]);
-        uint4* d = at(L + r);
-        if (s && d) {
-          v[i] = s[c];
-          dst[i] = d + c;
-        }
+      for (int u = 0; u < CR_UNROLL; ++u) {
+        const int e = e0 + u * step, i = e / units;
+        dst[u] = e < m * units ? to[i] : -1;
+        const long long off = (long long)(e - i * units) * unit_words + c;
+        v[u] = pool[dst[u] < 0 ? c : from[i] + off];  // (a row that stays: some word, not stored)
+        dst[u] = dst[u] < 0 ? -1 : dst[u] + off;
       }
-    }
-    __syncwarp();
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < CR_UNROLL; ++i)
-      if (dst[i]) *dst[i] = v[i];
-    __syncwarp();
+      for (int u = 0; u < CR_UNROLL; ++u)
+        if (dst[u] >= 0) pool[dst[u]] = v[u];
+    }
   }
 }
 
@@ -131,11 +135,11 @@ int launch_copy_pages(const KVDesc& kv, int layers, int esz, const int32_t* src,
 int launch_compact_rows(const KVDesc& kv, int layers, int esz, int n_seqs, const int* lengths, const int* path,
                         int max_path, const int* path_len, int* status, cudaStream_t s) {
   if (n_seqs <= 0 || max_path <= 0) return Q3TTS_OK;
-  const long long units = 2ll * layers * kv.Hkv;
-  if (n_seqs > 65535 || units > 0x7fffffff - CR_WARPS) return Q3TTS_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)((units + CR_WARPS - 1) / CR_WARPS), n_seqs);
-  return launch_pdl(compact_rows_kernel, grid, dim3(CR_WARPS * 32), 0, s, kv, kv.hd * esz / 16, lengths, path, max_path,
-                    path_len, (int)units, status) == cudaSuccess
+  if (layers > 65535) return Q3TTS_ERR_UNSUPPORTED;
+  int row_shift = 0;  // 16-byte words of a row: 8, 16 or 32
+  while ((16 << row_shift) < kv.hd * esz) ++row_shift;
+  return launch_pdl(compact_rows_kernel, dim3(n_seqs, layers), dim3(CR_THREADS), 0, s, kv, row_shift, lengths, path,
+                    max_path, path_len, status) == cudaSuccess
              ? Q3TTS_OK
              : Q3TTS_ERR_CUDA;
 }

@@ -40,6 +40,11 @@ struct TreeArgs {
   int ldo;
   int* status;
 };
+// Whether the cache and head counts are ones it takes (the pool's rows of head
+// dim elements are numbered in 32 bits).
+inline bool tree_attention_ok(const KVDesc& kv, int layers, int Hq) {
+  return Hq / kv.Hkv <= 1024 && 2ll * layers * kv.n_pages <= 0x7fffffffll / kv.Hkv / kv.page_size;
+}
 int launch_tree_attention(const TreeArgs& a, int layers, int kdt, cudaStream_t s);
 
 // Page copies and compaction (kv_pages.cu).

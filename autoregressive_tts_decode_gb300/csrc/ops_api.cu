@@ -84,7 +84,8 @@ int q3tts_tree_attention(const q3tts_kv_cache* kv, int layer, const int32_t* pag
   if (!table_ok(*kv, pages_per_seq) || (long long)n_q_heads * kv->head_dim > ldq ||
       (long long)n_q_heads * kv->head_dim > ldo)
     return Q3TTS_ERR_ARG;
-  if (n_q_heads / kv->n_kv_heads > 1024) return Q3TTS_ERR_UNSUPPORTED;
+  if (!q3::tree_attention_ok(desc(*kv, page_table_dev, pages_per_seq), kv->layers, n_q_heads))
+    return Q3TTS_ERR_UNSUPPORTED;
   q3::TreeArgs a;
   a.kv = desc(*kv, page_table_dev, pages_per_seq);
   a.layer = layer;

@@ -1,25 +1,56 @@
-// tree_attention.cu -- attention of drafted tree nodes over a paged cache.
+// tree_attention.cu -- attention of drafted tree nodes over a paged cache, on the
+// 5th-generation tensor cores.
 //
 // A sequence holds L committed positions and T drafted nodes, whose keys and
 // values sit in its pages at positions L .. L + T - 1 in node order.  Node i
 // sees every committed position and the nodes j of its mask (bit j of a 64-bit
 // word: its ancestors and itself), so for head h of kv head g
 //   s_p = q . k_p / sqrt(hd),  o = sum_p e^(s_p - m) v_p / sum_p e^(s_p - m)
-// over the positions p it sees, m their largest score; o = 0 when it sees none.
-// One node whose mask is its own bit is the ordinary decode of a single token,
-// a chain of nodes the causal attention of a short chunk.
+// over the positions p it sees, m about their largest score; o = 0 when it sees
+// none.  One node whose mask is its own bit is the ordinary decode of a single
+// token, a chain of nodes the causal attention of a short chunk.
 //
-// The rows of a sequence that share a kv head are the T nodes times the q
-// heads of the group (row n: node n / rep, head g rep + n % rep), so each cache
-// row is read once for all of them.  A CTA takes one tile of those rows and a
-// share of the positions; the CTAs of one thread-block cluster split the
-// positions of the same rows and join their (max, sum, output) through
-// distributed shared memory: no workspace, no counters, one launch, and the
-// same result on every run.
+// The few query rows that share a kv head (nodes x q heads of the group) are
+// the MMA's N side, 128 cached positions its M side, so that one row costs no
+// more lanes than sixteen:
+//   S^T = K Q^T   M 128 positions, K the head dimension; K arrives by TMA, page
+//                 by page, as it lies in the cache;
+//   P^T = 2^(c S^T - base)  c = log2(e) / sqrt(hd), in registers, a running
+//                 base per row;
+//   O^T = V^T P^T M the head dimension, K 128 positions; V is read as it lies in
+//                 the cache (an M-major operand).
+// The base of a row follows its largest score only when a score passes it by
+// more than 2^8: until then weights up to 256 are exact multiples that the
+// final division removes, and a tile needs one vote of the softmax threads
+// instead of a maximum over them.
+//
+// Precision.  Keys and values are bf16 as cached; Q and P enter as three bf16
+// terms each, which hold all 24 bits of an fp32 value (two terms of P alone
+// leave 2e-6 of the output).  The terms are stacked along N, so that a tile of
+// K or V is read from shared memory once for all of them; each has its own
+// accumulator columns (of 64 rows, the two small ones share) and they are added
+// in fp32 registers, like the outputs of successive tiles: the tensor cores
+// truncate as they accumulate, and summed in tensor memory over 32768 positions
+// the error was 3.7e-5 of the output.
+//
+// Roles of a CTA (one per SM): one warp issues the TMA loads into a ring of K
+// and V tiles, one thread the MMAs (scores of tile t + 1 before the outputs of
+// tile t), four warps are the softmax and two bring in the queries.  A CTA works
+// through several items (sequence, kv head, tile of rows) and the roles run
+// ahead into the next one, so only the first pays the latency of its start.
+// Items are dealt longest first, in rounds of alternating direction: on 128
+// sequences of 256..2048 positions the SMs then end together.
+// The bound is the cache's bytes, read once for up to 64 rows.
+// Every wait is bounded; on expiry the CTA records Q3TTS_ERR_TIMEOUT, waits
+// (bounded) for its copies and MMAs in flight, frees its tensor memory and
+// writes nothing more.
 #include <cooperative_groups.h>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
 
 #include "ops.cuh"
-#include "tree.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -27,256 +58,1116 @@ namespace q3 {
 
 namespace {
 
-// Element offset of (position, k|v, kv head) of a sequence; a page id outside
-// the pool is reported and page 0 read in its place.
-__device__ __forceinline__ size_t tree_offset(const TreeArgs& a, const int* table, int pos, int kvsel, int g) {
-  const KVDesc& kv = a.kv;
-  int page = table[pos / kv.page_size];
-  if (page < 0 || page >= kv.n_pages) {
+// What a CTA works on; false when it has no rows.  Lengths and row offsets
+// come from device memory, so they are checked here: a sequence whose entries
+// do not fit the cache or the buffers is left out and reported.
+struct TreeSeq {
+  int L, T, row0, P;  // committed positions, nodes, first row of q/out, L + T
+};
+__device__ __forceinline__ bool tree_seq(const TreeArgs& a, int seq, TreeSeq& t) {
+  t.L = a.lengths[seq];
+  t.row0 = a.node_start[seq];
+  const int end = a.node_start[seq + 1];
+  const long long cap = (long long)a.kv.pages_per_stream * a.kv.page_size;
+  if (t.row0 < 0 || end < t.row0 || end > a.n_rows || end - t.row0 > a.max_nodes || t.L < 0 ||
+      (long long)t.L + (end - t.row0) > cap) {
     op_status(a.status, Q3TTS_ERR_ARG);
-    page = 0;
+    return false;
   }
-  return ((((size_t)a.layer * kv.n_pages + page) * 2 + kvsel) * kv.Hkv + g) * kv.page_size * kv.hd +
-         (size_t)(pos % kv.page_size) * kv.hd;
+  t.T = end - t.row0;
+  t.P = t.L + t.T;
+  return t.T > 0;
 }
 
-__device__ __forceinline__ bool node_sees(unsigned long long mask, int pos, int L) {
-  return pos < L || ((mask >> (pos - L)) & 1ull) != 0;
-}
+constexpr int TM_PT = 128;       // positions of a tile
+constexpr int TM_QTHREADS = 32;
+constexpr int TM_SORT = 256;     // sequences that are dealt by length, at most (no more than threads)
+constexpr int TM_MASKS = 4;      // items whose masks are held: the softmax's, and the scores may be three ahead
+constexpr long long TM_WAIT_CYCLES = 4000000000ll;  // ~2 s
+constexpr float TM_FLOOR = -1e30f;  // base of a row that has seen nothing: below every score
+constexpr float TM_SLACK = 8.f;     // how far (log2) a score may pass its row's base
 
-// ------------------------------------------------------- fp32 arithmetic
-//
-// Any cache type, page size and head dimension 64 or 128.  Tiles of 32
-// positions are copied into shared memory (cp.async, two stages), scores and
-// outputs are fp32 FMAs in registers, the running maximum and sum stay in fp32.
-constexpr int TF_THREADS = 128, TF_PT = 32;
+// How a tile of K or V gets from the cache into shared memory.
+enum TmLoad {
+  kTma,    // bf16, pages of 8, 16, 32, 64 or a multiple of 128 positions: a TMA box per page
+  kCopy,   // bf16, any page size: 16-byte asynchronous copies, row by row
+  kSplit,  // fp32, any page size: loaded, split into three bf16 terms, stored as three tiles
+};
 
-template <class KT, int HD, int RT>
-struct TfCfg {
-  static constexpr int KLD = HD + 16 / (int)sizeof(KT);  // padded row: consecutive rows start in other banks
-  static constexpr int TILE = TF_PT * KLD;               // elements of a K or V tile
-  static constexpr size_t SMEM =
-      sizeof(KT) * 4 * (size_t)TILE + sizeof(float) * ((size_t)RT * HD * 2 + (size_t)RT * TF_PT + 3 * RT) + 8 * RT;
+template <int HD, int N, int MODE>
+struct TmCfg {
+  // softmax groups of four warps, each with its share of the rows; then a warp
+  // for the MMAs, one for the queries, and 2 LW for the keys and values
+  static constexpr int SW = N <= 32 ? 1 : 2, NC = N / SW;
+  static constexpr int LW = MODE == kTma || N > 32 ? 1 : 2;
+  static constexpr int MMA_WARP = 4 * SW, QUERY_WARP = MMA_WARP + 1, LOAD_WARP = MMA_WARP + 2;
+  static constexpr int THREADS = 128 * SW + 64 + 64 * LW;
+  static constexpr int TERMS = MODE == kSplit ? 3 : 1;   // ring tiles of a K or V tile
+  static constexpr uint32_t FULL = MODE == kTma ? 1 : 64 * LW;  // arrivals that fill a ring tile
+  static constexpr int BLK = HD / 64;               // 128-byte swizzle blocks of a row
+  static constexpr uint32_t SLOT = TM_PT * HD * 2;  // a K or V tile
+  static constexpr uint32_t TERM = N * 128;         // one term of one 64-element block (of Q or P)
+  static constexpr uint32_t QBYTES = BLK * 3 * TERM, PBYTES = 2 * 3 * TERM;
+  static constexpr int G = N <= 32 ? 3 : 2;         // accumulator groups: the terms, or the large one and the others
+  static constexpr int NP = N <= 32 ? 2 : 1;        // P buffers
+  static constexpr uint32_t Q = 0, P = QBYTES, RING = P + NP * PBYTES;
+  static constexpr uint32_t CTL_BYTES = 6144;
+  static constexpr int FIT = (int)((227u * 1024 - 1024 - CTL_BYTES - RING) / SLOT);
+  static constexpr int S = FIT < 8 ? FIT : 8;       // tiles in the ring
+  static constexpr uint32_t CTL = RING + S * SLOT;
+  static constexpr size_t SMEM = 1024 + CTL + CTL_BYTES;
+  static constexpr uint32_t TM_S = G * N, TM_O = 2 * TM_S;  // columns: S twice, O twice
+  static constexpr uint32_t TMEM_COLS = 4 * G * N <= 256 ? 256 : 512;
+  // three places: a TMA warp skips two ring tiles at most, which its parity waits
+  // bear; the softmax of tile t waits for V_t, which takes the place of K_t (or,
+  // split, of K_(t + 1)'s terms) at the latest; a split tile is stored whole
+  static_assert(S >= 3 && (MODE != kSplit || G == 3) && 4 * G * N <= 512 && N * HD * 4 <= (int)(NP * PBYTES), "ring, tensor memory, output rows");
+};
+
+// Control block (shared memory).
+template <int N, int S>
+struct TmCtl {
+  unsigned long long full[S], empty[S], s_full[2], s_free[2], p_full[2], p_free[2], q_full[TM_MASKS], q_free, done, v_full[2];
+  uint32_t tmem;
+  int abort_w;
+  float base[N], corr[N], sum[N];  // a row's base, the factor of its last rise, its sum of weights
+  float part[4][N];
+  unsigned bad[4];
+  unsigned long long mask[TM_MASKS][N];
+  int len[TM_SORT];
+  uint16_t order[TM_SORT];  // sequences, longest first
+  int copies[2][8];  // TMA: the last ring tiles that each loading warp has filled
 };
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+__device__ __forceinline__ void mbar_init(uint32_t b, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(b), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 128-byte swizzled operand tiles: rows of 128 bytes, 8-row atoms 1024 bytes
+// apart (stride byte offset), descriptor version 1, swizzle mode 2.  K-major:
+// the leading offset is not used.  M-major (V^T: 64 head-dim elements are a
+// row's 128 bytes, positions the rows): the leading offset is the distance of
+// the second 64 elements' block.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lead = 16) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lead & 0x3FFFFu) >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16: D fp32, A and B bf16, B K-major; A K-major or M-major (bit 15).
+__host__ __device__ constexpr uint32_t f16_idesc(int M, int N, bool a_m_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_m_major ? 1u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(
+          tmem_d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// 16 fp32 columns of the warp's 32 lanes, one lane per thread (complete after wait::ld).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// N fp32 columns of 16 lanes, eight columns at a time in the fragment order of
+// an 8 x 8 matrix store: registers 4 b and 4 b + 1 hold columns 8 b + 2 (lane % 4)
+// and the next of lane / 4, registers 4 b + 2 and 4 b + 3 the same of
+// lane / 4 + 8.
+template <int N>
+__device__ __forceinline__ void tmem_frag(uint32_t taddr, uint32_t (&r)[N / 2]);
+template <>
+__device__ __forceinline__ void tmem_frag<16>(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+template <>
+__device__ __forceinline__ void tmem_frag<32>(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr));
+}
+// Four 8 x 8 matrices of 16-bit elements, transposed on the way: matrix m goes
+// to the rows at lanes 8 m .. 8 m + 7's addresses.
+__device__ __forceinline__ void store_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+// Pairs of floats (one 64-bit register pair, one instruction each).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
+      " mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// Two floats to bf16 (x in the low half).
+__device__ __forceinline__ uint32_t pack_bf16(float2 v) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Barrier and vote of the 128 threads of softmax group wg.
+__device__ __forceinline__ void soft_sync(int wg) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + 2 * wg) : "memory");
+}
+__device__ __forceinline__ bool soft_any(bool p, int wg) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "r"(2 + 2 * wg)
+      : "memory");
+  return r != 0;
+}
+// Barrier and vote of all softmax threads; giving up is decided here alone, so
+// that both groups leave together.
+template <int COUNT>
+__device__ __forceinline__ bool all_any(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 5, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "n"(COUNT)
+      : "memory");
+  return r != 0;
 }
 
-__device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+// Bounded wait on an mbarrier phase; false on expiry or when another role of
+// the CTA has given up.
+__device__ __noinline__ bool tm_wait_long(uint32_t bar, uint32_t parity, volatile int* abort_w, int* status) {
+  const long long t0 = clock64();
+  unsigned it = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    if ((++it & 63u) == 0) {
+      if (*abort_w) return false;
+      if (clock64() - t0 > TM_WAIT_CYCLES) {
+        *abort_w = 1;
+        op_status(status, Q3TTS_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
 }
-__device__ __forceinline__ void load4(const bf16* p, float (&f)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
-  f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
+__device__ __forceinline__ bool tm_wait(uint32_t bar, uint32_t parity, volatile int* abort_w, int* status) {
+  return mbar_try_wait(bar, parity) || tm_wait_long(bar, parity, abort_w, status);
 }
 
-template <class KT, int HD, int RT>
-__global__ void __launch_bounds__(TF_THREADS) tree_fma_kernel(TreeArgs a, int row_tiles) {
-  using C = TfCfg<KT, HD, RT>;
-  constexpr int CG = HD / 4, RG = TF_THREADS / CG;  // output: column groups of 4, row groups
-  constexpr int OR = (RT + RG - 1) / RG;            // output rows of a thread
-  constexpr int SR = (RT + 7) / 8;                  // score rows of a thread (8 row groups x 16 position pairs)
-  pdl_wait();  // q and the appended keys and values come from the previous kernels
-  extern __shared__ __align__(16) uint8_t tf_raw[];
-  KT* kt = reinterpret_cast<KT*>(tf_raw);  // [2 stages][K | V][TILE]
-  float* qs = reinterpret_cast<float*>(kt + 4 * C::TILE);  // [RT][HD]
-  float* os = qs + RT * HD;                                // [RT][HD] this CTA's output
-  float* ps = os + RT * HD;                                // [RT][TF_PT]
-  float* mrow = ps + RT * TF_PT;                           // running max, sum, rescale factor
-  float* lrow = mrow + RT;
-  float* crow = lrow + RT;
-  unsigned long long* mk = reinterpret_cast<unsigned long long*>(crow + RT);
+// Max or sum over the lanes that hold the same columns (lane % 4).
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Ring position of tile t's K and V among n tiles: K0 K1 V0 K2 V1 .. V(n-1).
+__device__ __forceinline__ int k_item(int t) { return t == 0 ? 0 : 2 * t - 1; }
+__device__ __forceinline__ int v_item(int t, int n) { return t == n - 1 ? 2 * n - 1 : 2 * t + 2; }
+
+// One item of work.
+struct TmItem {
+  TreeSeq t;
+  int seq, g, n0, rows;  // kv head, first row of the tile, rows
+  int t0, nt;            // first position tile, tiles
+};
+
+// How the items are dealt.
+struct TmDeal {
+  int items, row_tiles, rows;  // rows of a tile
+  int stride, first;           // clusters, this one
+  int rank, cl;                // CTA of the cluster, CTAs
+  const uint16_t* order;       // sequences, longest first, or NULL
+};
+
+// The k-th item of a CTA: 1 if there is one, 0 if it has no rows (or does not
+// fit, which is reported), -1 past the last.
+__device__ __forceinline__ int tm_item(const TreeArgs& a, const TmDeal& d, int k, TmItem& m) {
+  if ((long long)k * d.stride >= d.items) return -1;
+  const int idx = k * d.stride + ((k & 1) ? d.stride - 1 - d.first : d.first);
+  if (idx >= d.items) return 0;
+  const int rep = a.Hq / a.kv.Hkv;
+  m.g = idx / d.row_tiles % a.kv.Hkv;
+  m.seq = idx / d.row_tiles / a.kv.Hkv;
+  if (d.order) m.seq = d.order[m.seq];
+  m.n0 = idx % d.row_tiles * d.rows;
+  if (!tree_seq(a, m.seq, m.t) || m.n0 >= m.t.T * rep) return 0;
+  m.rows = min(d.rows, m.t.T * rep - m.n0);
+  const int all = (m.t.P + TM_PT - 1) / TM_PT, per = (all + d.cl - 1) / d.cl;
+  m.t0 = min(all, d.rank * per);
+  m.nt = min(all, m.t0 + per) - m.t0;
+  return 1;
+}
+
+template <int HD, int N, int MODE>
+__global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
+    tree_mma_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ TreeArgs a, int row_tiles, int box, int items, int vec,
+                    unsigned rep_inv) {
+  using C = TmCfg<HD, N, MODE>;
+  using Ctl = TmCtl<N, C::S>;
+  static_assert(sizeof(Ctl) <= C::CTL_BYTES, "control block");
+  extern __shared__ uint8_t tm_raw[];
+  const uint32_t raw = su32(tm_raw), sbase = (raw + 1023u) & ~1023u;
+  uint8_t* sp = tm_raw + (sbase - raw);
+  Ctl& ctl = *reinterpret_cast<Ctl*>(sp + C::CTL);
+  volatile int* abort_w = &ctl.abort_w;
 
   cg::cluster_group cl = cg::this_cluster();
-  const int C_ = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int CL = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int item = blockIdx.x / C_;
-  const int rt = item % row_tiles, g = item / row_tiles % a.kv.Hkv, seq = item / row_tiles / a.kv.Hkv;
-  const int rep = a.Hq / a.kv.Hkv, n0 = rt * RT;
-  TreeSeq t;
-  // every CTA of the cluster sees the same entries, so all of them leave here
-  if (!tree_seq(a, seq, t) || n0 >= t.T * rep) return;
-  const int rows = min(RT, t.T * rep - n0);
-  const float scale = 1.0f / sqrtf((float)HD);
-  for (int e = tid; e < RT * HD; e += TF_THREADS) {
-    const int r = e / HD, i = e % HD, n = n0 + r;
-    qs[e] = r < rows ? a.q[(size_t)(t.row0 + n / rep) * a.ldq + (size_t)(g * rep + n % rep) * HD + i] * scale : 0.f;
-  }
-  for (int r = tid; r < RT; r += TF_THREADS) {
-    mrow[r] = -INFINITY;
-    lrow[r] = 0.f;
-    mk[r] = r < rows ? a.masks[t.row0 + (n0 + r) / rep] : 0ull;
-  }
-  const int* table = a.kv.page_table + (size_t)seq * a.kv.pages_per_stream;
-  const int ntiles = (t.P + TF_PT - 1) / TF_PT, per = (ntiles + C_ - 1) / C_;
-  const int t0 = min(ntiles, rank * per), t1 = min(ntiles, t0 + per);
+  const int rep = a.Hq / a.kv.Hkv;
 
-  constexpr int CH = HD * (int)sizeof(KT) / 16;  // 16-byte pieces of a row
-  auto stage = [&](int tile) {
-    if (tile < t1) {
-      KT* dst = kt + (size_t)(tile & 1) * 2 * C::TILE;
-      for (int e = tid; e < 2 * TF_PT * CH; e += TF_THREADS) {
-        const int c = e % CH, r = e / CH % TF_PT, sel = e / CH / TF_PT;
-        const int pos = tile * TF_PT + r;
-        const bool in = pos < t.P;  // rows past the last node are zeroes (unwritten words may hold NaN)
-        const KT* src = (const KT*)a.kv.pool + (in ? tree_offset(a, table, pos, sel, g) : 0) + c * (16 / sizeof(KT));
-        cp_async16(su32(dst + (size_t)sel * C::TILE + r * C::KLD) + c * 16, src, in ? 16 : 0);
-      }
+  if (tid == 0) {
+    for (int i = 0; i < C::S; ++i) {
+      mbar_init(su32(&ctl.full[i]), C::FULL);
+      mbar_init(su32(&ctl.empty[i]), 1);
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-
-  float o[OR][4];
-#pragma unroll
-  for (int i = 0; i < OR; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-  const int oc = (tid % CG) * 4, og = tid / CG;       // output columns, row group
-  const int sp = (tid & 15) * 2, sg = tid >> 4;       // score positions, row group
-  stage(t0);
-  for (int tile = t0; tile < t1; ++tile) {
-    stage(tile + 1);
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(su32(&ctl.s_full[i]), 1);
+      mbar_init(su32(&ctl.s_free[i]), 128 * C::SW);
+      mbar_init(su32(&ctl.p_full[i]), 128 * C::SW);
+      mbar_init(su32(&ctl.p_free[i]), 1);
+    }
+    for (int i = 0; i < TM_MASKS; ++i) mbar_init(su32(&ctl.q_full[i]), TM_QTHREADS);
+    mbar_init(su32(&ctl.q_free), 1);
+    mbar_init(su32(&ctl.done), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(su32(&ctl.v_full[i]), 64 * C::LW);
+    ctl.abort_w = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == C::MMA_WARP) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&ctl.tmem)),
+                 "r"(C::TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();  // q and the appended keys and values come from the previous kernels
+  const bool sorted = items > (int)gridDim.x / CL && a.n_seqs <= TM_SORT;
+  if (sorted) {
+    const int mine = tid < a.n_seqs ? a.lengths[tid] : 0;
+    if (tid < TM_SORT) ctl.len[tid] = mine;
     __syncthreads();
-    const KT* kb = kt + (size_t)(tile & 1) * 2 * C::TILE;
-    const KT* vb = kb + C::TILE;
-    float sc[SR][2];
-#pragma unroll
-    for (int i = 0; i < SR; ++i) sc[i][0] = sc[i][1] = 0.f;
-#pragma unroll 4
-    for (int c = 0; c < HD; c += 4) {
-      float k0[4], k1[4];
-      load4(kb + sp * C::KLD + c, k0);
-      load4(kb + (sp + 1) * C::KLD + c, k1);
-#pragma unroll
-      for (int i = 0; i < SR; ++i) {
-        const float4 qv = *reinterpret_cast<const float4*>(qs + min(sg + 8 * i, RT - 1) * HD + c);
-        sc[i][0] = fmaf(qv.x, k0[0], fmaf(qv.y, k0[1], fmaf(qv.z, k0[2], fmaf(qv.w, k0[3], sc[i][0]))));
-        sc[i][1] = fmaf(qv.x, k1[0], fmaf(qv.y, k1[1], fmaf(qv.z, k1[2], fmaf(qv.w, k1[3], sc[i][1]))));
-      }
+    int r = 0;
+#pragma unroll 8
+    for (int j = 0; j < a.n_seqs; ++j) {
+      const int o = ctl.len[j];
+      r += o > mine || (o == mine && j < tid);
     }
+    if (tid < a.n_seqs) ctl.order[r] = (uint16_t)tid;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  const uint32_t ring = sbase + C::RING;
+
+  const TmDeal deal{items, row_tiles, N, (int)gridDim.x / CL, (int)blockIdx.x / CL, rank, CL,
+                    sorted ? ctl.order : nullptr};
+  // row / rep for rows of an item (rep_inv = ceil(2^32 / rep); exact for rows and rep up to 2^16)
+  auto div_rep = [&](int row) -> int { return rep == 1 ? row : (int)__umulhi((unsigned)row, rep_inv); };
+  TmItem m;
+  int have = 0;
+  bool ok = true;
+
+  if (warp >= C::LOAD_WARP) {
+    // ---- loads
+    const bool values = MODE == kTma && warp > C::LOAD_WARP;  // TMA: a warp for the keys and one for the values
+    const int ps = a.kv.page_size;
+    const long long plane = (long long)a.kv.Hkv * ps;  // rows of a page's keys (or values)
+    int ic = 0, issued = 0;                            // position tiles so far, TMA copies of this warp
+    for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
+      if (have == 0 || m.nt == 0) continue;
+      const int* table = a.kv.page_table + (size_t)m.seq * a.kv.pages_per_stream;
+      // row of the pool ([layer][page][k|v][kv head][position]) of a position on `page`
+      auto pool_row = [&](int page, int pos) -> int {
+        if (page < 0 || page >= a.kv.n_pages) {
+          op_status(a.status, Q3TTS_ERR_ARG);
+          page = 0;
+        }
+        return (int)((((long long)a.layer * a.kv.n_pages + page) * 2 + (values ? 1 : 0)) * plane +
+                     (long long)m.g * ps + pos % ps);
+      };
+      if constexpr (MODE == kTma) {
+        // lane (b, blk) copies block blk of page b's rows of a tile.  A warp's
+        // lanes issue one by one, 55 cycles each: from one warp for keys and
+        // values the 32 copies of 2 KB of a tile of 16-position pages took longer
+        // than the tile's bytes.
+        const int b = lane / C::BLK, blk = lane % C::BLK;
+        const int boxes = TM_PT / box;
+        // the page of this lane's box in tile i; looked up two tiles ahead and not
+        // touched until then, so the lookup's latency is never waited for
+        auto page_of = [&](int i) -> int {
+          const int pos = (m.t0 + i) * TM_PT + b * box;
+          return b < boxes && i < m.nt && pos < m.t.P ? __ldg(table + pos / ps) : 0;
+        };
+        int page_even = page_of(0), page_odd = page_of(1);
+        for (int tile = 0; tile < m.nt; ++tile) {
+          const int it = 2 * ic + (values ? v_item(tile, m.nt) : k_item(tile)), slot = it % C::S;
+          const int pos = (m.t0 + tile) * TM_PT + b * box;
+          const int page = (tile & 1) ? page_odd : page_even;
+          const uint32_t fb = su32(&ctl.full[slot]);
+          ok = __all_sync(0xffffffffu,
+                          tm_wait(su32(&ctl.empty[slot]), ((uint32_t)(it / C::S) & 1u) ^ 1u, abort_w, a.status));
+          if (!ok) break;
+          const int held = min(TM_PT, m.t.P - (m.t0 + tile) * TM_PT);
+          if (lane == 0) mbar_expect_tx(fb, (uint32_t)((held + box - 1) / box * box * HD * 2));
+          __syncwarp();
+          if (b < boxes && pos < m.t.P)
+            tma_load(ring + slot * C::SLOT + blk * (TM_PT * 128) + b * box * 128, &map, blk * 64, pool_row(page, pos), fb);
+          // the page two tiles on takes this one's place
+          if (tile & 1) page_odd = page_of(tile + 2); else page_even = page_of(tile + 2);
+          if (lane == 0) ctl.copies[warp - C::LOAD_WARP][issued % 8] = it;
+          ++issued;
+        }
+      } else {
+        // all loading warps share every tile, in the ring's order (so that a place
+        // is waited for at every phase of its barrier); warp lw has rows lw RW ..
+        // of it, lane l the pool rows of the l-th of them (and the 32nd after it)
+        constexpr int LWN = 2 * C::LW, RW = TM_PT / LWN, H = RW / 32;
+        const int lw = warp - C::LOAD_WARP;
+        const uint8_t* pool = static_cast<const uint8_t*>(a.kv.pool);
+        int pages[H], pages2[H], row_even[H], row_odd[H];  // pages of the next two tiles, key rows of the last two
+        auto look_up = [&](int i, int (&pg)[H]) {
 #pragma unroll
-    for (int i = 0; i < SR; ++i) {
-      const int r = sg + 8 * i;
-      if (r < RT) {
+          for (int h = 0; h < H; ++h) {
+            const int pos = (m.t0 + i) * TM_PT + lw * RW + lane + 32 * h;
+            pg[h] = i < m.nt && pos < m.t.P ? __ldg(table + pos / ps) : 0;
+          }
+        };
+        auto find_rows = [&](int i, int (&rows)[H]) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int pos = tile * TF_PT + sp + e;
-          ps[r * TF_PT + sp + e] = (r < rows && pos < t.P && node_sees(mk[r], pos, t.L)) ? sc[i][e] : -INFINITY;
+          for (int h = 0; h < H; ++h) {
+            const int pos = (m.t0 + i) * TM_PT + lw * RW + lane + 32 * h;
+            rows[h] = i < m.nt && pos < m.t.P ? pool_row(pages[h], pos) : -1;
+            pages[h] = pages2[h];
+            // the next tile on its way to the L2: the loads that follow keep too few
+            // bytes in flight for the memory's latency
+            if (MODE == kSplit && i + 1 < m.nt && pos + TM_PT < m.t.P) {
+              const uint8_t* p = pool + (size_t)pool_row(pages[h], pos + TM_PT) * (HD * 4);
+#pragma unroll
+              for (int line = 0; line < HD * 4; line += 128) {
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p + line));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p + plane * (HD * 4) + line));
+              }
+            }
+          }
+          look_up(i + 2, pages2);
+        };
+        // what the i-th ring tile of the item holds
+        auto is_value = [&](int i) -> bool { return i == 2 * m.nt - 1 || (i >= 2 && (i & 1) == 0); };
+        auto tile_of = [&](int i) -> int {
+          return is_value(i) ? (i == 2 * m.nt - 1 ? m.nt - 1 : i / 2 - 1) : (i + 1) / 2;
+        };
+        look_up(0, pages);
+        look_up(1, pages2);
+        if constexpr (MODE == kCopy) {
+          constexpr int CH = HD / 8;  // 16-byte pieces of a row
+          const int c = lane % CH;
+          int pending = -1;           // the ring tile whose copies are on their way
+          for (int i = 0; i < 2 * m.nt; ++i) {
+            const int it = 2 * ic + i, tile = tile_of(i);
+            const bool v = is_value(i);
+            if (!v) {
+              if (tile & 1) find_rows(tile, row_odd); else find_rows(tile, row_even);
+            }
+            ok = __all_sync(0xffffffffu, tm_wait(su32(&ctl.empty[it % C::S]), ((uint32_t)(it / C::S) & 1u) ^ 1u, abort_w,
+                                                 a.status));
+            if (!ok) break;
+            const uint8_t* src = pool + c * 16 + (v ? plane * (HD * 2) : 0);
+            const uint32_t dst = ring + it % C::S * C::SLOT + (c >> 3) * (TM_PT * 128);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              const int mine = (tile & 1) ? row_odd[h] : row_even[h];
+#pragma unroll 8
+              for (int q = lane / CH; q < 32; q += 32 / CH) {
+                const int r = lw * RW + 32 * h + q, row = __shfl_sync(0xffffffffu, mine, q);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                             "l"(src + (size_t)max(row, 0) * (HD * 2)), "r"(row >= 0 ? 16 : 0)
+                             : "memory");
+              }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (pending >= 0) {  // the tile before has arrived
+              asm volatile("cp.async.wait_group 1;" ::: "memory");
+              proxy_fence();
+              mbar_arrive(su32(&ctl.full[pending % C::S]));
+            }
+            pending = it;
+          }
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+          if (pending >= 0) {
+            proxy_fence();
+            mbar_arrive(su32(&ctl.full[pending % C::S]));
+          }
+        } else {
+          // four elements of a row per lane, sixteen loads on their way while the
+          // sixteen before them are split and stored
+          constexpr int CH = HD / 4, U = 16, RPI = 32 / CH == 0 ? 1 : 32 / CH, BATCHES = RW / (U * RPI);
+          static_assert(BATCHES >= 1 && CH <= 32, "a warp's rows in whole batches");
+          const int c = lane % CH;
+          auto load = [&](int i, int batch, float4 (&x)[U]) {
+            i = min(i, 2 * m.nt - 1);  // (past the item: its last tile again, not used)
+            const int tile = tile_of(i);
+            const bool v = is_value(i);
+            if (!v && batch == 0) {
+              if (tile & 1) find_rows(tile, row_odd); else find_rows(tile, row_even);
+            }
+            const int mine = (tile & 1) ? row_odd[0] : row_even[0];
+            const uint8_t* src = pool + c * 16 + (v ? plane * (HD * 4) : 0);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              // a row past the sequence is read from the pool's first and zeroed when stored: a
+              // load under a branch would be waited for at the branch's end
+              const int row = __shfl_sync(0xffffffffu, mine, (batch * U + u) * RPI + lane / CH);
+              x[u] = __ldg(reinterpret_cast<const float4*>(src + (size_t)max(row, 0) * (HD * 4)));
+            }
+          };
+          float4 x[U], y[U];
+          load(0, 0, x);
+          for (int i = 0; i < 2 * m.nt; ++i) {
+            const int it = (2 * ic + i) * 3;
+            // the last of the three places is free last
+            const uint32_t eb = su32(&ctl.empty[(it + 2) % C::S]), ep = ((uint32_t)((it + 2) / C::S) & 1u) ^ 1u;
+            for (int term = 0; term < 2; ++term)
+              ok = tm_wait(su32(&ctl.empty[(it + term) % C::S]), ((uint32_t)((it + term) / C::S) & 1u) ^ 1u, abort_w,
+                           a.status) && ok;
+            ok = __all_sync(0xffffffffu, tm_wait(eb, ep, abort_w, a.status) && ok);
+            if (!ok) break;
+#pragma unroll
+            for (int batch = 0; batch < BATCHES; ++batch) {
+              if (batch + 1 < BATCHES) load(i, batch + 1, y); else load(i + 1, 0, y);
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                const int r = lw * RW + (batch * U + u) * RPI + lane / CH;
+                const uint32_t off = (c >> 4) * (TM_PT * 128) + r * 128 + ((((c >> 1) & 7) ^ (r & 7)) << 4) + (c & 1) * 8;
+                float2 v = make_float2(x[u].x, x[u].y), z = make_float2(x[u].z, x[u].w);
+                if ((m.t0 + tile_of(i)) * TM_PT + r >= m.t.P) v = z = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int term = 0; term < 3; ++term) {
+                  const uint32_t p = pack_bf16(v), q = pack_bf16(z);
+                  *reinterpret_cast<uint2*>(sp + C::RING + (it + term) % C::S * C::SLOT + off) = make_uint2(p, q);
+                  v = add2(v, make_float2(-__uint_as_float(p << 16), -__uint_as_float(p & 0xffff0000u)));
+                  z = add2(z, make_float2(-__uint_as_float(q << 16), -__uint_as_float(q & 0xffff0000u)));
+                }
+              }
+#pragma unroll
+              for (int u = 0; u < U; ++u) x[u] = y[u];
+            }
+            proxy_fence();
+#pragma unroll
+            for (int term = 0; term < 3; ++term) mbar_arrive(su32(&ctl.full[(it + term) % C::S]));
+            if (is_value(i)) mbar_arrive(su32(&ctl.v_full[(ic + tile_of(i)) & 1]));
+          }
+        }
+      }
+      ic += m.nt;
+    }
+    if (MODE == kTma && !ok) {  // copies in flight land before the CTA leaves (otherwise the MMAs have waited for them)
+      for (int j = issued > C::S ? issued - C::S : 0; j < issued; ++j) {
+        const int it = ctl.copies[warp - C::LOAD_WARP][j % 8];
+        const long long c0 = clock64();
+        while (!mbar_try_wait(su32(&ctl.full[it % C::S]), (uint32_t)(it / C::S) & 1u) &&
+               clock64() - c0 < TM_WAIT_CYCLES / 8) {
         }
       }
     }
-    __syncthreads();
-    // softmax of the tile: one warp per row, one position per lane
-    for (int r = warp; r < rows; r += TF_THREADS / 32) {
-      const float s = ps[r * TF_PT + lane];
-      const float mo = mrow[r], mn = fmaxf(mo, warp_max(s));
-      const float p = s == -INFINITY ? 0.f : expf(s - mn);
-      const float sum = warp_sum(p);
-      ps[r * TF_PT + lane] = p;
-      if (lane == 0) {
-        const float corr = mo == -INFINITY ? 0.f : expf(mo - mn);
-        crow[r] = corr;
-        lrow[r] = lrow[r] * corr + sum;
-        mrow[r] = mn;
+  } else if (warp == C::MMA_WARP) {
+    // ---- MMA issue
+    if (lane == 0) {
+      constexpr uint32_t idS = f16_idesc(TM_PT, (C::G == 3 ? 3 : 2) * N, false), idS1 = f16_idesc(TM_PT, N, false);
+      constexpr uint32_t idO = f16_idesc(TM_PT, (C::G == 3 ? 3 : 2) * N, true), idO1 = f16_idesc(TM_PT, N, true);
+      // a head dimension of 64 fills half of M: the other half's rows are read
+      // from the next atom and their results are not used
+      constexpr uint32_t v_lead = HD == 128 ? TM_PT * 128 : 1024;
+      int ic = 0, tc = 0, qi = 0;  // ring tiles, position tiles and items so far
+      for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
+        if (have == 0 || m.nt == 0) continue;
+        ok = tm_wait(su32(&ctl.q_full[qi % TM_MASKS]), (uint32_t)(qi / TM_MASKS) & 1u, abort_w, a.status);
+        tc_fence_after();
+        for (int i = 0; i <= m.nt && ok; ++i) {
+          if (i < m.nt) {  // scores of tile i
+            const int it = (ic + k_item(i)) * C::TERMS, t = tc + i;
+            ok = tm_wait(su32(&ctl.s_free[t & 1]), ((uint32_t)(t >> 1) & 1u) ^ 1u, abort_w, a.status);
+            const uint32_t d = tmem + (t & 1) * C::TM_S;
+#pragma unroll
+            for (int term = 0; term < C::TERMS; ++term) {
+              // term j of K meets the first 3 - j of Q, in the accumulators of the products' size
+              const int slot = (it + term) % C::S;
+              ok = ok && tm_wait(su32(&ctl.full[slot]), (uint32_t)((it + term) / C::S) & 1u, abort_w, a.status);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t kb = ring + slot * C::SLOT;
+#pragma unroll
+              for (int blk = 0; blk < C::BLK; ++blk) {
+                const uint64_t dk = sw128_desc(kb + blk * (TM_PT * 128));
+                const uint64_t dq = sw128_desc(sbase + C::Q + blk * 3 * C::TERM);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                  mma_bf16(d + term * N, dk + s * 2, dq + s * 2, idS - (uint32_t)((term * N) >> 3 << 17),
+                           (term | blk | s) != 0 ? 1u : 0u);
+                  if constexpr (C::G == 2) mma_bf16(d + N, dk + s * 2, dq + ((2 * C::TERM) >> 4) + s * 2, idS1, 1u);
+                }
+              }
+              mma_commit(su32(&ctl.empty[slot]));
+            }
+            if (!ok) break;
+            mma_commit(su32(&ctl.s_full[t & 1]));
+            if (i == m.nt - 1) mma_commit(su32(&ctl.q_free));
+          }
+          if (i > 0) {  // outputs of tile i - 1
+            const int it = (ic + v_item(i - 1, m.nt)) * C::TERMS, t = tc + i - 1, pb = t % C::NP;
+            ok = tm_wait(su32(&ctl.p_full[pb]), (uint32_t)(t / C::NP) & 1u, abort_w, a.status);
+            const uint32_t pbuf = sbase + C::P + pb * C::PBYTES, d = tmem + C::TM_O + (t & 1) * C::TM_S;
+#pragma unroll
+            for (int term = 0; term < C::TERMS; ++term) {
+              const int slot = (it + term) % C::S;
+              ok = ok && tm_wait(su32(&ctl.full[slot]), (uint32_t)((it + term) / C::S) & 1u, abort_w, a.status);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t vb = ring + slot * C::SLOT;
+#pragma unroll
+              for (int s = 0; s < 8; ++s) {
+                const uint64_t dv = sw128_desc(vb + s * 2048, v_lead);
+                const uint64_t dp = sw128_desc(pbuf + (s >> 2) * 3 * C::TERM) + (s & 3) * 2;
+                mma_bf16(d + term * N, dv, dp, idO - (uint32_t)((term * N) >> 3 << 17), (term | s) != 0 ? 1u : 0u);
+                if constexpr (C::G == 2) mma_bf16(d + N, dv, dp + ((2 * C::TERM) >> 4), idO1, 1u);
+              }
+              mma_commit(su32(&ctl.empty[slot]));
+            }
+            if (!ok) break;
+            mma_commit(su32(&ctl.p_free[pb]));
+          }
+        }
+        ic += 2 * m.nt;
+        tc += m.nt;
+        ++qi;
+      }
+      if (!ok) {  // what was issued completes before the tensor memory is given back
+        mma_commit(su32(&ctl.done));
+        const long long c0 = clock64();
+        while (!mbar_try_wait(su32(&ctl.done), 0u) && clock64() - c0 < TM_WAIT_CYCLES) {
+        }
       }
     }
-    __syncthreads();
+    __syncwarp();
+  } else if (warp == C::QUERY_WARP) {
+    // ---- queries and masks of the next item, as soon as the scores of the one before are done
+    int qi = 0;
+    for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
+      if (have == 0 || m.nt == 0) continue;
+      // four elements of a row per lane, eight loads on their way at a time;
+      // the first before the scores of the item before are done with Q's place
+      constexpr int CH = HD / 4, ALL = N * CH / TM_QTHREADS, UNITS = 8, MK = (N + 31) / 32;
+      unsigned long long mask[MK];
 #pragma unroll
-    for (int i = 0; i < OR; ++i) {
-      const int r = og + RG * i;
-      if (r < rows) {
-        const float corr = crow[r];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] *= corr;
+      for (int j = 0; j < MK; ++j) {
+        const int n = lane + 32 * j;
+        mask[j] = n < m.rows ? a.masks[m.t.row0 + div_rep(m.n0 + n)] : 0ull;
       }
+#pragma unroll 1
+      for (int u0 = 0; u0 < ALL && ok; u0 += UNITS) {
+        float4 x[UNITS];
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          const int e = (u0 + u) * TM_QTHREADS + lane, n = e / CH, row = m.n0 + n, node = div_rep(row);
+          const float* q =
+              a.q + (size_t)(m.t.row0 + node) * a.ldq + (size_t)(m.g * rep + row - node * rep) * HD + e % CH * 4;
+          x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (n < m.rows) x[u] = (vec & 1) ? *reinterpret_cast<const float4*>(q) : make_float4(q[0], q[1], q[2], q[3]);
+        }
+        if (u0 == 0) ok = tm_wait(su32(&ctl.q_free), ((uint32_t)qi & 1u) ^ 1u, abort_w, a.status);
+        if (!ok) break;
+        if (u0 == 0) {
+#pragma unroll
+          for (int j = 0; j < MK; ++j)
+            if (lane + 32 * j < N) ctl.mask[qi % TM_MASKS][lane + 32 * j] = mask[j];
+        }
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          const int e = (u0 + u) * TM_QTHREADS + lane, n = e / CH, c = e % CH;
+          uint8_t* dst = sp + C::Q + (c >> 4) * 3 * C::TERM + n * 128 + ((((c >> 1) & 7) ^ (n & 7)) << 4) + (c & 1) * 8;
+          float2 v = make_float2(x[u].x, x[u].y), w = make_float2(x[u].z, x[u].w);
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {  // x = the sum of its three terms
+            const uint32_t p = pack_bf16(v), r = pack_bf16(w);
+            *reinterpret_cast<uint2*>(dst + term * C::TERM) = make_uint2(p, r);
+            v = add2(v, make_float2(-__uint_as_float(p << 16), -__uint_as_float(p & 0xffff0000u)));
+            w = add2(w, make_float2(-__uint_as_float(r << 16), -__uint_as_float(r & 0xffff0000u)));
+          }
+        }
+      }
+      if (!ok) break;
+      proxy_fence();
+      mbar_arrive(su32(&ctl.q_full[qi % TM_MASKS]));
+      ++qi;
     }
-    // a row must not meet the values of nodes it does not see (they may be
-    // infinite or NaN): tiles with nodes skip weights of zero
-    const bool drafts = (tile + 1) * TF_PT > t.L;
+  } else {
+    // ---- softmax: group wg has rows c0 .. c0 + NC - 1 of the tile, one thread a position
+    constexpr int NC = C::NC;
+    const int wg = warp >> 2, wt = tid & 127, w4 = warp & 3, c0 = wg * NC;
+    const float c = 1.4426950408889634f / sqrtf((float)HD);
+    const float2 c2 = make_float2(c, c);
+    const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
+    constexpr int NB = NC / 8;  // blocks of eight rows; this thread holds rows n2, n2 + 1 of each
+    const int n2 = c0 + (lane & 3) * 2;
+    // where this lane's row of the four matrices of a block starts in P: row
+    // lane % 8, positions 32 w4 + 8 (lane / 8) ..
+    const uint32_t p_lane = (uint32_t)(w4 >> 1) * (3 * C::TERM) + (c0 + (lane & 7)) * 128 +
+                            (((((w4 & 1) * 4) + (lane >> 3)) ^ (lane & 7)) << 4);
+    int ic = 0, tc = 0, qi = 0;
+    for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
+      if (have == 0) continue;
+      float2 base[NB], l[NB];  // negated base, sum of the weights
+      float o[NC];             // element wt of the running output's rows
+      bool scaled = false;     // the bases rose with this tile: the outputs before it are still to be scaled
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        base[b] = make_float2(-TM_FLOOR, -TM_FLOOR);
+        l[b] = make_float2(0.f, 0.f);
+      }
+#pragma unroll
+      for (int n = 0; n < NC; ++n) o[n] = 0.f;
+      if (wt < NC) {
+        ctl.base[c0 + wt] = TM_FLOOR;
+        ctl.sum[c0 + wt] = 0.f;
+      }
+      if (m.nt > 0) {  // the item's masks are there
+        ok = tm_wait(su32(&ctl.q_full[qi % TM_MASKS]), (uint32_t)(qi / TM_MASKS) & 1u, abort_w, a.status);
+        if (all_any<128 * C::SW>(!ok)) {
+          ok = false;
+          break;
+        }
+      }
+      for (int i = 0; i <= m.nt; ++i) {
+        const int t = tc + i, pb = t % C::NP;
+        if (i < m.nt) {
+        ok = tm_wait(su32(&ctl.s_full[t & 1]), (uint32_t)(t >> 1) & 1u, abort_w, a.status) && ok;
+        if (all_any<128 * C::SW>(!ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // scores of positions 32 w4 + 16 h + 8 r + lane / 4, 32 rows at a time
+        uint32_t f[2][NC / 2];
+        constexpr int W = NC < 32 ? NC : 32;
+#pragma unroll
+        for (int n = 0; n < NC; n += W) {
+          uint32_t v[C::G][2][W / 2];
+#pragma unroll
+          for (int gr = 0; gr < C::G; ++gr)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              tmem_frag<W>(tmem + (t & 1) * C::TM_S + gr * N + c0 + n + lanes + ((uint32_t)(16 * h) << 16), v[gr][h]);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < W / 2; e += 2) {
+              float2 r = make_float2(__uint_as_float(v[C::G - 1][h][e]), __uint_as_float(v[C::G - 1][h][e + 1]));
+#pragma unroll
+              for (int gr = C::G - 2; gr >= 0; --gr)
+                r = add2(r, make_float2(__uint_as_float(v[gr][h][e]), __uint_as_float(v[gr][h][e + 1])));
+              f[h][n / 2 + e] = __float_as_uint(r.x);
+              f[h][n / 2 + e + 1] = __float_as_uint(r.y);
+            }
+        }
+        tc_fence_before();
+        mbar_arrive(su32(&ctl.s_free[t & 1]));
+        const int p0 = (m.t0 + i) * TM_PT + w4 * 32;  // the warp's first position
+        if ((m.t0 + i + 1) * TM_PT > m.t.L) {  // the tile reaches past the committed positions
+          // the value row of a position no row may meet is zeroed: one past the
+          // sequence (whatever lies there), or a node's with an infinity or NaN
+          const int it = (ic + v_item(i, m.nt)) * C::TERMS, pos = p0 + lane;
+          // split tiles have a barrier of their own here: the places' may be a phase behind
+          ok = MODE == kSplit ? tm_wait(su32(&ctl.v_full[t & 1]), (uint32_t)(t >> 1) & 1u, abort_w, a.status)
+                              : tm_wait(su32(&ctl.full[it % C::S]), (uint32_t)(it / C::S) & 1u, abort_w, a.status);
+          if (wg == 0 && ok) {
+            uint4* vr = reinterpret_cast<uint4*>(sp + C::RING + it % C::S * C::SLOT + wt * 128);
+            bool mine = false;
+            if (pos >= m.t.L && pos < m.t.P) {
+#pragma unroll
+              for (int e = 0; e < C::BLK * 8; ++e) {
+                const uint4 u = vr[(e >> 3) * (TM_PT * 8) + (e & 7)];
+                const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                  mine = mine || (x[h] & 0x7f80u) == 0x7f80u || (x[h] & 0x7f800000u) == 0x7f800000u;
+              }
+            }
+            if (pos >= m.t.P || mine)
+              for (int term = 0; term < C::TERMS; ++term) {
+                uint4* z = reinterpret_cast<uint4*>(sp + C::RING + (it + term) % C::S * C::SLOT + wt * 128);
 #pragma unroll 4
-    for (int p = 0; p < TF_PT; ++p) {
-      float v[4];
-      load4(vb + p * C::KLD + oc, v);
+                for (int e = 0; e < C::BLK * 8; ++e) z[(e >> 3) * (TM_PT * 8) + (e & 7)] = make_uint4(0, 0, 0, 0);
+              }
+            // positions of the warp whose values are infinite or NaN: a row that sees one is NaN
+            const unsigned found = __ballot_sync(0xffffffffu, mine);
+            if (lane == 0) ctl.bad[w4] = found;
+          }
+          if (all_any<128 * C::SW>(!ok)) {
+            ok = false;
+            break;
+          }
+          const unsigned bad = ctl.bad[w4];
+          // this lane's positions, counted from the first node (negative: committed)
+          const uint32_t* words = reinterpret_cast<const uint32_t*>(ctl.mask[qi % TM_MASKS]) + 2 * n2;
 #pragma unroll
-      for (int i = 0; i < OR; ++i) {
-        const int r = og + RG * i;
-        const float w = r < rows ? ps[r * TF_PT + p] : 0.f;
-        if (drafts && w == 0.f) continue;
+          for (int q = 0; q < 4; ++q) {
+            const int off = 8 * q + (lane >> 2), j = p0 + off - m.t.L;
+            if (j >= 0) {
+              const uint32_t past = j >= m.t.T ? 0u : ~0u, seen = (bad >> off) & 1u ? 0x7fc00000u : 0u;
+              const uint32_t* w = words + (min(j, 63) >> 5);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] = fmaf(w, v[e], o[i][e]);
+              for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  uint32_t& x = f[q >> 1][4 * b + 2 * (q & 1) + e];
+                  const bool sees = ((w[16 * b + 2 * e] & past) >> (j & 31)) & 1u;
+                  x = sees ? (seen ? seen : x) : 0xff800000u;  // -inf
+                }
+            }
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t* x = &f[q >> 1][4 * b + 2 * (q & 1)];
+            const float2 v = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, base[b]);
+            top = fmaxf(top, fmaxf(v.x, v.y));
+          }
+        if (soft_any(top > TM_SLACK, wg)) {
+          // new bases: the rows' largest scores so far
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              mx = fmaxf(mx, __uint_as_float(f[q >> 1][4 * b + 2 * (q & 1)]));
+              my = fmaxf(my, __uint_as_float(f[q >> 1][4 * b + 2 * (q & 1) + 1]));
+            }
+            mx = lanes_max(mx);
+            my = lanes_max(my);
+            if (lane < 4) {
+              ctl.part[w4][8 * b + n2] = mx * c;
+              ctl.part[w4][8 * b + n2 + 1] = my * c;
+            }
+          }
+          soft_sync(wg);
+          if (wt < NC) {
+            const int n = c0 + wt;
+            const float old = ctl.base[n];
+            const float nb =
+                fmaxf(fmaxf(fmaxf(ctl.part[0][n], ctl.part[1][n]), fmaxf(ctl.part[2][n], ctl.part[3][n])), old);
+            ctl.corr[n] = nb == old ? 1.f : exp2_fast(old - nb);
+            ctl.base[n] = nb;
+          }
+          soft_sync(wg);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const int n = 8 * b + n2;
+            base[b] = make_float2(-ctl.base[n], -ctl.base[n + 1]);
+            l[b].x *= ctl.corr[n];
+            l[b].y *= ctl.corr[n + 1];
+          }
+          scaled = true;
+        }
+        ok = tm_wait(su32(&ctl.p_free[pb]), ((uint32_t)(t / C::NP) & 1u) ^ 1u, abort_w, a.status) && ok;
+        const uint32_t ph = sbase + C::P + pb * C::PBYTES + p_lane;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float2 p[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t* x = &f[q >> 1][4 * b + 2 * (q & 1)];
+            const float2 e = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, base[b]);
+            p[q] = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+            l[b] = add2(l[b], p[q]);
+          }
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              w[q] = pack_bf16(p[q]);
+              p[q] = add2(p[q], make_float2(-__uint_as_float(w[q] << 16), -__uint_as_float(w[q] & 0xffff0000u)));
+            }
+            store_t(ph + term * C::TERM + b * 1024, w[0], w[1], w[2], w[3]);
+          }
+        }
+        proxy_fence();
+        tc_fence_before();
+        mbar_arrive(su32(&ctl.p_full[pb]));
+        }
+        // the output of the tile before joins the running one: the tensor cores
+        // have had this tile's softmax to finish it (one P buffer: it was complete
+        // before this tile's P was written, and its barrier may be a phase on)
+        if (i > 0) {
+          if (C::NP > 1 || i == m.nt)
+            ok = tm_wait(su32(&ctl.p_free[(t - 1) % C::NP]), (uint32_t)((t - 1) / C::NP) & 1u, abort_w, a.status) && ok;
+          tc_fence_after();
+          const uint32_t src = tmem + C::TM_O + ((t - 1) & 1) * C::TM_S + lanes;
+#pragma unroll
+          for (int n = 0; n < NC; n += 16) {
+            uint32_t v[C::G][16];
+#pragma unroll
+            for (int gr = 0; gr < C::G; ++gr) tmem_ld16(src + gr * N + c0 + n, v[gr]);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              float2 r = make_float2(__uint_as_float(v[C::G - 1][e]), __uint_as_float(v[C::G - 1][e + 1]));
+#pragma unroll
+              for (int gr = C::G - 2; gr >= 0; --gr)
+                r = add2(r, make_float2(__uint_as_float(v[gr][e]), __uint_as_float(v[gr][e + 1])));
+              r = add2(r, make_float2(o[n + e], o[n + e + 1]));
+              o[n + e] = r.x;
+              o[n + e + 1] = r.y;
+            }
+          }
+          if (scaled) {
+#pragma unroll
+            for (int n = 0; n < NC; ++n) o[n] *= ctl.corr[c0 + n];
+          }
+        }
+        scaled = false;
+      }
+      if (m.nt > 0) {
+        if (all_any<128 * C::SW>(!ok)) {  // every softmax thread comes here, whichever of them gave up
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float sx = lanes_sum(l[b].x), sy = lanes_sum(l[b].y);
+          if (lane < 4) {
+            ctl.part[w4][8 * b + n2] = sx;
+            ctl.part[w4][8 * b + n2 + 1] = sy;
+          }
+        }
+        soft_sync(wg);
+        if (wt < NC) {
+          const int n = c0 + wt;
+          const float sum = (ctl.part[0][n] + ctl.part[1][n]) + (ctl.part[2][n] + ctl.part[3][n]);
+          ctl.sum[n] = CL > 1 ? sum : (sum == 0.f ? 0.f : 1.f / sum);  // a row that saw nothing: zeroes
+        }
+        // the rows, through P's place (its readers are done) to whole lines
+        float* os = reinterpret_cast<float*>(sp + C::P);  // [N][HD]
+        if (wt < HD) {
+#pragma unroll
+          for (int n = 0; n < NC; ++n) os[(c0 + n) * HD + wt] = o[n];
+        }
+        soft_sync(wg);
+        if (CL == 1) {
+          constexpr int LPR = HD / 4;  // lanes of a row
+#pragma unroll 1
+          for (int n = c0 + wt / LPR; n < min(m.rows, c0 + NC); n += 128 / LPR) {
+            const int row = m.n0 + n, node = div_rep(row), d = wt % LPR * 4;
+            const float4 v = *reinterpret_cast<const float4*>(os + n * HD + d);
+            const float f = ctl.sum[n];
+            float* dst = a.out + (size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + row - node * rep) * HD + d;
+            if (vec & 2) {
+              *reinterpret_cast<float4*>(dst) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+            } else {
+              dst[0] = v.x * f;
+              dst[1] = v.y * f;
+              dst[2] = v.z * f;
+              dst[3] = v.w * f;
+            }
+          }
+          all_any<128 * C::SW>(false);  // P and the sums may be written again
+        }
+        ic += 2 * m.nt;
+        tc += m.nt;
+        ++qi;
+      }
+      if (CL > 1) break;  // one item for a cluster
+    }
+    if (!ok) *abort_w = 1;
+  }
+  if (CL > 1 && (have = tm_item(a, deal, 0, m)) == 1) {
+    // join: what each share's output of a row counts for, then every CL-th row
+    cl.sync();
+    float* fac = reinterpret_cast<float*>(ctl.mask);  // [CL][N], where the masks were
+    static_assert(sizeof(ctl.mask) >= 8 * N * sizeof(float), "a factor per share and row");
+    if (tid < N) {
+      float bs[8], sm[8], mx = TM_FLOOR, sum = 0.f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        bs[r] = r < CL ? *cl.map_shared_rank(&ctl.base[tid], r) : TM_FLOOR;
+        sm[r] = r < CL ? *cl.map_shared_rank(&ctl.sum[tid], r) : 0.f;
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r) mx = fmaxf(mx, bs[r]);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        bs[r] = sm[r] == 0.f ? 0.f : exp2_fast(bs[r] - mx);  // 0: the share saw nothing
+        sum = fmaf(sm[r], bs[r], sum);
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < CL) fac[r * N + tid] = sum == 0.f ? 0.f : bs[r] / sum;
+    }
+    __syncthreads();
+    constexpr int LPR = HD / 4;  // lanes of a row
+    if (!*abort_w) {
+      for (int n = rank + CL * (tid / LPR); n < m.rows; n += CL * (C::THREADS / LPR)) {
+        const int d = tid % LPR * 4;
+        float4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)  // a share without tiles wrote no output: its factor is 0
+          v[r] = r < CL && fac[r * N + n] != 0.f
+                     ? *reinterpret_cast<const float4*>(
+                           cl.map_shared_rank(reinterpret_cast<float*>(sp + C::P), r) + n * HD + d)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < CL) {
+            const float f = fac[r * N + n];
+            o.x = fmaf(v[r].x, f, o.x);
+            o.y = fmaf(v[r].y, f, o.y);
+            o.z = fmaf(v[r].z, f, o.z);
+            o.w = fmaf(v[r].w, f, o.w);
+          }
+        const int row = m.n0 + n, node = div_rep(row);
+        float* dst = a.out + (size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + row - node * rep) * HD + d;
+        if (vec & 2) {
+          *reinterpret_cast<float4*>(dst) = o;
+        } else {
+          dst[0] = o.x;
+          dst[1] = o.y;
+          dst[2] = o.z;
+          dst[3] = o.w;
+        }
       }
     }
-    __syncthreads();  // the stage and ps may be written again
+    cl.sync();  // the others may still read this CTA's shared memory
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  pdl_trigger();
-  if (C_ == 1) {
-#pragma unroll
-    for (int i = 0; i < OR; ++i) {
-      const int r = og + RG * i, n = n0 + r;
-      if (r < rows) {
-        const float l = lrow[r];
-        float* dst = a.out + (size_t)(t.row0 + n / rep) * a.ldo + (size_t)(g * rep + n % rep) * HD + oc;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dst[e] = l == 0.f ? 0.f : o[i][e] / l;
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < OR; ++i) {
-    const int r = og + RG * i;
-    if (r < RT)
-      *reinterpret_cast<float4*>(os + r * HD + oc) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-  }
-  cl.sync();
-  // join: the cluster's CTAs take the rows in turn
-  for (int r = rank + C_ * warp; r < rows; r += C_ * (TF_THREADS / 32)) {
-    float m = -INFINITY;
-    for (int c = 0; c < C_; ++c) m = fmaxf(m, *cl.map_shared_rank(mrow + r, c));
-    float l = 0.f, acc[HD / 32];
-#pragma unroll
-    for (int e = 0; e < HD / 32; ++e) acc[e] = 0.f;
-    for (int c = 0; c < C_; ++c) {
-      const float mc = *cl.map_shared_rank(mrow + r, c);
-      if (mc == -INFINITY) continue;  // no position of this share is seen
-      const float f = expf(mc - m);
-      l = fmaf(*cl.map_shared_rank(lrow + r, c), f, l);
-      const float* oc_ = cl.map_shared_rank(os + r * HD, c);
-#pragma unroll
-      for (int e = 0; e < HD / 32; ++e) acc[e] = fmaf(oc_[lane + 32 * e], f, acc[e]);
-    }
-    const int n = n0 + r;
-    float* dst = a.out + (size_t)(t.row0 + n / rep) * a.ldo + (size_t)(g * rep + n % rep) * HD;
-#pragma unroll
-    for (int e = 0; e < HD / 32; ++e) dst[lane + 32 * e] = l == 0.f ? 0.f : acc[e] / l;
-  }
-  cl.sync();  // the others may still read this CTA's shared memory
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::MMA_WARP)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
 }
 
-template <class KT, int HD, int RT>
-int launch_fma(const TreeArgs& a, int dev, int n_sm, cudaStream_t s) {
-  using C = TfCfg<KT, HD, RT>;
+// ------------------------------------------------------------- host side
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    else
+      cudaGetLastError();
+  });
+  return fn;
+}
+
+// CTAs of a cluster (which splits the positions of one item): enough to fill
+// the SMs, no more than there are tiles at the sequences' capacity, at most 8
+// (the portable cluster size).
+int cluster_size(long items, int tiles, int n_sm) {
+  int c = 1;
+  while (c < 8 && items * c * 2 <= n_sm && c * 2 <= tiles) c *= 2;
+  return c;
+}
+
+template <int HD, int N, int MODE>
+int launch_mma(const TreeArgs& a, int layers, int dev, int n_sm, cudaStream_t s) {
+  using C = TmCfg<HD, N, MODE>;
   static bool ready[kMaxDevices] = {};  // the attribute is the device's
   if (!ready[dev]) {
-    if (cudaFuncSetAttribute(tree_fma_kernel<KT, HD, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(tree_mma_kernel<HD, N, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)C::SMEM) != cudaSuccess)
       return Q3TTS_ERR_CUDA;
     ready[dev] = true;
   }
-  const int rep = a.Hq / a.kv.Hkv, row_tiles = (a.max_nodes * rep + RT - 1) / RT;
+  // the pool as a matrix of head-dim rows, read one page's rows (at most a
+  // tile's) by 64 elements at a time
+  const int box = a.kv.page_size < TM_PT ? a.kv.page_size : TM_PT;
+  CUtensorMap map = {};
+  if (MODE == kTma) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    if (!enc) return Q3TTS_ERR_CUDA;
+    const cuuint64_t dims[2] = {(cuuint64_t)HD, (cuuint64_t)((long long)layers * a.kv.n_pages * 2 * a.kv.Hkv * a.kv.page_size)};
+    const cuuint64_t strides[1] = {(cuuint64_t)HD * 2};
+    const cuuint32_t boxd[2] = {64, (cuuint32_t)box};
+    const cuuint32_t estr[2] = {1, 1};
+    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.kv.pool, dims, strides, boxd, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return Q3TTS_ERR_CUDA;
+  }
+  const int row_tiles = (a.max_nodes * (a.Hq / a.kv.Hkv) + N - 1) / N;
   const long items = (long)a.n_seqs * a.kv.Hkv * row_tiles;
-  const int tiles = (int)(((long)a.kv.pages_per_stream * a.kv.page_size + TF_PT - 1) / TF_PT);
-  const int c = tree_cluster(items, tiles, 4 * n_sm);
-  if (items * c > 0x7fffffffL) return Q3TTS_ERR_UNSUPPORTED;
+  const int tiles = (int)(((long)a.kv.pages_per_stream * a.kv.page_size + TM_PT - 1) / TM_PT);
+  const int c = cluster_size(items, tiles, n_sm);
+  if (items > 0x7fffffffL / 2) return Q3TTS_ERR_UNSUPPORTED;
+  // split items: one for each cluster; whole ones: a CTA on every SM works through them
+  const long grid = c > 1 ? items * c : (items < n_sm ? items : n_sm);
+  const int vec = (((uintptr_t)a.q & 15) == 0 && a.ldq % 4 == 0 ? 1 : 0) |  // float4 loads of q, stores of out
+                  (((uintptr_t)a.out & 15) == 0 && a.ldo % 4 == 0 ? 2 : 0);
+  const unsigned rep = (unsigned)(a.Hq / a.kv.Hkv), rep_inv = (unsigned)(((1ull << 32) + rep - 1) / rep);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items * c));
-  cfg.blockDim = dim3(TF_THREADS);
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
@@ -287,31 +1178,37 @@ int launch_fma(const TreeArgs& a, int dev, int n_sm, cudaStream_t s) {
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, tree_fma_kernel<KT, HD, RT>, a, row_tiles) == cudaSuccess ? Q3TTS_OK
-                                                                                           : Q3TTS_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, tree_mma_kernel<HD, N, MODE>, map, a, row_tiles, box, (int)items, vec, rep_inv) == cudaSuccess
+             ? Q3TTS_OK
+             : Q3TTS_ERR_CUDA;
 }
 
-template <class KT>
-int launch_fma_any(const TreeArgs& a, int dev, int n_sm, cudaStream_t s) {
+template <int HD, int MODE>
+int launch_rows(const TreeArgs& a, int layers, int dev, int n_sm, cudaStream_t s) {
   const int rows = a.max_nodes * (a.Hq / a.kv.Hkv);
-  if (a.kv.hd == 128) return rows <= 8 ? launch_fma<KT, 128, 8>(a, dev, n_sm, s) : launch_fma<KT, 128, 32>(a, dev, n_sm, s);
-  return rows <= 8 ? launch_fma<KT, 64, 8>(a, dev, n_sm, s) : launch_fma<KT, 64, 32>(a, dev, n_sm, s);
+  if (rows <= 16) return launch_mma<HD, 16, MODE>(a, layers, dev, n_sm, s);
+  if (rows <= 32 || MODE == kSplit) return launch_mma<HD, 32, MODE>(a, layers, dev, n_sm, s);
+  return launch_mma<HD, MODE == kSplit ? 32 : 64, MODE>(a, layers, dev, n_sm, s);
+}
+
+template <int HD>
+int launch_mode(const TreeArgs& a, int layers, int kdt, int dev, int n_sm, cudaStream_t s) {
+  if (kdt == Q3TTS_F32) return launch_rows<HD, kSplit>(a, layers, dev, n_sm, s);
+  // TMA boxes are pages of whole swizzle atoms (8 rows) that fill a tile a whole
+  // number of times, or whole tiles of larger pages
+  const int ps = a.kv.page_size;
+  if ((ps >= 8 && ps <= TM_PT && TM_PT % ps == 0) || ps % TM_PT == 0)
+    return launch_rows<HD, kTma>(a, layers, dev, n_sm, s);
+  return launch_rows<HD, kCopy>(a, layers, dev, n_sm, s);
 }
 
 }  // namespace
-
-int tree_cluster(long items, int tiles, long slots) {
-  int c = 1;
-  while (c < 8 && items * c * 2 <= slots && c * 2 <= tiles) c *= 2;
-  return c;
-}
 
 int launch_tree_attention(const TreeArgs& a, int layers, int kdt, cudaStream_t s) {
   if (a.n_seqs <= 0 || a.n_rows <= 0) return Q3TTS_OK;
   int dev = 0, n_sm = 0;
   if (!current_device(&dev, &n_sm)) return Q3TTS_ERR_CUDA;
-  if (tree_mma_ok(a, layers, kdt)) return launch_tree_mma(a, layers, dev, n_sm, s);
-  return kdt == Q3TTS_BF16 ? launch_fma_any<bf16>(a, dev, n_sm, s) : launch_fma_any<float>(a, dev, n_sm, s);
+  return a.kv.hd == 128 ? launch_mode<128>(a, layers, kdt, dev, n_sm, s) : launch_mode<64>(a, layers, kdt, dev, n_sm, s);
 }
 
 }  // namespace q3

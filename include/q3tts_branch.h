@@ -122,6 +122,8 @@ typedef struct q3tts_kv_cache {
  *                   elements apart; q head h reads kv head
  *                   h / (n_q_heads / n_kv_heads), at most 1024 of them one;
  *                   scale 1 / sqrt(head_dim).
+ * Caches of up to 2^31 rows of head_dim elements in all (else
+ * Q3TTS_ERR_UNSUPPORTED).
  * Rows outside every sequence's range are left as they were, like the rows of
  * a sequence whose entries do not fit (reported in status_dev).  out may not
  * overlap q.  Accumulation in fp32; a row's result does not depend on the run,

@@ -74,6 +74,11 @@ def test_tree_attention_refuses(lib, kw):
     assert tree(lib, **kw) == q3tts.ERR_ARG
 
 
+def test_tree_attention_limits(lib):
+    assert tree(lib, heads=2 * 1025, ldq=1 << 20, ldo=1 << 20) == q3tts.ERR_UNSUPPORTED
+    assert tree(lib, cache(n_pages=1 << 25)) == q3tts.ERR_UNSUPPORTED  # 2^32 rows
+
+
 @pytest.mark.parametrize("bad,code", BAD_CACHES)
 def test_caches_are_checked(lib, bad, code):
     kv = cache(**bad)

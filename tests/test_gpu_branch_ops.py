@@ -67,12 +67,22 @@ def test_tree_attention(q3, case, dtype):
     assert int(status) == 0
 
 
-def test_tree_attention_many_sequences(q3):
+@pytest.mark.parametrize("seqs,longest,most,heads,kv_heads,hd,page", [
+    (97, 700, 13, 16, 8, 128, 16), (60, 1500, 1, 8, 8, 128, 16), (300, 90, 3, 4, 2, 64, 16),
+    (70, 700, 9, 4, 1, 64, 8), (45, 600, 40, 8, 4, 128, 16), (41, 900, 16, 16, 8, 128, 12),
+    (33, 800, 64, 2, 1, 64, 24)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_tree_attention_many_sequences(q3, dtype, seqs, longest, most, heads, kv_heads, hd, page):
+    """More sequences, heads and row tiles than SMs: each SM works through several
+    of them, one to many tiles long, some without nodes."""
     import torch
     rng = np.random.default_rng(8)
-    lens, nodes = rng.integers(0, 700, 97).tolist(), rng.integers(0, 13, 97).tolist()
-    c = tree_case(rng, lens, nodes, 16, 8, 128, 16, torch.bfloat16)
-    check_tree(c, run_tree(q3, c))
+    lens, nodes = rng.integers(0, longest, seqs).tolist(), rng.integers(0, most + 1, seqs).tolist()
+    c = tree_case(rng, lens, nodes, heads, kv_heads, hd, page, getattr(torch, dtype))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = run_tree(q3, c, status=status)
+    check_tree(c, out)
+    assert int(status) == 0 and torch.equal(out, run_tree(q3, c))
 
 
 def test_chain_and_masks_that_see_nothing(q3):
