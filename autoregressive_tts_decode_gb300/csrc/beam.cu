@@ -5,9 +5,9 @@
 // the repetition penalty and the mask of special codes (the sampler's rule),
 //   score(b, v) = scores[b] + (x_v - max x) - log sum_v e^(x_v - max x),
 // and a group keeps the k candidates with the largest scores among its beams'
-// vocabularies.  Scores are compared in 64 bits, so that candidates of
-// different beams order as their exact values do; equal scores go to the lower
-// beam, then the larger logit, then the lower code.  A finished beam offers one
+// vocabularies.  Scores are compared to 2^-46 of their size, so that candidates
+// of different beams order as their exact values do; equal scores go to the
+// lower beam, then the larger logit, then the lower code.  A finished beam offers one
 // candidate, its end code at its own score.
 //
 // Within a row scores order as logits do, so a row's own k best logits are all
@@ -21,8 +21,8 @@
 // distributed shared memory, took one launch but 47 us for 8 groups of 16 beams
 // over 131072 codes: no more than 7 such clusters run at once, or their CTAs
 // share SMs.)
-// The GPU's fp64 rate is low: the few values that need 64 bits (a row's log sum,
-// a candidate's score) are computed in them, and compared as ordered integers.
+// The GPU's fp64 rate is low: a row's log sum is computed in fp64, a candidate's
+// score as a sum of two floats, and compared as an ordered integer.
 #include "ops.cuh"
 
 namespace q3 {
@@ -46,10 +46,6 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t b = __float_as_uint(x);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
-__device__ __forceinline__ u64 ordered(double x) {
-  const u64 b = (u64)__double_as_longlong(x);
-  return (b >> 63) ? ~b : (b | (1ull << 63));
-}
 // Larger key: larger logit, then lower code.  Keys of a row are distinct; 0 is
 // below every key.
 __device__ __forceinline__ u64 make_key(float x, int v) { return ((u64)ordered(x) << 32) | (uint32_t)~v; }
@@ -68,36 +64,42 @@ struct Piece {
 
 struct BeamSmem {
   float red[2][32];
-  float group[64];
+  float group[64], bound;
   u64 best[BM_MAXK], top[BM_MAXK];
   int n_cand;
   u64 cand[BM_CAND];
 };
 
 struct JoinSmem {
-  double lse[BM_MAXB];  // the beam's score less the log of its row's sum (relative to its maximum)
+  float hi[BM_MAXB], lo[BM_MAXB];  // the beam's score less the log of its row's sum (relative to its maximum), in two floats
   float mx[BM_MAXB];
-  u64 group[64];
+  uint32_t group[128], bound;
   int n_cand;
   u64 score[BM_LISTS * BM_MAXK], key[BM_LISTS * BM_MAXK];  // the candidates that may be kept
   int row[BM_LISTS * BM_MAXK];
 };
 
-// The k-th largest of 64 values in shared memory (k <= 64), for every lane of a
-// warp; v0 and v1 are the lane's two of them.
-template <class T>
-__device__ __forceinline__ T kth_of_64(const T* g, int k) {
-  const int lane = threadIdx.x & 31;
-  const T v0 = g[lane], v1 = g[lane + 32];
-  int r0 = 0, r1 = 0;  // how many come before each: larger, or equal and earlier
-#pragma unroll 8
-  for (int j = 0; j < 32; ++j) {
-    const T a = g[j], b = g[j + 32];
-    r0 += (a > v0 || (a == v0 && j < lane)) + (b > v0);
-    r1 += (a >= v1) + (b > v1 || (b == v1 && j < lane));
+// The k-th largest of the G group values g[0 .. G) into *out (k <= G).  Each warp
+// ranks its share of them, 32 comparisons a ballot.  All threads; ends in a
+// block barrier, and expects one since g was written.
+template <int G, class T>
+__device__ __forceinline__ void kth_group(const T* g, int k, T* out) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int PER = G / BM_WARPS;
+  T v[G / 32];
+#pragma unroll
+  for (int c = 0; c < G / 32; ++c) v[c] = g[c * 32 + lane];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int me = warp * PER + i;
+    const T x = g[me];
+    int r = 0;  // how many come before it: larger, or equal and earlier
+#pragma unroll
+    for (int c = 0; c < G / 32; ++c)
+      r += __popc(__ballot_sync(0xffffffffu, v[c] > x || (v[c] == x && c * 32 + lane < me)));
+    if (r == k - 1 && lane == 0) *out = x;
   }
-  const unsigned at0 = __ballot_sync(0xffffffffu, r0 == k - 1), at1 = __ballot_sync(0xffffffffu, r1 == k - 1);
-  return at0 ? __shfl_sync(0xffffffffu, v0, __ffs(at0) - 1) : __shfl_sync(0xffffffffu, v1, __ffs(at1) - 1);
+  __syncthreads();
 }
 
 // The k best of sm.cand[0 .. n) into sm.best, in order, the rest 0.  All
@@ -125,12 +127,13 @@ __device__ void keep_best(BeamSmem& sm, int n, int k) {
   }
   if (tid < BM_MAXK) sm.best[tid] = 0;
   __syncthreads();
-  if (tid < n) {
-    const u64 key = from[tid];
+  // a warp ranks every sixteenth, 32 comparisons a ballot
+  const int lane = tid & 31;
+  for (int i = tid >> 5; i < n; i += BM_WARPS) {
+    const u64 key = from[i];
     int r = 0;
-#pragma unroll 8
-    for (int j = 0; j < n; ++j) r += from[j] > key;
-    if (r < k) sm.best[r] = key;
+    for (int j = 0; j < n; j += 32) r += __popc(__ballot_sync(0xffffffffu, j + lane < n && from[j + lane] > key));
+    if (lane == 0 && r < k) sm.best[r] = key;
   }
   __syncthreads();
 }
@@ -287,7 +290,8 @@ __device__ __forceinline__ void scan_piece(BeamSmem& sm, Piece& out, const BeamA
       for (int o = 4; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
       if ((lane & 7) == 0) sm.group[warp * 4 + (lane >> 3)] = gm;
       __syncthreads();
-      bound = kth_of_64(sm.group, k);
+      kth_group<64>(sm.group, k, &sm.bound);
+      bound = sm.bound;
     }
     int at = -1;
     if (tm > thr && tm >= bound) {
@@ -374,7 +378,34 @@ __device__ __forceinline__ double log_of(double x) {
   return fma((double)e, 0.6931471805599453, 2.0 * fma(t * t2, p, t));
 }
 
-// Joins a group's lists: every entry's score in 64 bits, a bound that the k
+// score = (hi + lo) + (x - mx) as an ordered integer, 0 for none (-inf or NaN): a
+// sum of two floats (about 48 bits), the larger one's bits above the smaller
+// one's.  (The fp64 units are too slow for a thousand of these.)
+__device__ __forceinline__ u64 score_key(float hi, float lo, float x, float mx) {
+  if (!(hi > -INFINITY)) return 0;
+  float h, l;
+  if (x == mx || (fabsf(x) < 1e36f && fabsf(mx) < 1e36f && fabsf(hi) < 1e36f)) {
+    // x - mx = d + e exactly (infinite logits share the weight: 0)
+    const float d = x == mx ? 0.f : x - mx;
+    const float t = d - x, e = x == mx ? 0.f : (x - (d - t)) + (-mx - t);
+    // hi + d = s + f exactly
+    const float s = hi + d, u = s - hi, f = (hi - (s - u)) + (d - u);
+    const float r = f + (lo + e);
+    h = s + r;
+    l = h - h == 0.f ? (s - h) + r : 0.f;
+  } else {  // sums that may leave fp32's range
+    const double v = ((double)hi + (double)lo) + ((double)x - (double)mx);
+    if (!(v > -INFINITY)) return 0;
+    h = (float)fmin(fmax(v, -3.4028234663852886e38), 3.4028234663852886e38);
+    l = (float)(v - (double)h);
+    if (v == INFINITY) h = INFINITY, l = 0.f;
+  }
+  return ((u64)ordered(h) << 32) | ordered(l + 0.f);
+}
+// The score of a key, rounded once.
+__device__ __forceinline__ float score_of(u64 k) { return key_value(k) + key_value(k << 32); }
+
+// Joins a group's lists: every entry's score, a bound that the k
 // best are at or above (as in the scan), and the order of what passes it.  Lane
 // i of a warp holds entry i of its lists.
 __global__ void __launch_bounds__(BM_THREADS) beam_join_kernel(BeamArgs a, int pieces, const Piece* ws) {
@@ -401,7 +432,9 @@ __global__ void __launch_bounds__(BM_THREADS) beam_join_kernel(BeamArgs a, int p
 #pragma unroll 4
     for (int p = 0; p < pieces; ++p) ss += (double)(p0[p].sum * exp_off(p0[p].mx, mm));
     // what a candidate's logit is scored against
-    jn.lse[tid] = ss > 0.0 ? (double)a.scores[g * a.beams + tid] - log_of(ss) : 0.0;  // 0: a row without candidates
+    const double base = (double)a.scores[g * a.beams + tid] - (ss > 0.0 ? log_of(ss) : 0.0);
+    jn.hi[tid] = (float)base;
+    jn.lo[tid] = (float)(base - (double)(float)base);
     jn.mx[tid] = mm;
   }
   if (tid == 0) jn.n_cand = 0;
@@ -412,24 +445,22 @@ __global__ void __launch_bounds__(BM_THREADS) beam_join_kernel(BeamArgs a, int p
     sc[i] = 0;
     if (key[i] != 0) {
       const int b = (warp + i * BM_WARPS) / pieces;
-      const float x = key_value(key[i]), mm = jn.mx[b];
-      // score + (x - max) - log sum; infinite logits share the weight
-      const double v = jn.lse[b] + (x == mm ? 0.0 : (double)x - (double)mm);
-      if (v > -INFINITY) sc[i] = ordered(v);
+      sc[i] = score_key(jn.hi[b], jn.lo[b], key_value(key[i]), jn.mx[b]);
     }
     best = sc[i] > best ? sc[i] : best;
   }
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) {
-    const u64 v = __shfl_xor_sync(0xffffffffu, best, o);
-    best = v > best ? v : best;
-  }
-  if ((lane & 7) == 0) jn.group[warp * 4 + (lane >> 3)] = best;
+  // groups of lanes l, l + 8, l + 16 and l + 24 (of sorted lists: the larger
+  // entries apart), by the scores' high words
+  uint32_t top = (uint32_t)(best >> 32);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+  if (lane < 8) jn.group[warp * 8 + lane] = top;
   __syncthreads();
-  const u64 bound = kth_of_64(jn.group, k);
+  kth_group<128>(jn.group, k, &jn.bound);
+  const uint32_t bound = jn.bound;
 #pragma unroll
   for (int i = 0; i < PER; ++i)
-    if (sc[i] != 0 && sc[i] >= bound) {
+    if (sc[i] != 0 && (uint32_t)(sc[i] >> 32) >= bound) {
       const int at = atomicAdd(&jn.n_cand, 1);
       jn.score[at] = sc[i];
       jn.key[at] = key[i];
@@ -437,22 +468,23 @@ __global__ void __launch_bounds__(BM_THREADS) beam_join_kernel(BeamArgs a, int p
     }
   __syncthreads();
   const int n = jn.n_cand;
-  for (int i = tid; i < n; i += BM_THREADS) {
-    const u64 sc = jn.score[i];
-    const u64 key = jn.key[i];
-    const int b = jn.row[i];
+  for (int i = warp; i < n; i += BM_WARPS) {
+    const u64 s0 = jn.score[i], k0 = jn.key[i];
+    const int b0 = jn.row[i];
     int r = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const u64 so = jn.score[j];
-      r += so > sc;
-      if (so == sc && j != i) r += jn.row[j] < b || (jn.row[j] == b && jn.key[j] > key);
+    for (int j0 = 0; j0 < n; j0 += 32) {
+      const int j = j0 + lane;
+      bool before = false;
+      if (j < n) {
+        const u64 s1 = jn.score[j];
+        before = s1 > s0 || (s1 == s0 && (jn.row[j] < b0 || (jn.row[j] == b0 && jn.key[j] > k0)));
+      }
+      r += __popc(__ballot_sync(0xffffffffu, before));
     }
-    if (r < k) {
-      a.tokens[g * k + r] = key_code(key);
-      a.parents[g * k + r] = b;
-      const u64 raw = (sc >> 63) ? (sc & ~(1ull << 63)) : ~sc;
-      a.scores_out[g * k + r] = (float)__longlong_as_double((long long)raw);
+    if (lane == 0 && r < k) {
+      a.tokens[g * k + r] = key_code(k0);
+      a.parents[g * k + r] = b0;
+      a.scores_out[g * k + r] = score_of(s0);
     }
   }
   if (tid >= n && tid < k) {  // no candidate left for the slot

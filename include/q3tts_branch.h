@@ -159,8 +159,8 @@ int q3tts_compact_rows(const q3tts_kv_cache* kv, const int32_t* page_table_dev, 
  * offers one, eos_token (which must be a code then) at its own score.  The k
  * best of each group are written in order: tokens_dev, parents_dev (b) and
  * scores_out_dev, [groups][k] each (scores_out_dev may be scores_dev when k ==
- * beams).  Scores are compared in 64 bits and rounded once; of equal ones the
- * lower beam comes first, then the larger logit, then the lower code.  A slot
+ * beams).  Scores are compared to 2^-46 of their size and rounded once; of equal
+ * ones the lower beam comes first, then the larger logit, then the lower code.  A slot
  * without a candidate above -INFINITY gets token -1, parent 0 and score
  * -INFINITY.  beams and k up to Q3TTS_MAX_BEAMS, vocab up to 2^24.  Row ids
  * are not checked.  workspace_dev: device memory, 8-byte aligned, of at least
