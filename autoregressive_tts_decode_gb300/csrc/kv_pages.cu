@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(CP_THREADS) copy_pages_kernel(uint4* pool, lon
 // are looked up once for all heads.
 constexpr int CR_THREADS = 256;
 constexpr int CR_UNROLL = 8;  // 16-byte loads in flight per thread
-constexpr int CR_ROWS = 256;  // rows looked up at a time
+constexpr int CR_ROWS = CR_THREADS;  // rows looked up at a time
 
 __global__ void __launch_bounds__(CR_THREADS) compact_rows_kernel(KVDesc kv, int row_shift, const int* lengths,
                                                                   const int* path, int max_path, const int* path_len,
@@ -62,17 +62,23 @@ __global__ void __launch_bounds__(CR_THREADS) compact_rows_kernel(KVDesc kv, int
   const int* pa = path + (size_t)seq * max_path;
   const int* table = kv.page_table + (size_t)seq * kv.pages_per_stream;
   const long long cap = (long long)kv.pages_per_stream * kv.page_size;
-  bool ok = n >= 0 && n <= max_path && L >= 0;
   // the row's place, -1 if its page is outside the pool
   auto place = [&](int pos) -> long long {
     const int page = table[pos / kv.page_size];
     if (page < 0 || page >= kv.n_pages) return -1;
     return ((long long)page * 2 * kv.Hkv * kv.page_size + pos % kv.page_size) << row_shift;
   };
+  bool ok = n >= 0 && n <= max_path && L >= 0;
   if (ok)
     for (int i = tid; i < n; i += CR_THREADS) {
-      const int p = pa[i];
-      ok = ok && p >= 0 && (long long)L + p < cap && (i == 0 || p > pa[i - 1]) && place(L + p) >= 0 && place(L + i) >= 0;
+      const int p = pa[i], before = i ? pa[i - 1] : -1;
+      ok = ok && p > before && (long long)L + p < cap;
+      const long long f = ok ? place(L + p) : -1, t = ok ? place(L + i) : -1;
+      ok = ok && f >= 0 && t >= 0;
+      if (i < CR_ROWS) {  // (longer paths: looked up again below)
+        from[i] = f;
+        to[i] = p == i ? -1 : t;  // -1: already there
+      }
     }
   if (!__syncthreads_and(ok)) {
     if (tid == 0 && layer == 0) op_status(status, Q3TTS_ERR_ARG);
@@ -85,13 +91,15 @@ __global__ void __launch_bounds__(CR_THREADS) compact_rows_kernel(KVDesc kv, int
   const int c = tid & ((1 << row_shift) - 1), step = CR_THREADS >> row_shift;
   for (int i0 = 0; i0 < n; i0 += CR_ROWS) {
     const int m = min(CR_ROWS, n - i0);
-    __syncthreads();
-    if (tid < m) {
-      const int i = i0 + tid, p = pa[i];
-      from[tid] = place(L + p);
-      to[tid] = p == i ? -1 : place(L + i);  // -1: already there
+    if (i0) {
+      __syncthreads();
+      if (tid < m) {
+        const int i = i0 + tid, p = pa[i];
+        from[tid] = place(L + p);
+        to[tid] = p == i ? -1 : place(L + i);
+      }
+      __syncthreads();
     }
-    __syncthreads();
     for (int e0 = tid >> row_shift; e0 - (tid >> row_shift) < m * units; e0 += step * CR_UNROLL) {
       uint4 v[CR_UNROLL];
       long long dst[CR_UNROLL];

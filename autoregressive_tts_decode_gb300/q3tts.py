@@ -352,6 +352,7 @@ def beam_select(logits, scores, k: Optional[int] = None, row_ids=None, finished=
     i32 = torch.int32
     k = beams if k is None else int(k)
     if out is None:
+        # (one block cut into views would cost the host more than three allocations)
         best = torch.empty_like(scores) if k == beams else scores.new_empty((groups, max(k, 0)))
         tokens = torch.empty_like(best, dtype=i32)
         parents = torch.empty_like(best, dtype=i32)
@@ -363,13 +364,13 @@ def beam_select(logits, scores, k: Optional[int] = None, row_ids=None, finished=
     if workspace is None:
         workspace = torch.empty(beam_workspace_size(groups, beams, vocab, k), dtype=torch.uint8, device=logits.device)
     n_ws = workspace.numel()
+    p_ws = _cuda(workspace, "workspace", torch.uint8, dev, n_ws, what)
     _call(dev, load().q3tts_beam_select, what, logits.data_ptr(), ld,
           None if row_ids is None else _cuda(row_ids, "row_ids", i32, dev, n, what), groups, beams, vocab,
           _cuda(scores, "scores", torch.float32, dev, n, what),
           None if finished is None else _cuda(finished, "finished", torch.uint8, dev, rows, what),
           None if history is None else _cuda(history, "history", torch.uint8, dev, rows * vocab, what),
-          eos_token, special_from, repetition_penalty, k, *p_out,
-          _cuda(workspace, "workspace", torch.uint8, dev, n_ws, what), n_ws)
+          eos_token, special_from, repetition_penalty, k, *p_out, p_ws, n_ws)
     return tokens, parents, best
 
 
