@@ -44,13 +44,7 @@
 // Every wait is bounded; on expiry the CTA records Q3TTS_ERR_TIMEOUT, waits
 // (bounded) for its copies and MMAs in flight, frees its tensor memory and
 // writes nothing more.
-#include <cooperative_groups.h>
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
-#include "ops.cuh"
+#include "tree.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -58,34 +52,8 @@ namespace q3 {
 
 namespace {
 
-// What a CTA works on; false when it has no rows.  Lengths and row offsets
-// come from device memory, so they are checked here: a sequence whose entries
-// do not fit the cache or the buffers is left out and reported.
-struct TreeSeq {
-  int L, T, row0, P;  // committed positions, nodes, first row of q/out, L + T
-};
-__device__ __forceinline__ bool tree_seq(const TreeArgs& a, int seq, TreeSeq& t) {
-  t.L = a.lengths[seq];
-  t.row0 = a.node_start[seq];
-  const int end = a.node_start[seq + 1];
-  const long long cap = (long long)a.kv.pages_per_stream * a.kv.page_size;
-  if (t.row0 < 0 || end < t.row0 || end > a.n_rows || end - t.row0 > a.max_nodes || t.L < 0 ||
-      (long long)t.L + (end - t.row0) > cap) {
-    op_status(a.status, Q3TTS_ERR_ARG);
-    return false;
-  }
-  t.T = end - t.row0;
-  t.P = t.L + t.T;
-  return t.T > 0;
-}
-
-constexpr int TM_PT = 128;       // positions of a tile
 constexpr int TM_QTHREADS = 32;
-constexpr int TM_SORT = 256;     // sequences that are dealt by length, at most (no more than threads)
 constexpr int TM_MASKS = 4;      // items whose masks are held: the softmax's, and the scores may be three ahead
-constexpr long long TM_WAIT_CYCLES = 4000000000ll;  // ~2 s
-constexpr float TM_FLOOR = -1e30f;  // base of a row that has seen nothing: below every score
-constexpr float TM_SLACK = 8.f;     // how far (log2) a score may pass its row's base
 
 // How a tile of K or V gets from the cache into shared memory.
 enum TmLoad {
@@ -139,68 +107,6 @@ struct TmCtl {
   int copies[2][8];  // TMA: the last ring tiles that each loading warp has filled
 };
 
-__device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void mbar_init(uint32_t b, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t b, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait(uint32_t b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(b), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// 128-byte swizzled operand tiles: rows of 128 bytes, 8-row atoms 1024 bytes
-// apart (stride byte offset), descriptor version 1, swizzle mode 2.  K-major:
-// the leading offset is not used.  M-major (V^T: 64 head-dim elements are a
-// row's 128 bytes, positions the rows): the leading offset is the distance of
-// the second 64 elements' block.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lead = 16) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lead & 0x3FFFFu) >> 4) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-// kind::f16: D fp32, A and B bf16, B K-major; A K-major or M-major (bit 15).
-__host__ __device__ constexpr uint32_t f16_idesc(int M, int N, bool a_m_major) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (a_m_major ? 1u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
-}
-__device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(
-          tmem_d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accum)
-      : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-// 16 fp32 columns of the warp's 32 lanes, one lane per thread (complete after wait::ld).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
 // N fp32 columns of 16 lanes, eight columns at a time in the fragment order of
 // an 8 x 8 matrix store: registers 4 b and 4 b + 1 hold columns 8 b + 2 (lane % 4)
 // and the next of lane / 4, registers 4 b + 2 and 4 b + 3 the same of
@@ -225,34 +131,6 @@ __device__ __forceinline__ void store_t(uint32_t addr, uint32_t a, uint32_t b, u
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                "r"(d)
                : "memory");
-}
-// Pairs of floats (one 64-bit register pair, one instruction each).
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
-      " mov.b64 {%0, %1}, d;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-// Two floats to bf16 (x in the low half).
-__device__ __forceinline__ uint32_t pack_bf16(float2 v) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
-  return r;
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 // Barrier and vote of the 128 threads of softmax group wg.
 __device__ __forceinline__ void soft_sync(int wg) {
@@ -280,27 +158,6 @@ __device__ __forceinline__ bool all_any(bool p) {
   return r != 0;
 }
 
-// Bounded wait on an mbarrier phase; false on expiry or when another role of
-// the CTA has given up.
-__device__ __noinline__ bool tm_wait_long(uint32_t bar, uint32_t parity, volatile int* abort_w, int* status) {
-  const long long t0 = clock64();
-  unsigned it = 0;
-  while (!mbar_try_wait(bar, parity)) {
-    if ((++it & 63u) == 0) {
-      if (*abort_w) return false;
-      if (clock64() - t0 > TM_WAIT_CYCLES) {
-        *abort_w = 1;
-        op_status(status, Q3TTS_ERR_TIMEOUT);
-        return false;
-      }
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ bool tm_wait(uint32_t bar, uint32_t parity, volatile int* abort_w, int* status) {
-  return mbar_try_wait(bar, parity) || tm_wait_long(bar, parity, abort_w, status);
-}
-
 // Max or sum over the lanes that hold the same columns (lane % 4).
 __device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
@@ -311,44 +168,6 @@ __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
   for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
-}
-
-// Ring position of tile t's K and V among n tiles: K0 K1 V0 K2 V1 .. V(n-1).
-__device__ __forceinline__ int k_item(int t) { return t == 0 ? 0 : 2 * t - 1; }
-__device__ __forceinline__ int v_item(int t, int n) { return t == n - 1 ? 2 * n - 1 : 2 * t + 2; }
-
-// One item of work.
-struct TmItem {
-  TreeSeq t;
-  int seq, g, n0, rows;  // kv head, first row of the tile, rows
-  int t0, nt;            // first position tile, tiles
-};
-
-// How the items are dealt.
-struct TmDeal {
-  int items, row_tiles, rows;  // rows of a tile
-  int stride, first;           // clusters, this one
-  int rank, cl;                // CTA of the cluster, CTAs
-  const uint16_t* order;       // sequences, longest first, or NULL
-};
-
-// The k-th item of a CTA: 1 if there is one, 0 if it has no rows (or does not
-// fit, which is reported), -1 past the last.
-__device__ __forceinline__ int tm_item(const TreeArgs& a, const TmDeal& d, int k, TmItem& m) {
-  if ((long long)k * d.stride >= d.items) return -1;
-  const int idx = k * d.stride + ((k & 1) ? d.stride - 1 - d.first : d.first);
-  if (idx >= d.items) return 0;
-  const int rep = a.Hq / a.kv.Hkv;
-  m.g = idx / d.row_tiles % a.kv.Hkv;
-  m.seq = idx / d.row_tiles / a.kv.Hkv;
-  if (d.order) m.seq = d.order[m.seq];
-  m.n0 = idx % d.row_tiles * d.rows;
-  if (!tree_seq(a, m.seq, m.t) || m.n0 >= m.t.T * rep) return 0;
-  m.rows = min(d.rows, m.t.T * rep - m.n0);
-  const int all = (m.t.P + TM_PT - 1) / TM_PT, per = (all + d.cl - 1) / d.cl;
-  m.t0 = min(all, d.rank * per);
-  m.nt = min(all, m.t0 + per) - m.t0;
-  return 1;
 }
 
 template <int HD, int N, int MODE>
@@ -395,18 +214,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
   }
   pdl_wait();  // q and the appended keys and values come from the previous kernels
   const bool sorted = items > (int)gridDim.x / CL && a.n_seqs <= TM_SORT;
-  if (sorted) {
-    const int mine = tid < a.n_seqs ? a.lengths[tid] : 0;
-    if (tid < TM_SORT) ctl.len[tid] = mine;
-    __syncthreads();
-    int r = 0;
-#pragma unroll 8
-    for (int j = 0; j < a.n_seqs; ++j) {
-      const int o = ctl.len[j];
-      r += o > mine || (o == mine && j < tid);
-    }
-    if (tid < a.n_seqs) ctl.order[r] = (uint16_t)tid;
-  }
+  if (sorted) sort_lengths(a, ctl.len, ctl.order);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -415,63 +223,22 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
 
   const TmDeal deal{items, row_tiles, N, (int)gridDim.x / CL, (int)blockIdx.x / CL, rank, CL,
                     sorted ? ctl.order : nullptr};
-  // row / rep for rows of an item (rep_inv = ceil(2^32 / rep); exact for rows and rep up to 2^16)
-  auto div_rep = [&](int row) -> int { return rep == 1 ? row : (int)__umulhi((unsigned)row, rep_inv); };
   TmItem m;
   int have = 0;
   bool ok = true;
 
   if (warp >= C::LOAD_WARP) {
     // ---- loads
-    const bool values = MODE == kTma && warp > C::LOAD_WARP;  // TMA: a warp for the keys and one for the values
-    const int ps = a.kv.page_size;
-    const long long plane = (long long)a.kv.Hkv * ps;  // rows of a page's keys (or values)
-    int ic = 0, issued = 0;                            // position tiles so far, TMA copies of this warp
-    for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
-      if (have == 0 || m.nt == 0) continue;
-      const int* table = a.kv.page_table + (size_t)m.seq * a.kv.pages_per_stream;
-      // row of the pool ([layer][page][k|v][kv head][position]) of a position on `page`
-      auto pool_row = [&](int page, int pos) -> int {
-        if (page < 0 || page >= a.kv.n_pages) {
-          op_status(a.status, Q3TTS_ERR_ARG);
-          page = 0;
-        }
-        return (int)((((long long)a.layer * a.kv.n_pages + page) * 2 + (values ? 1 : 0)) * plane +
-                     (long long)m.g * ps + pos % ps);
-      };
-      if constexpr (MODE == kTma) {
-        // lane (b, blk) copies block blk of page b's rows of a tile.  A warp's
-        // lanes issue one by one, 55 cycles each: from one warp for keys and
-        // values the 32 copies of 2 KB of a tile of 16-position pages took longer
-        // than the tile's bytes.
-        const int b = lane / C::BLK, blk = lane % C::BLK;
-        const int boxes = TM_PT / box;
-        // the page of this lane's box in tile i; looked up two tiles ahead and not
-        // touched until then, so the lookup's latency is never waited for
-        auto page_of = [&](int i) -> int {
-          const int pos = (m.t0 + i) * TM_PT + b * box;
-          return b < boxes && i < m.nt && pos < m.t.P ? __ldg(table + pos / ps) : 0;
-        };
-        int page_even = page_of(0), page_odd = page_of(1);
-        for (int tile = 0; tile < m.nt; ++tile) {
-          const int it = 2 * ic + (values ? v_item(tile, m.nt) : k_item(tile)), slot = it % C::S;
-          const int pos = (m.t0 + tile) * TM_PT + b * box;
-          const int page = (tile & 1) ? page_odd : page_even;
-          const uint32_t fb = su32(&ctl.full[slot]);
-          ok = __all_sync(0xffffffffu,
-                          tm_wait(su32(&ctl.empty[slot]), ((uint32_t)(it / C::S) & 1u) ^ 1u, abort_w, a.status));
-          if (!ok) break;
-          const int held = min(TM_PT, m.t.P - (m.t0 + tile) * TM_PT);
-          if (lane == 0) mbar_expect_tx(fb, (uint32_t)((held + box - 1) / box * box * HD * 2));
-          __syncwarp();
-          if (b < boxes && pos < m.t.P)
-            tma_load(ring + slot * C::SLOT + blk * (TM_PT * 128) + b * box * 128, &map, blk * 64, pool_row(page, pos), fb);
-          // the page two tiles on takes this one's place
-          if (tile & 1) page_odd = page_of(tile + 2); else page_even = page_of(tile + 2);
-          if (lane == 0) ctl.copies[warp - C::LOAD_WARP][issued % 8] = it;
-          ++issued;
-        }
-      } else {
+    if constexpr (MODE == kTma) {
+      const int w = warp - C::LOAD_WARP;  // a warp for the keys and one for the values
+      ok = tma_loads<HD, C::S>(&map, a, deal, box, w > 0, ring, ctl.full, ctl.empty, ctl.copies[w], abort_w);
+    } else {
+      const int ps = a.kv.page_size;
+      const long long plane = (long long)a.kv.Hkv * ps;  // rows of a page's keys (or values)
+      int ic = 0;                                        // position tiles so far
+      for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
+        if (have == 0 || m.nt == 0) continue;
+        const int* table = a.kv.page_table + (size_t)m.seq * a.kv.pages_per_stream;
         // all loading warps share every tile, in the ring's order (so that a place
         // is waited for at every phase of its barrier); warp lw has rows lw RW ..
         // of it, lane l the pool rows of the l-th of them (and the 32nd after it)
@@ -490,12 +257,12 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
 #pragma unroll
           for (int h = 0; h < H; ++h) {
             const int pos = (m.t0 + i) * TM_PT + lw * RW + lane + 32 * h;
-            rows[h] = i < m.nt && pos < m.t.P ? pool_row(pages[h], pos) : -1;
+            rows[h] = i < m.nt && pos < m.t.P ? pool_row(a, m.g, false, pages[h], pos) : -1;
             pages[h] = pages2[h];
             // the next tile on its way to the L2: the loads that follow keep too few
             // bytes in flight for the memory's latency
             if (MODE == kSplit && i + 1 < m.nt && pos + TM_PT < m.t.P) {
-              const uint8_t* p = pool + (size_t)pool_row(pages[h], pos + TM_PT) * (HD * 4);
+              const uint8_t* p = pool + (size_t)pool_row(a, m.g, false, pages[h], pos + TM_PT) * (HD * 4);
 #pragma unroll
               for (int line = 0; line < HD * 4; line += 128) {
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(p + line));
@@ -612,16 +379,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
             if (is_value(i)) mbar_arrive(su32(&ctl.v_full[(ic + tile_of(i)) & 1]));
           }
         }
-      }
-      ic += m.nt;
-    }
-    if (MODE == kTma && !ok) {  // copies in flight land before the CTA leaves (otherwise the MMAs have waited for them)
-      for (int j = issued > C::S ? issued - C::S : 0; j < issued; ++j) {
-        const int it = ctl.copies[warp - C::LOAD_WARP][j % 8];
-        const long long c0 = clock64();
-        while (!mbar_try_wait(su32(&ctl.full[it % C::S]), (uint32_t)(it / C::S) & 1u) &&
-               clock64() - c0 < TM_WAIT_CYCLES / 8) {
-        }
+        ic += m.nt;
       }
     }
   } else if (warp == C::MMA_WARP) {
@@ -708,47 +466,20 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
     int qi = 0;
     for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
       if (have == 0 || m.nt == 0) continue;
-      // four elements of a row per lane, eight loads on their way at a time;
-      // the first before the scores of the item before are done with Q's place
-      constexpr int CH = HD / 4, ALL = N * CH / TM_QTHREADS, UNITS = 8, MK = (N + 31) / 32;
+      constexpr int MK = (N + 31) / 32;
       unsigned long long mask[MK];
 #pragma unroll
       for (int j = 0; j < MK; ++j) {
         const int n = lane + 32 * j;
-        mask[j] = n < m.rows ? a.masks[m.t.row0 + div_rep(m.n0 + n)] : 0ull;
+        mask[j] = n < m.rows ? a.masks[m.t.row0 + div_rep(m.n0 + n, rep, rep_inv)] : 0ull;
       }
-#pragma unroll 1
-      for (int u0 = 0; u0 < ALL && ok; u0 += UNITS) {
-        float4 x[UNITS];
+      ok = load_queries<HD, N, TM_QTHREADS>(a, m, rep, rep_inv, vec & 1, lane, sp + C::Q, [&] {
+        if (!tm_wait(su32(&ctl.q_free), ((uint32_t)qi & 1u) ^ 1u, abort_w, a.status)) return false;
 #pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          const int e = (u0 + u) * TM_QTHREADS + lane, n = e / CH, row = m.n0 + n, node = div_rep(row);
-          const float* q =
-              a.q + (size_t)(m.t.row0 + node) * a.ldq + (size_t)(m.g * rep + row - node * rep) * HD + e % CH * 4;
-          x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (n < m.rows) x[u] = (vec & 1) ? *reinterpret_cast<const float4*>(q) : make_float4(q[0], q[1], q[2], q[3]);
-        }
-        if (u0 == 0) ok = tm_wait(su32(&ctl.q_free), ((uint32_t)qi & 1u) ^ 1u, abort_w, a.status);
-        if (!ok) break;
-        if (u0 == 0) {
-#pragma unroll
-          for (int j = 0; j < MK; ++j)
-            if (lane + 32 * j < N) ctl.mask[qi % TM_MASKS][lane + 32 * j] = mask[j];
-        }
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          const int e = (u0 + u) * TM_QTHREADS + lane, n = e / CH, c = e % CH;
-          uint8_t* dst = sp + C::Q + (c >> 4) * 3 * C::TERM + n * 128 + ((((c >> 1) & 7) ^ (n & 7)) << 4) + (c & 1) * 8;
-          float2 v = make_float2(x[u].x, x[u].y), w = make_float2(x[u].z, x[u].w);
-#pragma unroll
-          for (int term = 0; term < 3; ++term) {  // x = the sum of its three terms
-            const uint32_t p = pack_bf16(v), r = pack_bf16(w);
-            *reinterpret_cast<uint2*>(dst + term * C::TERM) = make_uint2(p, r);
-            v = add2(v, make_float2(-__uint_as_float(p << 16), -__uint_as_float(p & 0xffff0000u)));
-            w = add2(w, make_float2(-__uint_as_float(r << 16), -__uint_as_float(r & 0xffff0000u)));
-          }
-        }
-      }
+        for (int j = 0; j < MK; ++j)
+          if (lane + 32 * j < N) ctl.mask[qi % TM_MASKS][lane + 32 * j] = mask[j];
+        return true;
+      });
       if (!ok) break;
       proxy_fence();
       mbar_arrive(su32(&ctl.q_full[qi % TM_MASKS]));
@@ -1015,7 +746,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
           constexpr int LPR = HD / 4;  // lanes of a row
 #pragma unroll 1
           for (int n = c0 + wt / LPR; n < min(m.rows, c0 + NC); n += 128 / LPR) {
-            const int row = m.n0 + n, node = div_rep(row), d = wt % LPR * 4;
+            const int row = m.n0 + n, node = div_rep(row, rep, rep_inv), d = wt % LPR * 4;
             const float4 v = *reinterpret_cast<const float4*>(os + n * HD + d);
             const float f = ctl.sum[n];
             float* dst = a.out + (size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + row - node * rep) * HD + d;
@@ -1039,63 +770,9 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
     if (!ok) *abort_w = 1;
   }
   if (CL > 1 && (have = tm_item(a, deal, 0, m)) == 1) {
-    // join: what each share's output of a row counts for, then every CL-th row
-    cl.sync();
-    float* fac = reinterpret_cast<float*>(ctl.mask);  // [CL][N], where the masks were
-    static_assert(sizeof(ctl.mask) >= 8 * N * sizeof(float), "a factor per share and row");
-    if (tid < N) {
-      float bs[8], sm[8], mx = TM_FLOOR, sum = 0.f;
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        bs[r] = r < CL ? *cl.map_shared_rank(&ctl.base[tid], r) : TM_FLOOR;
-        sm[r] = r < CL ? *cl.map_shared_rank(&ctl.sum[tid], r) : 0.f;
-      }
-#pragma unroll
-      for (int r = 0; r < 8; ++r) mx = fmaxf(mx, bs[r]);
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        bs[r] = sm[r] == 0.f ? 0.f : exp2_fast(bs[r] - mx);  // 0: the share saw nothing
-        sum = fmaf(sm[r], bs[r], sum);
-      }
-#pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r < CL) fac[r * N + tid] = sum == 0.f ? 0.f : bs[r] / sum;
-    }
-    __syncthreads();
-    constexpr int LPR = HD / 4;  // lanes of a row
-    if (!*abort_w) {
-      for (int n = rank + CL * (tid / LPR); n < m.rows; n += CL * (C::THREADS / LPR)) {
-        const int d = tid % LPR * 4;
-        float4 v[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r)  // a share without tiles wrote no output: its factor is 0
-          v[r] = r < CL && fac[r * N + n] != 0.f
-                     ? *reinterpret_cast<const float4*>(
-                           cl.map_shared_rank(reinterpret_cast<float*>(sp + C::P), r) + n * HD + d)
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < CL) {
-            const float f = fac[r * N + n];
-            o.x = fmaf(v[r].x, f, o.x);
-            o.y = fmaf(v[r].y, f, o.y);
-            o.z = fmaf(v[r].z, f, o.z);
-            o.w = fmaf(v[r].w, f, o.w);
-          }
-        const int row = m.n0 + n, node = div_rep(row);
-        float* dst = a.out + (size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + row - node * rep) * HD + d;
-        if (vec & 2) {
-          *reinterpret_cast<float4*>(dst) = o;
-        } else {
-          dst[0] = o.x;
-          dst[1] = o.y;
-          dst[2] = o.z;
-          dst[3] = o.w;
-        }
-      }
-    }
-    cl.sync();  // the others may still read this CTA's shared memory
+    static_assert(sizeof(ctl.mask) >= 8 * N * sizeof(float), "a factor per share and row, where the masks were");
+    join_shares<HD, N, C::THREADS, HD>(a, m, rep, rep_inv, vec & 2, ctl.base, ctl.sum, reinterpret_cast<float*>(ctl.mask),
+                                       reinterpret_cast<float*>(sp + C::P), abort_w);
   }
   tc_fence_before();
   __syncthreads();
@@ -1104,30 +781,6 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
 }
 
 // ------------------------------------------------------------- host side
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    else
-      cudaGetLastError();
-  });
-  return fn;
-}
-
-// CTAs of a cluster (which splits the positions of one item): enough to fill
-// the SMs, no more than there are tiles at the sequences' capacity, at most 8
-// (the portable cluster size).
-int cluster_size(long items, int tiles, int n_sm) {
-  int c = 1;
-  while (c < 8 && items * c * 2 <= n_sm && c * 2 <= tiles) c *= 2;
-  return c;
-}
 
 template <int HD, int N, int MODE>
 int launch_mma(const TreeArgs& a, int layers, int dev, int n_sm, cudaStream_t s) {
@@ -1139,48 +792,7 @@ int launch_mma(const TreeArgs& a, int layers, int dev, int n_sm, cudaStream_t s)
       return Q3TTS_ERR_CUDA;
     ready[dev] = true;
   }
-  // the pool as a matrix of head-dim rows, read one page's rows (at most a
-  // tile's) by 64 elements at a time
-  const int box = a.kv.page_size < TM_PT ? a.kv.page_size : TM_PT;
-  CUtensorMap map = {};
-  if (MODE == kTma) {
-    const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
-    if (!enc) return Q3TTS_ERR_CUDA;
-    const cuuint64_t dims[2] = {(cuuint64_t)HD, (cuuint64_t)((long long)layers * a.kv.n_pages * 2 * a.kv.Hkv * a.kv.page_size)};
-    const cuuint64_t strides[1] = {(cuuint64_t)HD * 2};
-    const cuuint32_t boxd[2] = {64, (cuuint32_t)box};
-    const cuuint32_t estr[2] = {1, 1};
-    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.kv.pool, dims, strides, boxd, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return Q3TTS_ERR_CUDA;
-  }
-  const int row_tiles = (a.max_nodes * (a.Hq / a.kv.Hkv) + N - 1) / N;
-  const long items = (long)a.n_seqs * a.kv.Hkv * row_tiles;
-  const int tiles = (int)(((long)a.kv.pages_per_stream * a.kv.page_size + TM_PT - 1) / TM_PT);
-  const int c = cluster_size(items, tiles, n_sm);
-  if (items > 0x7fffffffL / 2) return Q3TTS_ERR_UNSUPPORTED;
-  // split items: one for each cluster; whole ones: a CTA on every SM works through them
-  const long grid = c > 1 ? items * c : (items < n_sm ? items : n_sm);
-  const int vec = (((uintptr_t)a.q & 15) == 0 && a.ldq % 4 == 0 ? 1 : 0) |  // float4 loads of q, stores of out
-                  (((uintptr_t)a.out & 15) == 0 && a.ldo % 4 == 0 ? 2 : 0);
-  const unsigned rep = (unsigned)(a.Hq / a.kv.Hkv), rep_inv = (unsigned)(((1ull << 32) + rep - 1) / rep);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = c;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, tree_mma_kernel<HD, N, MODE>, map, a, row_tiles, box, (int)items, vec, rep_inv) == cudaSuccess
-             ? Q3TTS_OK
-             : Q3TTS_ERR_CUDA;
+  return launch_items(tree_mma_kernel<HD, N, MODE>, C::THREADS, C::SMEM, MODE == kTma, N, a, layers, n_sm, s);
 }
 
 template <int HD, int MODE>
@@ -1188,6 +800,7 @@ int launch_rows(const TreeArgs& a, int layers, int dev, int n_sm, cudaStream_t s
   const int rows = a.max_nodes * (a.Hq / a.kv.Hkv);
   if (rows <= 16) return launch_mma<HD, 16, MODE>(a, layers, dev, n_sm, s);
   if (rows <= 32 || MODE == kSplit) return launch_mma<HD, 32, MODE>(a, layers, dev, n_sm, s);
+  if (MODE == kTma && rows > 64) return launch_tree_wide(a, layers, dev, n_sm, s);
   return launch_mma<HD, MODE == kSplit ? 32 : 64, MODE>(a, layers, dev, n_sm, s);
 }
 

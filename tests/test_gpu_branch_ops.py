@@ -53,6 +53,10 @@ TREES = [
     ([300], [20], 12, 3, 128, 32), ([129], [5], 4, 2, 64, 64), ([511], [40], 4, 4, 64, 128),
     ([600], [13], 4, 2, 128, 256), ([70], [64], 16, 1, 64, 16), ([45], [6], 2, 1, 128, 1),
     ([2048], [16], 16, 8, 128, 16), ([5000, 1], [3, 3], 2, 1, 64, 16), ([333], [17], 10, 2, 128, 24),
+    # more than 64 rows to a kv head
+    ([9000], [64], 4, 2, 128, 16), ([700, 3, 0, 260], [64, 33, 40, 0], 16, 2, 128, 16), ([500, 129], [64, 50], 8, 2, 64, 32),
+    ([300], [33], 2, 1, 128, 128), ([127, 64, 0], [64, 64, 64], 2, 1, 128, 8), ([383], [22], 3, 1, 64, 256),
+    ([0], [5], 16, 1, 128, 64),
 ]
 
 
@@ -70,7 +74,7 @@ def test_tree_attention(q3, case, dtype):
 @pytest.mark.parametrize("seqs,longest,most,heads,kv_heads,hd,page", [
     (97, 700, 13, 16, 8, 128, 16), (60, 1500, 1, 8, 8, 128, 16), (300, 90, 3, 4, 2, 64, 16),
     (70, 700, 9, 4, 1, 64, 8), (45, 600, 40, 8, 4, 128, 16), (41, 900, 16, 16, 8, 128, 12),
-    (33, 800, 64, 2, 1, 64, 24)])
+    (33, 800, 64, 2, 1, 64, 24), (60, 700, 64, 8, 4, 128, 16), (170, 300, 33, 8, 1, 64, 64)])
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
 def test_tree_attention_many_sequences(q3, dtype, seqs, longest, most, heads, kv_heads, hd, page):
     """More sequences, heads and row tiles than SMs: each SM works through several
@@ -85,11 +89,12 @@ def test_tree_attention_many_sequences(q3, dtype, seqs, longest, most, heads, kv
     assert int(status) == 0 and torch.equal(out, run_tree(q3, c))
 
 
-def test_chain_and_masks_that_see_nothing(q3):
+@pytest.mark.parametrize("heads", [4, 32])
+def test_chain_and_masks_that_see_nothing(q3, heads):
     """A chain is causal attention; a mask of zeroes sees the context only, and
     without a context nothing: zeroes, whatever the cache holds."""
     import torch
-    c = tree_case(np.random.default_rng(9), [40, 0, 0], [12, 4, 5], 4, 2, 128, 16, torch.bfloat16,
+    c = tree_case(np.random.default_rng(9), [40, 0, 0], [12, 4, 5], heads, 2, 128, 16, torch.bfloat16,
                   parents=[list(range(-1, 11)), [-1, 0, 1, 2], [-1] * 5])
     c["masks"][12 + 2] = 0
     c["masks"][3] = 0
@@ -98,12 +103,13 @@ def test_chain_and_masks_that_see_nothing(q3):
     assert bool((out[12 + 2] == 0).all())
 
 
+@pytest.mark.parametrize("heads", [4, 32])
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
-def test_large_scores_and_masked_infinities(q3, dtype):
+def test_large_scores_and_masked_infinities(q3, dtype, heads):
     """Scores hundreds apart, rising along the context; infinities and NaN at
     nodes that no mask shows."""
     import torch
-    c = tree_case(np.random.default_rng(10), [400], [6], 4, 2, 128, 16, getattr(torch, dtype),
+    c = tree_case(np.random.default_rng(10), [400], [6], heads, 2, 128, 16, getattr(torch, dtype),
                   parents=[[-1, 0, -1, 2, -1, 4]])
     pos = torch.arange(406, device="cuda")
     pg, slot = c["table"][0].long()[pos // 16], pos % 16
@@ -123,16 +129,17 @@ def test_large_scores_and_masked_infinities(q3, dtype):
     assert bool(((out.double() - want).abs() <= tol).all())
 
 
-def test_row_pitches_and_rows_left_alone(q3):
+@pytest.mark.parametrize("heads", [4, 40])
+def test_row_pitches_and_rows_left_alone(q3, heads):
     """q inside a wider buffer at an odd pitch, out likewise; rows behind the last
     sequence and other columns keep their values."""
     import torch
-    c = tree_case(np.random.default_rng(11), [33, 90], [5, 7], 4, 2, 64, 16, torch.bfloat16)
-    wide = torch.full((15, 4 * 64 + 37), 3.25, device="cuda")
-    wide[:12, 1:257] = c["q"].reshape(12, -1)
-    qv = wide[:, 1:257].unflatten(1, (4, 64))
-    outw = torch.full((15, 4 * 64 + 3), -7.5, device="cuda")
-    ov = outw[:, 3:].unflatten(1, (4, 64))
+    c = tree_case(np.random.default_rng(11), [33, 90], [5, 7], heads, 2, 64, 16, torch.bfloat16)
+    wide = torch.full((15, heads * 64 + 37), 3.25, device="cuda")
+    wide[:12, 1:heads * 64 + 1] = c["q"].reshape(12, -1)
+    qv = wide[:, 1:heads * 64 + 1].unflatten(1, (heads, 64))
+    outw = torch.full((15, heads * 64 + 3), -7.5, device="cuda")
+    ov = outw[:, 3:].unflatten(1, (heads, 64))
     masks = torch.cat([bu.masks_tensor(c["masks"]), torch.zeros(3, dtype=torch.int64, device="cuda")])
     q3.tree_attention(c["pool"], 1, c["table"], c["lengths"], c["start"], masks, qv, max_nodes=7, out=ov)
     check_tree(c, ov[:12])
