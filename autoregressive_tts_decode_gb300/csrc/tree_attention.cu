@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
 
   cg::cluster_group cl = cg::this_cluster();
   const int CL = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int rep = a.Hq / a.kv.Hkv;
 
   if (tid == 0) {
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
   const uint32_t ring = sbase + C::RING;
 
   const TmDeal deal{items, row_tiles, N, (int)gridDim.x / CL, (int)blockIdx.x / CL, rank, CL,
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
     }
   } else if (warp == C::MMA_WARP) {
     // ---- MMA issue
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idS = f16_idesc(TM_PT, (C::G == 3 ? 3 : 2) * N, false), idS1 = f16_idesc(TM_PT, N, false);
       constexpr uint32_t idO = f16_idesc(TM_PT, (C::G == 3 ? 3 : 2) * N, true), idO1 = f16_idesc(TM_PT, N, true);
       // a head dimension of 64 fills half of M: the other half's rows are read

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
 
   namespace cg = cooperative_groups;
   const int CL = (int)cg::this_cluster().num_blocks(), rank = (int)cg::this_cluster().block_rank();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int rep = a.Hq / a.kv.Hkv;
 
   if (tid == 0) {
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
   const uint32_t ring = sbase + C::RING;
   float* shares = reinterpret_cast<float*>(sp);  // bases and sums for the other shares of the item, factors; in Q's place
 
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
     ok = tma_loads<HD, C::S>(&map, a, deal, box, w > 0, ring, ctl.full, ctl.empty, ctl.copies[w], abort_w);
   } else if (warp == C::MMA_WARP) {
     // ---- MMA issue
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idS = f16_idesc(TW_ROWS, TM_PT, false), idO = f16_idesc(TW_ROWS, HD, false) | 1u << 16;  // B N-major
       int ic = 0, tc = 0, qi = 0;  // ring tiles, position tiles and items so far
       for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
@@ -171,16 +171,14 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
             ok = tm_wait(su32(&ctl.full[slot]), (uint32_t)(it / C::S) & 1u, abort_w, a.status);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t kb = ring + slot * C::SLOT, d = tmem + (t & 1) * C::TM_B;
+            const uint32_t d = tmem + (t & 1) * C::TM_B;
+            const uint64_t dk = sw128_desc(ring) + slot * (C::SLOT >> 4), dq = sw128_desc(sbase);
 #pragma unroll
             for (int term = 2; term >= 0; --term)
 #pragma unroll
-              for (int blk = 0; blk < C::BLK; ++blk) {
-                const uint64_t dk = sw128_desc(kb + blk * (TM_PT * 128));
-                const uint64_t dq = sw128_desc(sbase + (blk * 3 + term) * C::TERM);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) mma_bf16(d, dq + s * 2, dk + s * 2, idS, (term < 2 || (blk | s) != 0) ? 1u : 0u);
-              }
+              for (int s = 0; s < HD / 16; ++s)
+                mma_bf16(d, dq + (((s >> 2) * 3 + term) * C::TERM >> 4) + (s & 3) * 2, dk + ((s >> 2) * TM_PT * 128 >> 4) + (s & 3) * 2,
+                         idS, (term < 2 || s != 0) ? 1u : 0u);
             mma_commit(su32(&ctl.empty[slot]));
             mma_commit(su32(&ctl.s_full[t & 1]));
             if (i == m.nt - 1) mma_commit(su32(&ctl.q_free));
@@ -191,14 +189,14 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
                  tm_wait(su32(&ctl.p_full), (uint32_t)t & 1u, abort_w, a.status);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t vb = ring + slot * C::SLOT, p = tmem + (t & 1) * C::TM_B;
+            const uint32_t p = tmem + (t & 1) * C::TM_B;
+            const uint64_t dv = sw128_desc(ring, HD == 128 ? TM_PT * 128 : 1024) + slot * (C::SLOT >> 4);
 #pragma unroll
             for (int term = 2; term >= 0; --term)
 #pragma unroll
               for (int s = 0; s < 8; ++s) {  // 16 positions: eight columns of a term
                 const uint32_t at = term == 2 ? C::TM_LO + 8 * s : 32 * (s >> 1) + 16 * term + 8 * (s & 1);
-                mma_bf16_ts(tmem + C::TM_O, p + at, sw128_desc(vb + s * 2048, HD == 128 ? TM_PT * 128 : 1024), idO,
-                            (term < 2 || s != 0) ? 1u : 0u);
+                mma_bf16_ts(tmem + C::TM_O, p + at, dv + (s * 2048 >> 4), idO, (term < 2 || s != 0) ? 1u : 0u);
               }
             mma_commit(su32(&ctl.empty[slot]));
             mma_commit(su32(&ctl.o_full));
