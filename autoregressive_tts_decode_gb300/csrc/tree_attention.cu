@@ -77,8 +77,7 @@ struct TmCfg {
   static constexpr uint32_t TERM = N * 128;         // one term of one 64-element block (of Q or P)
   static constexpr uint32_t QBYTES = BLK * 3 * TERM, PBYTES = 2 * 3 * TERM;
   static constexpr int G = N <= 32 ? 3 : 2;         // accumulator groups: the terms, or the large one and the others
-  static constexpr int NP = N <= 32 ? 2 : 1;        // P buffers
-  static constexpr uint32_t Q = 0, P = QBYTES, RING = P + NP * PBYTES;
+  static constexpr uint32_t Q = 0, P = QBYTES, RING = P + PBYTES;  // (a second P would cost a place of the ring: 125 against 122 us, 16 nodes)
   static constexpr uint32_t CTL_BYTES = 6144;
   static constexpr int FIT = (int)((227u * 1024 - 1024 - CTL_BYTES - RING) / SLOT);
   static constexpr int S = FIT < 8 ? FIT : 8;       // tiles in the ring
@@ -89,13 +88,13 @@ struct TmCfg {
   // three places: a TMA warp skips two ring tiles at most, which its parity waits
   // bear; the softmax of tile t waits for V_t, which takes the place of K_t (or,
   // split, of K_(t + 1)'s terms) at the latest; a split tile is stored whole
-  static_assert(S >= 3 && (MODE != kSplit || G == 3) && 4 * G * N <= 512 && N * HD * 4 <= (int)(NP * PBYTES), "ring, tensor memory, output rows");
+  static_assert(S >= 3 && (MODE != kSplit || G == 3) && 4 * G * N <= 512 && N * HD * 4 <= (int)PBYTES, "ring, tensor memory, output rows");
 };
 
 // Control block (shared memory).
 template <int N, int S>
 struct TmCtl {
-  unsigned long long full[S], empty[S], s_full[2], s_free[2], p_full[2], p_free[2], q_full[TM_MASKS], q_free, done, v_full[2];
+  unsigned long long full[S], empty[S], s_full[2], s_free[2], p_full, p_free, q_full[TM_MASKS], q_free, done, v_full[2];
   uint32_t tmem;
   int abort_w;
   float base[N], corr[N], sum[N];  // a row's base, the factor of its last rise, its sum of weights
@@ -196,9 +195,9 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(su32(&ctl.s_full[i]), 1);
       mbar_init(su32(&ctl.s_free[i]), 128 * C::SW);
-      mbar_init(su32(&ctl.p_full[i]), 128 * C::SW);
-      mbar_init(su32(&ctl.p_free[i]), 1);
     }
+    mbar_init(su32(&ctl.p_full), 128 * C::SW);
+    mbar_init(su32(&ctl.p_free), 1);
     for (int i = 0; i < TM_MASKS; ++i) mbar_init(su32(&ctl.q_full[i]), TM_QTHREADS);
     mbar_init(su32(&ctl.q_free), 1);
     mbar_init(su32(&ctl.done), 1);
@@ -426,9 +425,9 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
             if (i == m.nt - 1) mma_commit(su32(&ctl.q_free));
           }
           if (i > 0) {  // outputs of tile i - 1
-            const int it = (ic + v_item(i - 1, m.nt)) * C::TERMS, t = tc + i - 1, pb = t % C::NP;
-            ok = tm_wait(su32(&ctl.p_full[pb]), (uint32_t)(t / C::NP) & 1u, abort_w, a.status);
-            const uint32_t pbuf = sbase + C::P + pb * C::PBYTES, d = tmem + C::TM_O + (t & 1) * C::TM_S;
+            const int it = (ic + v_item(i - 1, m.nt)) * C::TERMS, t = tc + i - 1;
+            ok = tm_wait(su32(&ctl.p_full), (uint32_t)t & 1u, abort_w, a.status);
+            const uint32_t pbuf = sbase + C::P, d = tmem + C::TM_O + (t & 1) * C::TM_S;
 #pragma unroll
             for (int term = 0; term < C::TERMS; ++term) {
               const int slot = (it + term) % C::S;
@@ -446,7 +445,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
               mma_commit(su32(&ctl.empty[slot]));
             }
             if (!ok) break;
-            mma_commit(su32(&ctl.p_free[pb]));
+            mma_commit(su32(&ctl.p_free));
           }
         }
         ic += 2 * m.nt;
@@ -523,7 +522,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
         }
       }
       for (int i = 0; i <= m.nt; ++i) {
-        const int t = tc + i, pb = t % C::NP;
+        const int t = tc + i;
         if (i < m.nt) {
         ok = tm_wait(su32(&ctl.s_full[t & 1]), (uint32_t)(t >> 1) & 1u, abort_w, a.status) && ok;
         if (all_any<128 * C::SW>(!ok)) {
@@ -657,8 +656,8 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
           }
           scaled = true;
         }
-        ok = tm_wait(su32(&ctl.p_free[pb]), ((uint32_t)(t / C::NP) & 1u) ^ 1u, abort_w, a.status) && ok;
-        const uint32_t ph = sbase + C::P + pb * C::PBYTES + p_lane;
+        ok = tm_wait(su32(&ctl.p_free), ((uint32_t)t & 1u) ^ 1u, abort_w, a.status) && ok;
+        const uint32_t ph = sbase + C::P + p_lane;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           float2 p[4];
@@ -682,14 +681,12 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
         }
         proxy_fence();
         tc_fence_before();
-        mbar_arrive(su32(&ctl.p_full[pb]));
+        mbar_arrive(su32(&ctl.p_full));
         }
-        // the output of the tile before joins the running one: the tensor cores
-        // have had this tile's softmax to finish it (one P buffer: it was complete
-        // before this tile's P was written, and its barrier may be a phase on)
+        // the output of the tile before joins the running one: it was complete before
+        // this tile's P was written (whose barrier may be a phase on)
         if (i > 0) {
-          if (C::NP > 1 || i == m.nt)
-            ok = tm_wait(su32(&ctl.p_free[(t - 1) % C::NP]), (uint32_t)((t - 1) / C::NP) & 1u, abort_w, a.status) && ok;
+          if (i == m.nt) ok = tm_wait(su32(&ctl.p_free), (uint32_t)(t - 1) & 1u, abort_w, a.status) && ok;
           tc_fence_after();
           const uint32_t src = tmem + C::TM_O + ((t - 1) & 1) * C::TM_S + lanes;
 #pragma unroll
