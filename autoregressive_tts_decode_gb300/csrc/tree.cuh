@@ -7,6 +7,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "ops.cuh"
@@ -143,6 +144,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Infinities and NaN in 16 bytes of bf16: an exponent of ones carries into the sign
+// bit's place (bits 15 and 31 of the result, gathered by or).
+__device__ __forceinline__ uint32_t not_finite(uint4 u, uint32_t found) {
+  found |= (u.x & 0x7f807f80u) + 0x00800080u;
+  found |= (u.y & 0x7f807f80u) + 0x00800080u;
+  found |= (u.z & 0x7f807f80u) + 0x00800080u;
+  return found | ((u.w & 0x7f807f80u) + 0x00800080u);
 }
 // Bounded wait on an mbarrier phase; false on expiry or when another role of
 // the CTA has given up.
@@ -281,13 +290,23 @@ __device__ __forceinline__ bool tma_loads(const CUtensorMap* map, const TreeArgs
   return ok;
 }
 
+// The first item's lengths, row offsets and page ids on their way to the L2 before
+// anything is known that leads to them.
+__device__ __forceinline__ void prefetch_first(const TreeArgs& a, const TmDeal& d) {
+  const int i = threadIdx.x, seq = d.first / d.row_tiles / a.kv.Hkv;
+  if (seq >= a.n_seqs) return;
+  const int* p = i == 0 ? a.lengths + seq : i == 1 ? a.node_start + seq : a.kv.page_table + (size_t)seq * a.kv.pages_per_stream + (i - 2) * 32;
+  if (i < 2 || (i < 32 && (i - 2) * 32 < a.kv.pages_per_stream)) asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // The queries of an item as three bf16 terms (x = their sum), K-major swizzled
-// tiles of N rows, by QT threads: four elements of a row each, eight loads on
-// their way at a time, the first before `ready` says that Q's place is free.
+// tiles of N rows, by QT threads: four elements of a row each, up to sixteen loads
+// on their way at a time, the first before `ready` says that Q's place is free.
 template <int HD, int N, int QT, class Ready>
 __device__ __forceinline__ bool load_queries(const TreeArgs& a, const TmItem& m, int rep, unsigned rep_inv, bool wide, int lane,
                                              uint8_t* dst0, Ready ready) {
-  constexpr int CH = HD / 4, ALL = N * CH / QT, UNITS = 8;
+  constexpr int CH = HD / 4, ALL = N * CH / QT, UNITS = ALL < 16 ? ALL : 16;
+  static_assert(ALL % UNITS == 0, "whole batches");
   constexpr uint32_t TERM = N * 128;
 #pragma unroll 1
   for (int u0 = 0; u0 < ALL; u0 += UNITS) {
@@ -412,13 +431,28 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// CTAs of a cluster (which splits the positions of one item): enough to fill
-// the SMs, no more than there are tiles at the sequences' capacity, at most 8
-// (the portable cluster size).
-inline int cluster_size(long items, int tiles, int n_sm) {
-  int c = 1;
-  while (c < 8 && items * c * 2 <= n_sm && c * 2 <= tiles) c *= 2;
-  return c;
+// What the host keeps of a kernel, for each device.
+struct TmKernel {
+  std::atomic<bool> ready{false};
+  int clusters[9] = {};  // clusters of that many CTAs that run at once
+};
+
+// CTAs of a cluster (which splits the positions of one item), of those that run
+// all at once.  A tile more to a CTA costs about a microsecond (8 nodes over 12
+// tiles: 17.5 us whole, 9.5 in shares), the shares' join two (3 tiles: 8.5 whole,
+// 8.6 in shares), and more CTAs start later (6 tiles of 24 items: 10.9 us with 144,
+// 9.7 with 72): the cheapest by that, in 64ths of a tile.
+inline int cluster_size(long items, int tiles, const TmKernel& k) {
+  int best = 1;
+  long least = 64l * tiles + items;
+  for (int c = 2; c <= 8; ++c) {
+    const long cost = 64l * ((tiles + c - 1) / c) + 128 + items * c;
+    if (items <= k.clusters[c] && cost < least) {
+      best = c;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 // The pool as a matrix of head-dim rows, read one page's rows (at most a tile's)
@@ -438,32 +472,42 @@ inline bool pool_map(const TreeArgs& a, int layers, int box, CUtensorMap* map) {
 // One launch: a cluster for each item whose positions it splits, or a CTA on
 // every SM that works through whole items.
 template <class Kernel>
-int launch_items(Kernel kernel, int threads, size_t smem, bool tma, int tile_rows, const TreeArgs& a, int layers, int n_sm,
-                 cudaStream_t s) {
+int launch_items(Kernel kernel, TmKernel& known, int threads, size_t smem, bool tma, int tile_rows, const TreeArgs& a, int layers,
+                 int n_sm, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  if (!known.ready.load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return Q3TTS_ERR_CUDA;
+    cfg.numAttrs = 1;
+    for (int c = 2; c <= 8; ++c) {
+      cfg.gridDim = dim3(c);
+      at[0].val.clusterDim.x = c;
+      if (cudaOccupancyMaxActiveClusters(&known.clusters[c], kernel, &cfg) != cudaSuccess) return Q3TTS_ERR_CUDA;
+    }
+    known.ready.store(true, std::memory_order_release);
+  }
   const int box = a.kv.page_size < TM_PT ? a.kv.page_size : TM_PT;
   CUtensorMap map = {};
   if (tma && !pool_map(a, layers, box, &map)) return Q3TTS_ERR_CUDA;
   const int row_tiles = (a.max_nodes * (a.Hq / a.kv.Hkv) + tile_rows - 1) / tile_rows;
   const long items = (long)a.n_seqs * a.kv.Hkv * row_tiles;
   const int tiles = (int)(((long)a.kv.pages_per_stream * a.kv.page_size + TM_PT - 1) / TM_PT);
-  const int c = cluster_size(items, tiles, n_sm);
   if (items > 0x7fffffffL / 2) return Q3TTS_ERR_UNSUPPORTED;
+  const int c = cluster_size(items, tiles, known);
   const long grid = c > 1 ? items * c : (items < n_sm ? items : n_sm);
   const int vec = (((uintptr_t)a.q & 15) == 0 && a.ldq % 4 == 0 ? 1 : 0) |  // float4 loads of q, stores of out
                   (((uintptr_t)a.out & 15) == 0 && a.ldo % 4 == 0 ? 2 : 0);
   const unsigned rep = (unsigned)(a.Hq / a.kv.Hkv), rep_inv = (unsigned)(((1ull << 32) + rep - 1) / rep);
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = c;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, map, a, row_tiles, box, (int)items, vec, rep_inv) == cudaSuccess ? Q3TTS_OK
                                                                                                          : Q3TTS_ERR_CUDA;

@@ -94,7 +94,7 @@ struct TmCfg {
 // Control block (shared memory).
 template <int N, int S>
 struct TmCtl {
-  unsigned long long full[S], empty[S], s_full[2], s_free[2], p_full, p_free, q_full[TM_MASKS], q_free, done, v_full[2];
+  unsigned long long full[S], empty[S], s_full[2], s_free[2], p_full, p_free, q_first, q_full[TM_MASKS], q_free, done, v_full[2];
   uint32_t tmem;
   int abort_w;
   float base[N], corr[N], sum[N];  // a row's base, the factor of its last rise, its sum of weights
@@ -187,6 +187,9 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int rep = a.Hq / a.kv.Hkv;
 
+  TmDeal deal{items, row_tiles, N, (int)gridDim.x / CL, (int)blockIdx.x / CL, rank, CL,
+                    nullptr};
+  prefetch_first(a, deal);
   if (tid == 0) {
     for (int i = 0; i < C::S; ++i) {
       mbar_init(su32(&ctl.full[i]), C::FULL);
@@ -199,6 +202,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
     mbar_init(su32(&ctl.p_full), 128 * C::SW);
     mbar_init(su32(&ctl.p_free), 1);
     for (int i = 0; i < TM_MASKS; ++i) mbar_init(su32(&ctl.q_full[i]), TM_QTHREADS);
+    mbar_init(su32(&ctl.q_first), 128 * C::SW);
     mbar_init(su32(&ctl.q_free), 1);
     mbar_init(su32(&ctl.done), 1);
     for (int i = 0; i < 2; ++i) mbar_init(su32(&ctl.v_full[i]), 64 * C::LW);
@@ -213,6 +217,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
   }
   pdl_wait();  // q and the appended keys and values come from the previous kernels
   const bool sorted = items > (int)gridDim.x / CL && a.n_seqs <= TM_SORT;
+  if (sorted) deal.order = ctl.order;
   if (sorted) sort_lengths(a, ctl.len, ctl.order);
   tc_fence_before();
   __syncthreads();
@@ -220,8 +225,11 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
   const uint32_t ring = sbase + C::RING;
 
-  const TmDeal deal{items, row_tiles, N, (int)gridDim.x / CL, (int)blockIdx.x / CL, rank, CL,
-                    sorted ? ctl.order : nullptr};
+  // the queries and masks of the CTA's qi-th item
+  auto q_wait = [&](int qi) -> bool {
+    return qi == 0 ? tm_wait(su32(&ctl.q_first), 0u, abort_w, a.status)
+                   : tm_wait(su32(&ctl.q_full[qi % TM_MASKS]), (uint32_t)((qi - 1) / TM_MASKS) & 1u, abort_w, a.status);
+  };
   TmItem m;
   int have = 0;
   bool ok = true;
@@ -392,7 +400,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
       int ic = 0, tc = 0, qi = 0;  // ring tiles, position tiles and items so far
       for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
         if (have == 0 || m.nt == 0) continue;
-        ok = tm_wait(su32(&ctl.q_full[qi % TM_MASKS]), (uint32_t)(qi / TM_MASKS) & 1u, abort_w, a.status);
+        ok = q_wait(qi);
         tc_fence_after();
         for (int i = 0; i <= m.nt && ok; ++i) {
           if (i < m.nt) {  // scores of tile i
@@ -461,10 +469,10 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
     }
     __syncwarp();
   } else if (warp == C::QUERY_WARP) {
-    // ---- queries and masks of the next item, as soon as the scores of the one before are done
-    int qi = 0;
+    // ---- queries and masks of the items after the first, as soon as the scores of the one before are done
+    int qi = -1;
     for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
-      if (have == 0 || m.nt == 0) continue;
+      if (have == 0 || m.nt == 0 || ++qi == 0) continue;
       constexpr int MK = (N + 31) / 32;
       unsigned long long mask[MK];
 #pragma unroll
@@ -482,7 +490,6 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
       if (!ok) break;
       proxy_fence();
       mbar_arrive(su32(&ctl.q_full[qi % TM_MASKS]));
-      ++qi;
     }
   } else {
     // ---- softmax: group wg has rows c0 .. c0 + NC - 1 of the tile, one thread a position
@@ -500,6 +507,12 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
     int ic = 0, tc = 0, qi = 0;
     for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
       if (have == 0) continue;
+      if (m.nt > 0 && qi == 0) {  // the first item's queries: nothing else to do yet
+        if (tid < N) ctl.mask[0][tid] = tid < m.rows ? a.masks[m.t.row0 + div_rep(m.n0 + tid, rep, rep_inv)] : 0ull;
+        load_queries<HD, N, 128 * C::SW>(a, m, rep, rep_inv, vec & 1, tid, sp + C::Q, [] { return true; });
+        proxy_fence();
+        mbar_arrive(su32(&ctl.q_first));
+      }
       float2 base[NB], l[NB];  // negated base, sum of the weights
       float o[NC];             // element wt of the running output's rows
       bool scaled = false;     // the bases rose with this tile: the outputs before it are still to be scaled
@@ -515,7 +528,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
         ctl.sum[c0 + wt] = 0.f;
       }
       if (m.nt > 0) {  // the item's masks are there
-        ok = tm_wait(su32(&ctl.q_full[qi % TM_MASKS]), (uint32_t)(qi / TM_MASKS) & 1u, abort_w, a.status);
+        ok = q_wait(qi);
         if (all_any<128 * C::SW>(!ok)) {
           ok = false;
           break;
@@ -566,22 +579,18 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
                               : tm_wait(su32(&ctl.full[it % C::S]), (uint32_t)(it / C::S) & 1u, abort_w, a.status);
           if (wg == 0 && ok) {
             uint4* vr = reinterpret_cast<uint4*>(sp + C::RING + it % C::S * C::SLOT + wt * 128);
-            bool mine = false;
+            uint32_t bits = 0;
             if (pos >= m.t.L && pos < m.t.P) {
 #pragma unroll
-              for (int e = 0; e < C::BLK * 8; ++e) {
-                const uint4 u = vr[(e >> 3) * (TM_PT * 8) + (e & 7)];
-                const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-                  mine = mine || (x[h] & 0x7f80u) == 0x7f80u || (x[h] & 0x7f800000u) == 0x7f800000u;
-              }
+              for (int e = 0; e < C::BLK * 8; ++e)
+                bits = not_finite(vr[(e >> 3) * (TM_PT * 8) + ((e ^ lane) & 7)], bits);
             }
+            const bool mine = (bits & 0x80008000u) != 0;
             if (pos >= m.t.P || mine)
               for (int term = 0; term < C::TERMS; ++term) {
                 uint4* z = reinterpret_cast<uint4*>(sp + C::RING + (it + term) % C::S * C::SLOT + wt * 128);
 #pragma unroll 4
-                for (int e = 0; e < C::BLK * 8; ++e) z[(e >> 3) * (TM_PT * 8) + (e & 7)] = make_uint4(0, 0, 0, 0);
+                for (int e = 0; e < C::BLK * 8; ++e) z[(e >> 3) * (TM_PT * 8) + ((e ^ lane) & 7)] = make_uint4(0, 0, 0, 0);
               }
             // positions of the warp whose values are infinite or NaN: a row that sees one is NaN
             const unsigned found = __ballot_sync(0xffffffffu, mine);
@@ -782,14 +791,24 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
 template <int HD, int N, int MODE>
 int launch_mma(const TreeArgs& a, int layers, int dev, int n_sm, cudaStream_t s) {
   using C = TmCfg<HD, N, MODE>;
-  static bool ready[kMaxDevices] = {};  // the attribute is the device's
-  if (!ready[dev]) {
-    if (cudaFuncSetAttribute(tree_mma_kernel<HD, N, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)C::SMEM) != cudaSuccess)
-      return Q3TTS_ERR_CUDA;
-    ready[dev] = true;
-  }
-  return launch_items(tree_mma_kernel<HD, N, MODE>, C::THREADS, C::SMEM, MODE == kTma, N, a, layers, n_sm, s);
+  static TmKernel known[kMaxDevices];
+  return launch_items(tree_mma_kernel<HD, N, MODE>, known[dev], C::THREADS, C::SMEM, MODE == kTma, N, a, layers, n_sm, s);
+}
+
+// Whether tiles of 128 rows (tree_wide.cu) are done sooner than tiles of 64 on
+// twice the CTAs.  A round of items costs about 6 us and 1.3 us for a tile of
+// positions here, 9 and 1.65 us there; 64 nodes with two heads each (tiles of
+// positions: us here, us there): 8 kv heads 1: 9.2, 11.4, 64: 25.2, 27.2; 32 kv
+// heads 8: 16.3, 17.3, 16: 23.3, 21.0; 152 kv heads 1: 18.8, 13.2, 64: 209, 138;
+// 512 kv heads 64: 711, 532.
+bool wide_pays(const TreeArgs& a, int n_sm) {
+  const long rows = (long)a.max_nodes * (a.Hq / a.kv.Hkv), heads = (long)a.n_seqs * a.kv.Hkv;
+  const long tiles = ((long)a.kv.pages_per_stream * a.kv.page_size + TM_PT - 1) / TM_PT;
+  auto us = [&](long items, double item, double tile) {
+    const long rounds = (items + n_sm - 1) / n_sm, most = n_sm / items < 8 ? n_sm / items : 8, share = rounds > 1 ? 1 : most;
+    return rounds * (item + tile * ((tiles + share - 1) / share));
+  };
+  return us(heads * ((rows + 127) / 128), 9, 1.65) < us(heads * ((rows + 63) / 64), 6, 1.3);
 }
 
 template <int HD, int MODE>
@@ -797,7 +816,7 @@ int launch_rows(const TreeArgs& a, int layers, int dev, int n_sm, cudaStream_t s
   const int rows = a.max_nodes * (a.Hq / a.kv.Hkv);
   if (rows <= 16) return launch_mma<HD, 16, MODE>(a, layers, dev, n_sm, s);
   if (rows <= 32 || MODE == kSplit) return launch_mma<HD, 32, MODE>(a, layers, dev, n_sm, s);
-  if (MODE == kTma && rows > 64) return launch_tree_wide(a, layers, dev, n_sm, s);
+  if (MODE == kTma && rows > 64 && wide_pays(a, n_sm)) return launch_tree_wide(a, layers, dev, n_sm, s);
   return launch_mma<HD, MODE == kSplit ? 32 : 64, MODE>(a, layers, dev, n_sm, s);
 }
 

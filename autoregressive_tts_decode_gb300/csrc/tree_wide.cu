@@ -89,6 +89,19 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t tmem_d, uint32_t a, uint64_
       : "memory");
 }
 
+// Lanes `away` apart exchange b of the lower for a of the upper.
+__device__ __forceinline__ void exchange(float4& a, float4& b, bool upper, int away) {
+  const float4 give = upper ? a : b;
+  float4 take;
+  take.x = __shfl_xor_sync(0xffffffffu, give.x, away);
+  take.y = __shfl_xor_sync(0xffffffffu, give.y, away);
+  take.z = __shfl_xor_sync(0xffffffffu, give.z, away);
+  take.w = __shfl_xor_sync(0xffffffffu, give.w, away);
+  if (upper)
+    a = take;
+  else
+    b = take;
+}
 // Barrier and vote of the softmax threads.
 __device__ __forceinline__ bool vote(bool p, int id) {
   uint32_t r;
@@ -118,6 +131,9 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int rep = a.Hq / a.kv.Hkv;
 
+  TmDeal deal{items, row_tiles, TW_ROWS, (int)gridDim.x / CL, (int)blockIdx.x / CL, rank, CL,
+                    nullptr};
+  prefetch_first(a, deal);
   if (tid == 0) {
     for (int i = 0; i < C::S; ++i) {
       mbar_init(su32(&ctl.full[i]), 1);
@@ -139,6 +155,7 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
   }
   pdl_wait();  // q and the appended keys and values come from the previous kernels
   const bool sorted = items > (int)gridDim.x / CL && a.n_seqs <= TM_SORT;
+  if (sorted) deal.order = ctl.order;
   if (sorted) sort_lengths(a, reinterpret_cast<int*>(ctl.part), ctl.order);
   tc_fence_before();
   __syncthreads();
@@ -147,8 +164,6 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
   const uint32_t ring = sbase + C::RING;
   float* shares = reinterpret_cast<float*>(sp);  // bases and sums for the other shares of the item, factors; in Q's place
 
-  const TmDeal deal{items, row_tiles, TW_ROWS, (int)gridDim.x / CL, (int)blockIdx.x / CL, rank, CL,
-                    sorted ? ctl.order : nullptr};
   TmItem m;
   int have = 0;
   bool ok = true;
@@ -262,20 +277,15 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
             ok = tm_wait(su32(&ctl.full[it % C::S]), (uint32_t)(it / C::S) & 1u, abort_w, a.status) && ok;
             if (wg == 0) {
               uint4* vr = reinterpret_cast<uint4*>(sp + C::RING + it % C::S * C::SLOT + r * 128);
-              bool mine = false;
+              uint32_t bits = 0;
               if (ok && pos >= m.t.L && pos < m.t.P) {
-#pragma unroll 4
-                for (int e = 0; e < C::BLK * 8; ++e) {
-                  const uint4 u = vr[(e >> 3) * (TM_PT * 8) + (e & 7)];
-                  const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                  for (int h = 0; h < 4; ++h)
-                    mine = mine || (x[h] & 0x7f80u) == 0x7f80u || (x[h] & 0x7f800000u) == 0x7f800000u;
-                }
+                for (int e = 0; e < C::BLK * 8; ++e) bits = not_finite(vr[(e >> 3) * (TM_PT * 8) + ((e ^ lane) & 7)], bits);
               }
+              const bool mine = (bits & 0x80008000u) != 0;
               if (ok && (pos >= m.t.P || mine)) {
 #pragma unroll 4
-                for (int e = 0; e < C::BLK * 8; ++e) vr[(e >> 3) * (TM_PT * 8) + (e & 7)] = make_uint4(0, 0, 0, 0);
+                for (int e = 0; e < C::BLK * 8; ++e) vr[(e >> 3) * (TM_PT * 8) + ((e ^ lane) & 7)] = make_uint4(0, 0, 0, 0);
                 proxy_fence();
               }
               // positions whose values are infinite or NaN: a row that sees one is NaN
@@ -294,16 +304,13 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
           auto take = [&](int ch, float (&x)[32]) {
             tmem_ld32(src + 32 * ch, x);
             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-            if (edge) {
-              const int d = p0 + 32 * ch - m.t.L;  // its first position, counted from the first node
-              const uint32_t sees = d >= 64    ? 0u
-                                    : d >= 0   ? (uint32_t)(mask >> d)
-                                    : d <= -32 ? 0xffffffffu
-                                               : (uint32_t)(mask << -d) | ((1u << -d) - 1);
-              const uint32_t bad = ctl.bad[t & 1][ch];
+            const int d = p0 + 32 * ch - m.t.L;  // its first position, counted from the first node
+            if (d > -32) {
+              const uint32_t sees = d >= 64 ? 0u : d >= 0 ? (uint32_t)(mask >> d) : (uint32_t)(mask << -d) | ((1u << -d) - 1);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                x[e] = (sees >> e) & 1u ? ((bad >> e) & 1u ? __uint_as_float(0x7fc00000u) : x[e]) : -INFINITY;
+              for (int e = 0; e < 32; ++e) x[e] = (sees >> e) & 1u ? x[e] : -INFINITY;
+              const uint32_t bad = ctl.bad[t & 1][ch];
+              if (bad & sees) x[0] = __uint_as_float(0x7fc00000u);
             }
           };
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -404,18 +411,33 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
           *reinterpret_cast<float4*>(os + n) = make_float4(o[n / 2].x, o[n / 2].y, o[n / 2 + 1].x, o[n / 2 + 1].y);
         break;
       }
-      if (r < m.rows) {
-        const float f = l == 0.f ? 0.f : 1.f / l;  // a row that saw nothing: zeroes
-        float* dst = a.out + (size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + row - node * rep) * HD + wg * HW;
-        if (vec & 2) {
+      // four lanes exchange quarters of their rows, so that they write 64 bytes of one
+      // row after the other
+      const float f = l == 0.f ? 0.f : 1.f / l;  // a row that saw nothing: zeroes
 #pragma unroll
-          for (int n = 0; n < HW; n += 4)
-            *reinterpret_cast<float4*>(dst + n) = make_float4(o[n / 2].x * f, o[n / 2].y * f, o[n / 2 + 1].x * f, o[n / 2 + 1].y * f);
-        } else {
+      for (int n = 0; n < HW; n += 16) {
+        float4 v[4];
 #pragma unroll
-          for (int n = 0; n < HW; n += 2) {
-            dst[n] = o[n / 2].x * f;
-            dst[n + 1] = o[n / 2].y * f;
+        for (int q = 0; q < 4; ++q)
+          v[q] = make_float4(o[n / 2 + 2 * q].x * f, o[n / 2 + 2 * q].y * f, o[n / 2 + 2 * q + 1].x * f, o[n / 2 + 2 * q + 1].y * f);
+        exchange(v[0], v[1], lane & 1, 1);
+        exchange(v[2], v[3], lane & 1, 1);
+        exchange(v[0], v[2], lane & 2, 2);
+        exchange(v[1], v[3], lane & 2, 2);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r4 = (r & ~3) + q, row4 = m.n0 + r4, node4 = div_rep(row4, rep, rep_inv);
+          float* dst = a.out + (size_t)(m.t.row0 + node4) * a.ldo + (size_t)(m.g * rep + row4 - node4 * rep) * HD + wg * HW + n +
+                       (lane & 3) * 4;
+          if (r4 < m.rows) {
+            if (vec & 2) {
+              *reinterpret_cast<float4*>(dst) = v[q];
+            } else {
+              dst[0] = v[q].x;
+              dst[1] = v[q].y;
+              dst[2] = v[q].z;
+              dst[3] = v[q].w;
+            }
           }
         }
       }
@@ -433,13 +455,8 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
 template <int HD>
 int launch_wide(const TreeArgs& a, int layers, int dev, int n_sm, cudaStream_t s) {
   using C = TwCfg<HD>;
-  static bool ready[kMaxDevices] = {};  // the attribute is the device's
-  if (!ready[dev]) {
-    if (cudaFuncSetAttribute(tree_wide_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
-      return Q3TTS_ERR_CUDA;
-    ready[dev] = true;
-  }
-  return launch_items(tree_wide_kernel<HD>, C::THREADS, C::SMEM, true, TW_ROWS, a, layers, n_sm, s);
+  static TmKernel known[kMaxDevices];
+  return launch_items(tree_wide_kernel<HD>, known[dev], C::THREADS, C::SMEM, true, TW_ROWS, a, layers, n_sm, s);
 }
 
 }  // namespace

@@ -53,15 +53,16 @@ TREES = [
     ([300], [20], 12, 3, 128, 32), ([129], [5], 4, 2, 64, 64), ([511], [40], 4, 4, 64, 128),
     ([600], [13], 4, 2, 128, 256), ([70], [64], 16, 1, 64, 16), ([45], [6], 2, 1, 128, 1),
     ([2048], [16], 16, 8, 128, 16), ([5000, 1], [3, 3], 2, 1, 64, 16), ([333], [17], 10, 2, 128, 24),
-    # more than 64 rows to a kv head
-    ([9000], [64], 4, 2, 128, 16), ([700, 3, 0, 260], [64, 33, 40, 0], 16, 2, 128, 16), ([500, 129], [64, 50], 8, 2, 64, 32),
-    ([300], [33], 2, 1, 128, 128), ([127, 64, 0], [64, 64, 64], 2, 1, 128, 8), ([383], [22], 3, 1, 64, 256),
-    ([0], [5], 16, 1, 128, 64),
+    # more than 64 rows to a kv head: few heads and sequences, then many
+    ([9000], [64], 4, 2, 128, 16), ([960, 3, 0], [64, 33, 40], 16, 2, 128, 16), ([383], [22], 3, 1, 64, 256),
+    ([9000, 0, 700, 5000] * 4, [64, 40, 33, 1] * 4, 4, 2, 128, 16), ([383] * 19, [22] * 19, 24, 8, 64, 256),
+    ([127, 64, 0, 200] * 20, [64, 64, 64, 10] * 20, 4, 2, 128, 8), ([700, 3, 0, 260] * 3, [64, 33, 40, 0] * 3, 16, 2, 128, 16),
+    ([500, 129] * 12, [64, 50] * 12, 8, 2, 64, 32), ([300, 0] * 40, [33, 5] * 40, 4, 2, 128, 128),
 ]
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
-@pytest.mark.parametrize("case", TREES, ids=lambda c: "-".join(str(x) for x in c).replace(" ", ""))
+@pytest.mark.parametrize("case", TREES, ids=lambda c: "-".join(str(x) for x in c).replace(" ", "")[:60])
 def test_tree_attention(q3, case, dtype):
     import torch
     c = tree_case(np.random.default_rng(7), *case, dtype=getattr(torch, dtype))
@@ -89,12 +90,12 @@ def test_tree_attention_many_sequences(q3, dtype, seqs, longest, most, heads, kv
     assert int(status) == 0 and torch.equal(out, run_tree(q3, c))
 
 
-@pytest.mark.parametrize("heads", [4, 32])
-def test_chain_and_masks_that_see_nothing(q3, heads):
+@pytest.mark.parametrize("heads,kv_heads", [(4, 2), (600, 100)])
+def test_chain_and_masks_that_see_nothing(q3, heads, kv_heads):
     """A chain is causal attention; a mask of zeroes sees the context only, and
     without a context nothing: zeroes, whatever the cache holds."""
     import torch
-    c = tree_case(np.random.default_rng(9), [40, 0, 0], [12, 4, 5], heads, 2, 128, 16, torch.bfloat16,
+    c = tree_case(np.random.default_rng(9), [40, 0, 0], [12, 4, 5], heads, kv_heads, 128, 16, torch.bfloat16,
                   parents=[list(range(-1, 11)), [-1, 0, 1, 2], [-1] * 5])
     c["masks"][12 + 2] = 0
     c["masks"][3] = 0
@@ -103,13 +104,13 @@ def test_chain_and_masks_that_see_nothing(q3, heads):
     assert bool((out[12 + 2] == 0).all())
 
 
-@pytest.mark.parametrize("heads", [4, 32])
+@pytest.mark.parametrize("heads,kv_heads", [(4, 2), (1920, 160)])
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
-def test_large_scores_and_masked_infinities(q3, dtype, heads):
+def test_large_scores_and_masked_infinities(q3, dtype, heads, kv_heads):
     """Scores hundreds apart, rising along the context; infinities and NaN at
     nodes that no mask shows."""
     import torch
-    c = tree_case(np.random.default_rng(10), [400], [6], heads, 2, 128, 16, getattr(torch, dtype),
+    c = tree_case(np.random.default_rng(10), [400], [6], heads, kv_heads, 128, 16, getattr(torch, dtype),
                   parents=[[-1, 0, -1, 2, -1, 4]])
     pos = torch.arange(406, device="cuda")
     pg, slot = c["table"][0].long()[pos // 16], pos % 16
@@ -129,12 +130,12 @@ def test_large_scores_and_masked_infinities(q3, dtype, heads):
     assert bool(((out.double() - want).abs() <= tol).all())
 
 
-@pytest.mark.parametrize("heads", [4, 40])
-def test_row_pitches_and_rows_left_alone(q3, heads):
+@pytest.mark.parametrize("heads,kv_heads", [(4, 2), (800, 80)])
+def test_row_pitches_and_rows_left_alone(q3, heads, kv_heads):
     """q inside a wider buffer at an odd pitch, out likewise; rows behind the last
     sequence and other columns keep their values."""
     import torch
-    c = tree_case(np.random.default_rng(11), [33, 90], [5, 7], heads, 2, 64, 16, torch.bfloat16)
+    c = tree_case(np.random.default_rng(11), [33, 90], [5, 7], heads, kv_heads, 64, 16, torch.bfloat16)
     wide = torch.full((15, heads * 64 + 37), 3.25, device="cuda")
     wide[:12, 1:heads * 64 + 1] = c["q"].reshape(12, -1)
     qv = wide[:, 1:heads * 64 + 1].unflatten(1, (heads, 64))
@@ -146,12 +147,13 @@ def test_row_pitches_and_rows_left_alone(q3, heads):
     assert bool((outw[12:] == -7.5).all()) and bool((outw[:, :3] == -7.5).all())
 
 
+@pytest.mark.parametrize("heads,kv_heads", [(4, 2), (1440, 60)])
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
-def test_bad_device_entries_are_reported(q3, dtype):
+def test_bad_device_entries_are_reported(q3, dtype, heads, kv_heads):
     """Lengths, row offsets and page ids that do not fit: reported, the others'
     rows are right, and the left-out rows keep their values."""
     import torch
-    c = tree_case(np.random.default_rng(12), [20, 30, 40], [3, 3, 3], 4, 2, 64, 16, getattr(torch, dtype))
+    c = tree_case(np.random.default_rng(12), [20, 30, 40], [3, 3, 3], heads, kv_heads, 64, 16, getattr(torch, dtype))
     for change in ("length", "negative", "start", "page"):
         lengths, start, table = c["lengths"].clone(), c["start"].clone(), c["table"].clone()
         if change == "length":
