@@ -33,14 +33,29 @@
 // truncate as they accumulate, and summed in tensor memory over 32768 positions
 // the error was 3.7e-5 of the output.
 //
-// Roles of a CTA (one per SM): one warp issues the TMA loads into a ring of K
-// and V tiles, one thread the MMAs (scores of tile t + 1 before the outputs of
-// tile t), four warps are the softmax and two bring in the queries.  A CTA works
-// through several items (sequence, kv head, tile of rows) and the roles run
-// ahead into the next one, so only the first pays the latency of its start.
-// Items are dealt longest first, in rounds of alternating direction: on 128
-// sequences of 256..2048 positions the SMs then end together.
-// The bound is the cache's bytes, read once for up to 64 rows.
+// Roles of a CTA (one per SM): two or four warps bring the keys and values into a
+// ring of tiles, one thread issues the MMAs (scores of tile t + 1 before the
+// outputs of tile t), one warp brings in the queries of the items after the
+// first, and four warps are the softmax (eight, each four with half of the rows,
+// for tiles of 64).  A CTA works through several items (sequence, kv head, tile of
+// rows) and the roles run ahead into the next one, so only the first pays the
+// latency of its start.  Items are dealt longest first, in rounds of alternating
+// direction: on 128 sequences of 256..2048 positions the SMs then end together.
+// Few items are split over the positions in clusters, whose CTAs join their shares
+// through each other's shared memory.
+//
+// How the cache is read follows its type and page size.  bf16 pages that TMA boxes
+// fit come in whole boxes; other page sizes row by row, in 16-byte asynchronous
+// copies (128 sequences of 1000 positions, 8 nodes: 88 us in boxes, 104 in rows);
+// fp32 rows are loaded, split into three bf16 terms on the way and multiplied term
+// by term.  Tiles have the smallest of 16, 32 and 64 rows that hold a sequence's
+// (there, 16 rows in tiles of 16, 32 or 64: 88, 97, 126 us; 32 rows in tiles of 32
+// or 64: 101, 130).
+//
+// The bound is the cache's bytes, read once for up to 64 rows: 128 sequences of
+// 256..2048 positions, 16 nodes with two heads each: 118 us, 5.5 TB/s.  Short
+// calls are bound by latency (the launch, the chain from lengths to page ids to
+// first rows, a tile's way through the tensor cores): 131 positions, 8 nodes: 7.5 us.
 // Every wait is bounded; on expiry the CTA records Q3TTS_ERR_TIMEOUT, waits
 // (bounded) for its copies and MMAs in flight, frees its tensor memory and
 // writes nothing more.
@@ -209,13 +224,14 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
     ctl.abort_w = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  pdl_wait();  // q and the appended keys and values come from the previous kernels
+  // (tensor memory after the wait: a kernel before may still be about to take its own)
   if (warp == C::MMA_WARP) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&ctl.tmem)),
                  "r"(C::TMEM_COLS)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  pdl_wait();  // q and the appended keys and values come from the previous kernels
   const bool sorted = items > (int)gridDim.x / CL && a.n_seqs <= TM_SORT;
   if (sorted) deal.order = ctl.order;
   if (sorted) sort_lengths(a, ctl.len, ctl.order);

@@ -23,7 +23,10 @@
 // tile t + 1 wait for its P, which the softmax announces when it has also read
 // the outputs of tile t.
 //
-// The bound is the tensor cores' time for six products of 128 x 128 x 128 a tile.
+// The bound is the tensor cores' time for six products of 128 x 128 x 128 a tile:
+// four sequences of 30011 .. 32768 positions, 64 nodes with two heads each: 127 us
+// (tiles of 64 rows: 230), of which the products alone take 99 on the 128 SMs that
+// 32 items in clusters of four fill.
 #include "tree.cuh"
 
 namespace q3 {
@@ -149,11 +152,12 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
     ctl.abort_w = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  pdl_wait();  // q and the appended keys and values come from the previous kernels
+  // (tensor memory after the wait: a kernel before may still be about to take its own)
   if (warp == C::MMA_WARP) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&ctl.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  pdl_wait();  // q and the appended keys and values come from the previous kernels
   const bool sorted = items > (int)gridDim.x / CL && a.n_seqs <= TM_SORT;
   if (sorted) deal.order = ctl.order;
   if (sorted) sort_lengths(a, reinterpret_cast<int*>(ctl.part), ctl.order);

@@ -235,7 +235,7 @@ def _pitch(t, rows: int, heads: int, hd: int, name: str, what: str) -> int:
     if t.is_contiguous():
         return heads * hd
     n, h, d = t.stride()
-    if (heads > 1 and h != hd) or d != 1 or (rows > 1 and n < heads * hd):
+    if (heads > 1 and h != hd) or d != 1 or (rows > 1 and not heads * hd <= n < 1 << 31):
         _bad(what, name, "[rows, heads, head dim] with contiguous rows")
     return n if rows > 1 else heads * hd
 
@@ -316,9 +316,15 @@ def compact_rows(pool, page_table, lengths, path, path_len, status=None):
     return pool
 
 
-def beam_workspace_size(groups: int, beams: int, vocab: int, k: int) -> int:
-    """Bytes of workspace beam_select uses for this shape on the current device."""
-    return int(load().q3tts_beam_workspace_size(groups, beams, vocab, k))
+def beam_workspace_size(groups: int, beams: int, vocab: int, k: int, device: Optional[int] = None) -> int:
+    """Bytes of workspace beam_select uses for this shape on the CUDA device of that
+    index (default: the current one)."""
+    from torch import _C
+    if device is None or device == _C._cuda_getDevice():
+        return int(load().q3tts_beam_workspace_size(groups, beams, vocab, k))
+    import torch
+    with torch.cuda.device(device):
+        return int(load().q3tts_beam_workspace_size(groups, beams, vocab, k))
 
 
 def beam_select(logits, scores, k: Optional[int] = None, row_ids=None, finished=None, history=None,
@@ -362,7 +368,7 @@ def beam_select(logits, scores, k: Optional[int] = None, row_ids=None, finished=
         p_out = (_cuda(tokens, "out[0]", i32, dev, groups * k, what), _cuda(parents, "out[1]", i32, dev, groups * k, what),
                  _cuda(best, "out[2]", torch.float32, dev, groups * k, what))
     if workspace is None:
-        workspace = torch.empty(beam_workspace_size(groups, beams, vocab, k), dtype=torch.uint8, device=logits.device)
+        workspace = torch.empty(beam_workspace_size(groups, beams, vocab, k, dev), dtype=torch.uint8, device=logits.device)
     n_ws = workspace.numel()
     p_ws = _cuda(workspace, "workspace", torch.uint8, dev, n_ws, what)
     _call(dev, load().q3tts_beam_select, what, logits.data_ptr(), ld,

@@ -93,7 +93,8 @@ int q3tts_beam_frame(q3tts_handle* h, const q3tts_sampling* params, const int32_
  * status_dev, where a call has it, is NULL or a device int32: what can only be
  * checked on the device (lengths, paths, page ids, parents) and is wrong is
  * left out, and Q3TTS_ERR_ARG put there unless it already holds a code; the
- * caller clears it. */
+ * caller clears it.  Q3TTS_ERR_TIMEOUT there: the attention gave up a wait
+ * inside a kernel; its output is unspecified. */
 
 /* A paged cache: pool is device memory, 16-byte aligned, of
  * [layers][n_pages][k|v][n_kv_heads][page_size][head_dim] elements of kv_dtype
@@ -125,7 +126,8 @@ typedef struct q3tts_kv_cache {
  * Caches of up to 2^31 rows of head_dim elements in all (else
  * Q3TTS_ERR_UNSUPPORTED).
  * Rows outside every sequence's range are left as they were, like the rows of
- * a sequence whose entries do not fit (reported in status_dev).  out may not
+ * a sequence whose length or offsets do not fit; page ids outside the pool leave
+ * the sequence's rows unspecified (both reported in status_dev).  out may not
  * overlap q.  Accumulation in fp32; a row's result does not depend on the run,
  * but may on n_seqs and max_nodes, which decide how positions are split. */
 int q3tts_tree_attention(const q3tts_kv_cache* kv, int layer, const int32_t* page_table_dev, int pages_per_seq,

@@ -2,6 +2,7 @@
 against streams that were prefilled and stepped one by one."""
 import ctypes as C
 import dataclasses
+import math
 
 import numpy as np
 import pytest
@@ -276,6 +277,51 @@ def test_accepted_path_becomes_the_context(q3, weights, oracle_mod, kind, path):
     for f in range(1, 5):
         frame_like(a, b, [0], sp, f, history, oracle_mod, TOL[kind])
         assert np.max(np.abs(pending(a, 0)[1] - pending(b, 0)[1])) <= TOL[kind]
+    a.close(), b.close()
+
+
+@pytest.mark.parametrize("then", ["frame", "static", "fork", "beam", "prefill", "reset", "tree"])
+def test_a_tree_that_no_path_is_taken_of(q3, weights, then):
+    """A drafted tree leaves its stream as it was for whatever comes next, and is
+    gone once that call has changed the stream."""
+    import torch
+    parents = [-1] + [0] * 39
+    codes = torch.from_numpy(random_codes(np.random.default_rng(4), len(parents))).cuda()
+    a, b = (engine(q3, weights, "f32", 2, cap=96) for _ in range(2))
+    for e in (a, b):
+        e.prefill(0, prompt(41))
+        e.prefill(1, prompt(30, seed=2))
+    a.tree_step(0, codes, parents)
+    for e in (a, b):
+        u, c = torch.full((1, 16), 0.5, device="cuda"), torch.zeros((1, 16), dtype=torch.int32, device="cuda")
+        if then == "frame":
+            frame(e, [0], GREEDY, 0)
+        elif then == "static":
+            e.step_frame_static(0, GREEDY, u, c)
+        elif then == "fork":
+            e.fork(0, [1])
+        elif then == "beam":
+            e.beam_frame([[0, 1]], GREEDY, torch.tensor([[0.0, -math.inf]], device="cuda"), u.repeat(2, 1), c.repeat(2, 1))
+        elif then == "prefill":
+            e.prefill(0, prompt(20, seed=5))
+        elif then == "reset":
+            e.reset(0)
+            e.prefill(0, prompt(33, seed=6))
+        else:
+            hid = torch.zeros((3, TINY.talker_hidden), device="cuda")
+            e.tree_step(0, codes[5:8].contiguous(), [-1, 0, 1], hidden=hid)
+            e.tree_accept(0, [0, 1])
+        e.sync()
+    if then != "fork":
+        with pytest.raises(q3.Q3TTSError) as err:
+            a.tree_accept(0, [0])
+        assert err.value.code == q3.ERR_STATE
+    for f in range(1, 3):
+        for s in (0, 1):
+            frame(a, [s], GREEDY, f, forced=frame(b, [s], GREEDY, f))
+            assert a.length(s) == b.length(s)
+            for x, y in zip(pending(a, s), pending(b, s)):
+                assert np.max(np.abs(x - y)) <= TOL["f32"] * 5
     a.close(), b.close()
 
 

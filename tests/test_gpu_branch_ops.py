@@ -178,11 +178,12 @@ def test_bad_device_entries_are_reported(q3, dtype, heads, kv_heads):
             assert bool((out[bad] == -7.5).all())
 
 
-def test_tree_attention_repeats_captures_and_follows_new_lengths(q3):
+@pytest.mark.parametrize("heads,kv_heads", [(16, 8), (800, 100)])
+def test_tree_attention_repeats_captures_and_follows_new_lengths(q3, heads, kv_heads):
     """The same bits on every run; a captured call replays with other lengths and
     masks; two graphs of it replay side by side on two streams."""
     import torch
-    c = tree_case(np.random.default_rng(13), [250, 61], [9, 4], 16, 8, 128, 16, torch.bfloat16)
+    c = tree_case(np.random.default_rng(13), [250, 61], [9, 4], heads, kv_heads, 128, 16, torch.bfloat16)
     masks = bu.masks_tensor(c["masks"])
     first = run_tree(q3, c)
     assert torch.equal(first, run_tree(q3, c))
@@ -207,6 +208,58 @@ def test_tree_attention_repeats_captures_and_follows_new_lengths(q3):
     graphs[0].replay()
     torch.cuda.synchronize()
     check_tree(c, outs[0])
+
+
+FIRST_CALLS = """
+import torch
+from autoregressive_tts_decode_gb300 import q3tts
+from tests import branch_util as bu
+import numpy as np
+rng = np.random.default_rng(15)
+pool, table = bu.paged_cache(rng, [1030] * 8, 16, 2, 8, 128, torch.bfloat16)
+i32 = dict(dtype=torch.int32, device="cuda")
+lengths, start = torch.full((8,), 1000, **i32), torch.arange(9, **i32) * 30
+masks = bu.masks_tensor(sum((bu.tree_masks(bu.tree_parents(rng, 30)) for _ in range(8)), []))
+q = torch.randn((240, 32, 128), device="cuda")
+logits, scores = torch.randn((2, 4, 9000), device="cuda"), torch.zeros((2, 4), device="cuda")
+path, count = torch.tensor([[1, 3]] * 8, **i32), torch.full((8,), 2, **i32)
+torch.cuda.synchronize()
+kept = pool.clone()
+
+def calls():
+    out = q3tts.tree_attention(pool, 1, table, lengths, start, masks, q, max_nodes=30)
+    few = q3tts.tree_attention(pool, 0, table, lengths, start, masks, q[:, :8].contiguous(), max_nodes=30)
+    picks = q3tts.beam_select(logits, scores)
+    moved = torch.empty_like(logits)
+    q3tts.reorder_rows([logits], [moved], picks[1])
+    q3tts.copy_pages(pool, [0], [pool.shape[1] - 1])
+    q3tts.compact_rows(pool, table, lengths, path, count)
+    return out, few, *picks, moved
+
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = calls()
+bits = lambda x: x.view(torch.int16)  # (unused places hold NaN)
+assert torch.equal(bits(pool), bits(kept))  # nothing ran yet
+g.replay()
+torch.cuda.synchronize()
+after, got = pool.clone(), [x.clone() for x in got]
+pool.copy_(kept)
+for a, b in zip(got, calls()):
+    assert torch.equal(a, b)
+assert torch.equal(bits(after), bits(pool))
+print("same")
+"""
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first call of each operator is a captured one."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 def test_cache_offsets_past_32_bits(q3):
