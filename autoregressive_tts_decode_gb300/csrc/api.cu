@@ -146,7 +146,7 @@ size_t carve(const q3tts_config& c, void* base, q3tts_handle* h) {
   int32_t* beam_tokens = cv.take<int32_t>(d.S);
   int32_t* beam_parents = cv.take<int32_t>(d.S);
   float* beam_scores = cv.take<float>(d.S);
-  char* beam_ws = cv.take<char>(q3::beam_workspace(1, 1, 1, 1) * d.S);
+  char* beam_ws = cv.take<char>(q3::beam_workspace(1, Q3TTS_MAX_BEAMS, 1, 1) / Q3TTS_MAX_BEAMS * d.S);
   if (h) {
     h->tree_codes = tree_codes; h->tree_h = tree_h; h->tree_logits = tree_logits;
     h->tree_masks = tree_masks; h->tree_meta = tree_meta;

@@ -16,14 +16,19 @@
 // (first the k-th largest maximum of 32 groups of threads, then, whenever the
 // buffer fills, the k-th best itself), so most tiles of a long row need one
 // barrier and no selection at all.  A CTA scans a row, or a piece of a long one
-// where there are few, and leaves its maximum, sum and list in the workspace; a
-// second kernel joins a group's.  (Joining in a cluster of 16 CTAs, through
-// distributed shared memory, took one launch but 47 us for 8 groups of 16 beams
-// over 131072 codes: no more than 7 such clusters run at once, or their CTAs
-// share SMs.)
+// where there are few.  Up to eight whole rows of a group are a cluster, whose
+// first CTA joins their maxima, sums and lists through distributed shared memory;
+// otherwise they are left in a workspace and a second kernel joins a group's.
+// (Clusters of 16 for 8 groups of 16 beams over 131072 codes took 47 us, against
+// 29 in two kernels: no more than 7 such clusters run at once, or their CTAs share
+// SMs.)
 // The GPU's fp64 rate is low: a row's log sum is computed in fp64, a candidate's
 // score as a sum of two floats, and compared as an ordered integer.
+#include <cooperative_groups.h>
+
 #include "ops.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace q3 {
 
@@ -35,6 +40,7 @@ constexpr int BM_TILE = BM_THREADS * BM_PER;     // logits of a tile
 constexpr int BM_MAXK = 32;                      // candidates kept
 constexpr int BM_MAXB = 32;                      // beams of a group
 constexpr int BM_LISTS = 128;                    // lists (rows or pieces of rows) of a group at most
+constexpr int BM_GROUP = 8;                      // beams of a group that a cluster takes (the portable size)
 constexpr int BM_FULL = 256;                     // buffered candidates that call for a selection
 constexpr int BM_CAND = BM_FULL + BM_TILE;       // a tile adds all of its logits at most
 static_assert(BM_LISTS >= BM_MAXB, "a list for every beam");
@@ -337,25 +343,29 @@ __device__ __forceinline__ void scan_piece(BeamSmem& sm, Piece& out, const BeamA
   }
 }
 
+// Codes from v0 on of row gb (a finished beam: its one candidate, where they start).
 template <bool HIST>
-__global__ void __launch_bounds__(BM_THREADS, 2) beam_scan_kernel(BeamArgs a, int pieces, int piece_len, Piece* ws) {
-  extern __shared__ __align__(16) uint8_t bm_raw[];
-  BeamSmem& sm = *reinterpret_cast<BeamSmem*>(bm_raw);
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, gb = blockIdx.x / pieces, piece = blockIdx.x % pieces;
-  const int row = a.row_ids ? a.row_ids[gb] : gb;
-  Piece& out = ws[blockIdx.x];
-  if (a.finished && a.finished[row]) {  // one candidate, from the first piece
-    if (tid < a.k) out.list[tid] = piece == 0 && tid == 0 ? make_key(0.f, a.eos) : 0;
+__device__ __forceinline__ void scan_row(BeamSmem& sm, Piece& out, const BeamArgs& a, int gb, int v0, int len) {
+  const int row = a.row_ids ? a.row_ids[gb] : gb, tid = threadIdx.x;
+  if (a.finished && a.finished[row]) {
+    if (tid < a.k) out.list[tid] = v0 == 0 && tid == 0 ? make_key(0.f, a.eos) : 0;
     if (tid == 0) {
       out.mx = 0.f;
-      out.sum = piece == 0 ? 1.f : 0.f;
+      out.sum = v0 == 0 ? 1.f : 0.f;
     }
     return;
   }
-  const int v0 = piece * piece_len, v1 = min(a.vocab, v0 + piece_len);
-  scan_piece<HIST>(sm, out, a, a.logits + (size_t)row * a.ld, HIST ? a.history + (size_t)row * a.vocab : nullptr, v0, v1);
+  scan_piece<HIST>(sm, out, a, a.logits + (size_t)row * a.ld, HIST ? a.history + (size_t)row * a.vocab : nullptr, v0,
+                   min(a.vocab, v0 + len));
+}
+
+template <bool HIST>
+__global__ void __launch_bounds__(BM_THREADS, 2) beam_scan_kernel(BeamArgs a, int pieces, int piece_len, Piece* ws) {
+  extern __shared__ __align__(16) uint8_t bm_raw[];
+  pdl_wait();
+  pdl_trigger();
+  scan_row<HIST>(*reinterpret_cast<BeamSmem*>(bm_raw), ws[blockIdx.x], a, blockIdx.x / pieces,
+                 (int)(blockIdx.x % pieces) * piece_len, piece_len);
 }
 
 // Natural logarithm of a positive normal number to about 1e-10: x = 2^e m with m
@@ -405,32 +415,31 @@ __device__ __forceinline__ u64 score_key(float hi, float lo, float x, float mx) 
 // The score of a key, rounded once.
 __device__ __forceinline__ float score_of(u64 k) { return key_value(k) + key_value(k << 32); }
 
-// Joins a group's lists: every entry's score, a bound that the k
-// best are at or above (as in the scan), and the order of what passes it.  Lane
-// i of a warp holds entry i of its lists.
-__global__ void __launch_bounds__(BM_THREADS) beam_join_kernel(BeamArgs a, int pieces, const Piece* ws) {
-  extern __shared__ __align__(16) uint8_t bm_raw[];
-  JoinSmem& jn = *reinterpret_cast<JoinSmem*>(bm_raw);
-  constexpr int PER = BM_LISTS / BM_WARPS;  // lists of a warp
-  pdl_wait();
-  pdl_trigger();
-  const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
-  const Piece* pc = ws + (size_t)g * a.beams * pieces;
+// Joins group g's lists, at most LISTS (list(u): the u-th, piece by piece of beam by
+// beam): every entry's score, a bound that the k best are at or above (as in the
+// scan), and the order of what passes it.  Lane i of a warp holds entry i of its
+// lists.
+template <int LISTS, class List>
+__device__ __forceinline__ void join_lists(JoinSmem& jn, const BeamArgs& a, int g, int pieces, List list) {
+  constexpr int PER = LISTS / BM_WARPS;  // lists of a warp
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
   const int lists = a.beams * pieces;
   u64 key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int u = warp + i * BM_WARPS;
-    key[i] = u < lists && lane < k ? pc[u].list[lane] : 0;
+    key[i] = u < lists && lane < k ? list(u)->list[lane] : 0;
   }
   if (tid < a.beams) {
-    const Piece* p0 = pc + tid * pieces;
     float mm = -INFINITY;
 #pragma unroll 4
-    for (int p = 0; p < pieces; ++p) mm = fmaxf(mm, p0[p].mx);
+    for (int p = 0; p < pieces; ++p) mm = fmaxf(mm, list(tid * pieces + p)->mx);
     double ss = 0.0;
 #pragma unroll 4
-    for (int p = 0; p < pieces; ++p) ss += (double)(p0[p].sum * exp_off(p0[p].mx, mm));
+    for (int p = 0; p < pieces; ++p) {
+      const Piece* q = list(tid * pieces + p);
+      ss += (double)(q->sum * exp_off(q->mx, mm));
+    }
     // what a candidate's logit is scored against
     const double base = (double)a.scores[g * a.beams + tid] - (ss > 0.0 ? log_of(ss) : 0.0);
     jn.hi[tid] = (float)base;
@@ -492,6 +501,31 @@ __global__ void __launch_bounds__(BM_THREADS) beam_join_kernel(BeamArgs a, int p
     a.parents[g * k + tid] = 0;
     a.scores_out[g * k + tid] = -INFINITY;
   }
+}
+
+__global__ void __launch_bounds__(BM_THREADS) beam_join_kernel(BeamArgs a, int pieces, const Piece* ws) {
+  extern __shared__ __align__(16) uint8_t bm_raw[];
+  pdl_wait();
+  pdl_trigger();
+  const Piece* pc = ws + (size_t)blockIdx.x * a.beams * pieces;
+  join_lists<BM_LISTS>(*reinterpret_cast<JoinSmem*>(bm_raw), a, blockIdx.x, pieces, [&](int u) { return pc + u; });
+}
+
+// A group of up to BM_GROUP beams whose rows are scanned whole: a cluster with a
+// CTA for each row, the first of which joins the lists.
+template <bool HIST>
+__global__ void __launch_bounds__(BM_THREADS, 2) beam_group_kernel(BeamArgs a) {
+  extern __shared__ __align__(16) uint8_t bm_raw[];
+  __shared__ Piece mine;
+  cg::cluster_group cl = cg::this_cluster();
+  pdl_wait();
+  pdl_trigger();
+  scan_row<HIST>(*reinterpret_cast<BeamSmem*>(bm_raw), mine, a, blockIdx.x, 0, a.vocab);
+  cl.sync();
+  if (cl.block_rank() == 0)
+    join_lists<BM_WARPS>(*reinterpret_cast<JoinSmem*>(bm_raw), a, blockIdx.x / a.beams, 1,
+                         [&](int u) -> const Piece* { return cl.map_shared_rank(&mine, u); });
+  cl.sync();  // the first CTA has read the others' lists
 }
 
 // --------------------------------------------------------------- reordering
@@ -597,7 +631,8 @@ static int beam_pieces(int groups, int beams, int vocab, int n_sm, int* len) {
 
 size_t beam_workspace(int groups, int beams, int vocab, int n_sm) {
   int len = 0;
-  return sizeof(Piece) * (size_t)groups * beams * beam_pieces(groups, beams, vocab, n_sm, &len);
+  const int pieces = beam_pieces(groups, beams, vocab, n_sm, &len);
+  return pieces == 1 && beams <= BM_GROUP ? 0 : sizeof(Piece) * (size_t)groups * beams * pieces;
 }
 
 int launch_beam_select(const BeamArgs& a, void* workspace, cudaStream_t s) {
@@ -605,18 +640,37 @@ int launch_beam_select(const BeamArgs& a, void* workspace, cudaStream_t s) {
   int dev = 0, n_sm = 0;
   if (!current_device(&dev, &n_sm)) return Q3TTS_ERR_CUDA;
   static bool ready[kMaxDevices] = {};  // the attributes are the device's
+  constexpr size_t kGroupSmem = sizeof(BeamSmem) > sizeof(JoinSmem) ? sizeof(BeamSmem) : sizeof(JoinSmem);
   if (!ready[dev]) {
-    if (cudaFuncSetAttribute(beam_scan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sizeof(BeamSmem)) != cudaSuccess ||
-        cudaFuncSetAttribute(beam_scan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sizeof(BeamSmem)) != cudaSuccess ||
-        cudaFuncSetAttribute(beam_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(JoinSmem)) !=
-            cudaSuccess)
+    auto allow = [](auto kernel, size_t smem) {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+    };
+    if (!allow(beam_scan_kernel<false>, sizeof(BeamSmem)) || !allow(beam_scan_kernel<true>, sizeof(BeamSmem)) ||
+        !allow(beam_join_kernel, sizeof(JoinSmem)) || !allow(beam_group_kernel<false>, kGroupSmem) ||
+        !allow(beam_group_kernel<true>, kGroupSmem))
       return Q3TTS_ERR_CUDA;
     ready[dev] = true;
   }
   int len = 0;
   const int pieces = beam_pieces(a.groups, a.beams, a.vocab, n_sm, &len);
+  if (pieces == 1 && a.beams <= BM_GROUP) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.groups * a.beams));
+    cfg.blockDim = dim3(BM_THREADS);
+    cfg.dynamicSmemBytes = kGroupSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = a.beams;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, a.history ? beam_group_kernel<true> : beam_group_kernel<false>, a) == cudaSuccess
+               ? Q3TTS_OK
+               : Q3TTS_ERR_CUDA;
+  }
   Piece* ws = static_cast<Piece*>(workspace);
   const dim3 grid((unsigned)((long)a.groups * a.beams * pieces));
   const cudaError_t e = launch_pdl(a.history ? beam_scan_kernel<true> : beam_scan_kernel<false>, grid, dim3(BM_THREADS),

@@ -157,7 +157,7 @@ int q3tts_beam_select(const float* logits_dev, size_t ld, const int32_t* row_ids
   if (groups == 0) return Q3TTS_OK;
   if (!logits_dev || !scores_dev || !tokens_dev || !parents_dev || !scores_out_dev || !aligned(logits_dev, 4) ||
       !aligned(row_ids_dev, 4) || !aligned(scores_dev, 4) || !aligned(tokens_dev, 4) || !aligned(parents_dev, 4) ||
-      !aligned(scores_out_dev, 4) || !workspace_dev || !aligned(workspace_dev, 8))
+      !aligned(scores_out_dev, 4) || !aligned(workspace_dev, 8))
     return Q3TTS_ERR_ARG;
   // a group's scores are read after another group's may have been written
   if (overlap(scores_dev, sizeof(float) * (size_t)groups * beams, scores_out_dev, sizeof(float) * (size_t)groups * k) &&
@@ -182,7 +182,8 @@ int q3tts_beam_select(const float* logits_dev, size_t ld, const int32_t* row_ids
   a.scores_out = scores_out_dev;
   int dev = 0, n_sm = 0;
   if (!q3::current_device(&dev, &n_sm)) return Q3TTS_ERR_CUDA;
-  if (workspace_bytes < q3::beam_workspace(groups, beams, vocab, n_sm)) return Q3TTS_ERR_ARG;
+  const size_t need = q3::beam_workspace(groups, beams, vocab, n_sm);
+  if (need && (!workspace_dev || workspace_bytes < need)) return Q3TTS_ERR_ARG;
   return q3::launch_beam_select(a, workspace_dev, (cudaStream_t)cuda_stream);
 }
 

@@ -8,6 +8,7 @@ work without the built library (no CPU path exists).
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import struct
 from typing import Dict, Optional, Sequence
@@ -187,7 +188,7 @@ def _need(t, name: str, dtype, numel: int, what: str):
 # the checks here read few tensor attributes and structs travel as packed bytes.
 
 _CACHE = struct.Struct("P6i")  # q3tts_kv_cache
-_ROWS = struct.Struct("PPNNN")  # q3tts_rows
+_ROWS = "PPNNN"  # q3tts_rows
 
 
 def _bad(what: str, name: str, want: str):
@@ -327,6 +328,9 @@ def beam_workspace_size(groups: int, beams: int, vocab: int, k: int, device: Opt
         return int(load().q3tts_beam_workspace_size(groups, beams, vocab, k))
 
 
+_workspace_bytes = functools.lru_cache(maxsize=64)(beam_workspace_size)
+
+
 def beam_select(logits, scores, k: Optional[int] = None, row_ids=None, finished=None, history=None,
                 eos_token: int = -1, special_from: int = 0, repetition_penalty: float = 1.0, out=None,
                 workspace=None):
@@ -335,7 +339,7 @@ def beam_select(logits, scores, k: Optional[int] = None, row_ids=None, finished=
     beams]; finished uint8 and history uint8 of logits' rows; k: candidates kept
     (default: beams).  Returns (tokens int32, parents int32, scores fp32), [groups,
     k] each; out: three tensors to write them to; workspace: a contiguous CUDA uint8
-    tensor of beam_workspace_size bytes (made if None)."""
+    tensor of beam_workspace_size bytes (made if None and any are needed)."""
     import torch
     what = "q3tts_beam_select"
     dev = logits.get_device()
@@ -367,10 +371,12 @@ def beam_select(logits, scores, k: Optional[int] = None, row_ids=None, finished=
         tokens, parents, best = out
         p_out = (_cuda(tokens, "out[0]", i32, dev, groups * k, what), _cuda(parents, "out[1]", i32, dev, groups * k, what),
                  _cuda(best, "out[2]", torch.float32, dev, groups * k, what))
-    if workspace is None:
-        workspace = torch.empty(beam_workspace_size(groups, beams, vocab, k, dev), dtype=torch.uint8, device=logits.device)
-    n_ws = workspace.numel()
-    p_ws = _cuda(workspace, "workspace", torch.uint8, dev, n_ws, what)
+    n_ws, p_ws = _workspace_bytes(groups, beams, vocab, k, dev), None
+    if workspace is None and n_ws:
+        workspace = torch.empty(n_ws, dtype=torch.uint8, device=logits.device)
+    if workspace is not None:
+        n_ws = workspace.numel()
+        p_ws = _cuda(workspace, "workspace", torch.uint8, dev, n_ws, what)
     _call(dev, load().q3tts_beam_select, what, logits.data_ptr(), ld,
           None if row_ids is None else _cuda(row_ids, "row_ids", i32, dev, n, what), groups, beams, vocab,
           _cuda(scores, "scores", torch.float32, dev, n, what),
@@ -391,17 +397,20 @@ def reorder_rows(src, dst, parents, status=None):
     groups, k = parents.shape
     dev = parents.get_device()
     p = _cuda(parents, "parents", torch.int32, dev, groups * k, what)
-    sets = b""
+    sets = []
     beams = src[0].shape[1] if src and src[0].dim() > 1 else 0
     for a, b in zip(src, dst):
-        sa, sb, dt, na = a.shape, b.shape, a.dtype, a.numel()
-        if len(sa) < 2 or sa[0] != groups or sa[1] != beams or sb[0] != groups or sb[1:2] != (k,) or sa[2:] != sb[2:]:
+        sa = a.shape
+        if len(sa) < 2 or sa[0] != groups or sa[1] != beams or b.shape != (groups, k, *sa[2:]):
             _bad(what, "src and dst", f"[{groups}, {beams}, ..] and [{groups}, {k}, ..]")
-        n = na // max(1, groups * beams) * a.element_size()
-        sets += _ROWS.pack(_cuda(a, "src", dt, dev, na, what), _cuda(b, "dst", dt, dev, b.numel(), what), n, n, n)
+        if (a.dtype != b.dtype or a.get_device() != dev or b.get_device() != dev or not a.is_contiguous()
+                or not b.is_contiguous()):
+            _bad(what, "src and dst", f"contiguous tensors of one type on cuda:{dev}")
+        n = a.numel() // (groups * beams or 1) * a.element_size()
+        sets += a.data_ptr(), b.data_ptr(), n, n, n
     if sets:
-        _call(dev, load().q3tts_reorder_rows, what, sets, len(src), None, p, groups, beams, k,
-              None if status is None else _cuda(status, "status", torch.int32, dev, 1, what))
+        _call(dev, load().q3tts_reorder_rows, what, struct.pack(_ROWS * len(src), *sets), len(src), None, p, groups,
+              beams, k, None if status is None else _cuda(status, "status", torch.int32, dev, 1, what))
     return dst
 
 

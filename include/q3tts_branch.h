@@ -166,8 +166,8 @@ int q3tts_compact_rows(const q3tts_kv_cache* kv, const int32_t* page_table_dev, 
  * without a candidate above -INFINITY gets token -1, parent 0 and score
  * -INFINITY.  beams and k up to Q3TTS_MAX_BEAMS, vocab up to 2^24.  Row ids
  * are not checked.  workspace_dev: device memory, 8-byte aligned, of at least
- * q3tts_beam_workspace_size bytes (on the current device; 0 for a shape that is
- * not taken), whose contents do not matter before and after; calls that may
+ * q3tts_beam_workspace_size bytes (on the current device; 0: none is needed, and
+ * it may be NULL, or the shape is not taken), whose contents do not matter before and after; calls that may
  * run at the same time need one each. */
 size_t q3tts_beam_workspace_size(int groups, int beams, int vocab, int k);
 int q3tts_beam_select(const float* logits_dev, size_t ld, const int32_t* row_ids_dev, int groups, int beams, int vocab,

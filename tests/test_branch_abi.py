@@ -1,6 +1,7 @@
 """Refusals of the branching-decode entries without a GPU: every argument check
 answers before any device work (the pointers are made up and never followed)."""
 import ctypes as C
+import struct
 import os
 import re
 
@@ -48,7 +49,7 @@ def test_struct_layouts_match_header():
         names = [n.strip().split()[-1].lstrip("*") for d in body.split(";") if d.strip() for n in d.split(",")]
         assert names == [f[0] for f in struct._fields_]
     # the binding packs the same layouts as bytes
-    assert q3tts._CACHE.size == C.sizeof(q3tts.KVCache) and q3tts._ROWS.size == C.sizeof(q3tts.Rows)
+    assert q3tts._CACHE.size == C.sizeof(q3tts.KVCache) and struct.calcsize(q3tts._ROWS) == C.sizeof(q3tts.Rows)
     consts = dict(re.findall(r"#define (Q3TTS_[A-Z_0-9]+) \(?(-?\d+)\)?", src))
     assert int(consts["Q3TTS_MAX_TREE_NODES"]) == q3tts.MAX_TREE_NODES
     assert int(consts["Q3TTS_MAX_BEAMS"]) == q3tts.MAX_BEAMS
@@ -130,7 +131,7 @@ def beam(lib, **kw):
     (dict(k=0), q3tts.ERR_ARG), (dict(scores=None), q3tts.ERR_ARG), (dict(tokens=None), q3tts.ERR_ARG),
     (dict(parents=None), q3tts.ERR_ARG), (dict(out=None), q3tts.ERR_ARG), (dict(eos=100), q3tts.ERR_ARG),
     (dict(special=101), q3tts.ERR_ARG), (dict(penalty=0.0), q3tts.ERR_ARG), (dict(finished=A), q3tts.ERR_ARG),
-    (dict(ws=None), q3tts.ERR_ARG), (dict(ws=A + 4), q3tts.ERR_ARG),
+    (dict(ws=A + 4), q3tts.ERR_ARG),
     (dict(out=A + 4096 + 4), q3tts.ERR_ARG), (dict(out=A + 4096, k=3), q3tts.ERR_ARG),
     (dict(beams=33), q3tts.ERR_UNSUPPORTED), (dict(k=33), q3tts.ERR_UNSUPPORTED),
     (dict(vocab=(1 << 24) + 1, ld=1 << 25), q3tts.ERR_UNSUPPORTED)])

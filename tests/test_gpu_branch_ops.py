@@ -392,6 +392,25 @@ def test_beam_select(q3, groups, beams, k, vocab):
     assert check_beam(run_beam(q3, logits, scores, k), logits, scores, k)
 
 
+def test_beam_workspace(q3):
+    """Groups of up to eight rows that are scanned whole need none; others are
+    refused with too little."""
+    import torch
+    rng = np.random.default_rng(16)
+    for groups, beams, vocab in ((1, 4, 2048), (2, 8, 8192), (3, 9, 2048), (1, 4, 100003)):
+        logits, scores = rng.standard_normal((groups, beams, vocab)).astype(np.float32), np.zeros((groups, beams), np.float32)
+        need = q3.beam_workspace_size(groups, beams, vocab, beams)
+        assert (need == 0) == (beams <= 8 and vocab <= 8192)
+        args = torch.from_numpy(logits).cuda(), torch.from_numpy(scores).cuda()
+        got = q3.beam_select(*args, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+        for a, b in zip(got, q3.beam_select(*args)):
+            assert torch.equal(a, b)
+        if need:
+            with pytest.raises(q3.Q3TTSError) as err:
+                q3.beam_select(*args, workspace=torch.empty(need - 8, dtype=torch.uint8, device="cuda"))
+            assert err.value.code == q3.ERR_ARG
+
+
 @pytest.mark.parametrize("vocab", [50, 2048, 20001])
 def test_beam_select_rules(q3, vocab):
     """Penalty, special codes, finished beams, dead beams."""
