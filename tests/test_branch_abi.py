@@ -1,9 +1,9 @@
 """Refusals of the branching-decode entries without a GPU: every argument check
 answers before any device work (the pointers are made up and never followed)."""
 import ctypes as C
-import struct
 import os
 import re
+from struct import calcsize
 
 import numpy as np
 import pytest
@@ -49,7 +49,7 @@ def test_struct_layouts_match_header():
         names = [n.strip().split()[-1].lstrip("*") for d in body.split(";") if d.strip() for n in d.split(",")]
         assert names == [f[0] for f in struct._fields_]
     # the binding packs the same layouts as bytes
-    assert q3tts._CACHE.size == C.sizeof(q3tts.KVCache) and struct.calcsize(q3tts._ROWS) == C.sizeof(q3tts.Rows)
+    assert q3tts._CACHE.size == C.sizeof(q3tts.KVCache) and calcsize(q3tts._ROWS) == C.sizeof(q3tts.Rows)
     consts = dict(re.findall(r"#define (Q3TTS_[A-Z_0-9]+) \(?(-?\d+)\)?", src))
     assert int(consts["Q3TTS_MAX_TREE_NODES"]) == q3tts.MAX_TREE_NODES
     assert int(consts["Q3TTS_MAX_BEAMS"]) == q3tts.MAX_BEAMS
