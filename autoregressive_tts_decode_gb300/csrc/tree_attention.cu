@@ -37,7 +37,8 @@
 // ring of tiles, one thread issues the MMAs (scores of tile t + 1 before the
 // outputs of tile t), one warp brings in the queries of the items after the
 // first, and four warps are the softmax (eight, each four with half of the rows,
-// for tiles of 64).  A CTA works through several items (sequence, kv head, tile of
+// for tiles of 32 and 64 rows: 118 -> 113 us for 128 sequences with 32; not beside
+// fp32 loads, which need the registers).  A CTA works through several items (sequence, kv head, tile of
 // rows) and the roles run ahead into the next one, so only the first pays the
 // latency of its start.  Items are dealt longest first, in rounds of alternating
 // direction: on 128 sequences of 256..2048 positions the SMs then end together.
@@ -50,10 +51,10 @@
 // fp32 rows are loaded, split into three bf16 terms on the way and multiplied term
 // by term.  Tiles have the smallest of 16, 32 and 64 rows that hold a sequence's
 // (there, 16 rows in tiles of 16, 32 or 64: 88, 97, 126 us; 32 rows in tiles of 32
-// or 64: 101, 130).
+// or 64: 99, 130).
 //
 // The bound is the cache's bytes, read once for up to 64 rows: 128 sequences of
-// 256..2048 positions, 16 nodes with two heads each: 118 us, 5.5 TB/s.  Short
+// 256..2048 positions, 16 nodes with two heads each: 113 us, 5.7 TB/s.  Short
 // calls are bound by latency (the launch, the chain from lengths to page ids to
 // first rows, a tile's way through the tensor cores): 131 positions, 8 nodes: 7.5 us.
 // Every wait is bounded; on expiry the CTA records Q3TTS_ERR_TIMEOUT, waits
@@ -81,7 +82,7 @@ template <int HD, int N, int MODE>
 struct TmCfg {
   // softmax groups of four warps, each with its share of the rows; then a warp
   // for the MMAs, one for the queries, and 2 LW for the keys and values
-  static constexpr int SW = N <= 32 ? 1 : 2, NC = N / SW;
+  static constexpr int SW = N <= 16 || (N == 32 && MODE == kSplit) ? 1 : 2, NC = N / SW;
   static constexpr int LW = MODE == kTma || N > 32 ? 1 : 2;
   static constexpr int MMA_WARP = 4 * SW, QUERY_WARP = MMA_WARP + 1, LOAD_WARP = MMA_WARP + 2;
   static constexpr int THREADS = 128 * SW + 64 + 64 * LW;

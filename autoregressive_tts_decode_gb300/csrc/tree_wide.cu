@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
         return tm_wait(su32(&ctl.q_free), (uint32_t)qi & 1u, abort_w, a.status);
       });
       if (!ok) break;
-    proxy_fence();
+      proxy_fence();
       mbar_arrive(su32(&ctl.q_full));
     }
   } else {
