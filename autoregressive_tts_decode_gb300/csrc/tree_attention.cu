@@ -38,12 +38,12 @@
 // outputs of tile t), one warp brings in the queries of the items after the
 // first, and four warps are the softmax (eight, each four with half of the rows,
 // for tiles of 32 and 64 rows: 118 -> 113 us for 128 sequences with 32; not beside
-// fp32 loads, which need the registers).  A CTA works through several items (sequence, kv head, tile of
-// rows) and the roles run ahead into the next one, so only the first pays the
-// latency of its start.  Items are dealt longest first, in rounds of alternating
-// direction: on 128 sequences of 256..2048 positions the SMs then end together.
-// Few items are split over the positions in clusters, whose CTAs join their shares
-// through each other's shared memory.
+// fp32 loads, which need the registers).  A CTA works through several items
+// (sequence, kv head, tile of rows) and the roles run ahead into the next one, so
+// only the first pays the latency of its start.  Items are dealt longest first, in
+// rounds of alternating direction: on 128 sequences of 256..2048 positions the SMs
+// then end together.  Few items are split over the positions in clusters, whose
+// CTAs join their shares through each other's shared memory.
 //
 // How the cache is read follows its type and page size.  bf16 pages that TMA boxes
 // fit come in whole boxes; other page sizes row by row, in 16-byte asynchronous

@@ -210,6 +210,40 @@ def test_tree_attention_repeats_captures_and_follows_new_lengths(q3, heads, kv_h
     check_tree(c, outs[0])
 
 
+def test_two_threads_at_once(q3):
+    """Two host threads, each with its stream and tensors, many calls each."""
+    import threading
+
+    import torch
+    rng = np.random.default_rng(17)
+    jobs, errors = [], []
+    for heads, kv_heads, seqs in ((16, 8, 3), (32, 4, 40)):
+        c = tree_case(rng, rng.integers(0, 600, seqs).tolist(), rng.integers(0, 30, seqs).tolist(), heads, kv_heads, 128, 16,
+                      torch.bfloat16)
+        c["mask_rows"] = bu.masks_tensor(c["masks"])
+        logits, scores = torch.randn((4, heads, 5000), device="cuda"), torch.zeros((4, heads), device="cuda")
+        jobs.append((c, logits, scores, run_tree(q3, c), q3.beam_select(logits, scores)))
+    torch.cuda.synchronize()
+
+    def work(c, logits, scores, want, picks):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    out = q3.tree_attention(c["pool"], 1, c["table"], c["lengths"], c["start"], c["mask_rows"], c["q"],
+                                            max_nodes=max(c["nodes"]))
+                    got = q3.beam_select(logits, scores)
+                    assert torch.equal(out, want) and all(torch.equal(a, b) for a, b in zip(got, picks))
+        except BaseException as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
 FIRST_CALLS = """
 import torch
 from autoregressive_tts_decode_gb300 import q3tts
