@@ -22,6 +22,10 @@
 // (Clusters of 16 for 8 groups of 16 beams over 131072 codes took 47 us, against
 // 29 in two kernels: no more than 7 such clusters run at once, or their CTAs share
 // SMs.)
+// Measured with the reordering of a state of 2048 floats a beam: 4 beams of 4096
+// codes 9.5 us, 32 groups of them 11.7, both latency; 8 groups of 16 beams of 131072
+// codes (67 MB) 30 us, of which the scan takes 18 (a plain read 14.5): it waits at
+// a barrier per tile.
 // The GPU's fp64 rate is low: a row's log sum is computed in fp64, a candidate's
 // score as a sum of two floats, and compared as an ordered integer.
 #include <cooperative_groups.h>
@@ -529,6 +533,10 @@ __global__ void __launch_bounds__(BM_THREADS, 2) beam_group_kernel(BeamArgs a) {
 }
 
 // --------------------------------------------------------------- reordering
+//
+// Bytes moved once: a block column per row (or, in place, per group) and set, all
+// sets of a kind in one launch; a word of every row of a group is read before one
+// is written in place.  A beam's state of 10 KB takes a launch's time, 3 us.
 
 constexpr int RO_SETS = 8;
 constexpr int RO_THREADS = 256;

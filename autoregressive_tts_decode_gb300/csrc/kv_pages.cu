@@ -13,7 +13,9 @@ namespace {
 // ------------------------------------------------------------ page copies
 //
 // The page ids are host data (the allocator's), so they travel as kernel
-// parameters: no upload, and a captured launch keeps its own copy of them.
+// parameters: no upload, and a captured launch keeps its own copy of them.  300
+// pages of 28 layers (1.1 GB moved): 159 us, 6.9 TB/s, the rate of a plain copy; 3
+// pages: 3.4 us, a launch's time.
 constexpr int CP_PAIRS = 448;   // pairs of a launch (kernel parameters: 3.5 KB of the 4 KB every device takes)
 constexpr int CP_THREADS = 256;
 constexpr int CP_UNROLL = 8;    // 16-byte loads in flight per thread
@@ -46,7 +48,10 @@ __global__ void __launch_bounds__(CP_THREADS) copy_pages_kernel(uint4* pool, lon
 // path ascends, so path[i] >= i: rows are taken in order, a chunk of them is
 // loaded whole before any of it is stored, and a row is never written before it
 // has been read.  A CTA moves one sequence's rows in one layer: path and pages
-// are looked up once for all heads.
+// are looked up once for all heads (a CTA per head: 21.4 us).  64 sequences, up to
+// 12 rows of 28 layers (81 MB moved): 18 us, 4.5 TB/s, bound by the latency of
+// three dependent loads in each of three waves of CTAs; 4, 6 or 12 loads in flight
+// per thread or five to eight CTAs per SM were no faster.
 constexpr int CR_THREADS = 256;
 constexpr int CR_UNROLL = 8;  // 16-byte loads in flight per thread
 constexpr int CR_ROWS = CR_THREADS;  // rows looked up at a time

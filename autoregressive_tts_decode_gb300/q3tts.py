@@ -365,7 +365,7 @@ def beam_select(logits, scores, k: Optional[int] = None, row_ids=None, finished=
         # (one block cut into views would cost the host more than three allocations)
         best = torch.empty_like(scores) if k == beams else scores.new_empty((groups, max(k, 0)))
         tokens = torch.empty_like(best, dtype=i32)
-        parents = torch.empty_like(best, dtype=i32)
+        parents = torch.empty_like(tokens)
         p_out = tokens.data_ptr(), parents.data_ptr(), best.data_ptr()
     else:
         tokens, parents, best = out
