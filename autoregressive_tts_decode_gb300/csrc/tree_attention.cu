@@ -33,23 +33,24 @@
 // truncate as they accumulate, and summed in tensor memory over 32768 positions
 // the error was 3.7e-5 of the output.
 //
-// Roles of a CTA (one per SM): two or four warps bring the keys and values into a
+// Roles of a CTA (one per SM): two to eight warps bring the keys and values into a
 // ring of tiles, one thread issues the MMAs (scores of tile t + 1 before the
 // outputs of tile t), one warp brings in the queries of the items after the
 // first, and four warps are the softmax (eight, each four with half of the rows,
-// for tiles of 32 and 64 rows: 118 -> 113 us for 128 sequences with 32; not beside
-// fp32 loads, which need the registers).  A CTA works through several items
-// (sequence, kv head, tile of rows) and the roles run ahead into the next one, so
-// only the first pays the latency of its start.  Items are dealt longest first, in
-// rounds of alternating direction: on 128 sequences of 256..2048 positions the SMs
-// then end together.  Few items are split over the positions in clusters, whose
-// CTAs join their shares through each other's shared memory.
+// for tiles of 32 and 64 rows: 118 -> 113 us for 128 sequences with 32).  A CTA
+// works through several items (sequence, kv head, tile of rows) and the roles run
+// ahead into the next one, so only the first pays the latency of its start.  Items
+// are dealt longest first, in rounds of alternating direction: on 128 sequences of
+// 256..2048 positions the SMs then end together.  Few items are split over the
+// positions in clusters, whose CTAs join their shares through each other's shared
+// memory.
 //
 // How the cache is read follows its type and page size.  bf16 pages that TMA boxes
 // fit come in whole boxes; other page sizes row by row, in 16-byte asynchronous
 // copies (128 sequences of 1000 positions, 8 nodes: 88 us in boxes, 104 in rows);
-// fp32 rows are loaded, split into three bf16 terms on the way and multiplied term
-// by term.  Tiles have the smallest of 16, 32 and 64 rows that hold a sequence's
+// fp32 rows are loaded, split into three bf16 terms on the way by eight warps and
+// multiplied term by term (100 sequences of 1000 positions, 8 nodes: 207 us, 4.1
+// TB/s; four warps with twice the loads each: 291).  Tiles have the smallest of 16, 32 and 64 rows that hold a sequence's
 // (there, 16 rows in tiles of 16, 32 or 64: 88, 97, 126 us; 32 rows in tiles of 32
 // or 64: 99, 130).
 //
@@ -82,8 +83,8 @@ template <int HD, int N, int MODE>
 struct TmCfg {
   // softmax groups of four warps, each with its share of the rows; then a warp
   // for the MMAs, one for the queries, and 2 LW for the keys and values
-  static constexpr int SW = N <= 16 || (N == 32 && MODE == kSplit) ? 1 : 2, NC = N / SW;
-  static constexpr int LW = MODE == kTma || N > 32 ? 1 : 2;
+  static constexpr int SW = N <= 16 ? 1 : 2, NC = N / SW;
+  static constexpr int LW = MODE == kSplit ? 4 : MODE == kTma || N > 32 ? 1 : 2;
   static constexpr int MMA_WARP = 4 * SW, QUERY_WARP = MMA_WARP + 1, LOAD_WARP = MMA_WARP + 2;
   static constexpr int THREADS = 128 * SW + 64 + 64 * LW;
   static constexpr int TERMS = MODE == kSplit ? 3 : 1;   // ring tiles of a K or V tile
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
         // all loading warps share every tile, in the ring's order (so that a place
         // is waited for at every phase of its barrier); warp lw has rows lw RW ..
         // of it, lane l the pool rows of the l-th of them (and the 32nd after it)
-        constexpr int LWN = 2 * C::LW, RW = TM_PT / LWN, H = RW / 32;
+        constexpr int LWN = 2 * C::LW, RW = TM_PT / LWN, H = RW < 32 ? 1 : RW / 32;
         const int lw = warp - C::LOAD_WARP;
         const uint8_t* pool = static_cast<const uint8_t*>(a.kv.pool);
         int pages[H], pages2[H], row_even[H], row_odd[H];  // pages of the next two tiles, key rows of the last two
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
             pages[h] = pages2[h];
             // the next tile on its way to the L2: the loads that follow keep too few
             // bytes in flight for the memory's latency
-            if (MODE == kSplit && i + 1 < m.nt && pos + TM_PT < m.t.P) {
+            if (MODE == kSplit && lane < RW && i + 1 < m.nt && pos + TM_PT < m.t.P) {
               const uint8_t* p = pool + (size_t)pool_row(a, m.g, false, pages[h], pos + TM_PT) * (HD * 4);
 #pragma unroll
               for (int line = 0; line < HD * 4; line += 128) {
@@ -344,9 +345,9 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
             mbar_arrive(su32(&ctl.full[pending % C::S]));
           }
         } else {
-          // four elements of a row per lane, sixteen loads on their way while the
-          // sixteen before them are split and stored
-          constexpr int CH = HD / 4, U = 16, RPI = 32 / CH == 0 ? 1 : 32 / CH, BATCHES = RW / (U * RPI);
+          // four elements of a row per lane, eight loads on their way while the eight
+          // before them are split and stored
+          constexpr int CH = HD / 4, U = 8, RPI = 32 / CH == 0 ? 1 : 32 / CH, BATCHES = RW / (U * RPI);
           static_assert(BATCHES >= 1 && CH <= 32, "a warp's rows in whole batches");
           const int c = lane % CH;
           auto load = [&](int i, int batch, float4 (&x)[U]) {
