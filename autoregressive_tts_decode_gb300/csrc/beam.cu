@@ -23,7 +23,7 @@
 // 29 in two kernels: no more than 7 such clusters run at once, or their CTAs share
 // SMs.)
 // Measured with the reordering of a state of 2048 floats a beam: 4 beams of 4096
-// codes 9.5 us, 32 groups of them 11.7, both latency; 8 groups of 16 beams of 131072
+// codes 9.5 us, 32 groups of 4 beams of 2048 11.7, both latency; 8 groups of 16 beams of 131072
 // codes (67 MB) 30 us, of which the scan takes 18 (a plain read 14.5): it waits at
 // a barrier per tile.
 // The GPU's fp64 rate is low: a row's log sum is computed in fp64, a candidate's
@@ -536,10 +536,12 @@ __global__ void __launch_bounds__(BM_THREADS, 2) beam_group_kernel(BeamArgs a) {
 //
 // Bytes moved once: a block column per row (or, in place, per group) and set, all
 // sets of a kind in one launch; a word of every row of a group is read before one
-// is written in place.  A beam's state of 10 KB takes a launch's time, 3 us.
+// is written in place.  32 groups of 4 beams' 12 KB: 2.4 us; 64 of 32 beams' 266 KB
+// (1.1 GB moved, some of it read twice): 135 us, in place 174.
 
 constexpr int RO_SETS = 8;
 constexpr int RO_THREADS = 256;
+constexpr int RO_UNROLL = 4;  // loads in flight per thread
 
 struct RowSets {
   q3tts_rows set[RO_SETS];
@@ -549,7 +551,20 @@ template <class W>
 __device__ __forceinline__ void gather_row(const q3tts_rows& r, int src_row, int dst_row, size_t w0, size_t words) {
   const W* s = reinterpret_cast<const W*>(static_cast<const uint8_t*>(r.src) + (size_t)src_row * r.src_stride);
   W* d = reinterpret_cast<W*>(static_cast<uint8_t*>(r.dst) + (size_t)dst_row * r.dst_stride);
-  for (size_t w = w0; w < words; w += (size_t)gridDim.x * RO_THREADS) d[w] = s[w];
+  const size_t step = (size_t)gridDim.x * RO_THREADS;
+  if (step >= words) {
+    if (w0 < words) d[w0] = s[w0];
+    return;
+  }
+  for (size_t w = w0; w < words; w += RO_UNROLL * step) {
+    W v[RO_UNROLL];
+#pragma unroll
+    for (int u = 0; u < RO_UNROLL; ++u)
+      if (w + u * step < words) v[u] = s[w + u * step];
+#pragma unroll
+    for (int u = 0; u < RO_UNROLL; ++u)
+      if (w + u * step < words) d[w + u * step] = v[u];
+  }
 }
 
 // dst row (g, j) = src row (g, parents[g][j]); src and dst do not overlap.
@@ -693,6 +708,8 @@ int launch_beam_select(const BeamArgs& a, void* workspace, cudaStream_t s) {
 int launch_reorder_rows(const q3tts_rows* sets, int n_sets, const int* row_ids, const int* parents, int groups,
                         int beams_in, int beams_out, int* status, cudaStream_t s) {
   if (groups <= 0) return Q3TTS_OK;
+  int dev = 0, n_sm = 0;
+  if (!current_device(&dev, &n_sm)) return Q3TTS_ERR_CUDA;
   for (int inplace = 0; inplace < 2; ++inplace) {
     for (int i0 = 0; i0 < n_sets;) {
       RowSets p = {};
@@ -706,7 +723,10 @@ int launch_reorder_rows(const q3tts_rows* sets, int n_sets, const int* row_ids, 
         }
       if (!m) continue;
       const size_t blocks = (most + RO_THREADS - 1) / RO_THREADS;
-      const unsigned bx = (unsigned)(blocks < 1024 ? blocks : 1024);
+      // a row of a gather goes to more CTAs only while there are few rows (64 x 32 rows
+      // of 262 KB: 346 us with a CTA for each 4 KB of a row)
+      const size_t few = (size_t)(8 * n_sm / (groups * beams_out * m) + 1), most_x = inplace ? 1024 : few;
+      const unsigned bx = (unsigned)(blocks < most_x ? blocks : most_x);
       cudaError_t e;
       if (!inplace)
         e = launch_pdl(gather_rows_kernel, dim3(bx, groups * beams_out, m), dim3(RO_THREADS), 0, s, p, row_ids, parents,
