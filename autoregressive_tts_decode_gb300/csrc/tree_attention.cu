@@ -84,7 +84,7 @@ struct TmCfg {
   // softmax groups of four warps, each with its share of the rows; then a warp
   // for the MMAs, one for the queries, and 2 LW for the keys and values
   static constexpr int SW = N <= 16 ? 1 : 2, NC = N / SW;
-  static constexpr int LW = MODE == kSplit ? 4 : MODE == kTma || N > 32 ? 1 : 2;
+  static constexpr int LW = MODE == kSplit || (MODE == kCopy && N <= 32) ? 4 : MODE == kTma ? 1 : 2;
   static constexpr int MMA_WARP = 4 * SW, QUERY_WARP = MMA_WARP + 1, LOAD_WARP = MMA_WARP + 2;
   static constexpr int THREADS = 128 * SW + 64 + 64 * LW;
   static constexpr int TERMS = MODE == kSplit ? 3 : 1;   // ring tiles of a K or V tile
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
             for (int h = 0; h < H; ++h) {
               const int mine = (tile & 1) ? row_odd[h] : row_even[h];
 #pragma unroll 8
-              for (int q = lane / CH; q < 32; q += 32 / CH) {
+              for (int q = lane / CH; q < (RW < 32 ? RW : 32); q += 32 / CH) {
                 const int r = lw * RW + 32 * h + q, row = __shfl_sync(0xffffffffu, mine, q);
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                                  dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
