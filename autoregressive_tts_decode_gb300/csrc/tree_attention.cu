@@ -47,7 +47,7 @@
 //
 // How the cache is read follows its type and page size.  bf16 pages that TMA boxes
 // fit come in whole boxes; other page sizes row by row, in 16-byte asynchronous
-// copies (128 sequences of 1000 positions, 8 nodes: 88 us in boxes, 104 in rows);
+// copies (128 sequences of 1000 positions, 8 nodes: 88 us in boxes, 96 in rows);
 // fp32 rows are loaded, split into three bf16 terms on the way by eight warps and
 // multiplied term by term (100 sequences of 1000 positions, 8 nodes: 207 us, 4.1
 // TB/s; four warps with twice the loads each: 291).  Tiles have the smallest of 16, 32 and 64 rows that hold a sequence's
@@ -82,7 +82,9 @@ enum TmLoad {
 template <int HD, int N, int MODE>
 struct TmCfg {
   // softmax groups of four warps, each with its share of the rows; then a warp
-  // for the MMAs, one for the queries, and 2 LW for the keys and values
+  // for the MMAs, one for the queries, and 2 LW for the keys and values (rows
+  // copied by 8 instead of 4 warps: 96 us, 103; beside 64 rows' softmax, for want
+  // of registers, 4: 161 us, 8: 214, 2: 181)
   static constexpr int SW = N <= 16 ? 1 : 2, NC = N / SW;
   static constexpr int LW = MODE == kSplit || (MODE == kCopy && N <= 32) ? 4 : MODE == kTma ? 1 : 2;
   static constexpr int MMA_WARP = 4 * SW, QUERY_WARP = MMA_WARP + 1, LOAD_WARP = MMA_WARP + 2;
