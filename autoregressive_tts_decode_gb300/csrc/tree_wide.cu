@@ -134,8 +134,7 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int rep = a.Hq / a.kv.Hkv;
 
-  TmDeal deal{items, row_tiles, TW_ROWS, (int)gridDim.x / CL, (int)blockIdx.x / CL, rank, CL,
-                    nullptr};
+  TmDeal deal{items, row_tiles, TW_ROWS, (int)gridDim.x / CL, (int)blockIdx.x / CL, rank, CL, nullptr};
   prefetch_first(a, deal);
   if (tid == 0) {
     for (int i = 0; i < C::S; ++i) {
@@ -159,8 +158,10 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   const bool sorted = items > (int)gridDim.x / CL && a.n_seqs <= TM_SORT;
-  if (sorted) deal.order = ctl.order;
-  if (sorted) sort_lengths(a, reinterpret_cast<int*>(ctl.part), ctl.order);
+  if (sorted) {
+    deal.order = ctl.order;
+    sort_lengths(a, reinterpret_cast<int*>(ctl.part), ctl.order);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
