@@ -54,9 +54,9 @@ def masks_tensor(masks):
 
 def tree_reference(pool, layer, table, lens, nodes, masks, q):
     """(output, bound) in 64 bits.  The bound counts roundings: probabilities
-    carried as two bf16 terms (2^-18 of each), the score's and the exponent's
-    error (products and sums in fp32, 2^-24 each), and fp32 sums over the
-    positions."""
+    carried as three bf16 terms (24 bits: 2^-24 of each), the exponential's own
+    error (2^-21), the score's (products and sums in fp32, 2^-24 each), and fp32
+    sums over the positions."""
     import torch
     rows, heads, hd = q.shape
     kvh, page = pool.shape[3], pool.shape[4]
@@ -81,7 +81,7 @@ def tree_reference(pool, layer, table, lens, nodes, masks, q):
             p = torch.softmax(sc, -1)
             p = torch.where(ok.any(-1, keepdim=True), p, torch.zeros_like(p))
             size = (qs.abs() @ kh.abs().T / math.sqrt(hd)).masked_fill(~ok, 0.0).amax(-1, keepdim=True)
-            err = 2.0 ** -18 + 2.0 ** -21 + 2 * (hd + 8) * 2.0 ** -24 * size + total * 2.0 ** -24
+            err = 2.0 ** -24 + 2.0 ** -21 + 2 * (hd + 8) * 2.0 ** -24 * size + total * 2.0 ** -24
             out[r0:r0 + n, h] = p @ vh
             tol[r0:r0 + n, h] = (p @ vh.abs()) * err
         r0 += n
