@@ -3,6 +3,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <utility>
 #include <vector>
 
 #include "ops.cuh"
@@ -61,6 +62,82 @@ bool beam_shape(int groups, int beams, int vocab, int k) {
 bool overlap(const void* p, size_t n, const void* q, size_t m) {
   const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
   return a < b + m && b < a + n;
+}
+
+// Rows of a call: n of `bytes` bytes, `stride` (at least bytes) apart.
+struct Span {
+  const void* p;
+  size_t bytes, stride;
+  long long n;
+};
+uintptr_t start_of(const Span& r) { return (uintptr_t)r.p; }
+uintptr_t end_of(const Span& r) { return (uintptr_t)r.p + (size_t)(r.n - 1) * r.stride + r.bytes; }
+
+// A row of a and a row of b share a byte (rows that lie between each other's, as
+// the fields of records do, need not).
+bool rows_overlap(const Span& a, const Span& b) {
+  if (!a.bytes || !b.bytes || a.n < 1 || b.n < 1) return false;
+  if (start_of(a) >= end_of(b) || start_of(b) >= end_of(a)) return false;
+  if (a.stride == b.stride) {
+    // row i + d of b starts diff + d stride after row i of a: the least d in range for
+    // which it does not end before that row, and whether it then starts before its end
+    const long long st = (long long)a.stride, diff = (long long)start_of(b) - (long long)start_of(a);
+    long long d = (-diff - (long long)b.bytes) / st - 1;
+    while (diff + d * st <= -(long long)b.bytes) ++d;  // (two steps at most)
+    d = std::max(d, 1 - a.n);
+    return d < b.n && diff + d * st < (long long)a.bytes;
+  }
+  uintptr_t x = start_of(a), y = start_of(b);
+  for (long long i = 0, j = 0; i < a.n && j < b.n;) {
+    if (x + a.bytes <= y) {  // (all of a's rows up to the one that y may meet)
+      const long long skip = (long long)((y - x - a.bytes) / a.stride) + 1;
+      i += skip;
+      x += (size_t)skip * a.stride;
+    } else if (y + b.bytes <= x) {
+      const long long skip = (long long)((x - y - b.bytes) / b.stride) + 1;
+      j += skip;
+      y += (size_t)skip * b.stride;
+    } else {
+      return true;
+    }
+  }
+  return false;
+}
+// Rows that are numbered by one list of ids: whether row r of one meets row r of
+// the other, whatever r is (other strides: not known).
+bool same_rows_overlap(const Span& a, const Span& b) {
+  return a.bytes && b.bytes && a.n > 0 && b.n > 0 && a.stride == b.stride && overlap(a.p, a.bytes, b.p, b.bytes);
+}
+
+// Whether a set writes what another one reads or writes (rows by number, or by ids).
+bool sets_meet(const q3tts_rows* sets, int n_sets, bool ids, long long n_in, long long n_out) {
+  auto meet = [&](const Span& a, const Span& b) { return ids ? same_rows_overlap(a, b) : rows_overlap(a, b); };
+  auto span = [&](const q3tts_rows& r, bool dst) {
+    return dst ? Span{r.dst, r.row_bytes, r.dst_stride, n_out} : Span{r.src, r.row_bytes, r.src_stride, n_in};
+  };
+  if (n_sets > 8 && !ids && n_in > 0) {
+    // many sets: the spans by their starts; where none begins inside one before it
+    // (two that are only read aside), none meet
+    std::vector<std::pair<Span, bool>> all;
+    for (int i = 0; i < n_sets; ++i)
+      for (int d = sets[i].src == sets[i].dst; d < 2; ++d)
+        if (sets[i].row_bytes) all.emplace_back(span(sets[i], d != 0), d != 0);
+    std::sort(all.begin(), all.end(), [](const auto& a, const auto& b) { return start_of(a.first) < start_of(b.first); });
+    uintptr_t read = 0, written = 0;
+    bool close = false;
+    for (const auto& e : all) {
+      close = close || start_of(e.first) < (e.second ? std::max(read, written) : written);
+      uintptr_t& end = e.second ? written : read;
+      end = std::max(end, end_of(e.first));
+    }
+    if (!close) return false;
+  }
+  for (int i = 0; i < n_sets; ++i)
+    for (int j = 0; j < n_sets; ++j)
+      if (i != j && (meet(span(sets[i], true), span(sets[j], false)) ||
+                     (j < i && meet(span(sets[i], true), span(sets[j], true)))))
+        return true;
+  return false;
 }
 
 }  // namespace
@@ -194,17 +271,24 @@ int q3tts_reorder_rows(const q3tts_rows* sets, int n_sets, const int32_t* row_id
     return Q3TTS_ERR_UNSUPPORTED;
   if (row_ids_dev && beams_in != beams_out) return Q3TTS_ERR_ARG;
   if (!aligned(row_ids_dev, 4) || !aligned(status_dev, 4)) return Q3TTS_ERR_ARG;
+  const long long n_in = (long long)groups * beams_in, n_out = (long long)groups * beams_out;
   for (int i = 0; i < n_sets; ++i) {
     const q3tts_rows& r = sets[i];
     if (r.row_bytes == 0) continue;
     if (!r.src || !r.dst || r.src_stride < r.row_bytes || r.dst_stride < r.row_bytes) return Q3TTS_ERR_ARG;
+    const Span src{r.src, r.row_bytes, r.src_stride, n_in}, dst{r.dst, r.row_bytes, r.dst_stride, n_out};
     if (r.src == r.dst) {  // in place
       if (r.src_stride != r.dst_stride || beams_in != beams_out) return Q3TTS_ERR_ARG;
-    } else if (groups && !row_ids_dev &&
-               overlap(r.src, ((size_t)groups * beams_in - 1) * r.src_stride + r.row_bytes, r.dst,
-                       ((size_t)groups * beams_out - 1) * r.dst_stride + r.row_bytes)) {
+    } else if (row_ids_dev ? same_rows_overlap(src, dst) : rows_overlap(src, dst)) {
       return Q3TTS_ERR_ARG;
     }
+    if (!row_ids_dev && parents_dev && rows_overlap(dst, Span{parents_dev, sizeof(int32_t) * (size_t)n_out, r.dst_stride, 1}))
+      return Q3TTS_ERR_ARG;
+  }
+  try {
+    if (n_sets > 1 && sets_meet(sets, n_sets, row_ids_dev != nullptr, n_in, n_out)) return Q3TTS_ERR_ARG;
+  } catch (...) {
+    return Q3TTS_ERR_CAPACITY;  // no host memory for the check
   }
   if (groups == 0 || n_sets == 0) return Q3TTS_OK;
   if (!parents_dev || !aligned(parents_dev, 4)) return Q3TTS_ERR_ARG;

@@ -388,8 +388,8 @@ def beam_select(logits, scores, k: Optional[int] = None, row_ids=None, finished=
 
 def reorder_rows(src, dst, parents, status=None):
     """q3tts_reorder_rows: dst[i][g, j] = src[i][g, parents[g, j]] for lists of
-    contiguous CUDA tensors [groups, beams, ..] of any type; dst[i] may be src[i].
-    parents int32 [groups, beams out].  Returns dst."""
+    contiguous CUDA tensors [groups, beams, ..] of any type; dst[i] may be src[i],
+    and shares no memory with the other tensors otherwise.  parents int32 [groups, beams out].  Returns dst."""
     import torch
     what = "q3tts_reorder_rows"
     if parents.dim() != 2 or len(src) != len(dst):

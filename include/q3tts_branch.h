@@ -187,7 +187,11 @@ typedef struct q3tts_rows {
  * src (sets: host array).  Rows are numbered g x beams_in + b in src and g x
  * beams_out + j in dst, or both by row_ids_dev (int32 [groups x beams], then
  * beams_in == beams_out; distinct rows, not checked).  dst is src (in place;
- * strides and beams equal then) or does not overlap it. */
+ * strides and beams equal then), or no row of it shares a byte with one of src.
+ * The sets of a call may run at once: no row of a dst may share a byte with a row
+ * of another set's src or dst, or with parents_dev (Q3TTS_ERR_ARG, where it can be
+ * told: under row_ids_dev only for equal strides).  groups x Q3TTS_MAX_BEAMS up
+ * to 65535. */
 int q3tts_reorder_rows(const q3tts_rows* sets, int n_sets, const int32_t* row_ids_dev, const int32_t* parents_dev,
                        int groups, int beams_in, int beams_out, int32_t* status_dev, void* cuda_stream);
 

@@ -181,3 +181,73 @@ def test_binding_refuses_cpu_tensors():
         q3tts.beam_select(torch.zeros(1, 1, 8), torch.zeros(1, 1))
     with pytest.raises(q3tts.Q3TTSError):
         q3tts.reorder_rows([torch.zeros(1, 1, 8)], [torch.zeros(1, 1, 8)], i[None])
+
+
+def reorder(lib, rows, groups=2, b_in=2, b_out=2, ids=None, parents=A + (1 << 30)):
+    sets = (q3tts.Rows * len(rows))(*[q3tts.Rows(*r) for r in rows])
+    return lib.q3tts_reorder_rows(sets, len(rows), ids, parents, groups, b_in, b_out, None, None)
+
+
+X, Y = A, A + 4096
+
+
+@pytest.mark.parametrize("rows", [
+    [(X, Y, 64, 64, 64), (Y, X, 64, 64, 64)],                  # two buffers exchanged
+    [(X, X, 64, 64, 64), (X, X, 64, 64, 64)],                  # one buffer twice, in place
+    [(X, Y, 64, 64, 64), (X + 8192, Y + 64, 64, 64, 64)],      # one dst, a row on
+    [(X, X, 64, 64, 64), (X + 100, Y, 64, 64, 64)],            # a dst that another set reads
+    [(X, Y, 64, 64, 64), (Y + 250, Y + 4096, 8, 8, 8)],        # by its last bytes
+    [(X, X, 16, 64, 64), (X + 8, X + 8, 16, 64, 64)],          # fields of a record that overlap
+    [(X, X, 16, 64, 64), (X + 16, Y, 16, 40, 40)],             # other strides: rows meet at the second
+    [(X, Y, 64, 64, 64)] + [(X + 8192 + 4096 * i, Y + 4096 * i, 0, 0, 0) for i in range(8)] + [(Y, X + 65536, 4, 4, 4)]])
+def test_reorder_rows_refuses_sets_that_meet(lib, rows):
+    """All sets of a call may run at once, so one may not write what another reads or writes."""
+    assert reorder(lib, rows) == q3tts.ERR_ARG
+    assert reorder(lib, rows[::-1]) == q3tts.ERR_ARG
+
+
+def test_reorder_rows_refuses_by_ids_and_parents(lib):
+    """Rows by ids: the same rows of equally spaced buffers.  A dst on the parents."""
+    for rows in ([(X, Y, 64, 64, 64), (Y, X, 64, 64, 64)], [(X, X, 64, 64, 64)] * 2, [(X, X + 32, 64, 64, 64)]):
+        assert reorder(lib, rows, ids=A) == q3tts.ERR_ARG
+    assert reorder(lib, [(X, Y, 4, 4, 4)], parents=Y) == q3tts.ERR_ARG
+    assert reorder(lib, [(X, Y, 4, 4, 4)], parents=Y + 12) == q3tts.ERR_ARG
+
+
+def test_reorder_rows_tells_rows_that_meet_from_rows_between_rows(lib):
+    """Against the bytes themselves, for random sets.  (What is not refused ends at the
+    launch: there is no GPU here.  With one the addresses would be followed.)"""
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses")
+    rng = np.random.default_rng(2)
+    seen = set()
+    for _ in range(3000):
+        groups, b_in, b_out = (int(rng.integers(1, 4)) for _ in range(3))
+        many = int(rng.integers(1, 3)) if rng.random() < 0.8 else 10
+        rows, bad, marks = [], False, {}
+        for i in range(many):
+            nb = int(rng.integers(1, 7))
+            st = int(rng.choice([nb, 8, 12, 24]))
+            st = max(st, nb)
+            span = 60 if many < 9 else 900
+            src = A + int(rng.integers(0, span))
+            if b_in == b_out and rng.random() < 0.4:
+                row = (src, src, nb, st, st)
+            else:
+                row = (src, A + int(rng.integers(0, span)), nb, st, max(nb, int(rng.choice([st, 12]))))
+                if row[1] == src:
+                    continue
+            rows.append(row)
+            read = {src + r * row[3] + e for r in range(groups * b_in) for e in range(nb)}
+            write = {row[1] + r * row[4] + e for r in range(groups * b_out) for e in range(nb)}
+            bad = bad or (row[0] != row[1] and bool(read & write))
+            for o_read, o_write in marks.values():
+                bad = bad or bool(write & o_read) or bool(write & o_write) or bool(read & o_write)
+            marks[i] = read, write
+        if not rows:
+            continue
+        rc = reorder(lib, rows, groups, b_in, b_out)
+        assert rc == (q3tts.ERR_ARG if bad else q3tts.ERR_CUDA), rows
+        seen.add((bad, len(rows) > 8))
+    assert len(seen) == 4

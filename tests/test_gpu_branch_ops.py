@@ -542,6 +542,36 @@ def test_reorder_rows_reports_bad_parents(q3):
         assert int(status) == q3.ERR_ARG and dst[0, :, 0].tolist() == want
 
 
+def test_reorder_rows_refuses_buffers_exchanged(q3):
+    import torch
+    a, b = torch.randn((1, 3, 4), device="cuda"), torch.randn((1, 3, 4), device="cuda")
+    par = torch.tensor([[2, 2, 0]], dtype=torch.int32, device="cuda")
+    for src, dst in (([a, b], [b, a]), ([a, a], [a, a]), ([a, b], [b, b]), ([par], [par])):
+        with pytest.raises(q3.Q3TTSError) as err:
+            q3.reorder_rows(src, dst, par)
+        assert err.value.code == q3.ERR_ARG
+    out = torch.empty((2, 1, 3, 4), device="cuda")
+    q3.reorder_rows([a, a], [out[0], out[1]], par)  # one source may be read twice
+    assert torch.equal(out[0], a[:, [2, 2, 0]]) and torch.equal(out[1], out[0])
+
+
+def test_reorder_rows_of_records_with_fields(q3):
+    """Rows that lie between each other's: two fields of a record in place, and a
+    third into a fourth."""
+    import ctypes as C
+
+    import torch
+    rec = torch.arange(6 * 64, device="cuda", dtype=torch.uint8).reshape(6, 64)
+    par = torch.tensor([[1, 1, 0], [2, 0, 0]], dtype=torch.int32, device="cuda")
+    want, rows = rec.clone(), torch.tensor([1, 1, 0, 5, 3, 3], device="cuda")
+    want[:, 0:16], want[:, 20:27], want[:, 48:64] = rec[rows, 0:16], rec[rows, 20:27], rec[rows, 32:48]
+    p = rec.data_ptr()
+    sets = (q3.Rows * 3)(q3.Rows(p, p, 16, 64, 64), q3.Rows(p + 20, p + 20, 7, 64, 64), q3.Rows(p + 32, p + 48, 16, 64, 64))
+    s = torch.cuda.current_stream().cuda_stream
+    assert q3.load().q3tts_reorder_rows(sets, 3, None, par.data_ptr(), 2, 3, 3, None, s) == q3.OK
+    assert torch.equal(rec, want)
+
+
 # --------------------------------------------------------------- together
 def test_a_search_step_with_the_operators(q3):
     """Trees are scored for two sequences, paths accepted, a page forked, beams
