@@ -186,6 +186,23 @@ void drop_page(q3tts_handle* h, int page) {
   if (--h->page_ref[page] == 0) h->free_pages.push_back(page);
 }
 
+int pages_for(const q3tts_handle* h, int len) { return len < 1 ? 0 : (len + h->c.page_size - 1) / h->c.page_size; }
+
+void trim_pages(q3tts_handle* h, int sid, int len) {
+  std::vector<int>& list = h->pages[sid];
+  for (const size_t keep = (size_t)pages_for(h, len); list.size() > keep; list.pop_back()) drop_page(h, list.back());
+}
+
+int tree_pages(const q3tts_handle* h, int len) {
+  return h->tree_sid < 0 ? 0 : std::max(0, (int)h->pages[h->tree_sid].size() - pages_for(h, len));
+}
+
+void drop_tree(q3tts_handle* h, int len) {
+  if (h->tree_sid < 0) return;
+  trim_pages(h, h->tree_sid, len);
+  h->tree_sid = -1;
+}
+
 bool check_sampling(const q3tts_sampling& p, int Vt) {
   if (p.do_sample && !(p.temperature > 0.f)) return false;
   if (p.sub_do_sample && !(p.sub_temperature > 0.f)) return false;
@@ -378,7 +395,7 @@ int q3tts_step_frame(q3tts_handle* h, const q3tts_sampling* params, const int32_
   static thread_local q3::StepDesc d;
   d.n = n_active;
   std::vector<char> seen(h->c.max_streams, 0);
-  int pages_needed = 0;
+  int pages_needed = 0, spare = 0;
   for (int b = 0; b < n_active; ++b) {
     int s = stream_ids[b];
     if (s < 0 || s >= h->c.max_streams || seen[s]) return Q3TTS_ERR_ARG;
@@ -387,8 +404,11 @@ int q3tts_step_frame(q3tts_handle* h, const q3tts_sampling* params, const int32_
     if (h->len[s] < 1) return Q3TTS_ERR_STATE;
     if (h->len[s] >= h->c.kv_cap_steps) return Q3TTS_ERR_CAPACITY;
     if (h->len[s] / h->c.page_size >= (int)h->pages[s].size()) ++pages_needed;
+    if (h->tree_sid == s) spare = q3::tree_pages(h, h->len[s] + 1);
   }
-  if (pages_needed > (int)h->free_pages.size()) return Q3TTS_ERR_CAPACITY;
+  if (pages_needed > (int)h->free_pages.size() + spare) return Q3TTS_ERR_CAPACITY;
+  // a tree ends with the frame of its stream; the pages past this frame go back
+  if (h->tree_sid >= 0 && seen[h->tree_sid]) q3::drop_tree(h, h->len[h->tree_sid] + 1);
   // pages are picked from the top of the free list here and taken off it only
   // once the frame is launched, so a failed launch leaves every list as it was
   int taken = 0;
@@ -410,7 +430,6 @@ int q3tts_step_frame(q3tts_handle* h, const q3tts_sampling* params, const int32_
   for (int b = 0; b < n_active; ++b) {
     if (d.newpage[b] >= 0) q3::take_page(h, stream_ids[b], d.newpage[b]);
     h->len[stream_ids[b]] += 1;
-    if (h->tree_sid == stream_ids[b]) h->tree_sid = -1;
   }
   h->free_pages.resize(h->free_pages.size() - taken);
   return Q3TTS_OK;
@@ -479,7 +498,7 @@ int q3tts_step_frame_static(q3tts_handle* h, const q3tts_sampling* params, int s
     q3::take_page(h, s, newpage);
   }
   h->len[s] += 1;
-  if (h->tree_sid == s) h->tree_sid = -1;
+  if (h->tree_sid == s) q3::drop_tree(h, h->len[s]);
   return Q3TTS_OK;
 }
 

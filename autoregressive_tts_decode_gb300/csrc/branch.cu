@@ -25,8 +25,6 @@ q3tts_kv_cache cache_of(const q3tts_handle* h) {
   return c;
 }
 
-int pages_for(const q3tts_handle* h, int len) { return (len + h->c.page_size - 1) / h->c.page_size; }
-
 // New contexts for the streams ids[0..n): stream ids[b] takes over the first
 // len positions of src[b] (a stream; its own id: unchanged).  Planned in full
 // before anything changes.
@@ -158,9 +156,12 @@ int fork(q3tts_handle* h, int src, const int32_t* dst, int n) {
 
 int tree_step(q3tts_handle* h, int sid, const int32_t* codes_dev, const int32_t* parents, int n, float* hidden_dev,
               float* logits_dev) {
-  const int len = h->len[sid], have = (int)h->pages[sid].size(), need = pages_for(h, len + n);
-  if (need - have > (int)h->free_pages.size()) return Q3TTS_ERR_CAPACITY;
-  h->tree_sid = -1;
+  const int len = h->len[sid], need = pages_for(h, len + n);
+  // the tree before this one makes room
+  const int freed = h->tree_sid < 0 ? 0 : tree_pages(h, h->len[h->tree_sid]);
+  const int have = (int)h->pages[sid].size() - (h->tree_sid == sid ? freed : 0);
+  if (need - have > (int)h->free_pages.size() + freed) return Q3TTS_ERR_CAPACITY;
+  if (h->tree_sid >= 0) drop_tree(h, h->len[h->tree_sid]);
   for (int i = have; i < need; ++i) {
     const int page = h->free_pages.back();
     h->free_pages.pop_back();
@@ -186,12 +187,16 @@ int tree_step(q3tts_handle* h, int sid, const int32_t* codes_dev, const int32_t*
                                         cudaMemcpyDeviceToDevice, h->s) != cudaSuccess)
     rc = Q3TTS_ERR_CUDA;
   if (rc == Q3TTS_OK) rc = tree_layered(h, sid, n);
-  if (rc != Q3TTS_OK) return rc;
-  if ((hidden_dev && cudaMemcpyAsync(hidden_dev, h->tree_h, sizeof(float) * (size_t)n * h->Dt,
-                                     cudaMemcpyDeviceToDevice, h->s) != cudaSuccess) ||
-      (logits_dev && cudaMemcpyAsync(logits_dev, h->tree_logits, sizeof(float) * (size_t)n * h->Vt,
-                                     cudaMemcpyDeviceToDevice, h->s) != cudaSuccess))
-    return Q3TTS_ERR_CUDA;
+  if (rc == Q3TTS_OK &&
+      ((hidden_dev && cudaMemcpyAsync(hidden_dev, h->tree_h, sizeof(float) * (size_t)n * h->Dt,
+                                      cudaMemcpyDeviceToDevice, h->s) != cudaSuccess) ||
+       (logits_dev && cudaMemcpyAsync(logits_dev, h->tree_logits, sizeof(float) * (size_t)n * h->Vt,
+                                      cudaMemcpyDeviceToDevice, h->s) != cudaSuccess)))
+    rc = Q3TTS_ERR_CUDA;
+  if (rc != Q3TTS_OK) {
+    trim_pages(h, sid, len);
+    return rc;
+  }
   h->tree_sid = sid;
   h->tree_n = n;
   std::copy(parents, parents + n, h->tree_parent);
@@ -210,12 +215,7 @@ int tree_accept(q3tts_handle* h, int sid, const int32_t* path, int n) {
     // the rows may have moved in part: no prompt until a prefill succeeds
     h->len[sid] = rc == Q3TTS_OK ? h->len[sid] + n : -1;
   }
-  // pages that only other nodes used go back to the pool
-  const size_t keep = h->len[sid] < 0 ? 0 : (size_t)pages_for(h, h->len[sid]);
-  while (h->pages[sid].size() > keep) {
-    drop_page(h, h->pages[sid].back());
-    h->pages[sid].pop_back();
-  }
+  trim_pages(h, sid, h->len[sid]);  // pages that only other nodes used go back to the pool
   return rc;
 }
 

@@ -149,6 +149,12 @@ void step_graph_destroy(q3tts_handle* h);
 // Page bookkeeping (api.cu).
 void take_page(q3tts_handle* h, int sid, int page);  // a page off the free list joins sid's
 void drop_page(q3tts_handle* h, int page);           // one holder less; free at none
+int pages_for(const q3tts_handle* h, int len);       // pages of a context of len positions
+void trim_pages(q3tts_handle* h, int sid, int len);  // the pages past those go back
+// The drafted tree's pages past the first len positions of its stream: how many,
+// and their return (the tree is forgotten).  No other stream holds such pages.
+int tree_pages(const q3tts_handle* h, int len);
+void drop_tree(q3tts_handle* h, int len);
 bool check_sampling(const q3tts_sampling& p, int Vt);
 q3tts_sampling device_sampling(const q3tts_sampling& p, int Vt);
 

@@ -44,9 +44,9 @@ int q3tts_fork(q3tts_handle* h, int src, const int32_t* dst_ids, int n);
  *               after a frame with those codes.
  * The stream itself does not advance; q3tts_tree_accept makes a path of the
  * tree part of it.  The handle holds one tree, the latest; a call that changes
- * its stream drops it.  Asynchronous.  Q3TTS_ERR_STATE without a prompt,
- * Q3TTS_ERR_CAPACITY if the stream's capacity or the pool lacks room for
- * n_nodes more positions. */
+ * its stream drops it, and its pages return to the pool.  Asynchronous.
+ * Q3TTS_ERR_STATE without a prompt, Q3TTS_ERR_CAPACITY if the stream's capacity
+ * or the pool lacks room for n_nodes more positions (the tree before stays then). */
 int q3tts_tree_step(q3tts_handle* h, int stream_id, const int32_t* codes_dev, const int32_t* parents, int n_nodes,
                     float* hidden_dev, float* logits_dev);
 

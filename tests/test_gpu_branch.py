@@ -325,6 +325,58 @@ def test_a_tree_that_no_path_is_taken_of(q3, weights, then):
     a.close(), b.close()
 
 
+@pytest.mark.parametrize("then", ["frame", "static", "frames of both", "tree", "smaller tree", "fork", "beam"])
+def test_a_dropped_tree_gives_its_pages_back(q3, weights, then):
+    """A tree of 40 frames fills the pool; whatever drops it returns its pages, so
+    that another stream's prompt fits, and the refused calls before leave it."""
+    import torch
+    parents = [-1] + [0] * 39
+    codes = torch.from_numpy(random_codes(np.random.default_rng(4), 64)).cuda()
+    eng = engine(q3, weights, "f32", 3, cap=96, kv_pages=7)
+    eng.prefill(0, prompt(41))             # 3 pages
+    eng.prefill(1, prompt(16, seed=2))     # 1 page, full
+    eng.tree_step(0, codes, parents)       # 3 more
+    u, c = torch.full((2, 16), 0.5, device="cuda"), torch.zeros((2, 16), dtype=torch.int32, device="cuda")
+
+    def full(f):
+        with pytest.raises(q3.Q3TTSError) as e:
+            f()
+        assert e.value.code == q3.ERR_CAPACITY
+
+    full(lambda: frame(eng, [1], GREEDY, 0))                                    # opens a page
+    full(lambda: eng.tree_step(1, codes, [-1] * 64))                            # 4 more pages: one too many
+    eng.tree_accept(0, []) if then == "fork" else None                          # (a fork leaves its source's tree)
+    if then == "frame":
+        frame(eng, [0], GREEDY, 0)
+    elif then == "static":
+        eng.step_frame_static(0, GREEDY, u, c)
+    elif then == "frames of both":
+        frame(eng, [0, 1], GREEDY, 0)      # the tree's pages are the other's new one
+        assert eng.length(1) == 17
+    elif then == "tree":
+        eng.tree_step(1, codes, [-1] * 40)  # 3 pages: the first tree's
+        eng.tree_accept(1, [])
+    elif then == "smaller tree":
+        eng.tree_step(0, codes, [-1, 0])
+        eng.prefill(2, prompt(48, seed=3))
+        eng.reset(2)
+        eng.tree_accept(0, [0, 1])
+        assert eng.length(0) == 43
+    elif then == "fork":
+        eng.fork(0, [2])
+        eng.reset(2)
+    else:
+        eng.beam_frame([[0]], GREEDY, torch.zeros((1, 1), device="cuda"), u[:1].contiguous(), c[:1].contiguous())
+    left = 7 - 3 - (2 if then == "frames of both" else 1)
+    full(lambda: eng.prefill(2, prompt(16 * left + 1, seed=3)))
+    eng.prefill(2, prompt(16 * left, seed=3))
+    want = engine(q3, weights, "f32", 3, cap=96)
+    want.prefill(2, prompt(16 * left, seed=3))
+    for x, y in zip(pending(eng, 2), pending(want, 2)):
+        assert np.max(np.abs(x - y)) <= TOL["f32"] * 5
+    eng.close(), want.close()
+
+
 # ------------------------------------------------------------------- beams
 def test_one_beam_is_the_greedy_decode(q3, weights):
     import torch
