@@ -598,7 +598,9 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
           // split tiles have a barrier of their own here: the places' may be a phase behind
           ok = MODE == kSplit ? tm_wait(su32(&ctl.v_full[t & 1]), (uint32_t)(t >> 1) & 1u, abort_w, a.status)
                               : tm_wait(su32(&ctl.full[it % C::S]), (uint32_t)(it / C::S) & 1u, abort_w, a.status);
-          if (wg == 0 && ok) {
+          // (by whole warps: the wait may have run out for some lanes of one, and the ballot
+          // below takes all of them)
+          if (wg == 0 && __all_sync(0xffffffffu, ok)) {
             uint4* vr = reinterpret_cast<uint4*>(sp + C::RING + it % C::S * C::SLOT + wt * 128);
             uint32_t bits = 0;
             if (pos >= m.t.L && pos < m.t.P) {
@@ -687,6 +689,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
           scaled = true;
         }
         ok = tm_wait(su32(&ctl.p_free), ((uint32_t)t & 1u) ^ 1u, abort_w, a.status) && ok;
+        __syncwarp();
         const uint32_t ph = sbase + C::P + p_lane;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -717,6 +720,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
         // this tile's P was written (whose barrier may be a phase on)
         if (i > 0) {
           if (i == m.nt) ok = tm_wait(su32(&ctl.p_free), (uint32_t)(t - 1) & 1u, abort_w, a.status) && ok;
+          __syncwarp();
           tc_fence_after();
           const uint32_t src = tmem + C::TM_O + ((t - 1) & 1) * C::TM_S + lanes;
 #pragma unroll
