@@ -598,18 +598,16 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
           // split tiles have a barrier of their own here: the places' may be a phase behind
           ok = MODE == kSplit ? tm_wait(su32(&ctl.v_full[t & 1]), (uint32_t)(t >> 1) & 1u, abort_w, a.status)
                               : tm_wait(su32(&ctl.full[it % C::S]), (uint32_t)(it / C::S) & 1u, abort_w, a.status);
-          // (by whole warps: the wait may have run out for some lanes of one, and the ballot
-          // below takes all of them)
-          if (wg == 0 && __all_sync(0xffffffffu, ok)) {
+          if (wg == 0) {  // (the wait may have run out for some lanes of a warp: all of them come to its ballot)
             uint4* vr = reinterpret_cast<uint4*>(sp + C::RING + it % C::S * C::SLOT + wt * 128);
             uint32_t bits = 0;
-            if (pos >= m.t.L && pos < m.t.P) {
+            if (ok && pos >= m.t.L && pos < m.t.P) {
 #pragma unroll
               for (int e = 0; e < C::BLK * 8; ++e)
                 bits = not_finite(vr[(e >> 3) * (TM_PT * 8) + ((e ^ lane) & 7)], bits);
             }
             const bool mine = (bits & 0x80008000u) != 0;
-            if (pos >= m.t.P || mine)
+            if (ok && (pos >= m.t.P || mine))
               for (int term = 0; term < C::TERMS; ++term) {
                 uint4* z = reinterpret_cast<uint4*>(sp + C::RING + (it + term) % C::S * C::SLOT + wt * 128);
 #pragma unroll 4
