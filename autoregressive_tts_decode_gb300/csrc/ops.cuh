@@ -39,6 +39,10 @@ struct TreeArgs {
   float* out;  // [n_rows][ldo]
   int ldo;
   int* status;
+  // the limit of the waits inside the kernels in units of 1024 cycles and, for the test of
+  // their running out, the position tile at which the first CTA's products are lost (-1: none)
+  int wait_1024 = 4 << 20;  // ~2 s
+  int lost_tile = -1;
 };
 // Whether the cache and head counts are ones it takes (the pool's rows of head
 // dim elements are numbered in 32 bits).

@@ -26,6 +26,13 @@ bool current_device(int* dev, int* n_sm) {
 
 namespace {
 
+// q3tts_debug_lose_tile, for the thread's next attention.
+struct Lose {
+  bool armed;
+  int tile, wait_us;
+};
+thread_local Lose lose = {};
+
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 int esz(int dtype) { return dtype == Q3TTS_F32 ? 4 : 2; }
@@ -178,7 +185,18 @@ int q3tts_tree_attention(const q3tts_kv_cache* kv, int layer, const int32_t* pag
   a.out = out_dev;
   a.ldo = ldo;
   a.status = status_dev;
+  if (lose.armed) {
+    a.lost_tile = lose.tile;
+    a.wait_1024 = 2 * lose.wait_us;  // (at the highest SM clock, 2070 MHz; less than 2 << 22)
+    lose.armed = false;
+  }
   return q3::launch_tree_attention(a, kv->layers, kv->kv_dtype, (cudaStream_t)cuda_stream);
+}
+
+int q3tts_debug_lose_tile(int tile, int wait_us) {
+  if (tile < 0 || wait_us < 1 || wait_us > 2000000) return Q3TTS_ERR_ARG;
+  lose = {true, tile, wait_us};
+  return Q3TTS_OK;
 }
 
 int q3tts_copy_pages(const q3tts_kv_cache* kv, const int32_t* src, const int32_t* dst, int n, void* cuda_stream) {

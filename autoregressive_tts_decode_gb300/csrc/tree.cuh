@@ -43,7 +43,7 @@ __device__ __forceinline__ bool tree_seq(const TreeArgs& a, int seq, TreeSeq& t)
 
 constexpr int TM_PT = 128;       // positions of a tile
 constexpr int TM_SORT = 256;     // sequences that are dealt by length, at most (no more than threads)
-constexpr long long TM_WAIT_CYCLES = 4000000000ll;  // ~2 s
+constexpr long long TM_LAND_CYCLES = 500000000ll;  // ~0.25 s: copies and products in flight on giving up
 constexpr float TM_FLOOR = -1e30f;  // base of a row that has seen nothing: below every score
 constexpr float TM_SLACK = 8.f;     // how far (log2) a score may pass its row's base
 
@@ -154,14 +154,14 @@ __device__ __forceinline__ uint32_t not_finite(uint4 u, uint32_t found) {
   return found | ((u.w & 0x7f807f80u) + 0x00800080u);
 }
 // Bounded wait on an mbarrier phase; false on expiry or when another role of
-// the CTA has given up.
+// the CTA has given up (abort_w[0]; abort_w[1]: the limit in units of 1024 cycles).
 __device__ __noinline__ bool tm_wait_long(uint32_t bar, uint32_t parity, volatile int* abort_w, int* status) {
   const long long t0 = clock64();
   unsigned it = 0;
   while (!mbar_try_wait(bar, parity)) {
     if ((++it & 63u) == 0) {
       if (*abort_w) return false;
-      if (clock64() - t0 > TM_WAIT_CYCLES) {
+      if ((clock64() - t0) >> 10 >= abort_w[1]) {
         *abort_w = 1;
         op_status(status, Q3TTS_ERR_TIMEOUT);
         return false;
@@ -172,6 +172,34 @@ __device__ __noinline__ bool tm_wait_long(uint32_t bar, uint32_t parity, volatil
 }
 __device__ __forceinline__ bool tm_wait(uint32_t bar, uint32_t parity, volatile int* abort_w, int* status) {
   return mbar_try_wait(bar, parity) || tm_wait_long(bar, parity, abort_w, status);
+}
+
+// What a CTA that has given up waits for (bounded) before it leaves, once all its
+// roles have ended: any of them may have been the one, with copies of a loading
+// warp that was itself done still on their way into shared memory, or products
+// into the tensor memory that is about to be given back.
+
+// Copies of loading warp w (copies: the last eight ring tiles of S places that each
+// of the two has filled, -1: none).  A place that was filled again had landed.
+template <int S>
+__device__ __forceinline__ void land_copies(const int (&copies)[2][8], int w, unsigned long long* full) {
+  const int lane = threadIdx.x & 31, it = lane < 8 ? copies[w][lane] : -1;
+  bool last = it >= 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const int o = copies[j >> 3][j & 7];
+    last = last && !(o > it && (o - it) % S == 0);
+  }
+  const long long c0 = clock64();
+  while (last && !mbar_try_wait(su32(&full[it % S]), (uint32_t)(it / S) & 1u) && clock64() - c0 < TM_LAND_CYCLES) {
+  }
+}
+// Products issued by the calling thread (`done`: a barrier of one arrival, not used before).
+__device__ __forceinline__ void land_products(uint32_t done) {
+  mma_commit(done);
+  const long long c0 = clock64();
+  while (!mbar_try_wait(done, 0u) && clock64() - c0 < TM_LAND_CYCLES) {
+  }
 }
 
 // Ring position of tile t's K and V among n tiles: K0 K1 V0 K2 V1 .. V(n-1).
@@ -233,10 +261,9 @@ __device__ __forceinline__ int pool_row(const TreeArgs& a, int g, bool values, i
 // their places of a ring of S tiles.  Lane (b, blk) copies block blk of page b's
 // rows of a tile.  A warp's lanes issue one by one, 55 cycles each: from one warp
 // for keys and values the 32 copies of 2 KB of a tile of 16-position pages took
-// longer than the tile's bytes.  copies: the last eight ring tiles filled, so that
-// on giving up those in flight land before the CTA leaves (otherwise the MMAs have
-// waited for them).  S is at least three: a warp skips two ring tiles at most,
-// which its parity waits bear.
+// longer than the tile's bytes.  copies: the last eight ring tiles filled, for
+// land_copies.  S is at least three: a warp skips two ring tiles at most, which its
+// parity waits bear.
 template <int HD, int S>
 __device__ __forceinline__ bool tma_loads(const CUtensorMap* map, const TreeArgs& a, const TmDeal& deal, int box, bool values,
                                           uint32_t ring, unsigned long long* full, unsigned long long* empty,
@@ -277,15 +304,6 @@ __device__ __forceinline__ bool tma_loads(const CUtensorMap* map, const TreeArgs
       ++issued;
     }
     ic += m.nt;
-  }
-  if (!ok) {
-    __syncwarp();
-    for (int j = issued > S ? issued - S : 0; j < issued; ++j) {
-      const int it = copies[j % 8];
-      const long long c0 = clock64();
-      while (!mbar_try_wait(su32(&full[it % S]), (uint32_t)(it / S) & 1u) && clock64() - c0 < TM_WAIT_CYCLES / 8) {
-      }
-    }
   }
   return ok;
 }

@@ -115,7 +115,7 @@ template <int N, int S>
 struct TmCtl {
   unsigned long long full[S], empty[S], s_full[2], s_free[2], p_full, p_free, q_first, q_full[TM_MASKS], q_free, done, v_full[2];
   uint32_t tmem;
-  int abort_w;
+  int abort_w[2];  // given up, limit of the waits
   float base[N], corr[N], sum[N];  // a row's base, the factor of its last rise, its sum of weights
   float part[4][N];
   unsigned bad[4];
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
   const uint32_t raw = su32(tm_raw), sbase = (raw + 1023u) & ~1023u;
   uint8_t* sp = tm_raw + (sbase - raw);
   Ctl& ctl = *reinterpret_cast<Ctl*>(sp + C::CTL);
-  volatile int* abort_w = &ctl.abort_w;
+  volatile int* abort_w = ctl.abort_w;
 
   cg::cluster_group cl = cg::this_cluster();
   const int CL = (int)cl.num_blocks(), rank = (int)cl.block_rank();
@@ -224,7 +224,9 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
     mbar_init(su32(&ctl.q_free), 1);
     mbar_init(su32(&ctl.done), 1);
     for (int i = 0; i < 2; ++i) mbar_init(su32(&ctl.v_full[i]), 64 * C::LW);
-    ctl.abort_w = 0;
+    for (int i = 0; i < 16; ++i) ctl.copies[i >> 3][i & 7] = -1;
+    ctl.abort_w[0] = 0;
+    ctl.abort_w[1] = a.wait_1024;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();  // q and the appended keys and values come from the previous kernels
@@ -317,8 +319,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
             if (!v) {
               if (tile & 1) find_rows(tile, row_odd); else find_rows(tile, row_even);
             }
-            ok = __all_sync(0xffffffffu, tm_wait(su32(&ctl.empty[it % C::S]), ((uint32_t)(it / C::S) & 1u) ^ 1u, abort_w,
-                                                 a.status));
+            ok = __all_sync(0xffffffffu, tm_wait(su32(&ctl.empty[it % C::S]), ((uint32_t)(it / C::S) & 1u) ^ 1u, abort_w, a.status));
             if (!ok) break;
             const uint8_t* src = pool + c * 16 + (v ? plane * (HD * 2) : 0);
             const uint32_t dst = ring + it % C::S * C::SLOT + (c >> 3) * (TM_PT * 128);
@@ -377,8 +378,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
             // the last of the three places is free last
             const uint32_t eb = su32(&ctl.empty[(it + 2) % C::S]), ep = ((uint32_t)((it + 2) / C::S) & 1u) ^ 1u;
             for (int term = 0; term < 2; ++term)
-              ok = tm_wait(su32(&ctl.empty[(it + term) % C::S]), ((uint32_t)((it + term) / C::S) & 1u) ^ 1u, abort_w,
-                           a.status) && ok;
+              ok = tm_wait(su32(&ctl.empty[(it + term) % C::S]), ((uint32_t)((it + term) / C::S) & 1u) ^ 1u, abort_w, a.status) && ok;
             ok = __all_sync(0xffffffffu, tm_wait(eb, ep, abort_w, a.status) && ok);
             if (!ok) break;
 #pragma unroll
@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
       // a head dimension of 64 fills half of M: the other half's rows are read
       // from the next atom and their results are not used
       constexpr uint32_t v_lead = HD == 128 ? TM_PT * 128 : 1024;
+      const int lost = blockIdx.x == 0 ? a.lost_tile : -1;
       int ic = 0, tc = 0, qi = 0;  // ring tiles, position tiles and items so far
       for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
         if (have == 0 || m.nt == 0) continue;
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
         for (int i = 0; i <= m.nt && ok; ++i) {
           if (i < m.nt) {  // scores of tile i
             const int it = (ic + k_item(i)) * C::TERMS, t = tc + i;
-            ok = tm_wait(su32(&ctl.s_free[t & 1]), ((uint32_t)(t >> 1) & 1u) ^ 1u, abort_w, a.status);
+            ok = t != lost && tm_wait(su32(&ctl.s_free[t & 1]), ((uint32_t)(t >> 1) & 1u) ^ 1u, abort_w, a.status);
             const uint32_t d = tmem + (t & 1) * C::TM_S;
 #pragma unroll
             for (int term = 0; term < C::TERMS; ++term) {
@@ -480,12 +481,6 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
         ic += 2 * m.nt;
         tc += m.nt;
         ++qi;
-      }
-      if (!ok) {  // what was issued completes before the tensor memory is given back
-        mma_commit(su32(&ctl.done));
-        const long long c0 = clock64();
-        while (!mbar_try_wait(su32(&ctl.done), 0u) && clock64() - c0 < TM_WAIT_CYCLES) {
-        }
       }
     }
     __syncwarp();
@@ -805,6 +800,11 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (*abort_w) {
+    if (MODE == kTma && warp >= C::LOAD_WARP) land_copies<C::S>(ctl.copies, warp - C::LOAD_WARP, ctl.full);
+    if (warp == C::MMA_WARP && elect_one()) land_products(su32(&ctl.done));
+    __syncwarp();
+  }
   if (warp == C::MMA_WARP)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
 }

@@ -58,7 +58,7 @@ template <int S>
 struct TwCtl {
   unsigned long long full[S], empty[S], s_full[2], p_full, o_full, q_first, q_full, q_free, done;
   uint32_t tmem;
-  int abort_w;
+  int abort_w[2];  // given up, limit of the waits
   unsigned bad[2][4];
   int copies[2][8];
   uint16_t order[TM_SORT];  // sequences, longest first
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
   const uint32_t raw = su32(tw_raw), sbase = (raw + 1023u) & ~1023u;
   uint8_t* sp = tw_raw + (sbase - raw);
   Ctl& ctl = *reinterpret_cast<Ctl*>(sp + C::CTL);
-  volatile int* abort_w = &ctl.abort_w;
+  volatile int* abort_w = ctl.abort_w;
 
   namespace cg = cooperative_groups;
   const int CL = (int)cg::this_cluster().num_blocks(), rank = (int)cg::this_cluster().block_rank();
@@ -148,7 +148,9 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
     mbar_init(su32(&ctl.q_full), 32);
     mbar_init(su32(&ctl.q_free), 1);
     mbar_init(su32(&ctl.done), 1);
-    ctl.abort_w = 0;
+    for (int i = 0; i < 16; ++i) ctl.copies[i >> 3][i & 7] = -1;
+    ctl.abort_w[0] = 0;
+    ctl.abort_w[1] = a.wait_1024;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();  // q and the appended keys and values come from the previous kernels
@@ -180,6 +182,7 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
     // ---- MMA issue
     if (elect_one()) {
       constexpr uint32_t idS = f16_idesc(TW_ROWS, TM_PT, false), idO = f16_idesc(TW_ROWS, HD, false) | 1u << 16;  // B N-major
+      const int lost = blockIdx.x == 0 ? a.lost_tile : -1;
       int ic = 0, tc = 0, qi = 0;  // ring tiles, position tiles and items so far
       for (int k = 0; ok && (have = tm_item(a, deal, k, m)) >= 0; ++k) {
         if (have == 0 || m.nt == 0) continue;
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
         for (int i = 0; i <= m.nt && ok; ++i) {
           if (i < m.nt) {  // scores of tile i
             const int it = ic + k_item(i), t = tc + i, slot = it % C::S;
-            ok = tm_wait(su32(&ctl.full[slot]), (uint32_t)(it / C::S) & 1u, abort_w, a.status);
+            ok = t != lost && tm_wait(su32(&ctl.full[slot]), (uint32_t)(it / C::S) & 1u, abort_w, a.status);
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + (t & 1) * C::TM_B;
@@ -225,12 +228,6 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
         ic += 2 * m.nt;
         tc += m.nt;
         ++qi;
-      }
-      if (!ok) {  // what was issued completes before the tensor memory is given back
-        mma_commit(su32(&ctl.done));
-        const long long c0 = clock64();
-        while (!mbar_try_wait(su32(&ctl.done), 0u) && clock64() - c0 < TM_WAIT_CYCLES) {
-        }
       }
     }
     __syncwarp();
@@ -454,6 +451,11 @@ __global__ void __launch_bounds__(TwCfg<HD>::THREADS, 1)
                                                 reinterpret_cast<float*>(sp + C::RING), abort_w);
   tc_fence_before();
   __syncthreads();
+  if (*abort_w) {
+    if (warp == C::KEY_WARP || warp == C::VALUE_WARP) land_copies<C::S>(ctl.copies, warp - C::KEY_WARP, ctl.full);
+    if (warp == C::MMA_WARP && elect_one()) land_products(su32(&ctl.done));
+    __syncwarp();
+  }
   if (warp == C::MMA_WARP) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 

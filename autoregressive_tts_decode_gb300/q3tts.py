@@ -80,7 +80,8 @@ EXPORTS = ("q3tts_workspace_size", "q3tts_create", "q3tts_prefill", "q3tts_step_
 # include/q3tts_branch.h
 BRANCH_EXPORTS = ("q3tts_fork", "q3tts_tree_step", "q3tts_tree_accept", "q3tts_beam_frame",
                   "q3tts_tree_attention", "q3tts_copy_pages", "q3tts_compact_rows",
-                  "q3tts_beam_workspace_size", "q3tts_beam_select", "q3tts_reorder_rows")
+                  "q3tts_beam_workspace_size", "q3tts_beam_select", "q3tts_reorder_rows",
+                  "q3tts_debug_lose_tile")
 MAX_CHUNK = 64
 MAX_TREE_NODES = 64
 MAX_BEAMS = 32
@@ -125,6 +126,7 @@ def load(path: str = LIB_PATH):
     # structs by address: a ctypes instance (byref) or packed bytes
     L.q3tts_tree_attention.argtypes = [vp, C.c_int, vp, C.c_int, C.c_int, vp, vp, vp, C.c_int, C.c_int, C.c_int,
                                        vp, C.c_int, vp, C.c_int, vp, vp]
+    L.q3tts_debug_lose_tile.argtypes = [C.c_int, C.c_int]
     L.q3tts_copy_pages.argtypes = [vp, vp, vp, C.c_int, vp]
     L.q3tts_compact_rows.argtypes = [vp, vp, C.c_int, C.c_int, vp, vp, C.c_int, vp, vp, vp]
     L.q3tts_beam_select.argtypes = [vp, C.c_size_t, vp, C.c_int, C.c_int, C.c_int, vp, vp, vp, C.c_int, C.c_int,
@@ -274,6 +276,13 @@ def tree_attention(pool, layer: int, page_table, lengths, node_start, masks, q, 
           out.data_ptr(), _pitch(out, rows, heads, hd, "out", what),
           None if status is None else _cuda(status, "status", i32, dev, 1, what))
     return out
+
+
+def debug_lose_tile(tile: int, wait_us: int) -> None:
+    """q3tts_debug_lose_tile: the calling thread's next tree_attention gives up."""
+    rc = load().q3tts_debug_lose_tile(int(tile), int(wait_us))
+    if rc != OK:
+        raise Q3TTSError(rc, "q3tts_debug_lose_tile")
 
 
 def _host_ids(v, name: str, what: str):

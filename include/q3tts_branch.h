@@ -135,6 +135,16 @@ int q3tts_tree_attention(const q3tts_kv_cache* kv, int layer, const int32_t* pag
                          const uint64_t* masks_dev, int n_rows, int max_nodes, int n_q_heads, const float* q_dev,
                          int ldq, float* out_dev, int ldo, int32_t* status_dev, void* cuda_stream);
 
+/* Test hook for the attention's failure path: arms the calling thread's next
+ * q3tts_tree_attention that reaches the device so that the products of its first
+ * CTA are lost from position tile `tile` (0-based, 128 positions each) on, and
+ * every wait inside the kernel gives up after about wait_us microseconds.  No GPU
+ * fault, trap or endless wait is involved: the waits for those products run out,
+ * the CTA records Q3TTS_ERR_TIMEOUT, lets its copies and products in flight land
+ * and returns.  A tile past the CTA's last one changes nothing but the limit.
+ * Q3TTS_ERR_ARG for tile < 0 or wait_us outside 1..2,000,000. */
+int q3tts_debug_lose_tile(int tile, int wait_us);
+
 /* Copies page src[i] to page dst[i] in every layer, i < n (host arrays).
  * Q3TTS_ERR_ARG if an id is outside the pool, a page is written twice, or one
  * is both read and written. */

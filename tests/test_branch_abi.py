@@ -80,6 +80,11 @@ def test_tree_attention_limits(lib):
     assert tree(lib, cache(n_pages=1 << 25)) == q3tts.ERR_UNSUPPORTED  # 2^32 rows
 
 
+@pytest.mark.parametrize("tile,us", [(-1, 100), (0, 0), (0, -5), (0, 2000001)])
+def test_lose_tile_refuses(lib, tile, us):
+    assert lib.q3tts_debug_lose_tile(tile, us) == q3tts.ERR_ARG
+
+
 @pytest.mark.parametrize("bad,code", BAD_CACHES)
 def test_caches_are_checked(lib, bad, code):
     kv = cache(**bad)

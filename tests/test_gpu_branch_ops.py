@@ -244,6 +244,55 @@ def test_two_threads_at_once(q3):
     assert not errors, errors
 
 
+LOST = [
+    # lens, nodes, heads, kv heads, head dim, page: an SM's one short item, an item shared by a
+    # cluster, several items of several tiles to an SM
+    ([131], [8], 2, 1, 128, 16), ([9000], [8], 2, 1, 128, 16), ([600] * 200, [8] * 200, 2, 1, 128, 16),
+    ([131], [16], 2, 1, 64, 16), ([9000], [16], 4, 2, 64, 16), ([600] * 200, [16] * 200, 2, 1, 128, 16),
+    ([131], [32], 2, 1, 128, 16), ([9000], [32], 2, 1, 128, 16), ([600] * 200, [32] * 200, 2, 1, 64, 16),
+    # more than 64 rows to a kv head
+    ([600] * 160, [64] * 160, 2, 1, 128, 16), ([600] * 160, [64] * 160, 2, 1, 64, 16), ([9000], [64], 38, 19, 128, 16),
+    # pages that boxes do not fit
+    ([131], [8], 2, 1, 128, 12), ([9000], [16], 2, 1, 128, 12), ([600] * 200, [32] * 200, 2, 1, 64, 12)]
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("tile", [0, 1, 3])
+@pytest.mark.parametrize("case", LOST, ids=lambda c: "-".join(str(x) for x in c).replace(" ", "")[:20] + "-" + "-".join(
+    str(x) for x in (c[1][0], *c[2:])))
+def test_a_wait_that_runs_out(q3, case, tile, dtype):
+    """The products of one CTA never come: its waits run out after 2 ms, the call
+    reports it, and the next one is right (copies and tensor memory given back)."""
+    import time
+
+    import torch
+    c = tree_case(np.random.default_rng(18), *case, dtype=getattr(torch, dtype))
+    masks = bu.masks_tensor(c["masks"])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def run():
+        status.zero_()
+        out = q3.tree_attention(c["pool"], 1, c["table"], c["lengths"], c["start"], masks, c["q"],
+                                max_nodes=max(c["nodes"]), status=status)
+        return out, int(status)
+
+    want, code = run()
+    assert code == 0
+    q3.debug_lose_tile(1 << 30, 2000000)  # no such tile
+    out, code = run()
+    assert code == 0 and torch.equal(out, want)
+    for _ in range(2):
+        q3.debug_lose_tile(tile, 2000)
+        t0 = time.perf_counter()
+        code = run()[1]
+        if tile < -(-(case[0][0] + case[1][0]) // 128):
+            assert code == q3.ERR_TIMEOUT and time.perf_counter() - t0 < 1.0
+        else:
+            assert code == 0
+        out, code = run()
+        assert code == 0 and torch.equal(out, want)
+
+
 FIRST_CALLS = """
 import torch
 from autoregressive_tts_decode_gb300 import q3tts
