@@ -224,11 +224,11 @@ __global__ void __launch_bounds__(TmCfg<HD, N, MODE>::THREADS, 1)
     mbar_init(su32(&ctl.q_free), 1);
     mbar_init(su32(&ctl.done), 1);
     for (int i = 0; i < 2; ++i) mbar_init(su32(&ctl.v_full[i]), 64 * C::LW);
-    for (int i = 0; i < 16; ++i) ctl.copies[i >> 3][i & 7] = -1;
     ctl.abort_w[0] = 0;
     ctl.abort_w[1] = a.wait_1024;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (tid >= 32 && tid < 48) ctl.copies[(tid >> 3) & 1][tid & 7] = -1;
   pdl_wait();  // q and the appended keys and values come from the previous kernels
   // (tensor memory after the wait: a kernel before may still be about to take its own)
   if (warp == C::MMA_WARP) {
