@@ -56,9 +56,9 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t b = __float_as_uint(x);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
-// Larger key: larger logit, then lower code.  Keys of a row are distinct; 0 is
-// below every key.
-__device__ __forceinline__ u64 make_key(float x, int v) { return ((u64)ordered(x) << 32) | (uint32_t)~v; }
+// Larger key: larger logit (-0 is +0), then lower code.  Keys of a row are
+// distinct; 0 is below every key.
+__device__ __forceinline__ u64 make_key(float x, int v) { return ((u64)ordered(x + 0.f) << 32) | (uint32_t)~v; }
 __device__ __forceinline__ float key_value(u64 k) {
   const uint32_t o = (uint32_t)(k >> 32);
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);

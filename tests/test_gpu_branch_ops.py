@@ -541,6 +541,21 @@ def test_beam_select_hard_rows(q3, kind, vocab):
     assert check_beam(run_beam(q3, logits, scores, k), logits, scores, k)
 
 
+@pytest.mark.parametrize("vocab", [2, 600, 8192, 20001])
+def test_beam_select_signed_zeros_are_equal(q3, vocab):
+    """-0 and +0 are equal logits: the lower code first, within a tile and across."""
+    logits = np.zeros((1, 2, vocab), np.float32)
+    logits[0, :, ::2] = -0.0
+    logits[0, 1, vocab // 3:] = 0.0
+    logits[0, 1, :vocab // 3] = -0.0
+    scores = np.zeros((1, 2), np.float32)
+    k = min(vocab, 7)
+    tok, par, _ = run_beam(q3, logits, scores, k)
+    assert tok.tolist() == [list(range(k))] and (par == 0).all()
+    tok, par, _ = run_beam(q3, logits[:, 1:], scores[:, 1:], k)
+    assert tok.tolist() == [list(range(k))]
+
+
 def test_beam_select_row_ids_pitch_and_in_place_scores(q3):
     import torch
     rng = np.random.default_rng(21)
