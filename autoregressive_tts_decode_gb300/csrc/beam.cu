@@ -398,7 +398,7 @@ __device__ __forceinline__ double log_of(double x) {
 __device__ __forceinline__ u64 score_key(float hi, float lo, float x, float mx) {
   if (!(hi > -INFINITY)) return 0;
   float h, l;
-  if (x == mx || (fabsf(x) < 1e36f && fabsf(mx) < 1e36f && fabsf(hi) < 1e36f)) {
+  if (fabsf(hi) < 1e36f && (x == mx || (fabsf(x) < 1e36f && fabsf(mx) < 1e36f))) {
     // x - mx = d + e exactly (infinite logits share the weight: 0)
     const float d = x == mx ? 0.f : x - mx;
     const float t = d - x, e = x == mx ? 0.f : (x - (d - t)) + (-mx - t);
@@ -408,7 +408,7 @@ __device__ __forceinline__ u64 score_key(float hi, float lo, float x, float mx) 
     h = s + r;
     l = h - h == 0.f ? (s - h) + r : 0.f;
   } else {  // sums that may leave fp32's range
-    const double v = ((double)hi + (double)lo) + ((double)x - (double)mx);
+    const double v = ((double)hi + (double)lo) + (x == mx ? 0.0 : (double)x - (double)mx);
     if (!(v > -INFINITY)) return 0;
     h = (float)fmin(fmax(v, -3.4028234663852886e38), 3.4028234663852886e38);
     l = (float)(v - (double)h);
@@ -447,7 +447,7 @@ __device__ __forceinline__ void join_lists(JoinSmem& jn, const BeamArgs& a, int 
     // what a candidate's logit is scored against
     const double base = (double)a.scores[g * a.beams + tid] - (ss > 0.0 ? log_of(ss) : 0.0);
     jn.hi[tid] = (float)base;
-    jn.lo[tid] = (float)(base - (double)(float)base);
+    jn.lo[tid] = fabs(base) < INFINITY ? (float)(base - (double)(float)base) : 0.f;
     jn.mx[tid] = mm;
   }
   if (tid == 0) jn.n_cand = 0;

@@ -556,6 +556,22 @@ def test_beam_select_signed_zeros_are_equal(q3, vocab):
     assert tok.tolist() == [list(range(k))]
 
 
+@pytest.mark.parametrize("vocab", [9, 2048, 20001])
+def test_beam_select_infinite_and_huge_scores(q3, vocab):
+    """A beam at +infinity stays there (its best logits first), one at -infinity or NaN
+    has no candidate; scores at the end of fp32's range keep their order."""
+    rng = np.random.default_rng(vocab)
+    logits = (2 * rng.standard_normal((4, 4, vocab))).astype(np.float32)
+    logits[2, 1, vocab // 2] = np.inf
+    big = np.float32(3.4028234e38)
+    scores = np.array([[0, np.inf, -np.inf, 1], [np.nan, -np.inf, -np.inf, -np.inf], [1, np.inf, -1, np.inf],
+                       [-big, big, -big, 2e37]], np.float32)
+    got = run_beam(q3, logits, scores, 6)
+    tok, par, best = bu.beam_reference(logits, scores, 6)
+    assert np.array_equal(got[2], best.astype(np.float32))
+    assert np.array_equal(got[1], par) and np.array_equal(got[0], tok)
+
+
 def test_beam_select_row_ids_pitch_and_in_place_scores(q3):
     import torch
     rng = np.random.default_rng(21)
