@@ -243,7 +243,7 @@ int beam_frame(q3tts_handle* h, const q3tts_sampling& sp, const int32_t* ids, in
   a.scores_out = h->beam_scores;
   rc = launch_beam_select(a, h->beam_ws, h->s);
   if (rc != Q3TTS_OK) return rc;
-  h->launches += 2;
+  h->launches += beam_workspace(groups, beams, h->Vt, 1) ? 2 : 1;  // a second kernel where the lists go through it
   // the page lists are host data: the parents are read back before the streams move
   std::vector<int> par(n);
   if (cudaMemcpyAsync(par.data(), h->beam_parents, sizeof(int) * n, cudaMemcpyDeviceToHost, h->s) != cudaSuccess ||

@@ -466,6 +466,27 @@ def test_beam_frames_equal_a_plain_search(q3, weights, kind, page, stop):
     eng.close(), ref.close()
 
 
+@pytest.mark.parametrize("beams,extra", [(4, 2), (8, 2), (9, 3)])
+def test_beam_frame_counts_its_launches(q3, weights, beams, extra):
+    """A frame of as many streams, and the selection (one launch up to eight beams, two
+    beyond) and the reordering; the context ends with a page, so none is copied."""
+    import torch
+    eng = engine(q3, weights, "f32", beams)
+    eng.prefill(0, prompt(16))
+    eng.fork(0, list(range(1, beams)))
+    u = torch.full((beams, 16), 0.5, device="cuda")
+    c = torch.zeros((beams, 16), dtype=torch.int32, device="cuda")
+    sc = torch.tensor([[0.0] + [-math.inf] * (beams - 1)], device="cuda")
+    counts = [eng.kernel_launches()]
+    eng.beam_frame([list(range(beams))], GREEDY, sc, u, c)
+    counts.append(eng.kernel_launches())
+    eng.step_frame(list(range(beams)), GREEDY, u, c)
+    counts.append(eng.kernel_launches())
+    eng.sync()
+    assert counts[1] - counts[0] == counts[2] - counts[1] + extra
+    eng.close()
+
+
 def test_a_finished_beam_keeps_its_score(q3, weights):
     """A group whose beams have all fed the end code stays as it is."""
     import torch
