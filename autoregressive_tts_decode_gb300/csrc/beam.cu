@@ -30,6 +30,8 @@
 // score as a sum of two floats, and compared as an ordered integer.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "ops.cuh"
 
 namespace cg = cooperative_groups;
@@ -662,9 +664,9 @@ int launch_beam_select(const BeamArgs& a, void* workspace, cudaStream_t s) {
   if (a.groups <= 0) return Q3TTS_OK;
   int dev = 0, n_sm = 0;
   if (!current_device(&dev, &n_sm)) return Q3TTS_ERR_CUDA;
-  static bool ready[kMaxDevices] = {};  // the attributes are the device's
+  static std::atomic<bool> ready[kMaxDevices];  // the attributes are the device's
   constexpr size_t kGroupSmem = sizeof(BeamSmem) > sizeof(JoinSmem) ? sizeof(BeamSmem) : sizeof(JoinSmem);
-  if (!ready[dev]) {
+  if (!ready[dev].load(std::memory_order_acquire)) {
     auto allow = [](auto kernel, size_t smem) {
       return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
     };
@@ -672,7 +674,7 @@ int launch_beam_select(const BeamArgs& a, void* workspace, cudaStream_t s) {
         !allow(beam_join_kernel, sizeof(JoinSmem)) || !allow(beam_group_kernel<false>, kGroupSmem) ||
         !allow(beam_group_kernel<true>, kGroupSmem))
       return Q3TTS_ERR_CUDA;
-    ready[dev] = true;
+    ready[dev].store(true, std::memory_order_release);
   }
   int len = 0;
   const int pieces = beam_pieces(a.groups, a.beams, a.vocab, n_sm, &len);

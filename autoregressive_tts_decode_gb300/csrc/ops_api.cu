@@ -3,6 +3,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <utility>
 #include <vector>
 
@@ -11,14 +12,14 @@
 namespace q3 {
 
 bool current_device(int* dev, int* n_sm) {
-  static int sms[kMaxDevices] = {};
+  static std::atomic<int> sms[kMaxDevices];
   if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) return false;
-  if (!sms[*dev]) {
-    int n = 0;
+  int n = sms[*dev].load(std::memory_order_relaxed);
+  if (!n) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess || n < 1) return false;
-    sms[*dev] = n;
+    sms[*dev].store(n, std::memory_order_relaxed);
   }
-  *n_sm = sms[*dev];
+  *n_sm = n;
   return true;
 }
 

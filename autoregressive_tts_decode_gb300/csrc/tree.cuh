@@ -452,6 +452,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // What the host keeps of a kernel, for each device.
 struct TmKernel {
   std::atomic<bool> ready{false};
+  std::mutex filling;
   int clusters[9] = {};  // clusters of that many CTAs that run at once
 };
 
@@ -503,9 +504,10 @@ int launch_items(Kernel kernel, TmKernel& known, int threads, size_t smem, bool 
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   if (!known.ready.load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> one(known.filling);
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return Q3TTS_ERR_CUDA;
     cfg.numAttrs = 1;
-    for (int c = 2; c <= 8; ++c) {
+    for (int c = 2; c <= 8 && !known.ready.load(std::memory_order_relaxed); ++c) {
       cfg.gridDim = dim3(c);
       at[0].val.clusterDim.x = c;
       if (cudaOccupancyMaxActiveClusters(&known.clusters[c], kernel, &cfg) != cudaSuccess) return Q3TTS_ERR_CUDA;

@@ -345,6 +345,56 @@ def test_first_calls_inside_a_capture():
     assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
+FIRST_THREADS = """
+import threading, torch
+from autoregressive_tts_decode_gb300 import q3tts
+from tests import branch_util as bu
+import numpy as np
+rng = np.random.default_rng(19)
+pool, table = bu.paged_cache(rng, [300] * 4, 16, 2, 8, 128, torch.bfloat16)
+i32 = dict(dtype=torch.int32, device="cuda")
+lengths, start = torch.full((4,), 290, **i32), torch.arange(5, **i32) * 10
+masks = bu.masks_tensor(sum((bu.tree_masks(bu.tree_parents(rng, 10)) for _ in range(4)), []))
+q = torch.randn((40, 16, 128), device="cuda")
+jobs = [(torch.randn(s, device="cuda"), torch.zeros(s[:2], device="cuda")) for s in ((2, 4, 900), (1, 9, 20000)) * 4]
+torch.cuda.synchronize()
+gate, got, errors = threading.Barrier(8), [None] * 8, []
+
+def calls(logits, scores):
+    picks = q3tts.beam_select(logits, scores)
+    moved = torch.empty_like(logits)
+    q3tts.reorder_rows([logits], [moved], picks[1])
+    return [q3tts.tree_attention(pool, 1, table, lengths, start, masks, q, max_nodes=10), *picks, moved]
+
+def work(i):
+    try:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            gate.wait()
+            got[i] = calls(*jobs[i])
+            torch.cuda.current_stream().synchronize()
+    except BaseException as e:
+        errors.append(e)
+
+threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert not errors, errors
+for g, j in zip(got, jobs):
+    assert all(torch.equal(a, b) for a, b in zip(g, calls(*j)))
+print("same")
+"""
+
+
+def test_first_calls_of_many_threads():
+    """A process whose first calls are eight threads' at once."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_THREADS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
 def test_cache_offsets_past_32_bits(q3):
     """A cache of more than 2^32 elements: pages near its end are read and copied."""
     import torch
