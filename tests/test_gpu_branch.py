@@ -551,3 +551,61 @@ def test_other_streams_are_left_alone(q3, weights):
         a.reset(2)
         assert np.array_equal(frame(a, [4], SAMPLED, f), frame(b, [4], SAMPLED, f))
     a.close(), b.close()
+
+
+def test_another_stream_between_branches_draws_its_own_codes(q3, weights, oracle_mod):
+    """The same as above, compared as frame_like compares: the other stream's logits
+    agree and its codes are the sampler's on its own logits."""
+    import torch
+    a, b = engine(q3, weights, "f32", 5), engine(q3, weights, "f32", 5)
+    for e in (a, b):
+        e.prefill(4, prompt(17, seed=8))
+    a.prefill(0, prompt(22))
+    sc = torch.tensor([[0.0, -np.inf]], device="cuda")
+    c = torch.zeros((2, 16), dtype=torch.int32, device="cuda")
+    u = torch.zeros((2, 16), device="cuda")
+    codes = torch.from_numpy(random_codes(np.random.default_rng(1), 6)).cuda()
+    history = {4: []}
+    for f in range(4):
+        a.fork(0, [1])
+        a.tree_step(0, codes, [-1, 0, 0, 1, 2, -1])
+        a.beam_frame([[0, 1]], SAMPLED, sc, u, c)
+        a.tree_step(1, codes, [-1, 0, 0, 1, 2, -1])
+        a.tree_accept(1, [0, 2])
+        a.fork(1, [0, 2])
+        a.reset(2)
+        frame_like(a, b, [4], SAMPLED, f, history, oracle_mod, TOL["f32"])
+    a.close(), b.close()
+
+
+def test_a_finished_beams_score_stays_its_own(q3, weights):
+    """Of two codes one is the end code, so that a beam ends in the first frame: from
+    then on a slot whose parent has ended has the parent's score, bit for bit, feeds
+    nothing and stays ended."""
+    import torch
+    v = TINY.codec_vocab
+    sp = dataclasses.replace(GREEDY, special_from=1, eos_token=v - 1)  # codes 0 and the end code
+    beams = 3
+    eng = engine(q3, weights, "f32", beams)
+    eng.prefill(0, prompt(20))
+    eng.fork(0, [1, 2])
+    sc = torch.tensor([[0.0, -np.inf, -np.inf]], device="cuda")
+    c = torch.zeros((beams, 16), dtype=torch.int32, device="cuda")
+    u = torch.zeros((beams, 16), device="cuda")
+    stayed = 0
+    for f in range(8):
+        before, ended = sc.cpu().numpy()[0], [eng.finished(s) for s in range(beams)]
+        par = eng.beam_frame([[0, 1, 2]], sp, sc, u, c)[0]
+        eng.sync()
+        after, codes = sc.cpu().numpy()[0], c.cpu().numpy()
+        for b in range(beams):
+            if ended[par[b]] and after[b] > -np.inf:
+                stayed += 1
+                assert after[b] == before[par[b]] and (codes[b] == -1).all() and eng.finished(b)
+            elif after[b] > -np.inf:
+                assert after[b] < before[par[b]] and codes[b, 0] in (0, v - 1)
+                assert eng.finished(b) == (codes[b, 0] == v - 1)
+        if f == 0:  # both codes, and no third continuation
+            assert sorted(codes[:2, 0].tolist()) == [0, v - 1] and after[2] == -np.inf
+    assert stayed >= 8
+    eng.close()
