@@ -171,6 +171,10 @@ int q3tts_tree_attention(const q3tts_kv_cache* kv, int layer, const int32_t* pag
     return Q3TTS_ERR_ARG;
   if (!q3::tree_attention_ok(desc(*kv, page_table_dev, pages_per_seq), kv->layers, n_q_heads))
     return Q3TTS_ERR_UNSUPPORTED;
+  // rows of one sequence are written while another's queries are still read
+  const size_t row = sizeof(float) * (size_t)n_q_heads * kv->head_dim;
+  if (rows_overlap(Span{q_dev, row, sizeof(float) * (size_t)ldq, n_rows}, Span{out_dev, row, sizeof(float) * (size_t)ldo, n_rows}))
+    return Q3TTS_ERR_ARG;
   q3::TreeArgs a;
   a.kv = desc(*kv, page_table_dev, pages_per_seq);
   a.layer = layer;

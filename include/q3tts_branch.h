@@ -127,8 +127,8 @@ typedef struct q3tts_kv_cache {
  * Q3TTS_ERR_UNSUPPORTED).
  * Rows outside every sequence's range are left as they were, like the rows of
  * a sequence whose length or offsets do not fit; page ids outside the pool leave
- * the sequence's rows unspecified (both reported in status_dev).  out may not
- * overlap q.  Accumulation in fp32; a row's result does not depend on the run,
+ * the sequence's rows unspecified (both reported in status_dev).  No row of out
+ * may share a byte with one of q (Q3TTS_ERR_ARG).  Accumulation in fp32; a row's result does not depend on the run,
  * but may on n_seqs and max_nodes, which decide how positions are split. */
 int q3tts_tree_attention(const q3tts_kv_cache* kv, int layer, const int32_t* page_table_dev, int pages_per_seq,
                          int n_seqs, const int32_t* lengths_dev, const int32_t* node_start_dev,

@@ -80,6 +80,14 @@ def test_tree_attention_limits(lib):
     assert tree(lib, cache(n_pages=1 << 25)) == q3tts.ERR_UNSUPPORTED  # 2^32 rows
 
 
+@pytest.mark.parametrize("kw", [dict(out=A), dict(out=A + 4), dict(out=A + 1024), dict(out=A + 8191 * 4),
+                                dict(out=A + 1024, ldq=512), dict(q=A + 1024, out=A, ldo=512)])
+def test_tree_attention_refuses_to_write_its_queries(lib, kw):
+    a = dict(n_rows=40, out=A)
+    a.update(kw)
+    assert tree(lib, **a) == q3tts.ERR_ARG
+
+
 @pytest.mark.parametrize("tile,us", [(-1, 100), (0, 0), (0, -5), (0, 2000001)])
 def test_lose_tile_refuses(lib, tile, us):
     assert lib.q3tts_debug_lose_tile(tile, us) == q3tts.ERR_ARG

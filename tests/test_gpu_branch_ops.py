@@ -147,6 +147,21 @@ def test_row_pitches_and_rows_left_alone(q3, heads, kv_heads):
     assert bool((outw[12:] == -7.5).all()) and bool((outw[:, :3] == -7.5).all())
 
 
+def test_queries_and_outputs_in_one_buffer(q3):
+    """Outputs beside the queries of their rows; on them they are refused."""
+    import torch
+    c = tree_case(np.random.default_rng(20), [33, 90], [5, 7], 4, 2, 64, 16, torch.bfloat16)
+    both = torch.zeros((12, 2, 4, 64), device="cuda")
+    both[:, 0] = c["q"]
+    c["q"] = both[:, 0]
+    run_tree(q3, c, out=both[:, 1])
+    check_tree(c, both[:, 1])
+    for out in (both[:, 0], both.view(24, 4, 64)[1:13]):
+        with pytest.raises(q3.Q3TTSError) as err:
+            run_tree(q3, c, out=out)
+        assert err.value.code == q3.ERR_ARG
+
+
 @pytest.mark.parametrize("heads,kv_heads", [(4, 2), (1440, 60)])
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
 def test_bad_device_entries_are_reported(q3, dtype, heads, kv_heads):
