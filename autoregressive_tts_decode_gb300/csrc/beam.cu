@@ -5,10 +5,11 @@
 // the repetition penalty and the mask of special codes (the sampler's rule),
 //   score(b, v) = scores[b] + (x_v - max x) - log sum_v e^(x_v - max x),
 // and a group keeps the k candidates with the largest scores among its beams'
-// vocabularies.  Scores are compared to 2^-46 of their size, so that candidates
-// of different beams order as their exact values do; equal scores go to the
-// lower beam, then the larger logit, then the lower code.  A finished beam offers one
-// candidate, its end code at its own score.
+// vocabularies.  Scores are sums of two floats, so that candidates of one beam order
+// exactly as their logits do; between beams they are as exact as the rows' sums,
+// fp32 sums of fp32 exponentials (up to about 2^-20 relative, a few 2^-24 as a rule).
+// Equal scores go to the lower beam, then the larger logit, then the lower code.  A
+// finished beam offers one candidate, its end code at its own score.
 //
 // Within a row scores order as logits do, so a row's own k best logits are all
 // it can contribute.  One pass over a row keeps the running maximum and sum of

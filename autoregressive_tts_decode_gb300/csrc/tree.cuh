@@ -44,7 +44,8 @@ __device__ __forceinline__ bool tree_seq(const TreeArgs& a, int seq, TreeSeq& t)
 constexpr int TM_PT = 128;       // positions of a tile
 constexpr int TM_SORT = 256;     // sequences that are dealt by length, at most (no more than threads)
 constexpr long long TM_LAND_CYCLES = 500000000ll;  // ~0.25 s: copies and products in flight on giving up
-constexpr float TM_FLOOR = -1e30f;  // base of a row that has seen nothing: below every score
+constexpr float TM_FLOOR = -1e30f;  // base of a row that has seen nothing: below every score (which are limited to 2^27:
+                                    // c s - base is rounded where base is, by up to 2^-24 of it, a power of two to the weights)
 constexpr float TM_SLACK = 8.f;     // how far (log2) a score may pass its row's base
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }

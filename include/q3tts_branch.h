@@ -33,7 +33,9 @@ extern "C" {
 int q3tts_fork(q3tts_handle* h, int src, const int32_t* dst_ids, int n);
 
 /* Runs the Talker over a tree of n_nodes (1 .. Q3TTS_MAX_TREE_NODES) drafted
- * frames that continue the stream, all of them in one pass.
+ * frames that continue the stream, all of them in one pass.  What it tells of a
+ * frame is its semantic code: the CodePredictor does not run, so whether the model
+ * would have drawn a frame's 15 acoustic codes is not known from it.
  *   codes_dev   device int32 [n_nodes][16]: each drafted frame's codes.  A code
  *               outside its vocabulary makes q3tts_sync_status return
  *               Q3TTS_ERR_ARG, and the results are unspecified.
@@ -115,7 +117,8 @@ typedef struct q3tts_kv_cache {
  * bit j of its mask is set (its ancestors and itself, as a rule); one that sees
  * nothing gets zeroes.  One node with its own bit is a decode step's token.
  * What a row does not see does not touch it, infinities and NaN among it; a
- * row that sees such a key or value is unspecified.
+ * row that sees such a key or value is unspecified, like one with scores (q . k /
+ * sqrt(head_dim)) above 2^27 or values above 2^90 in size.
  *   page_table_dev  int32 [n_seqs][pages_per_seq]; entries past a sequence's
  *                   last position are not read.
  *   masks_dev       uint64 [n_rows], 8-byte aligned.
@@ -128,8 +131,11 @@ typedef struct q3tts_kv_cache {
  * Rows outside every sequence's range are left as they were, like the rows of
  * a sequence whose length or offsets do not fit; page ids outside the pool leave
  * the sequence's rows unspecified (both reported in status_dev).  No row of out
- * may share a byte with one of q (Q3TTS_ERR_ARG).  Accumulation in fp32; a row's result does not depend on the run,
- * but may on n_seqs and max_nodes, which decide how positions are split. */
+ * may share a byte with one of q (Q3TTS_ERR_ARG).  Accumulation in fp32; a row's
+ * result does not depend on the run, but may on n_seqs, max_nodes and pages_per_seq,
+ * which decide how positions are split: the table's width stands for the lengths,
+ * which the host does not know, so a short sequence in a wide table is split as a
+ * long one. */
 int q3tts_tree_attention(const q3tts_kv_cache* kv, int layer, const int32_t* page_table_dev, int pages_per_seq,
                          int n_seqs, const int32_t* lengths_dev, const int32_t* node_start_dev,
                          const uint64_t* masks_dev, int n_rows, int max_nodes, int n_q_heads, const float* q_dev,
@@ -171,10 +177,13 @@ int q3tts_compact_rows(const q3tts_kv_cache* kv, const int32_t* page_table_dev, 
  * offers one, eos_token (which must be a code then) at its own score.  The k
  * best of each group are written in order: tokens_dev, parents_dev (b) and
  * scores_out_dev, [groups][k] each (scores_out_dev may be scores_dev when k ==
- * beams).  Scores are compared to 2^-46 of their size and rounded once; of equal
- * ones the lower beam comes first, then the larger logit, then the lower code.  A slot
- * without a candidate above -INFINITY gets token -1, parent 0 and score
- * -INFINITY.  beams and k up to Q3TTS_MAX_BEAMS, vocab up to 2^24.  Row ids
+ * beams).  Candidates of one beam come in the exact order of their logits.  Scores
+ * carry the error of their row's fp32 sum of exponentials, up to about 2^-20, and one
+ * rounding: candidates of different beams that are closer than that may come in
+ * either order.  Of equal ones the lower beam comes first, then the larger logit
+ * (-0 equals +0), then the lower code.  A slot without a candidate above -INFINITY
+ * gets token -1, parent 0 and score -INFINITY; a beam whose score is -INFINITY or
+ * NaN has none.  beams and k up to Q3TTS_MAX_BEAMS, vocab up to 2^24.  Row ids
  * are not checked.  workspace_dev: device memory, 8-byte aligned, of at least
  * q3tts_beam_workspace_size bytes (on the current device; 0: none is needed, and
  * it may be NULL, or the shape is not taken), whose contents do not matter before and after; calls that may

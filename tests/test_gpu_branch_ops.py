@@ -130,6 +130,32 @@ def test_large_scores_and_masked_infinities(q3, dtype, heads, kv_heads):
     assert bool(((out.double() - want).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("seqs,nodes", [(1, 3), (160, 64)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_scores_up_to_their_limit(q3, dtype, seqs, nodes):
+    """Scores of 2^26 and 2^27, exact and of one sign in each head: the positions at the
+    largest share the weight equally.  (Bound: some 20 roundings of a weight's sum and 16
+    of an output's, 2^-24 each.)"""
+    import torch
+    n, hd = 300, 64
+    c = tree_case(np.random.default_rng(23), [n] * seqs, [nodes] * seqs, 2, 1, hd, 16, getattr(torch, dtype))
+    pos = torch.arange(n + nodes, device="cuda")
+    small = (pos % 7 == 2) & (pos < n)  # at 2^26, the others at 2^27
+    k = torch.zeros((n + nodes, hd), device="cuda")
+    k[:, 0] = torch.where(small, -(2.0 ** 14), -(2.0 ** 15))
+    c["q"][:] = 0
+    c["q"][:, 0, 0], c["q"][:, 1, 0] = 2.0 ** 15, -(2.0 ** 15)
+    for s in range(seqs):
+        c["pool"][:, c["table"][s].long()[pos // 16], 0, 0, pos % 16] = k.to(c["pool"].dtype)
+    out = run_tree(q3, c)
+    for s in {0, seqs - 1}:
+        v = c["pool"][1, c["table"][s].long()[pos // 16], 1, 0, pos % 16].double()
+        for i in range(s * nodes, (s + 1) * nodes):
+            sees = torch.tensor([j < n or bool(c["masks"][i] >> (j - n) & 1) for j in range(n + nodes)], device="cuda")
+            for h, rows in ((0, small), (1, ~small & sees)):
+                assert bool(((out[i, h].double() - v[rows].mean(0)).abs() <= 2.0 ** -18 * v[rows].abs().mean(0)).all())
+
+
 @pytest.mark.parametrize("heads,kv_heads", [(4, 2), (800, 80)])
 def test_row_pitches_and_rows_left_alone(q3, heads, kv_heads):
     """q inside a wider buffer at an odd pitch, out likewise; rows behind the last
