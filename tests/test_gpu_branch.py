@@ -325,6 +325,42 @@ def test_a_tree_that_no_path_is_taken_of(q3, weights, then):
     a.close(), b.close()
 
 
+@pytest.mark.parametrize("plen", [30, 32])
+def test_other_calls_between_a_tree_and_its_acceptance(q3, weights, plen):
+    """Forks of the tree's stream, frames, beams, prompts and trees that are refused leave
+    the tree; the forks are not touched when it is accepted."""
+    import torch
+    parents = [-1, 0, 0, 1, -1, 4] + [5] * 20
+    codes = random_codes(np.random.default_rng(6), len(parents))
+    dev = torch.from_numpy(codes).cuda()
+    path = [0, 2]
+    a, b = engine(q3, weights, "f32", 5, cap=80), engine(q3, weights, "f32", 5, cap=80)
+    for e in (a, b):
+        e.prefill(0, prompt(plen))
+        e.prefill(1, prompt(20, seed=2))
+        e.prefill(2, prompt(20, seed=2))
+    a.tree_step(0, dev, parents)
+    a.fork(0, [3])
+    frame(a, [1, 3], GREEDY, 0, forced=codes[7:9])
+    a.beam_frame([[1, 2]], GREEDY, torch.zeros((1, 2), device="cuda"), torch.zeros((2, 16), device="cuda"),
+                 torch.zeros((2, 16), dtype=torch.int32, device="cuda"))
+    a.prefill(4, prompt(33, seed=5))
+    with pytest.raises(q3.Q3TTSError):
+        a.tree_step(1, torch.zeros((64, 16), dtype=torch.int32, device="cuda"), [-1] * 64)
+    a.tree_accept(0, path)
+    for j in path:
+        frame(b, [0], GREEDY, 0, forced=codes[j:j + 1])
+    b.prefill(3, prompt(plen))
+    frame(b, [3], GREEDY, 0, forced=codes[8:9])
+    for f in range(1, 3):
+        for s in (0, 3):
+            frame(b, [s], GREEDY, f, forced=frame(a, [s], GREEDY, f))
+            assert a.length(s) == b.length(s)
+            for x, y in zip(pending(a, s), pending(b, s)):
+                assert np.max(np.abs(x - y)) <= TOL["f32"] * 5
+    a.close(), b.close()
+
+
 @pytest.mark.parametrize("then", ["frame", "static", "frames of both", "tree", "smaller tree", "fork", "beam"])
 def test_a_dropped_tree_gives_its_pages_back(q3, weights, then):
     """A tree of 40 frames fills the pool; whatever drops it returns its pages, so

@@ -90,6 +90,22 @@ def test_tree_attention_many_sequences(q3, dtype, seqs, longest, most, heads, kv
     assert int(status) == 0 and torch.equal(out, run_tree(q3, c))
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("heads,kv_heads,page,nodes", [(1024, 1, 16, 3), (999, 1, 16, 2), (14, 2, 12, 33), (27, 3, 16, 64)])
+def test_many_and_odd_heads_to_a_kv_head(q3, heads, kv_heads, page, nodes, dtype):
+    """Rows of one node in several tiles, tiles of rows of several nodes; rows before the
+    first sequence's are left alone."""
+    import torch
+    c = tree_case(np.random.default_rng(22), [40, 0, 200], [nodes, 1, nodes // 2], heads, kv_heads, 64, page, getattr(torch, dtype))
+    want = run_tree(q3, c)
+    check_tree(c, want)
+    q, m = torch.zeros((len(c["masks"]) + 5, heads, 64), device="cuda"), bu.masks_tensor([0] * 5 + c["masks"])
+    q[5:] = c["q"]
+    out = torch.full_like(q, -7.5)
+    q3.tree_attention(c["pool"], 1, c["table"], c["lengths"], c["start"] + 5, m, q, max_nodes=nodes, out=out)
+    assert torch.equal(out[5:], want) and bool((out[:5] == -7.5).all())
+
+
 @pytest.mark.parametrize("heads,kv_heads", [(4, 2), (600, 100)])
 def test_chain_and_masks_that_see_nothing(q3, heads, kv_heads):
     """A chain is causal attention; a mask of zeroes sees the context only, and
@@ -494,6 +510,28 @@ def test_compact_rows(q3, page, hd, dtype):
         for to, of in enumerate(p):
             a, b = lens[s] + of, lens[s] + to
             want[:, table[s, b // page], :, :, b % page] = pool[:, table[s, a // page], :, :, a % page]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, **i32)
+    q3.compact_rows(pool, table, torch.tensor(lens, **i32), torch.from_numpy(path).cuda(),
+                    torch.tensor([len(p) for p in paths], **i32), status=status)
+    assert torch.equal(torch.nan_to_num(pool.float()), torch.nan_to_num(want.float())) and int(status) == 0
+
+
+@pytest.mark.parametrize("page,hd,dtype", [(16, 128, "bfloat16"), (7, 64, "float32")])
+def test_compact_rows_of_long_paths(q3, page, hd, dtype):
+    """Paths of more rows than a CTA looks up at a time."""
+    import torch
+    rng = np.random.default_rng(31)
+    lens, most = [13, 0, 100], 700
+    pool, table = bu.paged_cache(rng, [n + most for n in lens], page, 2, 3, hd, getattr(torch, dtype))
+    paths = [sorted(rng.permutation(most)[:513].tolist()), list(range(1, most)), sorted(rng.permutation(most)[:256].tolist())]
+    path = np.zeros((3, most), np.int32)
+    want = pool.clone()
+    for s, p in enumerate(paths):
+        path[s, :len(p)] = p
+        to, of = (torch.tensor(x, device="cuda") + lens[s] for x in (list(range(len(p))), p))
+        tb = table[s].long()
+        want[:, tb[to // page], :, :, to % page] = pool[:, tb[of // page], :, :, of % page]
     i32 = dict(dtype=torch.int32, device="cuda")
     status = torch.zeros(1, **i32)
     q3.compact_rows(pool, table, torch.tensor(lens, **i32), torch.from_numpy(path).cuda(),
