@@ -24,7 +24,7 @@
 // 29 in two kernels: no more than 7 such clusters run at once, or their CTAs share
 // SMs.)
 // Measured with the reordering of a state of 2048 floats a beam: 4 beams of 4096
-// codes 9.5 us, 32 groups of 4 beams of 2048 11.7, both latency; 8 groups of 16 beams of 131072
+// codes 9.2 us, 32 groups of 4 beams of 2048 11.3, both latency; 8 groups of 16 beams of 131072
 // codes (67 MB) 30 us, of which the scan takes 18 (a plain read 14.5): it waits at
 // a barrier per tile.
 // The GPU's fp64 rate is low: a row's log sum is computed in fp64, a candidate's

@@ -15,7 +15,7 @@ namespace {
 // The page ids are host data (the allocator's), so they travel as kernel
 // parameters: no upload, and a captured launch keeps its own copy of them.  300
 // pages of 28 layers (1.1 GB moved): 159 us, 6.9 TB/s, the rate of a plain copy; 3
-// pages: 3.4 us, a launch's time.
+// pages: 3.6 us, a launch's time.
 constexpr int CP_PAIRS = 448;   // pairs of a launch (kernel parameters: 3.5 KB of the 4 KB every device takes)
 constexpr int CP_THREADS = 256;
 constexpr int CP_UNROLL = 8;    // 16-byte loads in flight per thread

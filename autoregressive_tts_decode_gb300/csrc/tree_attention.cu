@@ -57,7 +57,7 @@
 // The bound is the cache's bytes, read once for up to 64 rows: 128 sequences of
 // 256..2048 positions, 16 nodes with two heads each: 113 us, 5.7 TB/s.  Short
 // calls are bound by latency (the launch, the chain from lengths to page ids to
-// first rows, a tile's way through the tensor cores): 131 positions, 8 nodes: 7.5 us.
+// first rows, a tile's way through the tensor cores): 131 positions, 8 nodes: 7.6 us.
 // Every wait is bounded; on expiry the CTA records Q3TTS_ERR_TIMEOUT, waits
 // (bounded) for its copies and MMAs in flight, frees its tensor memory and
 // writes nothing more.

@@ -25,7 +25,7 @@
 //
 // The bound is the tensor cores' time for six products of 128 x 128 x 128 a tile:
 // four sequences of 30011 .. 32768 positions, 64 nodes with two heads each: 127 us
-// (tiles of 64 rows: 230), of which the products alone take 99 on the 128 SMs that
+// (tiles of 64 rows: 197), of which the products alone take 99 on the 128 SMs that
 // 32 items in clusters of four fill.
 #include "tree.cuh"
 
