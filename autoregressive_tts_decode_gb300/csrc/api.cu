@@ -410,7 +410,8 @@ int q3tts_step_frame(q3tts_handle* h, const q3tts_sampling* params, const int32_
   // a tree ends with the frame of its stream; the pages past this frame go back
   if (h->tree_sid >= 0 && seen[h->tree_sid]) q3::drop_tree(h, h->len[h->tree_sid] + 1);
   // pages are picked from the top of the free list here and taken off it only
-  // once the frame is launched, so a failed launch leaves every list as it was
+  // once the frame is launched, so a failed launch leaves every list as it was (but
+  // for the tree's)
   int taken = 0;
   for (int b = 0; b < n_active; ++b) {
     int s = stream_ids[b];
