@@ -1,0 +1,78 @@
+// kv8.cuh -- the paged cache in 8 bits: its descriptor, what its kernels share
+// and their launchers.  Arguments are checked by the callers (kv8_api.cu); a
+// launcher returns a status code.
+#pragma once
+
+#include "ops.cuh"
+#include "q3tts_kv8.h"
+
+namespace q3 {
+
+// Rows of a call: sequence s has rows start[s] .. start[s + 1] - 1 at positions
+// lengths[s] and on.
+struct Kv8Rows {
+  const int* page_table;  // [n_seqs][pps]
+  const int* lengths;
+  const int* start;  // [n_seqs + 1]
+  int pps, n_seqs, n_rows, max_rows;
+  int* status;
+};
+
+// Row r of codes ([layer][page][k|v][kv head][slot], head dim bytes each); powers are
+// one byte for each `block` slots of it.
+struct Kv8Cache {
+  uint8_t* codes;
+  uint8_t* powers;
+  int n_pages, Hkv, page, hd, block, layer;
+};
+__device__ __forceinline__ long long kv8_row(const Kv8Cache& c, int page, int kv, int head, int slot) {
+  return ((((long long)c.layer * c.n_pages + page) * 2 + kv) * c.Hkv + head) * c.page + slot;
+}
+
+struct Kv8Seq {
+  int L, n, row0;
+};
+// Lengths and rows come from device memory, so they are checked here: a sequence
+// whose entries do not fit is left out and reported.
+__device__ __forceinline__ bool kv8_seq(const Kv8Rows& r, long long page, int seq, bool positions, Kv8Seq& t) {
+  t.L = r.lengths[seq];
+  t.row0 = r.start[seq];
+  const int end = r.start[seq + 1];
+  t.n = end - t.row0;
+  const bool ok = t.row0 >= 0 && end >= t.row0 && end <= r.n_rows && t.n <= r.max_rows && t.L >= 0 &&
+                  (!positions || (long long)t.L + t.n <= r.pps * page);
+  if (!ok) op_status(r.status, Q3TTS_ERR_ARG);
+  return ok && t.n > 0;
+}
+
+// 2^(byte - 127) as fp32 (2^-127 is a denormal; 255: NaN).
+__device__ __forceinline__ float kv8_power(int byte) {
+  return __int_as_float(byte <= 0 ? 1 << 22 : byte >= 255 ? 0x7fc00000 : byte << 23);
+}
+
+// Four fp32 values (448 at most in size) to E4M3, nearest even; NaN stays NaN.
+__device__ __forceinline__ uint32_t kv8_codes(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return (uint32_t)lo | (uint32_t)hi << 16;
+}
+
+struct Kv8AttnArgs {
+  Kv8Cache c;
+  Kv8Rows r;
+  const unsigned long long* masks;  // [n_rows], or NULL: causal
+  const void* q;
+  void* out;
+  int ldq, ldo, Hq;
+};
+
+// Quantising writes and reading back (kv8_cache.cu).
+int launch_kv8_write(const Kv8Cache& c, const Kv8Rows& r, int dtype, const void* k, int ldk, const void* v, int ldv,
+                     cudaStream_t s);
+int launch_kv8_read(const Kv8Cache& c, const Kv8Rows& r, const int* path, int dtype, void* k, int ldk, void* v, int ldv,
+                    cudaStream_t s);
+// Attention (kv8_attention.cu).
+int launch_kv8_attention(const Kv8AttnArgs& a, int layers, int dtype, cudaStream_t s);
+
+}  // namespace q3

@@ -7,6 +7,7 @@
 #include <utility>
 #include <vector>
 
+#include "api_checks.h"
 #include "ops.cuh"
 
 namespace q3 {
@@ -33,8 +34,6 @@ struct Lose {
   int tile, wait_us;
 };
 thread_local Lose lose = {};
-
-bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 int esz(int dtype) { return dtype == Q3TTS_F32 ? 4 : 2; }
 
@@ -66,51 +65,6 @@ bool beam_shape(int groups, int beams, int vocab, int k) {
          k <= Q3TTS_MAX_BEAMS && (long long)groups * Q3TTS_MAX_BEAMS <= 1 << 24;
 }
 
-// [p, p + n) and [q, q + m) share a byte
-bool overlap(const void* p, size_t n, const void* q, size_t m) {
-  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-  return a < b + m && b < a + n;
-}
-
-// Rows of a call: n of `bytes` bytes, `stride` (at least bytes) apart.
-struct Span {
-  const void* p;
-  size_t bytes, stride;
-  long long n;
-};
-uintptr_t start_of(const Span& r) { return (uintptr_t)r.p; }
-uintptr_t end_of(const Span& r) { return (uintptr_t)r.p + (size_t)(r.n - 1) * r.stride + r.bytes; }
-
-// A row of a and a row of b share a byte (rows that lie between each other's, as
-// the fields of records do, need not).
-bool rows_overlap(const Span& a, const Span& b) {
-  if (!a.bytes || !b.bytes || a.n < 1 || b.n < 1) return false;
-  if (start_of(a) >= end_of(b) || start_of(b) >= end_of(a)) return false;
-  if (a.stride == b.stride) {
-    // row i + d of b starts diff + d stride after row i of a: the least d in range for
-    // which it does not end before that row, and whether it then starts before its end
-    const long long st = (long long)a.stride, diff = (long long)start_of(b) - (long long)start_of(a);
-    long long d = (-diff - (long long)b.bytes) / st - 1;
-    while (diff + d * st <= -(long long)b.bytes) ++d;  // (two steps at most)
-    d = std::max(d, 1 - a.n);
-    return d < b.n && diff + d * st < (long long)a.bytes;
-  }
-  uintptr_t x = start_of(a), y = start_of(b);
-  for (long long i = 0, j = 0; i < a.n && j < b.n;) {
-    if (x + a.bytes <= y) {  // (all of a's rows up to the one that y may meet)
-      const long long skip = (long long)((y - x - a.bytes) / a.stride) + 1;
-      i += skip;
-      x += (size_t)skip * a.stride;
-    } else if (y + b.bytes <= x) {
-      const long long skip = (long long)((x - y - b.bytes) / b.stride) + 1;
-      j += skip;
-      y += (size_t)skip * b.stride;
-    } else {
-      return true;
-    }
-  }
-  return false;
-}
 // Rows that are numbered by one list of ids: whether row r of one meets row r of
 // the other, whatever r is (other strides: not known).
 bool same_rows_overlap(const Span& a, const Span& b) {

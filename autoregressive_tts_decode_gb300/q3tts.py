@@ -1,5 +1,5 @@
-"""ctypes binding of libq3tts (include/q3tts.h, include/q3tts_branch.h): argument
-marshalling only.
+"""ctypes binding of libq3tts (include/q3tts.h, include/q3tts_branch.h,
+include/q3tts_kv8.h): argument marshalling only.
 
 Every step of the decode runs in the CUDA library; this module turns torch
 tensors into device pointers and status codes into exceptions.  It refuses to
@@ -52,6 +52,11 @@ class KVCache(C.Structure):
         "layers", "n_pages", "n_kv_heads", "page_size", "head_dim", "kv_dtype")]
 
 
+class KV8Cache(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("powers", C.c_void_p)] + [(n, C.c_int) for n in (
+        "layers", "n_pages", "n_kv_heads", "page_size", "head_dim", "block")]
+
+
 class Rows(C.Structure):
     _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("row_bytes", C.c_size_t),
                 ("src_stride", C.c_size_t), ("dst_stride", C.c_size_t)]
@@ -82,6 +87,8 @@ BRANCH_EXPORTS = ("q3tts_fork", "q3tts_tree_step", "q3tts_tree_accept", "q3tts_b
                   "q3tts_tree_attention", "q3tts_copy_pages", "q3tts_compact_rows",
                   "q3tts_beam_workspace_size", "q3tts_beam_select", "q3tts_reorder_rows",
                   "q3tts_debug_lose_tile")
+# include/q3tts_kv8.h
+KV8_EXPORTS = ("q3tts_kv8_write", "q3tts_kv8_read", "q3tts_kv8_attention")
 MAX_CHUNK = 64
 MAX_TREE_NODES = 64
 MAX_BEAMS = 32
@@ -134,6 +141,12 @@ def load(path: str = LIB_PATH):
     L.q3tts_beam_workspace_size.argtypes = [C.c_int] * 4
     L.q3tts_beam_workspace_size.restype = C.c_size_t
     L.q3tts_reorder_rows.argtypes = [vp, C.c_int, vp, vp, C.c_int, C.c_int, C.c_int, vp, vp]
+    kv8 = [vp, C.c_int, vp, C.c_int, C.c_int, vp, vp]  # cache, layer, table, its width, sequences, lengths, row starts
+    rows = [vp, C.c_int, vp, C.c_int]  # two row buffers with their pitches
+    tail = [C.c_int] * 3 + [vp, vp]  # row type, rows, most of a sequence; status, stream
+    L.q3tts_kv8_write.argtypes = kv8 + rows + tail
+    L.q3tts_kv8_read.argtypes = kv8 + [vp] + rows + tail
+    L.q3tts_kv8_attention.argtypes = kv8 + [vp] + rows + [C.c_int] + tail
     L.q3tts_strerror.restype = C.c_char_p
     L.q3tts_strerror.argtypes = [C.c_int]
     _lib = L
@@ -421,6 +434,115 @@ def reorder_rows(src, dst, parents, status=None):
         _call(dev, load().q3tts_reorder_rows, what, struct.pack(_ROWS * len(src), *sets), len(src), None, p, groups,
               beams, k, None if status is None else _cuda(status, "status", torch.int32, dev, 1, what))
     return dst
+
+
+# ---- the paged cache in 8 bits (include/q3tts_kv8.h)
+
+_CACHE8 = struct.Struct("2P6i")  # q3tts_kv8_cache
+
+
+def _kv8(pool, scales, layer, page_table, lengths, start, what: str):
+    """(device, kv heads, head dim, the arguments that the calls begin with)."""
+    import torch
+    dev, i32 = pool.get_device(), torch.int32
+    if dev < 0 or pool.dtype != torch.float8_e4m3fn or pool.dim() != 6 or not pool.is_contiguous():
+        _bad(what, "pool", "a contiguous CUDA float8_e4m3fn tensor [layers, pages, 2, kv heads, page size, head dim]")
+    layers, pages, two, heads, page, hd = pool.shape
+    blocks = scales.shape[-1] if scales.dim() == 5 else 0
+    if two != 2 or blocks < 1 or page % blocks:
+        _bad(what, "pool and scales", "[layers, pages, 2, kv heads, page size, head dim] and [.., page size / block]")
+    if page_table.dim() != 2:
+        _bad(what, "page_table", "[seqs, pages per seq]")
+    seqs, pps = page_table.shape
+    kind = torch.uint8 if scales.dtype == torch.uint8 else torch.float8_e8m0fnu
+    powers = _cuda(scales, "scales", kind, dev, layers * pages * 2 * heads * blocks, what)
+    if scales.shape[:4] != pool.shape[:4]:
+        _bad(what, "scales", "[layers, pages, 2, kv heads, page size / block]")
+    return dev, heads, hd, (_CACHE8.pack(pool.data_ptr(), powers, layers, pages, heads, page, hd, page // blocks), layer,
+                            _cuda(page_table, "page_table", i32, dev, seqs * pps, what), pps, seqs,
+                            _cuda(lengths, "lengths", i32, dev, seqs, what),
+                            _cuda(start, "start", i32, dev, seqs + 1, what))
+
+
+def _row_pair(a, b, names, heads, hd: int, dev: int, what: str):
+    """(rows, heads, type code, [address and pitch of both]) of two tensors [rows,
+    heads, head dim] of one type; heads None: as a has them."""
+    import torch
+    ok = a.dim() == 3 and a.get_device() == dev and a.dtype in (torch.float32, torch.bfloat16)
+    if not ok or a.shape[2] != hd or a.shape[1] != (heads or a.shape[1]):
+        _bad(what, names[0], f"an fp32 or bf16 tensor [rows, {heads or 'heads'}, {hd}] on cuda:{dev}")
+    if b.shape != a.shape or b.dtype != a.dtype or b.get_device() != dev:
+        _bad(what, names[1], f"of {names[0]}'s shape and type on cuda:{dev}")
+    n, h, _ = a.shape
+    return n, h, F32 if a.dtype == torch.float32 else BF16, (
+        a.data_ptr(), _pitch(a, n, h, hd, names[0], what), b.data_ptr(), _pitch(b, n, h, hd, names[1], what))
+
+
+def _status(status, dev: int, what: str):
+    import torch
+    return None if status is None else _cuda(status, "status", torch.int32, dev, 1, what)
+
+
+def kv8_write(pool, scales, layer: int, page_table, lengths, start, k, v, max_rows: Optional[int] = None, status=None):
+    """q3tts_kv8_write.  pool: CUDA float8_e4m3fn [layers, pages, 2, kv heads, page
+    size, head dim]; scales: float8_e8m0fnu or uint8 [layers, pages, 2, kv heads,
+    page size / block]; page_table int32 [seqs, pages per seq]; lengths int32
+    [seqs]: positions held; start int32 [seqs + 1]: rows start[s] .. start[s + 1] - 1
+    of k and v (fp32 or bf16 [rows, kv heads, head dim], rows contiguous, any row
+    pitch) go to the positions after them; max_rows: the most rows of a sequence
+    (default: as many as there are rows).  Returns (pool, scales)."""
+    what = "q3tts_kv8_write"
+    dev, heads, hd, head = _kv8(pool, scales, layer, page_table, lengths, start, what)
+    n, _, kind, pair = _row_pair(k, v, ("k", "v"), heads, hd, dev, what)
+    _call(dev, load().q3tts_kv8_write, what, *head, *pair, kind, n, max(1, n) if max_rows is None else max_rows,
+          _status(status, dev, what))
+    return pool, scales
+
+
+def kv8_read(pool, scales, layer: int, page_table, lengths, start, path=None, max_rows: Optional[int] = None, out=None,
+             status=None):
+    """q3tts_kv8_read: keys and values of positions lengths[s] + i for rows start[s] +
+    i, or lengths[s] + path[row] (int32 [rows]).  out: two tensors [rows, kv heads,
+    head dim], fp32 or bf16 (rows contiguous, any row pitch); needed without a path, made
+    as bf16 with zeroes in rows that are not read otherwise.  The other arguments as for
+    kv8_write.  Returns out."""
+    import torch
+    what = "q3tts_kv8_read"
+    dev, heads, hd, head = _kv8(pool, scales, layer, page_table, lengths, start, what)
+    if out is None:
+        if path is None:
+            _bad(what, "out", "given, or a path")
+        out = tuple(torch.zeros((path.numel(), heads, hd), dtype=torch.bfloat16, device=pool.device) for _ in range(2))
+    n, _, kind, pair = _row_pair(out[0], out[1], ("out[0]", "out[1]"), heads, hd, dev, what)
+    _call(dev, load().q3tts_kv8_read, what, *head,
+          None if path is None else _cuda(path, "path", torch.int32, dev, n, what), *pair, kind, n,
+          max(1, n) if max_rows is None else max_rows, _status(status, dev, what))
+    return out
+
+
+def kv8_attention(pool, scales, layer: int, page_table, lengths, start, q, masks=None, max_rows: Optional[int] = None,
+                  out=None, status=None):
+    """q3tts_kv8_attention: q fp32 or bf16 [rows, q heads, head dim] (rows contiguous,
+    any row pitch), rows start[s] .. start[s + 1] - 1 of sequence s at the positions
+    after its lengths[s], whose keys and values the cache holds too.  masks: None (a
+    row sees the sequence's rows up to itself) or int64 / uint64 [rows], bit j of a
+    row's word: it sees row j of its sequence; max_rows: the most rows of a sequence
+    (default: as many as there are rows, with masks up to MAX_TREE_NODES).  The other
+    arguments as for kv8_write.  Returns out (as q; made if None, with zeroes in rows
+    outside every sequence)."""
+    import torch
+    what = "q3tts_kv8_attention"
+    dev, _, hd, head = _kv8(pool, scales, layer, page_table, lengths, start, what)
+    if out is None:
+        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    n, heads, kind, pair = _row_pair(q, out, ("q", "out"), None, hd, dev, what)
+    if max_rows is None:
+        max_rows = max(1, n if masks is None else min(n, MAX_TREE_NODES))
+    m = None
+    if masks is not None:
+        m = _cuda(masks, "masks", torch.uint64 if masks.dtype == torch.uint64 else torch.int64, dev, n, what)
+    _call(dev, load().q3tts_kv8_attention, what, *head, m, *pair, heads, kind, n, max_rows, _status(status, dev, what))
+    return out
 
 
 class Engine:

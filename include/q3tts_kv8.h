@@ -1,0 +1,94 @@
+/*
+ * q3tts_kv8.h -- C ABI of libq3tts, third part: a paged cache held in 8 bits.
+ *
+ * Operators for programs that keep their own paged caches (as those of
+ * q3tts_branch.h): keys and values are quantised as they are written, read back,
+ * and attended over as they lie.  Conventions, status codes and dtypes are
+ * q3tts.h's; status_dev is q3tts_branch.h's.
+ */
+#ifndef Q3TTS_KV8_H
+#define Q3TTS_KV8_H
+
+#include "q3tts_branch.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* The cache: codes is device memory, 16-byte aligned, of
+ * [layers][n_pages][k|v][n_kv_heads][page_size][head_dim] FP8 E4M3 codes, powers of
+ * [layers][n_pages][k|v][n_kv_heads][page_size / block] E8M0 bytes; head_dim 64
+ * or 128, block a divisor of page_size.  The element with code c in a block with
+ * byte b is c x 2^(b - 127); a byte of 255 stands for NaN in the whole block.  A
+ * sequence's position p is slot p % page_size of page page_table[p / page_size],
+ * in every layer.  No block that a call writes may belong to two sequences of it. */
+typedef struct q3tts_kv8_cache {
+  void* codes;
+  void* powers;
+  int layers, n_pages, n_kv_heads, page_size, head_dim;
+  int block;
+} q3tts_kv8_cache;
+
+/* In all three calls sequence s holds lengths_dev[s] positions (0 or more), and
+ * its rows, row_start_dev[s] .. row_start_dev[s + 1] - 1 of a call's rows, stand
+ * at the positions after them in order; max_rows (1 or more) bounds every
+ * sequence's count and sizes the launch.  page_table_dev: int32
+ * [n_seqs][pages_per_seq]; entries past a sequence's last position are not read.
+ * Rows are n_rows of fp32 or bf16 elements (row_dtype: Q3TTS_F32 or Q3TTS_BF16),
+ * their pitch (ldk, ldv, ldq, ldo) counted in elements.  A sequence whose length
+ * or rows do not fit its table, the rows or max_rows is left out, and page ids
+ * outside the pool are not followed (both reported in status_dev). */
+
+/* Quantises the keys and values of new rows (n_rows of n_kv_heads x head_dim
+ * elements) and writes them to one layer.  A block's power is the smallest of 2^-127
+ * and up that brings the largest finite magnitude of its rows to 448 or below;
+ * codes are rounded to the nearest, ties to even; infinities and NaN become NaN
+ * and do not count for the power.  In a block whose first rows are positions that
+ * the sequence holds already the power does not fall: where it rises, those rows'
+ * codes are rounded again to the new one.  Rows of a block behind the last one
+ * written are left as they were.  A block on a page outside the pool is left out. */
+int q3tts_kv8_write(const q3tts_kv8_cache* kv, int layer, const int32_t* page_table_dev, int pages_per_seq,
+                    int n_seqs, const int32_t* lengths_dev, const int32_t* row_start_dev, const void* k_dev, int ldk,
+                    const void* v_dev, int ldv, int row_dtype, int n_rows, int max_rows, int32_t* status_dev,
+                    void* cuda_stream);
+
+/* Reads keys and values back into rows, each element rounded once to row_dtype.  Row
+ * i of sequence s is position lengths_dev[s] + i, or lengths_dev[s] + path_dev[row]
+ * where path_dev (int32 [n_rows]; not negative, any order) is given; an entry
+ * outside the sequence's table or on a page outside the pool leaves its row as it
+ * was (reported in status_dev), like rows outside every sequence.  With a path,
+ * reading the accepted nodes of a drafted tree and writing them as new rows at
+ * lengths_dev moves them to the places after the last position held.  No row of
+ * k_out may share a byte with one of v_out (Q3TTS_ERR_ARG). */
+int q3tts_kv8_read(const q3tts_kv8_cache* kv, int layer, const int32_t* page_table_dev, int pages_per_seq, int n_seqs,
+                   const int32_t* lengths_dev, const int32_t* row_start_dev, const int32_t* path_dev, void* k_out_dev,
+                   int ldk, void* v_out_dev, int ldv, int row_dtype, int n_rows, int max_rows, int32_t* status_dev,
+                   void* cuda_stream);
+
+/* Attention of new rows over the cache, in one layer; the rows' own keys and values
+ * have been written to it.  q_dev and out_dev: n_rows rows of n_q_heads x head_dim
+ * of row_dtype; q head h reads kv head h / (n_q_heads / n_kv_heads), at most 1024
+ * of them one; scale 1 / sqrt(head_dim).  A row sees every position held and, of
+ * the sequence's new rows, itself and those before it (masks_dev NULL: a prompt's
+ * chunk, or one token), or row j if bit j of its mask is set (masks_dev: uint64
+ * [n_rows], 8-byte aligned; a drafted tree, max_rows up to
+ * Q3TTS_MAX_TREE_NODES).  One that sees nothing gets zeroes.  What a row does not
+ * see does not touch it, NaN among it; a row that sees a NaN is unspecified, like
+ * one with scores above 2^27, or values above 2^60 in size.  Blocks whose power is
+ * below 2^-60 count as zeroes in the values.  Rows outside every sequence's range
+ * are left as they were; page ids outside the pool leave the sequence's rows
+ * unspecified.  No row of out may share a byte with one of q (Q3TTS_ERR_ARG).
+ * Caches of up to 2^31 rows of head_dim elements in all (else
+ * Q3TTS_ERR_UNSUPPORTED).  Scores, weights and sums are held in 32 bits and rounded
+ * once to row_dtype; a row's result does not depend on the run, but may on n_seqs,
+ * max_rows and pages_per_seq, which decide how positions are split. */
+int q3tts_kv8_attention(const q3tts_kv8_cache* kv, int layer, const int32_t* page_table_dev, int pages_per_seq,
+                        int n_seqs, const int32_t* lengths_dev, const int32_t* row_start_dev,
+                        const uint64_t* masks_dev, const void* q_dev, int ldq, void* out_dev, int ldo, int n_q_heads,
+                        int row_dtype, int n_rows, int max_rows, int32_t* status_dev, void* cuda_stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* Q3TTS_KV8_H */
