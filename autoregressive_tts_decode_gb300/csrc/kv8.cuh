@@ -65,6 +65,10 @@ struct Kv8AttnArgs {
   const void* q;
   void* out;
   int ldq, ldo, Hq;
+  // the limit of the waits inside the kernels in units of 1024 cycles and, for the test of
+  // their running out, the position tile at which the first CTA's products are lost (-1: none)
+  int wait_1024 = 4 << 20;  // ~2 s
+  int lost_tile = -1;
 };
 
 // Quantising writes and reading back (kv8_cache.cu).

@@ -131,6 +131,11 @@ int q3tts_kv8_attention(const q3tts_kv8_cache* kv, int layer, const int32_t* pag
   a.ldq = ldq;
   a.ldo = ldo;
   a.Hq = n_q_heads;
+  const q3::Lose l = q3::take_lose();
+  if (l.armed) {
+    a.lost_tile = l.tile;
+    a.wait_1024 = l.wait_1024();
+  }
   return q3::launch_kv8_attention(a, kv->layers, row_dtype, (cudaStream_t)cuda_stream);
 }
 

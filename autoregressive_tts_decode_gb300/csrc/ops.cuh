@@ -19,6 +19,14 @@ constexpr int kMaxDevices = 64;  // devices the per-device launch settings cover
 // index past kMaxDevices.
 bool current_device(int* dev, int* n_sm);
 
+// q3tts_debug_lose_tile, for the calling thread's next attention (which takes it).
+struct Lose {
+  bool armed;
+  int tile, wait_us;
+  int wait_1024() const { return 2 * wait_us; }  // (at the highest SM clock, 2070 MHz; less than 2 << 22)
+};
+Lose take_lose();
+
 // Records err in *status (device int, may be NULL) unless one is recorded.
 __device__ __forceinline__ void op_status(int* status, int err) {
   if (status) atomicCAS(status, 0, err);

@@ -28,12 +28,7 @@ bool current_device(int* dev, int* n_sm) {
 
 namespace {
 
-// q3tts_debug_lose_tile, for the thread's next attention.
-struct Lose {
-  bool armed;
-  int tile, wait_us;
-};
-thread_local Lose lose = {};
+thread_local q3::Lose lose = {};
 
 int esz(int dtype) { return dtype == Q3TTS_F32 ? 4 : 2; }
 
@@ -104,6 +99,12 @@ bool sets_meet(const q3tts_rows* sets, int n_sets, bool ids, long long n_in, lon
 
 }  // namespace
 
+q3::Lose q3::take_lose() {
+  const Lose l = lose;
+  lose.armed = false;
+  return l;
+}
+
 extern "C" {
 
 int q3tts_tree_attention(const q3tts_kv_cache* kv, int layer, const int32_t* page_table_dev, int pages_per_seq,
@@ -144,10 +145,10 @@ int q3tts_tree_attention(const q3tts_kv_cache* kv, int layer, const int32_t* pag
   a.out = out_dev;
   a.ldo = ldo;
   a.status = status_dev;
-  if (lose.armed) {
-    a.lost_tile = lose.tile;
-    a.wait_1024 = 2 * lose.wait_us;  // (at the highest SM clock, 2070 MHz; less than 2 << 22)
-    lose.armed = false;
+  const q3::Lose l = q3::take_lose();
+  if (l.armed) {
+    a.lost_tile = l.tile;
+    a.wait_1024 = l.wait_1024();
   }
   return q3::launch_tree_attention(a, kv->layers, kv->kv_dtype, (cudaStream_t)cuda_stream);
 }

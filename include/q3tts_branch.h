@@ -142,7 +142,7 @@ int q3tts_tree_attention(const q3tts_kv_cache* kv, int layer, const int32_t* pag
                          int ldq, float* out_dev, int ldo, int32_t* status_dev, void* cuda_stream);
 
 /* Test hook for the attention's failure path: arms the calling thread's next
- * q3tts_tree_attention that reaches the device so that the products of its first
+ * q3tts_tree_attention (or q3tts_kv8_attention) that reaches the device so that the products of its first
  * CTA are lost from position tile `tile` (0-based, 128 positions each) on, and
  * every wait inside the kernel gives up after about wait_us microseconds.  No GPU
  * fault, trap or endless wait is involved: the waits for those products run out,
