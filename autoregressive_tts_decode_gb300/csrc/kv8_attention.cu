@@ -20,8 +20,7 @@
 // largest c s_p + b_p so far.  It is followed only when a weight passes 2^3: weights up to 2^4
 // have a step of 2^-28, and a tile needs one vote of the softmax threads instead of
 // a maximum over them.  The sum of 2^(c s_p - base) is held beside it in fp32.
-#include "kv8.cuh"
-#include "tree.cuh"
+#include "kv8_tiles.cuh"
 
 namespace q3 {
 
@@ -30,7 +29,6 @@ namespace {
 constexpr int KF_DIGITS = 8;
 constexpr float KF_SLACK = 8.f;          // how large a weight may be
 constexpr float KF_STEP = 268435456.f;  // 2^28: its fixed-point step
-constexpr int KF_SORT = 256;            // sequences that are dealt by length, at most
 
 template <int HD, int R>
 struct KfCfg {
@@ -63,13 +61,6 @@ struct KfCtl {
   float fac[8][R];
 };
 
-struct KfDeal {
-  int items, row_tiles, box, vec;
-  unsigned rep_inv;
-  int sorted;
-  int wait_1024, lost_tile;
-};
-
 // kind::f8f6f4: D fp32, A and B E4M3, B K-major; A K-major or M-major (bit 15).
 __host__ __device__ constexpr uint32_t f8_idesc(int M, int N, bool a_m_major) {
   return (1u << 4) | (a_m_major ? 1u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -81,19 +72,6 @@ __device__ __forceinline__ void mma_f8(uint32_t tmem_d, uint64_t a, uint64_t b, 
       "l"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
 }
-// Swizzled operand tiles with rows of W bytes (128 or 64) in atoms of eight rows.
-template <int W>
-__device__ __forceinline__ uint64_t sw_desc(uint32_t saddr, uint32_t lead = 16) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lead & 0x3FFFFu) >> 4) << 16) | ((uint64_t)(8 * W >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)(W == 128 ? 2 : 4) << 61);
-}
-// Byte offset of 16-byte chunk c of row r in such a tile.
-template <int W>
-__device__ __forceinline__ uint32_t sw_at(int r, int c) {
-  const uint32_t o = (uint32_t)(r * W + c * 16);
-  return W == 128 ? o ^ ((o >> 3) & 0x70u) : o ^ ((o >> 3) & 0x30u);
-}
-
 __device__ __forceinline__ bool kf_vote(bool p) {
   uint32_t r;
   asm volatile(
@@ -103,39 +81,6 @@ __device__ __forceinline__ bool kf_vote(bool p) {
       : "memory");
   return r != 0;
 }
-
-// Four consecutive elements of a row of q.
-__device__ __forceinline__ float4 q4(const float* p, bool wide) {
-  return wide ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
-}
-__device__ __forceinline__ float4 q4(const bf16* p, bool wide) {
-  if (!wide) return make_float4(to_f(p[0]), to_f(p[1]), to_f(p[2]), to_f(p[3]));
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xffff0000u));
-}
-
-struct KfItem {
-  Kv8Seq t;
-  int seq, g, n0, rows;  // kv head, first row of the tile, rows
-  int end;               // positions that its rows may see
-  int t0, nt;            // first position tile, tiles
-};
-
-// Position p of a sequence: its page's entry of the table and slot.
-struct Place {
-  int entry, slot;
-  __device__ __forceinline__ Place(int pos, int page) : entry(pos / page), slot(pos - pos / page * page) {}
-  // 128 positions on (dq, dr: 128 / page, 128 % page)
-  __device__ __forceinline__ void next(int dq, int dr, int page) {
-    entry += dq;
-    slot += dr;
-    if (slot >= page) {
-      slot -= page;
-      ++entry;
-    }
-  }
-};
 
 template <class T, int HD, int R, bool TMA>
 __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
@@ -179,138 +124,24 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // the item
   KfItem m;
-  const int idx = (int)blockIdx.x / CL;
-  m.n0 = idx % d.row_tiles * R;
-  m.g = idx / d.row_tiles % a.c.Hkv;
-  m.seq = idx / d.row_tiles / a.c.Hkv;
-  if (d.sorted) {
-    // the sequences longest first
-    int* len = reinterpret_cast<int*>(sp);
-    for (int i = tid; i < a.r.n_seqs; i += C::THREADS) len[i] = a.r.lengths[i];
-    __syncthreads();
-    for (int i = tid; i < a.r.n_seqs; i += C::THREADS) {
-      const int mine = len[i];
-      int r = 0;
-#pragma unroll 8
-      for (int j = 0; j < a.r.n_seqs; ++j) {
-        const int o = len[j];
-        r += o > mine || (o == mine && j < i);
-      }
-      if (r == m.seq) ctl.seq = i;
-    }
-  }
+  const int wanted = first_item(a, d, CL, R, m);
+  if (d.sorted) find_sequence<C::THREADS>(a.r, wanted, reinterpret_cast<int*>(sp), &ctl.seq);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (d.sorted) m.seq = ctl.seq;
+  m.seq = d.sorted ? ctl.seq : wanted;
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
   const uint32_t ring = sbase + C::RING;
-  const bool have = kv8_seq(a.r, a.c.page, m.seq, true, m.t) && m.n0 < m.t.n * rep;
-  m.rows = m.nt = m.t0 = m.end = 0;
-  if (have) {
-    m.rows = min(R, m.t.n * rep - m.n0);
-    m.end = m.t.L + (a.masks ? m.t.n : div_rep(m.n0 + m.rows - 1, rep, d.rep_inv) + 1);
-    const int all = (m.end + TM_PT - 1) / TM_PT, per = (all + CL - 1) / CL;
-    m.t0 = min(all, rank * per);
-    m.nt = min(all, m.t0 + per) - m.t0;
-  }
+  const bool have = take_item(a, d, CL, rank, R, m);
   const int ps = a.c.page, dq = TM_PT / ps, dr = TM_PT % ps;
   const int* table = a.r.page_table + (size_t)m.seq * a.r.pps;
-  // a page that is not the pool's is reported and read as page 0
-  auto checked = [&](int page) -> int {
-    if (page >= 0 && page < a.c.n_pages) return page;
-    op_status(status, Q3TTS_ERR_ARG);
-    return 0;
-  };
   bool ok = true;
-
   int issued = 0;  // tiles that the loading warp has filled or is filling
 
   if (m.nt > 0) {
     if (warp == C::LOAD_WARP) {
-      if constexpr (TMA) {
-        // lane (kv, b): box b of a tile's keys or values
-        const int kv = lane >> 4, b = lane & 15, boxes = TM_PT / d.box;
-        auto page_of = [&](int i) -> int {
-          const int pos = (m.t0 + i) * TM_PT + b * d.box;
-          return b < boxes && i < m.nt && pos < m.end ? __ldg(table + pos / ps) : 0;
-        };
-        int page0 = page_of(0), page1 = page_of(1);  // looked up two tiles ahead
-        for (int i = 0; i < m.nt; ++i) {
-          const int pos = (m.t0 + i) * TM_PT + b * d.box;
-          const int held = min(TM_PT, m.end - (m.t0 + i) * TM_PT);
-          const bool mine = b < boxes && pos < m.end;
-          const int row = mine ? (int)kv8_row(a.c, checked(page0), kv, m.g, pos % ps) : 0;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int it = 2 * i + h, slot = it % C::S;
-            ok = ok && tm_wait(su32(&ctl.empty[slot]), ((uint32_t)(it / C::S) & 1u) ^ 1u, abort_w, status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const uint32_t fb = su32(&ctl.full[slot]);
-            if (lane == 0) mbar_expect_tx(fb, (uint32_t)((held + d.box - 1) / d.box * d.box * HD));
-            __syncwarp();
-            if (mine && kv == h) tma_load(ring + slot * C::SLOT + b * d.box * HD, &map, 0, row, fb);
-            ++issued;
-          }
-          if (!ok) break;
-          page0 = page1;
-          page1 = page_of(i + 2);
-        }
-      } else {
-        // 16-byte copies, row by row: lane l has chunk l % CH of rows l / CH, ..
-        constexpr int CH = HD / 16, RPI = 32 / CH;
-        const int c = lane % CH;
-        const long long plane = (long long)a.c.Hkv * ps;
-        int row[TM_PT / 32], page[TM_PT / 32];  // pool rows of positions lane + 32 j of the tile; the next tile's pages
-        auto look_up = [&](int i) {
-#pragma unroll
-          for (int j = 0; j < TM_PT / 32; ++j) {
-            const int pos = (m.t0 + i) * TM_PT + lane + 32 * j;
-            page[j] = i < m.nt && pos < m.end ? __ldg(table + pos / ps) : 0;
-          }
-        };
-        look_up(0);
-        int arrived = 0;
-        for (int i = 0; i < m.nt && ok; ++i) {
-#pragma unroll
-          for (int j = 0; j < TM_PT / 32; ++j) {
-            const int pos = (m.t0 + i) * TM_PT + lane + 32 * j;
-            row[j] = pos < m.end ? (int)kv8_row(a.c, checked(page[j]), 0, m.g, pos % ps) : -1;
-          }
-          look_up(i + 1);
-          for (int h = 0; h < 2; ++h) {
-            const int it = 2 * i + h, slot = it % C::S;
-            ok = tm_wait(su32(&ctl.empty[slot]), ((uint32_t)(it / C::S) & 1u) ^ 1u, abort_w, status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const uint32_t dst = ring + slot * C::SLOT;
-            const uint8_t* src = a.c.codes + (h ? plane * HD : 0) + c * 16;
-#pragma unroll
-            for (int j = 0; j < TM_PT / 32; ++j)
-#pragma unroll 8
-              for (int e = lane / CH; e < 32; e += RPI) {
-                const int from = __shfl_sync(0xffffffffu, row[j], e);
-                if (from >= 0)
-                  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + sw_at<HD>(32 * j + e, c)),
-                               "l"(src + (size_t)from * HD)
-                               : "memory");
-              }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            ++issued;
-            if (issued - arrived > 2) {  // (two tiles stay on their way)
-              asm volatile("cp.async.wait_group 2;" ::: "memory");
-              proxy_fence();
-              mbar_arrive(su32(&ctl.full[arrived++ % C::S]));
-            }
-          }
-        }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        proxy_fence();
-        for (; arrived < issued; ++arrived) mbar_arrive(su32(&ctl.full[arrived % C::S]));
-      }
+      ok = load_tiles<HD, C::S, TMA>(&map, a, m, d.box, ring, ctl.full, ctl.empty, issued, abort_w);
     } else if (warp == C::MMA_WARP) {
       if (elect_one()) {
         constexpr uint32_t idS = f8_idesc(TM_PT, C::N, false), idO = f8_idesc(TM_PT, C::N, true);
@@ -624,138 +455,26 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
 }
 
-// The codes as a matrix of head-dim rows, read one page's rows (at most a tile's) at a time.
-bool codes_map(const Kv8Cache& c, int layers, int box, CUtensorMap* map) {
-  const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
-  if (!enc) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)c.hd, (cuuint64_t)((long long)layers * c.n_pages * 2 * c.Hkv * c.page)};
-  const cuuint64_t strides[1] = {(cuuint64_t)c.hd};
-  const cuuint32_t boxd[2] = {(cuuint32_t)c.hd, (cuuint32_t)box};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c.codes, dims, strides, boxd, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             c.hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <class T, int HD, int R, bool TMA>
-int launch_few(const Kv8AttnArgs& a, int layers, int dev, int n_sm, cudaStream_t s) {
+int launch_few(const Kv8AttnArgs& a, int layers, int dev, cudaStream_t s) {
   using C = KfCfg<HD, R>;
-  static TmKernel known_of[kMaxDevices];
-  TmKernel& known = known_of[dev];
-  auto kernel = kv8_few_kernel<T, HD, R, TMA>;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  if (!known.ready.load(std::memory_order_acquire)) {
-    std::lock_guard<std::mutex> one(known.filling);
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess) return Q3TTS_ERR_CUDA;
-    cfg.numAttrs = 1;
-    for (int c = 1; c <= 8 && !known.ready.load(std::memory_order_relaxed); ++c) {
-      cfg.gridDim = dim3(c);
-      at[0].val.clusterDim.x = c;
-      if (cudaOccupancyMaxActiveClusters(&known.clusters[c], kernel, &cfg) != cudaSuccess) return Q3TTS_ERR_CUDA;
-    }
-    known.ready.store(true, std::memory_order_release);
-  }
-  KfDeal d;
-  d.box = a.c.page < TM_PT ? a.c.page : TM_PT;
-  CUtensorMap map = {};
-  if (TMA && !codes_map(a.c, layers, d.box, &map)) return Q3TTS_ERR_CUDA;
-  const int rep = a.Hq / a.c.Hkv;
-  d.row_tiles = (int)(((long)a.r.max_rows * rep + R - 1) / R);
-  const long items = (long)a.r.n_seqs * a.c.Hkv * d.row_tiles;
-  if (items > 0x7fffffffL / 8) return Q3TTS_ERR_UNSUPPORTED;
-  d.items = (int)items;
-  const int tiles = (int)(((long)a.r.pps * a.c.page + TM_PT - 1) / TM_PT);
-  const int c = cluster_size(items, tiles, known);
-  const size_t al = 4 * sizeof(T);
-  d.vec = ((uintptr_t)a.q & (al - 1)) == 0 && a.ldq % 4 == 0;
-  d.rep_inv = (unsigned)(((1ull << 32) + rep - 1) / rep);
-  d.sorted = items * c > known.clusters[1] && a.r.n_seqs > 1 && a.r.n_seqs <= KF_SORT;
-  d.wait_1024 = a.wait_1024;
-  d.lost_tile = a.lost_tile;
-  cfg.gridDim = dim3((unsigned)(items * c));
-  at[0].val.clusterDim.x = c;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, map, a, d) == cudaSuccess ? Q3TTS_OK : Q3TTS_ERR_CUDA;
+  static TmKernel known[kMaxDevices];
+  return launch_tiles(kv8_few_kernel<T, HD, R, TMA>, known[dev], C::THREADS, C::SMEM, TMA, R, 4 * sizeof(T), a, layers, s);
 }
 
 template <class T, int HD, bool TMA>
-int launch_few_rows(const Kv8AttnArgs& a, int layers, int dev, int n_sm, cudaStream_t s) {
+int launch_few_rows(const Kv8AttnArgs& a, int layers, int dev, cudaStream_t s) {
   const long rows = (long)a.r.max_rows * (a.Hq / a.c.Hkv);
-  if (rows <= 2) return launch_few<T, HD, 2, TMA>(a, layers, dev, n_sm, s);
-  if (rows <= 4) return launch_few<T, HD, 4, TMA>(a, layers, dev, n_sm, s);
-  if (rows <= 8) return launch_few<T, HD, 8, TMA>(a, layers, dev, n_sm, s);
-  return launch_few<T, HD, 16, TMA>(a, layers, dev, n_sm, s);
+  if (rows <= 2) return launch_few<T, HD, 2, TMA>(a, layers, dev, s);
+  if (rows <= 4) return launch_few<T, HD, 4, TMA>(a, layers, dev, s);
+  if (rows <= 8) return launch_few<T, HD, 8, TMA>(a, layers, dev, s);
+  return launch_few<T, HD, 16, TMA>(a, layers, dev, s);
 }
 
-template <class T, int HD>
-int launch_few_mode(const Kv8AttnArgs& a, int layers, int dev, int n_sm, cudaStream_t s) {
-  // TMA boxes are pages of whole swizzle atoms (8 rows) that fill a tile a whole
-  // number of times, or whole tiles of larger pages
-  const int ps = a.c.page;
-  if ((ps >= 8 && ps <= TM_PT && TM_PT % ps == 0) || ps % TM_PT == 0) return launch_few_rows<T, HD, true>(a, layers, dev, n_sm, s);
-  return launch_few_rows<T, HD, false>(a, layers, dev, n_sm, s);
-}
-
-constexpr int KA_THREADS = 128;
-
-template <class T, int HD>
-__global__ void __launch_bounds__(KA_THREADS) kv8_rows_kernel(const __grid_constant__ Kv8AttnArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  constexpr int EPL = HD / 32;  // elements of a lane
-  const int lane = threadIdx.x & 31;
-  const int h = blockIdx.y, seq = blockIdx.z, i = blockIdx.x * (KA_THREADS / 32) + (threadIdx.x >> 5);
-  Kv8Seq t;
-  if (!kv8_seq(a.r, a.c.page, seq, true, t) || i >= t.n) return;
-  const int row = t.row0 + i, g = h / (a.Hq / a.c.Hkv);
-  const T* qp = static_cast<const T*>(a.q) + (size_t)row * a.ldq + h * HD + lane * EPL;
-  float q[EPL], o[EPL];
-#pragma unroll
-  for (int e = 0; e < EPL; ++e) {
-    q[e] = to_f(qp[e]) / sqrtf((float)HD);
-    o[e] = 0.f;
-  }
-  const unsigned long long mask = a.masks ? a.masks[row] : 0;
-  const int end = t.L + (a.masks ? t.n : i + 1);
-  float m = -INFINITY, l = 0.f;
-  for (int p = 0; p < end; ++p) {
-    if (p >= t.L && a.masks && !((mask >> (p - t.L)) & 1)) continue;
-    int page = __ldg(a.r.page_table + (size_t)seq * a.r.pps + p / a.c.page);
-    if (page < 0 || page >= a.c.n_pages) {
-      op_status(a.r.status, Q3TTS_ERR_ARG);
-      page = 0;
-    }
-    const long long kr = kv8_row(a.c, page, 0, g, p % a.c.page), vr = kv8_row(a.c, page, 1, g, p % a.c.page);
-    float f[4];
-    auto load = [&](long long at) {
-      const uint8_t* c = a.c.codes + at * HD + lane * EPL;
-      fp8x4_to_f32(EPL == 4 ? *reinterpret_cast<const uint32_t*>(c) : *reinterpret_cast<const uint16_t*>(c), f);
-    };
-    load(kr);
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) s = fmaf(q[e], f[e], s);
-    s = warp_sum(s) * kv8_power(a.c.powers[kr / a.c.block]);
-    load(vr);
-    const float top = fmaxf(m, s), was = expf(m - top), w = expf(s - top);
-    const float wv = w * kv8_power(a.c.powers[vr / a.c.block]);
-    m = top;
-    l = l * was + w;
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) o[e] = fmaf(wv, f[e], o[e] * was);
-  }
-  T* op = static_cast<T*>(a.out) + (size_t)row * a.ldo + h * HD + lane * EPL;
-#pragma unroll
-  for (int e = 0; e < EPL; ++e) op[e] = from_f<T>(l > 0.f ? o[e] / l : 0.f);
+template <class T>
+int launch_few_of(const Kv8AttnArgs& a, int layers, bool tma, int dev, cudaStream_t s) {
+  if (a.c.hd == 128) return tma ? launch_few_rows<T, 128, true>(a, layers, dev, s) : launch_few_rows<T, 128, false>(a, layers, dev, s);
+  return tma ? launch_few_rows<T, 64, true>(a, layers, dev, s) : launch_few_rows<T, 64, false>(a, layers, dev, s);
 }
 
 }  // namespace
@@ -763,17 +482,12 @@ __global__ void __launch_bounds__(KA_THREADS) kv8_rows_kernel(const __grid_const
 int launch_kv8_attention(const Kv8AttnArgs& a, int layers, int dtype, cudaStream_t s) {
   int dev = 0, n_sm = 0;
   if (!current_device(&dev, &n_sm)) return Q3TTS_ERR_CUDA;
-  if ((long)a.r.max_rows * (a.Hq / a.c.Hkv) <= 32) {
-    if (dtype == Q3TTS_F32)
-      return a.c.hd == 128 ? launch_few_mode<float, 128>(a, layers, dev, n_sm, s) : launch_few_mode<float, 64>(a, layers, dev, n_sm, s);
-    return a.c.hd == 128 ? launch_few_mode<bf16, 128>(a, layers, dev, n_sm, s) : launch_few_mode<bf16, 64>(a, layers, dev, n_sm, s);
-  }
-  const dim3 grid((a.r.max_rows + 3) / 4, a.Hq, a.r.n_seqs);
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, dim3(KA_THREADS), 0, s, a) == cudaSuccess ? Q3TTS_OK : Q3TTS_ERR_CUDA;
-  };
-  if (dtype == Q3TTS_F32) return a.c.hd == 128 ? go(kv8_rows_kernel<float, 128>) : go(kv8_rows_kernel<float, 64>);
-  return a.c.hd == 128 ? go(kv8_rows_kernel<bf16, 128>) : go(kv8_rows_kernel<bf16, 64>);
+  // TMA boxes are pages of whole swizzle atoms (8 rows) that fill a tile a whole
+  // number of times, or whole tiles of larger pages
+  const int ps = a.c.page;
+  const bool tma = (ps >= 8 && ps <= TM_PT && TM_PT % ps == 0) || ps % TM_PT == 0;
+  if ((long)a.r.max_rows * (a.Hq / a.c.Hkv) > 32) return launch_kv8_wide(a, layers, dtype, tma, dev, s);
+  return dtype == Q3TTS_F32 ? launch_few_of<float>(a, layers, tma, dev, s) : launch_few_of<bf16>(a, layers, tma, dev, s);
 }
 
 }  // namespace q3

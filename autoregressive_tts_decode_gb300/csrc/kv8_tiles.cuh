@@ -1,0 +1,275 @@
+// kv8_tiles.cuh -- what the tensor-core kernels of the 8-bit cache's attention share
+// (kv8_attention.cu, kv8_wide.cu): items of work, the loading of code tiles, operand
+// descriptors, the launch.
+#pragma once
+
+#include "kv8.cuh"
+#include "tree.cuh"
+
+namespace q3 {
+
+// Tiles of 128 rows (kv8_wide.cu); tma: whether pages come in boxes (load_tiles).
+int launch_kv8_wide(const Kv8AttnArgs& a, int layers, int dtype, bool tma, int dev, cudaStream_t s);
+
+namespace {
+
+constexpr int KF_SORT = 256;  // sequences that are dealt by length, at most
+
+struct KfDeal {
+  int items, row_tiles, box;
+  int vec;  // four elements of a query row in one load
+  unsigned rep_inv;
+  int sorted;  // the sequences are taken longest first
+  int wait_1024, lost_tile;
+};
+
+struct KfItem {
+  Kv8Seq t;
+  int seq, g, n0, rows;  // kv head, first row of the tile, rows
+  int end;               // positions that its rows may see
+  int t0, nt;            // first position tile, tiles
+};
+
+// The CTA's row tile and kv head; returns its sequence, or that one's place by length. The
+// last rows of a sequence, which see the most, come first.
+__device__ __forceinline__ int first_item(const Kv8AttnArgs& a, const KfDeal& d, int cl, int rows, KfItem& m) {
+  const int idx = (int)blockIdx.x / cl;
+  m.g = idx % a.c.Hkv;
+  m.n0 = (d.row_tiles - 1 - idx / a.c.Hkv % d.row_tiles) * rows;
+  return idx / a.c.Hkv / d.row_tiles;
+}
+// The sequence that is the wanted-th longest (all threads; len: room for KF_SORT; ordered by
+// the caller's next barrier).
+template <int THREADS>
+__device__ __forceinline__ void find_sequence(const Kv8Rows& rows, int wanted, int* len, int* seq) {
+  for (int i = threadIdx.x; i < rows.n_seqs; i += THREADS) len[i] = rows.lengths[i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows.n_seqs; i += THREADS) {
+    const int mine = len[i];
+    int r = 0;
+#pragma unroll 8
+    for (int j = 0; j < rows.n_seqs; ++j) {
+      const int o = len[j];
+      r += o > mine || (o == mine && j < i);
+    }
+    if (r == wanted) *seq = i;
+  }
+}
+// The item's rows and positions, of which the CTA has its share; false when it has no rows
+// (or the sequence does not fit, which is reported).
+__device__ __forceinline__ bool take_item(const Kv8AttnArgs& a, const KfDeal& d, int cl, int rank, int rows, KfItem& m) {
+  const int rep = a.Hq / a.c.Hkv;
+  m.rows = m.nt = m.t0 = m.end = 0;
+  if (!kv8_seq(a.r, a.c.page, m.seq, true, m.t) || m.n0 >= m.t.n * rep) return false;
+  m.rows = min(rows, m.t.n * rep - m.n0);
+  m.end = m.t.L + (a.masks ? m.t.n : div_rep(m.n0 + m.rows - 1, rep, d.rep_inv) + 1);
+  const int all = (m.end + TM_PT - 1) / TM_PT, per = (all + cl - 1) / cl;
+  m.t0 = min(all, rank * per);
+  m.nt = min(all, m.t0 + per) - m.t0;
+  return true;
+}
+
+// Position p of a sequence: its page's entry of the table and slot.
+struct Place {
+  int entry, slot;
+  __device__ __forceinline__ Place(int pos, int page) : entry(pos / page), slot(pos - pos / page * page) {}
+  // 128 positions on (dq, dr: 128 / page, 128 % page)
+  __device__ __forceinline__ void next(int dq, int dr, int page) {
+    entry += dq;
+    slot += dr;
+    if (slot >= page) {
+      slot -= page;
+      ++entry;
+    }
+  }
+};
+
+// Swizzled operand tiles with rows of W bytes (128 or 64) in atoms of eight rows.
+template <int W>
+__device__ __forceinline__ uint64_t sw_desc(uint32_t saddr, uint32_t lead = 16) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lead & 0x3FFFFu) >> 4) << 16) | ((uint64_t)(8 * W >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)(W == 128 ? 2 : 4) << 61);
+}
+// Byte offset of 16-byte chunk c of row r in such a tile.
+template <int W>
+__device__ __forceinline__ uint32_t sw_at(int r, int c) {
+  const uint32_t o = (uint32_t)(r * W + c * 16);
+  return W == 128 ? o ^ ((o >> 3) & 0x70u) : o ^ ((o >> 3) & 0x30u);
+}
+
+// Four consecutive elements of a row of q.
+__device__ __forceinline__ float4 q4(const float* p, bool wide) {
+  return wide ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
+}
+__device__ __forceinline__ float4 q4(const bf16* p, bool wide) {
+  if (!wide) return make_float4(to_f(p[0]), to_f(p[1]), to_f(p[2]), to_f(p[3]));
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xffff0000u));
+}
+
+// A warp's loads of the key and value tiles of an item, as codes, into a ring of S tiles
+// (K0 V0 K1 V1 ..).  TMA: pages of 8 positions or more that fill a tile a whole number of
+// times (or whole tiles of larger pages) come in boxes, swizzled on the way; other pages row by row in
+// 16-byte asynchronous copies, by all lanes.  issued: tiles under way or there.
+template <int HD, int S, bool TMA>
+__device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8AttnArgs& a, const KfItem& m, int box, uint32_t ring,
+                                           unsigned long long* full, unsigned long long* empty, int& issued,
+                                           volatile int* abort_w) {
+  static_assert(S >= 4, "two tiles stay on their way");
+  const int lane = threadIdx.x & 31, ps = a.c.page;
+  const int* table = a.r.page_table + (size_t)m.seq * a.r.pps;
+  int* status = a.r.status;
+  bool ok = true;
+  // a page that is not the pool's is reported and read as page 0
+  auto checked = [&](int page) -> int {
+    if (page >= 0 && page < a.c.n_pages) return page;
+    op_status(status, Q3TTS_ERR_ARG);
+    return 0;
+  };
+  if constexpr (TMA) {
+    // lane (kv, b): box b of a tile's keys or values
+    const int kv = lane >> 4, b = lane & 15, boxes = TM_PT / box;
+    auto page_of = [&](int i) -> int {
+      const int pos = (m.t0 + i) * TM_PT + b * box;
+      return b < boxes && i < m.nt && pos < m.end ? __ldg(table + pos / ps) : 0;
+    };
+    int page0 = page_of(0), page1 = page_of(1);  // looked up two tiles ahead
+    for (int i = 0; i < m.nt; ++i) {
+      const int pos = (m.t0 + i) * TM_PT + b * box;
+      const int held = min(TM_PT, m.end - (m.t0 + i) * TM_PT);
+      const bool mine = b < boxes && pos < m.end;
+      const int row = mine ? (int)kv8_row(a.c, checked(page0), kv, m.g, pos % ps) : 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int it = 2 * i + h, slot = it % S;
+        ok = ok && tm_wait(su32(&empty[slot]), ((uint32_t)(it / S) & 1u) ^ 1u, abort_w, status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t fb = su32(&full[slot]);
+        if (lane == 0) mbar_expect_tx(fb, (uint32_t)((held + box - 1) / box * box * HD));
+        __syncwarp();
+        if (mine && kv == h) tma_load(ring + slot * (TM_PT * HD) + b * box * HD, map, 0, row, fb);
+        ++issued;
+      }
+      if (!ok) break;
+      page0 = page1;
+      page1 = page_of(i + 2);
+    }
+  } else {
+    // 16-byte copies, row by row: lane l has chunk l % CH of rows l / CH, ..
+    constexpr int CH = HD / 16, RPI = 32 / CH;
+    const int c = lane % CH;
+    const long long plane = (long long)a.c.Hkv * ps;
+    int row[TM_PT / 32], page[TM_PT / 32];  // pool rows of positions lane + 32 j of the tile; the next tile's pages
+    auto look_up = [&](int i) {
+#pragma unroll
+      for (int j = 0; j < TM_PT / 32; ++j) {
+        const int pos = (m.t0 + i) * TM_PT + lane + 32 * j;
+        page[j] = i < m.nt && pos < m.end ? __ldg(table + pos / ps) : 0;
+      }
+    };
+    look_up(0);
+    int arrived = 0;
+    for (int i = 0; i < m.nt && ok; ++i) {
+#pragma unroll
+      for (int j = 0; j < TM_PT / 32; ++j) {
+        const int pos = (m.t0 + i) * TM_PT + lane + 32 * j;
+        row[j] = pos < m.end ? (int)kv8_row(a.c, checked(page[j]), 0, m.g, pos % ps) : -1;
+      }
+      look_up(i + 1);
+      for (int h = 0; h < 2; ++h) {
+        const int it = 2 * i + h, slot = it % S;
+        ok = tm_wait(su32(&empty[slot]), ((uint32_t)(it / S) & 1u) ^ 1u, abort_w, status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t dst = ring + slot * (TM_PT * HD);
+        const uint8_t* src = a.c.codes + (h ? plane * HD : 0) + c * 16;
+#pragma unroll
+        for (int j = 0; j < TM_PT / 32; ++j)
+#pragma unroll 8
+          for (int e = lane / CH; e < 32; e += RPI) {
+            const int from = __shfl_sync(0xffffffffu, row[j], e);
+            if (from >= 0)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + sw_at<HD>(32 * j + e, c)),
+                           "l"(src + (size_t)from * HD)
+                           : "memory");
+          }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ++issued;
+        if (issued - arrived > 2) {  // (two tiles stay on their way)
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
+          proxy_fence();
+          mbar_arrive(su32(&full[arrived++ % S]));
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    proxy_fence();
+    for (; arrived < issued; ++arrived) mbar_arrive(su32(&full[arrived % S]));
+  }
+  return ok;
+}
+
+// The codes as a matrix of head-dim rows, read one page's rows (at most a tile's) at a time.
+bool codes_map(const Kv8Cache& c, int layers, int box, CUtensorMap* map) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)c.hd, (cuuint64_t)((long long)layers * c.n_pages * 2 * c.Hkv * c.page)};
+  const cuuint64_t strides[1] = {(cuuint64_t)c.hd};
+  const cuuint32_t boxd[2] = {(cuuint32_t)c.hd, (cuuint32_t)box};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c.codes, dims, strides, boxd, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             c.hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One launch: a CTA, or a cluster that splits the positions, for each item.
+template <class Kernel>
+int launch_tiles(Kernel kernel, TmKernel& known, int threads, size_t smem, bool tma, int rows, size_t vec_bytes,
+                 const Kv8AttnArgs& a, int layers, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  if (!known.ready.load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> one(known.filling);
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return Q3TTS_ERR_CUDA;
+    cfg.numAttrs = 1;
+    for (int c = 1; c <= 8 && !known.ready.load(std::memory_order_relaxed); ++c) {
+      cfg.gridDim = dim3(c);
+      at[0].val.clusterDim.x = c;
+      if (cudaOccupancyMaxActiveClusters(&known.clusters[c], kernel, &cfg) != cudaSuccess) return Q3TTS_ERR_CUDA;
+    }
+    known.ready.store(true, std::memory_order_release);
+  }
+  KfDeal d;
+  d.box = a.c.page < TM_PT ? a.c.page : TM_PT;
+  CUtensorMap map = {};
+  if (tma && !codes_map(a.c, layers, d.box, &map)) return Q3TTS_ERR_CUDA;
+  const int rep = a.Hq / a.c.Hkv;
+  d.row_tiles = (int)(((long)a.r.max_rows * rep + rows - 1) / rows);
+  const long items = (long)a.r.n_seqs * a.c.Hkv * d.row_tiles;
+  if (items > 0x7fffffffL / 8) return Q3TTS_ERR_UNSUPPORTED;
+  d.items = (int)items;
+  const int tiles = (int)(((long)a.r.pps * a.c.page + TM_PT - 1) / TM_PT);
+  const int c = cluster_size(items, tiles, known);
+  d.vec = ((uintptr_t)a.q & (vec_bytes - 1)) == 0 && a.ldq % 4 == 0;
+  d.rep_inv = (unsigned)(((1ull << 32) + rep - 1) / rep);
+  d.sorted = items * c > known.clusters[1] && a.r.n_seqs > 1 && a.r.n_seqs <= KF_SORT;
+  d.wait_1024 = a.wait_1024;
+  d.lost_tile = a.lost_tile;
+  cfg.gridDim = dim3((unsigned)(items * c));
+  at[0].val.clusterDim.x = c;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, map, a, d) == cudaSuccess ? Q3TTS_OK : Q3TTS_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace q3

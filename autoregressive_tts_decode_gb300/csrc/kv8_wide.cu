@@ -1,0 +1,569 @@
+// kv8_wide.cu -- attention of many new rows over the 8-bit cache (chunks of prompts, large
+// drafted trees): 128 rows (new rows x q heads of a kv head's group) to a tile.
+//
+// The mathematics are kv8_attention.cu's.  From some rows on the tensor cores are the bound, and
+// two fp16 products cost less than eight of E4M3: fp16 holds every E4M3 code, and two fp16
+// terms hold 22 bits of a query or a weight.  Of bf16 rows a query is one term (fp16 has the more bits, and
+// the row is scaled so that its largest element is 2^14 or more), and so is a weight: its 11 bits are
+// rounded off by half a step, 2^-11 of it, against the output's own 2^-8.
+//   S = Q K^T  M 128 rows, N 128 positions: Q in tensor memory, K converted;
+//   O = P V    P in tensor memory, in its scores' place, V converted (an N-major operand).
+// The small terms are multiplied first into one accumulator; the outputs of successive tiles
+// are added in fp32 registers.  Keys' powers are factors of the scores' columns, values' powers of the
+// weights', both in fp32; a row's base is its largest score and power so far, less 8 (weights of
+// 2^8, and up to 2^15 before the base follows: fp16's smallest step is 2^-24).
+//
+// Roles of a CTA (one per SM): a warp loads codes, four convert them (a row's 16 codes a lane), one
+// thread issues the MMAs (scores of tile t + 1 before the outputs of tile t), and two groups of
+// four warps are the softmax, each with half of a tile's positions and half of the
+// output's elements (one thread a row and half).  The tensor cores work in order, which orders most of what shares
+// tensor memory: the scores of tile t + 2 come after the outputs of tile t, which have
+// read P where they go; the outputs of tile t + 1 wait for its P, which the softmax announces
+// when it has also read the outputs of tile t.
+#include "kv8_tiles.cuh"
+
+namespace q3 {
+
+namespace {
+
+constexpr int KW_ROWS = 128;  // rows of a tile
+constexpr int KW_SOFT = 256;  // softmax threads
+constexpr int KW_CONV = 128;  // converting threads
+constexpr float KW_BASE = 8.f, KW_MOST = 15.f;  // log2 of the weights at the base, and at most
+
+template <class T, int HD>
+struct KwCfg {
+  static constexpr int MMA_WARP = 8, LOAD_WARP = 9, CONV_WARP = 12, THREADS = 512;
+  static constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;
+  static constexpr uint32_t TILE = TM_PT * HD * 2;   // a converted K or V tile
+  static constexpr uint32_t SLOT = TM_PT * HD;       // a tile of codes
+  static constexpr int S = 4 * (128 / HD);           // tiles of codes in their ring
+  static constexpr uint32_t K = 0, V = 2 * TILE, RING = 4 * TILE, CTL = RING + S * SLOT;
+  static constexpr int LD = HD + 4;                  // a row of the outputs in shared memory
+  static constexpr size_t SMEM = 227 * 1024;         // (all of an SM's, as of its tensor memory)
+  // columns: scores and P of even and of odd tiles, outputs, queries
+  static constexpr uint32_t TM_O = 256, TM_Q = 384, TM_QT = HD / 2;
+  static_assert(KW_ROWS * LD * 4 <= 4 * TILE, "the outputs, where the converted tiles were");
+};
+
+template <int S>
+struct KwCtl {
+  unsigned long long full[S], empty[S], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full, o_full, q_full, done, pw_full[4];
+  uint32_t tmem;
+  int abort_w[2];  // given up, limit of the waits
+  int seq;
+  unsigned bad[4][4];         // positions of a tile with a NaN value that rows may see
+  float2 power[4][TM_PT];     // factors of a position's scores and weights
+  float part[2][KW_ROWS];
+  float base[KW_ROWS], sum[KW_ROWS];
+  float fac[8][KW_ROWS];
+  int len[KF_SORT];
+};
+
+// kind::f16: D fp32, A and B fp16, A in tensor memory; B K-major or N-major (bit 16).
+__host__ __device__ constexpr uint32_t h16_idesc(int M, int N, bool b_n_major) {
+  return (1u << 4) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(
+          tmem_d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]),
+        "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]),
+        "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Two floats to fp16 (x in the low half), and back.
+__device__ __forceinline__ uint32_t pack_half(float x, float y) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_half(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
+// Four E4M3 codes as fp16.
+__device__ __forceinline__ uint2 codes_half(uint32_t w) {
+  uint2 r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.x) : "h"(static_cast<unsigned short>(w & 0xffffu)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.y) : "h"(static_cast<unsigned short>(w >> 16)));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return fma2(a, b, make_float2(0.f, 0.f)); }
+// Barrier and vote of the softmax threads.
+__device__ __forceinline__ bool kw_vote(bool p, int id) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+template <class T, int HD, bool TMA>
+__global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
+    kv8_wide_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ Kv8AttnArgs a, const KfDeal d) {
+  using C = KwCfg<T, HD>;
+  using Ctl = KwCtl<C::S>;
+  static_assert(1024 + C::CTL + sizeof(Ctl) <= C::SMEM, "shared memory");
+  extern __shared__ uint8_t kw_raw[];
+  const uint32_t raw = su32(kw_raw), sbase = (raw + 1023u) & ~1023u;
+  uint8_t* sp = kw_raw + (sbase - raw);
+  Ctl& ctl = *reinterpret_cast<Ctl*>(sp + C::CTL);
+  volatile int* abort_w = ctl.abort_w;
+  int* status = a.r.status;
+
+  namespace cg = cooperative_groups;
+  cg::cluster_group cl = cg::this_cluster();
+  const int CL = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int rep = a.Hq / a.c.Hkv;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::S; ++i) {
+      mbar_init(su32(&ctl.full[i]), TMA ? 1 : 32);
+      mbar_init(su32(&ctl.empty[i]), KW_CONV);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(su32(&ctl.k_full[i]), KW_CONV);
+      mbar_init(su32(&ctl.v_full[i]), KW_CONV);
+      mbar_init(su32(&ctl.k_empty[i]), 1);
+      mbar_init(su32(&ctl.v_empty[i]), 1);
+      mbar_init(su32(&ctl.s_full[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(su32(&ctl.pw_full[i]), KW_CONV);
+    mbar_init(su32(&ctl.p_full), KW_SOFT);
+    mbar_init(su32(&ctl.o_full), 1);
+    mbar_init(su32(&ctl.q_full), KW_SOFT);
+    mbar_init(su32(&ctl.done), 1);
+    ctl.abort_w[0] = 0;
+    ctl.abort_w[1] = d.wait_1024;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();  // q and the rows written to the cache come from the previous kernels
+  pdl_trigger();
+  // (tensor memory after the wait: a kernel before may still be about to take its own)
+  if (warp == C::MMA_WARP) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&ctl.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  KfItem m;
+  const int wanted = first_item(a, d, CL, KW_ROWS, m);
+  if (d.sorted) find_sequence<C::THREADS>(a.r, wanted, ctl.len, &ctl.seq);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  m.seq = d.sorted ? ctl.seq : wanted;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
+  const bool have = take_item(a, d, CL, rank, KW_ROWS, m);
+  bool ok = true;
+  int issued = 0;  // tiles that the loading warp has filled or is filling
+  float* os = reinterpret_cast<float*>(sp);  // [KW_ROWS][LD]: the outputs, where the converted tiles were
+
+  if (m.nt > 0) {
+    if (warp == C::LOAD_WARP) {
+      ok = load_tiles<HD, C::S, TMA>(&map, a, m, d.box, sbase + C::RING, ctl.full, ctl.empty, issued, abort_w);
+    } else if (warp == C::MMA_WARP) {
+      // ---- MMA issue
+      if (elect_one()) {
+        constexpr uint32_t idS = h16_idesc(KW_ROWS, TM_PT, false), idO = h16_idesc(KW_ROWS, HD, true);
+        const int lost = blockIdx.x == 0 ? d.lost_tile : -1;
+        auto wait = [&](unsigned long long* bar, int phase) { return tm_wait(su32(bar), (uint32_t)phase & 1u, abort_w, status); };
+        ok = wait(&ctl.q_full, 0);
+        for (int i = 0; i <= m.nt && ok; ++i) {
+          if (i < m.nt) {  // scores of tile i
+            const int b = i & 1;
+            ok = i != lost && wait(&ctl.k_full[b], i >> 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dk = sw128_desc(sbase + C::K + b * C::TILE);
+#pragma unroll
+            for (int term = C::TERMS - 1; term >= 0; --term)
+#pragma unroll
+              for (int s = 0; s < HD / 16; ++s)
+                mma_f16_ts(tmem + b * 128, tmem + C::TM_Q + term * C::TM_QT + s * 8, dk + ((s >> 2) * TM_PT * 128 >> 4) + (s & 3) * 2, idS,
+                           term < C::TERMS - 1 || s != 0);
+            mma_commit(su32(&ctl.k_empty[b]));
+            mma_commit(su32(&ctl.s_full[b]));
+          }
+          if (i > 0) {  // outputs of tile i - 1
+            const int b = (i - 1) & 1;
+            ok = wait(&ctl.v_full[b], (i - 1) >> 1) && wait(&ctl.p_full, i - 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dv = sw128_desc(sbase + C::V + b * C::TILE, HD == 128 ? TM_PT * 128 : 1024);
+#pragma unroll
+            for (int term = C::TERMS - 1; term >= 0; --term)
+#pragma unroll
+              for (int s = 0; s < 8; ++s)  // 16 positions: eight columns of a term
+                mma_f16_ts(tmem + C::TM_O, tmem + b * 128 + 32 * (s >> 1) + 16 * term + 8 * (s & 1), dv + (s * 2048 >> 4), idO,
+                           term < C::TERMS - 1 || s != 0);
+            mma_commit(su32(&ctl.v_empty[b]));
+            mma_commit(su32(&ctl.o_full));
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp >= C::CONV_WARP) {
+      // ---- codes to fp16; a thread has a position's powers, and of a tile's rows chunk ct % CH of every RPI-th
+      constexpr int CH = HD / 16, RPI = KW_CONV / CH;
+      const int ct = tid - C::CONV_WARP * 32, c = ct % CH, cw = warp - C::CONV_WARP;
+      const int ps = a.c.page, dq = TM_PT / ps, dr = TM_PT % ps, per_page = ps / a.c.block;
+      const int* table = a.r.page_table + (size_t)m.seq * a.r.pps;
+      const size_t pstride = (size_t)a.c.Hkv * per_page;  // from a key block's power to its value block's
+      Place at(m.t0 * TM_PT + ct, ps);
+      auto powers_of = [&](int pos, const Place& x, int& kp, int& vp) {
+        kp = vp = 127;
+        if (pos < m.end) {
+          int page = __ldg(table + x.entry);
+          if (page < 0 || page >= a.c.n_pages) page = 0;  // (reported by the loading warp)
+          const uint8_t* p = a.c.powers + ((((size_t)a.c.layer * a.c.n_pages + page) * 2) * a.c.Hkv + m.g) * per_page + x.slot / a.c.block;
+          kp = __ldg(p);
+          vp = __ldg(p + pstride);
+        }
+      };
+      int kp, vp;
+      powers_of(m.t0 * TM_PT + ct, at, kp, vp);
+      for (int i = 0; i < m.nt && ok; ++i) {
+        const int b = i & 1, p0 = (m.t0 + i) * TM_PT;
+        const bool edge = p0 + TM_PT > m.t.L;  // the tile reaches past the committed positions
+        // a new row's block of NaN: rows that see it are told by its bit alone
+        const bool bad = p0 + ct >= m.t.L && (kp == 255 || vp == 255);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const int it = 2 * i + h, slot = it % C::S;
+          ok = tm_wait(su32(&ctl.full[slot]), (uint32_t)(it / C::S) & 1u, abort_w, status) &&
+               tm_wait(su32(h ? &ctl.v_empty[b] : &ctl.k_empty[b]), ((uint32_t)(i >> 1) & 1u) ^ 1u, abort_w, status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint8_t* src = sp + C::RING + slot * C::SLOT;
+          uint8_t* dst = sp + (h ? C::V : C::K) + b * C::TILE;
+          if (h == 0) {
+            // (the tile four before was done with: its outputs came before the scores whose keys' place this takes)
+            ctl.power[i & 3][ct] = bad ? make_float2(1.f, 1.f) : make_float2(kv8_power(kp), kv8_power(vp));
+            at.next(dq, dr, ps);
+            if (i + 1 < m.nt) powers_of(p0 + TM_PT + ct, at, kp, vp);
+          }
+          uint4 x[TM_PT / RPI];
+#pragma unroll
+          for (int u = 0; u < TM_PT / RPI; ++u) x[u] = *reinterpret_cast<const uint4*>(src + sw_at<HD>(ct / CH + u * RPI, c));
+          if (h && edge) {
+            // the value row of a position no row may meet is zeroed: one behind the last that is
+            // seen (whatever lies there), or a new row's with a NaN
+            unsigned found = __ballot_sync(0xffffffffu, bad);  // this warp's positions 32 cw ..
+            if (lane == 0) ctl.bad[i & 3][cw] = found;
+            asm volatile("barrier.cta.sync 3, 128;" ::: "memory");
+#pragma unroll
+            for (int u = 0; u < TM_PT / RPI; ++u) {
+              const int r = ct / CH + u * RPI, pos = p0 + r;
+              const uint32_t bits = ((x[u].x & 0x7f7f7f7fu) + 0x01010101u) | ((x[u].y & 0x7f7f7f7fu) + 0x01010101u) |
+                                    ((x[u].z & 0x7f7f7f7fu) + 0x01010101u) | ((x[u].w & 0x7f7f7f7fu) + 0x01010101u);
+              const unsigned row = ((1u << CH) - 1) << (lane / CH * CH);  // the lanes of this row
+              const bool nan = (__ballot_sync(0xffffffffu, (bits & 0x80808080u) != 0) & row) != 0 && pos >= m.t.L && pos < m.end;
+              const bool mine = nan || ((ctl.bad[i & 3][r >> 5] >> (r & 31)) & 1u);
+              if (mine || pos >= m.end) x[u] = make_uint4(0, 0, 0, 0);
+              if (nan && c == 0) atomicOr(&ctl.bad[i & 3][r >> 5], 1u << (r & 31));
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < TM_PT / RPI; ++u) {
+            const int r = ct / CH + u * RPI;
+            const uint2 p0_ = codes_half(x[u].x), p1 = codes_half(x[u].y), p2 = codes_half(x[u].z), p3 = codes_half(x[u].w);
+            uint8_t* row = dst + (c >> 2) * (TM_PT * 128) + r * 128;
+            *reinterpret_cast<uint4*>(row + (((2 * (c & 3)) ^ (r & 7)) << 4)) = make_uint4(p0_.x, p0_.y, p1.x, p1.y);
+            *reinterpret_cast<uint4*>(row + (((2 * (c & 3) + 1) ^ (r & 7)) << 4)) = make_uint4(p2.x, p2.y, p3.x, p3.y);
+          }
+          mbar_arrive(su32(&ctl.empty[slot]));
+          proxy_fence();
+          mbar_arrive(su32(h ? &ctl.v_full[b] : &ctl.k_full[b]));
+          if (h == edge) mbar_arrive(su32(&ctl.pw_full[i & 3]));  // (an edge tile's bits come with the values)
+        }
+      }
+    } else if (warp < C::MMA_WARP) {
+      // ---- softmax: group wg has positions 64 wg .. of a tile, elements wg HD / 2 .. of the output
+      constexpr int HW = HD / 2;  // elements of the output that a thread holds
+      const int wg = warp >> 2, r = tid & 127;
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const int row = m.n0 + r, node = div_rep(min(row, m.n0 + m.rows - 1), rep, d.rep_inv);
+      float qs;
+      {
+        // the row's query, scaled to 2^14 .. 2^15, in tensor memory: this group's half of it
+        const T* q = static_cast<const T*>(a.q) + (size_t)(m.t.row0 + node) * a.ldq + (size_t)(m.g * rep + min(row, m.n0 + m.rows - 1) - node * rep) * HD + wg * HW;
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < HW; e += 4) {
+          const float4 x = q4(q + e, d.vec & 1);
+          top = max(max(top, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu)),
+                    max(__float_as_uint(x.z) & 0x7fffffffu, __float_as_uint(x.w) & 0x7fffffffu));
+        }
+        ctl.part[wg][r] = __uint_as_float(top);
+        kw_vote(false, 1);
+        top = max(top, __float_as_uint(ctl.part[wg ^ 1][r]));
+        const int E = min(max((int)(top >> 23) - 126, -100), 127);  // |q| < 2^E
+        const float by = __int_as_float((127 + 15 - E) << 23);
+        qs = 1.4426950408889634f / sqrtf((float)HD) * __int_as_float((127 - 15 + E) << 23);
+#pragma unroll 1
+        for (int e0 = 0; e0 < HW; e0 += 32) {
+          float x[32];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 v = q4(q + e0 + e, d.vec & 1);
+            x[e] = v.x * by;
+            x[e + 1] = v.y * by;
+            x[e + 2] = v.z * by;
+            x[e + 3] = v.w * by;
+          }
+#pragma unroll
+          for (int term = 0; term < C::TERMS; ++term) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              w[e] = pack_half(x[2 * e], x[2 * e + 1]);
+              const float2 h = unpack_half(w[e]);
+              x[2 * e] -= h.x;
+              x[2 * e + 1] -= h.y;
+            }
+            tmem_st16u(tmem + C::TM_Q + term * C::TM_QT + (wg * HW + e0) / 2 + lanes, w);
+          }
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        mbar_arrive(su32(&ctl.q_full));
+      }
+      // what the row sees of the new rows
+      unsigned long long mask = a.masks && r < m.rows ? a.masks[m.t.row0 + node] : 0ull;
+      if (m.t.n < 64) mask &= (1ull << m.t.n) - 1;
+      float base = TM_FLOOR, l = 0.f, corr = 1.f;  // the row's base, sum of weights, factor of the base's last rise
+      float2 o[HW / 2];
+#pragma unroll
+      for (int n = 0; n < HW / 2; ++n) o[n] = make_float2(0.f, 0.f);
+      for (int i = 0; i <= m.nt; ++i) {
+        const int b = i & 1;
+        const bool scores = i < m.nt;
+        if (scores) {
+          const int p0 = (m.t0 + i) * TM_PT;
+          ok = tm_wait(su32(&ctl.s_full[b]), (uint32_t)(i >> 1) & 1u, abort_w, status) &&
+               tm_wait(su32(&ctl.pw_full[i & 3]), (uint32_t)(i >> 2) & 1u, abort_w, status) && ok;
+          __syncwarp();
+          tc_fence_after();
+          const uint32_t src = tmem + b * 128 + lanes;
+          const float4* pw = reinterpret_cast<const float4*>(ctl.power[i & 3]);  // two positions each
+          // what the row sees of 32 positions: x is -inf elsewhere, NaN where a value is
+          auto see = [&](int ch, float (&x)[32]) {
+            const int dd = p0 + 32 * ch - m.t.L;  // the first of them, counted from the first new row
+            if (dd > -32) {
+              uint32_t sees;
+              if (a.masks) {
+                sees = dd >= 64 ? 0u : dd >= 0 ? (uint32_t)(mask >> dd) : (uint32_t)(mask << -dd) | ((1u << -dd) - 1);
+              } else {
+                const int n = node + 1 - dd;
+                sees = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+              }
+              const uint32_t nan = ctl.bad[i & 3][ch];
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                x[e] = !((sees >> e) & 1u) ? -INFINITY : (nan >> e) & 1u ? __uint_as_float(0x7fc00000u) : x[e];
+            }
+          };
+          // the largest score and power
+          float top = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x[32];
+            tmem_ld32f(src + 32 * (2 * wg + h), x);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float4 p = pw[(64 * wg + 32 * h + e) / 2];
+              x[e] = fmaf(x[e], p.x * qs, fminf(fmaxf((float)((__float_as_int(p.y) >> 23) - 127), -60.f), 60.f));
+              x[e + 1] = fmaf(x[e + 1], p.z * qs, fminf(fmaxf((float)((__float_as_int(p.w) >> 23) - 127), -60.f), 60.f));
+            }
+            see(2 * wg + h, x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, x[e]);
+          }
+          corr = 1.f;
+          if (kw_vote(top - base > KW_MOST || !ok, 2)) {  // both halves of a row have the same base
+            ctl.part[wg][r] = top;
+            if (kw_vote(!ok, 1)) {
+              ok = false;
+              break;
+            }
+            top = fmaxf(top, ctl.part[wg ^ 1][r]);
+            if (top - base > KW_MOST) {
+              corr = exp2_fast(base - (top - KW_BASE));
+              base = top - KW_BASE;
+              l *= corr;
+            }
+          }
+          const float2 nb = make_float2(-base, -base);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int ch = 2 * wg + h;
+            float x[32];
+            tmem_ld32f(src + 32 * ch, x);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float4 p = pw[(64 * wg + 32 * h + e) / 2];
+              const float2 v = fma2(make_float2(x[e], x[e + 1]), mul2(make_float2(p.x, p.z), make_float2(qs, qs)), nb);
+              x[e] = v.x;
+              x[e + 1] = v.y;
+            }
+            see(ch, x);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float4 p = pw[(64 * wg + 32 * h + e) / 2];
+              float2 w = make_float2(exp2_fast(x[e]), exp2_fast(x[e + 1]));
+              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], w);
+              w = mul2(w, make_float2(p.y, p.w));
+              x[e] = w.x;
+              x[e + 1] = w.y;
+            }
+#pragma unroll
+            for (int term = 0; term < C::TERMS; ++term) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                w[e] = pack_half(x[2 * e], x[2 * e + 1]);
+                if (term + 1 < C::TERMS) {
+                  const float2 g = unpack_half(w[e]);
+                  x[2 * e] -= g.x;
+                  x[2 * e + 1] -= g.y;
+                }
+              }
+              tmem_st16u(src + 32 * ch + 16 * term, w);
+            }
+          }
+          // (the running sum takes a tile's at a time: its own roundings stay few)
+          sum[0] = add2(sum[0], sum[1]);
+          l += sum[0].x + sum[0].y;
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        }
+        // the output of the tile before joins the running one: the tensor cores have had
+        // this tile's softmax to finish it
+        if (i > 0) {
+          ok = tm_wait(su32(&ctl.o_full), (uint32_t)(i - 1) & 1u, abort_w, status) && ok;
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll
+          for (int n = 0; n < HW; n += 32) {
+            float x[32];
+            tmem_ld32f(tmem + C::TM_O + wg * HW + n + lanes, x);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) o[(n + e) / 2] = add2(o[(n + e) / 2], make_float2(x[e], x[e + 1]));
+          }
+          if (__any_sync(0xffffffffu, scores && corr != 1.f)) {
+#pragma unroll
+            for (int n = 0; n < HW / 2; ++n) o[n] = make_float2(o[n].x * corr, o[n].y * corr);
+          }
+        }
+        if (scores) {
+          tc_fence_before();
+          mbar_arrive(su32(&ctl.p_full));
+        }
+      }
+      ctl.part[wg][r] = l;
+      if (kw_vote(!ok, 1)) {
+        ok = false;
+        *abort_w = 1;
+      }
+      if (wg == 0) {
+        ctl.base[r] = base;
+        ctl.sum[r] = ctl.part[0][r] + ctl.part[1][r];
+      }
+#pragma unroll
+      for (int n = 0; n < HW; n += 4)
+        *reinterpret_cast<float4*>(os + r * C::LD + wg * HW + n) = make_float4(o[n / 2].x, o[n / 2].y, o[n / 2 + 1].x, o[n / 2 + 1].y);
+    }
+  } else if (have && tid < KW_ROWS) {
+    ctl.base[tid] = TM_FLOOR;
+    ctl.sum[tid] = 0.f;
+  }
+  __syncwarp();
+  // the shares of an item are joined: what each counts for, then every CL-th row
+  if (CL > 1)
+    cl.sync();
+  else
+    __syncthreads();
+  if (have && tid < KW_ROWS) {
+    float bs[8], sm[8], mx = TM_FLOOR, all = 0.f;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      bs[s] = s < CL ? *cl.map_shared_rank(&ctl.base[tid], s) : TM_FLOOR;
+      sm[s] = s < CL ? *cl.map_shared_rank(&ctl.sum[tid], s) : 0.f;
+      mx = fmaxf(mx, bs[s]);
+    }
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      bs[s] = sm[s] == 0.f ? 0.f : exp2_fast(bs[s] - mx);  // 0: the share saw nothing
+      all = fmaf(sm[s], bs[s], all);
+    }
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s < CL) ctl.fac[s][tid] = all == 0.f ? 0.f : bs[s] / all;
+  }
+  __syncthreads();
+  if (have && !*abort_w) {
+    T* out = static_cast<T*>(a.out);
+    for (int e = tid; e < KW_ROWS * HD; e += C::THREADS) {
+      const int n = e / HD * CL + rank;
+      if (n >= m.rows) break;
+      float sum = 0.f;
+#pragma unroll
+      for (int s = 0; s < 8; ++s)  // a share without tiles wrote no output: its factor is 0
+        if (s < CL && ctl.fac[s][n] != 0.f) sum = fmaf(*(cl.map_shared_rank(os, s) + n * C::LD + e % HD), ctl.fac[s][n], sum);
+      const int row = m.n0 + n, node = div_rep(row, rep, d.rep_inv);
+      out[(size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + row - node * rep) * HD + e % HD] = from_f<T>(sum);
+    }
+  }
+  if (CL > 1) cl.sync();  // the others may still read this CTA's shared memory
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_w) {  // what is on its way lands first
+    if (TMA && warp == C::LOAD_WARP) {
+      const long long c0 = clock64();
+      for (int it = max(0, issued - C::S); it < issued; ++it)
+        while (!mbar_try_wait(su32(&ctl.full[it % C::S]), (uint32_t)(it / C::S) & 1u) && clock64() - c0 < TM_LAND_CYCLES) {
+        }
+    }
+    if (warp == C::MMA_WARP && elect_one()) land_products(su32(&ctl.done));
+    __syncwarp();
+  }
+  if (warp == C::MMA_WARP) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+template <class T, int HD, bool TMA>
+int launch_wide(const Kv8AttnArgs& a, int layers, int dev, cudaStream_t s) {
+  using C = KwCfg<T, HD>;
+  static TmKernel known[kMaxDevices];
+  return launch_tiles(kv8_wide_kernel<T, HD, TMA>, known[dev], C::THREADS, C::SMEM, TMA, KW_ROWS, 4 * sizeof(T), a, layers, s);
+}
+
+template <class T>
+int launch_wide_of(const Kv8AttnArgs& a, int layers, bool tma, int dev, cudaStream_t s) {
+  if (a.c.hd == 128) return tma ? launch_wide<T, 128, true>(a, layers, dev, s) : launch_wide<T, 128, false>(a, layers, dev, s);
+  return tma ? launch_wide<T, 64, true>(a, layers, dev, s) : launch_wide<T, 64, false>(a, layers, dev, s);
+}
+
+}  // namespace
+
+int launch_kv8_wide(const Kv8AttnArgs& a, int layers, int dtype, bool tma, int dev, cudaStream_t s) {
+  return dtype == Q3TTS_F32 ? launch_wide_of<float>(a, layers, tma, dev, s) : launch_wide_of<bf16>(a, layers, tma, dev, s);
+}
+
+}  // namespace q3

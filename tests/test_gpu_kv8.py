@@ -560,3 +560,34 @@ def test_binding_refuses(q3):
                dict(masks=m.int()), dict(max_rows=65), dict(q=q[..., :32])):
         with pytest.raises(q3.Q3TTSError):
             calls[2](good, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("case,tile", [(([300], [1], 4, 2, 128, 16, 16), 0), (([300], [1], 4, 2, 128, 16, 16), 1),
+                                       (([3000], [4], 8, 2, 128, 12, 4), 0), (([700], [9], 4, 2, 64, 32, 8), 3),
+                                       (([500], [64], 4, 2, 128, 16, 16), 1), (([900, 20], [100, 70], 16, 8, 64, 12, 12), 0),
+                                       (([9000], [64], 2, 1, 128, 16, 16), 2)])
+def test_products_that_never_come(q3, case, tile, dtype):
+    """A wait inside the kernel that runs out: reported within the limit, and the next
+    calls are right."""
+    import time
+    import torch
+    c = attend_case(np.random.default_rng(22), *case, dtype=dtype, tree=False)
+    want = run_attention(q3, c)
+
+    def run():
+        status = ku.ints([0])
+        out = run_attention(q3, c, status=status)
+        return out, int(status)
+
+    q3.debug_lose_tile(1 << 30, 2000000)  # no such tile
+    out, code = run()
+    assert code == 0 and torch.equal(out, want)
+    for _ in range(2):
+        q3.debug_lose_tile(tile, 2000)
+        t0 = time.perf_counter()
+        code = run()[1]
+        # (a share of a split item may have fewer tiles than the item)
+        assert code in ((q3.ERR_TIMEOUT,) if tile == 0 else (q3.ERR_TIMEOUT, 0)) and time.perf_counter() - t0 < 1.0
+        out, code = run()
+        assert code == 0 and torch.equal(out, want)
