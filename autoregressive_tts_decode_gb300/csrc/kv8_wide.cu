@@ -13,7 +13,7 @@
 // weights', both in fp32; a row's base is its largest score and power so far, less 8 (weights of
 // 2^8, and up to 2^15 before the base follows: fp16's smallest step is 2^-24).
 //
-// Roles of a CTA (one per SM): a warp loads codes, four convert them (a row's 16 codes a lane), one
+// Roles of a CTA (one per SM): a warp loads codes, two convert them (a row's 16 codes a lane), one
 // thread issues the MMAs (scores of tile t + 1 before the outputs of tile t), and two groups of
 // four warps are the softmax, each with half of a tile's positions and half of the
 // output's elements (one thread a row and half).  The tensor cores work in order, which orders most of what shares
@@ -28,12 +28,13 @@ namespace {
 
 constexpr int KW_ROWS = 128;  // rows of a tile
 constexpr int KW_SOFT = 256;  // softmax threads
-constexpr int KW_CONV = 128;  // converting threads
+constexpr int KW_CONV = 64;   // converting threads
+constexpr int KW_EXP = 60;  // exponents of the values' powers that count: -KW_EXP .. KW_EXP
 constexpr float KW_BASE = 8.f, KW_MOST = 15.f;  // log2 of the weights at the base, and at most
 
 template <class T, int HD>
 struct KwCfg {
-  static constexpr int MMA_WARP = 8, LOAD_WARP = 9, CONV_WARP = 12, THREADS = 512;
+  static constexpr int MMA_WARP = 8, LOAD_WARP = 9, CONV_WARP = 10, THREADS = 384;
   static constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;
   static constexpr uint32_t TILE = TM_PT * HD * 2;   // a converted K or V tile
   static constexpr uint32_t SLOT = TM_PT * HD;       // a tile of codes
@@ -52,8 +53,9 @@ struct KwCtl {
   uint32_t tmem;
   int abort_w[2];  // given up, limit of the waits
   int seq;
-  unsigned bad[4][4];         // positions of a tile with a NaN value that rows may see
-  float2 power[4][TM_PT];     // factors of a position's scores and weights
+  alignas(16) unsigned none[2][4];  // positions of a tile whose values do not count
+  unsigned bad[4][4];               // of them, new rows with a NaN
+  float4 power[4][TM_PT];     // of a position (or four that share a block): key power, value power's exponent, its inverse
   float part[2][KW_ROWS];
   float base[KW_ROWS], sum[KW_ROWS];
   float fac[8][KW_ROWS];
@@ -103,19 +105,19 @@ __device__ __forceinline__ uint2 codes_half(uint32_t w) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.y) : "h"(static_cast<unsigned short>(w >> 16)));
   return r;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return fma2(a, b, make_float2(0.f, 0.f)); }
-// Barrier and vote of the softmax threads.
+// Barrier and vote of COUNT threads.
+template <int COUNT = KW_SOFT>
 __device__ __forceinline__ bool kw_vote(bool p, int id) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"((uint32_t)p), "r"(id)
+      : "r"((uint32_t)p), "r"(id), "n"(COUNT)
       : "memory");
   return r != 0;
 }
 
-template <class T, int HD, bool TMA>
+template <class T, int HD, int GRAN, bool TMA>
 __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
     kv8_wide_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ Kv8AttnArgs a, const KfDeal d) {
   using C = KwCfg<T, HD>;
@@ -220,73 +222,95 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
       }
       __syncwarp();
     } else if (warp >= C::CONV_WARP) {
-      // ---- codes to fp16; a thread has a position's powers, and of a tile's rows chunk ct % CH of every RPI-th
-      constexpr int CH = HD / 16, RPI = KW_CONV / CH;
+      // ---- codes to fp16; a thread has chunk ct % CH of every RPI-th of a tile's rows, and two positions' powers
+      constexpr int CH = HD / 16, RPI = KW_CONV / CH, PP = TM_PT / KW_CONV;
       const int ct = tid - C::CONV_WARP * 32, c = ct % CH, cw = warp - C::CONV_WARP;
       const int ps = a.c.page, dq = TM_PT / ps, dr = TM_PT % ps, per_page = ps / a.c.block;
       const int* table = a.r.page_table + (size_t)m.seq * a.r.pps;
       const size_t pstride = (size_t)a.c.Hkv * per_page;  // from a key block's power to its value block's
-      Place at(m.t0 * TM_PT + ct, ps);
-      auto powers_of = [&](int pos, const Place& x, int& kp, int& vp) {
-        kp = vp = 127;
-        if (pos < m.end) {
-          int page = __ldg(table + x.entry);
-          if (page < 0 || page >= a.c.n_pages) page = 0;  // (reported by the loading warp)
-          const uint8_t* p = a.c.powers + ((((size_t)a.c.layer * a.c.n_pages + page) * 2) * a.c.Hkv + m.g) * per_page + x.slot / a.c.block;
-          kp = __ldg(p);
-          vp = __ldg(p + pstride);
+      Place at[PP] = {{m.t0 * TM_PT + ct, ps}, {m.t0 * TM_PT + ct + KW_CONV, ps}};
+      int kp[PP], vp[PP];
+      auto powers_of = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < PP; ++j) {
+          kp[j] = vp[j] = 127;
+          if (i < m.nt && (m.t0 + i) * TM_PT + ct + KW_CONV * j < m.end) {
+            int page = __ldg(table + at[j].entry);
+            if (page < 0 || page >= a.c.n_pages) page = 0;  // (reported by the loading warp)
+            const uint8_t* p = a.c.powers + ((((size_t)a.c.layer * a.c.n_pages + page) * 2) * a.c.Hkv + m.g) * per_page + at[j].slot / a.c.block;
+            kp[j] = __ldg(p);
+            vp[j] = __ldg(p + pstride);
+          }
+          at[j].next(dq, dr, ps);
         }
       };
-      int kp, vp;
-      powers_of(m.t0 * TM_PT + ct, at, kp, vp);
+      powers_of(0);
       for (int i = 0; i < m.nt && ok; ++i) {
         const int b = i & 1, p0 = (m.t0 + i) * TM_PT;
         const bool edge = p0 + TM_PT > m.t.L;  // the tile reaches past the committed positions
-        // a new row's block of NaN: rows that see it are told by its bit alone
-        const bool bad = p0 + ct >= m.t.L && (kp == 255 || vp == 255);
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const int it = 2 * i + h, slot = it % C::S;
           ok = tm_wait(su32(&ctl.full[slot]), (uint32_t)(it / C::S) & 1u, abort_w, status) &&
                tm_wait(su32(h ? &ctl.v_empty[b] : &ctl.k_empty[b]), ((uint32_t)(i >> 1) & 1u) ^ 1u, abort_w, status);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+          if (kw_vote<KW_CONV>(!ok, 3)) {  // (giving up too: they leave together)
+            ok = false;
+            break;
+          }
           const uint8_t* src = sp + C::RING + slot * C::SLOT;
           uint8_t* dst = sp + (h ? C::V : C::K) + b * C::TILE;
           if (h == 0) {
             // (the tile four before was done with: its outputs came before the scores whose keys' place this takes)
-            ctl.power[i & 3][ct] = bad ? make_float2(1.f, 1.f) : make_float2(kv8_power(kp), kv8_power(vp));
-            at.next(dq, dr, ps);
-            if (i + 1 < m.nt) powers_of(p0 + TM_PT + ct, at, kp, vp);
-          }
-          uint4 x[TM_PT / RPI];
 #pragma unroll
-          for (int u = 0; u < TM_PT / RPI; ++u) x[u] = *reinterpret_cast<const uint4*>(src + sw_at<HD>(ct / CH + u * RPI, c));
-          if (h && edge) {
+            for (int j = 0; j < PP; ++j) {
+              const int at = ct + KW_CONV * j, pos = p0 + at, e = min(max(vp[j] - 127, -KW_EXP), KW_EXP);
+              // a new row's block of NaN: rows that see it are told by its bit alone
+              const bool bad = pos >= m.t.L && (kp[j] == 255 || vp[j] == 255);
+              const bool none = bad || vp[j] < 127 - KW_EXP || pos >= m.end;  // no values, or none that count
+              if (ct % GRAN == 0)
+                ctl.power[i & 3][at / GRAN] = make_float4(bad ? 1.f : kv8_power(kp[j]), vp[j] == 255 && !bad ? kv8_power(255) : (float)e,
+                                                          __int_as_float((127 - e) << 23), 0.f);
+              const unsigned b0 = __ballot_sync(0xffffffffu, bad), n0 = __ballot_sync(0xffffffffu, none);
+              if (lane == 0) {
+                ctl.bad[i & 3][cw + 2 * j] = b0;
+                ctl.none[i & 1][cw + 2 * j] = n0;
+              }
+            }
+            powers_of(i + 1);
+          }
+          bool some = false;
+          if (h) {
             // the value row of a position no row may meet is zeroed: one behind the last that is
             // seen (whatever lies there), or a new row's with a NaN
-            unsigned found = __ballot_sync(0xffffffffu, bad);  // this warp's positions 32 cw ..
-            if (lane == 0) ctl.bad[i & 3][cw] = found;
-            asm volatile("barrier.cta.sync 3, 128;" ::: "memory");
-#pragma unroll
-            for (int u = 0; u < TM_PT / RPI; ++u) {
-              const int r = ct / CH + u * RPI, pos = p0 + r;
-              const uint32_t bits = ((x[u].x & 0x7f7f7f7fu) + 0x01010101u) | ((x[u].y & 0x7f7f7f7fu) + 0x01010101u) |
-                                    ((x[u].z & 0x7f7f7f7fu) + 0x01010101u) | ((x[u].w & 0x7f7f7f7fu) + 0x01010101u);
-              const unsigned row = ((1u << CH) - 1) << (lane / CH * CH);  // the lanes of this row
-              const bool nan = (__ballot_sync(0xffffffffu, (bits & 0x80808080u) != 0) & row) != 0 && pos >= m.t.L && pos < m.end;
-              const bool mine = nan || ((ctl.bad[i & 3][r >> 5] >> (r & 31)) & 1u);
-              if (mine || pos >= m.end) x[u] = make_uint4(0, 0, 0, 0);
-              if (nan && c == 0) atomicOr(&ctl.bad[i & 3][r >> 5], 1u << (r & 31));
-            }
+            const uint4 z = *reinterpret_cast<const uint4*>(ctl.none[i & 1]);
+            some = edge || (z.x | z.y | z.z | z.w);
           }
+          constexpr int U = TM_PT / RPI < 8 ? TM_PT / RPI : 8;  // of the thread's rows, loads on their way
+#pragma unroll 1
+          for (int r0 = ct / CH; r0 < TM_PT; r0 += U * RPI) {
+            uint4 x[U];
 #pragma unroll
-          for (int u = 0; u < TM_PT / RPI; ++u) {
-            const int r = ct / CH + u * RPI;
-            const uint2 p0_ = codes_half(x[u].x), p1 = codes_half(x[u].y), p2 = codes_half(x[u].z), p3 = codes_half(x[u].w);
-            uint8_t* row = dst + (c >> 2) * (TM_PT * 128) + r * 128;
-            *reinterpret_cast<uint4*>(row + (((2 * (c & 3)) ^ (r & 7)) << 4)) = make_uint4(p0_.x, p0_.y, p1.x, p1.y);
-            *reinterpret_cast<uint4*>(row + (((2 * (c & 3) + 1) ^ (r & 7)) << 4)) = make_uint4(p2.x, p2.y, p3.x, p3.y);
+            for (int u = 0; u < U; ++u) x[u] = *reinterpret_cast<const uint4*>(src + sw_at<HD>(r0 + u * RPI, c));
+            if (some) {
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                const int r = r0 + u * RPI, pos = p0 + r;
+                const uint32_t bits = ((x[u].x & 0x7f7f7f7fu) + 0x01010101u) | ((x[u].y & 0x7f7f7f7fu) + 0x01010101u) |
+                                      ((x[u].z & 0x7f7f7f7fu) + 0x01010101u) | ((x[u].w & 0x7f7f7f7fu) + 0x01010101u);
+                const unsigned row = ((1u << CH) - 1) << (lane / CH * CH);  // the lanes of this row
+                const bool nan = (__ballot_sync(0xffffffffu, (bits & 0x80808080u) != 0) & row) != 0 && pos >= m.t.L && pos < m.end;
+                if (nan || ((ctl.none[i & 1][r >> 5] >> (r & 31)) & 1u)) x[u] = make_uint4(0, 0, 0, 0);
+                if (nan && c == 0) atomicOr(&ctl.bad[i & 3][r >> 5], 1u << (r & 31));
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int r = r0 + u * RPI;
+              const uint2 h0 = codes_half(x[u].x), h1 = codes_half(x[u].y), h2 = codes_half(x[u].z), h3 = codes_half(x[u].w);
+              uint8_t* row = dst + (c >> 2) * (TM_PT * 128) + r * 128;
+              *reinterpret_cast<uint4*>(row + (((2 * (c & 3)) ^ (r & 7)) << 4)) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+              *reinterpret_cast<uint4*>(row + (((2 * (c & 3) + 1) ^ (r & 7)) << 4)) = make_uint4(h2.x, h2.y, h3.x, h3.y);
+            }
           }
           mbar_arrive(su32(&ctl.empty[slot]));
           proxy_fence();
@@ -362,7 +386,7 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
           __syncwarp();
           tc_fence_after();
           const uint32_t src = tmem + b * 128 + lanes;
-          const float4* pw = reinterpret_cast<const float4*>(ctl.power[i & 3]);  // two positions each
+          const float4* pw = ctl.power[i & 3] + 64 / GRAN * wg;
           // what the row sees of 32 positions: x is -inf elsewhere, NaN where a value is
           auto see = [&](int ch, float (&x)[32]) {
             const int dd = p0 + 32 * ch - m.t.L;  // the first of them, counted from the first new row
@@ -381,58 +405,58 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
             }
           };
           // the largest score and power
-          float top = -INFINITY;
-#pragma unroll
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             float x[32];
             tmem_ld32f(src + 32 * (2 * wg + h), x);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float4 p = pw[(64 * wg + 32 * h + e) / 2];
-              x[e] = fmaf(x[e], p.x * qs, fminf(fmaxf((float)((__float_as_int(p.y) >> 23) - 127), -60.f), 60.f));
-              x[e + 1] = fmaf(x[e + 1], p.z * qs, fminf(fmaxf((float)((__float_as_int(p.w) >> 23) - 127), -60.f), 60.f));
+            for (int e = 0; e < 32; e += GRAN) {
+              const float4 p = pw[(32 * h + e) / GRAN];
+              const float kq = p.x * qs;
+#pragma unroll
+              for (int f = 0; f < GRAN; ++f) x[e + f] = fmaf(x[e + f], kq, p.y);
             }
             see(2 * wg + h, x);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, x[e]);
+            for (int e = 0; e < 32; ++e) top[e & 1] = fmaxf(top[e & 1], x[e]);
           }
+          top[0] = fmaxf(top[0], top[1]);
           corr = 1.f;
-          if (kw_vote(top - base > KW_MOST || !ok, 2)) {  // both halves of a row have the same base
-            ctl.part[wg][r] = top;
+          if (kw_vote(top[0] - base > KW_MOST || !ok, 2)) {  // both halves of a row have the same base
+            ctl.part[wg][r] = top[0];
             if (kw_vote(!ok, 1)) {
               ok = false;
               break;
             }
-            top = fmaxf(top, ctl.part[wg ^ 1][r]);
-            if (top - base > KW_MOST) {
-              corr = exp2_fast(base - (top - KW_BASE));
-              base = top - KW_BASE;
+            top[0] = fmaxf(top[0], ctl.part[wg ^ 1][r]);
+            if (top[0] - base > KW_MOST) {
+              corr = exp2_fast(base - (top[0] - KW_BASE));
+              base = top[0] - KW_BASE;
               l *= corr;
             }
           }
-          const float2 nb = make_float2(-base, -base);
+          // weights 2^(score + power - base); without the power they join the sum
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const int ch = 2 * wg + h;
             float x[32];
             tmem_ld32f(src + 32 * ch, x);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float4 p = pw[(64 * wg + 32 * h + e) / 2];
-              const float2 v = fma2(make_float2(x[e], x[e + 1]), mul2(make_float2(p.x, p.z), make_float2(qs, qs)), nb);
-              x[e] = v.x;
-              x[e + 1] = v.y;
+            for (int e = 0; e < 32; e += GRAN) {
+              const float4 p = pw[(32 * h + e) / GRAN];
+              const float kq = p.x * qs, nb = p.y - base;
+#pragma unroll
+              for (int f = 0; f < GRAN; ++f) x[e + f] = fmaf(x[e + f], kq, nb);
             }
             see(ch, x);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float4 p = pw[(64 * wg + 32 * h + e) / 2];
-              float2 w = make_float2(exp2_fast(x[e]), exp2_fast(x[e + 1]));
-              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], w);
-              w = mul2(w, make_float2(p.y, p.w));
-              x[e] = w.x;
-              x[e + 1] = w.y;
+              const float ia = pw[(32 * h + e) / GRAN].z, ib = pw[(32 * h + e + 1) / GRAN].z;
+              x[e] = exp2_fast(x[e]);
+              x[e + 1] = exp2_fast(x[e + 1]);
+              sum[(e >> 1) & 1] = fma2(make_float2(x[e], x[e + 1]), make_float2(ia, ib), sum[(e >> 1) & 1]);
             }
 #pragma unroll
             for (int term = 0; term < C::TERMS; ++term) {
@@ -547,23 +571,24 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
   if (warp == C::MMA_WARP) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-template <class T, int HD, bool TMA>
+template <class T, int HD, int GRAN, bool TMA>
 int launch_wide(const Kv8AttnArgs& a, int layers, int dev, cudaStream_t s) {
   using C = KwCfg<T, HD>;
   static TmKernel known[kMaxDevices];
-  return launch_tiles(kv8_wide_kernel<T, HD, TMA>, known[dev], C::THREADS, C::SMEM, TMA, KW_ROWS, 4 * sizeof(T), a, layers, s);
+  return launch_tiles(kv8_wide_kernel<T, HD, GRAN, TMA>, known[dev], C::THREADS, C::SMEM, TMA, KW_ROWS, 4 * sizeof(T), a, layers, s);
 }
 
-template <class T>
+template <class T, int HD>
 int launch_wide_of(const Kv8AttnArgs& a, int layers, bool tma, int dev, cudaStream_t s) {
-  if (a.c.hd == 128) return tma ? launch_wide<T, 128, true>(a, layers, dev, s) : launch_wide<T, 128, false>(a, layers, dev, s);
-  return tma ? launch_wide<T, 64, true>(a, layers, dev, s) : launch_wide<T, 64, false>(a, layers, dev, s);
+  if (a.c.block % 4 == 0) return tma ? launch_wide<T, HD, 4, true>(a, layers, dev, s) : launch_wide<T, HD, 4, false>(a, layers, dev, s);
+  return tma ? launch_wide<T, HD, 1, true>(a, layers, dev, s) : launch_wide<T, HD, 1, false>(a, layers, dev, s);
 }
 
 }  // namespace
 
 int launch_kv8_wide(const Kv8AttnArgs& a, int layers, int dtype, bool tma, int dev, cudaStream_t s) {
-  return dtype == Q3TTS_F32 ? launch_wide_of<float>(a, layers, tma, dev, s) : launch_wide_of<bf16>(a, layers, tma, dev, s);
+  if (dtype == Q3TTS_F32) return a.c.hd == 128 ? launch_wide_of<float, 128>(a, layers, tma, dev, s) : launch_wide_of<float, 64>(a, layers, tma, dev, s);
+  return a.c.hd == 128 ? launch_wide_of<bf16, 128>(a, layers, tma, dev, s) : launch_wide_of<bf16, 64>(a, layers, tma, dev, s);
 }
 
 }  // namespace q3
