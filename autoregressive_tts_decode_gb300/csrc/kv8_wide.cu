@@ -13,7 +13,7 @@
 // weights', both in fp32; a row's base is its largest score and power so far, less 8 (weights of
 // 2^8, and up to 2^15 before the base follows: fp16's smallest step is 2^-24).
 //
-// Roles of a CTA (one per SM): a warp loads codes, two convert them (a row's 16 codes a lane), one
+// Roles of a CTA (one per SM): a warp loads codes, four convert them (a row's 16 codes a lane), one
 // thread issues the MMAs (scores of tile t + 1 before the outputs of tile t), and two groups of
 // four warps are the softmax, each with half of a tile's positions and half of the
 // output's elements (one thread a row and half).  The tensor cores work in order, which orders most of what shares
@@ -28,13 +28,14 @@ namespace {
 
 constexpr int KW_ROWS = 128;  // rows of a tile
 constexpr int KW_SOFT = 256;  // softmax threads
-constexpr int KW_CONV = 64;   // converting threads
+constexpr int KW_CONV = 128;  // converting threads
 constexpr int KW_EXP = 60;  // exponents of the values' powers that count: -KW_EXP .. KW_EXP
+constexpr float KW_TINY = 1e-37f;  // the least factor of a score: a masked one stays -inf
 constexpr float KW_BASE = 8.f, KW_MOST = 15.f;  // log2 of the weights at the base, and at most
 
 template <class T, int HD>
 struct KwCfg {
-  static constexpr int MMA_WARP = 8, LOAD_WARP = 9, CONV_WARP = 10, THREADS = 384;
+  static constexpr int MMA_WARP = 8, LOAD_WARP = 9, CONV_WARP = 10, THREADS = 448;
   static constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;
   static constexpr uint32_t TILE = TM_PT * HD * 2;   // a converted K or V tile
   static constexpr uint32_t SLOT = TM_PT * HD;       // a tile of codes
@@ -222,27 +223,25 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
       }
       __syncwarp();
     } else if (warp >= C::CONV_WARP) {
-      // ---- codes to fp16; a thread has chunk ct % CH of every RPI-th of a tile's rows, and two positions' powers
-      constexpr int CH = HD / 16, RPI = KW_CONV / CH, PP = TM_PT / KW_CONV;
+      // ---- codes to fp16; a thread has chunk ct % CH of every RPI-th of a tile's rows, and a position's powers
+      constexpr int CH = HD / 16, RPI = KW_CONV / CH;
       const int ct = tid - C::CONV_WARP * 32, c = ct % CH, cw = warp - C::CONV_WARP;
       const int ps = a.c.page, dq = TM_PT / ps, dr = TM_PT % ps, per_page = ps / a.c.block;
       const int* table = a.r.page_table + (size_t)m.seq * a.r.pps;
       const size_t pstride = (size_t)a.c.Hkv * per_page;  // from a key block's power to its value block's
-      Place at[PP] = {{m.t0 * TM_PT + ct, ps}, {m.t0 * TM_PT + ct + KW_CONV, ps}};
-      int kp[PP], vp[PP];
+      static_assert(KW_CONV == TM_PT, "a thread a position");
+      Place at(m.t0 * TM_PT + ct, ps);
+      int kp, vp;
       auto powers_of = [&](int i) {
-#pragma unroll
-        for (int j = 0; j < PP; ++j) {
-          kp[j] = vp[j] = 127;
-          if (i < m.nt && (m.t0 + i) * TM_PT + ct + KW_CONV * j < m.end) {
-            int page = __ldg(table + at[j].entry);
-            if (page < 0 || page >= a.c.n_pages) page = 0;  // (reported by the loading warp)
-            const uint8_t* p = a.c.powers + ((((size_t)a.c.layer * a.c.n_pages + page) * 2) * a.c.Hkv + m.g) * per_page + at[j].slot / a.c.block;
-            kp[j] = __ldg(p);
-            vp[j] = __ldg(p + pstride);
-          }
-          at[j].next(dq, dr, ps);
+        kp = vp = 127;
+        if (i < m.nt && (m.t0 + i) * TM_PT + ct < m.end) {
+          int page = __ldg(table + at.entry);
+          if (page < 0 || page >= a.c.n_pages) page = 0;  // (reported by the loading warp)
+          const uint8_t* p = a.c.powers + ((((size_t)a.c.layer * a.c.n_pages + page) * 2) * a.c.Hkv + m.g) * per_page + at.slot / a.c.block;
+          kp = __ldg(p);
+          vp = __ldg(p + pstride);
         }
+        at.next(dq, dr, ps);
       };
       powers_of(0);
       for (int i = 0; i < m.nt && ok; ++i) {
@@ -261,20 +260,17 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
           uint8_t* dst = sp + (h ? C::V : C::K) + b * C::TILE;
           if (h == 0) {
             // (the tile four before was done with: its outputs came before the scores whose keys' place this takes)
-#pragma unroll
-            for (int j = 0; j < PP; ++j) {
-              const int at = ct + KW_CONV * j, pos = p0 + at, e = min(max(vp[j] - 127, -KW_EXP), KW_EXP);
-              // a new row's block of NaN: rows that see it are told by its bit alone
-              const bool bad = pos >= m.t.L && (kp[j] == 255 || vp[j] == 255);
-              const bool none = bad || vp[j] < 127 - KW_EXP || pos >= m.end;  // no values, or none that count
-              if (ct % GRAN == 0)
-                ctl.power[i & 3][at / GRAN] = make_float4(bad ? 1.f : kv8_power(kp[j]), vp[j] == 255 && !bad ? kv8_power(255) : (float)e,
-                                                          __int_as_float((127 - e) << 23), 0.f);
-              const unsigned b0 = __ballot_sync(0xffffffffu, bad), n0 = __ballot_sync(0xffffffffu, none);
-              if (lane == 0) {
-                ctl.bad[i & 3][cw + 2 * j] = b0;
-                ctl.none[i & 1][cw + 2 * j] = n0;
-              }
+            const int pos = p0 + ct, e = min(max(vp - 127, -KW_EXP), KW_EXP);
+            // a new row's block of NaN: rows that see it are told by its bit alone
+            const bool bad = pos >= m.t.L && (kp == 255 || vp == 255);
+            const bool none = bad || vp < 127 - KW_EXP || pos >= m.end;  // no values, or none that count
+            if (ct % GRAN == 0)
+              ctl.power[i & 3][ct / GRAN] = make_float4(bad ? 1.f : kv8_power(kp), vp == 255 && !bad ? kv8_power(255) : (float)e,
+                                                        __int_as_float((127 - e) << 23), 0.f);
+            const unsigned b0 = __ballot_sync(0xffffffffu, bad), n0 = __ballot_sync(0xffffffffu, none);
+            if (lane == 0) {
+              ctl.bad[i & 3][cw] = b0;
+              ctl.none[i & 1][cw] = n0;
             }
             powers_of(i + 1);
           }
@@ -387,7 +383,7 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
           tc_fence_after();
           const uint32_t src = tmem + b * 128 + lanes;
           const float4* pw = ctl.power[i & 3] + 64 / GRAN * wg;
-          // what the row sees of 32 positions: x is -inf elsewhere, NaN where a value is
+          // what the row sees of 32 positions: x is far below all scores elsewhere, NaN where a value is
           auto see = [&](int ch, float (&x)[32]) {
             const int dd = p0 + 32 * ch - m.t.L;  // the first of them, counted from the first new row
             if (dd > -32) {
@@ -405,34 +401,32 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
             }
           };
           // the largest score and power
-          float top[2] = {-INFINITY, -INFINITY};
+          float top = -INFINITY;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             float x[32];
             tmem_ld32f(src + 32 * (2 * wg + h), x);
+            see(2 * wg + h, x);
 #pragma unroll
             for (int e = 0; e < 32; e += GRAN) {
               const float4 p = pw[(32 * h + e) / GRAN];
-              const float kq = p.x * qs;
+              float mx = x[e];
 #pragma unroll
-              for (int f = 0; f < GRAN; ++f) x[e + f] = fmaf(x[e + f], kq, p.y);
+              for (int f = 1; f < GRAN; ++f) mx = fmaxf(mx, x[e + f]);
+              top = fmaxf(top, fmaf(mx, fmaxf(p.x * qs, KW_TINY), p.y));
             }
-            see(2 * wg + h, x);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) top[e & 1] = fmaxf(top[e & 1], x[e]);
           }
-          top[0] = fmaxf(top[0], top[1]);
           corr = 1.f;
-          if (kw_vote(top[0] - base > KW_MOST || !ok, 2)) {  // both halves of a row have the same base
-            ctl.part[wg][r] = top[0];
-            if (kw_vote(!ok, 1)) {
+          if (kw_vote<64>(top - base > KW_MOST || !ok, 4 + (warp & 3))) {  // both halves of a row have the same base
+            ctl.part[wg][r] = top;
+            if (kw_vote<64>(!ok, 4 + (warp & 3))) {
               ok = false;
               break;
             }
-            top[0] = fmaxf(top[0], ctl.part[wg ^ 1][r]);
-            if (top[0] - base > KW_MOST) {
-              corr = exp2_fast(base - (top[0] - KW_BASE));
-              base = top[0] - KW_BASE;
+            top = fmaxf(top, ctl.part[wg ^ 1][r]);
+            if (top - base > KW_MOST) {
+              corr = exp2_fast(base - (top - KW_BASE));
+              base = top - KW_BASE;
               l *= corr;
             }
           }
@@ -443,20 +437,25 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
             const int ch = 2 * wg + h;
             float x[32];
             tmem_ld32f(src + 32 * ch, x);
+            see(ch, x);
 #pragma unroll
             for (int e = 0; e < 32; e += GRAN) {
               const float4 p = pw[(32 * h + e) / GRAN];
-              const float kq = p.x * qs, nb = p.y - base;
+              const float kq = fmaxf(p.x * qs, KW_TINY), nb = p.y - base;
+              if constexpr (GRAN == 1) {
+                x[e] = exp2_fast(fmaf(x[e], kq, nb));
+                sum[0].x = fmaf(x[e], p.z, sum[0].x);
+              } else {
+                float2 part = make_float2(0.f, 0.f);
 #pragma unroll
-              for (int f = 0; f < GRAN; ++f) x[e + f] = fmaf(x[e + f], kq, nb);
-            }
-            see(ch, x);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float ia = pw[(32 * h + e) / GRAN].z, ib = pw[(32 * h + e + 1) / GRAN].z;
-              x[e] = exp2_fast(x[e]);
-              x[e + 1] = exp2_fast(x[e + 1]);
-              sum[(e >> 1) & 1] = fma2(make_float2(x[e], x[e + 1]), make_float2(ia, ib), sum[(e >> 1) & 1]);
+                for (int f = 0; f < GRAN; f += 2) {
+                  const float2 v = fma2(make_float2(x[e + f], x[e + f + 1]), make_float2(kq, kq), make_float2(nb, nb));
+                  x[e + f] = exp2_fast(v.x);
+                  x[e + f + 1] = exp2_fast(v.y);
+                  part = add2(part, make_float2(x[e + f], x[e + f + 1]));
+                }
+                sum[(e / GRAN) & 1] = fma2(part, make_float2(p.z, p.z), sum[(e / GRAN) & 1]);
+              }
             }
 #pragma unroll
             for (int term = 0; term < C::TERMS; ++term) {
@@ -580,6 +579,7 @@ int launch_wide(const Kv8AttnArgs& a, int layers, int dev, cudaStream_t s) {
 
 template <class T, int HD>
 int launch_wide_of(const Kv8AttnArgs& a, int layers, bool tma, int dev, cudaStream_t s) {
+  if (a.c.block % 16 == 0) return tma ? launch_wide<T, HD, 16, true>(a, layers, dev, s) : launch_wide<T, HD, 16, false>(a, layers, dev, s);
   if (a.c.block % 4 == 0) return tma ? launch_wide<T, HD, 4, true>(a, layers, dev, s) : launch_wide<T, HD, 4, false>(a, layers, dev, s);
   return tma ? launch_wide<T, HD, 1, true>(a, layers, dev, s) : launch_wide<T, HD, 1, false>(a, layers, dev, s);
 }
