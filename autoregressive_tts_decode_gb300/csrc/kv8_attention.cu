@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
 
   if (m.nt > 0) {
     if (warp == C::LOAD_WARP) {
-      ok = load_tiles<HD, C::S, TMA>(&map, a, m, d.box, ring, ctl.full, ctl.empty, issued, abort_w);
+      ok = load_tiles<HD, C::S, TMA, false>(&map, a, m, d.box, ring, ctl.full, ctl.empty, 0, issued, abort_w);
     } else if (warp == C::MMA_WARP) {
       if (elect_one()) {
         constexpr uint32_t idS = f8_idesc(TM_PT, C::N, false), idO = f8_idesc(TM_PT, C::N, true);

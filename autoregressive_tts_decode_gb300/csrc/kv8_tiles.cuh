@@ -17,7 +17,7 @@ constexpr int KF_SORT = 256;  // sequences that are dealt by length, at most
 
 struct KfDeal {
   int items, row_tiles, box;
-  int vec;  // four elements of a query row in one load
+  int vec;  // four elements of a row in one access: 1 of q, 2 of out
   unsigned rep_inv;
   int sorted;  // the sequences are taken longest first
   int wait_1024, lost_tile;
@@ -108,15 +108,41 @@ __device__ __forceinline__ float4 q4(const bf16* p, bool wide) {
                      __uint_as_float(u.y & 0xffff0000u));
 }
 
+// Four consecutive elements of a row of out.
+__device__ __forceinline__ void store4(float* p, float4 v, bool wide) {
+  if (wide) {
+    *reinterpret_cast<float4*>(p) = v;
+  } else {
+    p[0] = v.x;
+    p[1] = v.y;
+    p[2] = v.z;
+    p[3] = v.w;
+  }
+}
+__device__ __forceinline__ void store4(bf16* p, float4 v, bool wide) {
+  if (wide) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(make_float2(v.x, v.y)), pack_bf16(make_float2(v.z, v.w)));
+  } else {
+    p[0] = from_f<bf16>(v.x);
+    p[1] = from_f<bf16>(v.y);
+    p[2] = from_f<bf16>(v.z);
+    p[3] = from_f<bf16>(v.w);
+  }
+}
+
 // A warp's loads of the key and value tiles of an item, as codes, into a ring of S tiles
 // (K0 V0 K1 V1 ..).  TMA: pages of 8 positions or more that fill a tile a whole number of
 // times (or whole tiles of larger pages) come in boxes, swizzled on the way; other pages row by row in
-// 16-byte asynchronous copies, by all lanes.  issued: tiles under way or there.
-template <int HD, int S, bool TMA>
+// 16-byte asynchronous copies, by all lanes.  SPLIT: two warps, the keys (kv 0) and the
+// values (1).  issued: tiles under way or there, up to the warp's last.
+template <int HD, int S, bool TMA, bool SPLIT>
 __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8AttnArgs& a, const KfItem& m, int box, uint32_t ring,
-                                           unsigned long long* full, unsigned long long* empty, int& issued,
+                                           unsigned long long* full, unsigned long long* empty, int kv, int& issued,
                                            volatile int* abort_w) {
-  static_assert(S >= 4, "two tiles stay on their way");
+  // tiles of the copying warp that stay on their way: fewer than its places of the ring
+  constexpr int AHEAD = SPLIT ? 1 : 2;
+  static_assert(S >= 4 && S % 2 == 0, "places");
+  const int first = SPLIT ? kv : 0, last = SPLIT ? kv : 1;
   const int lane = threadIdx.x & 31, ps = a.c.page;
   const int* table = a.r.page_table + (size_t)m.seq * a.r.pps;
   int* status = a.r.status;
@@ -128,8 +154,8 @@ __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8Attn
     return 0;
   };
   if constexpr (TMA) {
-    // lane (kv, b): box b of a tile's keys or values
-    const int kv = lane >> 4, b = lane & 15, boxes = TM_PT / box;
+    // lane (keys or values, b): box b of a tile
+    const int my = SPLIT ? kv : lane >> 4, b = lane & 15, boxes = TM_PT / box;
     auto page_of = [&](int i) -> int {
       const int pos = (m.t0 + i) * TM_PT + b * box;
       return b < boxes && i < m.nt && pos < m.end ? __ldg(table + pos / ps) : 0;
@@ -138,10 +164,9 @@ __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8Attn
     for (int i = 0; i < m.nt; ++i) {
       const int pos = (m.t0 + i) * TM_PT + b * box;
       const int held = min(TM_PT, m.end - (m.t0 + i) * TM_PT);
-      const bool mine = b < boxes && pos < m.end;
-      const int row = mine ? (int)kv8_row(a.c, checked(page0), kv, m.g, pos % ps) : 0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      const bool mine = b < boxes && pos < m.end && !(SPLIT && lane > 15);
+      const int row = mine ? (int)kv8_row(a.c, checked(page0), my, m.g, pos % ps) : 0;
+      for (int h = first; h <= last; ++h) {
         const int it = 2 * i + h, slot = it % S;
         ok = ok && tm_wait(su32(&empty[slot]), ((uint32_t)(it / S) & 1u) ^ 1u, abort_w, status);
         ok = __all_sync(0xffffffffu, ok);
@@ -149,8 +174,8 @@ __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8Attn
         const uint32_t fb = su32(&full[slot]);
         if (lane == 0) mbar_expect_tx(fb, (uint32_t)((held + box - 1) / box * box * HD));
         __syncwarp();
-        if (mine && kv == h) tma_load(ring + slot * (TM_PT * HD) + b * box * HD, map, 0, row, fb);
-        ++issued;
+        if (mine && my == h) tma_load(ring + slot * (TM_PT * HD) + b * box * HD, map, 0, row, fb);
+        issued = it + 1;
       }
       if (!ok) break;
       page0 = page1;
@@ -170,7 +195,8 @@ __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8Attn
       }
     };
     look_up(0);
-    int arrived = 0;
+    int sent = 0, arrived = 0;  // of the warp's tiles
+    auto arrive = [&](int n) { mbar_arrive(su32(&full[(SPLIT ? 2 * n + kv : n) % S])); };
     for (int i = 0; i < m.nt && ok; ++i) {
 #pragma unroll
       for (int j = 0; j < TM_PT / 32; ++j) {
@@ -178,7 +204,7 @@ __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8Attn
         row[j] = pos < m.end ? (int)kv8_row(a.c, checked(page[j]), 0, m.g, pos % ps) : -1;
       }
       look_up(i + 1);
-      for (int h = 0; h < 2; ++h) {
+      for (int h = first; h <= last; ++h) {
         const int it = 2 * i + h, slot = it % S;
         ok = tm_wait(su32(&empty[slot]), ((uint32_t)(it / S) & 1u) ^ 1u, abort_w, status);
         ok = __all_sync(0xffffffffu, ok);
@@ -196,17 +222,17 @@ __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8Attn
                            : "memory");
           }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        ++issued;
-        if (issued - arrived > 2) {  // (two tiles stay on their way)
-          asm volatile("cp.async.wait_group 2;" ::: "memory");
+        issued = it + 1;
+        if (++sent - arrived > AHEAD) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
           proxy_fence();
-          mbar_arrive(su32(&full[arrived++ % S]));
+          arrive(arrived++);
         }
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     proxy_fence();
-    for (; arrived < issued; ++arrived) mbar_arrive(su32(&full[arrived % S]));
+    for (; arrived < sent; ++arrived) arrive(arrived);
   }
   return ok;
 }
@@ -260,7 +286,8 @@ int launch_tiles(Kernel kernel, TmKernel& known, int threads, size_t smem, bool 
   d.items = (int)items;
   const int tiles = (int)(((long)a.r.pps * a.c.page + TM_PT - 1) / TM_PT);
   const int c = cluster_size(items, tiles, known);
-  d.vec = ((uintptr_t)a.q & (vec_bytes - 1)) == 0 && a.ldq % 4 == 0;
+  d.vec = (((uintptr_t)a.q & (vec_bytes - 1)) == 0 && a.ldq % 4 == 0 ? 1 : 0) |
+          (((uintptr_t)a.out & (vec_bytes - 1)) == 0 && a.ldo % 4 == 0 ? 2 : 0);
   d.rep_inv = (unsigned)(((1ull << 32) + rep - 1) / rep);
   d.sorted = items * c > known.clusters[1] && a.r.n_seqs > 1 && a.r.n_seqs <= KF_SORT;
   d.wait_1024 = a.wait_1024;

@@ -13,7 +13,7 @@
 // weights', both in fp32; a row's base is its largest score and power so far, less 8 (weights of
 // 2^8, and up to 2^15 before the base follows: fp16's smallest step is 2^-24).
 //
-// Roles of a CTA (one per SM): a warp loads codes, four convert them (a row's 16 codes a lane), one
+// Roles of a CTA (one per SM): two warps load codes, four convert them (a row's 16 codes a lane), one
 // thread issues the MMAs (scores of tile t + 1 before the outputs of tile t), and two groups of
 // four warps are the softmax, each with half of a tile's positions and half of the
 // output's elements (one thread a row and half).  The tensor cores work in order, which orders most of what shares
@@ -35,7 +35,7 @@ constexpr float KW_BASE = 8.f, KW_MOST = 15.f;  // log2 of the weights at the ba
 
 template <class T, int HD>
 struct KwCfg {
-  static constexpr int MMA_WARP = 8, LOAD_WARP = 9, CONV_WARP = 10, THREADS = 448;
+  static constexpr int MMA_WARP = 8, LOAD_WARP = 9, CONV_WARP = 11, THREADS = 480;
   static constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;
   static constexpr uint32_t TILE = TM_PT * HD * 2;   // a converted K or V tile
   static constexpr uint32_t SLOT = TM_PT * HD;       // a tile of codes
@@ -179,8 +179,9 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
   float* os = reinterpret_cast<float*>(sp);  // [KW_ROWS][LD]: the outputs, where the converted tiles were
 
   if (m.nt > 0) {
-    if (warp == C::LOAD_WARP) {
-      ok = load_tiles<HD, C::S, TMA>(&map, a, m, d.box, sbase + C::RING, ctl.full, ctl.empty, issued, abort_w);
+    if (warp == C::LOAD_WARP || warp == C::LOAD_WARP + 1) {
+      // (one warp for both: issuing the boxes of 16-position pages took longer than a tile's products)
+      ok = load_tiles<HD, C::S, TMA, true>(&map, a, m, d.box, sbase + C::RING, ctl.full, ctl.empty, warp - C::LOAD_WARP, issued, abort_w);
     } else if (warp == C::MMA_WARP) {
       // ---- MMA issue
       if (elect_one()) {
@@ -324,43 +325,40 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
       {
         // the row's query, scaled to 2^14 .. 2^15, in tensor memory: this group's half of it
         const T* q = static_cast<const T*>(a.q) + (size_t)(m.t.row0 + node) * a.ldq + (size_t)(m.g * rep + min(row, m.n0 + m.rows - 1) - node * rep) * HD + wg * HW;
-        uint32_t top = 0;
+        float x[HW];
 #pragma unroll
         for (int e = 0; e < HW; e += 4) {
-          const float4 x = q4(q + e, d.vec & 1);
-          top = max(max(top, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu)),
-                    max(__float_as_uint(x.z) & 0x7fffffffu, __float_as_uint(x.w) & 0x7fffffffu));
+          const float4 v = q4(q + e, d.vec & 1);
+          x[e] = v.x;
+          x[e + 1] = v.y;
+          x[e + 2] = v.z;
+          x[e + 3] = v.w;
         }
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < HW; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
         ctl.part[wg][r] = __uint_as_float(top);
         kw_vote(false, 1);
         top = max(top, __float_as_uint(ctl.part[wg ^ 1][r]));
         const int E = min(max((int)(top >> 23) - 126, -100), 127);  // |q| < 2^E
         const float by = __int_as_float((127 + 15 - E) << 23);
         qs = 1.4426950408889634f / sqrtf((float)HD) * __int_as_float((127 - 15 + E) << 23);
-#pragma unroll 1
-        for (int e0 = 0; e0 < HW; e0 += 32) {
-          float x[32];
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 v = q4(q + e0 + e, d.vec & 1);
-            x[e] = v.x * by;
-            x[e + 1] = v.y * by;
-            x[e + 2] = v.z * by;
-            x[e + 3] = v.w * by;
-          }
+        for (int e = 0; e < HW; ++e) x[e] *= by;
 #pragma unroll
-          for (int term = 0; term < C::TERMS; ++term) {
+        for (int term = 0; term < C::TERMS; ++term)
+#pragma unroll
+          for (int e0 = 0; e0 < HW; e0 += 32) {
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              w[e] = pack_half(x[2 * e], x[2 * e + 1]);
+              w[e] = pack_half(x[e0 + 2 * e], x[e0 + 2 * e + 1]);
               const float2 h = unpack_half(w[e]);
-              x[2 * e] -= h.x;
-              x[2 * e + 1] -= h.y;
+              x[e0 + 2 * e] -= h.x;
+              x[e0 + 2 * e + 1] -= h.y;
             }
             tmem_st16u(tmem + C::TM_Q + term * C::TM_QT + (wg * HW + e0) / 2 + lanes, w);
           }
-        }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         mbar_arrive(su32(&ctl.q_full));
@@ -542,25 +540,31 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
   }
   __syncthreads();
   if (have && !*abort_w) {
-    T* out = static_cast<T*>(a.out);
-    for (int e = tid; e < KW_ROWS * HD; e += C::THREADS) {
-      const int n = e / HD * CL + rank;
-      if (n >= m.rows) break;
-      float sum = 0.f;
+    constexpr int LPR = HD / 4;  // lanes of a row
+    const int e = tid % LPR * 4;
+    for (int n = rank + CL * (tid / LPR); n < m.rows; n += CL * (C::THREADS / LPR)) {
+      float4 v[8], sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int s = 0; s < 8; ++s)  // a share without tiles wrote no output: its factor is 0
-        if (s < CL && ctl.fac[s][n] != 0.f) sum = fmaf(*(cl.map_shared_rank(os, s) + n * C::LD + e % HD), ctl.fac[s][n], sum);
+        v[s] = s < CL && ctl.fac[s][n] != 0.f ? *reinterpret_cast<const float4*>(cl.map_shared_rank(os, s) + n * C::LD + e)
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s < CL) {
+          const float f = ctl.fac[s][n];
+          sum = make_float4(fmaf(v[s].x, f, sum.x), fmaf(v[s].y, f, sum.y), fmaf(v[s].z, f, sum.z), fmaf(v[s].w, f, sum.w));
+        }
       const int row = m.n0 + n, node = div_rep(row, rep, d.rep_inv);
-      out[(size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + row - node * rep) * HD + e % HD] = from_f<T>(sum);
+      store4(static_cast<T*>(a.out) + (size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + row - node * rep) * HD + e, sum, d.vec & 2);
     }
   }
   if (CL > 1) cl.sync();  // the others may still read this CTA's shared memory
   tc_fence_before();
   __syncthreads();
   if (*abort_w) {  // what is on its way lands first
-    if (TMA && warp == C::LOAD_WARP) {
+    if (TMA && (warp == C::LOAD_WARP || warp == C::LOAD_WARP + 1)) {
       const long long c0 = clock64();
-      for (int it = max(0, issued - C::S); it < issued; ++it)
+      for (int it = max(warp - C::LOAD_WARP, issued - C::S + 1); it < issued; it += 2)
         while (!mbar_try_wait(su32(&ctl.full[it % C::S]), (uint32_t)(it / C::S) & 1u) && clock64() - c0 < TM_LAND_CYCLES) {
         }
     }
