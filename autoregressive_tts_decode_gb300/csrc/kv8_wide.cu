@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
           const int it = 2 * i + h, slot = it % C::S;
           ok = tm_wait(su32(&ctl.full[slot]), (uint32_t)(it / C::S) & 1u, abort_w, status) &&
                tm_wait(su32(h ? &ctl.v_empty[b] : &ctl.k_empty[b]), ((uint32_t)(i >> 1) & 1u) ^ 1u, abort_w, status);
+          if (i == 1) ok = ok && tm_wait(su32(&ctl.q_full), 0u, abort_w, status);  // (the queries passed through its place)
           if (kw_vote<KW_CONV>(!ok, 3)) {  // (giving up too: they leave together)
             ok = false;
             break;
@@ -323,41 +324,51 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
       const int row = m.n0 + r, node = div_rep(min(row, m.n0 + m.rows - 1), rep, d.rep_inv);
       float qs;
       {
-        // the row's query, scaled to 2^14 .. 2^15, in tensor memory: this group's half of it
-        const T* q = static_cast<const T*>(a.q) + (size_t)(m.t.row0 + node) * a.ldq + (size_t)(m.g * rep + min(row, m.n0 + m.rows - 1) - node * rep) * HD + wg * HW;
-        float x[HW];
+        // the queries, scaled to 2^14 .. 2^15, go to tensor memory, a lane a row, by way of shared
+        // memory: a warp reads whole rows (a lane its own row: 3.5 us more).  Their place is that of
+        // the odd tiles, whose conversion waits for it.
+        constexpr int LPR = HD / 4, RPW = 32 / LPR, U = KW_ROWS / (KW_SOFT / 32) / RPW;
+        const int sub = lane / LPR, e = lane % LPR * 4;
+        const T* q0 = static_cast<const T*>(a.q) + (size_t)m.t.row0 * a.ldq + (size_t)m.g * rep * HD + e;
+        float4 x[U];
 #pragma unroll
-        for (int e = 0; e < HW; e += 4) {
-          const float4 v = q4(q + e, d.vec & 1);
-          x[e] = v.x;
-          x[e + 1] = v.y;
-          x[e + 2] = v.z;
-          x[e + 3] = v.w;
+        for (int u = 0; u < U; ++u) {
+          const int at = min(m.n0 + (warp * U + u) * RPW + sub, m.n0 + m.rows - 1), of = div_rep(at, rep, d.rep_inv);
+          x[u] = q4(q0 + (size_t)of * a.ldq + (size_t)(at - of * rep) * HD, d.vec & 1);
         }
-        uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < HW; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-        ctl.part[wg][r] = __uint_as_float(top);
+        for (int u = 0; u < U; ++u) {
+          const int at = (warp * U + u) * RPW + sub;
+          uint32_t top = max(max(__float_as_uint(x[u].x) & 0x7fffffffu, __float_as_uint(x[u].y) & 0x7fffffffu),
+                             max(__float_as_uint(x[u].z) & 0x7fffffffu, __float_as_uint(x[u].w) & 0x7fffffffu));
+          top = __reduce_max_sync(LPR == 32 ? 0xffffffffu : 0xffffu << (16 * sub), top);
+          const int E = min(max((int)(top >> 23) - 126, -100), 127);  // |q| < 2^E
+          const float by = __int_as_float((127 + 15 - E) << 23);
+          if (lane % LPR == 0) ctl.base[at] = 1.4426950408889634f / sqrtf((float)HD) * __int_as_float((127 - 15 + E) << 23);
+          float v[4] = {x[u].x * by, x[u].y * by, x[u].z * by, x[u].w * by};
+#pragma unroll
+          for (int term = 0; term < C::TERMS; ++term) {
+            const uint2 w = make_uint2(pack_half(v[0], v[1]), pack_half(v[2], v[3]));
+            *reinterpret_cast<uint2*>(sp + (term ? C::V : C::K) + C::TILE + at * (HD * 2) + (((e >> 3) ^ (at & 7)) << 4) + (e & 4) * 2) = w;
+            const float2 h0 = unpack_half(w.x), h1 = unpack_half(w.y);
+            v[0] -= h0.x;
+            v[1] -= h0.y;
+            v[2] -= h1.x;
+            v[3] -= h1.y;
+          }
+        }
         kw_vote(false, 1);
-        top = max(top, __float_as_uint(ctl.part[wg ^ 1][r]));
-        const int E = min(max((int)(top >> 23) - 126, -100), 127);  // |q| < 2^E
-        const float by = __int_as_float((127 + 15 - E) << 23);
-        qs = 1.4426950408889634f / sqrtf((float)HD) * __int_as_float((127 - 15 + E) << 23);
-#pragma unroll
-        for (int e = 0; e < HW; ++e) x[e] *= by;
+        qs = ctl.base[r];
 #pragma unroll
         for (int term = 0; term < C::TERMS; ++term)
 #pragma unroll
-          for (int e0 = 0; e0 < HW; e0 += 32) {
+          for (int c0 = 0; c0 < HW / 8; c0 += 4) {
             uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              w[e] = pack_half(x[e0 + 2 * e], x[e0 + 2 * e + 1]);
-              const float2 h = unpack_half(w[e]);
-              x[e0 + 2 * e] -= h.x;
-              x[e0 + 2 * e + 1] -= h.y;
-            }
-            tmem_st16u(tmem + C::TM_Q + term * C::TM_QT + (wg * HW + e0) / 2 + lanes, w);
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4*>(w + 4 * c) = *reinterpret_cast<const uint4*>(
+                  sp + (term ? C::V : C::K) + C::TILE + r * (HD * 2) + (((wg * (HW / 8) + c0 + c) ^ (r & 7)) << 4));
+            tmem_st16u(tmem + C::TM_Q + term * C::TM_QT + wg * (HW / 2) + c0 * 4 + lanes, w);
           }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
@@ -540,22 +551,35 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
   }
   __syncthreads();
   if (have && !*abort_w) {
-    constexpr int LPR = HD / 4;  // lanes of a row
+    constexpr int LPR = HD / 4, RPI = C::THREADS / LPR, U = 4;  // lanes of a row, rows at a time, loads on their way
     const int e = tid % LPR * 4;
-    for (int n = rank + CL * (tid / LPR); n < m.rows; n += CL * (C::THREADS / LPR)) {
-      float4 v[8], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    T* out = static_cast<T*>(a.out) + (size_t)m.t.row0 * a.ldo + (size_t)m.g * rep * HD + e;
+    for (int n0 = rank + CL * (tid / LPR); n0 < m.rows; n0 += CL * RPI * U) {
+      float4 sum[U];
 #pragma unroll
-      for (int s = 0; s < 8; ++s)  // a share without tiles wrote no output: its factor is 0
-        v[s] = s < CL && ctl.fac[s][n] != 0.f ? *reinterpret_cast<const float4*>(cl.map_shared_rank(os, s) + n * C::LD + e)
-                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int u = 0; u < U; ++u) sum[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = 0; s < CL; ++s) {
+        const float* from = CL > 1 ? cl.map_shared_rank(os, s) : os;
+        float4 v[U];
+        float f[U];
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
-        if (s < CL) {
-          const float f = ctl.fac[s][n];
-          sum = make_float4(fmaf(v[s].x, f, sum.x), fmaf(v[s].y, f, sum.y), fmaf(v[s].z, f, sum.z), fmaf(v[s].w, f, sum.w));
+        for (int u = 0; u < U; ++u) {
+          const int n = min(n0 + u * CL * RPI, m.rows - 1);
+          f[u] = ctl.fac[s][n];
+          v[u] = *reinterpret_cast<const float4*>(from + n * C::LD + e);
         }
-      const int row = m.n0 + n, node = div_rep(row, rep, d.rep_inv);
-      store4(static_cast<T*>(a.out) + (size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + row - node * rep) * HD + e, sum, d.vec & 2);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (f[u] != 0.f)  // 0: a share without tiles wrote no output
+            sum[u] = make_float4(fmaf(v[u].x, f[u], sum[u].x), fmaf(v[u].y, f[u], sum[u].y), fmaf(v[u].z, f[u], sum[u].z), fmaf(v[u].w, f[u], sum[u].w));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int n = n0 + u * CL * RPI;
+        if (n >= m.rows) break;
+        const int row = m.n0 + n, node = div_rep(row, rep, d.rep_inv);
+        store4(out + (size_t)node * a.ldo + (size_t)(row - node * rep) * HD, sum[u], d.vec & 2);
+      }
     }
   }
   if (CL > 1) cl.sync();  // the others may still read this CTA's shared memory
