@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
       if (elect_one()) {
         constexpr uint32_t idS = f8_idesc(TM_PT, C::N, false), idO = f8_idesc(TM_PT, C::N, true);
         const int lost = blockIdx.x == 0 ? d.lost_tile : -1;
-        auto wait = [&](unsigned long long* bar, int phase) { return tm_wait(su32(bar), (uint32_t)phase & 1u, abort_w, status); };
+        auto wait = [&](unsigned long long* bar, int phase) { return kv8_wait(su32(bar), (uint32_t)phase & 1u, abort_w, status); };
         auto scores = [&](int i) -> bool {
           const int it = 2 * i, slot = it % C::S;
           if (i == lost || !wait(&ctl.full[slot], it / C::S)) return false;
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
           // the value row of a position no row may meet is zeroed: one behind the last that
           // is seen (whatever lies there), or a new row's with a NaN
           const int it = 2 * i + 1;
-          ok = tm_wait(su32(&ctl.full[it % C::S]), (uint32_t)(it / C::S) & 1u, abort_w, status) && ok;
+          ok = kv8_wait(su32(&ctl.full[it % C::S]), (uint32_t)(it / C::S) & 1u, abort_w, status) && ok;
           uint8_t* vr = sp + C::RING + it % C::S * C::SLOT;
           if (ok && j >= 0 && pos < m.end) {
             uint32_t bits = 0;
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
           }
           __syncwarp();
         }
-        ok = tm_wait(su32(&ctl.s_full), (uint32_t)i & 1u, abort_w, status) && ok;
+        ok = kv8_wait(su32(&ctl.s_full), (uint32_t)i & 1u, abort_w, status) && ok;
         __syncwarp();
         tc_fence_after();
         // scores in units of log2; -inf where the row does not see the position
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
         tc_fence_before();
         mbar_arrive(su32(&ctl.p_full));
         // the tile's output joins the running one
-        ok = tm_wait(su32(&ctl.o_full), (uint32_t)i & 1u, abort_w, status);
+        ok = kv8_wait(su32(&ctl.o_full), (uint32_t)i & 1u, abort_w, status);
         __syncwarp();
         tc_fence_after();
 #pragma unroll

@@ -23,6 +23,24 @@ struct KfDeal {
   int wait_1024, lost_tile;
 };
 
+// tm_wait without a call, which a kernel that moves registers between its warps cannot make.
+__device__ __forceinline__ bool kv8_wait(uint32_t bar, uint32_t parity, volatile int* abort_w, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  unsigned it = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    if ((++it & 63u) == 0) {
+      if (*abort_w) return false;
+      if ((clock64() - t0) >> 10 >= abort_w[1]) {
+        *abort_w = 1;
+        op_status(status, Q3TTS_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
 struct KfItem {
   Kv8Seq t;
   int seq, g, n0, rows;  // kv head, first row of the tile, rows
@@ -168,7 +186,7 @@ __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8Attn
       const int row = mine ? (int)kv8_row(a.c, checked(page0), my, m.g, pos % ps) : 0;
       for (int h = first; h <= last; ++h) {
         const int it = 2 * i + h, slot = it % S;
-        ok = ok && tm_wait(su32(&empty[slot]), ((uint32_t)(it / S) & 1u) ^ 1u, abort_w, status);
+        ok = ok && kv8_wait(su32(&empty[slot]), ((uint32_t)(it / S) & 1u) ^ 1u, abort_w, status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t fb = su32(&full[slot]);
@@ -206,7 +224,7 @@ __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8Attn
       look_up(i + 1);
       for (int h = first; h <= last; ++h) {
         const int it = 2 * i + h, slot = it % S;
-        ok = tm_wait(su32(&empty[slot]), ((uint32_t)(it / S) & 1u) ^ 1u, abort_w, status);
+        ok = kv8_wait(su32(&empty[slot]), ((uint32_t)(it / S) & 1u) ^ 1u, abort_w, status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t dst = ring + slot * (TM_PT * HD);

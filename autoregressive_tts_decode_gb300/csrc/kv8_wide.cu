@@ -9,17 +9,15 @@
 //   S = Q K^T  M 128 rows, N 128 positions: Q in tensor memory, K converted;
 //   O = P V    P in tensor memory, in its scores' place, V converted (an N-major operand).
 // The small terms are multiplied first into one accumulator; the outputs of successive tiles
-// are added in fp32 registers.  Keys' powers are factors of the scores' columns, values' powers of the
-// weights', both in fp32; a row's base is its largest score and power so far, less 8 (weights of
+// are added in fp32 registers.  Keys' powers are factors of the scores, values' powers of the
+// weights; a row's base is its largest score and power so far, a whole number, less 8 (weights of
 // 2^8, and up to 2^15 before the base follows: fp16's smallest step is 2^-24).
 //
-// Roles of a CTA (one per SM): two warps load codes, four convert them (a row's 16 codes a lane), one
-// thread issues the MMAs (scores of tile t + 1 before the outputs of tile t), and two groups of
-// four warps are the softmax, each with half of a tile's positions and half of the
-// output's elements (one thread a row and half).  The tensor cores work in order, which orders most of what shares
-// tensor memory: the scores of tile t + 2 come after the outputs of tile t, which have
-// read P where they go; the outputs of tile t + 1 wait for its P, which the softmax announces
-// when it has also read the outputs of tile t.
+// Roles of a CTA (one per SM): two warps load codes, two convert the keys and two the values (a row's 16 codes a lane), one
+// thread issues the MMAs, two groups of four warps are the softmax, of the even and of the odd tiles
+// (one thread a row, which needs no word of another), and two add up the outputs (a row's half a thread).  While one
+// group works on its scores, the tensor cores make the other's, or outputs: scores of tile t + 2 follow the outputs of
+// tile t, whose P they overwrite, and are the time in which those outputs are read.
 #include "kv8_tiles.cuh"
 
 namespace q3 {
@@ -27,15 +25,15 @@ namespace q3 {
 namespace {
 
 constexpr int KW_ROWS = 128;  // rows of a tile
-constexpr int KW_SOFT = 256;  // softmax threads
-constexpr int KW_CONV = 128;  // converting threads
+constexpr int KW_SOFT = 256;  // softmax threads, and as many that add up
+constexpr int KW_CONV = 64;   // threads that convert keys, and as many that convert values
 constexpr int KW_EXP = 60;  // exponents of the values' powers that count: -KW_EXP .. KW_EXP
 constexpr float KW_TINY = 1e-37f;  // the least factor of a score: a masked one stays -inf
 constexpr float KW_BASE = 8.f, KW_MOST = 15.f;  // log2 of the weights at the base, and at most
 
 template <class T, int HD>
 struct KwCfg {
-  static constexpr int MMA_WARP = 8, LOAD_WARP = 9, CONV_WARP = 11, THREADS = 480;
+  static constexpr int SUM_WARP = 8, MMA_WARP = 16, LOAD_WARP = 17, CONV_WARP = 19, IDLE_WARP = 23, THREADS = 768;
   static constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;
   static constexpr uint32_t TILE = TM_PT * HD * 2;   // a converted K or V tile
   static constexpr uint32_t SLOT = TM_PT * HD;       // a tile of codes
@@ -50,14 +48,15 @@ struct KwCfg {
 
 template <int S>
 struct KwCtl {
-  unsigned long long full[S], empty[S], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full, o_full, q_full, done, pw_full[4];
+  unsigned long long full[S], empty[S], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full, o_free, q_full, done, pw_full[4], base_full[4];
   uint32_t tmem;
   int abort_w[2];  // given up, limit of the waits
   int seq;
   alignas(16) unsigned none[2][4];  // positions of a tile whose values do not count
   unsigned bad[4][4];               // of them, new rows with a NaN
   float4 power[4][TM_PT];     // of a position (or four that share a block): key power, value power's exponent, its inverse
-  float part[2][KW_ROWS];
+  float bases[4][KW_ROWS];    // of the rows in a tile
+  float end[2][2][KW_ROWS];   // each softmax group's last base and sum
   float base[KW_ROWS], sum[KW_ROWS];
   float fac[8][KW_ROWS];
   int len[KF_SORT];
@@ -74,6 +73,7 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t a, uint64_t
       "r"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
 }
+// 32 or 8 columns of the warp's 32 lanes, one lane per thread (the 8 complete after wait::ld).
 __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -84,6 +84,16 @@ __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&r)[32]) {
         "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_ld8u(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -106,6 +116,10 @@ __device__ __forceinline__ uint2 codes_half(uint32_t w) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.y) : "h"(static_cast<unsigned short>(w >> 16)));
   return r;
 }
+// Registers, of 80 a thread at the launch (768 x 80 in all): the softmax's two warpgroups take
+// what loading, converting and the issue of the MMAs do not need (256 x (104 + 80 + 56)).
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 104;"); }
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
 // Barrier and vote of COUNT threads.
 template <int COUNT = KW_SOFT>
 __device__ __forceinline__ bool kw_vote(bool p, int id) {
@@ -149,9 +163,13 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
       mbar_init(su32(&ctl.v_empty[i]), 1);
       mbar_init(su32(&ctl.s_full[i]), 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(su32(&ctl.pw_full[i]), KW_CONV);
-    mbar_init(su32(&ctl.p_full), KW_SOFT);
+    for (int i = 0; i < 2; ++i) mbar_init(su32(&ctl.p_full[i]), KW_ROWS);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(su32(&ctl.pw_full[i]), KW_CONV);
+      mbar_init(su32(&ctl.base_full[i]), KW_ROWS);
+    }
     mbar_init(su32(&ctl.o_full), 1);
+    mbar_init(su32(&ctl.o_free), KW_SOFT);
     mbar_init(su32(&ctl.q_full), KW_SOFT);
     mbar_init(su32(&ctl.done), 1);
     ctl.abort_w[0] = 0;
@@ -180,145 +198,200 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
 
   if (m.nt > 0) {
     if (warp == C::LOAD_WARP || warp == C::LOAD_WARP + 1) {
+      give_registers();
       // (one warp for both: issuing the boxes of 16-position pages took longer than a tile's products)
       ok = load_tiles<HD, C::S, TMA, true>(&map, a, m, d.box, sbase + C::RING, ctl.full, ctl.empty, warp - C::LOAD_WARP, issued, abort_w);
     } else if (warp == C::MMA_WARP) {
       // ---- MMA issue
+      give_registers();
       if (elect_one()) {
         constexpr uint32_t idS = h16_idesc(KW_ROWS, TM_PT, false), idO = h16_idesc(KW_ROWS, HD, true);
         const int lost = blockIdx.x == 0 ? d.lost_tile : -1;
-        auto wait = [&](unsigned long long* bar, int phase) { return tm_wait(su32(bar), (uint32_t)phase & 1u, abort_w, status); };
-        ok = wait(&ctl.q_full, 0);
-        for (int i = 0; i <= m.nt && ok; ++i) {
-          if (i < m.nt) {  // scores of tile i
-            const int b = i & 1;
-            ok = i != lost && wait(&ctl.k_full[b], i >> 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t dk = sw128_desc(sbase + C::K + b * C::TILE);
+        auto wait = [&](unsigned long long* bar, int phase) { return kv8_wait(su32(bar), (uint32_t)phase & 1u, abort_w, status); };
+        auto scores = [&](int t) -> bool {
+          const int b = t & 1;
+          if (t == lost || !wait(&ctl.k_full[b], t >> 1)) return false;
+          tc_fence_after();
+          const uint64_t dk = sw128_desc(sbase + C::K + b * C::TILE);
 #pragma unroll
-            for (int term = C::TERMS - 1; term >= 0; --term)
+          for (int term = C::TERMS - 1; term >= 0; --term)
 #pragma unroll
-              for (int s = 0; s < HD / 16; ++s)
-                mma_f16_ts(tmem + b * 128, tmem + C::TM_Q + term * C::TM_QT + s * 8, dk + ((s >> 2) * TM_PT * 128 >> 4) + (s & 3) * 2, idS,
-                           term < C::TERMS - 1 || s != 0);
-            mma_commit(su32(&ctl.k_empty[b]));
-            mma_commit(su32(&ctl.s_full[b]));
-          }
-          if (i > 0) {  // outputs of tile i - 1
-            const int b = (i - 1) & 1;
-            ok = wait(&ctl.v_full[b], (i - 1) >> 1) && wait(&ctl.p_full, i - 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t dv = sw128_desc(sbase + C::V + b * C::TILE, HD == 128 ? TM_PT * 128 : 1024);
+            for (int s = 0; s < HD / 16; ++s)
+              mma_f16_ts(tmem + b * 128, tmem + C::TM_Q + term * C::TM_QT + s * 8, dk + ((s >> 2) * TM_PT * 128 >> 4) + (s & 3) * 2, idS,
+                         term < C::TERMS - 1 || s != 0);
+          mma_commit(su32(&ctl.k_empty[b]));
+          mma_commit(su32(&ctl.s_full[b]));
+          return true;
+        };
+        ok = wait(&ctl.q_full, 0) && scores(0) && (m.nt < 2 || scores(1));
+        for (int t = 0; t < m.nt && ok; ++t) {
+          const int b = t & 1;
+          ok = wait(&ctl.v_full[b], t >> 1) && wait(&ctl.p_full[b], t >> 1) && (t == 0 || wait(&ctl.o_free, t - 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dv = sw128_desc(sbase + C::V + b * C::TILE, HD == 128 ? TM_PT * 128 : 1024);
 #pragma unroll
-            for (int term = C::TERMS - 1; term >= 0; --term)
+          for (int term = C::TERMS - 1; term >= 0; --term)
 #pragma unroll
-              for (int s = 0; s < 8; ++s)  // 16 positions: eight columns of a term
-                mma_f16_ts(tmem + C::TM_O, tmem + b * 128 + 32 * (s >> 1) + 16 * term + 8 * (s & 1), dv + (s * 2048 >> 4), idO,
-                           term < C::TERMS - 1 || s != 0);
-            mma_commit(su32(&ctl.v_empty[b]));
-            mma_commit(su32(&ctl.o_full));
-          }
+            for (int s = 0; s < 8; ++s)  // 16 positions: eight columns of a term
+              mma_f16_ts(tmem + C::TM_O, tmem + b * 128 + 16 * s + 8 * term, dv + (s * 2048 >> 4), idO,
+                         term < C::TERMS - 1 || s != 0);
+          mma_commit(su32(&ctl.v_empty[b]));
+          mma_commit(su32(&ctl.o_full));
+          if (t + 2 < m.nt) ok = scores(t + 2);
         }
       }
       __syncwarp();
+    } else if (warp == C::IDLE_WARP) {
+      give_registers();  // (all warps of a warpgroup)
     } else if (warp >= C::CONV_WARP) {
-      // ---- codes to fp16; a thread has chunk ct % CH of every RPI-th of a tile's rows, and a position's powers
-      constexpr int CH = HD / 16, RPI = KW_CONV / CH;
-      const int ct = tid - C::CONV_WARP * 32, c = ct % CH, cw = warp - C::CONV_WARP;
+      give_registers();
+      // ---- codes to fp16: two warps the keys, two the values and all that comes of the powers.  A thread has
+      // chunk c (16 codes) of every RPI-th row.  Eight lanes have four chunks of rows r and r ^ 5, whose
+      // places in the swizzle are apart both in the codes' tile and (at twice the chunk) in fp16's; rows RPI apart,
+      // a multiple of 8, have the same.
+      constexpr int RPI = KW_CONV / (HD / 16), ROWS = TM_PT / RPI, U = ROWS < 4 ? ROWS : 4;
+      static_assert(RPI % 8 == 0 && ROWS % U == 0, "rows of a thread");
+      const int h = (warp - C::CONV_WARP) >> 1, cw = (warp - C::CONV_WARP) & 1, ct = cw * 32 + lane;
+      const int oct = ct >> 3, pair = HD == 128 ? oct >> 1 : oct & 3, c = (lane & 3) + (HD == 128 ? (oct & 1) * 4 : 0);
+      const int r0 = (lane & 4 ? pair ^ 5 : pair) + (HD == 128 ? 0 : (oct >> 2) * 8);
+      // the lanes of this thread's rows
+      const unsigned row_lanes = HD == 128 ? 0x0f0fu << ((lane & 16) + (lane & 4)) : 0xfu << (lane & 28);
+      const uint8_t* src = sp + C::RING + sw_at<HD>(r0, c);
+      uint8_t* dst = sp + (h ? C::V : C::K) + (c >> 2) * (TM_PT * 128) + r0 * 128;
+      const uint32_t x0 = ((2 * (c & 3)) ^ (r0 & 7)) << 4, x1 = ((2 * (c & 3) + 1) ^ (r0 & 7)) << 4;
+      unsigned long long* const to_full = h ? ctl.v_full : ctl.k_full;
+      unsigned long long* const to_empty = h ? ctl.v_empty : ctl.k_empty;
       const int ps = a.c.page, dq = TM_PT / ps, dr = TM_PT % ps, per_page = ps / a.c.block;
       const int* table = a.r.page_table + (size_t)m.seq * a.r.pps;
       const size_t pstride = (size_t)a.c.Hkv * per_page;  // from a key block's power to its value block's
-      static_assert(KW_CONV == TM_PT, "a thread a position");
-      Place at(m.t0 * TM_PT + ct, ps);
-      int kp, vp;
+      Place at[2] = {{m.t0 * TM_PT + ct, ps}, {m.t0 * TM_PT + ct + KW_CONV, ps}};
+      int kp[2], vp[2];  // powers of positions ct and ct + KW_CONV of the next tile
       auto powers_of = [&](int i) {
-        kp = vp = 127;
-        if (i < m.nt && (m.t0 + i) * TM_PT + ct < m.end) {
-          int page = __ldg(table + at.entry);
-          if (page < 0 || page >= a.c.n_pages) page = 0;  // (reported by the loading warp)
-          const uint8_t* p = a.c.powers + ((((size_t)a.c.layer * a.c.n_pages + page) * 2) * a.c.Hkv + m.g) * per_page + at.slot / a.c.block;
-          kp = __ldg(p);
-          vp = __ldg(p + pstride);
-        }
-        at.next(dq, dr, ps);
-      };
-      powers_of(0);
-      for (int i = 0; i < m.nt && ok; ++i) {
-        const int b = i & 1, p0 = (m.t0 + i) * TM_PT;
-        const bool edge = p0 + TM_PT > m.t.L;  // the tile reaches past the committed positions
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          const int it = 2 * i + h, slot = it % C::S;
-          ok = tm_wait(su32(&ctl.full[slot]), (uint32_t)(it / C::S) & 1u, abort_w, status) &&
-               tm_wait(su32(h ? &ctl.v_empty[b] : &ctl.k_empty[b]), ((uint32_t)(i >> 1) & 1u) ^ 1u, abort_w, status);
-          if (i == 1) ok = ok && tm_wait(su32(&ctl.q_full), 0u, abort_w, status);  // (the queries passed through its place)
-          if (kw_vote<KW_CONV>(!ok, 3)) {  // (giving up too: they leave together)
-            ok = false;
-            break;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          kp[j] = vp[j] = 127;
+          if (i < m.nt && (m.t0 + i) * TM_PT + ct + KW_CONV * j < m.end) {
+            int page = __ldg(table + at[j].entry);
+            if (page < 0 || page >= a.c.n_pages) page = 0;  // (reported by the loading warps)
+            const uint8_t* p = a.c.powers + ((((size_t)a.c.layer * a.c.n_pages + page) * 2) * a.c.Hkv + m.g) * per_page + at[j].slot / a.c.block;
+            kp[j] = __ldg(p);
+            vp[j] = __ldg(p + pstride);
           }
-          const uint8_t* src = sp + C::RING + slot * C::SLOT;
-          uint8_t* dst = sp + (h ? C::V : C::K) + b * C::TILE;
-          if (h == 0) {
-            // (the tile four before was done with: its outputs came before the scores whose keys' place this takes)
-            const int pos = p0 + ct, e = min(max(vp - 127, -KW_EXP), KW_EXP);
+          at[j].next(dq, dr, ps);
+        }
+      };
+      if (h) powers_of(0);
+      for (int i = 0; i < m.nt; ++i) {
+        const int b = i & 1, p0 = (m.t0 + i) * TM_PT, it = 2 * i + h, slot = it % C::S;
+        const bool edge = p0 + TM_PT > m.t.L;  // the tile reaches past the committed positions
+        bool some = false;
+        if (h) {
+          // (the tile four before was done with: its outputs came before the place of the values two before was free)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int n = ct + KW_CONV * j, pos = p0 + n, e = min(max(vp[j] - 127, -KW_EXP), KW_EXP);
             // a new row's block of NaN: rows that see it are told by its bit alone
-            const bool bad = pos >= m.t.L && (kp == 255 || vp == 255);
-            const bool none = bad || vp < 127 - KW_EXP || pos >= m.end;  // no values, or none that count
-            if (ct % GRAN == 0)
-              ctl.power[i & 3][ct / GRAN] = make_float4(bad ? 1.f : kv8_power(kp), vp == 255 && !bad ? kv8_power(255) : (float)e,
-                                                        __int_as_float((127 - e) << 23), 0.f);
+            const bool bad = pos >= m.t.L && (kp[j] == 255 || vp[j] == 255);
+            const bool none = bad || vp[j] < 127 - KW_EXP || pos >= m.end;  // no values, or none that count
+            if (n % GRAN == 0)
+              ctl.power[i & 3][n / GRAN] = make_float4(bad ? 1.f : kv8_power(kp[j]), vp[j] == 255 && !bad ? kv8_power(255) : (float)e,
+                                                       __int_as_float((127 - e) << 23), 0.f);
             const unsigned b0 = __ballot_sync(0xffffffffu, bad), n0 = __ballot_sync(0xffffffffu, none);
             if (lane == 0) {
-              ctl.bad[i & 3][cw] = b0;
-              ctl.none[i & 1][cw] = n0;
+              ctl.bad[i & 3][cw + 2 * j] = b0;
+              ctl.none[i & 1][cw + 2 * j] = n0;
             }
-            powers_of(i + 1);
           }
-          bool some = false;
-          if (h) {
+          if (!edge) mbar_arrive(su32(&ctl.pw_full[i & 3]));  // (an edge tile's bits come with the values)
+          powers_of(i + 1);
+        }
+        ok = kv8_wait(su32(&ctl.full[slot]), (uint32_t)(it / C::S) & 1u, abort_w, status) &&
+             kv8_wait(su32(&to_empty[b]), ((uint32_t)(i >> 1) & 1u) ^ 1u, abort_w, status) &&
+             (i != 1 || kv8_wait(su32(&ctl.q_full), 0u, abort_w, status));  // (the queries passed through its place)
+        ok = __all_sync(0xffffffffu, ok);
+        if (h) {
+          ok = !kw_vote<KW_CONV>(!ok, 3);  // (giving up too: the two warps leave together)
+          const uint4 z = *reinterpret_cast<const uint4*>(ctl.none[i & 1]);
+          some = edge || (z.x | z.y | z.z | z.w);
+        }
+        if (!ok) break;
+#pragma unroll 1
+        for (int u0 = 0; u0 < ROWS; u0 += U) {
+          uint4 x[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) x[u] = *reinterpret_cast<const uint4*>(src + slot * C::SLOT + (u0 + u) * (RPI * HD));
+          if (some) {
             // the value row of a position no row may meet is zeroed: one behind the last that is
             // seen (whatever lies there), or a new row's with a NaN
-            const uint4 z = *reinterpret_cast<const uint4*>(ctl.none[i & 1]);
-            some = edge || (z.x | z.y | z.z | z.w);
-          }
-          constexpr int U = TM_PT / RPI < 8 ? TM_PT / RPI : 8;  // of the thread's rows, loads on their way
-#pragma unroll 1
-          for (int r0 = ct / CH; r0 < TM_PT; r0 += U * RPI) {
-            uint4 x[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) x[u] = *reinterpret_cast<const uint4*>(src + sw_at<HD>(r0 + u * RPI, c));
-            if (some) {
-#pragma unroll
-              for (int u = 0; u < U; ++u) {
-                const int r = r0 + u * RPI, pos = p0 + r;
-                const uint32_t bits = ((x[u].x & 0x7f7f7f7fu) + 0x01010101u) | ((x[u].y & 0x7f7f7f7fu) + 0x01010101u) |
-                                      ((x[u].z & 0x7f7f7f7fu) + 0x01010101u) | ((x[u].w & 0x7f7f7f7fu) + 0x01010101u);
-                const unsigned row = ((1u << CH) - 1) << (lane / CH * CH);  // the lanes of this row
-                const bool nan = (__ballot_sync(0xffffffffu, (bits & 0x80808080u) != 0) & row) != 0 && pos >= m.t.L && pos < m.end;
-                if (nan || ((ctl.none[i & 1][r >> 5] >> (r & 31)) & 1u)) x[u] = make_uint4(0, 0, 0, 0);
-                if (nan && c == 0) atomicOr(&ctl.bad[i & 3][r >> 5], 1u << (r & 31));
-              }
-            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-              const int r = r0 + u * RPI;
-              const uint2 h0 = codes_half(x[u].x), h1 = codes_half(x[u].y), h2 = codes_half(x[u].z), h3 = codes_half(x[u].w);
-              uint8_t* row = dst + (c >> 2) * (TM_PT * 128) + r * 128;
-              *reinterpret_cast<uint4*>(row + (((2 * (c & 3)) ^ (r & 7)) << 4)) = make_uint4(h0.x, h0.y, h1.x, h1.y);
-              *reinterpret_cast<uint4*>(row + (((2 * (c & 3) + 1) ^ (r & 7)) << 4)) = make_uint4(h2.x, h2.y, h3.x, h3.y);
+              const int r = r0 + (u0 + u) * RPI, pos = p0 + r;
+              const uint32_t bits = ((x[u].x & 0x7f7f7f7fu) + 0x01010101u) | ((x[u].y & 0x7f7f7f7fu) + 0x01010101u) |
+                                    ((x[u].z & 0x7f7f7f7fu) + 0x01010101u) | ((x[u].w & 0x7f7f7f7fu) + 0x01010101u);
+              const bool nan = (__ballot_sync(0xffffffffu, (bits & 0x80808080u) != 0) & row_lanes) != 0 && pos >= m.t.L && pos < m.end;
+              if (nan || ((ctl.none[i & 1][r >> 5] >> (r & 31)) & 1u)) x[u] = make_uint4(0, 0, 0, 0);
+              if (nan && c == 0) atomicOr(&ctl.bad[i & 3][r >> 5], 1u << (r & 31));
             }
           }
-          mbar_arrive(su32(&ctl.empty[slot]));
-          proxy_fence();
-          mbar_arrive(su32(h ? &ctl.v_full[b] : &ctl.k_full[b]));
-          if (h == edge) mbar_arrive(su32(&ctl.pw_full[i & 3]));  // (an edge tile's bits come with the values)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const uint2 h0 = codes_half(x[u].x), h1 = codes_half(x[u].y), h2 = codes_half(x[u].z), h3 = codes_half(x[u].w);
+            uint8_t* row = dst + b * C::TILE + (u0 + u) * (RPI * 128);
+            *reinterpret_cast<uint4*>(row + x0) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+            *reinterpret_cast<uint4*>(row + x1) = make_uint4(h2.x, h2.y, h3.x, h3.y);
+          }
         }
+        mbar_arrive(su32(&ctl.empty[slot]));
+        proxy_fence();
+        mbar_arrive(su32(&to_full[b]));
+        if (h && edge) mbar_arrive(su32(&ctl.pw_full[i & 3]));
       }
-    } else if (warp < C::MMA_WARP) {
-      // ---- softmax: group wg has positions 64 wg .. of a tile, elements wg HD / 2 .. of the output
-      constexpr int HW = HD / 2;  // elements of the output that a thread holds
+    } else if (warp >= C::SUM_WARP) {
+      // ---- outputs: group wg adds up elements wg HD / 2 .. of the rows
+      constexpr int HW = HD / 2;
+      const int wg = (warp - C::SUM_WARP) >> 2, r = tid & 127;
+      const uint32_t src = tmem + C::TM_O + wg * HW + ((uint32_t)((warp & 3) * 32) << 16);
+      float base = TM_FLOOR;  // what the sums are relative to: no tile's base is more than 2^10 above
+      float2 o[HW / 2];
+#pragma unroll
+      for (int n = 0; n < HW / 2; ++n) o[n] = make_float2(0.f, 0.f);
+      for (int t = 0; t < m.nt; ++t) {
+        ok = kv8_wait(su32(&ctl.o_full), (uint32_t)t & 1u, abort_w, status) &&
+             kv8_wait(su32(&ctl.base_full[t & 3]), (uint32_t)(t >> 2) & 1u, abort_w, status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const float nb = ctl.bases[t & 3][r];
+        const bool rises = nb - base > 10.f;
+        if (__any_sync(0xffffffffu, rises)) {
+          const float corr = rises ? exp2_fast(base - nb) : 1.f;
+          if (rises) base = nb;
+#pragma unroll
+          for (int n = 0; n < HW / 2; ++n) o[n] = make_float2(o[n].x * corr, o[n].y * corr);
+        }
+        const float f = exp2_fast(nb - base);  // (whole numbers: exact)
+#pragma unroll
+        for (int n = 0; n < HW; n += 8) {
+          uint32_t x[8];
+          tmem_ld8u(src + n, x);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+          for (int e = 0; e < 8; e += 2)
+            o[(n + e) / 2] = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), make_float2(f, f), o[(n + e) / 2]);
+        }
+        tc_fence_before();
+        mbar_arrive(su32(&ctl.o_free));
+      }
+      if (!ok) *abort_w = 1;
+      if (wg == 0) ctl.base[r] = base;
+#pragma unroll
+      for (int n = 0; n < HW; n += 4)
+        *reinterpret_cast<float4*>(os + r * C::LD + wg * HW + n) = make_float4(o[n / 2].x, o[n / 2].y, o[n / 2 + 1].x, o[n / 2 + 1].y);
+    } else {
+      // ---- softmax: group wg has the tiles of its parity, a thread a row
+      take_registers();
+      constexpr int HW = HD / 2;  // elements of its query that a thread brings in
       const int wg = warp >> 2, r = tid & 127;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const int row = m.n0 + r, node = div_rep(min(row, m.n0 + m.rows - 1), rep, d.rep_inv);
@@ -344,7 +417,7 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
           top = __reduce_max_sync(LPR == 32 ? 0xffffffffu : 0xffffu << (16 * sub), top);
           const int E = min(max((int)(top >> 23) - 126, -100), 127);  // |q| < 2^E
           const float by = __int_as_float((127 + 15 - E) << 23);
-          if (lane % LPR == 0) ctl.base[at] = 1.4426950408889634f / sqrtf((float)HD) * __int_as_float((127 - 15 + E) << 23);
+          if (lane % LPR == 0) ctl.sum[at] = 1.4426950408889634f / sqrtf((float)HD) * __int_as_float((127 - 15 + E) << 23);
           float v[4] = {x[u].x * by, x[u].y * by, x[u].z * by, x[u].w * by};
 #pragma unroll
           for (int term = 0; term < C::TERMS; ++term) {
@@ -358,7 +431,7 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
           }
         }
         kw_vote(false, 1);
-        qs = ctl.base[r];
+        qs = ctl.sum[r];
 #pragma unroll
         for (int term = 0; term < C::TERMS; ++term)
 #pragma unroll
@@ -377,156 +450,135 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
       // what the row sees of the new rows
       unsigned long long mask = a.masks && r < m.rows ? a.masks[m.t.row0 + node] : 0ull;
       if (m.t.n < 64) mask &= (1ull << m.t.n) - 1;
-      float base = TM_FLOOR, l = 0.f, corr = 1.f;  // the row's base, sum of weights, factor of the base's last rise
-      float2 o[HW / 2];
-#pragma unroll
-      for (int n = 0; n < HW / 2; ++n) o[n] = make_float2(0.f, 0.f);
-      for (int i = 0; i <= m.nt; ++i) {
-        const int b = i & 1;
-        const bool scores = i < m.nt;
-        if (scores) {
-          const int p0 = (m.t0 + i) * TM_PT;
-          ok = tm_wait(su32(&ctl.s_full[b]), (uint32_t)(i >> 1) & 1u, abort_w, status) &&
-               tm_wait(su32(&ctl.pw_full[i & 3]), (uint32_t)(i >> 2) & 1u, abort_w, status) && ok;
-          __syncwarp();
-          tc_fence_after();
-          const uint32_t src = tmem + b * 128 + lanes;
-          const float4* pw = ctl.power[i & 3] + 64 / GRAN * wg;
-          // what the row sees of 32 positions: x is far below all scores elsewhere, NaN where a value is
-          auto see = [&](int ch, float (&x)[32]) {
-            const int dd = p0 + 32 * ch - m.t.L;  // the first of them, counted from the first new row
-            if (dd > -32) {
-              uint32_t sees;
-              if (a.masks) {
-                sees = dd >= 64 ? 0u : dd >= 0 ? (uint32_t)(mask >> dd) : (uint32_t)(mask << -dd) | ((1u << -dd) - 1);
-              } else {
-                const int n = node + 1 - dd;
-                sees = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
-              }
-              const uint32_t nan = ctl.bad[i & 3][ch];
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                x[e] = !((sees >> e) & 1u) ? -INFINITY : (nan >> e) & 1u ? __uint_as_float(0x7fc00000u) : x[e];
+      float base = TM_FLOOR, l = 0.f;  // the row's base and sum of weights, without the values' powers
+      for (int t = wg; t < m.nt; t += 2) {
+        const int p0 = (m.t0 + t) * TM_PT;
+        ok = kv8_wait(su32(&ctl.s_full[wg]), (uint32_t)(t >> 1) & 1u, abort_w, status) &&
+             kv8_wait(su32(&ctl.pw_full[t & 3]), (uint32_t)(t >> 2) & 1u, abort_w, status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t src = tmem + wg * 128 + lanes;
+        const float4* pw = ctl.power[t & 3];
+        // The tile in chunks of 32 positions.  Weights are 2^(score + power - base); without the
+        // power they join the sum.
+        constexpr int CK = 32;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+        for (int ch = 0; ch < TM_PT / CK; ++ch) {
+          float x[CK];
+          tmem_ld32f(src + CK * ch, x);
+          const int dd = p0 + CK * ch - m.t.L;  // its first position, counted from the first new row
+          if (dd > -CK) {
+            // -inf where the row does not see the position, NaN where a value that it sees is
+            uint32_t sees;
+            if (a.masks) {
+              sees = dd >= 64 ? 0u : dd >= 0 ? (uint32_t)(mask >> dd) : (uint32_t)(mask << -dd) | ((1u << -dd) - 1);
+            } else {
+              const int n = node + 1 - dd;
+              sees = n >= CK ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
             }
-          };
-          // the largest score and power
+            const uint32_t nan = ctl.bad[t & 3][ch];
+#pragma unroll
+            for (int e = 0; e < CK; ++e)
+              x[e] = !((sees >> e) & 1u) ? -INFINITY : (nan >> e) & 1u ? __uint_as_float(0x7fc00000u) : x[e];
+          }
+          const float4* pc = pw + CK / GRAN * ch;
           float top = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < CK; e += GRAN) {
+            float mx[2] = {x[e], x[e + (GRAN > 1)]};
+#pragma unroll
+            for (int f = 2; f < GRAN; ++f) mx[f & 1] = fmaxf(mx[f & 1], x[e + f]);
+            top = fmaxf(top, fmaf(fmaxf(mx[0], mx[1]), fmaxf(pc[e / GRAN].x * qs, KW_TINY), pc[e / GRAN].y));
+          }
+          const bool rises = top - base > KW_MOST;
+          if (__any_sync(0xffffffffu, rises)) {
+            // a new base: the tile's weights so far are scaled to it (by powers of two)
+            const float nb = rises ? ceilf(top) - KW_BASE : base, corr = exp2_fast(base - nb);
+            base = nb;
+            l *= corr;
+            sum[0] = make_float2(sum[0].x * corr, sum[0].y * corr);
+            sum[1] = make_float2(sum[1].x * corr, sum[1].y * corr);
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            float x[32];
-            tmem_ld32f(src + 32 * (2 * wg + h), x);
-            see(2 * wg + h, x);
+            for (int col = 0; col < CK * ch; col += 8) {
+              // (of each 16 columns the first term has eight, the second, if there is one, the others)
+              if (C::TERMS == 1 && (col & 8)) continue;
+              uint32_t w[8];
+              tmem_ld8u(src + col, w);
+              asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-            for (int e = 0; e < 32; e += GRAN) {
-              const float4 p = pw[(32 * h + e) / GRAN];
-              float mx = x[e];
-#pragma unroll
-              for (int f = 1; f < GRAN; ++f) mx = fmaxf(mx, x[e + f]);
-              top = fmaxf(top, fmaf(mx, fmaxf(p.x * qs, KW_TINY), p.y));
-            }
-          }
-          corr = 1.f;
-          if (kw_vote<64>(top - base > KW_MOST || !ok, 4 + (warp & 3))) {  // both halves of a row have the same base
-            ctl.part[wg][r] = top;
-            if (kw_vote<64>(!ok, 4 + (warp & 3))) {
-              ok = false;
-              break;
-            }
-            top = fmaxf(top, ctl.part[wg ^ 1][r]);
-            if (top - base > KW_MOST) {
-              corr = exp2_fast(base - (top - KW_BASE));
-              base = top - KW_BASE;
-              l *= corr;
-            }
-          }
-          // weights 2^(score + power - base); without the power they join the sum
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            const int ch = 2 * wg + h;
-            float x[32];
-            tmem_ld32f(src + 32 * ch, x);
-            see(ch, x);
-#pragma unroll
-            for (int e = 0; e < 32; e += GRAN) {
-              const float4 p = pw[(32 * h + e) / GRAN];
-              const float kq = fmaxf(p.x * qs, KW_TINY), nb = p.y - base;
-              if constexpr (GRAN == 1) {
-                x[e] = exp2_fast(fmaf(x[e], kq, nb));
-                sum[0].x = fmaf(x[e], p.z, sum[0].x);
-              } else {
-                float2 part = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int f = 0; f < GRAN; f += 2) {
-                  const float2 v = fma2(make_float2(x[e + f], x[e + f + 1]), make_float2(kq, kq), make_float2(nb, nb));
-                  x[e + f] = exp2_fast(v.x);
-                  x[e + f + 1] = exp2_fast(v.y);
-                  part = add2(part, make_float2(x[e + f], x[e + f + 1]));
-                }
-                sum[(e / GRAN) & 1] = fma2(part, make_float2(p.z, p.z), sum[(e / GRAN) & 1]);
+              for (int e = 0; e < 8; ++e) {
+                const float2 v = unpack_half(w[e]);
+                w[e] = pack_half(v.x * corr, v.y * corr);
               }
+              tmem_st8u(src + col, w);
             }
+          }
 #pragma unroll
-            for (int term = 0; term < C::TERMS; ++term) {
-              uint32_t w[16];
+          for (int e = 0; e < CK; e += GRAN) {
+            const float4 p = pc[e / GRAN];
+            const float kq = fmaxf(p.x * qs, KW_TINY), nb = p.y - base;
+            if constexpr (GRAN == 1) {
+              x[e] = exp2_fast(fmaf(x[e], kq, nb));
+              sum[0].x = fmaf(x[e], p.z, sum[0].x);
+            } else {
+              float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                w[e] = pack_half(x[2 * e], x[2 * e + 1]);
-                if (term + 1 < C::TERMS) {
-                  const float2 g = unpack_half(w[e]);
-                  x[2 * e] -= g.x;
-                  x[2 * e + 1] -= g.y;
-                }
+              for (int f = 0; f < GRAN; f += 2) {
+                const float2 v = fma2(make_float2(x[e + f], x[e + f + 1]), make_float2(kq, kq), make_float2(nb, nb));
+                x[e + f] = exp2_fast(v.x);
+                x[e + f + 1] = exp2_fast(v.y);
+                part[(f >> 1) & 1] = add2(part[(f >> 1) & 1], make_float2(x[e + f], x[e + f + 1]));
               }
-              tmem_st16u(src + 32 * ch + 16 * term, w);
+              sum[0] = fma2(add2(part[0], part[1]), make_float2(p.z, p.z), sum[0]);
             }
           }
-          // (the running sum takes a tile's at a time: its own roundings stay few)
-          sum[0] = add2(sum[0], sum[1]);
-          l += sum[0].x + sum[0].y;
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        }
-        // the output of the tile before joins the running one: the tensor cores have had
-        // this tile's softmax to finish it
-        if (i > 0) {
-          ok = tm_wait(su32(&ctl.o_full), (uint32_t)(i - 1) & 1u, abort_w, status) && ok;
-          __syncwarp();
-          tc_fence_after();
 #pragma unroll
-          for (int n = 0; n < HW; n += 32) {
-            float x[32];
-            tmem_ld32f(tmem + C::TM_O + wg * HW + n + lanes, x);
+          for (int q = 0; q < CK; q += 16) {
+            uint32_t w[8];
+            if constexpr (C::TERMS == 2) {
+              // the upper 11 bits, and what is left of the weight
+              float2 lo[8];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) o[(n + e) / 2] = add2(o[(n + e) / 2], make_float2(x[e], x[e + 1]));
+              for (int e = 0; e < 8; ++e) {
+                const float2 v = make_float2(x[q + 2 * e], x[q + 2 * e + 1]);
+                const float2 hi = make_float2(__uint_as_float(__float_as_uint(v.x) & 0xffffe000u), __uint_as_float(__float_as_uint(v.y) & 0xffffe000u));
+                w[e] = pack_half(hi.x, hi.y);
+                lo[e] = fma2(hi, make_float2(-1.f, -1.f), v);
+              }
+              tmem_st8u(src + CK * ch + q, w);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = pack_half(lo[e].x, lo[e].y);
+              tmem_st8u(src + CK * ch + q + 8, w);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = pack_half(x[q + 2 * e], x[q + 2 * e + 1]);
+              tmem_st8u(src + CK * ch + q, w);
+            }
           }
-          if (__any_sync(0xffffffffu, scores && corr != 1.f)) {
-#pragma unroll
-            for (int n = 0; n < HW / 2; ++n) o[n] = make_float2(o[n].x * corr, o[n].y * corr);
-          }
         }
-        if (scores) {
-          tc_fence_before();
-          mbar_arrive(su32(&ctl.p_full));
-        }
+        sum[0] = add2(sum[0], sum[1]);
+        ctl.bases[t & 3][r] = base;
+        mbar_arrive(su32(&ctl.base_full[t & 3]));
+        // (the running sum takes a tile's at a time: its own roundings stay few)
+        l += sum[0].x + sum[0].y;
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        mbar_arrive(su32(&ctl.p_full[wg]));
       }
-      ctl.part[wg][r] = l;
-      if (kw_vote(!ok, 1)) {
-        ok = false;
-        *abort_w = 1;
-      }
-      if (wg == 0) {
-        ctl.base[r] = base;
-        ctl.sum[r] = ctl.part[0][r] + ctl.part[1][r];
-      }
-#pragma unroll
-      for (int n = 0; n < HW; n += 4)
-        *reinterpret_cast<float4*>(os + r * C::LD + wg * HW + n) = make_float4(o[n / 2].x, o[n / 2].y, o[n / 2 + 1].x, o[n / 2 + 1].y);
+      if (!ok) *abort_w = 1;
+      ctl.end[wg][0][r] = base;
+      ctl.end[wg][1][r] = l;
     }
   } else if (have && tid < KW_ROWS) {
     ctl.base[tid] = TM_FLOOR;
     ctl.sum[tid] = 0.f;
   }
-  __syncwarp();
+  __syncthreads();
+  if (m.nt > 0 && tid < KW_ROWS)
+    ctl.sum[tid] = ctl.end[0][1][tid] * exp2_fast(ctl.end[0][0][tid] - ctl.base[tid]) + ctl.end[1][1][tid] * exp2_fast(ctl.end[1][0][tid] - ctl.base[tid]);
   // the shares of an item are joined: what each counts for, then every CL-th row
   if (CL > 1)
     cl.sync();
