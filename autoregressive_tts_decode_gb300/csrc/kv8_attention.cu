@@ -134,8 +134,6 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
   const uint32_t ring = sbase + C::RING;
   const bool have = take_item(a, d, CL, rank, R, m);
-  const int ps = a.c.page, dq = TM_PT / ps, dr = TM_PT % ps;
-  const int* table = a.r.page_table + (size_t)m.seq * a.r.pps;
   bool ok = true;
   int issued = 0;  // tiles that the loading warp has filled or is filling
 
@@ -177,22 +175,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
     } else {
       // ---- softmax: a thread has a position of the tile and an element of the output
       const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-      Place at(m.t0 * TM_PT + tid, ps);
-      const int per_page = ps / a.c.block;
-      const size_t pstride = (size_t)a.c.Hkv * per_page;  // from a key block's power to its value block's
-      // the powers of the thread's position in a tile
-      auto powers_of = [&](int pos, const Place& x, int& kp, int& vp) {
-        kp = vp = 127;
-        if (pos < m.end) {
-          int page = __ldg(table + x.entry);
-          if (page < 0 || page >= a.c.n_pages) page = 0;  // (reported by the loading warp)
-          const uint8_t* p = a.c.powers + ((((size_t)a.c.layer * a.c.n_pages + page) * 2) * a.c.Hkv + m.g) * per_page + x.slot / a.c.block;
-          kp = __ldg(p);
-          vp = __ldg(p + pstride);
-        }
-      };
-      int kp, vp;
-      powers_of(m.t0 * TM_PT + tid, at, kp, vp);
+      Powers pw(a, d, m, tid);
       // the queries' digits: a warp a row, magnitudes as 32-bit whole numbers with the sign in each digit
       for (int r = warp; r < R; r += 4) {
         constexpr int EPL = 4, LPR = HD / EPL;  // (a head dimension of 64: half of the lanes)
@@ -245,9 +228,8 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
       for (int nib = 0; nib < 8; ++nib) pat[nib] = sbase + C::P + sw_at<128>(nib, tid >> 4) + (tid & 15);
       for (int i = 0; i < m.nt; ++i) {
         const int pos = (m.t0 + i) * TM_PT + tid, j = pos - m.t.L;
-        const float kf = kv8_power(kp) * 32.f, vf = kv8_power(vp), eb = (float)min(max(vp - 127, -60), 60);
-        at.next(dq, dr, ps);
-        if (i + 1 < m.nt) powers_of(pos + TM_PT, at, kp, vp);
+        const float kf = kv8_power(pw.k) * 32.f, vf = kv8_power(pw.v), eb = (float)min(max(pw.v - 127, -60), 60);
+        pw.next(a, d, m, i, tid);
         bool isbad = false;
         const bool edge = (m.t0 + i + 1) * TM_PT > m.t.L;  // the tile reaches past the committed positions
         if (edge) {

@@ -21,24 +21,31 @@ struct KfDeal {
   unsigned rep_inv;
   int sorted;  // the sequences are taken longest first
   int wait_1024, lost_tile;
+  // powers: blocks of a page, from a key block's to its value block's; 128 positions are step_pages
+  // pages, step_blocks blocks and step_rem positions
+  int per_page, to_values, step_pages, step_blocks, step_rem;
 };
 
-// tm_wait without a call, which a kernel that moves registers between its warps cannot make.
+// tm_wait without a call, which a kernel that moves registers between its warps cannot
+// make, and with a longer sleep between looks, whose instructions the working warps would wait for.
 __device__ __forceinline__ bool kv8_wait(uint32_t bar, uint32_t parity, volatile int* abort_w, int* status) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
-  unsigned it = 0;
-  while (!mbar_try_wait(bar, parity)) {
-    if ((++it & 63u) == 0) {
-      if (*abort_w) return false;
-      if ((clock64() - t0) >> 10 >= abort_w[1]) {
-        *abort_w = 1;
-        op_status(status, Q3TTS_ERR_TIMEOUT);
-        return false;
-      }
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000)  // ns, at most
+        : "memory");
+    if (ok) return true;
+    if (*abort_w) return false;
+    if ((clock64() - t0) >> 10 >= abort_w[1]) {
+      *abort_w = 1;
+      op_status(status, Q3TTS_ERR_TIMEOUT);
+      return false;
     }
   }
-  return true;
 }
 
 struct KfItem {
@@ -87,21 +94,63 @@ __device__ __forceinline__ bool take_item(const Kv8AttnArgs& a, const KfDeal& d,
   return true;
 }
 
-// Position p of a sequence: its page's entry of the table and slot.
-struct Place {
-  int entry, slot;
-  __device__ __forceinline__ Place(int pos, int page) : entry(pos / page), slot(pos - pos / page * page) {}
-  // 128 positions on (dq, dr: 128 / page, 128 % page)
-  __device__ __forceinline__ void next(int dq, int dr, int page) {
-    entry += dq;
-    slot += dr;
-    if (slot >= page) {
-      slot -= page;
+// The powers of one position of each of an item's tiles, on their way a tile ahead, and
+// its page, which leads to them, two: neither is waited for.  Blocks and pages are stepped
+// over without a division (KfDeal), which took longer than the rest of it.
+struct Powers {
+  int k, v;  // bytes of its key's and its value's block (127 past what is seen)
+  // of the next tile's position when a tile's are used: page; of the one after that: its entry of
+  // the table's row, block of the page, place in the block
+  int page, entry, block, rem;
+  const uint8_t* layer;  // the kv head's key powers on page 0
+
+  __device__ __forceinline__ Powers(const Kv8AttnArgs& a, const KfDeal& d, const KfItem& m, int lane) {
+    const int pos = m.t0 * TM_PT + lane, ps = a.c.page, slot = pos % ps;
+    entry = pos / ps;
+    block = slot / a.c.block;
+    rem = slot - block * a.c.block;
+    layer = a.c.powers + ((long long)a.c.layer * a.c.n_pages * 2 * a.c.Hkv + m.g) * d.per_page;
+    look(a, m, 0, lane);
+    bytes(a, d, m, 0, lane);
+    step(a, d);
+    look(a, m, 1, lane);
+  }
+  // after tile i's have been used
+  __device__ __forceinline__ void next(const Kv8AttnArgs& a, const KfDeal& d, const KfItem& m, int i, int lane) {
+    bytes(a, d, m, i + 1, lane);
+    step(a, d);
+    look(a, m, i + 2, lane);
+  }
+
+ private:
+  __device__ __forceinline__ bool there(const KfItem& m, int i, int lane) const { return i < m.nt && (m.t0 + i) * TM_PT + lane < m.end; }
+  __device__ __forceinline__ void look(const Kv8AttnArgs& a, const KfItem& m, int i, int lane) {
+    page = there(m, i, lane) ? __ldg(a.r.page_table + (size_t)m.seq * a.r.pps + entry) : 0;
+  }
+  __device__ __forceinline__ void bytes(const Kv8AttnArgs& a, const KfDeal& d, const KfItem& m, int i, int lane) {
+    k = v = 127;
+    if (there(m, i, lane)) {
+      const int pg = (unsigned)page < (unsigned)a.c.n_pages ? page : 0;  // (reported by the loading warps)
+      const uint8_t* p = layer + (long long)pg * (2 * d.to_values) + block;
+      k = __ldg(p);
+      v = __ldg(p + d.to_values);
+    }
+  }
+  // 128 positions on
+  __device__ __forceinline__ void step(const Kv8AttnArgs& a, const KfDeal& d) {
+    rem += d.step_rem;
+    block += d.step_blocks;
+    if (rem >= a.c.block) {
+      rem -= a.c.block;
+      ++block;
+    }
+    entry += d.step_pages;
+    if (block >= d.per_page) {
+      block -= d.per_page;
       ++entry;
     }
   }
 };
-
 // Swizzled operand tiles with rows of W bytes (128 or 64) in atoms of eight rows.
 template <int W>
 __device__ __forceinline__ uint64_t sw_desc(uint32_t saddr, uint32_t lead = 16) {
@@ -308,6 +357,11 @@ int launch_tiles(Kernel kernel, TmKernel& known, int threads, size_t smem, bool 
           (((uintptr_t)a.out & (vec_bytes - 1)) == 0 && a.ldo % 4 == 0 ? 2 : 0);
   d.rep_inv = (unsigned)(((1ull << 32) + rep - 1) / rep);
   d.sorted = items * c > known.clusters[1] && a.r.n_seqs > 1 && a.r.n_seqs <= KF_SORT;
+  d.per_page = a.c.page / a.c.block;
+  d.to_values = a.c.Hkv * d.per_page;
+  d.step_pages = TM_PT / a.c.block / d.per_page;
+  d.step_blocks = TM_PT / a.c.block % d.per_page;
+  d.step_rem = TM_PT % a.c.block;
   d.wait_1024 = a.wait_1024;
   d.lost_tile = a.lost_tile;
   cfg.gridDim = dim3((unsigned)(items * c));

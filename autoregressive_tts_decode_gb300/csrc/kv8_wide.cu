@@ -14,7 +14,7 @@
 // 2^8, and up to 2^15 before the base follows: fp16's smallest step is 2^-24).
 //
 // Roles of a CTA (one per SM): two warps load codes, two convert the keys and two the values (a row's 16 codes a lane), one
-// thread issues the MMAs, two groups of four warps are the softmax, of the even and of the odd tiles
+// looks up the powers, one thread issues the MMAs, two groups of four warps are the softmax, of the even and of the odd tiles
 // (one thread a row, which needs no word of another), and two add up the outputs (a row's half a thread).  While one
 // group works on its scores, the tensor cores make the other's, or outputs: scores of tile t + 2 follow the outputs of
 // tile t, whose P they overwrite, and are the time in which those outputs are read.
@@ -33,7 +33,7 @@ constexpr float KW_BASE = 8.f, KW_MOST = 15.f;  // log2 of the weights at the ba
 
 template <class T, int HD>
 struct KwCfg {
-  static constexpr int SUM_WARP = 8, MMA_WARP = 16, LOAD_WARP = 17, CONV_WARP = 19, IDLE_WARP = 23, THREADS = 768;
+  static constexpr int SUM_WARP = 8, MMA_WARP = 16, LOAD_WARP = 17, CONV_WARP = 19, POWER_WARP = 23, THREADS = 768;
   static constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;
   static constexpr uint32_t TILE = TM_PT * HD * 2;   // a converted K or V tile
   static constexpr uint32_t SLOT = TM_PT * HD;       // a tile of codes
@@ -48,11 +48,11 @@ struct KwCfg {
 
 template <int S>
 struct KwCtl {
-  unsigned long long full[S], empty[S], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full, o_free, q_full, done, pw_full[4], base_full[4];
+  unsigned long long full[S], empty[S], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full, o_free, q_full, done, pw_full[4], pw_empty[4], bad_full[4], base_full[4];
   uint32_t tmem;
   int abort_w[2];  // given up, limit of the waits
   int seq;
-  alignas(16) unsigned none[2][4];  // positions of a tile whose values do not count
+  alignas(16) unsigned none[4][4];  // positions of a tile whose values do not count
   unsigned bad[4][4];               // of them, new rows with a NaN
   float4 power[4][TM_PT];     // of a position (or four that share a block): key power, value power's exponent, its inverse
   float bases[4][KW_ROWS];    // of the rows in a tile
@@ -73,7 +73,7 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t a, uint64_t
       "r"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
 }
-// 32 or 8 columns of the warp's 32 lanes, one lane per thread (the 8 complete after wait::ld).
+// 32 or 8 columns of the warp's 32 lanes, one lane per thread (complete after wait::ld).
 __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -83,7 +83,6 @@ __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&r)[32]) {
         "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]),
         "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_ld8u(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -165,7 +164,9 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) mbar_init(su32(&ctl.p_full[i]), KW_ROWS);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(su32(&ctl.pw_full[i]), KW_CONV);
+      mbar_init(su32(&ctl.pw_full[i]), 32);
+      mbar_init(su32(&ctl.pw_empty[i]), KW_ROWS + KW_CONV);
+      mbar_init(su32(&ctl.bad_full[i]), KW_CONV);
       mbar_init(su32(&ctl.base_full[i]), KW_ROWS);
     }
     mbar_init(su32(&ctl.o_full), 1);
@@ -242,17 +243,40 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
         }
       }
       __syncwarp();
-    } else if (warp == C::IDLE_WARP) {
-      give_registers();  // (all warps of a warpgroup)
-    } else if (warp >= C::CONV_WARP) {
+    } else if (warp == C::POWER_WARP) {
+      // ---- powers, four positions a lane
       give_registers();
-      // ---- codes to fp16: two warps the keys, two the values and all that comes of the powers.  A thread has
-      // chunk c (16 codes) of every RPI-th row.  Eight lanes have four chunks of rows r and r ^ 5, whose
-      // places in the swizzle are apart both in the codes' tile and (at twice the chunk) in fp16's; rows RPI apart,
-      // a multiple of 8, have the same.
-      constexpr int RPI = KW_CONV / (HD / 16), ROWS = TM_PT / RPI, U = ROWS < 4 ? ROWS : 4;
+      Powers pw[4] = {{a, d, m, lane}, {a, d, m, lane + 32}, {a, d, m, lane + 64}, {a, d, m, lane + 96}};
+      for (int t = 0; t < m.nt; ++t) {
+        ok = kv8_wait(su32(&ctl.pw_empty[t & 3]), ((uint32_t)(t >> 2) & 1u) ^ 1u, abort_w, status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int n = lane + 32 * j, pos = (m.t0 + t) * TM_PT + n, e = min(max(pw[j].v - 127, -KW_EXP), KW_EXP);
+          // a new row's block of NaN: rows that see it are told by its bit alone
+          const bool bad = pos >= m.t.L && (pw[j].k == 255 || pw[j].v == 255);
+          const bool none = bad || pw[j].v < 127 - KW_EXP || pos >= m.end;  // no values, or none that count
+          if (n % GRAN == 0)
+            ctl.power[t & 3][n / GRAN] = make_float4(bad ? 1.f : kv8_power(pw[j].k), pw[j].v == 255 && !bad ? kv8_power(255) : (float)e,
+                                                     __int_as_float((127 - e) << 23), 0.f);
+          const unsigned b0 = __ballot_sync(0xffffffffu, bad), n0 = __ballot_sync(0xffffffffu, none);
+          if (lane == 0) {
+            ctl.bad[t & 3][j] = b0;
+            ctl.none[t & 3][j] = n0;
+          }
+          pw[j].next(a, d, m, t, n);
+        }
+        mbar_arrive(su32(&ctl.pw_full[t & 3]));
+      }
+    } else if (warp >= C::CONV_WARP) {
+      // ---- codes to fp16: two warps the keys, two the values.  A thread has chunk c (16 codes) of every RPI-th
+      // row.  Eight lanes have four chunks of rows r and r ^ 5, whose places in the swizzle are apart
+      // both in the codes' tile and (at twice the chunk) in fp16's; rows RPI apart, a multiple of 8, have the same.
+      give_registers();
+      constexpr int RPI = KW_CONV / (HD / 16), ROWS = TM_PT / RPI, U = 8;
       static_assert(RPI % 8 == 0 && ROWS % U == 0, "rows of a thread");
-      const int h = (warp - C::CONV_WARP) >> 1, cw = (warp - C::CONV_WARP) & 1, ct = cw * 32 + lane;
+      const int h = (warp - C::CONV_WARP) >> 1, ct = ((warp - C::CONV_WARP) & 1) * 32 + lane;
       const int oct = ct >> 3, pair = HD == 128 ? oct >> 1 : oct & 3, c = (lane & 3) + (HD == 128 ? (oct & 1) * 4 : 0);
       const int r0 = (lane & 4 ? pair ^ 5 : pair) + (HD == 128 ? 0 : (oct >> 2) * 8);
       // the lanes of this thread's rows
@@ -262,60 +286,19 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
       const uint32_t x0 = ((2 * (c & 3)) ^ (r0 & 7)) << 4, x1 = ((2 * (c & 3) + 1) ^ (r0 & 7)) << 4;
       unsigned long long* const to_full = h ? ctl.v_full : ctl.k_full;
       unsigned long long* const to_empty = h ? ctl.v_empty : ctl.k_empty;
-      const int ps = a.c.page, dq = TM_PT / ps, dr = TM_PT % ps, per_page = ps / a.c.block;
-      const int* table = a.r.page_table + (size_t)m.seq * a.r.pps;
-      const size_t pstride = (size_t)a.c.Hkv * per_page;  // from a key block's power to its value block's
-      Place at[2] = {{m.t0 * TM_PT + ct, ps}, {m.t0 * TM_PT + ct + KW_CONV, ps}};
-      int kp[2], vp[2];  // powers of positions ct and ct + KW_CONV of the next tile
-      auto powers_of = [&](int i) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          kp[j] = vp[j] = 127;
-          if (i < m.nt && (m.t0 + i) * TM_PT + ct + KW_CONV * j < m.end) {
-            int page = __ldg(table + at[j].entry);
-            if (page < 0 || page >= a.c.n_pages) page = 0;  // (reported by the loading warps)
-            const uint8_t* p = a.c.powers + ((((size_t)a.c.layer * a.c.n_pages + page) * 2) * a.c.Hkv + m.g) * per_page + at[j].slot / a.c.block;
-            kp[j] = __ldg(p);
-            vp[j] = __ldg(p + pstride);
-          }
-          at[j].next(dq, dr, ps);
-        }
-      };
-      if (h) powers_of(0);
       for (int i = 0; i < m.nt; ++i) {
         const int b = i & 1, p0 = (m.t0 + i) * TM_PT, it = 2 * i + h, slot = it % C::S;
-        const bool edge = p0 + TM_PT > m.t.L;  // the tile reaches past the committed positions
-        bool some = false;
-        if (h) {
-          // (the tile four before was done with: its outputs came before the place of the values two before was free)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int n = ct + KW_CONV * j, pos = p0 + n, e = min(max(vp[j] - 127, -KW_EXP), KW_EXP);
-            // a new row's block of NaN: rows that see it are told by its bit alone
-            const bool bad = pos >= m.t.L && (kp[j] == 255 || vp[j] == 255);
-            const bool none = bad || vp[j] < 127 - KW_EXP || pos >= m.end;  // no values, or none that count
-            if (n % GRAN == 0)
-              ctl.power[i & 3][n / GRAN] = make_float4(bad ? 1.f : kv8_power(kp[j]), vp[j] == 255 && !bad ? kv8_power(255) : (float)e,
-                                                       __int_as_float((127 - e) << 23), 0.f);
-            const unsigned b0 = __ballot_sync(0xffffffffu, bad), n0 = __ballot_sync(0xffffffffu, none);
-            if (lane == 0) {
-              ctl.bad[i & 3][cw + 2 * j] = b0;
-              ctl.none[i & 1][cw + 2 * j] = n0;
-            }
-          }
-          if (!edge) mbar_arrive(su32(&ctl.pw_full[i & 3]));  // (an edge tile's bits come with the values)
-          powers_of(i + 1);
-        }
         ok = kv8_wait(su32(&ctl.full[slot]), (uint32_t)(it / C::S) & 1u, abort_w, status) &&
              kv8_wait(su32(&to_empty[b]), ((uint32_t)(i >> 1) & 1u) ^ 1u, abort_w, status) &&
+             (!h || kv8_wait(su32(&ctl.pw_full[i & 3]), (uint32_t)(i >> 2) & 1u, abort_w, status)) &&
              (i != 1 || kv8_wait(su32(&ctl.q_full), 0u, abort_w, status));  // (the queries passed through its place)
         ok = __all_sync(0xffffffffu, ok);
-        if (h) {
-          ok = !kw_vote<KW_CONV>(!ok, 3);  // (giving up too: the two warps leave together)
-          const uint4 z = *reinterpret_cast<const uint4*>(ctl.none[i & 1]);
-          some = edge || (z.x | z.y | z.z | z.w);
-        }
         if (!ok) break;
+        bool some = false;
+        if (h) {
+          const uint4 z = *reinterpret_cast<const uint4*>(ctl.none[i & 3]);
+          some = p0 + TM_PT > m.t.L || (z.x | z.y | z.z | z.w);  // (an edge tile: it reaches past the committed positions)
+        }
 #pragma unroll 1
         for (int u0 = 0; u0 < ROWS; u0 += U) {
           uint4 x[U];
@@ -330,7 +313,7 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
               const uint32_t bits = ((x[u].x & 0x7f7f7f7fu) + 0x01010101u) | ((x[u].y & 0x7f7f7f7fu) + 0x01010101u) |
                                     ((x[u].z & 0x7f7f7f7fu) + 0x01010101u) | ((x[u].w & 0x7f7f7f7fu) + 0x01010101u);
               const bool nan = (__ballot_sync(0xffffffffu, (bits & 0x80808080u) != 0) & row_lanes) != 0 && pos >= m.t.L && pos < m.end;
-              if (nan || ((ctl.none[i & 1][r >> 5] >> (r & 31)) & 1u)) x[u] = make_uint4(0, 0, 0, 0);
+              if (nan || ((ctl.none[i & 3][r >> 5] >> (r & 31)) & 1u)) x[u] = make_uint4(0, 0, 0, 0);
               if (nan && c == 0) atomicOr(&ctl.bad[i & 3][r >> 5], 1u << (r & 31));
             }
           }
@@ -345,7 +328,10 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
         mbar_arrive(su32(&ctl.empty[slot]));
         proxy_fence();
         mbar_arrive(su32(&to_full[b]));
-        if (h && edge) mbar_arrive(su32(&ctl.pw_full[i & 3]));
+        if (h) {
+          mbar_arrive(su32(&ctl.bad_full[i & 3]));
+          mbar_arrive(su32(&ctl.pw_empty[i & 3]));
+        }
       }
     } else if (warp >= C::SUM_WARP) {
       // ---- outputs: group wg adds up elements wg HD / 2 .. of the rows
@@ -454,7 +440,9 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
       for (int t = wg; t < m.nt; t += 2) {
         const int p0 = (m.t0 + t) * TM_PT;
         ok = kv8_wait(su32(&ctl.s_full[wg]), (uint32_t)(t >> 1) & 1u, abort_w, status) &&
-             kv8_wait(su32(&ctl.pw_full[t & 3]), (uint32_t)(t >> 2) & 1u, abort_w, status);
+             kv8_wait(su32(&ctl.pw_full[t & 3]), (uint32_t)(t >> 2) & 1u, abort_w, status) &&
+             // (a tile that reaches past the committed positions: its values' bits)
+             (p0 + TM_PT <= m.t.L || kv8_wait(su32(&ctl.bad_full[t & 3]), (uint32_t)(t >> 2) & 1u, abort_w, status));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -468,6 +456,7 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
         for (int ch = 0; ch < TM_PT / CK; ++ch) {
           float x[CK];
           tmem_ld32f(src + CK * ch, x);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
           const int dd = p0 + CK * ch - m.t.L;  // its first position, counted from the first new row
           if (dd > -CK) {
             // -inf where the row does not see the position, NaN where a value that it sees is
@@ -567,6 +556,7 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         mbar_arrive(su32(&ctl.p_full[wg]));
+        mbar_arrive(su32(&ctl.pw_empty[t & 3]));
       }
       if (!ok) *abort_w = 1;
       ctl.end[wg][0][r] = base;
