@@ -436,51 +436,55 @@ def reorder_rows(src, dst, parents, status=None):
     return dst
 
 
-# ---- the paged cache in 8 bits (include/q3tts_kv8.h)
+# ---- the paged cache in 8 bits (include/q3tts_kv8.h).  The smallest calls cost the GPU 3 us and the
+# host several times that: types are looked up once, attributes read once, and what is wrong is
+# told apart only when something is.
 
 _CACHE8 = struct.Struct("2P6i")  # q3tts_kv8_cache
 
 
+@functools.lru_cache(maxsize=None)
+def _kv8_types():
+    """(codes, powers as two types, row types with their codes, int32, masks' types)."""
+    import torch
+    return (torch.float8_e4m3fn, (torch.float8_e8m0fnu, torch.uint8), {torch.float32: F32, torch.bfloat16: BF16},
+            torch.int32, (torch.int64, torch.uint64))
+
+
 def _kv8(pool, scales, layer, page_table, lengths, start, what: str):
     """(device, kv heads, head dim, the arguments that the calls begin with)."""
-    import torch
-    dev, i32 = pool.get_device(), torch.int32
-    if dev < 0 or pool.dtype != torch.float8_e4m3fn or pool.dim() != 6 or not pool.is_contiguous():
+    codes, powers, _, i32, _ = _kv8_types()
+    dev, shape, blocks = pool.get_device(), pool.shape, scales.shape
+    if dev < 0 or pool.dtype != codes or len(shape) != 6 or shape[2] != 2 or not pool.is_contiguous():
         _bad(what, "pool", "a contiguous CUDA float8_e4m3fn tensor [layers, pages, 2, kv heads, page size, head dim]")
-    layers, pages, two, heads, page, hd = pool.shape
-    blocks = scales.shape[-1] if scales.dim() == 5 else 0
-    if two != 2 or blocks < 1 or page % blocks:
-        _bad(what, "pool and scales", "[layers, pages, 2, kv heads, page size, head dim] and [.., page size / block]")
-    if page_table.dim() != 2:
-        _bad(what, "page_table", "[seqs, pages per seq]")
-    seqs, pps = page_table.shape
-    kind = torch.uint8 if scales.dtype == torch.uint8 else torch.float8_e8m0fnu
-    powers = _cuda(scales, "scales", kind, dev, layers * pages * 2 * heads * blocks, what)
-    if scales.shape[:4] != pool.shape[:4]:
+    layers, pages, _, heads, page, hd = shape
+    if len(blocks) != 5 or blocks[4] < 1 or page % blocks[4]:
         _bad(what, "scales", "[layers, pages, 2, kv heads, page size / block]")
-    return dev, heads, hd, (_CACHE8.pack(pool.data_ptr(), powers, layers, pages, heads, page, hd, page // blocks), layer,
-                            _cuda(page_table, "page_table", i32, dev, seqs * pps, what), pps, seqs,
-                            _cuda(lengths, "lengths", i32, dev, seqs, what),
-                            _cuda(start, "start", i32, dev, seqs + 1, what))
+    n, pps, per_page = 0, 0, blocks[4]
+    if page_table.dim() == 2:
+        n, pps = page_table.shape
+    if (blocks[0] != layers or blocks[1] != pages or blocks[2] != 2 or blocks[3] != heads or scales.dtype not in powers
+            or scales.get_device() != dev or not scales.is_contiguous()):
+        _bad(what, "scales", f"contiguous float8_e8m0fnu or uint8 [{layers}, {pages}, 2, {heads}, page size / block] on cuda:{dev}")
+    if (page_table.dim() != 2 or page_table.dtype != i32 or page_table.get_device() != dev
+            or not page_table.is_contiguous()):
+        _bad(what, "page_table", f"contiguous int32 [seqs, pages per seq] on cuda:{dev}")
+    return dev, heads, hd, (_CACHE8.pack(pool.data_ptr(), scales.data_ptr(), layers, pages, heads, page, hd, page // per_page),
+                            layer, page_table.data_ptr(), pps, n, _cuda(lengths, "lengths", i32, dev, n, what),
+                            _cuda(start, "start", i32, dev, n + 1, what))
 
 
 def _row_pair(a, b, names, heads, hd: int, dev: int, what: str):
     """(rows, heads, type code, [address and pitch of both]) of two tensors [rows,
     heads, head dim] of one type; heads None: as a has them."""
-    import torch
-    ok = a.dim() == 3 and a.get_device() == dev and a.dtype in (torch.float32, torch.bfloat16)
-    if not ok or a.shape[2] != hd or a.shape[1] != (heads or a.shape[1]):
+    kinds, dt, shape = _kv8_types()[2], a.dtype, a.shape
+    if len(shape) != 3 or dt not in kinds or a.get_device() != dev or shape[2] != hd or shape[1] != (heads or shape[1]):
         _bad(what, names[0], f"an fp32 or bf16 tensor [rows, {heads or 'heads'}, {hd}] on cuda:{dev}")
-    if b.shape != a.shape or b.dtype != a.dtype or b.get_device() != dev:
+    if b.shape != shape or b.dtype != dt or b.get_device() != dev:
         _bad(what, names[1], f"of {names[0]}'s shape and type on cuda:{dev}")
-    n, h, _ = a.shape
-    return n, h, F32 if a.dtype == torch.float32 else BF16, (
-        a.data_ptr(), _pitch(a, n, h, hd, names[0], what), b.data_ptr(), _pitch(b, n, h, hd, names[1], what))
-
-
-def _status(status, dev: int, what: str):
-    import torch
-    return None if status is None else _cuda(status, "status", torch.int32, dev, 1, what)
+    n, h, _ = shape
+    return n, h, kinds[dt], (a.data_ptr(), _pitch(a, n, h, hd, names[0], what), b.data_ptr(),
+                             _pitch(b, n, h, hd, names[1], what))
 
 
 def kv8_write(pool, scales, layer: int, page_table, lengths, start, k, v, max_rows: Optional[int] = None, status=None):
@@ -494,8 +498,8 @@ def kv8_write(pool, scales, layer: int, page_table, lengths, start, k, v, max_ro
     what = "q3tts_kv8_write"
     dev, heads, hd, head = _kv8(pool, scales, layer, page_table, lengths, start, what)
     n, _, kind, pair = _row_pair(k, v, ("k", "v"), heads, hd, dev, what)
-    _call(dev, load().q3tts_kv8_write, what, *head, *pair, kind, n, max(1, n) if max_rows is None else max_rows,
-          _status(status, dev, what))
+    _call(dev, (_lib or load()).q3tts_kv8_write, what, *head, *pair, kind, n, (n or 1) if max_rows is None else max_rows,
+          None if status is None else _cuda(status, "status", _kv8_types()[3], dev, 1, what))
     return pool, scales
 
 
@@ -506,17 +510,18 @@ def kv8_read(pool, scales, layer: int, page_table, lengths, start, path=None, ma
     head dim], fp32 or bf16 (rows contiguous, any row pitch); needed without a path, made
     as bf16 with zeroes in rows that are not read otherwise.  The other arguments as for
     kv8_write.  Returns out."""
-    import torch
     what = "q3tts_kv8_read"
     dev, heads, hd, head = _kv8(pool, scales, layer, page_table, lengths, start, what)
     if out is None:
+        import torch
         if path is None:
             _bad(what, "out", "given, or a path")
         out = tuple(torch.zeros((path.numel(), heads, hd), dtype=torch.bfloat16, device=pool.device) for _ in range(2))
     n, _, kind, pair = _row_pair(out[0], out[1], ("out[0]", "out[1]"), heads, hd, dev, what)
-    _call(dev, load().q3tts_kv8_read, what, *head,
-          None if path is None else _cuda(path, "path", torch.int32, dev, n, what), *pair, kind, n,
-          max(1, n) if max_rows is None else max_rows, _status(status, dev, what))
+    i32 = _kv8_types()[3]
+    _call(dev, (_lib or load()).q3tts_kv8_read, what, *head, None if path is None else _cuda(path, "path", i32, dev, n, what),
+          *pair, kind, n, (n or 1) if max_rows is None else max_rows,
+          None if status is None else _cuda(status, "status", i32, dev, 1, what))
     return out
 
 
@@ -530,18 +535,18 @@ def kv8_attention(pool, scales, layer: int, page_table, lengths, start, q, masks
     (default: as many as there are rows, with masks up to MAX_TREE_NODES).  The other
     arguments as for kv8_write.  Returns out (as q; made if None, with zeroes in rows
     outside every sequence)."""
-    import torch
     what = "q3tts_kv8_attention"
     dev, _, hd, head = _kv8(pool, scales, layer, page_table, lengths, start, what)
     if out is None:
+        import torch
         out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
     n, heads, kind, pair = _row_pair(q, out, ("q", "out"), None, hd, dev, what)
     if max_rows is None:
         max_rows = max(1, n if masks is None else min(n, MAX_TREE_NODES))
-    m = None
-    if masks is not None:
-        m = _cuda(masks, "masks", torch.uint64 if masks.dtype == torch.uint64 else torch.int64, dev, n, what)
-    _call(dev, load().q3tts_kv8_attention, what, *head, m, *pair, heads, kind, n, max_rows, _status(status, dev, what))
+    _, _, _, i32, wide = _kv8_types()
+    _call(dev, (_lib or load()).q3tts_kv8_attention, what, *head,
+          None if masks is None else _cuda(masks, "masks", wide[1] if masks.dtype == wide[1] else wide[0], dev, n, what),
+          *pair, heads, kind, n, max_rows, None if status is None else _cuda(status, "status", i32, dev, 1, what))
     return out
 
 
