@@ -36,7 +36,7 @@ struct KfCfg {
   static constexpr int N = KF_DIGITS * R;
   static constexpr uint32_t SLOT = TM_PT * HD;  // a K or V tile
   static constexpr uint32_t Q = 0, P = N * HD, RING = P + N * TM_PT;
-  static constexpr int S = (R <= 8 ? 4 : R == 16 ? 4 : 8) * (128 / HD);  // tiles in the ring
+  static constexpr int S = (R <= 8 ? 3 : 4) * (128 / HD);  // tiles in the ring
   static constexpr uint32_t CTL = RING + S * SLOT, CTL_BYTES = 2048;
   static constexpr uint32_t TMEM_COLS = 2 * N < 32 ? 32 : 2 * N;  // scores, outputs
   // A cluster's CTAs wait for one another, and for tensor memory: a CTA's share of an SM's 512
@@ -453,6 +453,23 @@ int launch_few_rows(const Kv8AttnArgs& a, int layers, int dev, cudaStream_t s) {
   return launch_few<T, HD, 16, TMA>(a, layers, dev, s);
 }
 
+// Whether tiles of 128 rows (kv8_wide.cu) are done sooner than tiles of 16, whose cache is read
+// again for each of them.  A round of items costs about 7 us and 2.3 us for a tile of positions here,
+// of two CTAs on an SM, 11 and 1.75 us there, one on an SM; positions are split in up to eight where
+// that leaves one round.  8 kv heads of two q heads, fp32 (sequences x positions, new rows: us here,
+// us there): 1 x 112, 32: 10.9, 14.5; 1 x 2000, 16: 13.2, 18.8; 4 x 8000, 9: 62, 40; 16 x 112, 32: 25.7, 15.5;
+// 64 x 112, 9: 41, 48; 64 x 2000, 16: 179, 148; 64 x 8000, 32: 966, 447.
+bool wide_pays(const Kv8AttnArgs& a, int n_sm) {
+  const long rows = (long)a.r.max_rows * (a.Hq / a.c.Hkv), heads = (long)a.r.n_seqs * a.c.Hkv;
+  if (rows <= 16) return false;  // one tile: the rest of a wide one would be empty
+  const long tiles = ((long)a.r.pps * a.c.page + TM_PT - 1) / TM_PT;
+  auto us = [&](long items, long slots, double item, double tile) {
+    const long rounds = (items + slots - 1) / slots, most = slots / items < 8 ? slots / items : 8, share = rounds > 1 ? 1 : most;
+    return rounds * (item + tile * ((tiles + share - 1) / share));
+  };
+  return us(heads * ((rows + 127) / 128), n_sm, 11, 1.75) < us(heads * ((rows + 15) / 16), 2l * n_sm, 7, 2.3);
+}
+
 template <class T>
 int launch_few_of(const Kv8AttnArgs& a, int layers, bool tma, int dev, cudaStream_t s) {
   if (a.c.hd == 128) return tma ? launch_few_rows<T, 128, true>(a, layers, dev, s) : launch_few_rows<T, 128, false>(a, layers, dev, s);
@@ -468,7 +485,7 @@ int launch_kv8_attention(const Kv8AttnArgs& a, int layers, int dtype, cudaStream
   // number of times, or whole tiles of larger pages
   const int ps = a.c.page;
   const bool tma = (ps >= 8 && ps <= TM_PT && TM_PT % ps == 0) || ps % TM_PT == 0;
-  if ((long)a.r.max_rows * (a.Hq / a.c.Hkv) > 32) return launch_kv8_wide(a, layers, dtype, tma, dev, s);
+  if (wide_pays(a, n_sm)) return launch_kv8_wide(a, layers, dtype, tma, dev, s);
   return dtype == Q3TTS_F32 ? launch_few_of<float>(a, layers, tma, dev, s) : launch_few_of<bf16>(a, layers, tma, dev, s);
 }
 

@@ -3,6 +3,8 @@
 // descriptors, the launch.
 #pragma once
 
+#include <limits.h>
+
 #include "kv8.cuh"
 #include "tree.cuh"
 
@@ -67,15 +69,16 @@ __device__ __forceinline__ int first_item(const Kv8AttnArgs& a, const KfDeal& d,
 // the caller's next barrier).
 template <int THREADS>
 __device__ __forceinline__ void find_sequence(const Kv8Rows& rows, int wanted, int* len, int* seq) {
-  for (int i = threadIdx.x; i < rows.n_seqs; i += THREADS) len[i] = rows.lengths[i];
+  for (int i = threadIdx.x; i < (rows.n_seqs + 3 & ~3); i += THREADS) len[i] = i < rows.n_seqs ? rows.lengths[i] : INT_MIN;
   __syncthreads();
   for (int i = threadIdx.x; i < rows.n_seqs; i += THREADS) {
     const int mine = len[i];
     int r = 0;
-#pragma unroll 8
-    for (int j = 0; j < rows.n_seqs; ++j) {
-      const int o = len[j];
-      r += o > mine || (o == mine && j < i);
+#pragma unroll 4
+    for (int j = 0; j < rows.n_seqs; j += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(len + j);
+      r += (o.x > mine || (o.x == mine && j < i)) + (o.y > mine || (o.y == mine && j + 1 < i)) +
+           (o.z > mine || (o.z == mine && j + 2 < i)) + (o.w > mine || (o.w == mine && j + 3 < i));
     }
     if (r == wanted) *seq = i;
   }
@@ -208,7 +211,7 @@ __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8Attn
                                            volatile int* abort_w) {
   // tiles of the copying warp that stay on their way: fewer than its places of the ring
   constexpr int AHEAD = SPLIT ? 1 : 2;
-  static_assert(S >= 4 && S % 2 == 0, "places");
+  static_assert(SPLIT ? S >= 4 && S % 2 == 0 : S >= 3, "places");
   const int first = SPLIT ? kv : 0, last = SPLIT ? kv : 1;
   const int lane = threadIdx.x & 31, ps = a.c.page;
   const int* table = a.r.page_table + (size_t)m.seq * a.r.pps;

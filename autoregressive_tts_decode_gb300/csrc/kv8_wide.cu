@@ -59,7 +59,7 @@ struct KwCtl {
   float end[2][2][KW_ROWS];   // each softmax group's last base and sum
   float base[KW_ROWS], sum[KW_ROWS];
   float fac[8][KW_ROWS];
-  int len[KF_SORT];
+  alignas(16) int len[KF_SORT];
 };
 
 // kind::f16: D fp32, A and B fp16, A in tensor memory; B K-major or N-major (bit 16).
