@@ -16,20 +16,31 @@ namespace q3 {
 
 namespace {
 
-constexpr int KV8_THREADS = 256;
+constexpr int KV8_THREADS = 256;  // of the reads
+constexpr int KV8_WRITE_THREADS = 128;
 
-// Four consecutive elements of a row as fp32.
+// Four consecutive elements of a row, as they lie and as fp32.
 __device__ __forceinline__ float4 load4(const float* p, bool wide) {
   return wide ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(p[0], p[1], p[2], p[3]);
 }
-__device__ __forceinline__ float4 load4(const bf16* p, bool wide) {
-  if (wide) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
-  }
-  return make_float4(to_f(p[0]), to_f(p[1]), to_f(p[2]), to_f(p[3]));
+__device__ __forceinline__ uint2 load4(const bf16* p, bool wide) {
+  if (wide) return __ldg(reinterpret_cast<const uint2*>(p));
+  const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
+  return make_uint2(u[0] | (uint32_t)u[1] << 16, u[2] | (uint32_t)u[3] << 16);
 }
+__device__ __forceinline__ float4 as_f(float4 v) { return v; }
+__device__ __forceinline__ float4 as_f(uint2 u) {
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xffff0000u));
+}
+template <class T>
+struct Four {
+  using V = float4;
+};
+template <>
+struct Four<bf16> {
+  using V = uint2;
+};
 // The bits of |x|, 0 for an infinity or NaN.
 __device__ __forceinline__ uint32_t finite_bits(float x) {
   const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
@@ -44,13 +55,13 @@ __device__ __forceinline__ float scaled(float x, float by) {
 // RPL rows.  Up to U loads of rows stay in registers between the maximum and the
 // rounding (blocks of more rows are read twice, the second time from the caches).
 template <class T, int HD, int U>
-__global__ void __launch_bounds__(KV8_THREADS) kv8_write_kernel(Kv8Cache c, Kv8Rows r, const T* k, int ldk, const T* v,
+__global__ void __launch_bounds__(KV8_WRITE_THREADS, U == 1 ? 8 : sizeof(T) == 4 ? 5 : 8) kv8_write_kernel(Kv8Cache c, Kv8Rows r, const T* k, int ldk, const T* v,
                                                                 int ldv, int blocks, long long units, int wide) {
   pdl_wait();
   pdl_trigger();
   constexpr int RPL = 128 / HD;
   const int lane = threadIdx.x & 31, sub = lane / (HD / 4), e0 = lane % (HD / 4) * 4;
-  const long long unit = ((long long)blockIdx.x * KV8_THREADS + threadIdx.x) >> 5;
+  const long long unit = ((long long)blockIdx.x * KV8_WRITE_THREADS + threadIdx.x) >> 5;
   if (unit >= units) return;
   const int jh = (int)(unit % (2 * c.Hkv)), j = jh >= c.Hkv, head = jh - j * c.Hkv;
   const int seq = (int)(unit / (2 * c.Hkv) / blocks), nth = (int)(unit / (2 * c.Hkv) % blocks);
@@ -60,15 +71,16 @@ __global__ void __launch_bounds__(KV8_THREADS) kv8_write_kernel(Kv8Cache c, Kv8R
   const int from = max(p0, t.L), to = min(p0 + c.block, t.L + t.n);  // new ones in it
   if (from >= to) return;
   const int m = to - from, held = from - p0;  // held: rows that were there
-  const T* src = (j ? v : k) + (size_t)(t.row0 + from - t.L) * (j ? ldv : ldk) + head * HD + e0;
-  const size_t ld = j ? ldv : ldk;
-  float4 x[U];
+  const int ld = j ? ldv : ldk;
+  const T* src = (j ? v : k) + (long long)(t.row0 + from - t.L) * ld + head * HD + e0;
+  using V = typename Four<T>::V;
+  V x[U];
   auto load = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * RPL + sub;
-      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < m) x[u] = load4(src + i * ld, wide);
+      x[u] = V{};
+      if (i < m) x[u] = load4(src + (long long)i * ld, wide);
     }
   };
   const int page = __ldg(r.page_table + (size_t)seq * r.pps + p0 / c.page);
@@ -76,8 +88,10 @@ __global__ void __launch_bounds__(KV8_THREADS) kv8_write_kernel(Kv8Cache c, Kv8R
   for (int i0 = 0; i0 < m; i0 += U * RPL) {
     load(i0);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      top = max(max(top, max(finite_bits(x[u].x), finite_bits(x[u].y))), max(finite_bits(x[u].z), finite_bits(x[u].w)));
+    for (int u = 0; u < U; ++u) {
+      const float4 f = as_f(x[u]);
+      top = max(max(top, max(finite_bits(f.x), finite_bits(f.y))), max(finite_bits(f.z), finite_bits(f.w)));
+    }
   }
   top = __reduce_max_sync(0xffffffffu, top);
   if (page < 0 || page >= c.n_pages) {
@@ -108,9 +122,8 @@ __global__ void __launch_bounds__(KV8_THREADS) kv8_write_kernel(Kv8Cache c, Kv8R
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * RPL + sub;
-      if (i < m)
-        *reinterpret_cast<uint32_t*>(dst + (size_t)i * HD) =
-            kv8_codes(scaled(x[u].x, by), scaled(x[u].y, by), scaled(x[u].z, by), scaled(x[u].w, by));
+      const float4 f = as_f(x[u]);
+      if (i < m) *reinterpret_cast<uint32_t*>(dst + i * HD) = kv8_codes(scaled(f.x, by), scaled(f.y, by), scaled(f.z, by), scaled(f.w, by));
     }
   }
   if (lane == 0) *power = (uint8_t)byte;
@@ -202,8 +215,8 @@ __global__ void __launch_bounds__(KV8_THREADS) kv8_read_kernel(Kv8Cache c, Kv8Ro
   }
 }
 
-int grid_of(long long units, unsigned* grid) {
-  const long long g = (units * 32 + KV8_THREADS - 1) / KV8_THREADS;
+int grid_of(long long units, int threads, unsigned* grid) {
+  const long long g = (units * 32 + threads - 1) / threads;
   if (g > 0x7fffffffll) return Q3TTS_ERR_UNSUPPORTED;
   *grid = (unsigned)g;
   return Q3TTS_OK;
@@ -214,10 +227,10 @@ int launch_write(const Kv8Cache& c, const Kv8Rows& r, const void* k, int ldk, co
   const int blocks = (int)(((long long)r.max_rows + 2ll * c.block - 2) / c.block);  // touched at most, from any offset
   const long long units = (long long)r.n_seqs * blocks * 2 * c.Hkv;
   unsigned grid;
-  const int rc = grid_of(units, &grid);
+  const int rc = grid_of(units, KV8_WRITE_THREADS, &grid);
   if (rc != Q3TTS_OK) return rc;
   const int wide = (((uintptr_t)k | (uintptr_t)v) & (4 * sizeof(T) - 1)) == 0 && ldk % 4 == 0 && ldv % 4 == 0;
-  return launch_pdl(kv8_write_kernel<T, HD, U>, dim3(grid), dim3(KV8_THREADS), 0, s, c, r, static_cast<const T*>(k), ldk,
+  return launch_pdl(kv8_write_kernel<T, HD, U>, dim3(grid), dim3(KV8_WRITE_THREADS), 0, s, c, r, static_cast<const T*>(k), ldk,
                     static_cast<const T*>(v), ldv, blocks, units, wide) == cudaSuccess
              ? Q3TTS_OK
              : Q3TTS_ERR_CUDA;
@@ -234,7 +247,7 @@ int launch_read(const Kv8Cache& c, const Kv8Rows& r, const int* path, void* k, i
   const int chunks = (int)(((long long)r.max_rows + KV8_READ_ROWS - 1) / KV8_READ_ROWS);
   const long long units = (long long)r.n_seqs * chunks * 2 * c.Hkv;
   unsigned grid;
-  const int rc = grid_of(units, &grid);
+  const int rc = grid_of(units, KV8_THREADS, &grid);
   if (rc != Q3TTS_OK) return rc;
   const size_t al = 32 / sizeof(T);
   const int wide = (((uintptr_t)k | (uintptr_t)v) & 31) == 0 && ldk % al == 0 && ldv % al == 0;
