@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
       // the queries' digits: a warp a row, magnitudes as 32-bit whole numbers with the sign in each digit
       for (int r = warp; r < R; r += 4) {
         constexpr int EPL = 4, LPR = HD / EPL;  // (a head dimension of 64: half of the lanes)
-        const int row = m.n0 + min(r, m.rows - 1), node = div_rep(row, rep, d.rep_inv);
+        const int row = m.n0 + min(r, m.rows - 1), node = kv8_div(row, rep, d.rep_inv);
         const T* q = static_cast<const T*>(a.q) + (size_t)(m.t.row0 + node) * a.ldq + (size_t)(m.g * rep + row - node * rep) * HD;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (lane < LPR) x = q4(q + lane * EPL, d.vec & 1);
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const bool sees = pos < m.end && (a.masks ? (ctl.mask[r] >> min(j, 63)) & 1ull
-                                                      : j <= div_rep(m.n0 + r, rep, d.rep_inv));
+                                                      : j <= kv8_div(m.n0 + r, rep, d.rep_inv));
             x[r] = !sees ? -INFINITY : isbad ? __int_as_float(0x7fc00000) : x[r];
           }
         }
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           if (r >= m.rows) break;
-          const int row = m.n0 + r, node = div_rep(row, rep, d.rep_inv);
+          const int row = m.n0 + r, node = kv8_div(row, rep, d.rep_inv);
           const float sum = ctl.sum[r];
           out[(size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + row - node * rep) * HD + tid] =
               from_f<T>(sum == 0.f ? 0.f : o[r] / sum);
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
 #pragma unroll
         for (int s = 0; s < 8; ++s)
           if (s < CL) sum = fmaf(v[s], ctl.fac[s][n], sum);
-        const int row = m.n0 + n, node = div_rep(row, rep, d.rep_inv);
+        const int row = m.n0 + n, node = kv8_div(row, rep, d.rep_inv);
         out[(size_t)(m.t.row0 + node) * a.ldo + (size_t)(m.g * rep + row - node * rep) * HD + e % HD] = from_f<T>(sum);
       }
     }

@@ -50,6 +50,13 @@ __device__ __forceinline__ bool kv8_wait(uint32_t bar, uint32_t parity, volatile
   }
 }
 
+// row / rep (inv = ceil(2^32 / rep)): the product is the quotient or, of many rows, one more.
+__device__ __forceinline__ int kv8_div(int row, int rep, unsigned inv) {
+  if (rep == 1) return row;
+  const int q = (int)__umulhi((unsigned)row, inv);
+  return q - (q * rep > row);
+}
+
 struct KfItem {
   Kv8Seq t;
   int seq, g, n0, rows;  // kv head, first row of the tile, rows
@@ -90,7 +97,7 @@ __device__ __forceinline__ bool take_item(const Kv8AttnArgs& a, const KfDeal& d,
   m.rows = m.nt = m.t0 = m.end = 0;
   if (!kv8_seq(a.r, a.c.page, m.seq, true, m.t) || m.n0 >= m.t.n * rep) return false;
   m.rows = min(rows, m.t.n * rep - m.n0);
-  m.end = m.t.L + (a.masks ? m.t.n : div_rep(m.n0 + m.rows - 1, rep, d.rep_inv) + 1);
+  m.end = m.t.L + (a.masks ? m.t.n : kv8_div(m.n0 + m.rows - 1, rep, d.rep_inv) + 1);
   const int all = (m.end + TM_PT - 1) / TM_PT, per = (all + cl - 1) / cl;
   m.t0 = min(all, rank * per);
   m.nt = min(all, m.t0 + per) - m.t0;

@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
       constexpr int HW = HD / 2;  // elements of its query that a thread brings in
       const int wg = warp >> 2, r = tid & 127;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-      const int row = m.n0 + r, node = div_rep(min(row, m.n0 + m.rows - 1), rep, d.rep_inv);
+      const int row = m.n0 + r, node = kv8_div(min(row, m.n0 + m.rows - 1), rep, d.rep_inv);
       float qs;
       {
         // the queries, scaled to 2^14 .. 2^15, go to tensor memory, a lane a row, by way of shared
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
         float4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int at = min(m.n0 + (warp * U + u) * RPW + sub, m.n0 + m.rows - 1), of = div_rep(at, rep, d.rep_inv);
+          const int at = min(m.n0 + (warp * U + u) * RPW + sub, m.n0 + m.rows - 1), of = kv8_div(at, rep, d.rep_inv);
           x[u] = q4(q0 + (size_t)of * a.ldq + (size_t)(at - of * rep) * HD, d.vec & 1);
         }
 #pragma unroll
@@ -574,7 +574,9 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
     cl.sync();
   else
     __syncthreads();
-  if (have && tid < KW_ROWS) {
+  if (have && CL == 1) {
+    if (tid < KW_ROWS) ctl.fac[0][tid] = ctl.sum[tid] == 0.f ? 0.f : 1.f / ctl.sum[tid];
+  } else if (have && tid < KW_ROWS) {
     float bs[8], sm[8], mx = TM_FLOOR, all = 0.f;
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
@@ -619,7 +621,7 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
       for (int u = 0; u < U; ++u) {
         const int n = n0 + u * CL * RPI;
         if (n >= m.rows) break;
-        const int row = m.n0 + n, node = div_rep(row, rep, d.rep_inv);
+        const int row = m.n0 + n, node = kv8_div(row, rep, d.rep_inv);
         store4(out + (size_t)node * a.ldo + (size_t)(row - node * rep) * HD, sum[u], d.vec & 2);
       }
     }
