@@ -24,6 +24,29 @@ struct Kv8Cache {
   uint8_t* codes;
   uint8_t* powers;
   int n_pages, Hkv, page, hd, block, layer;
+  unsigned page_inv, block_inv;  // for kv8_div
+};
+// n / d for whole numbers below 2^31, with inv = ceil(2^32 / d): the product is the quotient or,
+// of large ones, one more.
+__device__ __forceinline__ int kv8_div(int n, int d, unsigned inv) {
+  if (d == 1) return n;
+  const int q = (int)__umulhi((unsigned)n, inv);
+  return q - (q * d > n);
+}
+inline unsigned kv8_inverse(int d) { return (unsigned)(((1ull << 32) + d - 1) / d); }
+// Rows of codes and bytes of powers of one kv head's keys or values in a layer: of page 0, and
+// from one page to the next.
+struct Kv8Plane {
+  long long row, power;
+  int rows, powers, per_page;
+  __device__ __forceinline__ Kv8Plane(const Kv8Cache& c, int kv, int head) {
+    const long long first = ((long long)c.layer * c.n_pages * 2 + kv) * c.Hkv + head;
+    per_page = kv8_div(c.page, c.block, c.block_inv);
+    row = first * c.page;
+    power = first * per_page;
+    rows = 2 * c.Hkv * c.page;
+    powers = 2 * c.Hkv * per_page;
+  }
 };
 __device__ __forceinline__ long long kv8_row(const Kv8Cache& c, int page, int kv, int head, int slot) {
   return ((((long long)c.layer * c.n_pages + page) * 2 + kv) * c.Hkv + head) * c.page + slot;

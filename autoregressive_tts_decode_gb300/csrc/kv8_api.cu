@@ -23,6 +23,8 @@ q3::Kv8Cache desc(const q3tts_kv8_cache& c, int layer) {
   d.hd = c.head_dim;
   d.block = c.block;
   d.layer = layer;
+  d.page_inv = q3::kv8_inverse(c.page_size);
+  d.block_inv = q3::kv8_inverse(c.block);
   return d;
 }
 

@@ -56,18 +56,18 @@ __device__ __forceinline__ float scaled(float x, float by) {
 // rounding (blocks of more rows are read twice, the second time from the caches).
 template <class T, int HD, int U>
 __global__ void __launch_bounds__(KV8_WRITE_THREADS, U == 1 ? 8 : sizeof(T) == 4 ? 5 : 8) kv8_write_kernel(Kv8Cache c, Kv8Rows r, const T* k, int ldk, const T* v,
-                                                                int ldv, int blocks, long long units, int wide) {
+                                                                int ldv, int blocks, unsigned units, int wide) {
   pdl_wait();
   pdl_trigger();
   constexpr int RPL = 128 / HD;
   const int lane = threadIdx.x & 31, sub = lane / (HD / 4), e0 = lane % (HD / 4) * 4;
-  const long long unit = ((long long)blockIdx.x * KV8_WRITE_THREADS + threadIdx.x) >> 5;
+  const unsigned unit = (blockIdx.x * KV8_WRITE_THREADS + threadIdx.x) >> 5;
   if (unit >= units) return;
-  const int jh = (int)(unit % (2 * c.Hkv)), j = jh >= c.Hkv, head = jh - j * c.Hkv;
-  const int seq = (int)(unit / (2 * c.Hkv) / blocks), nth = (int)(unit / (2 * c.Hkv) % blocks);
+  const unsigned planes = 2 * c.Hkv, of = unit / planes, seq = of / blocks;
+  const int jh = unit - of * planes, j = jh >= c.Hkv, head = jh - j * c.Hkv, nth = of - seq * blocks;
   Kv8Seq t;
   if (!kv8_seq(r, c.page, seq, true, t)) return;
-  const int p0 = (t.L / c.block + nth) * c.block;                    // the block's first position
+  const int p0 = (kv8_div(t.L, c.block, c.block_inv) + nth) * c.block;  // the block's first position
   const int from = max(p0, t.L), to = min(p0 + c.block, t.L + t.n);  // new ones in it
   if (from >= to) return;
   const int m = to - from, held = from - p0;  // held: rows that were there
@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(KV8_WRITE_THREADS, U == 1 ? 8 : sizeof(T) == 4
       if (i < m) x[u] = load4(src + (long long)i * ld, wide);
     }
   };
-  const int page = __ldg(r.page_table + (size_t)seq * r.pps + p0 / c.page);
+  const int entry = kv8_div(p0, c.page, c.page_inv), slot = p0 - entry * c.page;
+  const int page = __ldg(r.page_table + (size_t)seq * r.pps + entry);
   uint32_t top = 0;
   for (int i0 = 0; i0 < m; i0 += U * RPL) {
     load(i0);
@@ -98,8 +99,9 @@ __global__ void __launch_bounds__(KV8_WRITE_THREADS, U == 1 ? 8 : sizeof(T) == 4
     if (lane == 0) op_status(r.status, Q3TTS_ERR_ARG);
     return;
   }
-  const long long row = kv8_row(c, page, j, head, p0 % c.page);
-  uint8_t* power = c.powers + row / c.block;
+  const Kv8Plane at(c, j, head);
+  const long long row = at.row + (long long)page * at.rows + slot;
+  uint8_t* power = c.powers + at.power + (long long)page * at.powers + kv8_div(slot, c.block, c.block_inv);
   int byte = max((int)((top + 0x1fffffu) >> 23) - 8, 0);
   if (held > 0) {
     const int before = *power;
@@ -107,10 +109,10 @@ __global__ void __launch_bounds__(KV8_WRITE_THREADS, U == 1 ? 8 : sizeof(T) == 4
       // what is there is rounded again
       const float by = kv8_power(before - byte + 127);
       for (int i = sub; i < held; i += RPL) {
-        uint32_t* at = reinterpret_cast<uint32_t*>(c.codes + (row + i) * HD + e0);
+        uint32_t* code = reinterpret_cast<uint32_t*>(c.codes + (row + i) * HD + e0);
         float f[4];
-        fp8x4_to_f32(*at, f);
-        *at = kv8_codes(f[0] * by, f[1] * by, f[2] * by, f[3] * by);
+        fp8x4_to_f32(*code, f);
+        *code = kv8_codes(f[0] * by, f[1] * by, f[2] * by, f[3] * by);
       }
     }
     byte = max(byte, before);
@@ -163,18 +165,21 @@ constexpr int KV8_READ_ROWS = 16;
 
 template <class T, int HD>
 __global__ void __launch_bounds__(KV8_THREADS) kv8_read_kernel(Kv8Cache c, Kv8Rows r, const int* path, T* k, int ldk, T* v,
-                                                               int ldv, int chunks, long long units, int wide) {
+                                                               int ldv, int chunks, unsigned units, int wide) {
   pdl_wait();
   pdl_trigger();
   constexpr int LPR = HD / 16, RPL = 32 / LPR, U = KV8_READ_ROWS / RPL;
   const int lane = threadIdx.x & 31, sub = lane / LPR, e0 = lane % LPR * 16;
-  const long long unit = ((long long)blockIdx.x * KV8_THREADS + threadIdx.x) >> 5;
+  const unsigned unit = (blockIdx.x * KV8_THREADS + threadIdx.x) >> 5;
   if (unit >= units) return;
-  const int jh = (int)(unit % (2 * c.Hkv)), j = jh >= c.Hkv, head = jh - j * c.Hkv;
-  const int seq = (int)(unit / (2 * c.Hkv) / chunks), i0 = (int)(unit / (2 * c.Hkv) % chunks) * KV8_READ_ROWS;
+  const unsigned planes = 2 * c.Hkv, of = unit / planes, seq = of / chunks;
+  const int jh = unit - of * planes, j = jh >= c.Hkv, head = jh - j * c.Hkv, i0 = (of - seq * chunks) * KV8_READ_ROWS;
   Kv8Seq t;
   if (!kv8_seq(r, c.page, seq, path == nullptr, t) || i0 >= t.n) return;
   const long long cap = (long long)r.pps * c.page;
+  const Kv8Plane at(c, j, head);
+  const int* table = r.page_table + (size_t)seq * r.pps;
+  const uint8_t *codes = c.codes + at.row * HD + e0, *powers = c.powers + at.power;
   uint4 x[U];
   int power[U];
   bool have[U];
@@ -184,22 +189,23 @@ __global__ void __launch_bounds__(KV8_THREADS) kv8_read_kernel(Kv8Cache c, Kv8Ro
     have[u] = i < t.n;
     const int off = have[u] && path ? path[t.row0 + i] : i;
     bool ok = off >= 0 && (long long)t.L + off < cap;
+    const int pos = ok ? t.L + off : 0, entry = kv8_div(pos, c.page, c.page_inv), slot = pos - entry * c.page;
     int page = 0;
-    const int pos = t.L + off;
     if (have[u] && ok) {
-      page = __ldg(r.page_table + (size_t)seq * r.pps + pos / c.page);
-      ok = page >= 0 && page < c.n_pages;
+      page = __ldg(table + entry);
+      ok = (unsigned)page < (unsigned)c.n_pages;
     }
     if (have[u] && !ok) op_status(r.status, Q3TTS_ERR_ARG);
     have[u] = have[u] && ok;
     x[u] = make_uint4(0, 0, 0, 0);
     power[u] = 0;
     if (have[u]) {
-      const long long row = kv8_row(c, page, j, head, pos % c.page);
-      x[u] = ld_stream16(c.codes + row * HD + e0);
-      power[u] = __ldg(c.powers + row / c.block);
+      x[u] = ld_stream16(codes + ((long long)page * at.rows + slot) * HD);
+      power[u] = __ldg(powers + (long long)page * at.powers + kv8_div(slot, c.block, c.block_inv));
     }
   }
+  const int ld = j ? ldv : ldk;
+  T* dst = (j ? v : k) + (long long)(t.row0 + i0 + sub) * ld + head * HD + e0;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (!have[u]) continue;
@@ -211,13 +217,13 @@ __global__ void __launch_bounds__(KV8_THREADS) kv8_read_kernel(Kv8Cache c, Kv8Ro
     const float by = kv8_power(power[u]);
 #pragma unroll
     for (int e = 0; e < 16; ++e) f[e] *= by;
-    store16((j ? v : k) + (size_t)(t.row0 + i0 + u * RPL + sub) * (j ? ldv : ldk) + head * HD + e0, f, wide);
+    store16(dst + (long long)(u * RPL) * ld, f, wide);
   }
 }
 
 int grid_of(long long units, int threads, unsigned* grid) {
   const long long g = (units * 32 + threads - 1) / threads;
-  if (g > 0x7fffffffll) return Q3TTS_ERR_UNSUPPORTED;
+  if (units > 0x7ffffffll) return Q3TTS_ERR_UNSUPPORTED;  // (threads are numbered in 32 bits)
   *grid = (unsigned)g;
   return Q3TTS_OK;
 }
@@ -231,7 +237,7 @@ int launch_write(const Kv8Cache& c, const Kv8Rows& r, const void* k, int ldk, co
   if (rc != Q3TTS_OK) return rc;
   const int wide = (((uintptr_t)k | (uintptr_t)v) & (4 * sizeof(T) - 1)) == 0 && ldk % 4 == 0 && ldv % 4 == 0;
   return launch_pdl(kv8_write_kernel<T, HD, U>, dim3(grid), dim3(KV8_WRITE_THREADS), 0, s, c, r, static_cast<const T*>(k), ldk,
-                    static_cast<const T*>(v), ldv, blocks, units, wide) == cudaSuccess
+                    static_cast<const T*>(v), ldv, blocks, (unsigned)units, wide) == cudaSuccess
              ? Q3TTS_OK
              : Q3TTS_ERR_CUDA;
 }
@@ -252,7 +258,7 @@ int launch_read(const Kv8Cache& c, const Kv8Rows& r, const int* path, void* k, i
   const size_t al = 32 / sizeof(T);
   const int wide = (((uintptr_t)k | (uintptr_t)v) & 31) == 0 && ldk % al == 0 && ldv % al == 0;
   return launch_pdl(kv8_read_kernel<T, HD>, dim3(grid), dim3(KV8_THREADS), 0, s, c, r, path, static_cast<T*>(k), ldk,
-                    static_cast<T*>(v), ldv, chunks, units, wide) == cudaSuccess
+                    static_cast<T*>(v), ldv, chunks, (unsigned)units, wide) == cudaSuccess
              ? Q3TTS_OK
              : Q3TTS_ERR_CUDA;
 }

@@ -50,13 +50,6 @@ __device__ __forceinline__ bool kv8_wait(uint32_t bar, uint32_t parity, volatile
   }
 }
 
-// row / rep (inv = ceil(2^32 / rep)): the product is the quotient or, of many rows, one more.
-__device__ __forceinline__ int kv8_div(int row, int rep, unsigned inv) {
-  if (rep == 1) return row;
-  const int q = (int)__umulhi((unsigned)row, inv);
-  return q - (q * rep > row);
-}
-
 struct KfItem {
   Kv8Seq t;
   int seq, g, n0, rows;  // kv head, first row of the tile, rows
@@ -235,14 +228,14 @@ __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8Attn
     const int my = SPLIT ? kv : lane >> 4, b = lane & 15, boxes = TM_PT / box;
     auto page_of = [&](int i) -> int {
       const int pos = (m.t0 + i) * TM_PT + b * box;
-      return b < boxes && i < m.nt && pos < m.end ? __ldg(table + pos / ps) : 0;
+      return b < boxes && i < m.nt && pos < m.end ? __ldg(table + kv8_div(pos, ps, a.c.page_inv)) : 0;
     };
     int page0 = page_of(0), page1 = page_of(1);  // looked up two tiles ahead
     for (int i = 0; i < m.nt; ++i) {
       const int pos = (m.t0 + i) * TM_PT + b * box;
       const int held = min(TM_PT, m.end - (m.t0 + i) * TM_PT);
       const bool mine = b < boxes && pos < m.end && !(SPLIT && lane > 15);
-      const int row = mine ? (int)kv8_row(a.c, checked(page0), my, m.g, pos % ps) : 0;
+      const int row = mine ? (int)kv8_row(a.c, checked(page0), my, m.g, pos - kv8_div(pos, ps, a.c.page_inv) * ps) : 0;
       for (int h = first; h <= last; ++h) {
         const int it = 2 * i + h, slot = it % S;
         ok = ok && kv8_wait(su32(&empty[slot]), ((uint32_t)(it / S) & 1u) ^ 1u, abort_w, status);
@@ -268,7 +261,7 @@ __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8Attn
 #pragma unroll
       for (int j = 0; j < TM_PT / 32; ++j) {
         const int pos = (m.t0 + i) * TM_PT + lane + 32 * j;
-        page[j] = i < m.nt && pos < m.end ? __ldg(table + pos / ps) : 0;
+        page[j] = i < m.nt && pos < m.end ? __ldg(table + kv8_div(pos, ps, a.c.page_inv)) : 0;
       }
     };
     look_up(0);
@@ -278,7 +271,7 @@ __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8Attn
 #pragma unroll
       for (int j = 0; j < TM_PT / 32; ++j) {
         const int pos = (m.t0 + i) * TM_PT + lane + 32 * j;
-        row[j] = pos < m.end ? (int)kv8_row(a.c, checked(page[j]), 0, m.g, pos % ps) : -1;
+        row[j] = pos < m.end ? (int)kv8_row(a.c, checked(page[j]), 0, m.g, pos - kv8_div(pos, ps, a.c.page_inv) * ps) : -1;
       }
       look_up(i + 1);
       for (int h = first; h <= last; ++h) {
@@ -365,7 +358,7 @@ int launch_tiles(Kernel kernel, TmKernel& known, int threads, size_t smem, bool 
   const int c = cluster_size(items, tiles, known);
   d.vec = (((uintptr_t)a.q & (vec_bytes - 1)) == 0 && a.ldq % 4 == 0 ? 1 : 0) |
           (((uintptr_t)a.out & (vec_bytes - 1)) == 0 && a.ldo % 4 == 0 ? 2 : 0);
-  d.rep_inv = (unsigned)(((1ull << 32) + rep - 1) / rep);
+  d.rep_inv = kv8_inverse(rep);
   d.sorted = items * c > known.clusters[1] && a.r.n_seqs > 1 && a.r.n_seqs <= KF_SORT;
   d.per_page = a.c.page / a.c.block;
   d.to_values = a.c.Hkv * d.per_page;
