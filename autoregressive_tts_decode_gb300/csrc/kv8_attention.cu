@@ -20,6 +20,18 @@
 // largest c s_p + b_p so far.  It is followed only when a weight passes 2^3: weights up to 2^4
 // have a step of 2^-28, and a tile needs one vote of the softmax threads instead of
 // a maximum over them.  The sum of 2^(c s_p - base) is held beside it in fp32.
+//
+// A CTA has one item: a sequence, a kv head, up to R = 2, 4, 8 or 16 rows, and with few items in a call
+// a share of the positions, joined in a cluster.  One warp loads, one thread issues the MMAs, four warps
+// are the softmax (a thread a position of the tile, and an element of the output).  Scores, weights and
+// outputs of a tile follow one another; what overlaps are the CTAs of an SM, four for two rows, whose
+// rings of three tiles keep 192 KB on their way.  Sequences are taken longest first, so that the
+// last ones to start are short.
+//
+// The bound is the cache's bytes: 128 sequences of 256 .. 2048 positions, one token of 16 heads over 8: 54 us,
+// 5.6 TB/s (loading alone 50; three CTAs with rings of four 59.6).  Short calls are latency, the chain from
+// lengths to pages to codes and a tile's way: 131 positions 6 us, 16 sequences of 32 .. 512 9 us.  More rows cost
+// their digits: 128 x 1152 positions, 2, 4, 8 new rows of two heads: 68, 85, 132 us.
 #include "kv8_tiles.cuh"
 
 namespace q3 {
@@ -27,7 +39,7 @@ namespace q3 {
 namespace {
 
 constexpr int KF_DIGITS = 8;
-constexpr float KF_SLACK = 8.f;          // how large a weight may be
+constexpr float KF_SLACK = 8.f;         // how large a weight may be
 constexpr float KF_STEP = 268435456.f;  // 2^28: its fixed-point step
 
 template <int HD, int R>

@@ -9,7 +9,11 @@
 // fills its power only rises; codes that are there already are then rounded again,
 // which loses nothing but what falls under the format's smallest step.
 //
-// Both are bound by the bytes they move: rows in one form, codes in the other.
+// Both are bound by the bytes they move, rows in one form and codes in the other: 125,000 rows of
+// eight kv heads read back to bf16 (771 MB): 122 us, 6.3 TB/s, 93 % of a plain copy (141 us with 64-bit
+// divisions in the addresses: three quarters of the issue slots were taken); eight fp32 prompts of 2 ..
+// 1982 rows written (81 MB): 17.9 us, 4.5 TB/s, waves of warps that each wait for their rows.  Calls for
+// single tokens are a launch and three dependent loads, 2.5 to 3 us.
 #include "kv8.cuh"
 
 namespace q3 {
@@ -53,10 +57,12 @@ __device__ __forceinline__ float scaled(float x, float by) {
 
 // A warp per block, kv head and k or v; a lane has four elements of a row, a load
 // RPL rows.  Up to U loads of rows stay in registers between the maximum and the
-// rounding (blocks of more rows are read twice, the second time from the caches).
+// rounding (blocks of more rows are read twice, the second time from the caches).  Five CTAs of 128
+// threads to an SM for fp32 rows, eight for bf16, which stay as they lie (two of 256 threads, all rows as
+// fp32: 20.8 us for the prompts above).
 template <class T, int HD, int U>
-__global__ void __launch_bounds__(KV8_WRITE_THREADS, U == 1 ? 8 : sizeof(T) == 4 ? 5 : 8) kv8_write_kernel(Kv8Cache c, Kv8Rows r, const T* k, int ldk, const T* v,
-                                                                int ldv, int blocks, unsigned units, int wide) {
+__global__ void __launch_bounds__(KV8_WRITE_THREADS, U == 1 || sizeof(T) == 2 ? 8 : 5)
+    kv8_write_kernel(Kv8Cache c, Kv8Rows r, const T* k, int ldk, const T* v, int ldv, int blocks, unsigned units, int wide) {
   pdl_wait();
   pdl_trigger();
   constexpr int RPL = 128 / HD;

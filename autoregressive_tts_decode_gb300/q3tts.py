@@ -218,17 +218,25 @@ def _cuda(t, name: str, dtype, dev: int, numel: int, what: str) -> int:
     return t.data_ptr()
 
 
+@functools.lru_cache(maxsize=None)
+def _cuda_state():
+    """torch's functions for the current device and a device's current stream (an import
+    statement in each call takes longer)."""
+    from torch import _C
+    return _C._cuda_getDevice, _C._cuda_getCurrentRawStream
+
+
 def _call(dev: int, fn, what: str, *args):
     """fn(*args, the current stream of device dev) with that device current."""
-    from torch import _C
+    device, stream = _cuda_state()
     if dev < 0:
         _bad(what, "every tensor", "on a CUDA device")
-    if dev == _C._cuda_getDevice():
-        rc = fn(*args, _C._cuda_getCurrentRawStream(dev))
+    if dev == device():
+        rc = fn(*args, stream(dev))
     else:
         import torch
         with torch.cuda.device(dev):
-            rc = fn(*args, _C._cuda_getCurrentRawStream(dev))
+            rc = fn(*args, stream(dev))
     if rc != OK:
         raise Q3TTSError(rc, what)
 
@@ -454,21 +462,17 @@ def _kv8_types():
 def _kv8(pool, scales, layer, page_table, lengths, start, what: str):
     """(device, kv heads, head dim, the arguments that the calls begin with)."""
     codes, powers, _, i32, _ = _kv8_types()
-    dev, shape, blocks = pool.get_device(), pool.shape, scales.shape
+    dev, shape, blocks, table = pool.get_device(), pool.shape, scales.shape, page_table.shape
     if dev < 0 or pool.dtype != codes or len(shape) != 6 or shape[2] != 2 or not pool.is_contiguous():
         _bad(what, "pool", "a contiguous CUDA float8_e4m3fn tensor [layers, pages, 2, kv heads, page size, head dim]")
     layers, pages, _, heads, page, hd = shape
-    if len(blocks) != 5 or blocks[4] < 1 or page % blocks[4]:
-        _bad(what, "scales", "[layers, pages, 2, kv heads, page size / block]")
-    n, pps, per_page = 0, 0, blocks[4]
-    if page_table.dim() == 2:
-        n, pps = page_table.shape
-    if (blocks[0] != layers or blocks[1] != pages or blocks[2] != 2 or blocks[3] != heads or scales.dtype not in powers
+    per_page = blocks[-1] if len(blocks) == 5 else 0
+    if (per_page < 1 or page % per_page or blocks != (layers, pages, 2, heads, per_page) or scales.dtype not in powers
             or scales.get_device() != dev or not scales.is_contiguous()):
-        _bad(what, "scales", f"contiguous float8_e8m0fnu or uint8 [{layers}, {pages}, 2, {heads}, page size / block] on cuda:{dev}")
-    if (page_table.dim() != 2 or page_table.dtype != i32 or page_table.get_device() != dev
-            or not page_table.is_contiguous()):
+        _bad(what, "scales", f"contiguous float8_e8m0fnu or uint8 [{layers}, {pages}, 2, {heads}, {page} / block] on cuda:{dev}")
+    if len(table) != 2 or page_table.dtype != i32 or page_table.get_device() != dev or not page_table.is_contiguous():
         _bad(what, "page_table", f"contiguous int32 [seqs, pages per seq] on cuda:{dev}")
+    n, pps = table
     return dev, heads, hd, (_CACHE8.pack(pool.data_ptr(), scales.data_ptr(), layers, pages, heads, page, hd, page // per_page),
                             layer, page_table.data_ptr(), pps, n, _cuda(lengths, "lengths", i32, dev, n, what),
                             _cuda(start, "start", i32, dev, n + 1, what))

@@ -74,14 +74,16 @@ int q3tts_kv8_read(const q3tts_kv8_cache* kv, int layer, const int32_t* page_tab
  * [n_rows], 8-byte aligned; a drafted tree, max_rows up to
  * Q3TTS_MAX_TREE_NODES).  One that sees nothing gets zeroes.  What a row does not
  * see does not touch it, NaN among it; a row that sees a NaN is unspecified, like
- * one with scores above 2^27, or values above 2^60 in size.  Blocks whose power is
- * below 2^-60 count as zeroes in the values.  Rows outside every sequence's range
+ * one with scores above 2^27, or values above 2^60 in size.  Values in blocks whose
+ * power is below 2^-60 may count as zeroes.  Rows outside every sequence's range
  * are left as they were; page ids outside the pool leave the sequence's rows
  * unspecified.  No row of out may share a byte with one of q (Q3TTS_ERR_ARG).
  * Caches of up to 2^31 rows of head_dim elements in all (else
- * Q3TTS_ERR_UNSUPPORTED).  Scores, weights and sums are held in 32 bits and rounded
- * once to row_dtype; a row's result does not depend on the run, but may on n_seqs,
- * max_rows and pages_per_seq, which decide how positions are split. */
+ * Q3TTS_ERR_UNSUPPORTED).  Scores, softmax statistics and sums are held in 32 bits;
+ * a weight meets the values with 22 bits or more (11 where row_dtype is bf16), and
+ * the result is rounded once to row_dtype.  It does not depend on the run, but may
+ * on n_seqs, max_rows and pages_per_seq, which decide how positions are split.
+ * q3tts_debug_lose_tile arms this call too. */
 int q3tts_kv8_attention(const q3tts_kv8_cache* kv, int layer, const int32_t* page_table_dev, int pages_per_seq,
                         int n_seqs, const int32_t* lengths_dev, const int32_t* row_start_dev,
                         const uint64_t* masks_dev, const void* q_dev, int ldq, void* out_dev, int ldo, int n_q_heads,

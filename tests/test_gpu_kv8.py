@@ -224,6 +224,58 @@ def test_read_leaves_out_what_does_not_fit(q3):
         assert torch.equal(o[:3], g[:3]) and bool((o[3:] == 9.0).all())
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_rows_that_are_not_aligned(q3, dtype):
+    """Rows at odd addresses with odd pitches, read and written: as aligned ones."""
+    import torch
+    rng, t = np.random.default_rng(24), dt(dtype)
+    lens, rows, kvh, hd = [3, 20, 0], [40, 1, 18], 3, 64
+    codes, powers, table = ku.cache(rng, [a + b for a, b in zip(lens, rows)], 16, 8, 1, kvh, hd)
+    n, start = sum(rows), ku.ints(ku.starts(rows))
+    pitch = 2 * kvh * hd + 1
+    kv = torch.empty(n * pitch + 3, dtype=t, device="cuda")[3:].view(n, pitch)
+    k, v = (kv[:, i * kvh * hd:(i + 1) * kvh * hd].unflatten(1, (kvh, hd)) for i in (0, 1))
+    k.copy_(randn(rng, (n, kvh, hd), t))
+    v.copy_(randn(rng, (n, kvh, hd), t))
+    got = []
+    for a, b in ((k, v), (k.contiguous(), v.contiguous())):
+        pool, scales, tab = ku.to_gpu(codes, powers, table)
+        q3.kv8_write(pool, scales, 0, tab, ku.ints(lens), start, a, b)
+        got.append((pool.view(torch.uint8), scales.view(torch.uint8)))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    kv.fill_(-7.5)
+    want = q3.kv8_read(pool, scales, 0, tab, ku.ints(lens), start, out=(torch.empty((n, kvh, hd), dtype=t, device="cuda"),
+                                                                        torch.empty((n, kvh, hd), dtype=t, device="cuda")))
+    q3.kv8_read(pool, scales, 0, tab, ku.ints(lens), start, out=(k, v))
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1]) and bool((kv[:, -1] == -7.5).all())
+
+
+def test_offsets_past_32_bits(q3):
+    """A cache of 9 GB whose used pages are its last ones: as one that has no others."""
+    import torch
+    rng = np.random.default_rng(25)
+    lens, rows, kvh, hd, page = [200, 0], [90, 1], 8, 128, 16
+    codes, powers, table = ku.cache(rng, [a + b for a, b in zip(lens, rows)], page, 16, 1, kvh, hd)
+    small, sp, tab = ku.to_gpu(codes, powers, table)
+    pages = codes.shape[1]
+    before = 9 * (1 << 30) // (2 * kvh * page * hd) - pages
+    big = torch.empty((1, before + pages, 2, kvh, page, hd), dtype=torch.uint8, device="cuda")
+    bp = torch.empty((1, before + pages, 2, kvh, 1), dtype=torch.uint8, device="cuda")
+    big[:, before:] = small.view(torch.uint8)
+    bp[:, before:] = sp.view(torch.uint8)
+    moved = torch.where(tab < pages, tab + before, tab)
+    start, ln = ku.ints(ku.starts(rows)), ku.ints(lens)
+    k, v, q = (randn(rng, (91, h, hd), torch.bfloat16) for h in (kvh, kvh, 16))
+    results = []
+    for pool, scales, t in ((small, sp, tab), (big.view(torch.float8_e4m3fn), bp.view(torch.float8_e8m0fnu), moved)):
+        q3.kv8_write(pool, scales, 0, t, ln, start, k, v, max_rows=90)
+        few = q3.kv8_attention(pool, scales, 0, t, ku.ints([289, 0]), ku.ints([0, 1, 2]), q[:2].contiguous(), max_rows=1)
+        results.append((q3.kv8_attention(pool, scales, 0, t, ln, start, q, max_rows=90), few,
+                        *q3.kv8_read(pool, scales, 0, t, ln, start, path=ku.ints([*range(90), 0]), max_rows=90)))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    assert torch.equal(big[:, before:], small.view(torch.uint8)) and torch.equal(bp[:, before:], sp.view(torch.uint8))
+
+
 def test_a_power_of_255_reads_as_nan(q3):
     import torch
     codes, powers, table = ku.cache(np.random.default_rng(7), [4], 16, 16, 1, 1, 64)
@@ -310,6 +362,21 @@ def test_attention_of_many_sequences(q3, dtype, tree, seqs, longest, most, heads
     out = run_attention(q3, c, status=status)
     check_attention(c, out)
     assert int(status) == 0 and torch.equal(out, run_attention(q3, c))
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("case", [([61, 0], [90, 33], 4, 2, 64, 1, 1), ([300], [70], 4, 2, 128, 3, 1), ([131], [100], 6, 2, 128, 5, 5),
+                                  ([450, 7], [80, 1], 4, 2, 128, 200, 8), ([450, 130], [1, 1], 4, 2, 64, 200, 40), ([700], [120], 2, 1, 64, 384, 96),
+                                  ([255, 256, 257], [65, 64, 63], 2, 1, 128, 128, 2)])
+def test_attention_over_pages_of_all_sizes(q3, case, dtype):
+    """Pages of one position, of odd numbers, larger than a tile and no multiple of it; the most
+    rows of a sequence left to the default."""
+    import torch
+    c = attend_case(np.random.default_rng(23), *case, dtype=dtype, tree=False)
+    pool, scales, tab = ku.to_gpu(c["codes"], c["powers"], c["table"])
+    out = q3.kv8_attention(pool, scales, 1, tab, ku.ints(c["lens"]), ku.ints(ku.starts(c["rows"])), c["q"])
+    check_attention(c, out)
+    assert torch.equal(out, run_attention(q3, c)) or max(c["rows"]) != sum(c["rows"])
 
 
 SHAPES = [(1, 4, 2, 300), (13, 4, 2, 300), (64, 4, 2, 500), (40, 16, 1, 77), (1, 2, 1, 3000), (5, 8, 1, 129)]
