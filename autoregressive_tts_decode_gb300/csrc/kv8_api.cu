@@ -5,10 +5,10 @@
 
 namespace {
 
-int check_cache(const q3tts_kv8_cache* kv, int layer) {
-  if (!kv || !kv->codes || !kv->powers || !aligned(kv->codes, 16)) return Q3TTS_ERR_ARG;
+int check_cache(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows) {
+  if (!kv || !rows || !kv->codes || !kv->powers || !aligned(kv->codes, 16)) return Q3TTS_ERR_ARG;
   if (kv->layers < 1 || kv->n_pages < 1 || kv->n_kv_heads < 1 || kv->page_size < 1) return Q3TTS_ERR_ARG;
-  if (kv->block < 1 || kv->page_size % kv->block || layer < 0 || layer >= kv->layers) return Q3TTS_ERR_ARG;
+  if (kv->block < 1 || kv->page_size % kv->block || rows->layer < 0 || rows->layer >= kv->layers) return Q3TTS_ERR_ARG;
   if (kv->head_dim != 64 && kv->head_dim != 128) return Q3TTS_ERR_UNSUPPORTED;
   return Q3TTS_OK;
 }
@@ -32,24 +32,23 @@ bool dtype_ok(int d) { return d == Q3TTS_F32 || d == Q3TTS_BF16; }
 size_t esz(int d) { return d == Q3TTS_F32 ? 4 : 2; }
 
 // What the calls have in common; *work: whether there is any.
-int check_rows(const q3tts_kv8_cache& c, const int32_t* table, int pps, int n_seqs, const int32_t* lengths,
-               const int32_t* start, int n_rows, int max_rows, int dtype, int32_t* status, q3::Kv8Rows* r, bool* work) {
+int check_rows(const q3tts_kv8_cache& c, const q3tts_kv8_rows& q, q3::Kv8Rows* r, bool* work) {
   *work = false;
-  if (n_seqs < 0 || n_rows < 0 || max_rows < 1 || !dtype_ok(dtype)) return Q3TTS_ERR_ARG;
-  if (n_seqs == 0 || n_rows == 0) return Q3TTS_OK;
-  if (!table || !lengths || !start || !aligned(table, 4) || !aligned(lengths, 4) || !aligned(start, 4) ||
-      !aligned(status, 4))
+  if (q.n_seqs < 0 || q.n_rows < 0 || q.max_rows < 1 || !dtype_ok(q.row_dtype)) return Q3TTS_ERR_ARG;
+  if (q.n_seqs == 0 || q.n_rows == 0) return Q3TTS_OK;
+  if (!q.page_table || !q.lengths || !q.row_start || !aligned(q.page_table, 4) || !aligned(q.lengths, 4) ||
+      !aligned(q.row_start, 4) || !aligned(q.status, 4))
     return Q3TTS_ERR_ARG;
   // positions of a sequence are 32-bit with room to spare
-  if (pps < 1 || (long long)pps * c.page_size > 1 << 30) return Q3TTS_ERR_ARG;
-  r->page_table = table;
-  r->lengths = lengths;
-  r->start = start;
-  r->pps = pps;
-  r->n_seqs = n_seqs;
-  r->n_rows = n_rows;
-  r->max_rows = max_rows < n_rows ? max_rows : n_rows;
-  r->status = status;
+  if (q.pages_per_seq < 1 || (long long)q.pages_per_seq * c.page_size > 1 << 30) return Q3TTS_ERR_ARG;
+  r->page_table = q.page_table;
+  r->lengths = q.lengths;
+  r->start = q.row_start;
+  r->pps = q.pages_per_seq;
+  r->n_seqs = q.n_seqs;
+  r->n_rows = q.n_rows;
+  r->max_rows = q.max_rows < q.n_rows ? q.max_rows : q.n_rows;
+  r->status = q.status;
   *work = true;
   return Q3TTS_OK;
 }
@@ -66,67 +65,55 @@ Span span(const void* p, int ld, int heads, int hd, int dtype, int n) {
 
 extern "C" {
 
-int q3tts_kv8_write(const q3tts_kv8_cache* kv, int layer, const int32_t* page_table_dev, int pages_per_seq,
-                    int n_seqs, const int32_t* lengths_dev, const int32_t* row_start_dev, const void* k_dev, int ldk,
-                    const void* v_dev, int ldv, int row_dtype, int n_rows, int max_rows, int32_t* status_dev,
-                    void* cuda_stream) {
-  int rc = check_cache(kv, layer);
+int q3tts_kv8_write(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const void* k_dev, int ldk,
+                    const void* v_dev, int ldv, void* cuda_stream) {
+  int rc = check_cache(kv, rows);
   if (rc != Q3TTS_OK) return rc;
   q3::Kv8Rows r;
   bool work;
-  rc = check_rows(*kv, page_table_dev, pages_per_seq, n_seqs, lengths_dev, row_start_dev, n_rows, max_rows, row_dtype,
-                  status_dev, &r, &work);
+  rc = check_rows(*kv, *rows, &r, &work);
   if (rc != Q3TTS_OK || !work) return rc;
-  if (!rows_ok(k_dev, ldk, kv->n_kv_heads, kv->head_dim, row_dtype) ||
-      !rows_ok(v_dev, ldv, kv->n_kv_heads, kv->head_dim, row_dtype))
+  const int dtype = rows->row_dtype;
+  if (!rows_ok(k_dev, ldk, kv->n_kv_heads, kv->head_dim, dtype) || !rows_ok(v_dev, ldv, kv->n_kv_heads, kv->head_dim, dtype))
     return Q3TTS_ERR_ARG;
-  return q3::launch_kv8_write(desc(*kv, layer), r, row_dtype, k_dev, ldk, v_dev, ldv, (cudaStream_t)cuda_stream);
+  return q3::launch_kv8_write(desc(*kv, rows->layer), r, dtype, k_dev, ldk, v_dev, ldv, (cudaStream_t)cuda_stream);
 }
 
-int q3tts_kv8_read(const q3tts_kv8_cache* kv, int layer, const int32_t* page_table_dev, int pages_per_seq, int n_seqs,
-                   const int32_t* lengths_dev, const int32_t* row_start_dev, const int32_t* path_dev, void* k_out_dev,
-                   int ldk, void* v_out_dev, int ldv, int row_dtype, int n_rows, int max_rows, int32_t* status_dev,
-                   void* cuda_stream) {
-  int rc = check_cache(kv, layer);
+int q3tts_kv8_read(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const int32_t* path_dev, void* k_out_dev,
+                   int ldk, void* v_out_dev, int ldv, void* cuda_stream) {
+  int rc = check_cache(kv, rows);
   if (rc != Q3TTS_OK) return rc;
   q3::Kv8Rows r;
   bool work;
-  rc = check_rows(*kv, page_table_dev, pages_per_seq, n_seqs, lengths_dev, row_start_dev, n_rows, max_rows, row_dtype,
-                  status_dev, &r, &work);
+  rc = check_rows(*kv, *rows, &r, &work);
   if (rc != Q3TTS_OK || !work) return rc;
-  const int heads = kv->n_kv_heads, hd = kv->head_dim;
-  if (!rows_ok(k_out_dev, ldk, heads, hd, row_dtype) || !rows_ok(v_out_dev, ldv, heads, hd, row_dtype) ||
-      !aligned(path_dev, 4))
+  const int heads = kv->n_kv_heads, hd = kv->head_dim, dtype = rows->row_dtype;
+  if (!rows_ok(k_out_dev, ldk, heads, hd, dtype) || !rows_ok(v_out_dev, ldv, heads, hd, dtype) || !aligned(path_dev, 4))
     return Q3TTS_ERR_ARG;
-  if (rows_overlap(span(k_out_dev, ldk, heads, hd, row_dtype, n_rows), span(v_out_dev, ldv, heads, hd, row_dtype, n_rows)))
+  if (rows_overlap(span(k_out_dev, ldk, heads, hd, dtype, r.n_rows), span(v_out_dev, ldv, heads, hd, dtype, r.n_rows)))
     return Q3TTS_ERR_ARG;
-  return q3::launch_kv8_read(desc(*kv, layer), r, path_dev, row_dtype, k_out_dev, ldk, v_out_dev, ldv,
+  return q3::launch_kv8_read(desc(*kv, rows->layer), r, path_dev, dtype, k_out_dev, ldk, v_out_dev, ldv,
                              (cudaStream_t)cuda_stream);
 }
 
-int q3tts_kv8_attention(const q3tts_kv8_cache* kv, int layer, const int32_t* page_table_dev, int pages_per_seq,
-                        int n_seqs, const int32_t* lengths_dev, const int32_t* row_start_dev,
-                        const uint64_t* masks_dev, const void* q_dev, int ldq, void* out_dev, int ldo, int n_q_heads,
-                        int row_dtype, int n_rows, int max_rows, int32_t* status_dev, void* cuda_stream) {
-  int rc = check_cache(kv, layer);
+int q3tts_kv8_attention(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const uint64_t* masks_dev,
+                        const void* q_dev, int ldq, void* out_dev, int ldo, int n_q_heads, void* cuda_stream) {
+  int rc = check_cache(kv, rows);
   if (rc != Q3TTS_OK) return rc;
-  if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads || (masks_dev && max_rows > Q3TTS_MAX_TREE_NODES)) return Q3TTS_ERR_ARG;
+  if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads || (masks_dev && rows->max_rows > Q3TTS_MAX_TREE_NODES)) return Q3TTS_ERR_ARG;
   q3::Kv8AttnArgs a;
   bool work;
-  rc = check_rows(*kv, page_table_dev, pages_per_seq, n_seqs, lengths_dev, row_start_dev, n_rows, max_rows, row_dtype,
-                  status_dev, &a.r, &work);
+  rc = check_rows(*kv, *rows, &a.r, &work);
   if (rc != Q3TTS_OK || !work) return rc;
-  const int hd = kv->head_dim;
-  if (!rows_ok(q_dev, ldq, n_q_heads, hd, row_dtype) || !rows_ok(out_dev, ldo, n_q_heads, hd, row_dtype) ||
-      !aligned(masks_dev, 8))
+  const int hd = kv->head_dim, dtype = rows->row_dtype, n = a.r.n_rows;
+  if (!rows_ok(q_dev, ldq, n_q_heads, hd, dtype) || !rows_ok(out_dev, ldo, n_q_heads, hd, dtype) || !aligned(masks_dev, 8))
     return Q3TTS_ERR_ARG;
   if (n_q_heads / kv->n_kv_heads > 1024 ||
       2ll * kv->layers * kv->n_pages > 0x7fffffffll / kv->n_kv_heads / kv->page_size)
     return Q3TTS_ERR_UNSUPPORTED;
   // rows of one sequence are written while another's queries are still read
-  if (rows_overlap(span(q_dev, ldq, n_q_heads, hd, row_dtype, n_rows), span(out_dev, ldo, n_q_heads, hd, row_dtype, n_rows)))
-    return Q3TTS_ERR_ARG;
-  a.c = desc(*kv, layer);
+  if (rows_overlap(span(q_dev, ldq, n_q_heads, hd, dtype, n), span(out_dev, ldo, n_q_heads, hd, dtype, n))) return Q3TTS_ERR_ARG;
+  a.c = desc(*kv, rows->layer);
   a.masks = reinterpret_cast<const unsigned long long*>(masks_dev);
   a.q = q_dev;
   a.out = out_dev;
@@ -138,7 +125,7 @@ int q3tts_kv8_attention(const q3tts_kv8_cache* kv, int layer, const int32_t* pag
     a.lost_tile = l.tile;
     a.wait_1024 = l.wait_1024();
   }
-  return q3::launch_kv8_attention(a, kv->layers, row_dtype, (cudaStream_t)cuda_stream);
+  return q3::launch_kv8_attention(a, kv->layers, dtype, (cudaStream_t)cuda_stream);
 }
 
 }  // extern "C"

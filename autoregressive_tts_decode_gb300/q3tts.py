@@ -57,6 +57,11 @@ class KV8Cache(C.Structure):
         "layers", "n_pages", "n_kv_heads", "page_size", "head_dim", "block")]
 
 
+class KV8Rows(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("page_table", "lengths", "row_start", "status")] + [(n, C.c_int) for n in (
+        "layer", "pages_per_seq", "n_seqs", "row_dtype", "n_rows", "max_rows")]
+
+
 class Rows(C.Structure):
     _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("row_bytes", C.c_size_t),
                 ("src_stride", C.c_size_t), ("dst_stride", C.c_size_t)]
@@ -141,12 +146,10 @@ def load(path: str = LIB_PATH):
     L.q3tts_beam_workspace_size.argtypes = [C.c_int] * 4
     L.q3tts_beam_workspace_size.restype = C.c_size_t
     L.q3tts_reorder_rows.argtypes = [vp, C.c_int, vp, vp, C.c_int, C.c_int, C.c_int, vp, vp]
-    kv8 = [vp, C.c_int, vp, C.c_int, C.c_int, vp, vp]  # cache, layer, table, its width, sequences, lengths, row starts
     rows = [vp, C.c_int, vp, C.c_int]  # two row buffers with their pitches
-    tail = [C.c_int] * 3 + [vp, vp]  # row type, rows, most of a sequence; status, stream
-    L.q3tts_kv8_write.argtypes = kv8 + rows + tail
-    L.q3tts_kv8_read.argtypes = kv8 + [vp] + rows + tail
-    L.q3tts_kv8_attention.argtypes = kv8 + [vp] + rows + [C.c_int] + tail
+    L.q3tts_kv8_write.argtypes = [vp, vp] + rows + [vp]
+    L.q3tts_kv8_read.argtypes = [vp, vp, vp] + rows + [vp]
+    L.q3tts_kv8_attention.argtypes = [vp, vp, vp] + rows + [C.c_int, vp]
     L.q3tts_strerror.restype = C.c_char_p
     L.q3tts_strerror.argtypes = [C.c_int]
     _lib = L
@@ -449,6 +452,7 @@ def reorder_rows(src, dst, parents, status=None):
 # told apart only when something is.
 
 _CACHE8 = struct.Struct("2P6i")  # q3tts_kv8_cache
+_ROWS8 = struct.Struct("4P6i")  # q3tts_kv8_rows
 
 
 @functools.lru_cache(maxsize=None)
@@ -460,7 +464,7 @@ def _kv8_types():
 
 
 def _kv8(pool, scales, layer, page_table, lengths, start, what: str):
-    """(device, kv heads, head dim, the arguments that the calls begin with)."""
+    """(device, kv heads, head dim, packed q3tts_kv8_cache, the first of a q3tts_kv8_rows up to its status, the next three)."""
     codes, powers, _, i32, _ = _kv8_types()
     dev, shape, blocks, table = pool.get_device(), pool.shape, scales.shape, page_table.shape
     if dev < 0 or pool.dtype != codes or len(shape) != 6 or shape[2] != 2 or not pool.is_contiguous():
@@ -473,9 +477,17 @@ def _kv8(pool, scales, layer, page_table, lengths, start, what: str):
     if len(table) != 2 or page_table.dtype != i32 or page_table.get_device() != dev or not page_table.is_contiguous():
         _bad(what, "page_table", f"contiguous int32 [seqs, pages per seq] on cuda:{dev}")
     n, pps = table
-    return dev, heads, hd, (_CACHE8.pack(pool.data_ptr(), scales.data_ptr(), layers, pages, heads, page, hd, page // per_page),
-                            layer, page_table.data_ptr(), pps, n, _cuda(lengths, "lengths", i32, dev, n, what),
-                            _cuda(start, "start", i32, dev, n + 1, what))
+    return (dev, heads, hd, _CACHE8.pack(pool.data_ptr(), scales.data_ptr(), layers, pages, heads, page, hd, page // per_page),
+            (page_table.data_ptr(), _cuda(lengths, "lengths", i32, dev, n, what), _cuda(start, "start", i32, dev, n + 1, what)),
+            (layer, pps, n))
+
+
+def _rows8(at, status, shape, dev: int, kind: int, n: int, most: int, what: str) -> bytes:
+    """A packed q3tts_kv8_rows."""
+    try:
+        return _ROWS8.pack(*at, 0 if status is None else _cuda(status, "status", _kv8_types()[3], dev, 1, what), *shape, kind, n, most)
+    except struct.error:
+        _bad(what, "layer and max_rows", "32-bit whole numbers")
 
 
 def _row_pair(a, b, names, heads, hd: int, dev: int, what: str):
@@ -500,10 +512,10 @@ def kv8_write(pool, scales, layer: int, page_table, lengths, start, k, v, max_ro
     pitch) go to the positions after them; max_rows: the most rows of a sequence
     (default: as many as there are rows).  Returns (pool, scales)."""
     what = "q3tts_kv8_write"
-    dev, heads, hd, head = _kv8(pool, scales, layer, page_table, lengths, start, what)
+    dev, heads, hd, cache, at, shape = _kv8(pool, scales, layer, page_table, lengths, start, what)
     n, _, kind, pair = _row_pair(k, v, ("k", "v"), heads, hd, dev, what)
-    _call(dev, (_lib or load()).q3tts_kv8_write, what, *head, *pair, kind, n, (n or 1) if max_rows is None else max_rows,
-          None if status is None else _cuda(status, "status", _kv8_types()[3], dev, 1, what))
+    rows = _rows8(at, status, shape, dev, kind, n, (n or 1) if max_rows is None else max_rows, what)
+    _call(dev, (_lib or load()).q3tts_kv8_write, what, cache, rows, *pair)
     return pool, scales
 
 
@@ -515,17 +527,16 @@ def kv8_read(pool, scales, layer: int, page_table, lengths, start, path=None, ma
     as bf16 with zeroes in rows that are not read otherwise.  The other arguments as for
     kv8_write.  Returns out."""
     what = "q3tts_kv8_read"
-    dev, heads, hd, head = _kv8(pool, scales, layer, page_table, lengths, start, what)
+    dev, heads, hd, cache, at, shape = _kv8(pool, scales, layer, page_table, lengths, start, what)
     if out is None:
         import torch
         if path is None:
             _bad(what, "out", "given, or a path")
         out = tuple(torch.zeros((path.numel(), heads, hd), dtype=torch.bfloat16, device=pool.device) for _ in range(2))
     n, _, kind, pair = _row_pair(out[0], out[1], ("out[0]", "out[1]"), heads, hd, dev, what)
-    i32 = _kv8_types()[3]
-    _call(dev, (_lib or load()).q3tts_kv8_read, what, *head, None if path is None else _cuda(path, "path", i32, dev, n, what),
-          *pair, kind, n, (n or 1) if max_rows is None else max_rows,
-          None if status is None else _cuda(status, "status", i32, dev, 1, what))
+    rows = _rows8(at, status, shape, dev, kind, n, (n or 1) if max_rows is None else max_rows, what)
+    _call(dev, (_lib or load()).q3tts_kv8_read, what, cache, rows,
+          None if path is None else _cuda(path, "path", _kv8_types()[3], dev, n, what), *pair)
     return out
 
 
@@ -540,17 +551,19 @@ def kv8_attention(pool, scales, layer: int, page_table, lengths, start, q, masks
     arguments as for kv8_write.  Returns out (as q; made if None, with zeroes in rows
     outside every sequence)."""
     what = "q3tts_kv8_attention"
-    dev, _, hd, head = _kv8(pool, scales, layer, page_table, lengths, start, what)
+    dev, _, hd, cache, at, shape = _kv8(pool, scales, layer, page_table, lengths, start, what)
     if out is None:
         import torch
         out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
     n, heads, kind, pair = _row_pair(q, out, ("q", "out"), None, hd, dev, what)
     if max_rows is None:
         max_rows = max(1, n if masks is None else min(n, MAX_TREE_NODES))
-    _, _, _, i32, wide = _kv8_types()
-    _call(dev, (_lib or load()).q3tts_kv8_attention, what, *head,
-          None if masks is None else _cuda(masks, "masks", wide[1] if masks.dtype == wide[1] else wide[0], dev, n, what),
-          *pair, heads, kind, n, max_rows, None if status is None else _cuda(status, "status", i32, dev, 1, what))
+    rows = _rows8(at, status, shape, dev, kind, n, max_rows, what)
+    m = None
+    if masks is not None:
+        wide = _kv8_types()[4]
+        m = _cuda(masks, "masks", wide[1] if masks.dtype == wide[1] else wide[0], dev, n, what)
+    _call(dev, (_lib or load()).q3tts_kv8_attention, what, cache, rows, m, *pair, heads)
     return out
 
 

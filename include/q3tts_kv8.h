@@ -4,7 +4,7 @@
  * Operators for programs that keep their own paged caches (as those of
  * q3tts_branch.h): keys and values are quantised as they are written, read back,
  * and attended over as they lie.  Conventions, status codes and dtypes are
- * q3tts.h's; status_dev is q3tts_branch.h's.
+ * q3tts.h's.
  */
 #ifndef Q3TTS_KV8_H
 #define Q3TTS_KV8_H
@@ -29,15 +29,25 @@ typedef struct q3tts_kv8_cache {
   int block;
 } q3tts_kv8_cache;
 
-/* In all three calls sequence s holds lengths_dev[s] positions (0 or more), and
- * its rows, row_start_dev[s] .. row_start_dev[s + 1] - 1 of a call's rows, stand
- * at the positions after them in order; max_rows (1 or more) bounds every
- * sequence's count and sizes the launch.  page_table_dev: int32
- * [n_seqs][pages_per_seq]; entries past a sequence's last position are not read.
- * Rows are n_rows of fp32 or bf16 elements (row_dtype: Q3TTS_F32 or Q3TTS_BF16),
- * their pitch (ldk, ldv, ldq, ldo) counted in elements.  A sequence whose length
- * or rows do not fit its table, the rows or max_rows is left out, and page ids
- * outside the pool are not followed (both reported in status_dev). */
+/* The sequences and rows of a call, in one layer: sequence s holds lengths[s]
+ * positions (0 or more), and its rows, row_start[s] .. row_start[s + 1] - 1 of the
+ * call's rows, stand at the positions after them in order; max_rows (1 or more)
+ * bounds every sequence's count and sizes the launch.  page_table (int32
+ * [n_seqs][pages_per_seq]), lengths, row_start and status (may be NULL;
+ * q3tts_branch.h's status_dev) are device memory; the table's entries past a
+ * sequence's last position are not read.  Rows are n_rows of fp32 or bf16 elements
+ * (row_dtype: Q3TTS_F32 or Q3TTS_BF16), their pitch (ldk, ldv, ldq, ldo) counted in
+ * elements.  A sequence whose length or rows do not fit its table, the rows or
+ * max_rows is left out, and page ids outside the pool are not followed (both
+ * reported in status). */
+typedef struct q3tts_kv8_rows {
+  const int32_t* page_table;
+  const int32_t* lengths;
+  const int32_t* row_start;
+  int32_t* status;
+  int layer, pages_per_seq, n_seqs;
+  int row_dtype, n_rows, max_rows;
+} q3tts_kv8_rows;
 
 /* Quantises the keys and values of new rows (n_rows of n_kv_heads x head_dim
  * elements) and writes them to one layer.  A block's power is the smallest of 2^-127
@@ -47,23 +57,19 @@ typedef struct q3tts_kv8_cache {
  * the sequence holds already the power does not fall: where it rises, those rows'
  * codes are rounded again to the new one.  Rows of a block behind the last one
  * written are left as they were.  A block on a page outside the pool is left out. */
-int q3tts_kv8_write(const q3tts_kv8_cache* kv, int layer, const int32_t* page_table_dev, int pages_per_seq,
-                    int n_seqs, const int32_t* lengths_dev, const int32_t* row_start_dev, const void* k_dev, int ldk,
-                    const void* v_dev, int ldv, int row_dtype, int n_rows, int max_rows, int32_t* status_dev,
-                    void* cuda_stream);
+int q3tts_kv8_write(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const void* k_dev, int ldk,
+                    const void* v_dev, int ldv, void* cuda_stream);
 
 /* Reads keys and values back into rows, each element rounded once to row_dtype.  Row
- * i of sequence s is position lengths_dev[s] + i, or lengths_dev[s] + path_dev[row]
+ * i of sequence s is position lengths[s] + i, or lengths[s] + path_dev[row]
  * where path_dev (int32 [n_rows]; not negative, any order) is given; an entry
  * outside the sequence's table or on a page outside the pool leaves its row as it
- * was (reported in status_dev), like rows outside every sequence.  With a path,
+ * was (reported in status), like rows outside every sequence.  With a path,
  * reading the accepted nodes of a drafted tree and writing them as new rows at
- * lengths_dev moves them to the places after the last position held.  No row of
+ * lengths moves them to the places after the last position held.  No row of
  * k_out may share a byte with one of v_out (Q3TTS_ERR_ARG). */
-int q3tts_kv8_read(const q3tts_kv8_cache* kv, int layer, const int32_t* page_table_dev, int pages_per_seq, int n_seqs,
-                   const int32_t* lengths_dev, const int32_t* row_start_dev, const int32_t* path_dev, void* k_out_dev,
-                   int ldk, void* v_out_dev, int ldv, int row_dtype, int n_rows, int max_rows, int32_t* status_dev,
-                   void* cuda_stream);
+int q3tts_kv8_read(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const int32_t* path_dev, void* k_out_dev,
+                   int ldk, void* v_out_dev, int ldv, void* cuda_stream);
 
 /* Attention of new rows over the cache, in one layer; the rows' own keys and values
  * have been written to it.  q_dev and out_dev: n_rows rows of n_q_heads x head_dim
@@ -84,10 +90,8 @@ int q3tts_kv8_read(const q3tts_kv8_cache* kv, int layer, const int32_t* page_tab
  * the result is rounded once to row_dtype.  It does not depend on the run, but may
  * on n_seqs, max_rows and pages_per_seq, which decide how positions are split.
  * q3tts_debug_lose_tile arms this call too. */
-int q3tts_kv8_attention(const q3tts_kv8_cache* kv, int layer, const int32_t* page_table_dev, int pages_per_seq,
-                        int n_seqs, const int32_t* lengths_dev, const int32_t* row_start_dev,
-                        const uint64_t* masks_dev, const void* q_dev, int ldq, void* out_dev, int ldo, int n_q_heads,
-                        int row_dtype, int n_rows, int max_rows, int32_t* status_dev, void* cuda_stream);
+int q3tts_kv8_attention(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const uint64_t* masks_dev,
+                        const void* q_dev, int ldq, void* out_dev, int ldo, int n_q_heads, void* cuda_stream);
 
 #ifdef __cplusplus
 }

@@ -27,16 +27,16 @@ def cache(**kw):
     return C.byref(q3tts.KV8Cache(*[f[n] for n, _ in q3tts.KV8Cache._fields_]))
 
 
-HEAD = dict(layer=0, table=A, pps=4, n_seqs=2, lengths=A, start=A)
-TAIL = dict(dtype=q3tts.F32, n_rows=8, max_rows=4, status=None, stream=None)
+ROWS = dict(table=A, lengths=A, start=A, status=None, layer=0, pps=4, n_seqs=2, dtype=q3tts.F32, n_rows=8, max_rows=4)
 PAIR = dict(a=A, lda=256, b=A + 65536, ldb=256)
 
 
-def call(fn, kv, extra_before, pair, extra_after, kw):
-    a = {**HEAD, **extra_before, **pair, **extra_after, **TAIL}
-    assert set(kw) <= set(a)
-    a.update(kw)
-    return fn(kv, *a.values())
+def call(fn, kv, before, pair, after, kw):
+    rows, args = dict(ROWS), {**before, **pair, **after, "stream": None}
+    assert set(kw) <= set(rows) | set(args)
+    rows.update((n, v) for n, v in kw.items() if n in rows)
+    args.update((n, v) for n, v in kw.items() if n in args)
+    return fn(kv, C.byref(q3tts.KV8Rows(*rows.values())), *args.values())
 
 
 def write(lib, kv=None, **kw):
@@ -61,11 +61,13 @@ def test_exports_every_declared_function(lib):
         assert hasattr(lib, n), n
 
 
-def test_struct_layout_matches_header():
-    body = re.search(r"typedef struct q3tts_kv8_cache \{(.*?)\} q3tts_kv8_cache", header(), re.S).group(1)
+@pytest.mark.parametrize("name,struct,packed", [("q3tts_kv8_cache", q3tts.KV8Cache, q3tts._CACHE8),
+                                                ("q3tts_kv8_rows", q3tts.KV8Rows, q3tts._ROWS8)])
+def test_struct_layouts_match_header(name, struct, packed):
+    body = re.search(r"typedef struct " + name + r" \{(.*?)\} " + name, header(), re.S).group(1)
     names = [n.strip().split()[-1].lstrip("*") for d in body.split(";") if d.strip() for n in d.split(",")]
-    assert names == [f[0] for f in q3tts.KV8Cache._fields_]
-    assert q3tts._CACHE8.size == C.sizeof(q3tts.KV8Cache)
+    assert names == [f[0] for f in struct._fields_]
+    assert packed.size == C.sizeof(struct)
 
 
 @pytest.mark.parametrize("fn", CALLS)
@@ -77,6 +79,12 @@ def test_struct_layout_matches_header():
 def test_caches_are_checked(lib, fn, bad, code):
     assert fn(lib, cache(**bad)) == code
     assert fn(lib, C.POINTER(q3tts.KV8Cache)()) == q3tts.ERR_ARG
+
+
+def test_no_rows_at_all(lib):
+    assert lib.q3tts_kv8_write(cache(), None, A, 256, A, 256, None) == q3tts.ERR_ARG
+    assert lib.q3tts_kv8_read(cache(), None, None, A, 256, A, 256, None) == q3tts.ERR_ARG
+    assert lib.q3tts_kv8_attention(cache(), None, None, A, 256, A, 256, 4, None) == q3tts.ERR_ARG
 
 
 @pytest.mark.parametrize("fn", CALLS)
