@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
     } else {
       // ---- softmax: a thread has a position of the tile and an element of the output
       const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-      Powers pw(a, d, m, tid);
+      Powers<1> pw(a, d, m, tid);
       // the queries' digits: a warp a row, magnitudes as 32-bit whole numbers with the sign in each digit
       for (int r = warp; r < R; r += 4) {
         constexpr int EPL = 4, LPR = HD / EPL;  // (a head dimension of 64: half of the lanes)
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
       for (int nib = 0; nib < 8; ++nib) pat[nib] = sbase + C::P + sw_at<128>(nib, tid >> 4) + (tid & 15);
       for (int i = 0; i < m.nt; ++i) {
         const int pos = (m.t0 + i) * TM_PT + tid, j = pos - m.t.L;
-        const float kf = kv8_power(pw.k) * 32.f, vf = kv8_power(pw.v), eb = (float)min(max(pw.v - 127, -60), 60);
+        const float kf = kv8_power(pw.k[0]) * 32.f, vf = kv8_power(pw.v[0]), eb = (float)min(max(pw.v[0] - 127, -60), 60);
         pw.next(a, d, m, i, tid);
         bool isbad = false;
         const bool edge = (m.t0 + i + 1) * TM_PT > m.t.L;  // the tile reaches past the committed positions

@@ -97,61 +97,62 @@ __device__ __forceinline__ bool take_item(const Kv8AttnArgs& a, const KfDeal& d,
   return true;
 }
 
-// The powers of one position of each of an item's tiles, on their way a tile ahead, and
-// its page, which leads to them, two: neither is waited for.  Blocks and pages are stepped
-// over without a division (KfDeal), which took longer than the rest of it.
+// The powers of a lane's N positions, 32 apart, of each of an item's tiles, on their way a
+// tile ahead, and their pages, which lead to them, two: neither is waited for.  Blocks and pages
+// are stepped over without a division (KfDeal), which took longer than the rest of it; all N are looked
+// up before the first is used.
+template <int N>
 struct Powers {
-  int k, v;  // bytes of its key's and its value's block (127 past what is seen)
-  // of the next tile's position when a tile's are used: page; of the one after that: its entry of
+  int k[N], v[N];  // bytes of a position's key block and value block (127 past what is seen)
+  // of the next tile's positions when a tile's are used: page; of the one after that: their entry of
   // the table's row, block of the page, place in the block
-  int page, entry, block, rem;
+  int page[N], entry[N], block[N], rem[N];
   const uint8_t* layer;  // the kv head's key powers on page 0
 
   __device__ __forceinline__ Powers(const Kv8AttnArgs& a, const KfDeal& d, const KfItem& m, int lane) {
-    const int pos = m.t0 * TM_PT + lane, ps = a.c.page, slot = pos % ps;
-    entry = pos / ps;
-    block = slot / a.c.block;
-    rem = slot - block * a.c.block;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int pos = m.t0 * TM_PT + lane + 32 * j;
+      entry[j] = kv8_div(pos, a.c.page, a.c.page_inv);
+      const int slot = pos - entry[j] * a.c.page;
+      block[j] = kv8_div(slot, a.c.block, a.c.block_inv);
+      rem[j] = slot - block[j] * a.c.block;
+    }
     layer = a.c.powers + ((long long)a.c.layer * a.c.n_pages * 2 * a.c.Hkv + m.g) * d.per_page;
     look(a, m, 0, lane);
-    bytes(a, d, m, 0, lane);
-    step(a, d);
-    look(a, m, 1, lane);
+    next(a, d, m, -1, lane);
   }
   // after tile i's have been used
   __device__ __forceinline__ void next(const Kv8AttnArgs& a, const KfDeal& d, const KfItem& m, int i, int lane) {
-    bytes(a, d, m, i + 1, lane);
-    step(a, d);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int pg = (unsigned)page[j] < (unsigned)a.c.n_pages ? page[j] : 0;  // (reported by the loading warps)
+      const uint8_t* p = layer + (long long)pg * (2 * d.to_values) + block[j];
+      const bool is = there(m, i + 1, lane + 32 * j);
+      k[j] = is ? __ldg(p) : 127;
+      v[j] = is ? __ldg(p + d.to_values) : 127;
+      // 128 positions on
+      rem[j] += d.step_rem;
+      block[j] += d.step_blocks;
+      if (rem[j] >= a.c.block) {
+        rem[j] -= a.c.block;
+        ++block[j];
+      }
+      entry[j] += d.step_pages;
+      if (block[j] >= d.per_page) {
+        block[j] -= d.per_page;
+        ++entry[j];
+      }
+    }
     look(a, m, i + 2, lane);
   }
 
  private:
-  __device__ __forceinline__ bool there(const KfItem& m, int i, int lane) const { return i < m.nt && (m.t0 + i) * TM_PT + lane < m.end; }
+  __device__ __forceinline__ bool there(const KfItem& m, int i, int at) const { return i < m.nt && (m.t0 + i) * TM_PT + at < m.end; }
   __device__ __forceinline__ void look(const Kv8AttnArgs& a, const KfItem& m, int i, int lane) {
-    page = there(m, i, lane) ? __ldg(a.r.page_table + (size_t)m.seq * a.r.pps + entry) : 0;
-  }
-  __device__ __forceinline__ void bytes(const Kv8AttnArgs& a, const KfDeal& d, const KfItem& m, int i, int lane) {
-    k = v = 127;
-    if (there(m, i, lane)) {
-      const int pg = (unsigned)page < (unsigned)a.c.n_pages ? page : 0;  // (reported by the loading warps)
-      const uint8_t* p = layer + (long long)pg * (2 * d.to_values) + block;
-      k = __ldg(p);
-      v = __ldg(p + d.to_values);
-    }
-  }
-  // 128 positions on
-  __device__ __forceinline__ void step(const Kv8AttnArgs& a, const KfDeal& d) {
-    rem += d.step_rem;
-    block += d.step_blocks;
-    if (rem >= a.c.block) {
-      rem -= a.c.block;
-      ++block;
-    }
-    entry += d.step_pages;
-    if (block >= d.per_page) {
-      block -= d.per_page;
-      ++entry;
-    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      page[j] = there(m, i, lane + 32 * j) ? __ldg(a.r.page_table + (size_t)m.seq * a.r.pps + entry[j]) : 0;
   }
 };
 // Swizzled operand tiles with rows of W bytes (128 or 64) in atoms of eight rows.

@@ -253,35 +253,35 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
     } else if (warp == C::POWER_WARP) {
       // ---- powers, four positions a lane
       give_registers();
-      Powers pw[4] = {{a, d, m, lane}, {a, d, m, lane + 32}, {a, d, m, lane + 64}, {a, d, m, lane + 96}};
+      Powers<4> pw(a, d, m, lane);
       for (int t = 0; t < m.nt; ++t) {
         ok = kv8_wait(su32(&ctl.pw_empty[t & 3]), ((uint32_t)(t >> 2) & 1u) ^ 1u, abort_w, status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int n = lane + 32 * j, pos = (m.t0 + t) * TM_PT + n, e = min(max(pw[j].v - 127, -KW_EXP), KW_EXP);
+          const int n = lane + 32 * j, pos = (m.t0 + t) * TM_PT + n, e = min(max(pw.v[j] - 127, -KW_EXP), KW_EXP);
           // a new row's block of NaN: rows that see it are told by its bit alone
-          const bool bad = pos >= m.t.L && (pw[j].k == 255 || pw[j].v == 255);
-          const bool none = bad || pw[j].v < 127 - KW_EXP || pos >= m.end;  // no values, or none that count
+          const bool bad = pos >= m.t.L && (pw.k[j] == 255 || pw.v[j] == 255);
+          const bool none = bad || pw.v[j] < 127 - KW_EXP || pos >= m.end;  // no values, or none that count
           if (n % GRAN == 0)
-            ctl.power[t & 3][n / GRAN] = make_float4(bad ? 1.f : kv8_power(pw[j].k), pw[j].v == 255 && !bad ? kv8_power(255) : (float)e,
+            ctl.power[t & 3][n / GRAN] = make_float4(bad ? 1.f : kv8_power(pw.k[j]), pw.v[j] == 255 && !bad ? kv8_power(255) : (float)e,
                                                      __int_as_float((127 - e) << 23), 0.f);
           const unsigned b0 = __ballot_sync(0xffffffffu, bad), n0 = __ballot_sync(0xffffffffu, none);
           if (lane == 0) {
             ctl.bad[t & 3][j] = b0;
             ctl.none[t & 3][j] = n0;
           }
-          pw[j].next(a, d, m, t, n);
         }
         mbar_arrive(su32(&ctl.pw_full[t & 3]));
+        pw.next(a, d, m, t, lane);
       }
     } else if (warp >= C::CONV_WARP) {
       // ---- codes to fp16: two warps the keys, two the values.  A thread has chunk c (16 codes) of every RPI-th
       // row.  Eight lanes have four chunks of rows r and r ^ 5, whose places in the swizzle are apart
       // both in the codes' tile and (at twice the chunk) in fp16's; rows RPI apart, a multiple of 8, have the same.
       give_registers();
-      constexpr int RPI = KW_CONV / (HD / 16), ROWS = TM_PT / RPI, U = 8;
+      constexpr int RPI = KW_CONV / (HD / 16), ROWS = TM_PT / RPI, U = 4;
       static_assert(RPI % 8 == 0 && ROWS % U == 0, "rows of a thread");
       const int h = (warp - C::CONV_WARP) >> 1, ct = ((warp - C::CONV_WARP) & 1) * 32 + lane;
       const int oct = ct >> 3, pair = HD == 128 ? oct >> 1 : oct & 3, c = (lane & 3) + (HD == 128 ? (oct & 1) * 4 : 0);
@@ -393,35 +393,42 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
         // the queries, scaled to 2^14 .. 2^15, go to tensor memory, a lane a row, by way of shared
         // memory: a warp reads whole rows (a lane its own row: 3.5 us more).  Their place is that of
         // the odd tiles, whose conversion waits for it.
-        constexpr int LPR = HD / 4, RPW = 32 / LPR, U = KW_ROWS / (KW_SOFT / 32) / RPW;
-        const int sub = lane / LPR, e = lane % LPR * 4;
+        // All its rows are on their way at once; half of them at a time are converted (unrolled over all,
+        // fetching the instructions took longer).
+        constexpr int LPR = HD / 4, RPW = 32 / LPR, ALL = KW_ROWS / (KW_SOFT / 32) / RPW, U = ALL / 2;
+        const int sub = lane / LPR, e = lane % LPR * 4, last = m.n0 + m.rows - 1;
         const T* q0 = static_cast<const T*>(a.q) + (size_t)m.t.row0 * a.ldq + (size_t)m.g * rep * HD + e;
-        float4 x[U];
+        float4 x[U], next[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int at = min(m.n0 + (warp * U + u) * RPW + sub, m.n0 + m.rows - 1), of = kv8_div(at, rep, d.rep_inv);
-          x[u] = q4(q0 + (size_t)of * a.ldq + (size_t)(at - of * rep) * HD, d.vec & 1);
+        for (int u = 0; u < ALL; ++u) {
+          const int at = min(m.n0 + (warp * ALL + u) * RPW + sub, last), of = kv8_div(at, rep, d.rep_inv);
+          (u < U ? x[u % U] : next[u % U]) = q4(q0 + (size_t)of * a.ldq + (at - of * rep) * HD, d.vec & 1);
         }
+#pragma unroll 1
+        for (int u0 = 0; u0 < ALL; u0 += U) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int at = (warp * U + u) * RPW + sub;
-          uint32_t top = max(max(__float_as_uint(x[u].x) & 0x7fffffffu, __float_as_uint(x[u].y) & 0x7fffffffu),
-                             max(__float_as_uint(x[u].z) & 0x7fffffffu, __float_as_uint(x[u].w) & 0x7fffffffu));
-          top = __reduce_max_sync(LPR == 32 ? 0xffffffffu : 0xffffu << (16 * sub), top);
-          const int E = min(max((int)(top >> 23) - 126, -100), 127);  // |q| < 2^E
-          const float by = __int_as_float((127 + 15 - E) << 23);
-          if (lane % LPR == 0) ctl.sum[at] = 1.4426950408889634f / sqrtf((float)HD) * __int_as_float((127 - 15 + E) << 23);
-          float v[4] = {x[u].x * by, x[u].y * by, x[u].z * by, x[u].w * by};
+          for (int u = 0; u < U; ++u) {
+            const int at = (warp * ALL + u0 + u) * RPW + sub;
+            uint32_t top = max(max(__float_as_uint(x[u].x) & 0x7fffffffu, __float_as_uint(x[u].y) & 0x7fffffffu),
+                               max(__float_as_uint(x[u].z) & 0x7fffffffu, __float_as_uint(x[u].w) & 0x7fffffffu));
+            top = __reduce_max_sync(LPR == 32 ? 0xffffffffu : 0xffffu << (16 * sub), top);
+            const int E = min(max((int)(top >> 23) - 126, -100), 127);  // |q| < 2^E
+            const float by = __int_as_float((127 + 15 - E) << 23);
+            if (lane % LPR == 0) ctl.sum[at] = 1.4426950408889634f / sqrtf((float)HD) * __int_as_float((127 - 15 + E) << 23);
+            float v[4] = {x[u].x * by, x[u].y * by, x[u].z * by, x[u].w * by};
 #pragma unroll
-          for (int term = 0; term < C::TERMS; ++term) {
-            const uint2 w = make_uint2(pack_half(v[0], v[1]), pack_half(v[2], v[3]));
-            *reinterpret_cast<uint2*>(sp + (term ? C::V : C::K) + C::TILE + at * (HD * 2) + (((e >> 3) ^ (at & 7)) << 4) + (e & 4) * 2) = w;
-            const float2 h0 = unpack_half(w.x), h1 = unpack_half(w.y);
-            v[0] -= h0.x;
-            v[1] -= h0.y;
-            v[2] -= h1.x;
-            v[3] -= h1.y;
+            for (int term = 0; term < C::TERMS; ++term) {
+              const uint2 w = make_uint2(pack_half(v[0], v[1]), pack_half(v[2], v[3]));
+              *reinterpret_cast<uint2*>(sp + (term ? C::V : C::K) + C::TILE + at * (HD * 2) + (((e >> 3) ^ (at & 7)) << 4) + (e & 4) * 2) = w;
+              const float2 h0 = unpack_half(w.x), h1 = unpack_half(w.y);
+              v[0] -= h0.x;
+              v[1] -= h0.y;
+              v[2] -= h1.x;
+              v[3] -= h1.y;
+            }
           }
+#pragma unroll
+          for (int u = 0; u < U; ++u) x[u] = next[u];
         }
         kw_vote(false, 1);
         qs = ctl.sum[r];
@@ -602,7 +609,7 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
   }
   __syncthreads();
   if (have && !*abort_w) {
-    constexpr int LPR = HD / 4, RPI = C::THREADS / LPR, U = 4;  // lanes of a row, rows at a time, loads on their way
+    constexpr int LPR = HD / 4, RPI = C::THREADS / LPR, U = 2;  // lanes of a row, rows at a time, loads on their way
     const int e = tid % LPR * 4;
     T* out = static_cast<T*>(a.out) + (size_t)m.t.row0 * a.ldo + (size_t)m.g * rep * HD + e;
     for (int n0 = rank + CL * (tid / LPR); n0 < m.rows; n0 += CL * RPI * U) {
