@@ -45,14 +45,16 @@ template <>
 struct Four<bf16> {
   using V = uint2;
 };
-// The bits of |x|, 0 for an infinity or NaN.
-__device__ __forceinline__ uint32_t finite_bits(float x) {
-  const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
-  return b < 0x7f800000u ? b : 0u;
-}
-// x / 2^e to be rounded; infinities become NaN.
-__device__ __forceinline__ float scaled(float x, float by) {
-  return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? __int_as_float(0x7fc00000) : x * by;
+// Whether x is an infinity or NaN.
+__device__ __forceinline__ bool special(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+// The largest of the magnitudes' bits; ALL: infinities and NaN among them.
+template <bool ALL>
+__device__ __forceinline__ uint32_t top_bits(uint32_t top, float4 f) {
+  const float x[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (ALL || !special(x[i])) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  return top;
 }
 
 // A warp per block, kv head and k or v; a lane has four elements of a row, a load
@@ -91,16 +93,24 @@ __global__ void __launch_bounds__(KV8_WRITE_THREADS, U == 1 || sizeof(T) == 2 ? 
   };
   const int entry = kv8_div(p0, c.page, c.page_inv), slot = p0 - entry * c.page;
   const int page = __ldg(r.page_table + (size_t)seq * r.pps + entry);
+  // (infinities and NaN do not count: sorted out, here and when rounding, only where there are any)
   uint32_t top = 0;
   for (int i0 = 0; i0 < m; i0 += U * RPL) {
     load(i0);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float4 f = as_f(x[u]);
-      top = max(max(top, max(finite_bits(f.x), finite_bits(f.y))), max(finite_bits(f.z), finite_bits(f.w)));
-    }
+    for (int u = 0; u < U; ++u) top = top_bits<true>(top, as_f(x[u]));
   }
   top = __reduce_max_sync(0xffffffffu, top);
+  const bool odd = top >= 0x7f800000u;
+  if (odd) {
+    top = 0;
+    for (int i0 = 0; i0 < m; i0 += U * RPL) {
+      if (m > U * RPL) load(i0);
+#pragma unroll
+      for (int u = 0; u < U; ++u) top = top_bits<false>(top, as_f(x[u]));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+  }
   if (page < 0 || page >= c.n_pages) {
     if (lane == 0) op_status(r.status, Q3TTS_ERR_ARG);
     return;
@@ -127,11 +137,13 @@ __global__ void __launch_bounds__(KV8_WRITE_THREADS, U == 1 || sizeof(T) == 2 ? 
   uint8_t* dst = c.codes + (row + held) * HD + e0;
   for (int i0 = 0; i0 < m; i0 += U * RPL) {
     if (m > U * RPL) load(i0);
+    const float nan = __int_as_float(0x7fc00000);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * RPL + sub;
-      const float4 f = as_f(x[u]);
-      if (i < m) *reinterpret_cast<uint32_t*>(dst + i * HD) = kv8_codes(scaled(f.x, by), scaled(f.y, by), scaled(f.z, by), scaled(f.w, by));
+      float4 f = as_f(x[u]);
+      if (odd) f = make_float4(special(f.x) ? nan : f.x, special(f.y) ? nan : f.y, special(f.z) ? nan : f.z, special(f.w) ? nan : f.w);
+      if (i < m) *reinterpret_cast<uint32_t*>(dst + i * HD) = kv8_codes(f.x * by, f.y * by, f.z * by, f.w * by);
     }
   }
   if (lane == 0) *power = (uint8_t)byte;
