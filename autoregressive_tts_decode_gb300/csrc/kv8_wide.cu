@@ -91,6 +91,16 @@ __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&r)[32]) {
         "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr));
 }
+// 16 columns into r[O ..] and the largest of them.
+template <int O>
+__device__ __forceinline__ void tmem_ld16_max(uint32_t taddr, float (&r)[32], float& top) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, %16, [%17];"
+      : "=f"(r[O]), "=f"(r[O + 1]), "=f"(r[O + 2]), "=f"(r[O + 3]), "=f"(r[O + 4]), "=f"(r[O + 5]), "=f"(r[O + 6]), "=f"(r[O + 7]),
+        "=f"(r[O + 8]), "=f"(r[O + 9]), "=f"(r[O + 10]), "=f"(r[O + 11]), "=f"(r[O + 12]), "=f"(r[O + 13]), "=f"(r[O + 14]),
+        "=f"(r[O + 15]), "=f"(top)
+      : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld8u(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -468,8 +478,13 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
         for (int ch = 0; ch < TM_PT / CK; ++ch) {
-          float x[CK];
-          tmem_ld32f(src + CK * ch, x);
+          float x[CK], most[2];  // (blocks of 16 positions or more: the largest score of each 16, found by the load)
+          if constexpr (GRAN == 16) {
+            tmem_ld16_max<0>(src + CK * ch, x, most[0]);
+            tmem_ld16_max<16>(src + CK * ch + 16, x, most[1]);
+          } else {
+            tmem_ld32f(src + CK * ch, x);
+          }
           asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
           const int dd = p0 + CK * ch - m.t.L;  // its first position, counted from the first new row
           if (dd > -CK) {
@@ -485,15 +500,24 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < CK; ++e)
               x[e] = !((sees >> e) & 1u) ? -INFINITY : (nan >> e) & 1u ? __uint_as_float(0x7fc00000u) : x[e];
+            if constexpr (GRAN == 16) {
+              most[0] = most[1] = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < CK; ++e) most[e / 16] = fmaxf(most[e / 16], x[e]);
+            }
           }
           const float4* pc = pw + CK / GRAN * ch;
           float top = -INFINITY;
 #pragma unroll
           for (int e = 0; e < CK; e += GRAN) {
-            float mx[2] = {x[e], x[e + (GRAN > 1)]};
+            float mx = x[e];
+            if constexpr (GRAN == 16) {
+              mx = most[e / 16];
+            } else {
 #pragma unroll
-            for (int f = 2; f < GRAN; ++f) mx[f & 1] = fmaxf(mx[f & 1], x[e + f]);
-            top = fmaxf(top, fmaf(fmaxf(mx[0], mx[1]), fmaxf(pc[e / GRAN].x * qs, KW_TINY), pc[e / GRAN].y));
+              for (int f = 1; f < GRAN; ++f) mx = fmaxf(mx, x[e + f]);
+            }
+            top = fmaxf(top, fmaf(mx, fmaxf(pc[e / GRAN].x * qs, KW_TINY), pc[e / GRAN].y));
           }
           const bool rises = top - base > KW_MOST;
           if (__any_sync(0xffffffffu, rises)) {
