@@ -12,8 +12,9 @@
 // Both are bound by the bytes they move, rows in one form and codes in the other: 125,000 rows of
 // eight kv heads read back to bf16 (771 MB): 122 us, 6.3 TB/s, 93 % of a plain copy (141 us with 64-bit
 // divisions in the addresses: three quarters of the issue slots were taken); eight fp32 prompts of 2 ..
-// 1982 rows written (81 MB): 17.9 us, 4.5 TB/s, waves of warps that each wait for their rows.  Calls for
-// single tokens are a launch and three dependent loads, 2.5 to 3 us.
+// 1982 rows written (81 MB): 16.0 us, 5.1 TB/s, waves of warps that each wait for their rows (17.9 with every
+// element looked at for infinities and NaN).  Calls for single tokens are a launch and three dependent
+// loads, 2.5 to 3 us.
 #include "kv8.cuh"
 
 namespace q3 {
