@@ -379,40 +379,42 @@ def test_attention_over_pages_of_all_sizes(q3, case, dtype):
     assert torch.equal(out, run_attention(q3, c)) or max(c["rows"]) != sum(c["rows"])
 
 
-SHAPES = [(1, 4, 2, 300), (13, 4, 2, 300), (64, 4, 2, 500), (40, 16, 1, 77), (1, 2, 1, 3000), (5, 8, 1, 129)]
+# rows, heads, kv heads, positions, sequences; the last three fill the GPU with tiles of 128 rows
+SHAPES = [(1, 4, 2, 300, 1), (13, 4, 2, 300, 1), (64, 4, 2, 500, 1), (40, 16, 1, 77, 1), (1, 2, 1, 3000, 1), (5, 8, 1, 129, 1),
+          (64, 4, 2, 200, 60), (33, 16, 2, 77, 50), (20, 8, 1, 300, 110)]
 
 
-@pytest.mark.parametrize("rows,heads,kvh,length", SHAPES)
+@pytest.mark.parametrize("rows,heads,kvh,length,seqs", SHAPES)
 @pytest.mark.parametrize("tree", [True, False])
-def test_attention_over_blocks_of_all_sizes(q3, tree, rows, heads, kvh, length):
+def test_attention_over_blocks_of_all_sizes(q3, tree, rows, heads, kvh, length, seqs):
     """Powers from 2^-40 to 2^40 in one sequence (queries small, so that scores stay in
     their range): small values count where the large ones get no weight."""
-    c = attend_case(np.random.default_rng(10), [length], [rows], heads, kvh, 128, 16, 4, "float32", tree, lo=87, hi=167)
+    c = attend_case(np.random.default_rng(10), [length] * seqs, [rows] * seqs, heads, kvh, 128, 16, 4, "float32", tree, lo=87, hi=167)
     c["powers"][:, :, 0] = np.where(c["powers"][:, :, 0] == 255, 255, 120)
     check_attention(c, run_attention(q3, c))
 
 
-@pytest.mark.parametrize("rows,heads,kvh,length", SHAPES)
+@pytest.mark.parametrize("rows,heads,kvh,length,seqs", SHAPES)
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
-def test_scores_far_apart(q3, rows, heads, kvh, length, dtype):
+def test_scores_far_apart(q3, rows, heads, kvh, length, seqs, dtype):
     """Scores up to hundreds: the largest rises from tile to tile, nearly all weights vanish."""
-    c = attend_case(np.random.default_rng(11), [length], [rows], heads, kvh, 128, 16, 16, dtype, False)
+    c = attend_case(np.random.default_rng(11), [length] * seqs, [rows] * seqs, heads, kvh, 128, 16, 16, dtype, False)
     c["q"] = (c["q"].float() * 16).to(c["q"].dtype)
     check_attention(c, run_attention(q3, c))
 
 
-@pytest.mark.parametrize("rows,heads,kvh,length", SHAPES)
-def test_rows_that_see_nothing_and_rows_that_do_not_see_nan(q3, rows, heads, kvh, length):
+@pytest.mark.parametrize("rows,heads,kvh,length,seqs", SHAPES)
+def test_rows_that_see_nothing_and_rows_that_do_not_see_nan(q3, rows, heads, kvh, length, seqs):
     """Masks of nothing (over an empty context: zeroes), and nodes that are NaN or huge, in
     their codes and in their blocks' powers, seen by none of the others."""
     import torch
-    rng = np.random.default_rng(12)
+    rng, n = np.random.default_rng(12), seqs + 1
     for ctx in (0, length):
-        c = attend_case(rng, [ctx, ctx], [rows, rows], heads, kvh, 64, 16, 1, "float32", True)
+        c = attend_case(rng, [ctx] * n, [rows] * n, heads, kvh, 64, 16, 1, "float32", True)
         c["masks"] = [m & ~1 if i % rows else 0 for i, m in enumerate(c["masks"])]
         if rows > 2:  # none sees node 1 either
             c["masks"] = [m & ~2 for m in c["masks"]]
-        for s in range(2):
+        for s in range(n):
             for node, power in ((0, 255), (1, 254)):
                 if node < rows:
                     pos = ctx + node
@@ -423,31 +425,35 @@ def test_rows_that_see_nothing_and_rows_that_do_not_see_nan(q3, rows, heads, kvh
         out = run_attention(q3, c)
         check_attention(c, out)
         if ctx == 0:
-            assert bool((out[0] == 0).all()) and bool((out[rows] == 0).all())
+            assert bool((out[::rows] == 0).all())
 
 
+@pytest.mark.parametrize("seqs", [1, 60])
 @pytest.mark.parametrize("rows", [1, 40, 64])
-def test_a_row_that_sees_nan_is_nan_alone(q3, rows):
-    """A NaN value that one node sees: its row is NaN, the others' results do not change."""
+def test_a_row_that_sees_nan_is_nan_alone(q3, rows, seqs):
+    """A NaN value that one node of each sequence sees: its row is NaN, the others' results
+    do not change."""
     import torch
-    c = attend_case(np.random.default_rng(13), [200], [rows], 4, 2, 128, 16, 16, "float32", True)
+    c = attend_case(np.random.default_rng(13), [200] * seqs, [rows] * seqs, 4, 2, 128, 16, 16, "float32", True)
     want = run_attention(q3, c)
     pos = 200 + rows - 1
-    c["codes"][:, c["table"][0, pos // 16], 1, :, pos % 16, 7] = ku.NAN
+    for s in range(seqs):
+        c["codes"][:, c["table"][s, pos // 16], 1, :, pos % 16, 7] = ku.NAN
     out = run_attention(q3, c)
-    assert torch.equal(out[:-1], want[:-1]) and bool(torch.isnan(out[-1, :, 7]).all())
+    last = torch.arange(rows * seqs, device="cuda") % rows == rows - 1
+    assert torch.equal(out[~last], want[~last]) and bool(torch.isnan(out[last, :, 7]).all())
 
 
-@pytest.mark.parametrize("rows,heads,kvh,length", SHAPES)
+@pytest.mark.parametrize("rows,heads,kvh,length,seqs", SHAPES)
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
-def test_pitches_and_rows_outside_the_sequences(q3, rows, heads, kvh, length, dtype):
+def test_pitches_and_rows_outside_the_sequences(q3, rows, heads, kvh, length, seqs, dtype):
     """Queries and outputs inside wider rows, at addresses that are not multiples of 16
     bytes; rows before the first sequence and behind the last are left alone."""
     import torch
     hd, extra = 64, 1
-    c = attend_case(np.random.default_rng(14), [length, 3], [rows, 1], heads, kvh, hd, 16, 16, dtype, False)
+    c = attend_case(np.random.default_rng(14), [length] * seqs + [3], [rows] * seqs + [1], heads, kvh, hd, 16, 16, dtype, False)
     want = run_attention(q3, c)
-    n = rows + 1
+    n = rows * seqs + 1
     buf = torch.full(((n + 4) * (heads * hd + extra) + 9,), -7.5, dtype=c["q"].dtype, device="cuda")
 
     def view():
@@ -460,15 +466,16 @@ def test_pitches_and_rows_outside_the_sequences(q3, rows, heads, kvh, length, dt
     assert torch.equal(out[2:-2], want) and bool((out[:2] == -7.5).all()) and bool((out[-2:] == -7.5).all())
 
 
-@pytest.mark.parametrize("rows", [1, 3, 50])
+@pytest.mark.parametrize("rows,seqs", [(1, 3), (3, 3), (50, 3), (50, 70)])
 @pytest.mark.parametrize("tree", [True, False])
-def test_attention_leaves_out_what_does_not_fit(q3, rows, tree):
+def test_attention_leaves_out_what_does_not_fit(q3, rows, seqs, tree):
     import torch
-    c = attend_case(np.random.default_rng(15), [100, 200, 150], [rows] * 3, 4, 2, 128, 16, 16, "float32", tree)
+    lens = ([100, 200, 150] * seqs)[:seqs]
+    c = attend_case(np.random.default_rng(15), lens, [rows] * seqs, 4, 2, 128, 16, 16, "float32", tree)
     want = run_attention(q3, c)
     cap = 16 * c["table"].shape[1]
     for bad in (cap - rows + 1, -1, 1 << 30):
-        d = dict(c, lens=[100, bad, 150])
+        d = dict(c, lens=[100, bad, *lens[2:]])
         out, status = torch.full_like(want, 3.0), ku.ints([0])
         run_attention(q3, d, out=out, status=status)
         assert int(status) == q3.ERR_ARG
