@@ -352,7 +352,8 @@ def test_attention(q3, case, tree, dtype):
 @pytest.mark.parametrize("tree,seqs,longest,most,heads,kvh,hd,page,block", [
     (True, 97, 700, 13, 16, 8, 128, 16, 16), (True, 60, 1500, 1, 8, 8, 128, 16, 16), (True, 300, 90, 3, 4, 2, 64, 16, 8),
     (True, 45, 600, 40, 8, 4, 128, 16, 16), (True, 33, 800, 64, 2, 1, 64, 24, 8), (False, 41, 900, 1, 16, 8, 128, 12, 12),
-    (False, 60, 300, 100, 8, 4, 128, 16, 16), (False, 170, 300, 33, 8, 1, 64, 64, 16), (False, 300, 40, 1, 4, 4, 128, 8, 4)])
+    (False, 60, 300, 100, 8, 4, 128, 16, 16), (False, 170, 300, 33, 8, 1, 64, 64, 16), (False, 300, 40, 1, 4, 4, 128, 8, 4),
+    (False, 270, 60, 40, 8, 1, 64, 16, 8), (True, 300, 150, 30, 8, 1, 128, 5, 5), (False, 70, 500, 60, 12, 3, 128, 200, 8)])
 def test_attention_of_many_sequences(q3, dtype, tree, seqs, longest, most, heads, kvh, hd, page, block):
     import torch
     rng = np.random.default_rng(9)
