@@ -223,8 +223,10 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
         }
         if (lane == 0) {
           // q is its digits' sum (the top one whole, codes for 2^-9 of a digit) x 2^(E - 32 + 28 + 9); the
-          // position's factor has 2^5 of that
-          ctl.qscale[r] = 1.4426950408889634f / sqrtf((float)HD) * __int_as_float(max(127 + E, 1) << 23);
+          // position's factor has 2^5 of that.  Infinities and NaN, which have no digits: NaN, and with it every
+          // score that the row sees
+          ctl.qscale[r] = top >= 0x7f800000u ? __int_as_float(0x7fc00000)
+                                             : 1.4426950408889634f / sqrtf((float)HD) * __int_as_float(max(127 + E, 1) << 23);
           ctl.mask[r] = r >= m.rows ? 0ull : a.masks ? a.masks[m.t.row0 + node] : 0ull;
           ctl.base[r] = TM_FLOOR;
         }

@@ -423,7 +423,8 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
                                max(__float_as_uint(x[u].z) & 0x7fffffffu, __float_as_uint(x[u].w) & 0x7fffffffu));
             top = __reduce_max_sync(LPR == 32 ? 0xffffffffu : 0xffffu << (16 * sub), top);
             const int E = min(max((int)(top >> 23) - 126, -100), 127);  // |q| < 2^E
-            const float by = __int_as_float((127 + 15 - E) << 23);
+            // (a row with an infinity or NaN becomes NaN: an infinity's scores might all be -inf, as if it saw nothing)
+            const float by = top >= 0x7f800000u ? __int_as_float(0x7fc00000) : __int_as_float((127 + 15 - E) << 23);
             if (lane % LPR == 0) ctl.sum[at] = 1.4426950408889634f / sqrtf((float)HD) * __int_as_float((127 - 15 + E) << 23);
             float v[4] = {x[u].x * by, x[u].y * by, x[u].z * by, x[u].w * by};
 #pragma unroll
