@@ -200,8 +200,9 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
         top = __reduce_max_sync(0xffffffffu, top);
-        const int E = max((int)(top >> 23) - 126, -90);  // |q| < 2^E
-        const float by0 = __int_as_float((127 + 16) << 23), by1 = __int_as_float((127 + 16 - E) << 23);
+        // |q| < 2^E, of the largest and of subnormal ones: 2^(32 - E) and, below, 2^E in two factors
+        const int E = min(max((int)(top >> 23) - 126, -125), 128), half = (32 - E) >> 1;
+        const float by0 = __int_as_float((127 + 32 - E - half) << 23), by1 = __int_as_float((127 + half) << 23);
         uint32_t ev[4], od[4], sg[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -222,11 +223,10 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
           }
         }
         if (lane == 0) {
-          // q is its digits' sum (the top one whole, codes for 2^-9 of a digit) x 2^(E - 32 + 28 + 9); the
-          // position's factor has 2^5 of that.  Infinities and NaN, which have no digits: NaN, and with it every
-          // score that the row sees
+          // q is its digits' sum (the top one whole, codes for 2^-9 of a digit) x 2^(E - 32 + 28 + 9), of which the
+          // sum takes 2^5.  Infinities and NaN, which have no digits: NaN, and with it every score that the row sees
           ctl.qscale[r] = top >= 0x7f800000u ? __int_as_float(0x7fc00000)
-                                             : 1.4426950408889634f / sqrtf((float)HD) * __int_as_float(max(127 + E, 1) << 23);
+                                             : 2.f * 1.4426950408889634f / sqrtf((float)HD) * __int_as_float((126 + E) << 23);
           ctl.mask[r] = r >= m.rows ? 0ull : a.masks ? a.masks[m.t.row0 + node] : 0ull;
           ctl.base[r] = TM_FLOOR;
         }
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
       for (int nib = 0; nib < 8; ++nib) pat[nib] = sbase + C::P + sw_at<128>(nib, tid >> 4) + (tid & 15);
       for (int i = 0; i < m.nt; ++i) {
         const int pos = (m.t0 + i) * TM_PT + tid, j = pos - m.t.L;
-        const float kf = kv8_power(pw.k[0]) * 32.f, vf = kv8_power(pw.v[0]), eb = (float)min(max(pw.v[0] - 127, -60), 60);
+        const float kf = kv8_power(pw.k[0]), vf = kv8_power(pw.v[0]), eb = (float)min(max(pw.v[0] - 127, -60), 60);
         pw.next(a, d, m, i, tid);
         bool isbad = false;
         const bool edge = (m.t0 + i + 1) * TM_PT > m.t.L;  // the tile reaches past the committed positions
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
             float s = __uint_as_float(v[8 * h]);
 #pragma unroll
             for (int nib = 1; nib < 8; ++nib) s = fmaf(s, 0.0625f, __uint_as_float(v[8 * h + nib]));
-            x[r + h] = s * kf * ctl.qscale[r + h];
+            x[r + h] = s * 32.f * (kf * ctl.qscale[r + h]);  // (large keys meet small queries, and the reverse)
           }
         }
         if (edge && j >= 0) {

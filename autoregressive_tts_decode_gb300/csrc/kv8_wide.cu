@@ -61,7 +61,7 @@ struct KwCtl {
   int seq;
   alignas(16) unsigned none[4][4];  // positions of a tile whose values do not count
   unsigned bad[4][4];               // of them, new rows with a NaN
-  float4 power[4][TM_PT];     // of a position (or four that share a block): key power, value power's exponent, its inverse
+  float4 power[4][TM_PT];     // of a position (or those that share a block): key power x 2^-15, value power's exponent, its inverse
   float bases[4][KW_ROWS];    // of the rows in a tile
   float end[2][2][KW_ROWS];   // each softmax group's last base and sum
   float base[KW_ROWS], sum[KW_ROWS];
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
           const bool bad = pos >= m.t.L && (pw.k[j] == 255 || pw.v[j] == 255);
           const bool none = bad || pw.v[j] < 127 - KW_EXP || pos >= m.end;  // no values, or none that count
           if (n % GRAN == 0)
-            ctl.power[t & 3][n / GRAN] = make_float4(bad ? 1.f : kv8_power(pw.k[j]), pw.v[j] == 255 && !bad ? kv8_power(255) : (float)e,
+            ctl.power[t & 3][n / GRAN] = make_float4(bad ? 1.f : kv8_power(pw.k[j]) * 0x1p-15f, pw.v[j] == 255 && !bad ? kv8_power(255) : (float)e,
                                                      __int_as_float((127 - e) << 23), 0.f);
           const unsigned b0 = __ballot_sync(0xffffffffu, bad), n0 = __ballot_sync(0xffffffffu, none);
           if (lane == 0) {
@@ -422,11 +422,14 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
             uint32_t top = max(max(__float_as_uint(x[u].x) & 0x7fffffffu, __float_as_uint(x[u].y) & 0x7fffffffu),
                                max(__float_as_uint(x[u].z) & 0x7fffffffu, __float_as_uint(x[u].w) & 0x7fffffffu));
             top = __reduce_max_sync(LPR == 32 ? 0xffffffffu : 0xffffu << (16 * sub), top);
-            const int E = min(max((int)(top >> 23) - 126, -100), 127);  // |q| < 2^E
+            // |q| < 2^E, of the largest and of subnormal ones: 2^(15 - E) and 2^E in two factors; of its inverse the
+            // keys' powers have 2^-15 (large keys meet small queries, and the reverse)
+            const int E = min(max((int)(top >> 23) - 126, -125), 128), half = (15 - E) >> 1;
             // (a row with an infinity or NaN becomes NaN: an infinity's scores might all be -inf, as if it saw nothing)
-            const float by = top >= 0x7f800000u ? __int_as_float(0x7fc00000) : __int_as_float((127 + 15 - E) << 23);
-            if (lane % LPR == 0) ctl.sum[at] = 1.4426950408889634f / sqrtf((float)HD) * __int_as_float((127 - 15 + E) << 23);
-            float v[4] = {x[u].x * by, x[u].y * by, x[u].z * by, x[u].w * by};
+            const float by = top >= 0x7f800000u ? __int_as_float(0x7fc00000) : __int_as_float((127 + 15 - E - half) << 23);
+            const float by1 = __int_as_float((127 + half) << 23);
+            if (lane % LPR == 0) ctl.sum[at] = 2.f * 1.4426950408889634f / sqrtf((float)HD) * __int_as_float((126 + E) << 23);
+            float v[4] = {x[u].x * by * by1, x[u].y * by * by1, x[u].z * by * by1, x[u].w * by * by1};
 #pragma unroll
             for (int term = 0; term < C::TERMS; ++term) {
               const uint2 w = make_uint2(pack_half(v[0], v[1]), pack_half(v[2], v[3]));

@@ -80,11 +80,12 @@ int q3tts_kv8_read(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const 
  * [n_rows], 8-byte aligned; a drafted tree, max_rows up to
  * Q3TTS_MAX_TREE_NODES).  One that sees nothing gets zeroes.  What a row does not
  * see does not touch it, NaN among it; a row that sees a NaN is unspecified, like
- * one with scores above 2^27, or values above 2^60 in size.  A head's query with an
- * infinity or NaN makes its output NaN, if it sees anything.  Values in blocks whose
- * power is below 2^-60 may count as zeroes.  Rows outside every sequence's range
- * are left as they were; page ids outside the pool leave the sequence's rows
- * unspecified.  No row of out may share a byte with one of q (Q3TTS_ERR_ARG).
+ * one with scores above 2^27, an element of its query times a key block's power above
+ * 2^100, or values above 2^60 in size.  A head's query with an infinity or NaN makes
+ * its output NaN, if it sees anything.  Values in blocks whose power is below 2^-60
+ * may count as zeroes.  Rows outside every sequence's range are left as they were;
+ * page ids outside the pool leave the sequence's rows unspecified.  No row of out may
+ * share a byte with one of q (Q3TTS_ERR_ARG).
  * Caches of up to 2^31 rows of head_dim elements in all (else
  * Q3TTS_ERR_UNSUPPORTED).  Scores, softmax statistics and sums are held in 32 bits;
  * a weight meets the values with 22 bits or more (11 where row_dtype is bf16), and

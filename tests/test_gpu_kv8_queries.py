@@ -55,3 +55,20 @@ def test_a_query_that_is_not_finite_and_sees_nothing(q3, rows, seqs):
     c["q"][rows - 1::rows, 1] = math.inf
     out = t8.run_attention(q3, c)
     assert torch.equal(out, want) and bool((out[rows - 1::rows] == 0).all())
+
+
+@pytest.mark.parametrize("rows,heads,kvh,length,seqs", t8.SHAPES)
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("size,byte", [(126, 1), (120, 7), (-100, 227), (-120, 247), (-127, 254)])
+def test_queries_at_either_end_of_the_range(q3, rows, heads, kvh, length, seqs, dtype, size, byte):
+    """Queries of up to 2^128 and down into the subnormals, over keys whose powers make the
+    scores ordinary ones."""
+    import torch
+    c = t8.attend_case(np.random.default_rng(33), [length] * seqs, [rows] * seqs, heads, kvh, 128, 16, 16, dtype, False)
+    codes, powers = c["codes"][:, :, 0], c["powers"][:, :, 0]
+    c["codes"][:, :, 0] = np.where(codes & 127 == t8.ku.NAN, t8.ku.NAN, codes & 0xBF)  # below 2 in size
+    c["powers"][:, :, 0] = np.where(powers == 255, 255, byte)
+    q = t8.randn(np.random.default_rng(34), c["q"].shape, torch.float64).clamp(-3.9, 3.9) * 2.0 ** size
+    c["q"] = q.to(t8.dt(dtype))
+    assert bool(c["q"].isfinite().all()) and (size < 126 or float(c["q"].abs().max()) >= 2.0 ** 127)
+    t8.check_attention(c, t8.run_attention(q3, c))
