@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
         const int pos = (m.t0 + i) * TM_PT + tid, j = pos - m.t.L;
         const float kf = kv8_power(pw.k[0]), vf = kv8_power(pw.v[0]), eb = (float)min(max(pw.v[0] - 127, -60), 60);
         pw.next(a, d, m, i, tid);
+        const float vl = fmaxf(vf, 0x1p-60f);  // as in eb: weights of values below it stay in range too
         bool isbad = false;
         const bool edge = (m.t0 + i + 1) * TM_PT > m.t.L;  // the tile reaches past the committed positions
         if (edge) {
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           w[r] = exp2_fast(x[r] - ctl.base[r]);
-          over = over || w[r] * vf > KF_SLACK;
+          over = over || w[r] * vl > KF_SLACK;
         }
         if (kf_vote(over || !ok)) {
           // new bases: the rows' largest score and power so far
