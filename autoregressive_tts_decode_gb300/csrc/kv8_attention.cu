@@ -242,9 +242,9 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
       for (int nib = 0; nib < 8; ++nib) pat[nib] = sbase + C::P + sw_at<128>(nib, tid >> 4) + (tid & 15);
       for (int i = 0; i < m.nt; ++i) {
         const int pos = (m.t0 + i) * TM_PT + tid, j = pos - m.t.L;
-        const float kf = kv8_power(pw.k[0]), vf = kv8_power(pw.v[0]), eb = (float)min(max(pw.v[0] - 127, -60), 60);
+        const float kf = kv8_power(pw.k[0]), vf = kv8_power(pw.v[0]), eb = (float)min(max(pw.v[0] - 127, -KV8_EXP), KV8_EXP);
         pw.next(a, d, m, i, tid);
-        const float vl = fmaxf(vf, 0x1p-60f);  // as in eb: weights of values below it stay in range too
+        const float vl = fmaxf(vf, kv8_power(127 - KV8_EXP));  // as in eb: weights of values below it stay in range too
         bool isbad = false;
         const bool edge = (m.t0 + i + 1) * TM_PT > m.t.L;  // the tile reaches past the committed positions
         if (edge) {

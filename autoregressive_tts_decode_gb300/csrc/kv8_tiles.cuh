@@ -16,6 +16,10 @@ int launch_kv8_wide(const Kv8AttnArgs& a, int layers, int dtype, bool tma, int d
 namespace {
 
 constexpr int KF_SORT = 256;  // sequences that are dealt by length, at most
+// Exponents of the values' powers that count: -KV8_EXP .. KV8_EXP.  A weight with its value's power is 2^-80 of
+// another's at the least for equal scores then, and fp32's exponents leave 2^-40 for what the scores differ by: weights
+// below that have no part in the softmax's sum (with 60 it was 2^-7 between blocks 2^120 apart).
+constexpr int KV8_EXP = 40;
 
 struct KfDeal {
   int items, row_tiles, box;

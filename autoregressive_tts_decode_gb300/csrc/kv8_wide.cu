@@ -34,7 +34,6 @@ namespace {
 constexpr int KW_ROWS = 128;  // rows of a tile
 constexpr int KW_SOFT = 256;  // softmax threads, and as many that add up
 constexpr int KW_CONV = 64;   // threads that convert keys, and as many that convert values
-constexpr int KW_EXP = 60;  // exponents of the values' powers that count: -KW_EXP .. KW_EXP
 constexpr float KW_TINY = 1e-37f;  // the least factor of a score: a masked one stays -inf
 constexpr float KW_BASE = 8.f, KW_MOST = 15.f;  // log2 of the weights at the base, and at most
 
@@ -270,10 +269,10 @@ __global__ void __launch_bounds__(KwCfg<T, HD>::THREADS, 1)
         if (!ok) break;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int n = lane + 32 * j, pos = (m.t0 + t) * TM_PT + n, e = min(max(pw.v[j] - 127, -KW_EXP), KW_EXP);
+          const int n = lane + 32 * j, pos = (m.t0 + t) * TM_PT + n, e = min(max(pw.v[j] - 127, -KV8_EXP), KV8_EXP);
           // a new row's block of NaN: rows that see it are told by its bit alone
           const bool bad = pos >= m.t.L && (pw.k[j] == 255 || pw.v[j] == 255);
-          const bool none = bad || pw.v[j] < 127 - KW_EXP || pos >= m.end;  // no values, or none that count
+          const bool none = bad || pw.v[j] < 127 - KV8_EXP || pos >= m.end;  // no values, or none that count
           if (n % GRAN == 0)
             ctl.power[t & 3][n / GRAN] = make_float4(bad ? 1.f : kv8_power(pw.k[j]) * 0x1p-15f, pw.v[j] == 255 && !bad ? kv8_power(255) : (float)e,
                                                      __int_as_float((127 - e) << 23), 0.f);

@@ -81,8 +81,8 @@ int q3tts_kv8_read(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const 
  * Q3TTS_MAX_TREE_NODES).  One that sees nothing gets zeroes.  What a row does not
  * see does not touch it, NaN among it; a row that sees a NaN is unspecified, like
  * one with scores above 2^27, an element of its query times a key block's power above
- * 2^100, or values above 2^60 in size.  A head's query with an infinity or NaN makes
- * its output NaN, if it sees anything.  Values in blocks whose power is below 2^-60
+ * 2^100, or a value block's power above 2^40.  A head's query with an infinity or NaN
+ * makes its output NaN, if it sees anything.  Values in blocks whose power is below 2^-40
  * may count as zeroes.  Rows outside every sequence's range are left as they were;
  * page ids outside the pool leave the sequence's rows unspecified.  No row of out may
  * share a byte with one of q (Q3TTS_ERR_ARG).
