@@ -28,6 +28,9 @@ q3::Kv8Cache desc(const q3tts_kv8_cache& c, int layer) {
   return d;
 }
 
+// Whether the kernels that number a page's rows (its keys and its values) in 32 bits take them.
+bool pages_ok(const q3tts_kv8_cache& c) { return 2ll * c.n_kv_heads <= 0x7fffffffll / c.page_size; }
+
 bool dtype_ok(int d) { return d == Q3TTS_F32 || d == Q3TTS_BF16; }
 size_t esz(int d) { return d == Q3TTS_F32 ? 4 : 2; }
 
@@ -76,6 +79,7 @@ int q3tts_kv8_write(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const
   const int dtype = rows->row_dtype;
   if (!rows_ok(k_dev, ldk, kv->n_kv_heads, kv->head_dim, dtype) || !rows_ok(v_dev, ldv, kv->n_kv_heads, kv->head_dim, dtype))
     return Q3TTS_ERR_ARG;
+  if (!pages_ok(*kv)) return Q3TTS_ERR_UNSUPPORTED;
   return q3::launch_kv8_write(desc(*kv, rows->layer), r, dtype, k_dev, ldk, v_dev, ldv, (cudaStream_t)cuda_stream);
 }
 
@@ -92,6 +96,7 @@ int q3tts_kv8_read(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const 
     return Q3TTS_ERR_ARG;
   if (rows_overlap(span(k_out_dev, ldk, heads, hd, dtype, r.n_rows), span(v_out_dev, ldv, heads, hd, dtype, r.n_rows)))
     return Q3TTS_ERR_ARG;
+  if (!pages_ok(*kv)) return Q3TTS_ERR_UNSUPPORTED;
   return q3::launch_kv8_read(desc(*kv, rows->layer), r, path_dev, dtype, k_out_dev, ldk, v_out_dev, ldv,
                              (cudaStream_t)cuda_stream);
 }
