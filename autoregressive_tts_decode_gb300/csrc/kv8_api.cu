@@ -79,7 +79,8 @@ int q3tts_kv8_write(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const
   const int dtype = rows->row_dtype;
   if (!rows_ok(k_dev, ldk, kv->n_kv_heads, kv->head_dim, dtype) || !rows_ok(v_dev, ldv, kv->n_kv_heads, kv->head_dim, dtype))
     return Q3TTS_ERR_ARG;
-  if (!pages_ok(*kv)) return Q3TTS_ERR_UNSUPPORTED;
+  // (a block's codes are numbered in 32 bits too)
+  if (!pages_ok(*kv) || (long long)kv->block * kv->head_dim > 0x7fffffffll) return Q3TTS_ERR_UNSUPPORTED;
   return q3::launch_kv8_write(desc(*kv, rows->layer), r, dtype, k_dev, ldk, v_dev, ldv, (cudaStream_t)cuda_stream);
 }
 

@@ -57,7 +57,8 @@ typedef struct q3tts_kv8_rows {
  * the sequence holds already the power does not fall: where it rises, those rows'
  * codes are rounded again to the new one.  Rows of a block behind the last one
  * written are left as they were.  A block on a page outside the pool is left out.
- * Pages of up to 2^31 rows of head_dim elements (else Q3TTS_ERR_UNSUPPORTED). */
+ * Pages of up to 2^31 rows of head_dim elements, blocks of up to 2^31 elements (else
+ * Q3TTS_ERR_UNSUPPORTED). */
 int q3tts_kv8_write(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const void* k_dev, int ldk,
                     const void* v_dev, int ldv, void* cuda_stream);
 
@@ -68,8 +69,8 @@ int q3tts_kv8_write(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const
  * was (reported in status), like rows outside every sequence.  With a path,
  * reading the accepted nodes of a drafted tree and writing them as new rows at
  * lengths moves them to the places after the last position held.  No row of
- * k_out may share a byte with one of v_out (Q3TTS_ERR_ARG).  Pages as for
- * q3tts_kv8_write. */
+ * k_out may share a byte with one of v_out (Q3TTS_ERR_ARG).  Pages of up to
+ * 2^31 rows (else Q3TTS_ERR_UNSUPPORTED). */
 int q3tts_kv8_read(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const int32_t* path_dev, void* k_out_dev,
                    int ldk, void* v_out_dev, int ldv, void* cuda_stream);
 
