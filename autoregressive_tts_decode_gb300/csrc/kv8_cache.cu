@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(KV8_WRITE_THREADS, U == 1 || sizeof(T) == 2 ? 
   pdl_trigger();
   constexpr int RPL = 128 / HD;
   const int lane = threadIdx.x & 31, sub = lane / (HD / 4), e0 = lane % (HD / 4) * 4;
-  const unsigned unit = (blockIdx.x * KV8_WRITE_THREADS + threadIdx.x) >> 5;
+  const unsigned unit = blockIdx.x * (KV8_WRITE_THREADS / 32) + (threadIdx.x >> 5);
   if (unit >= units) return;
   const unsigned planes = 2 * c.Hkv, of = unit / planes, seq = of / blocks;
   const int jh = unit - of * planes, j = jh >= c.Hkv, head = jh - j * c.Hkv, nth = of - seq * blocks;
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(KV8_THREADS) kv8_read_kernel(Kv8Cache c, Kv8Ro
   pdl_trigger();
   constexpr int LPR = HD / 16, RPL = 32 / LPR, U = KV8_READ_ROWS / RPL;
   const int lane = threadIdx.x & 31, sub = lane / LPR, e0 = lane % LPR * 16;
-  const unsigned unit = (blockIdx.x * KV8_THREADS + threadIdx.x) >> 5;
+  const unsigned unit = blockIdx.x * (KV8_THREADS / 32) + (threadIdx.x >> 5);
   if (unit >= units) return;
   const unsigned planes = 2 * c.Hkv, of = unit / planes, seq = of / chunks;
   const int jh = unit - of * planes, j = jh >= c.Hkv, head = jh - j * c.Hkv, i0 = (of - seq * chunks) * KV8_READ_ROWS;
@@ -241,9 +241,9 @@ __global__ void __launch_bounds__(KV8_THREADS) kv8_read_kernel(Kv8Cache c, Kv8Ro
 }
 
 int grid_of(long long units, int threads, unsigned* grid) {
-  const long long g = (units * 32 + threads - 1) / threads;
-  if (units > 0x7ffffffll) return Q3TTS_ERR_UNSUPPORTED;  // (threads are numbered in 32 bits)
-  *grid = (unsigned)g;
+  const int warps = threads / 32;
+  if (units > 0x7fffffffll) return Q3TTS_ERR_UNSUPPORTED;  // (warps are numbered in 32 bits)
+  *grid = (unsigned)((units + warps - 1) / warps);
   return Q3TTS_OK;
 }
 

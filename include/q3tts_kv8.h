@@ -32,7 +32,11 @@ typedef struct q3tts_kv8_cache {
 /* The sequences and rows of a call, in one layer: sequence s holds lengths[s]
  * positions (0 or more), and its rows, row_start[s] .. row_start[s + 1] - 1 of the
  * call's rows, stand at the positions after them in order; max_rows (1 or more)
- * bounds every sequence's count and sizes the launch.  page_table (int32
+ * bounds every sequence's count and sizes the launch, as if each had as many: the
+ * closer, the faster (a write's and a read's n_seqs x 2 n_kv_heads x its blocks, or
+ * sixteens of rows, are 2^31 at most, an attention's n_seqs x n_kv_heads x its tiles
+ * of 16 or 128 rows 2^28; else Q3TTS_ERR_UNSUPPORTED).  A table has up to 2^30
+ * positions for a sequence (else Q3TTS_ERR_ARG).  page_table (int32
  * [n_seqs][pages_per_seq]), lengths, row_start and status (may be NULL;
  * q3tts_branch.h's status_dev) are device memory; the table's entries past a
  * sequence's last position are not read.  Rows are n_rows of fp32 or bf16 elements
