@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(KV8_WRITE_THREADS, U == 1 || sizeof(T) == 2 ? 
   int byte = max((int)((top + 0x1fffffu) >> 23) - 8, 0);
   if (held > 0) {
     const int before = *power;
+    __syncwarp();  // all lanes have read it before lane 0 writes it
     if (byte > before) {
       // what is there is rounded again
       const float by = kv8_power(before - byte + 127);
