@@ -1,6 +1,10 @@
 // kv8.cuh -- the paged cache in 8 bits: its descriptor, what its kernels share
 // and their launchers.  Arguments are checked by the callers (kv8_api.cu); a
 // launcher returns a status code.
+//
+// A kernel here may begin while the one before it on the stream, which writes the codes and powers that
+// it reads, still runs (it waits before it reads anything).  So it reads no memory through the non-coherent
+// path, which is for data that nothing writes in a kernel's whole lifetime.
 #pragma once
 
 #include "ops.cuh"

@@ -26,10 +26,10 @@ constexpr int KV8_WRITE_THREADS = 128;
 
 // Four consecutive elements of a row, as they lie and as fp32.
 __device__ __forceinline__ float4 load4(const float* p, bool wide) {
-  return wide ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(p[0], p[1], p[2], p[3]);
+  return wide ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
 }
 __device__ __forceinline__ uint2 load4(const bf16* p, bool wide) {
-  if (wide) return __ldg(reinterpret_cast<const uint2*>(p));
+  if (wide) return *reinterpret_cast<const uint2*>(p);
   const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
   return make_uint2(u[0] | (uint32_t)u[1] << 16, u[2] | (uint32_t)u[3] << 16);
 }
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(KV8_WRITE_THREADS, U == 1 || sizeof(T) == 2 ? 
     }
   };
   const int entry = kv8_div(p0, c.page, c.page_inv), slot = p0 - entry * c.page;
-  const int page = __ldg(r.page_table + (size_t)seq * r.pps + entry);
+  const int page = r.page_table[(size_t)seq * r.pps + entry];
   // (infinities and NaN do not count: sorted out, here and when rounding, only where there are any)
   uint32_t top = 0;
   for (int i0 = 0; i0 < m; i0 += U * RPL) {
@@ -180,6 +180,16 @@ __device__ __forceinline__ void store16(bf16* p, const float* f, bool wide) {
   }
 }
 
+// 16 codes, which are not read again.
+__device__ __forceinline__ uint4 kv8_load16(const uint8_t* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
 // A warp per 16 rows, kv head and k or v; a lane has 16 codes of a row.
 constexpr int KV8_READ_ROWS = 16;
 
@@ -212,7 +222,7 @@ __global__ void __launch_bounds__(KV8_THREADS) kv8_read_kernel(Kv8Cache c, Kv8Ro
     const int pos = ok ? t.L + off : 0, entry = kv8_div(pos, c.page, c.page_inv), slot = pos - entry * c.page;
     int page = 0;
     if (have[u] && ok) {
-      page = __ldg(table + entry);
+      page = table[entry];
       ok = (unsigned)page < (unsigned)c.n_pages;
     }
     if (have[u] && !ok) op_status(r.status, Q3TTS_ERR_ARG);
@@ -220,8 +230,8 @@ __global__ void __launch_bounds__(KV8_THREADS) kv8_read_kernel(Kv8Cache c, Kv8Ro
     x[u] = make_uint4(0, 0, 0, 0);
     power[u] = 0;
     if (have[u]) {
-      x[u] = ld_stream16(codes + ((long long)page * at.rows + slot) * HD);
-      power[u] = __ldg(powers + (long long)page * at.powers + kv8_div(slot, c.block, c.block_inv));
+      x[u] = kv8_load16(codes + ((long long)page * at.rows + slot) * HD);
+      power[u] = powers[(long long)page * at.powers + kv8_div(slot, c.block, c.block_inv)];
     }
   }
   const int ld = j ? ldv : ldk;

@@ -133,8 +133,8 @@ struct Powers {
       const int pg = (unsigned)page[j] < (unsigned)a.c.n_pages ? page[j] : 0;  // (reported by the loading warps)
       const uint8_t* p = layer + (long long)pg * (2 * d.to_values) + block[j];
       const bool is = there(m, i + 1, lane + 32 * j);
-      k[j] = is ? __ldg(p) : 127;
-      v[j] = is ? __ldg(p + d.to_values) : 127;
+      k[j] = is ? *p : 127;
+      v[j] = is ? p[d.to_values] : 127;
       // 128 positions on
       rem[j] += d.step_rem;
       block[j] += d.step_blocks;
@@ -156,7 +156,7 @@ struct Powers {
   __device__ __forceinline__ void look(const Kv8AttnArgs& a, const KfItem& m, int i, int lane) {
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      page[j] = there(m, i, lane + 32 * j) ? __ldg(a.r.page_table + (size_t)m.seq * a.r.pps + entry[j]) : 0;
+      page[j] = there(m, i, lane + 32 * j) ? a.r.page_table[(size_t)m.seq * a.r.pps + entry[j]] : 0;
   }
 };
 // Swizzled operand tiles with rows of W bytes (128 or 64) in atoms of eight rows.
@@ -233,7 +233,7 @@ __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8Attn
     const int my = SPLIT ? kv : lane >> 4, b = lane & 15, boxes = TM_PT / box;
     auto page_of = [&](int i) -> int {
       const int pos = (m.t0 + i) * TM_PT + b * box;
-      return b < boxes && i < m.nt && pos < m.end ? __ldg(table + kv8_div(pos, ps, a.c.page_inv)) : 0;
+      return b < boxes && i < m.nt && pos < m.end ? table[kv8_div(pos, ps, a.c.page_inv)] : 0;
     };
     int page0 = page_of(0), page1 = page_of(1);  // looked up two tiles ahead
     for (int i = 0; i < m.nt; ++i) {
@@ -266,7 +266,7 @@ __device__ __forceinline__ bool load_tiles(const CUtensorMap* map, const Kv8Attn
 #pragma unroll
       for (int j = 0; j < TM_PT / 32; ++j) {
         const int pos = (m.t0 + i) * TM_PT + lane + 32 * j;
-        page[j] = i < m.nt && pos < m.end ? __ldg(table + kv8_div(pos, ps, a.c.page_inv)) : 0;
+        page[j] = i < m.nt && pos < m.end ? table[kv8_div(pos, ps, a.c.page_inv)] : 0;
       }
     };
     look_up(0);
