@@ -22,7 +22,7 @@ constexpr int KF_SORT = 256;  // sequences that are dealt by length, at most
 constexpr int KV8_EXP = 40;
 
 struct KfDeal {
-  int items, row_tiles, box;
+  int row_tiles, box;
   int vec;  // four elements of a row in one access: 1 of q, 2 of out
   unsigned rep_inv;
   int sorted;  // the sequences are taken longest first
@@ -358,7 +358,6 @@ int launch_tiles(Kernel kernel, TmKernel& known, int threads, size_t smem, bool 
   d.row_tiles = (int)(((long)a.r.max_rows * rep + rows - 1) / rows);
   const long items = (long)a.r.n_seqs * a.c.Hkv * d.row_tiles;
   if (items > 0x7fffffffL / 8) return Q3TTS_ERR_UNSUPPORTED;
-  d.items = (int)items;
   const int tiles = (int)(((long)a.r.pps * a.c.page + TM_PT - 1) / TM_PT);
   const int c = cluster_size(items, tiles, known);
   d.vec = (((uintptr_t)a.q & (vec_bytes - 1)) == 0 && a.ldq % 4 == 0 ? 1 : 0) |

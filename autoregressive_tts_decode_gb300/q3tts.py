@@ -509,8 +509,9 @@ def kv8_write(pool, scales, layer: int, page_table, lengths, start, k, v, max_ro
     page size / block]; page_table int32 [seqs, pages per seq]; lengths int32
     [seqs]: positions held; start int32 [seqs + 1]: rows start[s] .. start[s + 1] - 1
     of k and v (fp32 or bf16 [rows, kv heads, head dim], rows contiguous, any row
-    pitch) go to the positions after them; max_rows: the most rows of a sequence
-    (default: as many as there are rows).  Returns (pool, scales)."""
+    pitch) go to the positions after them; max_rows: the most rows of a sequence,
+    which sizes the launch (default: as many as there are rows in all, right for any
+    call and slow for many sequences).  Returns (pool, scales)."""
     what = "q3tts_kv8_write"
     dev, heads, hd, cache, at, shape = _kv8(pool, scales, layer, page_table, lengths, start, what)
     n, _, kind, pair = _row_pair(k, v, ("k", "v"), heads, hd, dev, what)
@@ -546,9 +547,9 @@ def kv8_attention(pool, scales, layer: int, page_table, lengths, start, q, masks
     any row pitch), rows start[s] .. start[s + 1] - 1 of sequence s at the positions
     after its lengths[s], whose keys and values the cache holds too.  masks: None (a
     row sees the sequence's rows up to itself) or int64 / uint64 [rows], bit j of a
-    row's word: it sees row j of its sequence; max_rows: the most rows of a sequence
-    (default: as many as there are rows, with masks up to MAX_TREE_NODES).  The other
-    arguments as for kv8_write.  Returns out (as q; made if None, with zeroes in rows
+    row's word: it sees row j of its sequence; max_rows: the most rows of a sequence,
+    which sizes the launch and its tiles (default: as many as there are rows in all, with masks
+    up to MAX_TREE_NODES).  The other arguments as for kv8_write.  Returns out (as q; made if None, with zeroes in rows
     outside every sequence)."""
     what = "q3tts_kv8_attention"
     dev, _, hd, cache, at, shape = _kv8(pool, scales, layer, page_table, lengths, start, what)
