@@ -51,9 +51,8 @@ struct KfCfg {
   static constexpr int S = (R <= 8 ? 3 : 4) * (128 / HD);  // tiles in the ring
   static constexpr uint32_t CTL = RING + S * SLOT, CTL_BYTES = 2048;
   static constexpr uint32_t TMEM_COLS = 2 * N < 32 ? 32 : 2 * N;  // scores, outputs
-  // A cluster's CTAs wait for one another, and for tensor memory: a CTA's share of an SM's 512
-  // columns is never larger than its share of the 228 KB of shared memory (each with 1 KB of the
-  // system's), so that what fits there has its columns too.
+  // A CTA's share of an SM's 512 columns of tensor memory is never larger than its share of the
+  // 228 KB of shared memory (each with 1 KB of the system's), so that what fits there has its columns too.
   static constexpr size_t NEEDS = 1024 + CTL + CTL_BYTES, SHARE = TMEM_COLS * 456 - 1024;
   static constexpr size_t SMEM = NEEDS < SHARE ? SHARE : NEEDS;
   static_assert(SMEM <= 227 * 1024 && R * HD * 4 <= S * SLOT, "shared memory");
@@ -397,6 +396,23 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
     ctl.sum[tid] = 0.f;
   }
   __syncwarp();
+  // Tensor memory is given back before the CTA waits for the others of its cluster.  One of those may be waiting for
+  // columns that a CTA of another stream's call holds (the tree attention's 32 rows at a head dimension of 64 take all columns
+  // and leave room in shared memory for a CTA here), whose cluster may be waiting for the columns held here.
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_w) {  // what is on its way lands first
+    if (TMA && warp == C::LOAD_WARP) {
+      const long long c0 = clock64();
+      for (int it = max(0, issued - C::S); it < issued; ++it)
+        while (!mbar_try_wait(su32(&ctl.full[it % C::S]), (uint32_t)(it / C::S) & 1u) && clock64() - c0 < TM_LAND_CYCLES) {
+        }
+    }
+    if (warp == C::MMA_WARP && elect_one()) land_products(su32(&ctl.done));
+    __syncwarp();
+  }
+  if (warp == C::MMA_WARP)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
   if (CL > 1) {
     // the shares of an item are joined: what each counts for, then every CL-th row
     cl.sync();
@@ -436,20 +452,6 @@ __global__ void __launch_bounds__(KfCfg<HD, R>::THREADS)
     }
     cl.sync();  // the others may still read this CTA's shared memory
   }
-  tc_fence_before();
-  __syncthreads();
-  if (*abort_w) {  // what is on its way lands first
-    if (TMA && warp == C::LOAD_WARP) {
-      const long long c0 = clock64();
-      for (int it = max(0, issued - C::S); it < issued; ++it)
-        while (!mbar_try_wait(su32(&ctl.full[it % C::S]), (uint32_t)(it / C::S) & 1u) && clock64() - c0 < TM_LAND_CYCLES) {
-        }
-    }
-    if (warp == C::MMA_WARP && elect_one()) land_products(su32(&ctl.done));
-    __syncwarp();
-  }
-  if (warp == C::MMA_WARP)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
 }
 
 template <class T, int HD, int R, bool TMA>
