@@ -93,13 +93,17 @@ int q3tts_kv8_read(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const 
  * may count as zeroes.  Rows outside every sequence's range are left as they were;
  * page ids outside the pool leave the sequence's rows unspecified.  No row of out may
  * share a byte with one of q (Q3TTS_ERR_ARG).  Caches of up to 2^31 rows of head_dim
- * elements in all (else Q3TTS_ERR_UNSUPPORTED).  Scores, softmax statistics and sums are held in 32 bits,
- * a query's elements to 2^-22 of the head's largest.  A weight meets the values off by
- * up to 2^-28 of the row's largest weight x value power and 2^-22 of itself (2^-11
- * where row_dtype is bf16 and the call is one for tiles of 128 rows), and is whole in
- * the softmax's sum; the result is rounded once to row_dtype.  It does not depend on
- * the run, but may, in its roundings, on n_seqs, max_rows and pages_per_seq, which
- * decide the tiles and how positions are split, and on the other rows of its tile.
+ * elements in all (else Q3TTS_ERR_UNSUPPORTED).
+ *
+ * Scores, softmax statistics and sums are held in 32 bits, a query's elements to
+ * 2^-22 of the head's largest.  A weight is a power of two to 2^-22, whose exponent
+ * (score and value power less the row's largest) is off by 2^-24 of its size.  It
+ * meets the values off by up to 2^-28 of the row's largest weight x value power and
+ * 2^-22 of itself (2^-11 where row_dtype is bf16 and the call is one for tiles of 128
+ * rows), and is whole in the softmax's sum; the result is rounded once to row_dtype.
+ * It does not depend on the run, but may, in its roundings, on n_seqs, max_rows and
+ * pages_per_seq, which decide the tiles and how positions are split, and on the other
+ * rows of its tile.
  * q3tts_debug_lose_tile arms this call too. */
 int q3tts_kv8_attention(const q3tts_kv8_cache* kv, const q3tts_kv8_rows* rows, const uint64_t* masks_dev,
                         const void* q_dev, int ldq, void* out_dev, int ldo, int n_q_heads, void* cuda_stream);
