@@ -29,7 +29,7 @@
 // last ones to start are short.
 //
 // The bound is the cache's bytes: 128 sequences of 256 .. 2048 positions, one token of 16 heads over 8: 54 us,
-// 5.6 TB/s (loading alone 50; three CTAs with rings of four 59.6).  Short calls are latency, the chain from
+// 5.7 TB/s (loading alone 50; three CTAs with rings of four 59.6).  Short calls are latency, the chain from
 // lengths to pages to codes and a tile's way: 131 positions 6 us, 16 sequences of 32 .. 512 9 us.  More rows cost
 // their digits: 128 x 1152 positions, 2, 4, 8 new rows of two heads: 68, 85, 132 us.
 #include "kv8_tiles.cuh"

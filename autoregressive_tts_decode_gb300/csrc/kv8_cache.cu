@@ -10,9 +10,9 @@
 // which loses nothing but what falls under the format's smallest step.
 //
 // Both are bound by the bytes they move, rows in one form and codes in the other: 125,000 rows of
-// eight kv heads read back to bf16 (771 MB): 122 us, 6.3 TB/s, 93 % of a plain copy (141 us with 64-bit
+// eight kv heads read back to bf16 (771 MB): 123 us, 6.3 TB/s, 92 % of a plain copy (141 us with 64-bit
 // divisions in the addresses: three quarters of the issue slots were taken); eight fp32 prompts of 2 ..
-// 1982 rows written (81 MB): 16.0 us, 5.1 TB/s, waves of warps that each wait for their rows (17.9 with every
+// 1982 rows written (81 MB): 15.7 us, 5.2 TB/s, waves of warps that each wait for their rows (17.9 with every
 // element looked at for infinities and NaN).  Calls for single tokens are a launch and three dependent
 // loads, 2.5 to 3 us.
 #include "kv8.cuh"

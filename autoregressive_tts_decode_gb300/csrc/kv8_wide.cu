@@ -20,8 +20,8 @@
 // other's, or outputs: scores of tile t + 2 follow the outputs of tile t, whose P they overwrite, and are the time in
 // which those outputs are read.
 //
-// Four sequences of 30011 .. 32768 positions, 64 nodes with two heads each, fp32: 118 us, 1.7 a tile of 128 x 128 (the
-// products take 1.05); 2048 bf16 rows after 14336: 316 us, 1.25 a tile (0.53).  Without the softmax's work these are 86
+// Four sequences of 30011 .. 32768 positions, 64 nodes with two heads each, fp32: 119 us, 1.7 a tile of 128 x 128 (the
+// products take 1.05); 2048 bf16 rows after 14336: 318 us, 1.25 a tile (0.53).  Without the softmax's work these are 86
 // and 221 us, without the conversion 107 and 269, without adding up 116 and 311, with a sixteenth of the products 92
 // and 277: no unit is full (a scheduler issues in half of its cycles), the instructions of all roles share it.  An item
 // begins and ends in about 11 us.
